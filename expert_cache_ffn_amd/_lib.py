@@ -14,9 +14,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libecf.so")
 
 ECF_OK, ECF_EINVAL, ECF_ENOSPC, ECF_EHIP, ECF_EUNSUPPORTED, ECF_ESTATE = 0, -1, -2, -3, -4, -5
-ECF_F32, ECF_BF16, ECF_MXFP4 = 0, 1, 2
+ECF_F32, ECF_BF16, ECF_MXFP4, ECF_F16 = 0, 1, 2, 3
 ECF_Q_AUTO, ECF_Q_ALL_GPU, ECF_Q_ALL_HOST, ECF_Q_FIXED = 0, 1, 2, 3
 ECF_PATH_AUTO, ECF_PATH_DECODE, ECF_PATH_PREFILL = 0, 1, 2
+ECF_ACT_NONE, ECF_ACT_SILU, ECF_ACT_GELU, ECF_ACT_GELU_TANH, ECF_ACT_RELU = 0, 1, 2, 3, 4
+ACTS = {"none": ECF_ACT_NONE, "silu": ECF_ACT_SILU, "gelu": ECF_ACT_GELU, "gelu_tanh": ECF_ACT_GELU_TANH,
+        "relu": ECF_ACT_RELU}
 DTYPES = {"f32": ECF_F32, "bf16": ECF_BF16, "mxfp4": ECF_MXFP4}
 
 # every symbol include/ecf.h declares
@@ -25,7 +28,9 @@ EXPORTS = [
     "ecf_cache_create", "ecf_cache_destroy", "expert_cache_lookup", "expert_cache_evict",
     "ecf_cache_available", "ecf_cache_slot_of", "ecf_cache_get_stats", "ecf_cache_resize",
     "prefetch_layer", "moe_layer_forward", "moe_layer_forward_noalloc", "ecf_noalloc_scratch_bytes",
-    "ecf_host_experts", "ecf_bandwidth_profile", "ecf_profile_enable",
+    "ecf_host_experts", "ecf_bandwidth_profile",
+    "ecf_gated_workspace_bytes", "ecf_gated_forward", "ecf_gated_backward",
+    "ecf_linear_workspace_bytes", "ecf_linear_forward", "ecf_linear_backward", "ecf_profile_enable",
     "ecf_profile_get", "ecf_profile_reset", "ecf_stream_read", "ecf_mfma_rate",
 ]
 
@@ -78,6 +83,30 @@ class LayerArgs(Structure):
     ]
 
 
+class GatedArgs(Structure):
+    _fields_ = [
+        ("hidden", c_int32), ("inter", c_int32), ("dtype", c_int32), ("act", c_int32),
+        ("d_x", c_void_p), ("d_w_gate", c_void_p), ("d_w_up", c_void_p), ("d_b_gate", c_void_p), ("d_b_up", c_void_p),
+        ("ld_x", c_int64), ("ld_w", c_int64), ("d_h", c_void_p), ("ld_h", c_int64),
+        ("d_a", c_void_p), ("d_b", c_void_p), ("ld_ab", c_int64), ("d_dh", c_void_p), ("ld_dh", c_int64),
+        ("d_dx", c_void_p), ("ld_dx", c_int64), ("wgrad_dtype", c_int32),
+        ("d_dw_gate", c_void_p), ("d_dw_up", c_void_p), ("ld_dw", c_int64),
+        ("d_db_gate", c_void_p), ("d_db_up", c_void_p), ("d_ws", c_void_p), ("ws_bytes", c_size_t),
+        ("stream", c_void_p),
+    ]
+
+
+class LinearArgs(Structure):
+    _fields_ = [
+        ("in_features", c_int32), ("out_features", c_int32), ("dtype", c_int32), ("out_dtype", c_int32),
+        ("act", c_int32), ("d_x", c_void_p), ("d_w", c_void_p), ("d_bias", c_void_p), ("d_residual", c_void_p),
+        ("ld_x", c_int64), ("ld_w", c_int64), ("ld_residual", c_int64), ("d_out", c_void_p), ("ld_out", c_int64),
+        ("d_z", c_void_p), ("ld_z", c_int64), ("d_dout", c_void_p), ("ld_dout", c_int64),
+        ("d_dx", c_void_p), ("ld_dx", c_int64), ("wgrad_dtype", c_int32), ("d_dw", c_void_p), ("ld_dw", c_int64),
+        ("d_dbias", c_void_p), ("d_ws", c_void_p), ("ws_bytes", c_size_t), ("stream", c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -122,6 +151,12 @@ def lib():
         L.ecf_bandwidth_profile.argtypes = [POINTER(Shape), c_int32, c_void_p, c_int32, c_void_p, c_size_t,
                                             c_void_p, c_double, POINTER(BwProfile)]
         L.ecf_bandwidth_profile.restype = c_int32
+        for name, args in (("gated", GatedArgs), ("linear", LinearArgs)):
+            ws = getattr(L, f"ecf_{name}_workspace_bytes")
+            ws.argtypes, ws.restype = [c_int32] * 5, c_size_t
+            for way in ("forward", "backward"):
+                f = getattr(L, f"ecf_{name}_{way}")
+                f.argtypes, f.restype = [POINTER(args), c_int32], c_int32
         L.ecf_profile_enable.argtypes, L.ecf_profile_enable.restype = [c_int32], c_int32
         L.ecf_profile_get.argtypes = [c_int32, POINTER(c_char_p), POINTER(c_int64), POINTER(c_double)]
         L.ecf_profile_get.restype = c_int32
@@ -274,6 +309,37 @@ def ecf_bandwidth_profile(shape: Shape, blob_ptrs, d_buf, d_buf_bytes, copy_stre
                                        int(d_buf) or None, int(d_buf_bytes), int(copy_stream) or None,
                                        float(seconds), ctypes.byref(out)))
     return out.as_dict()
+
+
+def _dense_ws(n: int) -> int:
+    if n == c_size_t(-1).value:
+        raise EcfError(ECF_EINVAL, lib().ecf_last_error().decode())
+    return n
+
+
+def ecf_gated_workspace_bytes(hidden, inter, dtype, n_tokens, backward=False) -> int:
+    return _dense_ws(lib().ecf_gated_workspace_bytes(int(hidden), int(inter), int(dtype), int(n_tokens), int(backward)))
+
+
+def ecf_gated_forward(args: GatedArgs, n_tokens):
+    _check(lib().ecf_gated_forward(ctypes.byref(args), n_tokens))
+
+
+def ecf_gated_backward(args: GatedArgs, n_tokens):
+    _check(lib().ecf_gated_backward(ctypes.byref(args), n_tokens))
+
+
+def ecf_linear_workspace_bytes(in_features, out_features, dtype, n_tokens, backward=False) -> int:
+    return _dense_ws(lib().ecf_linear_workspace_bytes(int(in_features), int(out_features), int(dtype), int(n_tokens),
+                                                      int(backward)))
+
+
+def ecf_linear_forward(args: LinearArgs, n_tokens):
+    _check(lib().ecf_linear_forward(ctypes.byref(args), n_tokens))
+
+
+def ecf_linear_backward(args: LinearArgs, n_tokens):
+    _check(lib().ecf_linear_backward(ctypes.byref(args), n_tokens))
 
 
 def ecf_profile_enable(on: bool):

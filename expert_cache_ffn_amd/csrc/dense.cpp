@@ -1,0 +1,373 @@
+// C-ABI entry points of the dense feed-forward operators: argument checks, the
+// workspace, and the matrix products and gradient kernels each call is made of.
+#include <algorithm>
+#include <cstdint>
+
+#include "dense_internal.h"
+
+namespace ecf {
+namespace {
+
+constexpr int32_t kDenseMax = 1 << 22;  // tokens and widths per call
+
+size_t al256(size_t v) { return (v + 255) & ~(size_t)255; }
+int64_t ld_or(int64_t ld, int64_t width) { return ld ? ld : width; }
+
+bool dense_dtype(int32_t t) { return t == ECF_F32 || t == ECF_BF16 || t == ECF_F16; }
+
+int check_common(const char *what, int32_t in, int32_t out, int32_t dtype, int32_t T)
+{
+    if (in < 1 || in > kDenseMax || out < 1 || out > kDenseMax || T < 0 || T > kDenseMax)
+        return set_error(ECF_EINVAL, "%s: widths must be 1..%d and n_tokens 0..%d (in=%d, out=%d, T=%d)", what,
+                         kDenseMax, kDenseMax, in, out, T);
+    if (!dense_dtype(dtype))
+        return set_error(ECF_EINVAL, "%s: dtype must be ECF_F32, ECF_BF16 or ECF_F16 (got %d)", what, dtype);
+    return ECF_OK;
+}
+
+// A matrix operand: present, aligned to its element, rows at least as far apart
+// as they are long, and 256 of them within a 31-bit byte offset.
+int check_matrix(const char *what, const char *name, const void *p, int64_t ld, int64_t width, int dtype)
+{
+    const size_t e = dense_esize(dtype);
+    if (!p)
+        return set_error(ECF_EINVAL, "%s: %s is NULL", what, name);
+    if ((uintptr_t)p % e)
+        return set_error(ECF_EINVAL, "%s: %s is not aligned to its %zu-byte elements", what, name, e);
+    if (ld < width)
+        return set_error(ECF_EINVAL, "%s: the row stride of %s (%lld) is below its width %lld", what, name,
+                         (long long)ld, (long long)width);
+    if (ld > (int64_t)(0x7fffffff / 256 / e))
+        return set_error(ECF_EUNSUPPORTED, "%s: 256 rows of %s (stride %lld) span 2 GiB or more", what, name,
+                         (long long)ld);
+    return ECF_OK;
+}
+
+int check_vector(const char *what, const char *name, const void *p, int dtype)
+{
+    if ((uintptr_t)p % dense_esize(dtype))
+        return set_error(ECF_EINVAL, "%s: %s is not aligned to its elements", what, name);
+    return ECF_OK;
+}
+
+int check_ws(const char *what, const void *ws, size_t have, size_t need)
+{
+    if (!need)
+        return ECF_OK;
+    if (!ws || have < need)
+        return set_error(ECF_ENOSPC, "%s: needs %zu bytes of workspace, got %zu", what, need, ws ? have : (size_t)0);
+    if ((uintptr_t)ws % 256)
+        return set_error(ECF_EINVAL, "%s: the workspace is not at a 256-byte boundary", what);
+    return ECF_OK;
+}
+
+int check_act(const char *what, int32_t act)
+{
+    if (act < ECF_ACT_NONE || act > ECF_ACT_RELU)
+        return set_error(ECF_EINVAL, "%s: unknown activation %d", what, act);
+    return ECF_OK;
+}
+
+int check_grad_dtype(const char *what, int32_t t, int32_t dtype)
+{
+    if (t != dtype && t != ECF_F32)
+        return set_error(ECF_EINVAL, "%s: wgrad_dtype must be dtype or ECF_F32 (got %d)", what, t);
+    return ECF_OK;
+}
+
+#define DENSE_TRY(expr)                \
+    do {                               \
+        const int _rc = (expr);        \
+        if (_rc != ECF_OK)             \
+            return _rc;                \
+    } while (0)
+
+// Backward workspace: dz rows in `dtype` (gated: da and db halves of one row),
+// then the column sums of each row block in fp32.
+struct BackWs {
+    int64_t pitch;
+    size_t partial, total;
+};
+BackWs back_ws(int64_t cols, int halves, int dtype, int32_t T)
+{
+    BackWs w;
+    w.pitch = halves * cols;
+    w.partial = al256((size_t)T * w.pitch * dense_esize(dtype));
+    w.total = w.partial + al256((size_t)dense_grad_row_blocks(T) * halves * cols * 4);
+    return w;
+}
+
+}  // namespace
+}  // namespace ecf
+
+using namespace ecf;
+
+extern "C" {
+
+size_t ecf_gated_workspace_bytes(int32_t hidden, int32_t inter, int32_t dtype, int32_t n_tokens, int32_t backward)
+{
+    if (check_common("ecf_gated_workspace_bytes", hidden, inter, dtype, n_tokens) != ECF_OK)
+        return SIZE_MAX;
+    return backward ? back_ws(inter, 2, dtype, n_tokens).total : 0;
+}
+
+int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
+{
+    return guarded("ecf_gated_forward", [&]() -> int {
+        const char *me = "ecf_gated_forward";
+        if (!a)
+            return set_error(ECF_EINVAL, "%s: args is NULL", me);
+        DENSE_TRY(check_common(me, a->hidden, a->inter, a->dtype, T));
+        DENSE_TRY(check_act(me, a->act));
+        const int64_t d = a->hidden, I = a->inter;
+        DenseGemm g{};
+        g.dtype = g.out_dtype = a->dtype;
+        g.gated = true;
+        g.ksegs = g.mhalves = 1;
+        g.M = T, g.N = a->inter, g.K = a->hidden;
+        g.lda = ld_or(a->ld_x, d), g.ldb = ld_or(a->ld_w, d);
+        g.ldout = ld_or(a->ld_h, I), g.ldsave = ld_or(a->ld_ab, I);
+        g.act = a->act;
+        if (T == 0)
+            return ECF_OK;
+        DENSE_TRY(check_matrix(me, "d_x", a->d_x, g.lda, d, a->dtype));
+        DENSE_TRY(check_matrix(me, "d_w_gate", a->d_w_gate, g.ldb, d, a->dtype));
+        DENSE_TRY(check_matrix(me, "d_w_up", a->d_w_up, g.ldb, d, a->dtype));
+        DENSE_TRY(check_vector(me, "d_b_gate", a->d_b_gate, a->dtype));
+        DENSE_TRY(check_vector(me, "d_b_up", a->d_b_up, a->dtype));
+        if (!a->d_a != !a->d_b)
+            return set_error(ECF_EINVAL, "%s: d_a and d_b come together", me);
+        if (a->d_h || !a->d_a)
+            DENSE_TRY(check_matrix(me, "d_h", a->d_h, g.ldout, I, a->dtype));
+        if (a->d_a) {
+            DENSE_TRY(check_matrix(me, "d_a", a->d_a, g.ldsave, I, a->dtype));
+            DENSE_TRY(check_matrix(me, "d_b", a->d_b, g.ldsave, I, a->dtype));
+        }
+        g.a[0] = a->d_x;
+        g.b[0] = a->d_w_gate, g.b[1] = a->d_w_up;
+        g.bias[0] = a->d_b_gate, g.bias[1] = a->d_b_up;
+        g.out[0] = a->d_h;
+        g.save[0] = a->d_a, g.save[1] = a->d_b;
+        return launch_dense_gemm(g, (hipStream_t)a->stream);
+    });
+}
+
+int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
+{
+    return guarded("ecf_gated_backward", [&]() -> int {
+        const char *me = "ecf_gated_backward";
+        if (!a)
+            return set_error(ECF_EINVAL, "%s: args is NULL", me);
+        DENSE_TRY(check_common(me, a->hidden, a->inter, a->dtype, T));
+        DENSE_TRY(check_act(me, a->act));
+        DENSE_TRY(check_grad_dtype(me, a->wgrad_dtype, a->dtype));
+        const int64_t d = a->hidden, I = a->inter;
+        const int64_t ldx = ld_or(a->ld_x, d), ldw = ld_or(a->ld_w, d), ldab = ld_or(a->ld_ab, I),
+                      lddh = ld_or(a->ld_dh, I), lddx = ld_or(a->ld_dx, d), lddw = ld_or(a->ld_dw, d);
+        if (!a->d_dw_gate != !a->d_dw_up)
+            return set_error(ECF_EINVAL, "%s: d_dw_gate and d_dw_up come together", me);
+        const bool want_dw = a->d_dw_gate, want_db = a->d_db_gate || a->d_db_up, want_dx = a->d_dx && T > 0;
+        if (T > 0) {
+            DENSE_TRY(check_matrix(me, "d_a", a->d_a, ldab, I, a->dtype));
+            DENSE_TRY(check_matrix(me, "d_b", a->d_b, ldab, I, a->dtype));
+            DENSE_TRY(check_matrix(me, "d_dh", a->d_dh, lddh, I, a->dtype));
+            if (want_dw)
+                DENSE_TRY(check_matrix(me, "d_x", a->d_x, ldx, d, a->dtype));
+        }
+        if (want_dx) {
+            DENSE_TRY(check_matrix(me, "d_w_gate", a->d_w_gate, ldw, d, a->dtype));
+            DENSE_TRY(check_matrix(me, "d_w_up", a->d_w_up, ldw, d, a->dtype));
+            DENSE_TRY(check_matrix(me, "d_dx", a->d_dx, lddx, d, a->dtype));
+        }
+        if (want_dw) {
+            DENSE_TRY(check_matrix(me, "d_dw_gate", a->d_dw_gate, lddw, d, a->wgrad_dtype));
+            DENSE_TRY(check_matrix(me, "d_dw_up", a->d_dw_up, lddw, d, a->wgrad_dtype));
+        }
+        DENSE_TRY(check_vector(me, "d_db_gate", a->d_db_gate, a->wgrad_dtype));
+        DENSE_TRY(check_vector(me, "d_db_up", a->d_db_up, a->wgrad_dtype));
+        const BackWs w = back_ws(I, 2, a->dtype, T);
+        DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
+        hipStream_t st = (hipStream_t)a->stream;
+        char *dz = (char *)a->d_ws;
+        float *partial = want_db ? (float *)(dz + w.partial) : nullptr;
+        if (T > 0 && (want_dw || want_dx || want_db)) {
+            DenseGrad q{};
+            q.dtype = q.dout_dtype = a->dtype;
+            q.act = a->act;
+            q.gated = true;
+            q.dout = a->d_dh, q.a = a->d_a, q.b = a->d_b;
+            q.lddout = lddh, q.ldab = ldab;
+            q.T = T, q.I = a->inter;
+            q.dz = want_dw || want_dx ? dz : nullptr;
+            q.pitch = w.pitch;
+            q.partial = partial;
+            q.row_blocks = dense_grad_row_blocks(T);
+            DENSE_TRY(launch_dense_grad(q, st));
+        }
+        if (want_db) {
+            void *const out[2] = {a->d_db_gate, a->d_db_up};
+            DENSE_TRY(launch_dense_colsum(partial, dense_grad_row_blocks(T), a->inter, 2, a->wgrad_dtype, out, st));
+        }
+        const char *dz2 = dz + (size_t)(w.pitch / 2) * dense_esize(a->dtype);
+        if (want_dx) {
+            DenseGemm g{};
+            g.dtype = g.out_dtype = a->dtype;
+            g.b_t = true;
+            g.ksegs = 2, g.mhalves = 1;
+            g.a[0] = dz, g.a[1] = dz2;
+            g.b[0] = a->d_w_gate, g.b[1] = a->d_w_up;
+            g.lda = w.pitch, g.ldb = ldw;
+            g.M = T, g.N = a->hidden, g.K = a->inter;
+            g.out[0] = a->d_dx;
+            g.ldout = lddx;
+            DENSE_TRY(launch_dense_gemm(g, st));
+        }
+        if (want_dw) {
+            DenseGemm g{};
+            g.dtype = a->dtype;
+            g.out_dtype = a->wgrad_dtype;
+            g.a_t = g.b_t = true;
+            g.ksegs = 1, g.mhalves = 2;
+            g.a[0] = dz, g.a[1] = dz2;
+            g.b[0] = a->d_x;
+            g.lda = w.pitch, g.ldb = ldx;
+            g.M = a->inter, g.N = a->hidden, g.K = T;
+            g.out[0] = a->d_dw_gate, g.out[1] = a->d_dw_up;
+            g.ldout = lddw;
+            DENSE_TRY(launch_dense_gemm(g, st));
+        }
+        return ECF_OK;
+    });
+}
+
+size_t ecf_linear_workspace_bytes(int32_t in_features, int32_t out_features, int32_t dtype, int32_t n_tokens,
+                                  int32_t backward)
+{
+    if (check_common("ecf_linear_workspace_bytes", in_features, out_features, dtype, n_tokens) != ECF_OK)
+        return SIZE_MAX;
+    return backward ? back_ws(out_features, 1, dtype, n_tokens).total : 0;
+}
+
+int ecf_linear_forward(const ecf_linear_args *a, int32_t T)
+{
+    return guarded("ecf_linear_forward", [&]() -> int {
+        const char *me = "ecf_linear_forward";
+        if (!a)
+            return set_error(ECF_EINVAL, "%s: args is NULL", me);
+        DENSE_TRY(check_common(me, a->in_features, a->out_features, a->dtype, T));
+        DENSE_TRY(check_act(me, a->act));
+        if (a->out_dtype != a->dtype && a->out_dtype != ECF_F32)
+            return set_error(ECF_EINVAL, "%s: out_dtype must be dtype or ECF_F32 (got %d)", me, a->out_dtype);
+        const int64_t K = a->in_features, N = a->out_features;
+        DenseGemm g{};
+        g.dtype = a->dtype, g.out_dtype = a->out_dtype;
+        g.ksegs = g.mhalves = 1;
+        g.M = T, g.N = a->out_features, g.K = a->in_features;
+        g.lda = ld_or(a->ld_x, K), g.ldb = ld_or(a->ld_w, K);
+        g.ldout = ld_or(a->ld_out, N), g.ldsave = ld_or(a->ld_z, N), g.ldres = ld_or(a->ld_residual, N);
+        g.act = a->act;
+        if (T == 0)
+            return ECF_OK;
+        DENSE_TRY(check_matrix(me, "d_x", a->d_x, g.lda, K, a->dtype));
+        DENSE_TRY(check_matrix(me, "d_w", a->d_w, g.ldb, K, a->dtype));
+        DENSE_TRY(check_matrix(me, "d_out", a->d_out, g.ldout, N, a->out_dtype));
+        DENSE_TRY(check_vector(me, "d_bias", a->d_bias, a->dtype));
+        if (a->d_residual)
+            DENSE_TRY(check_matrix(me, "d_residual", a->d_residual, g.ldres, N, a->out_dtype));
+        if (a->d_z)
+            DENSE_TRY(check_matrix(me, "d_z", a->d_z, g.ldsave, N, a->dtype));
+        g.a[0] = a->d_x, g.b[0] = a->d_w;
+        g.bias[0] = a->d_bias;
+        g.res = a->d_residual;
+        g.out[0] = a->d_out;
+        g.save[0] = a->d_z;
+        return launch_dense_gemm(g, (hipStream_t)a->stream);
+    });
+}
+
+int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
+{
+    return guarded("ecf_linear_backward", [&]() -> int {
+        const char *me = "ecf_linear_backward";
+        if (!a)
+            return set_error(ECF_EINVAL, "%s: args is NULL", me);
+        DENSE_TRY(check_common(me, a->in_features, a->out_features, a->dtype, T));
+        DENSE_TRY(check_act(me, a->act));
+        DENSE_TRY(check_grad_dtype(me, a->wgrad_dtype, a->dtype));
+        if (a->out_dtype != a->dtype && a->out_dtype != ECF_F32)
+            return set_error(ECF_EINVAL, "%s: out_dtype must be dtype or ECF_F32 (got %d)", me, a->out_dtype);
+        const int64_t K = a->in_features, N = a->out_features;
+        const int64_t ldx = ld_or(a->ld_x, K), ldw = ld_or(a->ld_w, K), ldz = ld_or(a->ld_z, N),
+                      lddy = ld_or(a->ld_dout, N), lddx = ld_or(a->ld_dx, K), lddw = ld_or(a->ld_dw, K);
+        const bool want_dx = a->d_dx && T > 0, act = a->act != ECF_ACT_NONE;
+        if (T > 0) {
+            DENSE_TRY(check_matrix(me, "d_dout", a->d_dout, lddy, N, a->out_dtype));
+            if (act)
+                DENSE_TRY(check_matrix(me, "d_z", a->d_z, ldz, N, a->dtype));
+            if (a->d_dw)
+                DENSE_TRY(check_matrix(me, "d_x", a->d_x, ldx, K, a->dtype));
+        }
+        if (want_dx) {
+            DENSE_TRY(check_matrix(me, "d_w", a->d_w, ldw, K, a->dtype));
+            DENSE_TRY(check_matrix(me, "d_dx", a->d_dx, lddx, K, a->dtype));
+        }
+        if (a->d_dw)
+            DENSE_TRY(check_matrix(me, "d_dw", a->d_dw, lddw, K, a->wgrad_dtype));
+        DENSE_TRY(check_vector(me, "d_dbias", a->d_dbias, a->wgrad_dtype));
+        const BackWs w = back_ws(N, 1, a->dtype, T);
+        DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
+        hipStream_t st = (hipStream_t)a->stream;
+        // without an activation and in the operands' type, dy is dz
+        const bool direct = !act && a->out_dtype == a->dtype;
+        const bool products = want_dx || (a->d_dw && T > 0);
+        float *partial = a->d_dbias ? (float *)((char *)a->d_ws + w.partial) : nullptr;
+        if (T > 0 && ((products && !direct) || a->d_dbias)) {
+            DenseGrad q{};
+            q.dtype = a->dtype, q.dout_dtype = a->out_dtype;
+            q.act = a->act;
+            q.dout = a->d_dout;
+            q.a = act ? a->d_z : nullptr;
+            q.lddout = lddy, q.ldab = ldz;
+            q.T = T, q.I = a->out_features;
+            q.dz = products && !direct ? a->d_ws : nullptr;
+            q.pitch = w.pitch;
+            q.partial = partial;
+            q.row_blocks = dense_grad_row_blocks(T);
+            DENSE_TRY(launch_dense_grad(q, st));
+        }
+        if (a->d_dbias) {
+            void *const out[2] = {a->d_dbias, nullptr};
+            DENSE_TRY(launch_dense_colsum(partial, dense_grad_row_blocks(T), a->out_features, 1, a->wgrad_dtype, out, st));
+        }
+        const void *dz = direct ? a->d_dout : a->d_ws;
+        const int64_t lddz = direct ? lddy : w.pitch;
+        DenseGemm g{};
+        g.dtype = a->dtype;
+        g.ksegs = g.mhalves = 1;
+        g.a[0] = dz;
+        g.lda = lddz;
+        g.b_t = true;
+        if (want_dx) {
+            g.out_dtype = a->dtype;
+            g.b[0] = a->d_w;
+            g.ldb = ldw;
+            g.M = T, g.N = a->in_features, g.K = a->out_features;
+            g.out[0] = a->d_dx;
+            g.ldout = lddx;
+            DENSE_TRY(launch_dense_gemm(g, st));
+        }
+        if (a->d_dw) {
+            g.out_dtype = a->wgrad_dtype;
+            g.a_t = true;
+            g.b[0] = a->d_x;
+            g.ldb = ldx;
+            g.M = a->out_features, g.N = a->in_features, g.K = T;
+            g.out[0] = a->d_dw;
+            g.ldout = lddw;
+            DENSE_TRY(launch_dense_gemm(g, st));
+        }
+        return ECF_OK;
+    });
+}
+
+}  // extern "C"

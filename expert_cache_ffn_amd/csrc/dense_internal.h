@@ -1,0 +1,58 @@
+// The dense feed-forward operators' internal interface: dense.cpp checks a
+// call and describes its matrix products, the k_dense*.hip launchers run them.
+#pragma once
+
+#include "ecf_internal.h"
+
+namespace ecf {
+
+inline size_t dense_esize(int dtype) { return dtype == ECF_F32 ? 4 : 2; }
+
+// One matrix product with its epilogue:
+//   acc_g[m][n] = sum_s sum_k A_s(m, k) B(n, k),  s < ksegs, k < K
+// A_s(m, k) is a[s][m * lda + k], or a[s][k * lda + m] with a_t; B likewise.
+//  - gated:       b[0] and b[1] give two sums over the one A; the epilogue joins them
+//  - ksegs == 2:  a[0] . b[0] + a[1] . b[1], both K long
+//  - mhalves == 2: a[h] gives out[h], h = 0, 1 (two products that share B)
+// At most one of the three holds.
+struct DenseGemm {
+    int dtype;  // of A, B, bias and saved pre-activations: ECF_F32, ECF_BF16 or ECF_F16
+    bool a_t, b_t;
+    const void *a[2], *b[2];
+    int64_t lda, ldb;
+    int M, N, K;
+    int ksegs, mhalves;
+    bool gated;
+    // epilogue: z = acc + bias; save <- z; out = act(z) + res, gated: act(z_0) * z_1
+    int act, out_dtype;
+    const void *bias[2];
+    const void *res;  // in out_dtype; not gated
+    int64_t ldres;
+    void *out[2];
+    int64_t ldout;
+    void *save[2];
+    int64_t ldsave;
+};
+int launch_dense_gemm(const DenseGemm &g, hipStream_t st);
+
+// dz rows of the backward passes, in the operands' type: dz[t][i] (linear) or
+// da = dz[t][i], db = dz[t][pitch / 2 + i] (gated).  Columns from I to the
+// (half) pitch are zeroed.  With colsum, per-block column sums go to
+// partial[block][2 or 1][I] in fp32; launch_dense_colsum adds them up.
+struct DenseGrad {
+    int dtype, dout_dtype, act;
+    bool gated;
+    const void *dout, *a, *b;  // linear: a = z (null when act is none)
+    int64_t lddout, ldab;
+    int T, I;
+    void *dz;  // null: column sums only
+    int64_t pitch;
+    float *partial;
+    int row_blocks;
+};
+int dense_grad_row_blocks(int T);
+int launch_dense_grad(const DenseGrad &g, hipStream_t st);
+int launch_dense_colsum(const float *partial, int row_blocks, int I, int n, int out_dtype, void *const out[2],
+                        hipStream_t st);
+
+}  // namespace ecf

@@ -1,0 +1,191 @@
+// Dense feed-forward operators: the matrix products of the gated projection and
+// of the linear layer, forward and backward, for any size, stride and alignment.
+//
+//   acc[m][n] = sum_k A(m, k) B(n, k), either operand k- or m-contiguous
+//
+// A block owns a 64 x 64 tile of the output, stages 16 k of both operands in
+// LDS as fp32 (widened once, exactly) and each of its 256 threads sums a 4 x 4
+// patch with fp32 FMAs; the gated form keeps two patches, one per projection,
+// and joins them in registers.  The epilogue adds bias, applies the activation,
+// adds the residual and rounds once.
+#include "dense_device.h"
+
+namespace ecf {
+namespace {
+
+constexpr int TM = 64, TN = 64, TK = 16;
+
+__device__ __forceinline__ float load_el(const void *p, int64_t i, int dtype)
+{
+    if (dtype == ECF_F32)
+        return ((const float *)p)[i];
+    const uint16_t v = ((const uint16_t *)p)[i];
+    return dtype == ECF_BF16 ? BF16::to_f(v) : F16::to_f(v);
+}
+
+__device__ __forceinline__ void store_el(void *p, int64_t i, float v, int dtype)
+{
+    if (dtype == ECF_F32)
+        ((float *)p)[i] = v;
+    else
+        ((uint16_t *)p)[i] = dtype == ECF_BF16 ? BF16::from_f(v) : F16::from_f(v);
+}
+
+// MHALVES: the upper half of gridDim.y works on a[1] -> out[1].
+template <bool GATED>
+__global__ __launch_bounds__(256) void k_dense_tile(DenseGemm g)
+{
+    __shared__ float As[TK][TM + 1], Bs[GATED ? 2 : 1][TK][TN + 1];
+    const int mt = (g.M + TM - 1) / TM;
+    const int half = (int)blockIdx.y / mt;
+    const int m0 = ((int)blockIdx.y % mt) * TM, n0 = (int)blockIdx.x * TN;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    float acc[GATED ? 2 : 1][4][4] = {};
+    for (int s = 0; s < g.ksegs; ++s) {
+        const void *pa = g.a[g.mhalves == 2 ? half : s];
+        for (int k0 = 0; k0 < g.K; k0 += TK) {
+            for (int i = tid; i < TM * TK; i += 256) {
+                const int m = g.a_t ? i % TM : i / TK, k = g.a_t ? i / TM : i % TK;
+                const int64_t gm = m0 + m, gk = k0 + k;
+                As[k][m] = gm < g.M && gk < g.K ? load_el(pa, g.a_t ? gk * g.lda + gm : gm * g.lda + gk, g.dtype) : 0.f;
+            }
+            for (int i = tid; i < TN * TK; i += 256) {
+                const int n = g.b_t ? i % TN : i / TK, k = g.b_t ? i / TN : i % TK;
+                const int64_t gn = n0 + n, gk = k0 + k;
+                const bool in = gn < g.N && gk < g.K;
+                const int64_t at = g.b_t ? gk * g.ldb + gn : gn * g.ldb + gk;
+                Bs[0][k][n] = in ? load_el(g.b[GATED ? 0 : s], at, g.dtype) : 0.f;
+                if (GATED)
+                    Bs[GATED][k][n] = in ? load_el(g.b[1], at, g.dtype) : 0.f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < TK; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        acc[0][i][j] += As[k][ty * 4 + i] * Bs[0][k][tx + 16 * j];
+                        if (GATED)
+                            acc[GATED][i][j] += As[k][ty * 4 + i] * Bs[GATED][k][tx + 16 * j];
+                    }
+            __syncthreads();
+        }
+    }
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) {
+            const int64_t m = m0 + ty * 4 + i, n = n0 + tx + 16 * j;
+            if (m >= g.M || n >= g.N)
+                continue;
+            float z[2];
+            for (int q = 0; q < (GATED ? 2 : 1); ++q) {
+                z[q] = acc[q][i][j] + (g.bias[q] ? load_el(g.bias[q], n, g.dtype) : 0.f);
+                if (g.save[q])
+                    store_el(g.save[q], m * g.ldsave + n, z[q], g.dtype);
+            }
+            void *out = g.out[half];
+            if (!out)
+                continue;
+            float y = act_value(z[0], g.act);
+            if (GATED)
+                y *= z[1];
+            else if (g.res)
+                y += load_el(g.res, m * g.ldres + n, g.out_dtype);
+            store_el(out, m * g.ldout + n, y, g.out_dtype);
+        }
+}
+
+// dz = dout * act'(a) (linear) or da = dout * b * act'(a), db = dout * act(a)
+// (gated), rounded once to the operands' type: they are operands of the two
+// matrix products that follow, which the matrix cores take in that type.  A
+// thread owns one column of kGradRows rows, so the block's column sums (of the
+// unrounded values) need no joining.
+constexpr int kGradRows = 64;
+
+__global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g)
+{
+    const int64_t half = g.gated ? g.pitch / 2 : g.pitch;
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int t0 = (int)blockIdx.y * kGradRows, t1 = min(g.T, t0 + kGradRows);
+    if (c >= max(half, (int64_t)g.I))
+        return;
+    float sa = 0.f, sb = 0.f;
+    for (int64_t t = t0; t < t1; ++t) {
+        float da = 0.f, db = 0.f;
+        if (c < g.I) {
+            const float d = load_el(g.dout, t * g.lddout + c, g.dout_dtype);
+            float v = 0.f, s = 1.f;
+            if (g.a)
+                act_both(load_el(g.a, t * g.ldab + c, g.dtype), g.act, v, s);
+            da = d * s;
+            if (g.gated) {
+                da *= load_el(g.b, t * g.ldab + c, g.dtype);
+                db = d * v;
+            }
+        }
+        sa += da;
+        sb += db;
+        if (g.dz) {
+            store_el(g.dz, t * g.pitch + c, da, g.dtype);
+            if (g.gated)
+                store_el(g.dz, t * g.pitch + half + c, db, g.dtype);
+        }
+    }
+    if (g.partial && c < g.I) {
+        float *p = g.partial + (int64_t)blockIdx.y * (g.gated ? 2 : 1) * g.I + c;
+        p[0] = sa;
+        if (g.gated)
+            p[g.I] = sb;
+    }
+}
+
+__global__ __launch_bounds__(256) void k_dense_colsum(const float *partial, int row_blocks, int I, int n, int out_dtype,
+                                                      void *out0, void *out1)
+{
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= (int64_t)n * I)
+        return;
+    float s = 0.f;
+    for (int64_t r = 0; r < row_blocks; ++r)
+        s += partial[r * n * I + c];
+    void *out = c < I ? out0 : out1;
+    if (out)
+        store_el(out, c < I ? c : c - I, s, out_dtype);
+}
+
+}  // namespace
+
+int launch_dense_gemm(const DenseGemm &g, hipStream_t st)
+{
+    ProfScope p(g.gated ? "dense_gated" : g.a_t ? "dense_gemm_tn" : g.b_t ? "dense_gemm_nn" : "dense_gemm_nt", st);
+    const dim3 grid((g.N + TN - 1) / TN, (g.M + TM - 1) / TM * g.mhalves);
+    if (g.gated)
+        hipLaunchKernelGGL(k_dense_tile<true>, grid, dim3(256), 0, st, g);
+    else
+        hipLaunchKernelGGL(k_dense_tile<false>, grid, dim3(256), 0, st, g);
+    ECF_HIP_CHECK(hipGetLastError());
+    return ECF_OK;
+}
+
+int dense_grad_row_blocks(int T) { return (T + kGradRows - 1) / kGradRows; }
+
+int launch_dense_grad(const DenseGrad &g, hipStream_t st)
+{
+    ProfScope p("dense_grad", st);
+    const int64_t cols = g.dz ? (g.gated ? g.pitch / 2 : g.pitch) : g.I;
+    hipLaunchKernelGGL(k_dense_grad, dim3((unsigned)((cols + 255) / 256), g.row_blocks), dim3(256), 0, st, g);
+    ECF_HIP_CHECK(hipGetLastError());
+    return ECF_OK;
+}
+
+int launch_dense_colsum(const float *partial, int row_blocks, int I, int n, int out_dtype, void *const out[2],
+                        hipStream_t st)
+{
+    ProfScope p("dense_colsum", st);
+    hipLaunchKernelGGL(k_dense_colsum, dim3((unsigned)(((int64_t)n * I + 255) / 256)), dim3(256), 0, st, partial,
+                       row_blocks, I, n, out_dtype, out[0], out[1]);
+    ECF_HIP_CHECK(hipGetLastError());
+    return ECF_OK;
+}
+
+}  // namespace ecf

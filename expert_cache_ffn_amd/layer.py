@@ -96,3 +96,217 @@ class Layer:
             raise ValueError(f"{T} tokens > workspace capacity {self.max_tokens}")
         assert x.is_contiguous() and out.is_contiguous() and out.dtype == torch.float32
         return L.moe_layer_forward(args, x.data_ptr(), T, out.data_ptr(), want_stats)
+
+
+# ---- dense feed-forward operators -------------------------------------------------
+
+_DENSE_DT = {torch.float32: L.ECF_F32, torch.bfloat16: L.ECF_BF16, torch.float16: L.ECF_F16}
+
+
+def _dense_dt(dtype, what):
+    if dtype not in _DENSE_DT:
+        raise ValueError(f"{what} must be float32, bfloat16 or float16, got {dtype}")
+    return _DENSE_DT[dtype]
+
+
+def _matrix(name, t, rows, cols, dtype, device):
+    """(address, row stride) of a [rows, cols] operand; its rows may lie apart but not overlap."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be a [{rows}, {cols}] tensor, got {tuple(getattr(t, 'shape', ()))}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the weights are on {device}")
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
+        raise ValueError(f"{name} must have contiguous rows (strides {t.stride()})")
+    if rows <= 1:
+        ld = cols  # a single row's stride says nothing
+    elif ld < cols:
+        raise ValueError(f"the rows of {name} overlap (strides {t.stride()}): make it contiguous")
+    return t.data_ptr(), ld
+
+
+def _vector(name, t, n, dtype, device):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.shape != (n,) or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name} must be a [{n}] tensor of {dtype} on {device}")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+class _Dense:
+    """What the two operators share: the weights' checks, workspaces and streams.
+
+    A call runs on the current stream of the weights' device and takes its
+    workspace from torch's allocator for that stream, so calls on several
+    streams, and captured graphs, never share one."""
+
+    def _setup(self, w, act, what):
+        if not isinstance(w, torch.Tensor) or w.dim() != 2 or not w.is_cuda or 0 in w.shape:
+            raise ValueError(f"{what} must be a non-empty 2-D tensor on the GPU")
+        if act not in L.ACTS:
+            raise ValueError(f"act must be one of {sorted(L.ACTS)}, got {act!r}")
+        self.device, self.dtype, self.act = w.device, w.dtype, act
+        self._dt = _dense_dt(w.dtype, what)
+        self._ws_of = {}
+
+    def _tokens(self, x):
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x must be a 2-D tensor [tokens, features]")
+        return x.shape[0]
+
+    def _run(self, fn, a, T, backward):
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self._run(fn, a, T, backward)
+        n = self._ws_of.get((T, backward))
+        if n is None:
+            n = self._ws_bytes(T, backward)
+            if len(self._ws_of) > 4096:
+                self._ws_of.clear()
+            self._ws_of[T, backward] = n
+        if n:
+            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+            a.d_ws, a.ws_bytes = ws.data_ptr(), n
+        a.stream = torch.cuda.current_stream().cuda_stream or None
+        fn(a, T)
+
+    def _wgrad(self, w_grad_dtype):
+        dt = self.dtype if w_grad_dtype is None else w_grad_dtype
+        if dt is not self.dtype and dt is not torch.float32:
+            raise ValueError(f"w_grad_dtype must be {self.dtype} or torch.float32, got {dt}")
+        return dt
+
+    def _out(self, name, t, rows, cols, dtype):
+        if t is None:
+            t = torch.empty((rows, cols), dtype=dtype, device=self.device)
+        return (t,) + _matrix(name, t, rows, cols, dtype, self.device)
+
+
+class GatedProjection(_Dense):
+    """h = act(x W_gate^T + b_gate) * (x W_up^T + b_up): the first half of a gated
+    feed-forward block (SwiGLU with act "silu"), in one kernel.
+
+    w_gate, w_up [inter, hidden] in fp32, bf16 or fp16, with the same row stride;
+    b_gate, b_up [inter] or None.  The object keeps the tensors, so their addresses
+    stay valid; in-place updates of the weights are seen by the next call."""
+
+    def __init__(self, w_gate, w_up, b_gate=None, b_up=None, act="silu"):
+        self._setup(w_gate, act, "w_gate")
+        self.inter, self.hidden = w_gate.shape
+        a = L.GatedArgs()
+        a.hidden, a.inter, a.dtype, a.act = self.hidden, self.inter, self._dt, L.ACTS[act]
+        a.d_w_gate, a.ld_w = _matrix("w_gate", w_gate, self.inter, self.hidden, self.dtype, self.device)
+        a.d_w_up, ld = _matrix("w_up", w_up, self.inter, self.hidden, self.dtype, self.device)
+        if ld != a.ld_w:
+            raise ValueError(f"w_gate and w_up must have the same row stride ({a.ld_w} and {ld})")
+        a.d_b_gate = _vector("b_gate", b_gate, self.inter, self.dtype, self.device)
+        a.d_b_up = _vector("b_up", b_up, self.inter, self.dtype, self.device)
+        self.w_gate, self.w_up, self.b_gate, self.b_up, self._a = w_gate, w_up, b_gate, b_up, a
+
+    def _ws_bytes(self, T, backward):
+        return L.ecf_gated_workspace_bytes(self.hidden, self.inter, self._dt, T, backward)
+
+    def forward(self, x, out=None, save=False):
+        """h [T, inter] (into `out` if given); with save, (h, a, b): also the two
+        sums, rounded to the weights' type, for backward()."""
+        T = self._tokens(x)
+        a = L.GatedArgs.from_buffer_copy(self._a)
+        a.d_x, a.ld_x = _matrix("x", x, T, self.hidden, self.dtype, self.device)
+        h, a.d_h, a.ld_h = self._out("out", out, T, self.inter, self.dtype)
+        if save:
+            sa, a.d_a, a.ld_ab = self._out("a", None, T, self.inter, self.dtype)
+            sb, a.d_b, _ = self._out("b", None, T, self.inter, self.dtype)
+        self._run(L.ecf_gated_forward, a, T, 0)
+        return (h, sa, sb) if save else h
+
+    def backward(self, x, a, b, dh, w_grad_dtype=None, dx=None):
+        """(dx, dw_gate, dw_up, db_gate, db_up) for the gradient dh of h, from the x
+        of the forward call and the a and b it saved; the last two are None without
+        the biases.  Weight and bias gradients come in w_grad_dtype (the weights'
+        type, or torch.float32)."""
+        T, gd = self._tokens(x), self._wgrad(w_grad_dtype)
+        q = L.GatedArgs.from_buffer_copy(self._a)
+        q.wgrad_dtype = _DENSE_DT[gd]
+        q.d_x, q.ld_x = _matrix("x", x, T, self.hidden, self.dtype, self.device)
+        q.d_a, q.ld_ab = _matrix("a", a, T, self.inter, self.dtype, self.device)
+        q.d_b, ld = _matrix("b", b, T, self.inter, self.dtype, self.device)
+        if ld != q.ld_ab:
+            raise ValueError(f"a and b must have the same row stride ({q.ld_ab} and {ld})")
+        q.d_dh, q.ld_dh = _matrix("dh", dh, T, self.inter, self.dtype, self.device)
+        dx, q.d_dx, q.ld_dx = self._out("dx", dx, T, self.hidden, self.dtype)
+        dwg, q.d_dw_gate, q.ld_dw = self._out("dw_gate", None, self.inter, self.hidden, gd)
+        dwu, q.d_dw_up, _ = self._out("dw_up", None, self.inter, self.hidden, gd)
+        dbg = dbu = None
+        if self.b_gate is not None:
+            dbg = torch.empty(self.inter, dtype=gd, device=self.device)
+            q.d_db_gate = dbg.data_ptr()
+        if self.b_up is not None:
+            dbu = torch.empty(self.inter, dtype=gd, device=self.device)
+            q.d_db_up = dbu.data_ptr()
+        self._run(L.ecf_gated_backward, q, T, 1)
+        return dx, dwg, dwu, dbg, dbu
+
+
+class Linear(_Dense):
+    """y = act(x W^T + bias) + residual, with bias, activation and residual in the
+    product's epilogue.
+
+    w [out_features, in_features] in fp32, bf16 or fp16, bias [out_features] or None.
+    y, the residual and dy are of out_dtype: the weights' type, or torch.float32 (the
+    running sum a moe_layer_forward call takes as its residual)."""
+
+    def __init__(self, w, bias=None, act="none", out_dtype=None):
+        self._setup(w, act, "w")
+        self.out_features, self.in_features = w.shape
+        self.out_dtype = w.dtype if out_dtype is None else out_dtype
+        if self.out_dtype is not w.dtype and self.out_dtype is not torch.float32:
+            raise ValueError(f"out_dtype must be {w.dtype} or torch.float32, got {out_dtype}")
+        a = L.LinearArgs()
+        a.in_features, a.out_features, a.dtype, a.act = self.in_features, self.out_features, self._dt, L.ACTS[act]
+        a.out_dtype = _DENSE_DT[self.out_dtype]
+        a.d_w, a.ld_w = _matrix("w", w, self.out_features, self.in_features, self.dtype, self.device)
+        a.d_bias = _vector("bias", bias, self.out_features, self.dtype, self.device)
+        self.w, self.bias, self._a = w, bias, a
+
+    def _ws_bytes(self, T, backward):
+        return L.ecf_linear_workspace_bytes(self.in_features, self.out_features, self._dt, T, backward)
+
+    def forward(self, x, residual=None, out=None, save=False):
+        """y [T, out_features] (into `out` if given, which may be the residual); with
+        save, (y, z): also z = x W^T + bias, rounded to the weights' type, for
+        backward() through an activation."""
+        T = self._tokens(x)
+        a = L.LinearArgs.from_buffer_copy(self._a)
+        a.d_x, a.ld_x = _matrix("x", x, T, self.in_features, self.dtype, self.device)
+        if residual is not None:
+            a.d_residual, a.ld_residual = _matrix("residual", residual, T, self.out_features, self.out_dtype,
+                                                  self.device)
+        y, a.d_out, a.ld_out = self._out("out", out, T, self.out_features, self.out_dtype)
+        if save:
+            z, a.d_z, a.ld_z = self._out("z", None, T, self.out_features, self.dtype)
+        self._run(L.ecf_linear_forward, a, T, 0)
+        return (y, z) if save else y
+
+    def backward(self, x, dout, z=None, w_grad_dtype=None, dx=None):
+        """(dx, dw, dbias) for the gradient dout of y, from the x of the forward call
+        and, with an activation, the z it saved; dbias is None without a bias.  The
+        residual's gradient is dout itself."""
+        T, gd = self._tokens(x), self._wgrad(w_grad_dtype)
+        q = L.LinearArgs.from_buffer_copy(self._a)
+        q.wgrad_dtype = _DENSE_DT[gd]
+        q.d_x, q.ld_x = _matrix("x", x, T, self.in_features, self.dtype, self.device)
+        if self.act != "none":
+            q.d_z, q.ld_z = _matrix("z", z, T, self.out_features, self.dtype, self.device)
+        q.d_dout, q.ld_dout = _matrix("dout", dout, T, self.out_features, self.out_dtype, self.device)
+        dx, q.d_dx, q.ld_dx = self._out("dx", dx, T, self.in_features, self.dtype)
+        dw, q.d_dw, q.ld_dw = self._out("dw", None, self.out_features, self.in_features, gd)
+        db = None
+        if self.bias is not None:
+            db = torch.empty(self.out_features, dtype=gd, device=self.device)
+            q.d_dbias = db.data_ptr()
+        self._run(L.ecf_linear_backward, q, T, 1)
+        return dx, dw, db

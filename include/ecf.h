@@ -58,7 +58,12 @@ extern "C" {
 const char *ecf_last_error(void);
 
 /* ---- shapes and expert blobs ------------------------------------------------- */
-typedef enum { ECF_F32 = 0, ECF_BF16 = 1, ECF_MXFP4 = 2 } ecf_dtype;
+typedef enum {
+    ECF_F32 = 0,
+    ECF_BF16 = 1,
+    ECF_MXFP4 = 2,
+    ECF_F16 = 3 /* IEEE half; the dense feed-forward operators only */
+} ecf_dtype;
 
 typedef struct {
     int32_t hidden;      /* d: model width; multiple of 256 */
@@ -329,6 +334,115 @@ typedef struct {
 int ecf_bandwidth_profile(const ecf_shape *shape, int32_t n_blobs, const void *const *h_blobs,
                           int32_t host_threads, void *d_buf, size_t d_buf_bytes, void *copy_stream,
                           double seconds, ecf_bw_profile *out);
+
+/* ---- dense feed-forward operators --------------------------------------------------
+ * What every token passes beside or instead of routed experts: a shared expert, a
+ * dense layer, a projection with residual.  Two operators, each with its backward
+ * pass, in fp32, bf16 or fp16 (ECF_F16; these operators only):
+ *
+ *   gated   h[t][i] = act(a) * b,  a = x[t] . W_gate[i] + b_gate[i],
+ *                                  b = x[t] . W_up[i] + b_up[i]
+ *   linear  y[t][n] = act(z) + residual[t][n],  z = x[t] . W[n] + bias[n]
+ *
+ * A gated call and a linear call with W_down and the running fp32 sum as its residual
+ * are a shared expert; that sum may be an ecf_layer_args.d_residual.
+ *
+ * Matrices are row-major with the given row strides, in elements (0 = rows without
+ * gaps); rows may start at any address that is a multiple of the element size, and
+ * sizes may be any number from 1 to 2^22 (n_tokens also 0: nothing is written by a
+ * forward call, weight and bias gradients are zeros).  256 rows of any operand must
+ * span less than 2 GiB (ECF_EUNSUPPORTED otherwise).  Nothing between the end of a row
+ * and the next row's start is read or written.  Products are summed in fp32, biases,
+ * activations and residuals are applied to the fp32 sums, and each output is rounded
+ * once; the backward passes also round da, db and dz once to `dtype`, the type that
+ * the two products behind them multiply.  Results do not depend on what runs beside a
+ * call, and the same call gives the same bits.  An infinite or NaN element makes
+ * outputs infinite or NaN only in rows (columns) that it is part of.
+ *
+ * d_ws needs ecf_*_workspace_bytes bytes at a 256-byte boundary (where that is 0 it may be
+ * NULL), holds nothing between calls, and must not be shared by calls that may overlap (two
+ * streams, two captured graphs that may run at once).  Calls are asynchronous on
+ * `stream`, a stream of the current device, allocate nothing and can be captured.
+ * Outputs must not overlap inputs, except that d_out may be d_residual (same stride).
+ */
+typedef enum {
+    ECF_ACT_NONE = 0,
+    ECF_ACT_SILU = 1,
+    ECF_ACT_GELU = 2,      /* v * Phi(v) */
+    ECF_ACT_GELU_TANH = 3, /* its tanh form */
+    ECF_ACT_RELU = 4       /* derivative 0 at 0 */
+} ecf_act;
+
+typedef struct {
+    int32_t hidden, inter;           /* d, I */
+    int32_t dtype;                   /* of every tensor below but the weight gradients */
+    int32_t act;                     /* ecf_act */
+    const void *d_x;                 /* [T][d] */
+    const void *d_w_gate, *d_w_up;   /* [I][d] each, both with stride ld_w */
+    const void *d_b_gate, *d_b_up;   /* [I] or NULL (forward only) */
+    int64_t ld_x, ld_w;
+    void *d_h;                       /* forward: [T][I]; may be NULL where d_a and d_b are given */
+    int64_t ld_h;
+    void *d_a, *d_b;                 /* [T][I] each, both with stride ld_ab: the sums a and b as the
+                                        backward pass takes them.  Forward: both written, or both NULL.
+                                        Backward: both read */
+    int64_t ld_ab;
+    /* backward only */
+    const void *d_dh;                /* [T][I] */
+    int64_t ld_dh;
+    void *d_dx;                      /* [T][d] or NULL: not wanted */
+    int64_t ld_dx;
+    int32_t wgrad_dtype;             /* of the four below: `dtype` or ECF_F32 */
+    void *d_dw_gate, *d_dw_up;       /* [I][d] each, both with stride ld_dw; both or neither */
+    int64_t ld_dw;
+    void *d_db_gate, *d_db_up;       /* [I], each may be NULL */
+    void *d_ws;
+    size_t ws_bytes;
+    void *stream;
+} ecf_gated_args;
+
+/* Workspace bytes of a call of up to n_tokens tokens (backward 0 or 1); 0 for a valid
+ * shape that needs none; SIZE_MAX for an invalid shape (ecf_last_error says why). */
+size_t ecf_gated_workspace_bytes(int32_t hidden, int32_t inter, int32_t dtype, int32_t n_tokens, int32_t backward);
+int ecf_gated_forward(const ecf_gated_args *args, int32_t n_tokens);
+/* dx = da W_gate + db W_up, dW_gate = da^T x, dW_up = db^T x, db_gate = sum_t da,
+ * db_up = sum_t db, with da = dh * b * act'(a), db = dh * act(a). */
+int ecf_gated_backward(const ecf_gated_args *args, int32_t n_tokens);
+
+typedef struct {
+    int32_t in_features, out_features; /* K, N */
+    int32_t dtype;                   /* of x, W, bias, z and dx */
+    int32_t out_dtype;               /* of y, the residual and dy: `dtype` or ECF_F32 */
+    int32_t act;                     /* ecf_act */
+    const void *d_x;                 /* [T][K] */
+    const void *d_w;                 /* [N][K] */
+    const void *d_bias;              /* [N] or NULL (forward only) */
+    const void *d_residual;          /* [T][N] or NULL (forward only; its gradient is dy) */
+    int64_t ld_x, ld_w, ld_residual;
+    void *d_out;                     /* forward: y [T][N] */
+    int64_t ld_out;
+    void *d_z;                       /* [T][N], z as the backward pass takes it.  Forward: written, or NULL.
+                                        Backward: read where act is not ECF_ACT_NONE */
+    int64_t ld_z;
+    /* backward only */
+    const void *d_dout;              /* dy [T][N] */
+    int64_t ld_dout;
+    void *d_dx;                      /* [T][K] or NULL */
+    int64_t ld_dx;
+    int32_t wgrad_dtype;             /* of the two below: `dtype` or ECF_F32 */
+    void *d_dw;                      /* [N][K] or NULL */
+    int64_t ld_dw;
+    void *d_dbias;                   /* [N] or NULL */
+    void *d_ws;
+    size_t ws_bytes;
+    void *stream;
+} ecf_linear_args;
+
+size_t ecf_linear_workspace_bytes(int32_t in_features, int32_t out_features, int32_t dtype, int32_t n_tokens,
+                                  int32_t backward);
+int ecf_linear_forward(const ecf_linear_args *args, int32_t n_tokens);
+/* dx = dz W, dW = dz^T x, dbias = sum_t dz, with dz = dy * act'(z). */
+int ecf_linear_backward(const ecf_linear_args *args, int32_t n_tokens);
 
 /* ---- measurement hooks ------------------------------------------------------------- */
 /* When enabled, every kernel launch is bracketed by HIP events on its stream

@@ -1,0 +1,410 @@
+"""GPU tests of the dense feed-forward operators against the 64-bit reference of
+dense_ref.py: types, activations, odd sizes, strides and alignment, long
+offsets, special values, streams, graphs, and the block they form together."""
+import numpy as np
+import pytest
+import torch
+
+import dense_ref as R
+import ecf_synth as syn
+import expert_cache_ffn_amd as ecf
+from expert_cache_ffn_amd.layer import GatedProjection, Linear
+from gpu_util import Case, say
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+ACTS = ["silu", "gelu", "gelu_tanh", "relu", "none"]
+
+
+def rand(seed, *shape, std=1.0, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g, dtype=torch.float64) * std).to(dtype).cuda()
+
+
+def strided(t, pad, shift):
+    """The same values in rows `pad` elements further apart, starting `shift` elements in; the
+    gaps hold NaN.  Returns (view, whole buffer)."""
+    rows, cols = t.shape
+    ld = cols + pad
+    buf = torch.full((rows * ld + shift,), float("nan"), dtype=t.dtype, device=t.device)
+    v = buf[shift:].view(rows, ld)[:, :cols]
+    v.copy_(t)
+    return v, buf
+
+
+def d64(*ts):
+    return [None if t is None else t.double() for t in ts]
+
+
+# (tokens, d, I): one of everything, single rows and columns, sizes off every tile and vector width, and
+# sizes where each kind of call changes its tiles
+SIZES = [(1, 1, 1), (1, 8, 3), (2, 7, 1), (3, 65, 17), (4, 64, 64), (5, 130, 36), (8, 520, 100), (16, 256, 128),
+         (17, 1000, 33), (31, 96, 264), (33, 72, 200), (64, 256, 128), (65, 129, 131), (100, 512, 72), (127, 257, 255),
+         (128, 128, 128), (200, 264, 520), (257, 320, 65), (300, 136, 1030), (513, 200, 392)]
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,d,I", SIZES)
+def test_gated_forward(T, d, I, dt):
+    say(f"case: gated forward T {T} d {d} I {I} {dt}")
+    dtype = DT[dt]
+    x, wg, wu = rand(1, T, d, dtype=dtype), rand(2, I, d, std=d ** -.5, dtype=dtype), rand(3, I, d, std=d ** -.5, dtype=dtype)
+    act = ACTS[(T + d + I) % 4]
+    bg, bu = (rand(4, I, dtype=dtype), rand(5, I, dtype=dtype)) if (d + I) % 2 else (None, None)
+    layer = GatedProjection(wg, wu, bg, bu, act=act)
+    ref = R.gated_forward(*d64(x, wg, wu, bg, bu), act, dtype)
+    h, a, b = layer.forward(x, save=True)
+    for name, got in (("h", h), ("a", a), ("b", b)):
+        R.check(name, got, ref[name])
+    assert torch.equal(layer.forward(x), h), "saving changes h, or two calls differ"
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,d,I", SIZES)
+def test_gated_backward(T, d, I, dt):
+    say(f"case: gated backward T {T} d {d} I {I} {dt}")
+    dtype = DT[dt]
+    x, wg, wu = rand(1, T, d, dtype=dtype), rand(2, I, d, std=d ** -.5, dtype=dtype), rand(3, I, d, std=d ** -.5, dtype=dtype)
+    a, b, dh = rand(6, T, I, dtype=dtype), rand(7, T, I, dtype=dtype), rand(8, T, I, std=0.1, dtype=dtype)
+    act = ACTS[(T + d + I) % 5]
+    gd = torch.float32 if T % 2 else dtype
+    bg = rand(4, I, dtype=dtype) if I % 3 else None
+    bu = rand(5, I, dtype=dtype) if I % 2 else None
+    layer = GatedProjection(wg, wu, bg, bu, act=act)
+    ref = R.gated_backward(*d64(x, wg, wu, a, b, dh), act, dtype, gd)
+    outs = layer.backward(x, a, b, dh, w_grad_dtype=gd)
+    for name, got in zip(("dx", "dw_gate", "dw_up", "db_gate", "db_up"), outs):
+        if name == "db_gate" and bg is None or name == "db_up" and bu is None:
+            assert got is None
+        else:
+            R.check(name, got, ref[name])
+    again = layer.backward(x, a, b, dh, w_grad_dtype=gd)
+    assert all(p is None or torch.equal(p, q) for p, q in zip(outs, again)), "two calls differ"
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,K,N", SIZES)
+def test_linear_forward(T, K, N, dt):
+    say(f"case: linear forward T {T} K {K} N {N} {dt}")
+    dtype = DT[dt]
+    out_dtype = torch.float32 if (T + N) % 2 else dtype
+    x, w = rand(1, T, K, dtype=dtype), rand(2, N, K, std=K ** -.5, dtype=dtype)
+    bias = rand(4, N, dtype=dtype) if K % 2 == 0 else None
+    residual = rand(5, T, N, dtype=out_dtype) if T % 3 else None
+    act = ACTS[(T + K + N) % 5]
+    layer = Linear(w, bias, act=act, out_dtype=out_dtype)
+    ref = R.linear_forward(*d64(x, w, bias), act, None if residual is None else residual.double(), dtype, out_dtype)
+    y, z = layer.forward(x, residual=residual, save=True)
+    R.check("z", z, ref["z"])
+    R.check("y", y, ref["y"])
+    if residual is not None:  # into the residual itself
+        run = residual.clone()
+        assert layer.forward(x, residual=run, out=run) is run
+        assert torch.equal(run, y), "in place differs"
+    else:
+        assert torch.equal(layer.forward(x), y)
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,K,N", SIZES)
+def test_linear_backward(T, K, N, dt):
+    say(f"case: linear backward T {T} K {K} N {N} {dt}")
+    dtype = DT[dt]
+    out_dtype = torch.float32 if (T + N) % 2 else dtype
+    gd = torch.float32 if K % 2 else dtype
+    act = ACTS[(T + K + N) % 5]
+    x, w = rand(1, T, K, dtype=dtype), rand(2, N, K, std=K ** -.5, dtype=dtype)
+    z, dout = rand(6, T, N, dtype=dtype), rand(8, T, N, std=0.1, dtype=out_dtype)
+    bias = rand(4, N, dtype=dtype) if N % 2 else None
+    layer = Linear(w, bias, act=act, out_dtype=out_dtype)
+    ref = R.linear_backward(*d64(x, w, z, dout), act, dtype, out_dtype, gd)
+    outs = layer.backward(x, dout, z=z, w_grad_dtype=gd)
+    for name, got in zip(("dx", "dw", "dbias"), outs):
+        if name == "dbias" and bias is None:
+            assert got is None
+        else:
+            R.check(name, got, ref[name])
+    again = layer.backward(x, dout, z=z, w_grad_dtype=gd)
+    assert all(p is None or torch.equal(p, q) for p, q in zip(outs, again)), "two calls differ"
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,d,I,pad,shift", [(3, 64, 40, 8, 0), (33, 128, 72, 8, 8), (70, 96, 136, 3, 1), (9, 65, 31, 1, 1),
+                                             (130, 256, 128, 64, 64), (20, 40, 24, 7, 5)])
+def test_strides_and_alignment(T, d, I, pad, shift, dt):
+    """Rows further apart than they are long, starting anywhere: the gaps (NaN)
+    are neither read nor written."""
+    say(f"case: strides T {T} d {d} I {I} pad {pad} shift {shift} {dt}")
+    dtype = DT[dt]
+    vals = dict(x=rand(1, T, d, dtype=dtype), wg=rand(2, I, d, std=d ** -.5, dtype=dtype),
+                wu=rand(3, I, d, std=d ** -.5, dtype=dtype), a=rand(6, T, I, dtype=dtype), b=rand(7, T, I, dtype=dtype),
+                dh=rand(8, T, I, std=.1, dtype=dtype), wd=rand(9, d, I, std=I ** -.5, dtype=dtype),
+                res=rand(10, T, d, dtype=dtype))
+    v = {k: strided(t, pad, shift)[0] for k, t in vals.items()}
+    layer = GatedProjection(v["wg"], v["wu"], act="silu")
+    h, hbuf = strided(torch.zeros(T, I, dtype=dtype, device="cuda"), pad, shift)
+    layer.forward(v["x"], out=h)
+    R.check("h", h, R.gated_forward(*d64(vals["x"], vals["wg"], vals["wu"]), None, None, "silu", dtype)["h"])
+    assert int(hbuf.isnan().sum()) == hbuf.numel() - T * I, "something beside h was written"
+    dx, dxbuf = strided(torch.zeros(T, d, dtype=dtype, device="cuda"), pad, shift)
+    outs = layer.backward(v["x"], v["a"], v["b"], v["dh"], dx=dx)
+    ref = R.gated_backward(*d64(*(vals[k] for k in ("x", "wg", "wu", "a", "b", "dh"))), "silu", dtype, dtype)
+    for name, got in zip(("dx", "dw_gate", "dw_up"), outs):
+        R.check(name, got, ref[name])
+    assert int(dxbuf.isnan().sum()) == dxbuf.numel() - T * d, "something beside dx was written"
+    lin = Linear(v["wd"])
+    y, ybuf = strided(torch.zeros(T, d, dtype=dtype, device="cuda"), pad, shift)
+    lin.forward(v["dh"], residual=v["res"], out=y)
+    R.check("y", y, R.linear_forward(*d64(vals["dh"], vals["wd"]), None, "none", vals["res"].double(), dtype, dtype)["y"])
+    assert int(ybuf.isnan().sum()) == ybuf.numel() - T * d, "something beside y was written"
+    outs = lin.backward(v["dh"], v["res"])
+    ref = R.linear_backward(*d64(vals["dh"], vals["wd"]), None, vals["res"].double(), "none", dtype, dtype, dtype)
+    for name, got in zip(("dx", "dw"), outs):
+        R.check(name, got, ref[name])
+
+
+@pytest.mark.parametrize("dt", DT)
+def test_no_tokens(dt):
+    dtype = DT[dt]
+    wg, wu, bias = rand(2, 40, 64, dtype=dtype), rand(3, 40, 64, dtype=dtype), rand(4, 40, dtype=dtype)
+    none = torch.empty(0, 64, dtype=dtype, device="cuda")
+    empty = torch.empty(0, 40, dtype=dtype, device="cuda")
+    g = GatedProjection(wg, wu, bias, bias)
+    assert g.forward(none).shape == (0, 40)
+    dx, *rest = g.backward(none, empty, empty, empty)
+    assert dx.shape == (0, 64) and all(not t.any() and t.isfinite().all() for t in rest)
+    lin = Linear(wg, bias, act="gelu")
+    assert lin.forward(none).shape == (0, 40)
+    dx, dw, db = lin.backward(none, empty, z=empty)
+    assert dx.shape == (0, 64) and not dw.any() and not db.any() and dw.isfinite().all() and db.isfinite().all()
+
+
+@pytest.mark.parametrize("T", [1, 5, 16, 40, 200])
+@pytest.mark.parametrize("dt", DT)
+def test_special_values_stay_in_their_row(dt, T):
+    """An infinity or NaN in one token's row, or one weight's row, spoils what it
+    is part of and nothing else."""
+    say(f"case: special values T {T} {dt}")
+    dtype, d, I = DT[dt], 136, 72
+    x, wg, wu = rand(1, T, d, dtype=dtype), rand(2, I, d, std=d ** -.5, dtype=dtype), rand(3, I, d, std=d ** -.5, dtype=dtype)
+    clean = GatedProjection(wg, wu).forward(x)
+    ylin = Linear(wg, out_dtype=torch.float32).forward(x)
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        xb = x.clone()
+        xb[T // 2, 5] = bad
+        h, y = GatedProjection(wg, wu).forward(xb), Linear(wg, out_dtype=torch.float32).forward(xb)
+        rows = torch.arange(T, device="cuda") != T // 2
+        assert torch.equal(h[rows], clean[rows]) and torch.equal(y[rows], ylin[rows])
+        if bad != bad:
+            assert h[T // 2].isnan().all() and y[T // 2].isnan().all()
+        else:  # an infinity times a weight that is not zero
+            want = torch.where(wg[:, 5] > 0, bad, -bad).float()
+            want[wg[:, 5] == 0] = float("nan")
+            assert torch.equal(y[T // 2][wg[:, 5] != 0], want[wg[:, 5] != 0])
+        wb = wg.clone()
+        wb[7, 3] = bad
+        h = GatedProjection(wb, wu).forward(x)
+        cols = torch.arange(I, device="cuda") != 7
+        assert torch.equal(h[:, cols], clean[:, cols])
+        if bad != bad:
+            assert h[:, 7].isnan().all()
+        # backward: dx keeps to the row, dW to the column of x
+        a, b, dh = rand(6, T, I, dtype=dtype), rand(7, T, I, dtype=dtype), rand(8, T, I, std=.1, dtype=dtype)
+        g = GatedProjection(wg, wu)
+        c, s = g.backward(x, a, b, dh), g.backward(xb, a, b, dh)
+        assert torch.equal(c[0], s[0])
+        cols = torch.arange(d, device="cuda") != 5
+        assert torch.equal(c[1][:, cols], s[1][:, cols]) and torch.equal(c[2][:, cols], s[2][:, cols])
+        assert not s[1][:, 5].isfinite().any()
+        dhb = dh.clone()
+        dhb[T // 2, 9] = bad
+        s = g.backward(x, a, b, dhb)
+        assert torch.equal(c[0][rows], s[0][rows])
+        keep = torch.arange(I, device="cuda") != 9
+        assert torch.equal(c[1][keep], s[1][keep]) and torch.equal(c[2][keep], s[2][keep])
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_activation_range(act):
+    """Every activation and its derivative from -inf to inf, NaN included, through
+    a product with the identity."""
+    v = torch.cat([torch.tensor([0.0, -0.0, float("inf"), float("-inf"), float("nan"), 3e38, -3e38, 1e-40]),
+                   torch.linspace(-30, 30, 441), torch.logspace(-6, 38, 60), -torch.logspace(-6, 38, 60)]).cuda()
+    v = v[:, None].contiguous()
+    one = torch.ones(1, 1, device="cuda")
+    fin = v[:, 0].isfinite()
+    y, z = Linear(one, act=act).forward(v, save=True)
+    assert torch.equal(z[fin], v[fin])
+    ref, slope = R.act_both(v.double(), act)
+    ok = (y.double() - ref).abs() <= ref.abs() * (R.act_rel(v.double().clamp(-40, 40)) + 2 ** -24) + 1e-37
+    assert ok[fin].all(), v[fin][~ok[fin]]
+    dx, _, = Linear(one, act=act).backward(v, torch.ones_like(v), z=v)[:2]
+    tol = (1 + v.double().abs().clamp(max=40)) * (R.act_rel(v.double().clamp(-40, 40)) + 4 * R.EPS23)
+    ok = (dx.double() - torch.where(v.double().abs() > 40, (v > 0).double() if act != "none" else 1.0, slope)).abs() <= tol
+    assert ok[fin].all(), v[fin][~ok[fin]]
+    inf, ninf, nan = (int(i) for i in (2, 3, 4))
+    assert y[inf] == float("inf") and y[nan].isnan().all() and dx[nan].isnan().all() == (act != "none")
+    assert y[ninf] == (float("-inf") if act == "none" else 0.0)
+    assert dx[inf] == 1.0 and dx[ninf] == (1.0 if act == "none" else 0.0)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_offsets_past_32_bits(dt):
+    """Outputs, saved sums and dz longer than 2^32 bytes (bf16: 2^31 elements too)."""
+    dtype, K, N = DT[dt], 24, 8192
+    T = 300_000 if dt == "bf16" else 140_000
+    say(f"case: long offsets T {T} N {N} {dt}")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, K, generator=g, device="cuda").to(dtype)
+    w = (torch.randn(N, K, generator=g, device="cuda") * K ** -.5).to(dtype)
+    y, z = Linear(w, act="silu").forward(x, save=True)
+    rows = torch.tensor([0, 1, T // 3, 131_071, 131_072, 131_073, T - 2, T - 1], device="cuda")
+    ref = R.linear_forward(*d64(x[rows], w), None, "silu", None, dtype, dtype)
+    R.check("y", y[rows], ref["y"])
+    R.check("z", z[rows], ref["z"])
+    dx, dw, _ = Linear(w, act="silu").backward(x, y, z=z, w_grad_dtype=torch.float32)
+    cols = torch.tensor([0, 5, N - 1], device="cuda")
+    zc, yc, xc = z[:, cols].double(), y[:, cols].double(), x.double()
+    part = R.linear_backward(xc, w[cols].double(), zc, yc, "silu", dtype, dtype, torch.float32)
+    R.check("dw", dw[cols], part["dw"])
+    del zc, yc, xc, part
+    ref = R.linear_backward(*d64(x[rows], w, z[rows], y[rows]), "silu", dtype, dtype, torch.float32)
+    R.check("dx", dx[rows], ref["dx"])
+
+
+@pytest.mark.parametrize("T,d,I,dt", [(1, 64, 48, "bf16"), (16, 256, 128, "bf16"), (100, 136, 72, "f16"), (70, 65, 33, "f32"),
+                                      (300, 512, 256, "bf16")])
+def test_graph_and_streams(T, d, I, dt):
+    """Both operators, forward and backward, captured once and replayed with new
+    inputs between eager work; two graphs replayed on two streams at once."""
+    say(f"case: graph T {T} d {d} I {I} {dt}")
+    dtype = DT[dt]
+    wg, wu, wd = (rand(s, *sh, std=.1, dtype=dtype) for s, sh in ((2, (I, d)), (3, (I, d)), (4, (d, I))))
+    bias = rand(5, I, dtype=dtype)
+    gp, lin = GatedProjection(wg, wu, bias, bias), Linear(wd, out_dtype=torch.float32)
+
+    def step(x, dy):
+        h, a, b = gp.forward(x, save=True)
+        y = lin.forward(h, residual=dy)
+        dh, dwd, _ = lin.backward(h, dy)
+        return (h, y, dh, dwd) + gp.backward(x, a, b, dh)
+
+    xs = [rand(20 + i, T, d, dtype=dtype) for i in range(4)]
+    dys = [rand(30 + i, T, d) for i in range(4)]
+    want = [step(x, dy) for x, dy in zip(xs, dys)]
+    torch.cuda.synchronize()
+    graphs = []
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        sx, sdy = xs[0].clone(), dys[0].clone()
+        with torch.cuda.stream(side):
+            side.wait_stream(torch.cuda.default_stream())
+            step(sx, sdy)
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs = step(sx, sdy)
+        graphs.append((g, sx, sdy, outs))
+    for i in (0, 1, 2, 3, 1):
+        for g, sx, sdy, outs in graphs[:1]:
+            sx.copy_(xs[i])
+            sdy.copy_(dys[i])
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(outs, want[i])), f"replay of input {i} differs"
+            again = step(xs[(i + 1) % 4], dys[(i + 1) % 4])  # eager work between replays
+            assert all(torch.equal(p, q) for p, q in zip(again, want[(i + 1) % 4]))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for k, (g, sx, sdy, outs) in enumerate(graphs):
+        sx.copy_(xs[k + 1])
+        sdy.copy_(dys[k + 1])
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (g, *_), s in zip(graphs, (s1, s2)):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for k, (g, sx, sdy, outs) in enumerate(graphs):
+        assert all(torch.equal(p, q) for p, q in zip(outs, want[k + 1])), "graphs replayed side by side differ"
+    # eager calls of one object on two streams at once
+    got = []
+    for k, s in enumerate((s1, s2)):
+        with torch.cuda.stream(s):
+            for _ in range(4):
+                got.append((k, step(xs[k], dys[k])))
+    torch.cuda.synchronize()
+    for k, outs in got:
+        assert all(torch.equal(p, q) for p, q in zip(outs, want[k])), "calls on two streams differ"
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_block_gradients_against_differences(act):
+    """A feed-forward block y = x' + W_down gated(x) in fp32, forward and backward
+    through both operators, against central differences of its 64-bit form."""
+    T, d, I = 37, 48, 40
+    x, dy = rand(1, T, d), rand(2, T, d)
+    wg, wu, wd = rand(3, I, d, std=d ** -.5), rand(4, I, d, std=d ** -.5), rand(5, d, I, std=I ** -.5)
+    bg, bu, bd = rand(6, I, std=.1), rand(7, I, std=.1), rand(8, d, std=.1)
+    gp, lin = GatedProjection(wg, wu, bg, bu, act=act), Linear(wd, bd)
+    h, a, b = gp.forward(x, save=True)
+    dh, dwd, dbd = lin.backward(h, dy)
+    dx, dwg, dwu, dbg, dbu = gp.backward(x, a, b, dh)
+    grads = [dx + dy, dwg, dwu, dbg, dbu, dwd, dbd]
+    params = d64(x, wg, wu, bg, bu, wd, bd)
+
+    def loss(x, wg, wu, bg, bu, wd, bd):
+        h = R.act_both(x @ wg.t() + bg, act)[0] * (x @ wu.t() + bu)
+        return float(((x + h @ wd.t() + bd) * dy.double()).sum())
+
+    # Central differences of step e along a unit-scale direction are within e^2/6 times the third derivative
+    # (of order |loss terms| here) plus 2^-52 |loss| / e: about 1e-8 and 1e-9 relative at e = 1e-4.  The
+    # fp32 gradients are within 1e-5 of theirs (sums of at most 48 products).
+    e = 1e-4
+    for i, g in enumerate(grads):
+        v = rand(50 + i, *g.shape).double()
+        lo, hi = list(params), list(params)
+        lo[i], hi[i] = params[i] - e * v, params[i] + e * v
+        num = (loss(*hi) - loss(*lo)) / (2 * e)
+        ana = float((g.double() * v).sum())
+        scale = float((g.double() * v).norm()) + 1e-9
+        assert abs(num - ana) <= 1e-4 * scale, (i, num, ana, scale)
+
+
+@pytest.mark.parametrize("T", [1, 16, 300])
+def test_shared_expert_beside_the_moe_layer(T):
+    """The use these operators are for: a shared expert beside routed ones.  The
+    gated projection and the linear layer write x' + shared(x) in fp32, which the
+    MoE layer takes as its residual."""
+    say(f"case: shared expert beside the layer, T {T}")
+    cfg = syn.gen.Config(190, "shared", (T,), 512, 8, 256, 2, "bf16", "bf16", "router")
+    case = Case(cfg, T)
+    x = case.x.cuda()
+    wg, wu = rand(41, 384, 512, std=512 ** -.5, dtype=torch.bfloat16), rand(42, 384, 512, std=512 ** -.5, dtype=torch.bfloat16)
+    wd = rand(43, 512, 384, std=384 ** -.5, dtype=torch.bfloat16)
+    stream = rand(44, T, 512)
+    h = GatedProjection(wg, wu).forward(x)
+    run = stream.clone()
+    Linear(wd, out_dtype=torch.float32).forward(h, residual=run, out=run)
+    href = R.gated_forward(*d64(x, wg, wu), None, None, "silu", torch.bfloat16)["h"]
+    y, bound = R.product(href[0], wd.double(), href[1])
+    shared = (stream.double() + y, bound + (stream.double() + y).abs() * 2.0 ** -23)
+    R.check("shared", run, shared)
+    alone = case.run()["out"]
+    both = case.run(residual=run)["out"]
+    # the layer adds its residual to the finished sum: one fp32 rounding
+    want = alone.astype(np.float64) + run.double().cpu().numpy()
+    assert np.all(np.abs(both - want) <= np.abs(want) * 2.0 ** -23 + 1e-30)
+
+
+def test_another_device_is_refused_or_served():
+    """Tensors must share the weights' device; a call made while another device
+    is current runs on the weights' own."""
+    w = rand(1, 8, 16)
+    with pytest.raises(ValueError):
+        Linear(w).forward(torch.zeros(2, 16))
+    if torch.cuda.device_count() > 1:
+        x = rand(2, 3, 16)
+        want = Linear(w).forward(x)
+        with torch.cuda.device(1):
+            assert torch.equal(Linear(w).forward(x), want)
