@@ -43,6 +43,14 @@ int check_matrix(const char *what, const char *name, const void *p, int64_t ld, 
     return ECF_OK;
 }
 
+// Rows of dz in the workspace obey the same limit.
+int check_pitch(const char *what, int64_t pitch, int dtype)
+{
+    if (pitch > (int64_t)(0x7fffffff / 256 / dense_esize(dtype)))
+        return set_error(ECF_EUNSUPPORTED, "%s: 256 rows of %lld gradients span 2 GiB or more", what, (long long)pitch);
+    return ECF_OK;
+}
+
 int check_vector(const char *what, const char *name, const void *p, int dtype)
 {
     if ((uintptr_t)p % dense_esize(dtype))
@@ -82,18 +90,20 @@ int check_grad_dtype(const char *what, int32_t t, int32_t dtype)
             return _rc;                \
     } while (0)
 
-// Backward workspace: dz rows in `dtype` (gated: da and db halves of one row),
-// then the column sums of each row block in fp32.
+// Backward workspace: dz rows in `dtype` (gated: da and db halves of one row,
+// each half's rows at 16-byte boundaries), the column sums of each row block in
+// fp32, and the partial sums of whichever product runs.
 struct BackWs {
     int64_t pitch;
-    size_t partial, total;
+    size_t colsum, split, total;
 };
-BackWs back_ws(int64_t cols, int halves, int dtype, int32_t T)
+BackWs back_ws(int64_t in, int64_t cols, int halves, int dtype, int32_t T)
 {
     BackWs w;
-    w.pitch = halves * cols;
-    w.partial = al256((size_t)T * w.pitch * dense_esize(dtype));
-    w.total = w.partial + al256((size_t)dense_grad_row_blocks(T) * halves * cols * 4);
+    w.pitch = halves * ((cols + 7) / 8 * 8);
+    w.colsum = al256((size_t)T * w.pitch * dense_esize(dtype));
+    w.split = w.colsum + al256((size_t)dense_grad_row_blocks(T) * halves * cols * 4);
+    w.total = w.split + std::max(dense_gemm_ws(dtype, T, in, 1), dense_gemm_ws(dtype, cols, in, halves));
     return w;
 }
 
@@ -108,7 +118,7 @@ size_t ecf_gated_workspace_bytes(int32_t hidden, int32_t inter, int32_t dtype, i
 {
     if (check_common("ecf_gated_workspace_bytes", hidden, inter, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
-    return backward ? back_ws(inter, 2, dtype, n_tokens).total : 0;
+    return backward ? back_ws(hidden, inter, 2, dtype, n_tokens).total : dense_gemm_ws(dtype, n_tokens, inter, 2);
 }
 
 int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
@@ -143,12 +153,14 @@ int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
             DENSE_TRY(check_matrix(me, "d_a", a->d_a, g.ldsave, I, a->dtype));
             DENSE_TRY(check_matrix(me, "d_b", a->d_b, g.ldsave, I, a->dtype));
         }
+        const size_t need = dense_gemm_ws(a->dtype, T, I, 2);
+        DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, need));
         g.a[0] = a->d_x;
         g.b[0] = a->d_w_gate, g.b[1] = a->d_w_up;
         g.bias[0] = a->d_b_gate, g.bias[1] = a->d_b_up;
         g.out[0] = a->d_h;
         g.save[0] = a->d_a, g.save[1] = a->d_b;
-        return launch_dense_gemm(g, (hipStream_t)a->stream);
+        return launch_dense_gemm(g, need ? a->d_ws : nullptr, (hipStream_t)a->stream);
     });
 }
 
@@ -185,11 +197,12 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         }
         DENSE_TRY(check_vector(me, "d_db_gate", a->d_db_gate, a->wgrad_dtype));
         DENSE_TRY(check_vector(me, "d_db_up", a->d_db_up, a->wgrad_dtype));
-        const BackWs w = back_ws(I, 2, a->dtype, T);
+        const BackWs w = back_ws(d, I, 2, a->dtype, T);
+        DENSE_TRY(check_pitch(me, w.pitch, a->dtype));
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
         hipStream_t st = (hipStream_t)a->stream;
         char *dz = (char *)a->d_ws;
-        float *partial = want_db ? (float *)(dz + w.partial) : nullptr;
+        float *partial = want_db ? (float *)(dz + w.colsum) : nullptr;
         if (T > 0 && (want_dw || want_dx || want_db)) {
             DenseGrad q{};
             q.dtype = q.dout_dtype = a->dtype;
@@ -220,7 +233,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
             g.M = T, g.N = a->hidden, g.K = a->inter;
             g.out[0] = a->d_dx;
             g.ldout = lddx;
-            DENSE_TRY(launch_dense_gemm(g, st));
+            DENSE_TRY(launch_dense_gemm(g, (char *)a->d_ws + w.split, st));
         }
         if (want_dw) {
             DenseGemm g{};
@@ -234,7 +247,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
             g.M = a->inter, g.N = a->hidden, g.K = T;
             g.out[0] = a->d_dw_gate, g.out[1] = a->d_dw_up;
             g.ldout = lddw;
-            DENSE_TRY(launch_dense_gemm(g, st));
+            DENSE_TRY(launch_dense_gemm(g, (char *)a->d_ws + w.split, st));
         }
         return ECF_OK;
     });
@@ -245,7 +258,8 @@ size_t ecf_linear_workspace_bytes(int32_t in_features, int32_t out_features, int
 {
     if (check_common("ecf_linear_workspace_bytes", in_features, out_features, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
-    return backward ? back_ws(out_features, 1, dtype, n_tokens).total : 0;
+    return backward ? back_ws(in_features, out_features, 1, dtype, n_tokens).total
+                    : dense_gemm_ws(dtype, n_tokens, out_features, 1);
 }
 
 int ecf_linear_forward(const ecf_linear_args *a, int32_t T)
@@ -276,12 +290,14 @@ int ecf_linear_forward(const ecf_linear_args *a, int32_t T)
             DENSE_TRY(check_matrix(me, "d_residual", a->d_residual, g.ldres, N, a->out_dtype));
         if (a->d_z)
             DENSE_TRY(check_matrix(me, "d_z", a->d_z, g.ldsave, N, a->dtype));
+        const size_t need = dense_gemm_ws(a->dtype, T, N, 1);
+        DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, need));
         g.a[0] = a->d_x, g.b[0] = a->d_w;
         g.bias[0] = a->d_bias;
         g.res = a->d_residual;
         g.out[0] = a->d_out;
         g.save[0] = a->d_z;
-        return launch_dense_gemm(g, (hipStream_t)a->stream);
+        return launch_dense_gemm(g, need ? a->d_ws : nullptr, (hipStream_t)a->stream);
     });
 }
 
@@ -314,13 +330,14 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         if (a->d_dw)
             DENSE_TRY(check_matrix(me, "d_dw", a->d_dw, lddw, K, a->wgrad_dtype));
         DENSE_TRY(check_vector(me, "d_dbias", a->d_dbias, a->wgrad_dtype));
-        const BackWs w = back_ws(N, 1, a->dtype, T);
+        const BackWs w = back_ws(K, N, 1, a->dtype, T);
+        DENSE_TRY(check_pitch(me, w.pitch, a->dtype));
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
         hipStream_t st = (hipStream_t)a->stream;
         // without an activation and in the operands' type, dy is dz
         const bool direct = !act && a->out_dtype == a->dtype;
         const bool products = want_dx || (a->d_dw && T > 0);
-        float *partial = a->d_dbias ? (float *)((char *)a->d_ws + w.partial) : nullptr;
+        float *partial = a->d_dbias ? (float *)((char *)a->d_ws + w.colsum) : nullptr;
         if (T > 0 && ((products && !direct) || a->d_dbias)) {
             DenseGrad q{};
             q.dtype = a->dtype, q.dout_dtype = a->out_dtype;
@@ -354,7 +371,7 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
             g.M = T, g.N = a->in_features, g.K = a->out_features;
             g.out[0] = a->d_dx;
             g.ldout = lddx;
-            DENSE_TRY(launch_dense_gemm(g, st));
+            DENSE_TRY(launch_dense_gemm(g, (char *)a->d_ws + w.split, st));
         }
         if (a->d_dw) {
             g.out_dtype = a->wgrad_dtype;
@@ -364,7 +381,7 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
             g.M = a->out_features, g.N = a->in_features, g.K = T;
             g.out[0] = a->d_dw;
             g.ldout = lddw;
-            DENSE_TRY(launch_dense_gemm(g, st));
+            DENSE_TRY(launch_dense_gemm(g, (char *)a->d_ws + w.split, st));
         }
         return ECF_OK;
     });

@@ -32,8 +32,14 @@ struct DenseGemm {
     int64_t ldout;
     void *save[2];
     int64_t ldsave;
+    // rows that start at 16-byte boundaries, set by the launcher
+    bool vec_bias, vec_res, vec_out, vec_save;
 };
-int launch_dense_gemm(const DenseGemm &g, hipStream_t st);
+// ws: room for dense_gemm_ws bytes (may be null where that is 0)
+int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st);
+// The largest workspace of any product of these types with up to M x N outputs.
+constexpr size_t kDensePartialBytes = (size_t)32 << 20;  // fp32 sums of split products
+size_t dense_gemm_ws(int dtype, int64_t M, int64_t N, int planes);
 
 // dz rows of the backward passes, in the operands' type: dz[t][i] (linear) or
 // da = dz[t][i], db = dz[t][pitch / 2 + i] (gated).  Columns from I to the

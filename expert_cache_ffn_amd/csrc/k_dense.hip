@@ -8,7 +8,9 @@
 // patch with fp32 FMAs; the gated form keeps two patches, one per projection,
 // and joins them in registers.  The epilogue adds bias, applies the activation,
 // adds the residual and rounds once.
-#include "dense_device.h"
+#include <algorithm>
+
+#include "dense_launch16.h"
 
 namespace ecf {
 namespace {
@@ -155,9 +157,91 @@ __global__ __launch_bounds__(256) void k_dense_colsum(const float *partial, int 
 
 }  // namespace
 
-int launch_dense_gemm(const DenseGemm &g, hipStream_t st)
+namespace {
+
+struct Tile16 {
+    int bm, bn;
+    double cost;  // of one k-tile of one block, in units of a 256 x 256 tile's
+};
+const Tile16 kTiles16[] = {{256, 256, 1.0}, {128, 256, 0.55}, {128, 128, 0.30}, {64, 128, 0.19}};
+
+bool aligned16(const void *p, int64_t ld, int dtype)
 {
+    return (uintptr_t)p % 16 == 0 && ld * (int64_t)dense_esize(dtype) % 16 == 0;
+}
+
+constexpr int kMaxSplits = 16;
+
+// The tile and the splits of K with the least estimated time: rounds of blocks
+// over the CUs times the k-tiles each walks, plus the join of the splits.
+DensePlan plan16(const DenseGemm &g, int cus, bool may_split)
+{
+    DensePlan best{0, 1, true};
+    for (int s = 0; s < g.ksegs || s < g.mhalves; ++s)
+        best.dma = best.dma && aligned16(g.a[s], g.lda, g.dtype);
+    for (int s = 0; s < (g.gated || g.ksegs == 2 ? 2 : 1); ++s)
+        best.dma = best.dma && aligned16(g.b[s], g.ldb, g.dtype);
+    best.dma = best.dma && (g.a_t ? g.M : g.K) % 8 == 0 && (g.b_t ? g.N : g.K) % 8 == 0;
+    const int kt = (g.K + 63) / 64 * g.ksegs;
+    const int64_t np = (g.N + 7) / 8 * 8, planes = g.gated ? 2 : g.mhalves;
+    double least = 1e300;
+    for (int t = 0; t < 4; ++t) {
+        const int64_t tm = (g.M + kTiles16[t].bm - 1) / kTiles16[t].bm * g.mhalves;
+        const int64_t tn = (g.N + kTiles16[t].bn / (g.gated ? 2 : 1) - 1) / (kTiles16[t].bn / (g.gated ? 2 : 1));
+        for (int s = 1; s <= kMaxSplits; s *= 2) {
+            const double part = (double)s * planes * g.M * np * 4;
+            if (s > 1 && (!may_split || kt / s < 4 || part > (double)kDensePartialBytes))
+                break;
+            const double rounds = (double)((tm * tn * s + cus - 1) / cus);
+            const double us = rounds * (kTiles16[t].cost * ((kt + s - 1) / s) + 2.0) + (s > 1 ? 4.0 + part / 2e6 : 0.0);
+            if (us < least) {
+                least = us;
+                best.tile = t;
+                best.splits = s;
+            }
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
+size_t dense_gemm_ws(int dtype, int64_t M, int64_t N, int planes)
+{
+    if (dtype == ECF_F32)
+        return 0;
+    const size_t all = (size_t)kMaxSplits * planes * M * ((N + 7) / 8 * 8) * 4;
+    return std::min(all, kDensePartialBytes);
+}
+
+int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
+{
+    DenseGemm g = gin;
     ProfScope p(g.gated ? "dense_gated" : g.a_t ? "dense_gemm_tn" : g.b_t ? "dense_gemm_nn" : "dense_gemm_nt", st);
+    if (g.dtype != ECF_F32) {
+        int dev = 0, cus = 0;
+        ECF_HIP_CHECK(hipGetDevice(&dev));
+        ECF_HIP_CHECK(hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev));
+        const DensePlan plan = plan16(g, cus, ws != nullptr);
+        g.vec_bias = aligned16(g.bias[0], 8, g.dtype) && aligned16(g.bias[1], 8, g.dtype);
+        g.vec_res = aligned16(g.res, g.ldres, g.out_dtype);
+        g.vec_out = aligned16(g.out[0], g.ldout, g.out_dtype) && aligned16(g.out[1], g.ldout, g.out_dtype);
+        g.vec_save = aligned16(g.save[0], g.ldsave, g.dtype) && aligned16(g.save[1], g.ldsave, g.dtype);
+        const Tile16 &t = kTiles16[plan.tile];
+        const int bn = g.gated ? t.bn / 2 : t.bn;
+        DenseGrid gr{};
+        gr.half_tiles = (g.M + t.bm - 1) / t.bm;
+        gr.tiles_m = gr.half_tiles * g.mhalves;
+        gr.tiles_n = (g.N + bn - 1) / bn;
+        gr.ktiles = (g.K + 63) / 64 * g.ksegs;
+        gr.splits = plan.splits;
+        gr.partial = (float *)ws;
+        gr.np = (g.N + 7) / 8 * 8;
+        return g.gated ? launch_gemm16_gated(g, plan, gr, st)
+               : g.a_t ? launch_gemm16_tn(g, plan, gr, st)
+               : g.b_t ? launch_gemm16_nn(g, plan, gr, st)
+                       : launch_gemm16_nt(g, plan, gr, st);
+    }
     const dim3 grid((g.N + TN - 1) / TN, (g.M + TM - 1) / TM * g.mhalves);
     if (g.gated)
         hipLaunchKernelGGL(k_dense_tile<true>, grid, dim3(256), 0, st, g);
