@@ -3,18 +3,18 @@
 //
 //   acc[m][n] = sum_k A(m, k) B(n, k), each operand k- or m/n-contiguous
 //
-// A block of WM x WN waves owns BM x BN outputs and walks K in tiles of 64, two
-// LDS stages: while the MFMAs of one k-tile run, the next one's operands travel.
+// A block of WM x WN waves owns BM x BN outputs and walks K in tiles of BK.
 //   DMA      16-byte aligned rows: global memory -> LDS directly
-//            (buffer_load ... lds), no operand passes through a register
+//            (buffer_load ... lds), no operand passes through a register; a ring
+//            of NS stages keeps NS - 1 k-tiles in flight ahead of the MFMAs
 //   register any alignment and any width: 16-byte loads at element alignment
-//            into registers at the top of a k-tile, LDS stores at its end
+//            into registers, two k-tiles ahead; LDS stores one k-tile ahead
 // Past the last row the last row is read again (its results are not stored);
 // past the last k both operands are zeros.
 //
-// LDS holds a k-contiguous operand as rows of eight 16-byte chunks, chunk c of
-// row r at c ^ (r & 7) ^ bit 3 of r (16 rows of one chunk touch 16 distinct
-// bank groups), read as one fragment of 8 k per ds_read_b128.  An m-contiguous
+// LDS holds a k-contiguous operand as rows of BK / 8 16-byte chunks, XOR-swizzled
+// (rswz: 16 rows of one chunk touch 16 distinct bank groups), read as one
+// fragment of 8 k per ds_read_b128.  An m-contiguous
 // operand keeps its global layout, k rows of BM elements, and is transposed on
 // the way to registers by ds_read_b64_tr_b16 (16 lanes fetch 4 k x 16 m and each
 // gets the 4 k of its m); the 64-byte groups of a row are XORed with k & 3, so
@@ -25,6 +25,8 @@
 // residual and the gated product are applied there to the fp32 sums, and loads
 // and stores are 16 bytes wide where alignment allows.
 #pragma once
+
+#include <type_traits>
 
 #include "dense_device.h"
 
@@ -55,7 +57,7 @@ __device__ __forceinline__ f32x16_t mfma16<F16>(u32x4_t a, u32x4_t b, f32x16_t c
 struct DenseGrid {
     int tiles_m, tiles_n;  // tiles_m: of both halves
     int half_tiles;        // tiles_m of one half
-    int ktiles, splits;
+    int splits;
     float *partial;  // splits > 1: fp32 sums [split][half or projection][M][np]
     int64_t np;
     __host__ __device__ int blocks() const { return tiles_m * tiles_n * splits; }
@@ -200,7 +202,6 @@ __device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t 
 
 namespace g16 {
 
-constexpr int BK = 64;
 constexpr uint32_t kNowhere = 0x80000000u;  // a buffer offset past every resource: reads zeros, touches no memory
 
 typedef uint32_t lds_addr;
@@ -233,14 +234,25 @@ __device__ __forceinline__ u32x4_t rsrc_of(const void *base)
     return r;
 }
 
-// the next stage has landed and this stage is read: wait for this wave's loads and LDS reads, meet the others
-__device__ __forceinline__ void stage_end()
+// At most N of this wave's loads are still under way (the k-tiles behind the next
+// one) and its LDS accesses are done: meet the other waves.
+template <int N>
+__device__ __forceinline__ void stage_ready()
 {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// m-contiguous tiles: the XOR of the 16-byte chunks of k row k (64-byte groups over 4 k rows; rows of 128 bytes
-// put two k rows side by side, so there it takes k / 2)
+// k-contiguous tiles: the XOR of the chunks of row r.  16 rows of one chunk then
+// lie in 16 distinct 16-byte bank groups of 256 bytes (rows of 128 bytes: two
+// rows per 256, eight chunks each; rows of 64 bytes: four rows, four chunks).
+template <int BK>
+__device__ __forceinline__ int rswz(int r)
+{
+    return BK == 64 ? (r & 7) ^ ((r >> 3) & 1) : (r >> 2) & 3;
+}
+// m-contiguous tiles: the XOR of the 16-byte chunks of k row k (64-byte groups
+// over 4 k rows; rows of 128 bytes put two k rows side by side, so there it takes
+// k / 2).
 template <int ROWS>
 __device__ __forceinline__ int kswz(int k)
 {
@@ -251,83 +263,97 @@ struct __attribute__((packed, aligned(2))) u128_any {
     u32x4_t v;
 };
 
-// One operand's tile of ROWS rows (m or n) x 64 k.  T: m-contiguous in memory.
-template <bool T, bool DMA, int ROWS, int NTH>
+// v shifted down by s 16-bit elements (0..7), zeros from above
+__device__ __forceinline__ u32x4_t shift_down(u32x4_t v, int s)
+{
+    if (s & 4)
+        v = u32x4_t{v[2], v[3], 0, 0};
+    if (s & 2)
+        v = u32x4_t{v[1], v[2], v[3], 0};
+    if (s & 1)
+        v = u32x4_t{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+    return v;
+}
+
+// One operand's tile of ROWS rows (m or n) x BK k.  T: m-contiguous in memory.
+template <bool T, bool DMA, int ROWS, int NTH, int BK>
 struct Tile {
-    static constexpr int NL = ROWS * 8 / NTH;  // 16-byte loads per thread and k-tile
-    static constexpr int CPR = T ? ROWS / 8 : 8;  // chunks per LDS row
-    static constexpr int KSTEP = NTH * 8 / ROWS;  // T: k rows between a thread's loads
-    static_assert(ROWS * 8 % NTH == 0 && NL >= 1, "tile too small for the block");
-    static_assert(!T || KSTEP % 4 == 0, "a thread's k rows share the swizzle");
+    static constexpr int CPR = T ? ROWS / 8 : BK / 8;  // chunks per LDS row
+    static constexpr int NL = ROWS * BK / 8 / NTH;     // 16-byte loads per thread and k-tile
+    static constexpr int STEP = NTH / CPR;             // LDS rows between a thread's loads
+    static constexpr int RPW = 64 / CPR;               // LDS rows that one load of a wave covers (not T)
+    static_assert(ROWS * BK / 8 % NTH == 0 && NL >= 1, "tile too small for the block");
+    static_assert(STEP % (T ? 4 : 16) == 0, "a thread's rows share the swizzle");
 
     uint32_t off[NL];  // byte offsets of this thread's chunks from the k-tile's base
-    int row, chunk;    // T: first k row and chunk; else: chunk of every row
-    int valid;         // T: elements of the chunk that exist (0..8); else unused
+    int row, chunk;    // the first of this thread's LDS rows, and its chunk in all of them
+    int valid;         // T: elements of the chunk that exist (up to 8, none if <= 0)
+    int width;         // elements in a row of the operand: those before a row's last chunk may be read
     u32x4_t reg[DMA ? 1 : NL];
 
-    // `rows` real rows from the tile's first on, row stride ld (elements); rowmap
-    // turns a tile row into a row relative to the base (before clamping)
+    // `rows` rows from the tile's first on, row stride ld (elements); rowmap turns a
+    // tile row into a row relative to the base (clamped to the last one)
     template <class F>
-    __device__ __forceinline__ void init(int tid, int rows, int64_t ld, F rowmap)
+    __device__ __forceinline__ void init(int tid, int rows, int width_, int64_t ld, F rowmap)
     {
+        row = tid / CPR;
+        width = width_;
         if constexpr (!T) {
-            row = tid >> 3;
-            chunk = (tid & 7) ^ (row & 7) ^ ((row >> 3) & 1);
+            chunk = (tid % CPR) ^ rswz<BK>(row);
             valid = 8;
 #pragma unroll
-            for (int q = 0; q < NL; ++q) {
-                const int64_t r = rowmap(row + (NTH / 8) * q);
-                off[q] = (uint32_t)(r * ld * 2) + chunk * 16;
-            }
+            for (int q = 0; q < NL; ++q)
+                off[q] = (uint32_t)(rowmap(row + STEP * q) * ld * 2) + chunk * 16;
         } else {
-            row = tid / CPR;
             chunk = (tid % CPR) ^ kswz<ROWS>(row);
-            valid = max(0, min(8, rows - chunk * 8));
+            valid = rows - chunk * 8;
 #pragma unroll
             for (int q = 0; q < NL; ++q)
-                off[q] = (uint32_t)((row + KSTEP * q) * ld * 2) + chunk * 16;
+                off[q] = (uint32_t)((row + STEP * q) * ld * 2) + chunk * 16;
         }
     }
 
-    // Start loading the k-tile at `base` with kleft k still to come (may be over 64).
-    // PAIR: tile rows r with bit 5 set come from base2 (the up projection); the 8
-    // rows that one load of a wave covers agree on that bit.
-    template <bool PAIR = false>
-    __device__ __forceinline__ void load(const void *base, int kleft, lds_addr lds, int wave,
-                                         const void *base2 = nullptr)
+    // Start loading the k-tile at `base` with kleft k still to come (over BK, or
+    // none and less: zeros).  PAIR: tile rows r with bit 5 set come from base2 (the
+    // up projection); the rows that one load of a wave covers agree on that bit.
+    static constexpr bool second(int q, int wave) { return (STEP * q + RPW * wave) >> 5 & 1; }
+
+    // DMA: load q of the k-tile
+    template <bool PAIR>
+    __device__ __forceinline__ void issue(u32x4_t rs, u32x4_t rs2, int q, int kleft, lds_addr lds, int wave)
     {
-        auto second = [&](int q) { return PAIR && ((((NTH / 8) * q + 8 * wave) >> 5) & 1); };
-        if constexpr (DMA) {
-            const u32x4_t rs = rsrc_of(base), rs2 = PAIR ? rsrc_of(base2) : rs;
-            if constexpr (!T) {
-                const bool in = chunk * 8 < kleft;
-#pragma unroll
-                for (int q = 0; q < NL; ++q)
-                    dma16(second(q) ? rs2 : rs, in ? off[q] : kNowhere, lds + (q * NTH + 64 * wave) * 16);
-            } else {
-#pragma unroll
-                for (int q = 0; q < NL; ++q)
-                    dma16(rs, valid && row + KSTEP * q < kleft ? off[q] : kNowhere, lds + (q * NTH + 64 * wave) * 16);
-            }
-        } else {
+        static_assert(!PAIR || (!T && RPW <= 32 && 32 % RPW == 0), "a wave's rows agree on bit 5");
+        const bool in = T ? valid > 0 && row + STEP * q < kleft : chunk * 8 < kleft;
+        dma16(PAIR && second(q, wave) ? rs2 : rs, in ? off[q] : kNowhere, lds + (q * NTH + 64 * wave) * 16);
+    }
+
+    // register path: the whole k-tile
+    template <bool PAIR>
+    __device__ __forceinline__ void load(const void *base, const void *base2, int kleft, int wave)
+    {
+        if constexpr (!DMA) {
             const int n = T ? valid : kleft - chunk * 8;
-            if (T ? n >= 8 && kleft >= BK : n >= 8) {
+            if (n >= 8 && (!T || kleft >= BK)) {
 #pragma unroll
                 for (int q = 0; q < NL; ++q)
-                    reg[q] = ((const u128_any *)((const char *)(second(q) ? base2 : base) + off[q]))->v;
+                    reg[q] = ((const u128_any *)((const char *)(PAIR && second(q, wave) ? base2 : base) + off[q]))->v;
             } else {
+                // a chunk that the operand's edge cuts: its 8 elements that end at the
+                // edge, shifted down (rows of under 8 elements: one by one)
 #pragma unroll
                 for (int q = 0; q < NL; ++q) {
-                    const bool in = !T || row + KSTEP * q < kleft;
-                    const uint16_t *p = (const uint16_t *)((const char *)(second(q) ? base2 : base) + off[q]);
+                    const uint16_t *p = (const uint16_t *)((const char *)(PAIR && second(q, wave) ? base2 : base) + off[q]);
+                    reg[q] = u32x4_t{0, 0, 0, 0};
+                    if (n <= 0 || (T && row + STEP * q >= kleft))
+                        continue;
+                    const int s = max(0, 8 - n);
+                    if (width >= 8) {
+                        reg[q] = shift_down(((const u128_any *)(p - s))->v, s);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t lo = 0, hi = 0;
-                        if (in && 2 * j < n)
-                            lo = p[2 * j];
-                        if (in && 2 * j + 1 < n)
-                            hi = p[2 * j + 1];
-                        reg[q][j] = lo | hi << 16;
+                        for (int j = 0; j < 8; ++j)
+                            if (j < n)
+                                reg[q][j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
                     }
                 }
             }
@@ -335,31 +361,30 @@ struct Tile {
     }
 
     // register path: the loaded k-tile to its stage
-    __device__ __forceinline__ void store(u32x4_t *stage, int tid)
+    __device__ __forceinline__ void store(char *stage, int tid)
     {
-        if constexpr (!DMA) {
 #pragma unroll
-            for (int q = 0; q < NL; ++q)
-                stage[q * NTH + tid] = reg[q];
-        }
+        for (int q = 0; q < NL; ++q)
+            ((u32x4_t *)stage)[q * NTH + tid] = reg[q];
     }
 };
 
 // Where a lane finds its fragments of an operand in a stage.  Fragment f: rows
-// r0 + 32 f + (lane & 31); step ks: k chunk 4 (lane >> 5) + ks, 8 k.
-template <bool T, int ROWS, int F>
+// r0 + 32 f + (lane & 31); step ks: k chunk BK / 16 (lane >> 5) + ks, 8 k.
+template <bool T, int ROWS, int F, int BK>
 struct Frag {
-    uint32_t at[T ? F : 4];
+    static constexpr int NK = BK / 16;
+    uint32_t at[T ? F : NK];
     __device__ __forceinline__ void init(int lane, int r0)
     {
         const int g = lane >> 5;
         if constexpr (!T) {
             const int r = r0 + (lane & 31);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                at[ks] = (r * 8 + ((4 * g + ks) ^ (r & 7) ^ ((r >> 3) & 1))) * 16;
+            for (int ks = 0; ks < NK; ++ks)
+                at[ks] = r * (BK * 2) + ((NK * g + ks) ^ rswz<BK>(r)) * 16;
         } else {
-            const int i = lane & 15, k = 32 * g + (i >> 2);
+            const int i = lane & 15, k = BK / 2 * g + (i >> 2);
 #pragma unroll
             for (int f = 0; f < F; ++f) {
                 const int m = r0 + 32 * f + (lane & 16) + (i & 3) * 4;
@@ -370,7 +395,7 @@ struct Frag {
     __device__ __forceinline__ u32x4_t read(const char *stage, int f, int ks) const
     {
         if constexpr (!T) {
-            return *(const u32x4_t *)(stage + at[ks] + f * 32 * 128);
+            return *(const u32x4_t *)(stage + at[ks] + f * 32 * (BK * 2));
         } else {
             u32x4_t v = {0, 0, 0, 0};
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -389,17 +414,19 @@ struct Frag {
 }  // namespace g16
 
 // grid: 1-D, one block per (split, output tile); see DenseGrid.
-template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(DenseGemm g,
+template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE>
+__global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 2) void k_gemm16(DenseGemm g,
                                                                                                    DenseGrid gr)
 {
     using namespace g16;
     constexpr int NW = WM * WN, NTH = 64 * NW, RM = BM / WM, RN = BN / WN, FM = RM / 32, FN = RN / 32;
-    static_assert(FM >= 1 && FN >= 1 && (!GATED || (FN == 2 && !BT)), "wave tile");
-    constexpr int SA = BM * 128, SB = BN * 128;  // bytes per stage
+    static_assert(BK % 32 == 0, "two sets of fragments take turns");
+    static_assert(FM >= 1 && FN >= 1 && (!GATED || (FN % 2 == 0 && !BT)), "wave tile");
+    constexpr int NS = DMA ? NSTAGE : 2;
+    constexpr int SA = BM * BK * 2, SB = BN * BK * 2;  // bytes per stage
     constexpr int PITCH = (FN >= 2 ? 64 : 32) + 4;  // fp32 per row of the output staging
-    static_assert(NW * 32 * PITCH * 4 <= 2 * (SA + SB), "output staging");
-    __shared__ __attribute__((aligned(16))) char lds[2 * (SA + SB)];
+    constexpr int OUT = NW * 32 * PITCH * 4, IN = NS * (SA + SB);
+    __shared__ __attribute__((aligned(16))) char lds[OUT > IN ? OUT : IN];
 
     int split, half, mt, nt;
     gr.locate(blockIdx.x, split, half, mt, nt);
@@ -408,17 +435,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(DenseGemm g,
     const int m0 = mt * BM, n0 = nt * (GATED ? BN / 2 : BN);
     const int mrows = min(BM, g.M - m0);
 
-    Tile<AT, DMA, BM, NTH> ta;
-    Tile<BT, DMA, BN, NTH> tb;
-    ta.init(tid, g.M - m0, g.lda, [&](int r) { return (int64_t)min(r, mrows - 1); });
-    if constexpr (GATED) {
-        // 64 tile rows: 32 of the gate projection, then the same 32 of the up projection
-        tb.init(tid, 0, g.ldb, [&](int r) { return (int64_t)min((r >> 6) * 32 + (r & 31), g.N - 1 - n0); });
-    } else {
-        tb.init(tid, g.N - n0, g.ldb, [&](int r) { return (int64_t)min(r, g.N - 1 - n0); });
-    }
-    Frag<AT, BM, FM> fa;
-    Frag<BT, BN, FN> fb;
+    Tile<AT, DMA, BM, NTH, BK> ta;
+    Tile<BT, DMA, BN, NTH, BK> tb;
+    const int nrows = GATED ? 0 : g.N - n0, nlast = g.N - 1 - n0;
+    ta.init(tid, g.M - m0, AT ? g.M : g.K, g.lda, [&](int r) { return (int64_t)min(r, mrows - 1); });
+    // gated: 64 tile rows are 32 of the gate projection, then the same 32 of the up projection
+    tb.init(tid, nrows, BT ? g.N : g.K, g.ldb,
+            [&](int r) { return (int64_t)min(GATED ? (r >> 6) * 32 + (r & 31) : r, nlast); });
+    Frag<AT, BM, FM, BK> fa;
+    Frag<BT, BN, FN, BK> fb;
     fa.init(lane, wm * RM);
     fb.init(lane, wn * RN);
 
@@ -432,111 +457,184 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm16(DenseGemm g,
                 acc[i][j][e] = 0.f;
 
     const int kper = (g.K + BK - 1) / BK;  // k-tiles per segment
-    const int kb = (int)((int64_t)gr.ktiles * split / gr.splits), ke = (int)((int64_t)gr.ktiles * (split + 1) / gr.splits);
-    auto load = [&](int kt, int stage) __attribute__((always_inline)) {
-        const int seg = kt >= kper ? 1 : 0, k0 = (kt - seg * kper) * BK;
-        const char *a = (const char *)(AT ? (half ? g.a[1] : g.a[0]) : (seg ? g.a[1] : g.a[0]));
-        const char *b = (const char *)(seg ? g.b[1] : g.b[0]);
-        a += (AT ? (int64_t)k0 * g.lda + m0 : (int64_t)m0 * g.lda + k0) * 2;
-        const int64_t bo = (BT ? (int64_t)k0 * g.ldb + n0 : (int64_t)n0 * g.ldb + k0) * 2;
-        ta.load(a, g.K - k0, lds_of(lds) + stage * SA, wave);
-        if constexpr (GATED)
-            tb.template load<true>(b + bo, g.K - k0, lds_of(lds) + 2 * SA + stage * SB, wave, (const char *)g.b[1] + bo);
+    const int64_t kall = (int64_t)kper * g.ksegs;
+    const int kb = (int)(kall * split / gr.splits), ke = (int)(kall * (split + 1) / gr.splits);
+    // Operand addresses of the block's first k, and the bytes from one k-tile to the
+    // next.  Held in scalar registers: left alone, the compiler reads the pointers
+    // from the kernel's arguments again in every k-tile and waits for them.
+    const char *pa[2], *pb[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        pa[q] = (const char *)g.a[AT ? half : q] + (AT ? (int64_t)m0 : (int64_t)m0 * g.lda) * 2;
+        pb[q] = (const char *)g.b[q] + (BT ? (int64_t)n0 : (int64_t)n0 * g.ldb) * 2;
+        asm volatile("" : "+s"(pa[q]), "+s"(pb[q]));
+    }
+    const int64_t stepa = (AT ? g.lda : 1) * (2 * BK), stepb = (BT ? g.ldb : 1) * (2 * BK);
+    constexpr int NLA = decltype(ta)::NL, NLD = NLA + decltype(tb)::NL;
+    // k-tile kt: past the end nothing is loaded (zeros)
+    struct Src {
+        const char *a, *b, *b2;
+        int kleft;
+    };
+    auto source = [&](int kt) __attribute__((always_inline)) {
+        const bool seg = kt >= kper;
+        const int k = seg ? kt - kper : kt;
+        return Src{(seg && !AT ? pa[1] : pa[0]) + k * stepa, (seg && !GATED ? pb[1] : pb[0]) + k * stepb,
+                   pb[1] + k * stepb, kt < ke ? g.K - k * BK : 0};
+    };
+    // DMA: load q of the NLD loads of a k-tile towards `stage`
+    auto issue = [&](const Src &s, int stage, int q) __attribute__((always_inline)) {
+        const lds_addr to = lds_of(lds) + stage * (SA + SB);
+        if (q < NLA)
+            ta.template issue<false>(rsrc_of(s.a), rsrc_of(s.a), q, s.kleft, to, wave);
         else
-            tb.load(b + bo, g.K - k0, lds_of(lds) + 2 * SA + stage * SB, wave);
+            tb.template issue<GATED>(rsrc_of(s.b), rsrc_of(GATED ? s.b2 : s.b), q - NLA, s.kleft, to + SA, wave);
+    };
+    auto load_reg = [&](int kt) __attribute__((always_inline)) {
+        const Src s = source(kt);
+        ta.template load<false>(s.a, s.a, s.kleft, wave);
+        tb.template load<GATED>(s.b, s.b2, s.kleft, wave);
         // issue the loads here, ahead of the MFMAs they travel under
         asm volatile("" ::: "memory");
     };
     auto put = [&](int stage) __attribute__((always_inline)) {
-        ta.store((u32x4_t *)(lds + stage * SA), tid);
-        tb.store((u32x4_t *)(lds + 2 * SA + stage * SB), tid);
+        ta.store(lds + stage * (SA + SB), tid);
+        tb.store(lds + stage * (SA + SB) + SA, tid);
     };
-    auto body = [&](int stage) __attribute__((always_inline)) {
-        const char *sa = lds + stage * SA, *sb = lds + 2 * SA + stage * SB;
-        // fragments of step ks + 1 are read under the MFMAs of step ks; the
-        // scheduling barriers keep the compiler from reading all four steps ahead,
-        // which takes more registers than there are
-        u32x4_t av[2][FM], bv[2][FN];
-        auto fetch = [&](int ks) __attribute__((always_inline)) {
+    // Two sets of fragments: step ks + 1 (or the next k-tile's step 0) is read under
+    // the MFMAs of step ks.
+    constexpr int NK = BK / 16;
+    u32x4_t av[2][FM], bv[2][FN];
+    auto fetch = [&](int stage, int ks, int set, int f) __attribute__((always_inline)) {
+        const char *sa = lds + stage * (SA + SB), *sb = sa + SA;
+        if (f < FN)
+            bv[set][f] = fb.read(sb, f, ks);
+        else
+            av[set][f - FN] = fa.read(sa, f - FN, ks);
+    };
+    auto fetch_all = [&](int stage) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
-                bv[ks & 1][j] = fb.read(sb, j, ks);
+        for (int f = 0; f < FM + FN; ++f)
+            fetch(stage, 0, 0, f);
+    };
+    // The MFMAs of the fragments in `set`.  Before MFMA i: fragments of step ks of
+    // `stage` into the other set, spread over the MFMAs so that they have the rest of
+    // the step to arrive, and (LOADS) global loads.  The scheduling barriers keep
+    // this order: left alone, the compiler moves the reads behind the last MFMAs.
+    constexpr int MF = FM * FN;
+    auto step = [&](int set, int stage, int ks, auto loads, const Src &s, int into) __attribute__((always_inline)) {
+        constexpr bool LOADS = decltype(loads)::value;
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
-                av[ks & 1][i] = fa.read(sa, i, ks);
-        };
-        fetch(0);
+        for (int i = 0; i < MF; ++i) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            if (ks < 3)
-                fetch(ks + 1);
+            for (int f = i * (FM + FN) / MF; f < (i + 1) * (FM + FN) / MF; ++f)
+                fetch(stage, ks, set ^ 1, f);
+            if constexpr (LOADS) {
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    acc[i][j] = mfma16<E>(av[ks & 1][i], bv[ks & 1][j], acc[i][j]);
+                for (int q = i * NLD / MF; q < (i + 1) * NLD / MF; ++q)
+                    issue(s, into, q);
+            }
+            acc[i / FN][i % FN] = mfma16<E>(av[set][i / FN], bv[set][i % FN], acc[i / FN][i % FN]);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
     if (kb < ke) {
-        load(kb, 0);
-        put(0);
-        stage_end();
-        int stage = 0;
-        for (int kt = kb; kt + 1 < ke; ++kt) {
-            load(kt + 1, stage ^ 1);
-            body(stage);
-            stage ^= 1;
-            put(stage);
-            stage_end();
+        // The k-tile's last step: its fragments are in registers, so this stage is
+        // done with; once the next k-tile has landed for every wave, its first
+        // fragments are read under the last step's MFMAs.
+        if constexpr (DMA) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const Src s = source(kb + i);
+#pragma unroll
+                for (int q = 0; q < NLD; ++q)
+                    issue(s, i, q);
+            }
+            stage_ready<(NS - 1) * NLD>();
+            fetch_all(0);
+            int stage = 0;
+            for (int kt = kb; kt < ke; ++kt) {
+                const Src s = source(kt + NS);
+#pragma unroll
+                for (int ks = 0; ks < NK - 1; ++ks)
+                    step(ks & 1, stage, ks + 1, std::false_type{}, s, 0);
+                const int next = stage + 1 == NS ? 0 : stage + 1;
+                stage_ready<(NS - 2) * NLD>();
+                step((NK - 1) & 1, next, 0, std::true_type{}, s, stage);
+                stage = next;
+            }
+            stage_ready<0>();
+        } else {
+            load_reg(kb);
+            put(0);
+            load_reg(kb + 1);
+            stage_ready<63>();
+            fetch_all(0);
+            int stage = 0;
+            const Src s{};
+            for (int kt = kb; kt < ke; ++kt) {
+                put(stage ^ 1);
+                load_reg(kt + 2);
+#pragma unroll
+                for (int ks = 0; ks < NK - 1; ++ks)
+                    step(ks & 1, stage, ks + 1, std::false_type{}, s, 0);
+                stage_ready<63>();
+                stage ^= 1;
+                step((NK - 1) & 1, stage, 0, std::false_type{}, s, 0);
+            }
+            stage_ready<63>();
         }
-        body(stage);
     }
-    __syncthreads();
 
     // Output through LDS: each wave puts 32 rows x (up to) 64 columns of fp32 sums
     // in its own buffer and takes them back by rows.  A wave's LDS accesses
     // complete in order, so only the compiler has to be kept from reordering them.
+    // The loops stay loops, with one copy of the epilogue: unrolled, its code is
+    // fetched from memory by every block (8192 x 16384 outputs of K 128: 350 us
+    // unrolled, see the figures at the launcher for the loop).
+    constexpr int CB = FN >= 2 ? 2 : 1, GROUPS = FM * (FN / CB);
+    constexpr int LPR = (GATED ? 32 : 32 * CB) / 8;  // lanes per output row
     float *eb = (float *)lds + wave * 32 * PITCH;
     const bool partial = gr.splits > 1;
+#pragma unroll 1
+    for (int grp = 0; grp < GROUPS; ++grp) {
+        asm volatile("" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
+        for (int i = 0; i < GROUPS; ++i)
+            if (grp == i) {
 #pragma unroll
-        for (int jp = 0; jp < FN; jp += 2) {
-            constexpr int CB = FN >= 2 ? 2 : 1;
-            asm volatile("" ::: "memory");
+                for (int j = 0; j < CB; ++j)
 #pragma unroll
-            for (int j = 0; j < CB; ++j)
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    eb[((e >> 2) * 8 + (lane >> 5) * 4 + (e & 3)) * PITCH + j * 32 + (lane & 31)] = acc[i][jp + j][e];
-            asm volatile("" ::: "memory");
-            constexpr int LPR = (GATED ? 32 : 32 * CB) / 8;  // lanes per output row
-#pragma unroll
-            for (int p = 0; p < 32 * LPR / 64; ++p) {
-                const int r = p * (64 / LPR) + lane / LPR, c = (lane % LPR) * 8;
-                const int64_t m = m0 + wm * RM + i * 32 + r;
-                const int n = n0 + (GATED ? wn * 32 : wn * RN + jp * 32) + c;
-                float z[GATED ? 2 : 1][8];
-#pragma unroll
-                for (int q = 0; q < (GATED ? 2 : 1); ++q) {
-                    const f32x4_t lo = *(const f32x4_t *)(eb + r * PITCH + q * 32 + c);
-                    const f32x4_t hi = *(const f32x4_t *)(eb + r * PITCH + q * 32 + c + 4);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        z[q][e] = lo[e], z[q][4 + e] = hi[e];
-                }
-                if (m >= g.M)
-                    continue;
-                if (!partial) {
-                    epilogue8<E, GATED>(g, half, m, n, z);
-                } else if (n < g.N) {
-#pragma unroll
-                    for (int q = 0; q < (GATED ? 2 : 1); ++q)
-                        store8<F32>(gr.partial, gr.partial_at(g, split, GATED ? q : half, m) + n, 8, true, z[q]);
-                }
+                    for (int e = 0; e < 16; ++e)
+                        eb[((e >> 2) * 8 + (lane >> 5) * 4 + (e & 3)) * PITCH + j * 32 + (lane & 31)] =
+                            acc[i / (FN / CB)][i % (FN / CB) * CB + j][e];
             }
-            asm volatile("" ::: "memory");
+        asm volatile("" ::: "memory");
+        const int r0 = wm * RM + grp / (FN / CB) * 32;
+        const int c0 = GATED ? (wn * RN + grp % (FN / CB) * 64) / 2 : wn * RN + grp % (FN / CB) * 64;
+#pragma unroll 1
+        for (int p = 0; p < 32 * LPR / 64; ++p) {
+            const int r = p * (64 / LPR) + lane / LPR, c = (lane % LPR) * 8;
+            const int64_t m = m0 + r0 + r;
+            const int n = n0 + c0 + c;
+            float z[GATED ? 2 : 1][8];
+#pragma unroll
+            for (int q = 0; q < (GATED ? 2 : 1); ++q) {
+                const f32x4_t lo = *(const f32x4_t *)(eb + r * PITCH + q * 32 + c);
+                const f32x4_t hi = *(const f32x4_t *)(eb + r * PITCH + q * 32 + c + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    z[q][e] = lo[e], z[q][4 + e] = hi[e];
+            }
+            if (m >= g.M)
+                continue;
+            if (!partial) {
+                epilogue8<E, GATED>(g, half, m, n, z);
+            } else if (n < g.N) {
+#pragma unroll
+                for (int q = 0; q < (GATED ? 2 : 1); ++q)
+                    store8<F32>(gr.partial, gr.partial_at(g, split, GATED ? q : half, m) + n, 8, true, z[q]);
+            }
         }
     }
 }

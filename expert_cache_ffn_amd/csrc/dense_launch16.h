@@ -5,10 +5,10 @@
 
 namespace ecf {
 
-template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN>
+template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN, int BK, int NS>
 void launch_gemm16(const DenseGemm &g, const DenseGrid &gr, hipStream_t st)
 {
-    hipLaunchKernelGGL((k_gemm16<E, AT, BT, GATED, DMA, BM, BN, WM, WN>), dim3(gr.blocks()), dim3(64 * WM * WN), 0, st,
+    hipLaunchKernelGGL((k_gemm16<E, AT, BT, GATED, DMA, BM, BN, WM, WN, BK, NS>), dim3(gr.blocks()), dim3(64 * WM * WN), 0, st,
                        g, gr);
 }
 
@@ -16,10 +16,10 @@ template <class E, bool AT, bool BT, bool GATED, bool DMA>
 int pick_gemm16(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st)
 {
     switch (p.tile) {  // the order of kTiles16
-    case 0: launch_gemm16<E, AT, BT, GATED, DMA, 256, 256, 2, 4>(g, gr, st); break;
-    case 1: launch_gemm16<E, AT, BT, GATED, DMA, 128, 256, 2, 4>(g, gr, st); break;
-    case 2: launch_gemm16<E, AT, BT, GATED, DMA, 128, 128, 2, 2>(g, gr, st); break;
-    default: launch_gemm16<E, AT, BT, GATED, DMA, 64, 128, 2, 2>(g, gr, st); break;
+    case 0: launch_gemm16<E, AT, BT, GATED, DMA, 256, 256, 2, 4, 64, 2>(g, gr, st); break;
+    case 1: launch_gemm16<E, AT, BT, GATED, DMA, 128, 256, 2, 4, 64, 3>(g, gr, st); break;
+    case 2: launch_gemm16<E, AT, BT, GATED, DMA, 128, 128, 2, 2, 64, 2>(g, gr, st); break;
+    default: launch_gemm16<E, AT, BT, GATED, DMA, 64, 128, 2, 2, 64, 3>(g, gr, st); break;
     }
     if (gr.splits > 1) {
         const int64_t n = gr.np / 8 * g.M * g.mhalves;

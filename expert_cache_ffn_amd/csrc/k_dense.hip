@@ -233,7 +233,6 @@ int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
         gr.half_tiles = (g.M + t.bm - 1) / t.bm;
         gr.tiles_m = gr.half_tiles * g.mhalves;
         gr.tiles_n = (g.N + bn - 1) / bn;
-        gr.ktiles = (g.K + 63) / 64 * g.ksegs;
         gr.splits = plan.splits;
         gr.partial = (float *)ws;
         gr.np = (g.N + 7) / 8 * 8;
