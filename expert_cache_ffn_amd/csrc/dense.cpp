@@ -202,8 +202,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
         hipStream_t st = (hipStream_t)a->stream;
         char *dz = (char *)a->d_ws;
-        float *partial = want_db ? (float *)(dz + w.colsum) : nullptr;
-        if (T > 0 && (want_dw || want_dx || want_db)) {
+        if (want_db || (T > 0 && (want_dw || want_dx))) {
             DenseGrad q{};
             q.dtype = q.dout_dtype = a->dtype;
             q.act = a->act;
@@ -213,13 +212,11 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
             q.T = T, q.I = a->inter;
             q.dz = want_dw || want_dx ? dz : nullptr;
             q.pitch = w.pitch;
-            q.partial = partial;
-            q.row_blocks = dense_grad_row_blocks(T);
+            q.want_sums = want_db;
+            q.sums[0] = a->d_db_gate, q.sums[1] = a->d_db_up;
+            q.sums_dtype = a->wgrad_dtype;
+            q.partial = (float *)(dz + w.colsum);
             DENSE_TRY(launch_dense_grad(q, st));
-        }
-        if (want_db) {
-            void *const out[2] = {a->d_db_gate, a->d_db_up};
-            DENSE_TRY(launch_dense_colsum(partial, dense_grad_row_blocks(T), a->inter, 2, a->wgrad_dtype, out, st));
         }
         const char *dz2 = dz + (size_t)(w.pitch / 2) * dense_esize(a->dtype);
         if (want_dx) {
@@ -337,8 +334,7 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         // without an activation and in the operands' type, dy is dz
         const bool direct = !act && a->out_dtype == a->dtype;
         const bool products = want_dx || (a->d_dw && T > 0);
-        float *partial = a->d_dbias ? (float *)((char *)a->d_ws + w.colsum) : nullptr;
-        if (T > 0 && ((products && !direct) || a->d_dbias)) {
+        if (a->d_dbias || (T > 0 && products && !direct)) {
             DenseGrad q{};
             q.dtype = a->dtype, q.dout_dtype = a->out_dtype;
             q.act = a->act;
@@ -348,13 +344,11 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
             q.T = T, q.I = a->out_features;
             q.dz = products && !direct ? a->d_ws : nullptr;
             q.pitch = w.pitch;
-            q.partial = partial;
-            q.row_blocks = dense_grad_row_blocks(T);
+            q.want_sums = a->d_dbias != nullptr;
+            q.sums[0] = a->d_dbias;
+            q.sums_dtype = a->wgrad_dtype;
+            q.partial = (float *)((char *)a->d_ws + w.colsum);
             DENSE_TRY(launch_dense_grad(q, st));
-        }
-        if (a->d_dbias) {
-            void *const out[2] = {a->d_dbias, nullptr};
-            DENSE_TRY(launch_dense_colsum(partial, dense_grad_row_blocks(T), a->out_features, 1, a->wgrad_dtype, out, st));
         }
         const void *dz = direct ? a->d_dout : a->d_ws;
         const int64_t lddz = direct ? lddy : w.pitch;

@@ -23,7 +23,7 @@
 //
 // Output goes out by rows through LDS, 8 columns per lane: bias, activation,
 // residual and the gated product are applied there to the fp32 sums, and loads
-// and stores are 16 bytes wide where alignment allows.
+// and stores are 16 bytes wide.
 #pragma once
 
 #include <type_traits>
@@ -82,56 +82,6 @@ struct DenseGrid {
 
 // ---- epilogue on 8 columns of one row -------------------------------------------------
 
-// p[0..8) of a row: 16-byte accesses where the launcher found every row aligned
-// (vec), else one element at a time, n of them.
-template <class E>
-__device__ __forceinline__ void load8(const void *p, int64_t i, int n, bool vec, float v[8])
-{
-    const typename E::raw *q = (const typename E::raw *)p + i;
-    if (vec && n >= 8) {
-        if constexpr (sizeof(typename E::raw) == 4) {
-            const f32x4_t a = *(const f32x4_t *)q, b = *(const f32x4_t *)(q + 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = a[j], v[4 + j] = b[j];
-        } else {
-            const u32x4_t a = *(const u32x4_t *)q;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = E::to_f((uint16_t)(a[j] & 0xffffu));
-                v[2 * j + 1] = E::to_f((uint16_t)(a[j] >> 16));
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] = j < n ? E::to_f(q[j]) : 0.f;
-}
-
-template <class E>
-__device__ __forceinline__ void store8(void *p, int64_t i, int n, bool vec, const float v[8])
-{
-    typename E::raw *q = (typename E::raw *)p + i;
-    if (vec && n >= 8) {
-        if constexpr (sizeof(typename E::raw) == 4) {
-            *(f32x4_t *)q = f32x4_t{v[0], v[1], v[2], v[3]};
-            *(f32x4_t *)(q + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
-        } else {
-            u32x4_t a;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                a[j] = (uint32_t)E::from_f(v[2 * j]) | (uint32_t)E::from_f(v[2 * j + 1]) << 16;
-            *(u32x4_t *)q = a;
-        }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < n)
-            q[j] = E::from_f(v[j]);
-}
-
 // Bias, saved sums, activation, gated product or residual, and the output of
 // columns n..n+7 of row m; z[q] are the fp32 sums (q = 1: the up projection).
 template <class E, bool GATED>
@@ -144,40 +94,23 @@ __device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t 
     for (int q = 0; q < (GATED ? 2 : 1); ++q) {
         if (g.bias[q]) {
             float bv[8];
-            load8<E>(g.bias[q], n, cnt, g.vec_bias, bv);
+            load8<E>(g.bias[q], n, cnt, bv);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 z[q][j] += bv[j];
         }
         if (g.save[q])
-            store8<E>(g.save[q], m * g.ldsave + n, cnt, g.vec_save, z[q]);
+            store8<E>(g.save[q], m * g.ldsave + n, cnt, z[q]);
     }
     void *out = g.out[half];
     if (!out)
         return;
     float y[8];
-    // the activation is uniform: one switch for the eight values
-    if (g.act == ECF_ACT_NONE) {
+    with_act(g.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            y[j] = z[0][j];
-    } else if (g.act == ECF_ACT_SILU) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = act_value(z[0][j], ECF_ACT_SILU);
-    } else if (g.act == ECF_ACT_GELU) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = act_value(z[0][j], ECF_ACT_GELU);
-    } else if (g.act == ECF_ACT_GELU_TANH) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = act_value(z[0][j], ECF_ACT_GELU_TANH);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = act_value(z[0][j], ECF_ACT_RELU);
-    }
+            y[j] = act_value(z[0][j], decltype(act)::value);
+    });
     if constexpr (GATED) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -185,17 +118,17 @@ __device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t 
     } else if (g.res) {
         float r[8];
         if (g.out_dtype == ECF_F32)
-            load8<F32>(g.res, m * g.ldres + n, cnt, g.vec_res, r);
+            load8<F32>(g.res, m * g.ldres + n, cnt, r);
         else
-            load8<E>(g.res, m * g.ldres + n, cnt, g.vec_res, r);
+            load8<E>(g.res, m * g.ldres + n, cnt, r);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             y[j] += r[j];
     }
     if (g.out_dtype == ECF_F32)
-        store8<F32>(out, m * g.ldout + n, cnt, g.vec_out, y);
+        store8<F32>(out, m * g.ldout + n, cnt, y);
     else
-        store8<E>(out, m * g.ldout + n, cnt, g.vec_out, y);
+        store8<E>(out, m * g.ldout + n, cnt, y);
 }
 
 // ---- operand tiles ----------------------------------------------------------------------
@@ -258,10 +191,6 @@ __device__ __forceinline__ int kswz(int k)
 {
     return ROWS >= 128 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
 }
-
-struct __attribute__((packed, aligned(2))) u128_any {
-    u32x4_t v;
-};
 
 // v shifted down by s 16-bit elements (0..7), zeros from above
 __device__ __forceinline__ u32x4_t shift_down(u32x4_t v, int s)
@@ -336,7 +265,7 @@ struct Tile {
             if (n >= 8 && (!T || kleft >= BK)) {
 #pragma unroll
                 for (int q = 0; q < NL; ++q)
-                    reg[q] = ((const u128_any *)((const char *)(PAIR && second(q, wave) ? base2 : base) + off[q]))->v;
+                    reg[q] = ((const any128x2 *)((const char *)(PAIR && second(q, wave) ? base2 : base) + off[q]))->v;
             } else {
                 // a chunk that the operand's edge cuts: its 8 elements that end at the
                 // edge, shifted down (rows of under 8 elements: one by one)
@@ -348,7 +277,7 @@ struct Tile {
                         continue;
                     const int s = max(0, 8 - n);
                     if (width >= 8) {
-                        reg[q] = shift_down(((const u128_any *)(p - s))->v, s);
+                        reg[q] = shift_down(((const any128x2 *)(p - s))->v, s);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
@@ -633,7 +562,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 
             } else if (n < g.N) {
 #pragma unroll
                 for (int q = 0; q < (GATED ? 2 : 1); ++q)
-                    store8<F32>(gr.partial, gr.partial_at(g, split, GATED ? q : half, m) + n, 8, true, z[q]);
+                    store8<F32>(gr.partial, gr.partial_at(g, split, GATED ? q : half, m) + n, 8, z[q]);
             }
         }
     }
@@ -655,7 +584,7 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseGemm g, DenseGrid gr)
 #pragma unroll
         for (int q = 0; q < (GATED ? 2 : 1); ++q) {
             float v[8];
-            load8<F32>(gr.partial, gr.partial_at(g, s, GATED ? q : half, m) + n, 8, true, v);
+            load8<F32>(gr.partial, gr.partial_at(g, s, GATED ? q : half, m) + n, 8, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 z[q][j] += v[j];

@@ -32,8 +32,6 @@ struct DenseGemm {
     int64_t ldout;
     void *save[2];
     int64_t ldsave;
-    // rows that start at 16-byte boundaries, set by the launcher
-    bool vec_bias, vec_res, vec_out, vec_save;
 };
 // ws: room for dense_gemm_ws bytes (may be null where that is 0)
 int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st);
@@ -42,9 +40,10 @@ constexpr size_t kDensePartialBytes = (size_t)32 << 20;  // fp32 sums of split p
 size_t dense_gemm_ws(int dtype, int64_t M, int64_t N, int planes);
 
 // dz rows of the backward passes, in the operands' type: dz[t][i] (linear) or
-// da = dz[t][i], db = dz[t][pitch / 2 + i] (gated).  Columns from I to the
-// (half) pitch are zeroed.  With colsum, per-block column sums go to
-// partial[block][2 or 1][I] in fp32; launch_dense_colsum adds them up.
+// da = dz[t][i], db = dz[t][pitch / 2 + i] (gated).  Columns from I to the (half)
+// pitch, the next multiple of 8, are zeroed.  With sums, the columns are added up:
+// into `sums` where one row block covers all tokens, else per row block into
+// partial [block][1 or 2][I], which launch_dense_colsum joins.
 struct DenseGrad {
     int dtype, dout_dtype, act;
     bool gated;
@@ -53,12 +52,12 @@ struct DenseGrad {
     int T, I;
     void *dz;  // null: column sums only
     int64_t pitch;
+    bool want_sums;
+    void *sums[2];  // each may be null
+    int sums_dtype;
     float *partial;
-    int row_blocks;
 };
 int dense_grad_row_blocks(int T);
 int launch_dense_grad(const DenseGrad &g, hipStream_t st);
-int launch_dense_colsum(const float *partial, int row_blocks, int I, int n, int out_dtype, void *const out[2],
-                        hipStream_t st);
 
 }  // namespace ecf

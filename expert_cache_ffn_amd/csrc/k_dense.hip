@@ -99,60 +99,100 @@ __global__ __launch_bounds__(256) void k_dense_tile(DenseGemm g)
 
 // dz = dout * act'(a) (linear) or da = dout * b * act'(a), db = dout * act(a)
 // (gated), rounded once to the operands' type: they are operands of the two
-// matrix products that follow, which the matrix cores take in that type.  A
-// thread owns one column of kGradRows rows, so the block's column sums (of the
-// unrounded values) need no joining.
-constexpr int kGradRows = 64;
+// matrix products that follow, which the matrix cores take in that type.
+// Bound by memory: reads dout, a and b, writes da and db.  A thread owns 8
+// columns (16-byte accesses) of every 8th of the block's 64 rows; the block's
+// column sums (of the unrounded values) are joined over its 8 row lanes in LDS,
+// always in the same order.
+constexpr int kGradRows = 64, kGradCols = 256;
 
-__global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g)
+template <class E, class ED, bool GATED>
+__global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks)
 {
-    const int64_t half = g.gated ? g.pitch / 2 : g.pitch;
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int t0 = (int)blockIdx.y * kGradRows, t1 = min(g.T, t0 + kGradRows);
-    if (c >= max(half, (int64_t)g.I))
-        return;
-    float sa = 0.f, sb = 0.f;
-    for (int64_t t = t0; t < t1; ++t) {
-        float da = 0.f, db = 0.f;
-        if (c < g.I) {
-            const float d = load_el(g.dout, t * g.lddout + c, g.dout_dtype);
-            float v = 0.f, s = 1.f;
+    constexpr int H = GATED ? 2 : 1;
+    __shared__ float red[8][H][kGradCols + 4];
+    const int cb = (int)blockIdx.x / row_blocks, rb = (int)blockIdx.x - cb * row_blocks;
+    const int cg = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int c = cb * kGradCols + cg * 8, n = g.I - c;
+    const int64_t half = g.pitch / H;
+    const int t1 = min(g.T, (rb + 1) * kGradRows);
+    float sum[H][8] = {};
+    if (n > 0) {
+#pragma unroll 2
+        for (int64_t t = rb * kGradRows + rl; t < t1; t += 8) {
+            float d[8], a[8], b[8], out[H][8];
+            load8<ED>(g.dout, t * g.lddout + c, n, d);
             if (g.a)
-                act_both(load_el(g.a, t * g.ldab + c, g.dtype), g.act, v, s);
-            da = d * s;
-            if (g.gated) {
-                da *= load_el(g.b, t * g.ldab + c, g.dtype);
-                db = d * v;
+                load8<E>(g.a, t * g.ldab + c, n, a);
+            if constexpr (GATED)
+                load8<E>(g.b, t * g.ldab + c, n, b);
+            with_act(g.act, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float v = 0.f, s = 1.f;
+                    if constexpr (GATED || decltype(act)::value != ECF_ACT_NONE)
+                        act_both(a[j], decltype(act)::value, v, s);
+                    out[0][j] = GATED ? d[j] * b[j] * s : d[j] * s;
+                    if constexpr (GATED)
+                        out[H - 1][j] = d[j] * v;
+                }
+            });
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (j >= n)
+                        out[h][j] = 0.f;
+                    sum[h][j] += out[h][j];
+                }
+                if (g.dz)
+                    store8<E>(g.dz, t * g.pitch + h * half + c, 8, out[h]);
             }
         }
-        sa += da;
-        sb += db;
-        if (g.dz) {
-            store_el(g.dz, t * g.pitch + c, da, g.dtype);
-            if (g.gated)
-                store_el(g.dz, t * g.pitch + half + c, db, g.dtype);
-        }
     }
-    if (g.partial && c < g.I) {
-        float *p = g.partial + (int64_t)blockIdx.y * (g.gated ? 2 : 1) * g.I + c;
-        p[0] = sa;
-        if (g.gated)
-            p[g.I] = sb;
+    if (!g.want_sums)
+        return;
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            red[rl][h][cg * 8 + j] = sum[h][j];
+    __syncthreads();
+    const int64_t col = (int64_t)cb * kGradCols + threadIdx.x;
+    if (col >= g.I)
+        return;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        float s = 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            s += red[r][h][threadIdx.x];
+        if (row_blocks > 1)
+            g.partial[((int64_t)rb * H + h) * g.I + col] = s;
+        else if (g.sums[h])
+            store_el(g.sums[h], col, s, g.sums_dtype);
     }
 }
 
+// Column sums of the row blocks' sums, and zeros where there is no row at all: a
+// block owns 64 columns, its four waves a quarter of the row blocks each.
 __global__ __launch_bounds__(256) void k_dense_colsum(const float *partial, int row_blocks, int I, int n, int out_dtype,
                                                       void *out0, void *out1)
 {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= (int64_t)n * I)
-        return;
+    __shared__ float red[4][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane, cols = (int64_t)n * I;
     float s = 0.f;
-    for (int64_t r = 0; r < row_blocks; ++r)
-        s += partial[r * n * I + c];
+    if (c < cols)
+        for (int64_t r = w; r < row_blocks; r += 4)
+            s += partial[r * cols + c];
+    red[w][lane] = s;
+    __syncthreads();
+    if (w || c >= cols)
+        return;
     void *out = c < I ? out0 : out1;
     if (out)
-        store_el(out, c < I ? c : c - I, s, out_dtype);
+        store_el(out, c < I ? c : c - I, (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]), out_dtype);
 }
 
 }  // namespace
@@ -223,10 +263,6 @@ int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
         ECF_HIP_CHECK(hipGetDevice(&dev));
         ECF_HIP_CHECK(hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev));
         const DensePlan plan = plan16(g, cus, ws != nullptr);
-        g.vec_bias = aligned16(g.bias[0], 8, g.dtype) && aligned16(g.bias[1], 8, g.dtype);
-        g.vec_res = aligned16(g.res, g.ldres, g.out_dtype);
-        g.vec_out = aligned16(g.out[0], g.ldout, g.out_dtype) && aligned16(g.out[1], g.ldout, g.out_dtype);
-        g.vec_save = aligned16(g.save[0], g.ldsave, g.dtype) && aligned16(g.save[1], g.ldsave, g.dtype);
         const Tile16 &t = kTiles16[plan.tile];
         const int bn = g.gated ? t.bn / 2 : t.bn;
         DenseGrid gr{};
@@ -254,20 +290,33 @@ int dense_grad_row_blocks(int T) { return (T + kGradRows - 1) / kGradRows; }
 
 int launch_dense_grad(const DenseGrad &g, hipStream_t st)
 {
-    ProfScope p("dense_grad", st);
-    const int64_t cols = g.dz ? (g.gated ? g.pitch / 2 : g.pitch) : g.I;
-    hipLaunchKernelGGL(k_dense_grad, dim3((unsigned)((cols + 255) / 256), g.row_blocks), dim3(256), 0, st, g);
-    ECF_HIP_CHECK(hipGetLastError());
-    return ECF_OK;
-}
-
-int launch_dense_colsum(const float *partial, int row_blocks, int I, int n, int out_dtype, void *const out[2],
-                        hipStream_t st)
-{
-    ProfScope p("dense_colsum", st);
-    hipLaunchKernelGGL(k_dense_colsum, dim3((unsigned)(((int64_t)n * I + 255) / 256)), dim3(256), 0, st, partial,
-                       row_blocks, I, n, out_dtype, out[0], out[1]);
-    ECF_HIP_CHECK(hipGetLastError());
+    const int rows = dense_grad_row_blocks(g.T);
+    if (rows > 0) {
+        ProfScope p("dense_grad", st);
+        const dim3 grid((unsigned)((g.I + kGradCols - 1) / kGradCols) * rows), block(256);
+        auto go = [&](auto e, auto ed) {
+            using E = decltype(e);
+            using ED = decltype(ed);
+            if (g.gated)
+                hipLaunchKernelGGL((k_dense_grad<E, ED, true>), grid, block, 0, st, g, rows);
+            else
+                hipLaunchKernelGGL((k_dense_grad<E, ED, false>), grid, block, 0, st, g, rows);
+        };
+        if (g.dtype == ECF_F32)
+            go(F32{}, F32{});
+        else if (g.dtype == ECF_BF16)
+            g.dout_dtype == ECF_F32 ? go(BF16{}, F32{}) : go(BF16{}, BF16{});
+        else
+            g.dout_dtype == ECF_F32 ? go(F16{}, F32{}) : go(F16{}, F16{});
+        ECF_HIP_CHECK(hipGetLastError());
+    }
+    if (g.want_sums && rows != 1) {
+        ProfScope p("dense_colsum", st);
+        const int n = g.gated ? 2 : 1;
+        hipLaunchKernelGGL(k_dense_colsum, dim3((unsigned)(((int64_t)n * g.I + 63) / 64)), dim3(256), 0, st, g.partial,
+                           rows, g.I, n, g.sums_dtype, g.sums[0], g.sums[1]);
+        ECF_HIP_CHECK(hipGetLastError());
+    }
     return ECF_OK;
 }
 
