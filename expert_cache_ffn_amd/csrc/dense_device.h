@@ -27,9 +27,10 @@ struct F16 {
     static __device__ __forceinline__ raw from_f(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 };
 
-// 8 consecutive elements of a row, at any multiple of their size: unaligned
-// 16-byte accesses are as fast as aligned ones within a cache line.  n < 8: the
-// row ends after n of them, which go one by one.
+// 8 consecutive elements of a row from column `col` on, at any multiple of their
+// size (unaligned 16-byte accesses are one instruction here).  n < 8: the row ends
+// after n of them; then the row's last 8 are read and moved down, zeros behind
+// them (a row of under 8 elements goes one by one).
 struct __attribute__((packed, aligned(2))) any128x2 {
     u32x4_t v;
 };
@@ -37,10 +38,11 @@ struct __attribute__((packed, aligned(4))) any128x4 {
     f32x4_t v;
 };
 template <class E>
-__device__ __forceinline__ void load8(const void *p, int64_t i, int n, float v[8])
+__device__ __forceinline__ void load8(const void *row, int64_t col, int n, float v[8])
 {
-    const typename E::raw *q = (const typename E::raw *)p + i;
-    if (n >= 8) {
+    const int s = n >= 8 ? 0 : 8 - n;
+    const typename E::raw *q = (const typename E::raw *)row + (col - s);
+    if (col >= s) {
         if constexpr (sizeof(typename E::raw) == 4) {
             const f32x4_t a = ((const any128x4 *)q)->v, b = ((const any128x4 *)(q + 4))->v;
 #pragma unroll
@@ -54,17 +56,25 @@ __device__ __forceinline__ void load8(const void *p, int64_t i, int n, float v[8
                 v[2 * j + 1] = E::to_f((uint16_t)(a[j] >> 16));
             }
         }
+        if (s) {
+#pragma unroll
+            for (int b = 4; b >= 1; b >>= 1)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (s & b)
+                        v[j] = j + b < 8 ? v[j + b] : 0.f;
+        }
         return;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        v[j] = j < n ? E::to_f(q[j]) : 0.f;
+        v[j] = j < n ? E::to_f(q[j + s]) : 0.f;
 }
 
 template <class E>
-__device__ __forceinline__ void store8(void *p, int64_t i, int n, const float v[8])
+__device__ __forceinline__ void store8(void *row, int64_t col, int n, const float v[8])
 {
-    typename E::raw *q = (typename E::raw *)p + i;
+    typename E::raw *q = (typename E::raw *)row + col;
     if (n >= 8) {
         if constexpr (sizeof(typename E::raw) == 4) {
             ((any128x4 *)q)->v = f32x4_t{v[0], v[1], v[2], v[3]};
@@ -181,6 +191,17 @@ __device__ __forceinline__ void with_act(int act, F f)
     case ECF_ACT_GELU_TANH: f(std::integral_constant<int, ECF_ACT_GELU_TANH>{}); break;
     default: f(std::integral_constant<int, ECF_ACT_RELU>{}); break;
     }
+}
+
+template <class E>
+__device__ __forceinline__ const void *row_at(const void *p, int64_t at)
+{
+    return (const typename E::raw *)p + at;
+}
+template <class E>
+__device__ __forceinline__ void *row_at(void *p, int64_t at)
+{
+    return (typename E::raw *)p + at;
 }
 
 }  // namespace ecf

@@ -100,7 +100,7 @@ __device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t 
                 z[q][j] += bv[j];
         }
         if (g.save[q])
-            store8<E>(g.save[q], m * g.ldsave + n, cnt, z[q]);
+            store8<E>(row_at<E>(g.save[q], m * g.ldsave), n, cnt, z[q]);
     }
     void *out = g.out[half];
     if (!out)
@@ -118,17 +118,17 @@ __device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t 
     } else if (g.res) {
         float r[8];
         if (g.out_dtype == ECF_F32)
-            load8<F32>(g.res, m * g.ldres + n, cnt, r);
+            load8<F32>(row_at<F32>(g.res, m * g.ldres), n, cnt, r);
         else
-            load8<E>(g.res, m * g.ldres + n, cnt, r);
+            load8<E>(row_at<E>(g.res, m * g.ldres), n, cnt, r);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             y[j] += r[j];
     }
     if (g.out_dtype == ECF_F32)
-        store8<F32>(out, m * g.ldout + n, cnt, y);
+        store8<F32>(row_at<F32>(out, m * g.ldout), n, cnt, y);
     else
-        store8<E>(out, m * g.ldout + n, cnt, y);
+        store8<E>(row_at<E>(out, m * g.ldout), n, cnt, y);
 }
 
 // ---- operand tiles ----------------------------------------------------------------------
@@ -192,7 +192,7 @@ __device__ __forceinline__ int kswz(int k)
     return ROWS >= 128 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
 }
 
-// v shifted down by s 16-bit elements (0..7), zeros from above
+// v shifted down by s 16-bit elements (0..7; v is 0 where s is more), zeros from above
 __device__ __forceinline__ u32x4_t shift_down(u32x4_t v, int s)
 {
     if (s & 4)
@@ -218,6 +218,7 @@ struct Tile {
     int row, chunk;    // the first of this thread's LDS rows, and its chunk in all of them
     int valid;         // T: elements of the chunk that exist (up to 8, none if <= 0)
     int width;         // elements in a row of the operand: those before a row's last chunk may be read
+    int shift;         // register path: elements by which the loaded chunks are to move down
     u32x4_t reg[DMA ? 1 : NL];
 
     // `rows` rows from the tile's first on, row stride ld (elements); rowmap turns a
@@ -262,22 +263,23 @@ struct Tile {
     {
         if constexpr (!DMA) {
             const int n = T ? valid : kleft - chunk * 8;
+            shift = max(0, 8 - n);
             if (n >= 8 && (!T || kleft >= BK)) {
 #pragma unroll
                 for (int q = 0; q < NL; ++q)
                     reg[q] = ((const any128x2 *)((const char *)(PAIR && second(q, wave) ? base2 : base) + off[q]))->v;
             } else {
                 // a chunk that the operand's edge cuts: its 8 elements that end at the
-                // edge, shifted down (rows of under 8 elements: one by one)
+                // edge, which store() shifts down (rows of under 8 elements: one by one)
 #pragma unroll
                 for (int q = 0; q < NL; ++q) {
-                    const uint16_t *p = (const uint16_t *)((const char *)(PAIR && second(q, wave) ? base2 : base) + off[q]);
+                    const uint16_t *p =
+                        (const uint16_t *)((const char *)(PAIR && second(q, wave) ? base2 : base) + off[q]);
                     reg[q] = u32x4_t{0, 0, 0, 0};
                     if (n <= 0 || (T && row + STEP * q >= kleft))
                         continue;
-                    const int s = max(0, 8 - n);
                     if (width >= 8) {
-                        reg[q] = shift_down(((const any128x2 *)(p - s))->v, s);
+                        reg[q] = ((const any128x2 *)(p - shift))->v;
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
@@ -285,6 +287,8 @@ struct Tile {
                                 reg[q][j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
                     }
                 }
+                if (width < 8)
+                    shift = 0;
             }
         }
     }
@@ -292,6 +296,11 @@ struct Tile {
     // register path: the loaded k-tile to its stage
     __device__ __forceinline__ void store(char *stage, int tid)
     {
+        if (shift) {
+#pragma unroll
+            for (int q = 0; q < NL; ++q)
+                reg[q] = shift_down(reg[q], shift);
+        }
 #pragma unroll
         for (int q = 0; q < NL; ++q)
             ((u32x4_t *)stage)[q * NTH + tid] = reg[q];

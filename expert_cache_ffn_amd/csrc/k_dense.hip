@@ -121,11 +121,11 @@ __global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks)
 #pragma unroll 2
         for (int64_t t = rb * kGradRows + rl; t < t1; t += 8) {
             float d[8], a[8], b[8], out[H][8];
-            load8<ED>(g.dout, t * g.lddout + c, n, d);
+            load8<ED>(row_at<ED>(g.dout, t * g.lddout), c, n, d);
             if (g.a)
-                load8<E>(g.a, t * g.ldab + c, n, a);
+                load8<E>(row_at<E>(g.a, t * g.ldab), c, n, a);
             if constexpr (GATED)
-                load8<E>(g.b, t * g.ldab + c, n, b);
+                load8<E>(row_at<E>(g.b, t * g.ldab), c, n, b);
             with_act(g.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks)
                     sum[h][j] += out[h][j];
                 }
                 if (g.dz)
-                    store8<E>(g.dz, t * g.pitch + h * half + c, 8, out[h]);
+                    store8<E>(row_at<E>(g.dz, t * g.pitch + h * half), c, 8, out[h]);
             }
         }
     }
