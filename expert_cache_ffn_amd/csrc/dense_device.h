@@ -27,6 +27,18 @@ struct F16 {
     static __device__ __forceinline__ raw from_f(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 };
 
+// v shifted down by s 16-bit elements (0..7; v is 0 where s is more), zeros from above
+__device__ __forceinline__ u32x4_t shift_down16(u32x4_t v, int s)
+{
+    if (s & 4)
+        v = u32x4_t{v[2], v[3], 0, 0};
+    if (s & 2)
+        v = u32x4_t{v[1], v[2], v[3], 0};
+    if (s & 1)
+        v = u32x4_t{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+    return v;
+}
+
 // 8 consecutive elements of a row from column `col` on, at any multiple of their
 // size (unaligned 16-byte accesses are one instruction here).  n < 8: the row ends
 // after n of them; then the row's last 8 are read and moved down, zeros behind

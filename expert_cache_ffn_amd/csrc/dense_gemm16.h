@@ -192,18 +192,6 @@ __device__ __forceinline__ int kswz(int k)
     return ROWS >= 128 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
 }
 
-// v shifted down by s 16-bit elements (0..7; v is 0 where s is more), zeros from above
-__device__ __forceinline__ u32x4_t shift_down(u32x4_t v, int s)
-{
-    if (s & 4)
-        v = u32x4_t{v[2], v[3], 0, 0};
-    if (s & 2)
-        v = u32x4_t{v[1], v[2], v[3], 0};
-    if (s & 1)
-        v = u32x4_t{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
-    return v;
-}
-
 // One operand's tile of ROWS rows (m or n) x BK k.  T: m-contiguous in memory.
 template <bool T, bool DMA, int ROWS, int NTH, int BK>
 struct Tile {
@@ -299,7 +287,7 @@ struct Tile {
         if (shift) {
 #pragma unroll
             for (int q = 0; q < NL; ++q)
-                reg[q] = shift_down(reg[q], shift);
+                reg[q] = shift_down16(reg[q], shift);
         }
 #pragma unroll
         for (int q = 0; q < NL; ++q)
@@ -589,6 +577,7 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseGemm g, DenseGrid gr)
     const int n = (int)(i - row * per) * 8, half = row >= g.M ? 1 : 0;
     const int64_t m = row - (half ? g.M : 0);
     float z[GATED ? 2 : 1][8] = {};
+#pragma unroll 4
     for (int s = 0; s < gr.splits; ++s)
 #pragma unroll
         for (int q = 0; q < (GATED ? 2 : 1); ++q) {

@@ -258,10 +258,12 @@ int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
 {
     DenseGemm g = gin;
     ProfScope p(g.gated ? "dense_gated" : g.a_t ? "dense_gemm_tn" : g.b_t ? "dense_gemm_nn" : "dense_gemm_nt", st);
+    int dev = 0, cus = 0;
+    ECF_HIP_CHECK(hipGetDevice(&dev));
+    ECF_HIP_CHECK(hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev));
+    if (!g.a_t && !g.b_t && g.M <= kFewTokens)
+        return launch_dense_few(g, cus, st);
     if (g.dtype != ECF_F32) {
-        int dev = 0, cus = 0;
-        ECF_HIP_CHECK(hipGetDevice(&dev));
-        ECF_HIP_CHECK(hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev));
         const DensePlan plan = plan16(g, cus, ws != nullptr);
         const Tile16 &t = kTiles16[plan.tile];
         const int bn = g.gated ? t.bn / 2 : t.bn;
