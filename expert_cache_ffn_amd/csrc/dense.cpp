@@ -90,9 +90,9 @@ int check_grad_dtype(const char *what, int32_t t, int32_t dtype)
             return _rc;                \
     } while (0)
 
-size_t forward_ws(int dtype, int64_t T, int64_t out, int planes)
+size_t forward_ws(int64_t T, int64_t out, int planes)
 {
-    return T <= kFewTokens ? 0 : dense_gemm_ws(dtype, T, out, planes);
+    return T <= kFewTokens ? 0 : dense_gemm_ws(T, out, planes);
 }
 
 // Backward workspace: dz rows in `dtype` (gated: da and db halves of one row,
@@ -108,7 +108,7 @@ BackWs back_ws(int64_t in, int64_t cols, int halves, int dtype, int32_t T)
     w.pitch = halves * ((cols + 7) / 8 * 8);
     w.colsum = al256((size_t)T * w.pitch * dense_esize(dtype));
     w.split = w.colsum + al256((size_t)dense_grad_row_blocks(T) * halves * cols * 4);
-    w.total = w.split + std::max(dense_gemm_ws(dtype, T, in, 1), dense_gemm_ws(dtype, cols, in, halves));
+    w.total = w.split + std::max(dense_gemm_ws(T, in, 1), dense_gemm_ws(cols, in, halves));
     return w;
 }
 
@@ -123,7 +123,7 @@ size_t ecf_gated_workspace_bytes(int32_t hidden, int32_t inter, int32_t dtype, i
 {
     if (check_common("ecf_gated_workspace_bytes", hidden, inter, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
-    return backward ? back_ws(hidden, inter, 2, dtype, n_tokens).total : forward_ws(dtype, n_tokens, inter, 2);
+    return backward ? back_ws(hidden, inter, 2, dtype, n_tokens).total : forward_ws(n_tokens, inter, 2);
 }
 
 int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
@@ -158,7 +158,7 @@ int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
             DENSE_TRY(check_matrix(me, "d_a", a->d_a, g.ldsave, I, a->dtype));
             DENSE_TRY(check_matrix(me, "d_b", a->d_b, g.ldsave, I, a->dtype));
         }
-        const size_t need = forward_ws(a->dtype, T, I, 2);
+        const size_t need = forward_ws(T, I, 2);
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, need));
         g.a[0] = a->d_x;
         g.b[0] = a->d_w_gate, g.b[1] = a->d_w_up;
@@ -261,7 +261,7 @@ size_t ecf_linear_workspace_bytes(int32_t in_features, int32_t out_features, int
     if (check_common("ecf_linear_workspace_bytes", in_features, out_features, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
     return backward ? back_ws(in_features, out_features, 1, dtype, n_tokens).total
-                    : forward_ws(dtype, n_tokens, out_features, 1);
+                    : forward_ws(n_tokens, out_features, 1);
 }
 
 int ecf_linear_forward(const ecf_linear_args *a, int32_t T)
@@ -292,7 +292,7 @@ int ecf_linear_forward(const ecf_linear_args *a, int32_t T)
             DENSE_TRY(check_matrix(me, "d_residual", a->d_residual, g.ldres, N, a->out_dtype));
         if (a->d_z)
             DENSE_TRY(check_matrix(me, "d_z", a->d_z, g.ldsave, N, a->dtype));
-        const size_t need = forward_ws(a->dtype, T, N, 1);
+        const size_t need = forward_ws(T, N, 1);
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, need));
         g.a[0] = a->d_x, g.b[0] = a->d_w;
         g.bias[0] = a->d_bias;

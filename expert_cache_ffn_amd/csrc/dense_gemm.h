@@ -1,5 +1,5 @@
-// The 16-bit (bf16, fp16) matrix products of the dense feed-forward operators on
-// gfx950 MFMA (v_mfma_f32_32x32x16), fp32 accumulators.
+// The matrix products of the dense feed-forward operators on gfx950 MFMA
+// (v_mfma_f32_32x32x16 of bf16 or fp16), fp32 accumulators.
 //
 //   acc[m][n] = sum_k A(m, k) B(n, k), each operand k- or m/n-contiguous
 //
@@ -20,6 +20,15 @@
 // gets the 4 k of its m); the 64-byte groups of a row are XORed with k & 3, so
 // that the four k rows of such a fetch lie in distinct banks.  So the backward
 // products read dz, W and x as they are, without a transposing pass.
+//
+// fp32 operands are split on their way to LDS into three bf16 parts, x = h + m + l
+// exactly (8 bits of the significand each, rounded to nearest), and six products
+// make one: hh' + hm' + mh' + hl' + lh' + mm'.  What is left out is below 2^-26 of
+// |x x'|, less than the rounding of an fp32 product.  Six bf16 MFMAs of 16 k take
+// 192 cycles of the matrix pipe, the eight fp32 ones they replace 512.  An
+// infinity or NaN goes into l alone, which meets only h' and so gives what it
+// should (infinity times infinity gives NaN); parts under bf16's subnormal step
+// are lost: 2^-134 |x'| per product.
 //
 // Output goes out by rows through LDS, 8 columns per lane: bias, activation,
 // residual and the gated product are applied there to the fp32 sums, and loads
@@ -48,6 +57,12 @@ __device__ __forceinline__ f32x16_t mfma16<F16>(u32x4_t a, u32x4_t b, f32x16_t c
 {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
                                                   0, 0);
+}
+
+template <>
+__device__ __forceinline__ f32x16_t mfma16<F32>(u32x4_t a, u32x4_t b, f32x16_t c)  // of parts
+{
+    return mfma16<BF16>(a, b, c);
 }
 
 // The blocks of one product, in one dimension: splits of K x output tiles.  Block b
@@ -133,7 +148,7 @@ __device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t 
 
 // ---- operand tiles ----------------------------------------------------------------------
 
-namespace g16 {
+namespace gemm {
 
 constexpr uint32_t kNowhere = 0x80000000u;  // a buffer offset past every resource: reads zeros, touches no memory
 
@@ -192,9 +207,69 @@ __device__ __forceinline__ int kswz(int k)
     return ROWS >= 128 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
 }
 
+// Two fp32 values to their three bf16 parts, packed: exact for finite values.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t &h, uint32_t &m, uint32_t &l)
+{
+    auto pack = [](float a, float b) {
+        const bf16x2_t v = {(__bf16)a, (__bf16)b};
+        return __builtin_bit_cast(uint32_t, v);
+    };
+    h = pack(x0, x1);
+    const float r0 = x0 - bf_lo(h), r1 = x1 - bf_hi(h);
+    m = pack(r0, r1);
+    l = pack(r0 - bf_lo(m), r1 - bf_hi(m));
+}
+
+// 8 fp32 values to three chunks of bf16 parts.  Values at or above the largest that
+// rounds to a finite bf16 take the slow way: there h is cut off instead of rounded,
+// and infinities and NaN go into l.
+__device__ __forceinline__ void split8(const u32x4_t v[2], u32x4_t part[3])
+{
+    constexpr uint32_t kBig = 0x7f7f8000u;
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        top = max(top, v[j >> 2][j & 3] & 0x7fffffffu);
+    if (top < kBig) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t h, m, l;
+            split2(__uint_as_float(v[j >> 1][2 * (j & 1)]), __uint_as_float(v[j >> 1][2 * (j & 1) + 1]), h, m, l);
+            part[0][j] = h, part[1][j] = m, part[2][j] = l;
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t w[3] = {0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t u = v[j >> 1][2 * (j & 1) + e], mag = u & 0x7fffffffu;
+            const float x = __uint_as_float(u);
+            uint32_t h, m, l;
+            split2(x, 0.f, h, m, l);
+            if (mag >= 0x7f800000u) {
+                h = m = 0;
+                l = f_to_bf(x);
+            } else if (mag >= kBig) {
+                h = u >> 16;
+                const float r = x - bf_to_f((uint16_t)h);
+                m = f_to_bf(r);
+                l = f_to_bf(r - bf_to_f((uint16_t)m));
+            }
+            w[0] |= (h & 0xffffu) << (16 * e), w[1] |= (m & 0xffffu) << (16 * e), w[2] |= (l & 0xffffu) << (16 * e);
+        }
+        part[0][j] = w[0], part[1][j] = w[1], part[2][j] = w[2];
+    }
+}
+
 // One operand's tile of ROWS rows (m or n) x BK k.  T: m-contiguous in memory.
-template <bool T, bool DMA, int ROWS, int NTH, int BK>
+// ES: bytes per element in memory; fp32 tiles (register path) lie in LDS as three
+// planes of bf16 parts.
+template <bool T, bool DMA, int ROWS, int NTH, int BK, int ES>
 struct Tile {
+    static_assert(ES == 2 || !DMA, "fp32 is split on its way to LDS");
+    static constexpr int W = ES / 2;  // 16-byte registers per chunk of 8 elements
     static constexpr int CPR = T ? ROWS / 8 : BK / 8;  // chunks per LDS row
     static constexpr int NL = ROWS * BK / 8 / NTH;     // 16-byte loads per thread and k-tile
     static constexpr int STEP = NTH / CPR;             // LDS rows between a thread's loads
@@ -207,7 +282,7 @@ struct Tile {
     int valid;         // T: elements of the chunk that exist (up to 8, none if <= 0)
     int width;         // elements in a row of the operand: those before a row's last chunk may be read
     int shift;         // register path: elements by which the loaded chunks are to move down
-    u32x4_t reg[DMA ? 1 : NL];
+    u32x4_t reg[DMA ? 1 : NL][W];
 
     // `rows` rows from the tile's first on, row stride ld (elements); rowmap turns a
     // tile row into a row relative to the base (clamped to the last one)
@@ -221,13 +296,13 @@ struct Tile {
             valid = 8;
 #pragma unroll
             for (int q = 0; q < NL; ++q)
-                off[q] = (uint32_t)(rowmap(row + STEP * q) * ld * 2) + chunk * 16;
+                off[q] = (uint32_t)(rowmap(row + STEP * q) * ld * ES) + chunk * (8 * ES);
         } else {
             chunk = (tid % CPR) ^ kswz<ROWS>(row);
             valid = rows - chunk * 8;
 #pragma unroll
             for (int q = 0; q < NL; ++q)
-                off[q] = (uint32_t)((row + STEP * q) * ld * 2) + chunk * 16;
+                off[q] = (uint32_t)((row + STEP * q) * ld * ES) + chunk * (8 * ES);
         }
     }
 
@@ -255,24 +330,29 @@ struct Tile {
             if (n >= 8 && (!T || kleft >= BK)) {
 #pragma unroll
                 for (int q = 0; q < NL; ++q)
-                    reg[q] = ((const any128x2 *)((const char *)(PAIR && second(q, wave) ? base2 : base) + off[q]))->v;
+                    take(q, (const char *)(PAIR && second(q, wave) ? base2 : base) + off[q]);
             } else {
                 // a chunk that the operand's edge cuts: its 8 elements that end at the
                 // edge, which store() shifts down (rows of under 8 elements: one by one)
 #pragma unroll
                 for (int q = 0; q < NL; ++q) {
-                    const uint16_t *p =
-                        (const uint16_t *)((const char *)(PAIR && second(q, wave) ? base2 : base) + off[q]);
-                    reg[q] = u32x4_t{0, 0, 0, 0};
+                    const char *p = (const char *)(PAIR && second(q, wave) ? base2 : base) + off[q];
+#pragma unroll
+                    for (int w = 0; w < W; ++w)
+                        reg[q][w] = u32x4_t{0, 0, 0, 0};
                     if (n <= 0 || (T && row + STEP * q >= kleft))
                         continue;
                     if (width >= 8) {
-                        reg[q] = ((const any128x2 *)(p - shift))->v;
+                        take(q, p - shift * ES);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            if (j < n)
-                                reg[q][j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+                            if (j < n) {
+                                if constexpr (ES == 2)
+                                    reg[q][0][j >> 1] |= (uint32_t)((const uint16_t *)p)[j] << (16 * (j & 1));
+                                else
+                                    reg[q][j >> 2][j & 3] = ((const uint32_t *)p)[j];
+                            }
                     }
                 }
                 if (width < 8)
@@ -281,17 +361,47 @@ struct Tile {
         }
     }
 
+    __device__ __forceinline__ void take(int q, const char *p)
+    {
+        if constexpr (ES == 2) {
+            reg[q][0] = ((const any128x2 *)p)->v;
+        } else {
+            reg[q][0] = __builtin_bit_cast(u32x4_t, ((const any128x4 *)p)->v);
+            reg[q][1] = __builtin_bit_cast(u32x4_t, ((const any128x4 *)(p + 16))->v);
+        }
+    }
+
     // register path: the loaded k-tile to its stage
     __device__ __forceinline__ void store(char *stage, int tid)
     {
         if (shift) {
 #pragma unroll
-            for (int q = 0; q < NL; ++q)
-                reg[q] = shift_down16(reg[q], shift);
+            for (int q = 0; q < NL; ++q) {
+                if constexpr (ES == 2) {
+                    reg[q][0] = shift_down16(reg[q][0], shift);
+                } else {
+#pragma unroll
+                    for (int b = 4; b >= 1; b >>= 1)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (shift & b)
+                                reg[q][j >> 2][j & 3] = j + b < 8 ? reg[q][(j + b) >> 2][(j + b) & 3] : 0u;
+                }
+            }
         }
 #pragma unroll
-        for (int q = 0; q < NL; ++q)
-            ((u32x4_t *)stage)[q * NTH + tid] = reg[q];
+        for (int q = 0; q < NL; ++q) {
+            u32x4_t *at = (u32x4_t *)stage + q * NTH + tid;
+            if constexpr (ES == 2) {
+                *at = reg[q][0];
+            } else {
+                u32x4_t part[3];
+                split8(reg[q], part);
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+                    at[p * (ROWS * BK / 8)] = part[p];
+            }
+        }
     }
 };
 
@@ -337,19 +447,20 @@ struct Frag {
     }
 };
 
-}  // namespace g16
+}  // namespace gemm
 
 // grid: 1-D, one block per (split, output tile); see DenseGrid.
 template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE>
-__global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 2) void k_gemm16(DenseGemm g,
+__global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 2) void k_gemm(DenseGemm g,
                                                                                                    DenseGrid gr)
 {
-    using namespace g16;
+    using namespace gemm;
     constexpr int NW = WM * WN, NTH = 64 * NW, RM = BM / WM, RN = BN / WN, FM = RM / 32, FN = RN / 32;
     static_assert(BK % 32 == 0, "two sets of fragments take turns");
     static_assert(FM >= 1 && FN >= 1 && (!GATED || (FN % 2 == 0 && !BT)), "wave tile");
     constexpr int NS = DMA ? NSTAGE : 2;
-    constexpr int SA = BM * BK * 2, SB = BN * BK * 2;  // bytes per stage
+    constexpr int ES = sizeof(typename E::raw), NP = ES == 4 ? 3 : 1;      // planes of parts
+    constexpr int PA = BM * BK * 2, PB = BN * BK * 2, SA = PA * NP, SB = PB * NP;  // bytes per plane and stage
     constexpr int PITCH = (FN >= 2 ? 64 : 32) + 4;  // fp32 per row of the output staging
     constexpr int OUT = NW * 32 * PITCH * 4, IN = NS * (SA + SB);
     __shared__ __attribute__((aligned(16))) char lds[OUT > IN ? OUT : IN];
@@ -361,8 +472,8 @@ __global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 
     const int m0 = mt * BM, n0 = nt * (GATED ? BN / 2 : BN);
     const int mrows = min(BM, g.M - m0);
 
-    Tile<AT, DMA, BM, NTH, BK> ta;
-    Tile<BT, DMA, BN, NTH, BK> tb;
+    Tile<AT, DMA, BM, NTH, BK, ES> ta;
+    Tile<BT, DMA, BN, NTH, BK, ES> tb;
     const int nrows = GATED ? 0 : g.N - n0, nlast = g.N - 1 - n0;
     ta.init(tid, g.M - m0, AT ? g.M : g.K, g.lda, [&](int r) { return (int64_t)min(r, mrows - 1); });
     // gated: 64 tile rows are 32 of the gate projection, then the same 32 of the up projection
@@ -391,11 +502,11 @@ __global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 
     const char *pa[2], *pb[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        pa[q] = (const char *)g.a[AT ? half : q] + (AT ? (int64_t)m0 : (int64_t)m0 * g.lda) * 2;
-        pb[q] = (const char *)g.b[q] + (BT ? (int64_t)n0 : (int64_t)n0 * g.ldb) * 2;
+        pa[q] = (const char *)g.a[AT ? half : q] + (AT ? (int64_t)m0 : (int64_t)m0 * g.lda) * ES;
+        pb[q] = (const char *)g.b[q] + (BT ? (int64_t)n0 : (int64_t)n0 * g.ldb) * ES;
         asm volatile("" : "+s"(pa[q]), "+s"(pb[q]));
     }
-    const int64_t stepa = (AT ? g.lda : 1) * (2 * BK), stepb = (BT ? g.ldb : 1) * (2 * BK);
+    const int64_t stepa = (AT ? g.lda : 1) * (ES * BK), stepb = (BT ? g.ldb : 1) * (ES * BK);
     constexpr int NLA = decltype(ta)::NL, NLD = NLA + decltype(tb)::NL;
     // k-tile kt: past the end nothing is loaded (zeros)
     struct Src {
@@ -430,13 +541,15 @@ __global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 
     // Two sets of fragments: step ks + 1 (or the next k-tile's step 0) is read under
     // the MFMAs of step ks.
     constexpr int NK = BK / 16;
-    u32x4_t av[2][FM], bv[2][FN];
+    u32x4_t av[2][FM][NP], bv[2][FN][NP];
     auto fetch = [&](int stage, int ks, int set, int f) __attribute__((always_inline)) {
         const char *sa = lds + stage * (SA + SB), *sb = sa + SA;
-        if (f < FN)
-            bv[set][f] = fb.read(sb, f, ks);
-        else
-            av[set][f - FN] = fa.read(sa, f - FN, ks);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+            if (f < FN)
+                bv[set][f][p] = fb.read(sb + p * PB, f, ks);
+            else
+                av[set][f - FN][p] = fa.read(sa + p * PA, f - FN, ks);
     };
     auto fetch_all = [&](int stage) __attribute__((always_inline)) {
 #pragma unroll
@@ -460,7 +573,16 @@ __global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 
                 for (int q = i * NLD / MF; q < (i + 1) * NLD / MF; ++q)
                     issue(s, into, q);
             }
-            acc[i / FN][i % FN] = mfma16<E>(av[set][i / FN], bv[set][i % FN], acc[i / FN][i % FN]);
+            const u32x4_t *a = av[set][i / FN], *b = bv[set][i % FN];
+            f32x16_t &c = acc[i / FN][i % FN];
+            if constexpr (NP == 3) {  // the small products first
+                c = mfma16<E>(a[1], b[1], c);
+                c = mfma16<E>(a[0], b[2], c);
+                c = mfma16<E>(a[2], b[0], c);
+                c = mfma16<E>(a[0], b[1], c);
+                c = mfma16<E>(a[1], b[0], c);
+            }
+            c = mfma16<E>(a[0], b[0], c);
             __builtin_amdgcn_sched_barrier(0);
         }
     };

@@ -38,9 +38,9 @@ int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st);
 // Forward products of at most kFewTokens rows (k_dense_few.hip) need no workspace.
 constexpr int kFewTokens = 16;
 int launch_dense_few(const DenseGemm &g, int cus, hipStream_t st);
-// The largest workspace of any product of these types with up to M x N outputs.
+// The largest workspace of any product with up to M x N outputs in each plane.
 constexpr size_t kDensePartialBytes = (size_t)32 << 20;  // fp32 sums of split products
-size_t dense_gemm_ws(int dtype, int64_t M, int64_t N, int planes);
+size_t dense_gemm_ws(int64_t M, int64_t N, int planes);
 
 // dz rows of the backward passes, in the operands' type: dz[t][i] (linear) or
 // da = dz[t][i], db = dz[t][pitch / 2 + i] (gated).  Columns from I to the (half)

@@ -1,0 +1,54 @@
+// Launches of the products for one pair of operand layouts.
+#pragma once
+
+#include "dense_gemm.h"
+
+namespace ecf {
+
+template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN, int BK, int NS>
+void launch_gemm(const DenseGemm &g, const DenseGrid &gr, hipStream_t st)
+{
+    hipLaunchKernelGGL((k_gemm<E, AT, BT, GATED, DMA, BM, BN, WM, WN, BK, NS>), dim3(gr.blocks()), dim3(64 * WM * WN), 0, st,
+                       g, gr);
+}
+
+template <class E, bool AT, bool BT, bool GATED, bool DMA>
+int pick_gemm(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st)
+{
+    if constexpr (std::is_same<E, F32>::value) {
+        if (p.tile == 0)  // the order of kTiles32
+            launch_gemm<E, AT, BT, GATED, false, 128, 128, 4, 2, 32, 2>(g, gr, st);
+        else
+            launch_gemm<E, AT, BT, GATED, false, 64, 64, 2, 1, 32, 2>(g, gr, st);
+    } else switch (p.tile) {  // the order of kTiles16
+    case 0: launch_gemm<E, AT, BT, GATED, DMA, 256, 256, 2, 4, 64, 2>(g, gr, st); break;
+    case 1: launch_gemm<E, AT, BT, GATED, DMA, 128, 256, 2, 4, 64, 3>(g, gr, st); break;
+    case 2: launch_gemm<E, AT, BT, GATED, DMA, 128, 128, 2, 2, 64, 2>(g, gr, st); break;
+    default: launch_gemm<E, AT, BT, GATED, DMA, 64, 128, 2, 2, 64, 3>(g, gr, st); break;
+    }
+    if (gr.splits > 1) {
+        const int64_t n = gr.np / 8 * g.M * g.mhalves;
+        hipLaunchKernelGGL((k_dense_join<E, GATED>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, g, gr);
+    }
+    ECF_HIP_CHECK(hipGetLastError());
+    return ECF_OK;
+}
+
+template <bool AT, bool BT, bool GATED>
+int run_gemm(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st)
+{
+    if (g.dtype == ECF_F32)
+        return pick_gemm<F32, AT, BT, GATED, false>(g, p, gr, st);
+    if (g.dtype == ECF_BF16)
+        return p.dma ? pick_gemm<BF16, AT, BT, GATED, true>(g, p, gr, st)
+                     : pick_gemm<BF16, AT, BT, GATED, false>(g, p, gr, st);
+    return p.dma ? pick_gemm<F16, AT, BT, GATED, true>(g, p, gr, st)
+                 : pick_gemm<F16, AT, BT, GATED, false>(g, p, gr, st);
+}
+
+int launch_gemm_gated(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st);
+int launch_gemm_nt(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st);
+int launch_gemm_nn(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st);
+int launch_gemm_tn(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st);
+
+}  // namespace ecf

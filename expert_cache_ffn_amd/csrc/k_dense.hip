@@ -1,29 +1,12 @@
-// Dense feed-forward operators: the matrix products of the gated projection and
-// of the linear layer, forward and backward, for any size, stride and alignment.
-//
-//   acc[m][n] = sum_k A(m, k) B(n, k), either operand k- or m-contiguous
-//
-// A block owns a 64 x 64 tile of the output, stages 16 k of both operands in
-// LDS as fp32 (widened once, exactly) and each of its 256 threads sums a 4 x 4
-// patch with fp32 FMAs; the gated form keeps two patches, one per projection,
-// and joins them in registers.  The epilogue adds bias, applies the activation,
-// adds the residual and rounds once.
+// Dense feed-forward operators: the choice of a product's kernel, the products of
+// fp32 operands with a short reduction, and the elementwise half of the backward passes.
 #include <algorithm>
+#include <atomic>
 
-#include "dense_launch16.h"
+#include "dense_launch.h"
 
 namespace ecf {
 namespace {
-
-constexpr int TM = 64, TN = 64, TK = 16;
-
-__device__ __forceinline__ float load_el(const void *p, int64_t i, int dtype)
-{
-    if (dtype == ECF_F32)
-        return ((const float *)p)[i];
-    const uint16_t v = ((const uint16_t *)p)[i];
-    return dtype == ECF_BF16 ? BF16::to_f(v) : F16::to_f(v);
-}
 
 __device__ __forceinline__ void store_el(void *p, int64_t i, float v, int dtype)
 {
@@ -33,32 +16,36 @@ __device__ __forceinline__ void store_el(void *p, int64_t i, float v, int dtype)
         ((uint16_t *)p)[i] = dtype == ECF_BF16 ? BF16::from_f(v) : F16::from_f(v);
 }
 
-// MHALVES: the upper half of gridDim.y works on a[1] -> out[1].
+// fp32 products over few k (under kShortK) with fp32 FMAs: a block owns a 64 x 64
+// tile of the output, stages 16 k of both operands in LDS and each of its 256
+// threads sums a 4 x 4 patch (two, gated).  grid: x over N, y over M of both halves.
+constexpr int TM = 64, TN = 64, TK = 16;
+
 template <bool GATED>
-__global__ __launch_bounds__(256) void k_dense_tile(DenseGemm g)
+__global__ __launch_bounds__(256) void k_dense_short(DenseGemm g, int tiles_n)
 {
     __shared__ float As[TK][TM + 1], Bs[GATED ? 2 : 1][TK][TN + 1];
-    const int mt = (g.M + TM - 1) / TM;
-    const int half = (int)blockIdx.y / mt;
-    const int m0 = ((int)blockIdx.y % mt) * TM, n0 = (int)blockIdx.x * TN;
+    const int mt = (g.M + TM - 1) / TM, ty0 = (int)blockIdx.x / tiles_n;
+    const int half = ty0 / mt;
+    const int m0 = (ty0 % mt) * TM, n0 = ((int)blockIdx.x % tiles_n) * TN;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     float acc[GATED ? 2 : 1][4][4] = {};
     for (int s = 0; s < g.ksegs; ++s) {
-        const void *pa = g.a[g.mhalves == 2 ? half : s];
+        const float *pa = (const float *)g.a[g.mhalves == 2 ? half : s];
         for (int k0 = 0; k0 < g.K; k0 += TK) {
             for (int i = tid; i < TM * TK; i += 256) {
                 const int m = g.a_t ? i % TM : i / TK, k = g.a_t ? i / TM : i % TK;
                 const int64_t gm = m0 + m, gk = k0 + k;
-                As[k][m] = gm < g.M && gk < g.K ? load_el(pa, g.a_t ? gk * g.lda + gm : gm * g.lda + gk, g.dtype) : 0.f;
+                As[k][m] = gm < g.M && gk < g.K ? pa[g.a_t ? gk * g.lda + gm : gm * g.lda + gk] : 0.f;
             }
             for (int i = tid; i < TN * TK; i += 256) {
                 const int n = g.b_t ? i % TN : i / TK, k = g.b_t ? i / TN : i % TK;
                 const int64_t gn = n0 + n, gk = k0 + k;
                 const bool in = gn < g.N && gk < g.K;
                 const int64_t at = g.b_t ? gk * g.ldb + gn : gn * g.ldb + gk;
-                Bs[0][k][n] = in ? load_el(g.b[GATED ? 0 : s], at, g.dtype) : 0.f;
+                Bs[0][k][n] = in ? ((const float *)g.b[GATED ? 0 : s])[at] : 0.f;
                 if (GATED)
-                    Bs[GATED][k][n] = in ? load_el(g.b[1], at, g.dtype) : 0.f;
+                    Bs[GATED][k][n] = in ? ((const float *)g.b[1])[at] : 0.f;
             }
             __syncthreads();
 #pragma unroll
@@ -81,19 +68,19 @@ __global__ __launch_bounds__(256) void k_dense_tile(DenseGemm g)
                 continue;
             float z[2];
             for (int q = 0; q < (GATED ? 2 : 1); ++q) {
-                z[q] = acc[q][i][j] + (g.bias[q] ? load_el(g.bias[q], n, g.dtype) : 0.f);
+                z[q] = acc[q][i][j] + (g.bias[q] ? ((const float *)g.bias[q])[n] : 0.f);
                 if (g.save[q])
-                    store_el(g.save[q], m * g.ldsave + n, z[q], g.dtype);
+                    ((float *)g.save[q])[m * g.ldsave + n] = z[q];
             }
-            void *out = g.out[half];
+            float *out = (float *)g.out[half];
             if (!out)
                 continue;
             float y = act_value(z[0], g.act);
             if (GATED)
                 y *= z[1];
             else if (g.res)
-                y += load_el(g.res, m * g.ldres + n, g.out_dtype);
-            store_el(out, m * g.ldout + n, y, g.out_dtype);
+                y += ((const float *)g.res)[m * g.ldres + n];
+            out[m * g.ldout + n] = y;
         }
 }
 
@@ -199,41 +186,67 @@ __global__ __launch_bounds__(256) void k_dense_colsum(const float *partial, int 
 
 namespace {
 
-struct Tile16 {
-    int bm, bn;
-    double cost;  // of one k-tile of one block, in units of a 256 x 256 tile's
+// A tile of the output and what it costs: `us` per k-tile of 64 with per_cu blocks
+// on every CU, `us1` with one (measured, K 4096); `fixed` per block for filling the
+// pipeline and the epilogue.
+struct TileCost {
+    int bm, bn, per_cu;
+    double us, us1, fixed;
 };
-const Tile16 kTiles16[] = {{256, 256, 1.0}, {128, 256, 0.55}, {128, 128, 0.30}, {64, 128, 0.19}};
+const TileCost kTiles16[] = {{256, 256, 1, 1.6, 1.6, 8.0}, {128, 256, 1, 0.92, 0.92, 6.0}, {128, 128, 2, 0.98, 0.6, 5.0}, {64, 128, 2, 0.7, 0.45, 4.0}};
+const TileCost kTiles32[] = {{128, 128, 1, 1.6, 1.6, 5.0}, {64, 64, 3, 1.5, 0.8, 4.0}};
+constexpr int kShortK = 32;
 
 bool aligned16(const void *p, int64_t ld, int dtype)
 {
     return (uintptr_t)p % 16 == 0 && ld * (int64_t)dense_esize(dtype) % 16 == 0;
 }
 
+// CUs of the current device, asked once per device.
+int cu_count(int *out)
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    ECF_HIP_CHECK(hipGetDevice(&dev));
+    const bool slot = dev >= 0 && dev < 64;
+    if (slot && (*out = known[dev].load(std::memory_order_relaxed)) > 0)
+        return ECF_OK;
+    ECF_HIP_CHECK(hipDeviceGetAttribute(out, hipDeviceAttributeMultiprocessorCount, dev));
+    if (slot)
+        known[dev].store(*out, std::memory_order_relaxed);
+    return ECF_OK;
+}
+
 constexpr int kMaxSplits = 16;
 
 // The tile and the splits of K with the least estimated time: rounds of blocks
 // over the CUs times the k-tiles each walks, plus the join of the splits.
-DensePlan plan16(const DenseGemm &g, int cus, bool may_split)
+DensePlan plan_gemm(const DenseGemm &g, int cus, bool may_split)
 {
-    DensePlan best{0, 1, true};
+    DensePlan best{0, 1, g.dtype != ECF_F32};
     for (int s = 0; s < g.ksegs || s < g.mhalves; ++s)
         best.dma = best.dma && aligned16(g.a[s], g.lda, g.dtype);
     for (int s = 0; s < (g.gated || g.ksegs == 2 ? 2 : 1); ++s)
         best.dma = best.dma && aligned16(g.b[s], g.ldb, g.dtype);
     best.dma = best.dma && (g.a_t ? g.M : g.K) % 8 == 0 && (g.b_t ? g.N : g.K) % 8 == 0;
+    const TileCost *tiles = g.dtype == ECF_F32 ? kTiles32 : kTiles16;
+    const int n_tiles = g.dtype == ECF_F32 ? 2 : 4;
     const int kt = (g.K + 63) / 64 * g.ksegs;
     const int64_t np = (g.N + 7) / 8 * 8, planes = g.gated ? 2 : g.mhalves;
     double least = 1e300;
-    for (int t = 0; t < 4; ++t) {
-        const int64_t tm = (g.M + kTiles16[t].bm - 1) / kTiles16[t].bm * g.mhalves;
-        const int64_t tn = (g.N + kTiles16[t].bn / (g.gated ? 2 : 1) - 1) / (kTiles16[t].bn / (g.gated ? 2 : 1));
+    for (int t = 0; t < n_tiles; ++t) {
+        const TileCost &c = tiles[t];
+        const int bn = c.bn / (g.gated ? 2 : 1);
+        const int64_t tiles_out = (int64_t)((g.M + c.bm - 1) / c.bm) * g.mhalves * ((g.N + bn - 1) / bn);
         for (int s = 1; s <= kMaxSplits; s *= 2) {
             const double part = (double)s * planes * g.M * np * 4;
-            if (s > 1 && (!may_split || kt / s < 4 || part > (double)kDensePartialBytes))
+            if (s > 1 && (!may_split || kt / s < 2 || part > (double)kDensePartialBytes))
                 break;
-            const double rounds = (double)((tm * tn * s + cus - 1) / cus);
-            const double us = rounds * (kTiles16[t].cost * ((kt + s - 1) / s) + 2.0) + (s > 1 ? 4.0 + part / 2e6 : 0.0);
+            // full rounds of per_cu blocks on every CU, then what is left
+            const int64_t blocks = tiles_out * s, round = (int64_t)cus * c.per_cu, rest = blocks % round;
+            const double tail = rest == 0 ? 0.0 : rest <= cus ? c.us1 : c.us;
+            const double walk = (double)((kt + s - 1) / s) * ((blocks / round) * c.us + tail);
+            const double us = walk + (double)((blocks + round - 1) / round) * c.fixed + (s > 1 ? 3.0 + part * 2 / 4e6 : 0.0);
             if (us < least) {
                 least = us;
                 best.tile = t;
@@ -246,46 +259,45 @@ DensePlan plan16(const DenseGemm &g, int cus, bool may_split)
 
 }  // namespace
 
-size_t dense_gemm_ws(int dtype, int64_t M, int64_t N, int planes)
+size_t dense_gemm_ws(int64_t M, int64_t N, int planes)
 {
-    if (dtype == ECF_F32)
-        return 0;
     const size_t all = (size_t)kMaxSplits * planes * M * ((N + 7) / 8 * 8) * 4;
     return std::min(all, kDensePartialBytes);
 }
 
-int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
+int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st)
 {
-    DenseGemm g = gin;
     ProfScope p(g.gated ? "dense_gated" : g.a_t ? "dense_gemm_tn" : g.b_t ? "dense_gemm_nn" : "dense_gemm_nt", st);
-    int dev = 0, cus = 0;
-    ECF_HIP_CHECK(hipGetDevice(&dev));
-    ECF_HIP_CHECK(hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev));
+    int cus = 0;
+    const int rc = cu_count(&cus);
+    if (rc != ECF_OK)
+        return rc;
     if (!g.a_t && !g.b_t && g.M <= kFewTokens)
         return launch_dense_few(g, cus, st);
-    if (g.dtype != ECF_F32) {
-        const DensePlan plan = plan16(g, cus, ws != nullptr);
-        const Tile16 &t = kTiles16[plan.tile];
-        const int bn = g.gated ? t.bn / 2 : t.bn;
-        DenseGrid gr{};
-        gr.half_tiles = (g.M + t.bm - 1) / t.bm;
-        gr.tiles_m = gr.half_tiles * g.mhalves;
-        gr.tiles_n = (g.N + bn - 1) / bn;
-        gr.splits = plan.splits;
-        gr.partial = (float *)ws;
-        gr.np = (g.N + 7) / 8 * 8;
-        return g.gated ? launch_gemm16_gated(g, plan, gr, st)
-               : g.a_t ? launch_gemm16_tn(g, plan, gr, st)
-               : g.b_t ? launch_gemm16_nn(g, plan, gr, st)
-                       : launch_gemm16_nt(g, plan, gr, st);
+    if (g.dtype == ECF_F32 && g.K < kShortK) {
+        const int tiles_n = (g.N + TN - 1) / TN;
+        const dim3 grid((unsigned)tiles_n * ((g.M + TM - 1) / TM) * g.mhalves);
+        if (g.gated)
+            hipLaunchKernelGGL(k_dense_short<true>, grid, dim3(256), 0, st, g, tiles_n);
+        else
+            hipLaunchKernelGGL(k_dense_short<false>, grid, dim3(256), 0, st, g, tiles_n);
+        ECF_HIP_CHECK(hipGetLastError());
+        return ECF_OK;
     }
-    const dim3 grid((g.N + TN - 1) / TN, (g.M + TM - 1) / TM * g.mhalves);
-    if (g.gated)
-        hipLaunchKernelGGL(k_dense_tile<true>, grid, dim3(256), 0, st, g);
-    else
-        hipLaunchKernelGGL(k_dense_tile<false>, grid, dim3(256), 0, st, g);
-    ECF_HIP_CHECK(hipGetLastError());
-    return ECF_OK;
+    const DensePlan plan = plan_gemm(g, cus, ws != nullptr);
+    const TileCost &t = (g.dtype == ECF_F32 ? kTiles32 : kTiles16)[plan.tile];
+    const int bn = g.gated ? t.bn / 2 : t.bn;
+    DenseGrid gr{};
+    gr.half_tiles = (g.M + t.bm - 1) / t.bm;
+    gr.tiles_m = gr.half_tiles * g.mhalves;
+    gr.tiles_n = (g.N + bn - 1) / bn;
+    gr.splits = plan.splits;
+    gr.partial = (float *)ws;
+    gr.np = (g.N + 7) / 8 * 8;
+    return g.gated ? launch_gemm_gated(g, plan, gr, st)
+           : g.a_t ? launch_gemm_tn(g, plan, gr, st)
+           : g.b_t ? launch_gemm_nn(g, plan, gr, st)
+                   : launch_gemm_nt(g, plan, gr, st);
 }
 
 int dense_grad_row_blocks(int T) { return (T + kGradRows - 1) / kGradRows; }
