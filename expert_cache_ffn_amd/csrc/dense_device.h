@@ -27,7 +27,7 @@ struct F16 {
     static __device__ __forceinline__ raw from_f(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 };
 
-// v shifted down by s 16-bit elements (0..7; v is 0 where s is more), zeros from above
+// v moved down by s 16-bit elements (0..7), zeros from above
 __device__ __forceinline__ u32x4_t shift_down16(u32x4_t v, int s)
 {
     if (s & 4)

@@ -8,7 +8,8 @@
 //            (buffer_load ... lds), no operand passes through a register; a ring
 //            of NS stages keeps NS - 1 k-tiles in flight ahead of the MFMAs
 //   register any alignment and any width: 16-byte loads at element alignment
-//            into registers, two k-tiles ahead; LDS stores one k-tile ahead
+//            into registers, NSTAGE sets of them in flight ahead; LDS stores
+//            between the MFMAs of the k-tile before
 // Past the last row the last row is read again (its results are not stored);
 // past the last k both operands are zeros.
 //
@@ -22,13 +23,13 @@
 // products read dz, W and x as they are, without a transposing pass.
 //
 // fp32 operands are split on their way to LDS into three bf16 parts, x = h + m + l
-// exactly (8 bits of the significand each, rounded to nearest), and six products
-// make one: hh' + hm' + mh' + hl' + lh' + mm'.  What is left out is below 2^-26 of
-// |x x'|, less than the rounding of an fp32 product.  Six bf16 MFMAs of 16 k take
-// 192 cycles of the matrix pipe, the eight fp32 ones they replace 512.  An
-// infinity or NaN goes into l alone, which meets only h' and so gives what it
-// should (infinity times infinity gives NaN); parts under bf16's subnormal step
-// are lost: 2^-134 |x'| per product.
+// exactly (h: the upper 8 bits of the significand; m: the rest rounded to 8; l: what
+// is left), and six products make one: hh' + hm' + mh' + hl' + lh' + mm'.  What is
+// left out, ml' + lm' + ll', is below 2^-22 |x x'| and of either sign, as the
+// rounding of an fp32 sum of a few terms is.  Six bf16 MFMAs of 16 k take 192 cycles
+// of the matrix pipe, the eight fp32 ones they replace 512.  An infinity or NaN goes
+// into l alone, which meets only h' and so gives what it should (but infinity times
+// infinity gives NaN); parts below bf16's subnormals are lost, 2^-134 |x'| per product.
 //
 // Output goes out by rows through LDS, 8 columns per lane: bias, activation,
 // residual and the gated product are applied there to the fp32 sums, and loads
@@ -207,66 +208,47 @@ __device__ __forceinline__ int kswz(int k)
     return ROWS >= 128 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
 }
 
-// Two fp32 values to their three bf16 parts, packed: exact for finite values.
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t &h, uint32_t &m, uint32_t &l)
+// 8 fp32 values to three chunks of bf16 parts.  `odd` becomes NaN if one of the
+// values is infinite or NaN; their k-tile is stored again through split8_odd.
+__device__ __forceinline__ void split8(const u32x4_t v[2], u32x4_t part[3], float &odd)
 {
-    auto pack = [](float a, float b) {
-        const bf16x2_t v = {(__bf16)a, (__bf16)b};
-        return __builtin_bit_cast(uint32_t, v);
-    };
-    h = pack(x0, x1);
-    const float r0 = x0 - bf_lo(h), r1 = x1 - bf_hi(h);
-    m = pack(r0, r1);
-    l = pack(r0 - bf_lo(m), r1 - bf_hi(m));
-}
-
-// 8 fp32 values to three chunks of bf16 parts.  Values at or above the largest that
-// rounds to a finite bf16 take the slow way: there h is cut off instead of rounded,
-// and infinities and NaN go into l.
-__device__ __forceinline__ void split8(const u32x4_t v[2], u32x4_t part[3])
-{
-    constexpr uint32_t kBig = 0x7f7f8000u;
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        top = max(top, v[j >> 2][j & 3] & 0x7fffffffu);
-    if (top < kBig) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t h, m, l;
-            split2(__uint_as_float(v[j >> 1][2 * (j & 1)]), __uint_as_float(v[j >> 1][2 * (j & 1) + 1]), h, m, l);
-            part[0][j] = h, part[1][j] = m, part[2][j] = l;
-        }
-        return;
-    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        uint32_t w[3] = {0, 0, 0};
+        const uint32_t u0 = v[j >> 1][2 * (j & 1)], u1 = v[j >> 1][2 * (j & 1) + 1];
+        const float x0 = __uint_as_float(u0), x1 = __uint_as_float(u1);
+        odd = __builtin_fmaf(x0, 0.f, odd);
+        odd = __builtin_fmaf(x1, 0.f, odd);
+        part[0][j] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);  // the upper halves
+        const float r0 = x0 - __uint_as_float(u0 & 0xffff0000u), r1 = x1 - __uint_as_float(u1 & 0xffff0000u);
+        const bf16x2_t m = {(__bf16)r0, (__bf16)r1};
+        const uint32_t mw = __builtin_bit_cast(uint32_t, m);
+        part[1][j] = mw;
+        // at most 8 bits are left: their upper half is all of them
+        part[2][j] = __builtin_amdgcn_perm(__float_as_uint(r1 - bf_hi(mw)), __float_as_uint(r0 - bf_lo(mw)), 0x07060302u);
+    }
+}
+
+__device__ __forceinline__ void split8_odd(const u32x4_t v[2], u32x4_t part[3])
+{
+    float odd = 0.f;
+    split8(v, part, odd);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t u = v[j >> 1][2 * (j & 1) + e], mag = u & 0x7fffffffu;
-            const float x = __uint_as_float(u);
-            uint32_t h, m, l;
-            split2(x, 0.f, h, m, l);
-            if (mag >= 0x7f800000u) {
-                h = m = 0;
-                l = f_to_bf(x);
-            } else if (mag >= kBig) {
-                h = u >> 16;
-                const float r = x - bf_to_f((uint16_t)h);
-                m = f_to_bf(r);
-                l = f_to_bf(r - bf_to_f((uint16_t)m));
-            }
-            w[0] |= (h & 0xffffu) << (16 * e), w[1] |= (m & 0xffffu) << (16 * e), w[2] |= (l & 0xffffu) << (16 * e);
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t u = v[j >> 2][j & 3];
+        if ((u & 0x7f800000u) == 0x7f800000u) {
+            const uint32_t keep = j & 1 ? 0x0000ffffu : 0xffff0000u;
+            const uint32_t top = (u & 0x7fffffu) ? u | 0x400000u : u;  // a NaN stays one in 16 bits
+            part[0][j >> 1] &= keep;
+            part[1][j >> 1] &= keep;
+            part[2][j >> 1] = (part[2][j >> 1] & keep) | (j & 1 ? top & 0xffff0000u : top >> 16);
         }
-        part[0][j] = w[0], part[1][j] = w[1], part[2][j] = w[2];
     }
 }
 
 // One operand's tile of ROWS rows (m or n) x BK k.  T: m-contiguous in memory.
 // ES: bytes per element in memory; fp32 tiles (register path) lie in LDS as three
 // planes of bf16 parts.
-template <bool T, bool DMA, int ROWS, int NTH, int BK, int ES>
+template <bool T, bool DMA, int ROWS, int NTH, int BK, int ES, int SETS>
 struct Tile {
     static_assert(ES == 2 || !DMA, "fp32 is split on its way to LDS");
     static constexpr int W = ES / 2;  // 16-byte registers per chunk of 8 elements
@@ -280,17 +262,25 @@ struct Tile {
     uint32_t off[NL];  // byte offsets of this thread's chunks from the k-tile's base
     int row, chunk;    // the first of this thread's LDS rows, and its chunk in all of them
     int valid;         // T: elements of the chunk that exist (up to 8, none if <= 0)
-    int width;         // elements in a row of the operand: those before a row's last chunk may be read
-    int shift;         // register path: elements by which the loaded chunks are to move down
-    u32x4_t reg[DMA ? 1 : NL][W];
+    // register path: the chunks of SETS k-tiles and the k each had left.  No load sits
+    // behind a branch (at the branch's end the compiler would wait for it): a lane
+    // with nothing to load reads `safe`, the operand's first 8 elements, and store()
+    // puts zeros.  A chunk that the operand's edge cuts is loaded as the 8 elements
+    // that end at the edge, and store() moves them down; the launcher sends operands
+    // with rows of under 8 elements elsewhere.
+    const char *safe;
+    bool inside;  // T: every row of the tile exists
+    int kl[SETS];
+    u32x4_t reg[SETS][DMA ? 1 : NL][W];
 
     // `rows` rows from the tile's first on, row stride ld (elements); rowmap turns a
     // tile row into a row relative to the base (clamped to the last one)
     template <class F>
-    __device__ __forceinline__ void init(int tid, int rows, int width_, int64_t ld, F rowmap)
+    __device__ __forceinline__ void init(int tid, int rows, const void *first, int64_t ld, F rowmap)
     {
         row = tid / CPR;
-        width = width_;
+        safe = (const char *)first;
+        inside = rows >= ROWS;
         if constexpr (!T) {
             chunk = (tid % CPR) ^ rswz<BK>(row);
             valid = 8;
@@ -320,83 +310,84 @@ struct Tile {
         dma16(PAIR && second(q, wave) ? rs2 : rs, in ? off[q] : kNowhere, lds + (q * NTH + 64 * wave) * 16);
     }
 
-    // register path: the whole k-tile
-    template <bool PAIR>
+    // register path: a whole k-tile into set S
+    template <bool PAIR, int S>
     __device__ __forceinline__ void load(const void *base, const void *base2, int kleft, int wave)
     {
-        if constexpr (!DMA) {
-            const int n = T ? valid : kleft - chunk * 8;
-            shift = max(0, 8 - n);
-            if (n >= 8 && (!T || kleft >= BK)) {
+        const int n = T ? valid : kleft - chunk * 8;
+        const uint32_t back = n < 8 ? (uint32_t)(8 - n) * ES : 0u;
+        kl[S] = kleft;
 #pragma unroll
-                for (int q = 0; q < NL; ++q)
-                    take(q, (const char *)(PAIR && second(q, wave) ? base2 : base) + off[q]);
+        for (int q = 0; q < NL; ++q) {
+            const bool in = n > 0 && (!T || row + STEP * q < kleft);
+            const char *p = (const char *)(PAIR && second(q, wave) ? base2 : base) + off[q] - back;
+            p = in ? p : safe;
+            if constexpr (ES == 2) {
+                reg[S][q][0] = ((const any128x2 *)p)->v;
             } else {
-                // a chunk that the operand's edge cuts: its 8 elements that end at the
-                // edge, which store() shifts down (rows of under 8 elements: one by one)
-#pragma unroll
-                for (int q = 0; q < NL; ++q) {
-                    const char *p = (const char *)(PAIR && second(q, wave) ? base2 : base) + off[q];
-#pragma unroll
-                    for (int w = 0; w < W; ++w)
-                        reg[q][w] = u32x4_t{0, 0, 0, 0};
-                    if (n <= 0 || (T && row + STEP * q >= kleft))
-                        continue;
-                    if (width >= 8) {
-                        take(q, p - shift * ES);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (j < n) {
-                                if constexpr (ES == 2)
-                                    reg[q][0][j >> 1] |= (uint32_t)((const uint16_t *)p)[j] << (16 * (j & 1));
-                                else
-                                    reg[q][j >> 2][j & 3] = ((const uint32_t *)p)[j];
-                            }
-                    }
-                }
-                if (width < 8)
-                    shift = 0;
+                reg[S][q][0] = __builtin_bit_cast(u32x4_t, ((const any128x4 *)p)->v);
+                reg[S][q][1] = __builtin_bit_cast(u32x4_t, ((const any128x4 *)(p + 16))->v);
             }
         }
     }
 
-    __device__ __forceinline__ void take(int q, const char *p)
+    // does the k-tile in set S reach over the operand's edge?
+    template <int S>
+    __device__ __forceinline__ bool edge() const
     {
+        return kl[S] < BK || (T && !inside);
+    }
+
+    // register path: chunk q of set S to its stage, as if nothing were cut or odd (see split8)
+    template <int S>
+    __device__ __forceinline__ void store(int q, char *stage, int tid, float &odd) const
+    {
+        u32x4_t *at = (u32x4_t *)stage + q * NTH + tid;
         if constexpr (ES == 2) {
-            reg[q][0] = ((const any128x2 *)p)->v;
+            *at = reg[S][q][0];
         } else {
-            reg[q][0] = __builtin_bit_cast(u32x4_t, ((const any128x4 *)p)->v);
-            reg[q][1] = __builtin_bit_cast(u32x4_t, ((const any128x4 *)(p + 16))->v);
+            u32x4_t part[3];
+            split8(reg[S][q], part, odd);
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                at[p * (ROWS * BK / 8)] = part[p];
         }
     }
 
-    // register path: the loaded k-tile to its stage
-    __device__ __forceinline__ void store(char *stage, int tid)
+    // The whole k-tile again: cut chunks moved down, zeros past the edge, and
+    // infinities and NaNs where they belong.  Apart from store(), so that store() is
+    // straight code between MFMAs.
+    template <int S>
+    __device__ __forceinline__ void store_again(char *stage, int tid) const
     {
-        if (shift) {
 #pragma unroll
-            for (int q = 0; q < NL; ++q) {
+        for (int q = 0; q < NL; ++q) {
+            u32x4_t v[W];
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                v[w] = reg[S][q][w];
+            const int n = T ? (row + STEP * q < kl[S] ? valid : 0) : kl[S] - chunk * 8, s = min(8, max(0, 8 - n));
+            if (s & 7) {
                 if constexpr (ES == 2) {
-                    reg[q][0] = shift_down16(reg[q][0], shift);
+                    v[0] = shift_down16(v[0], s & 7);
                 } else {
 #pragma unroll
                     for (int b = 4; b >= 1; b >>= 1)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            if (shift & b)
-                                reg[q][j >> 2][j & 3] = j + b < 8 ? reg[q][(j + b) >> 2][(j + b) & 3] : 0u;
+                            if (s & b)
+                                v[j >> 2][j & 3] = j + b < 8 ? v[(j + b) >> 2][(j + b) & 3] : 0u;
                 }
             }
-        }
 #pragma unroll
-        for (int q = 0; q < NL; ++q) {
+            for (int w = 0; w < W; ++w)
+                v[w] = s >= 8 ? u32x4_t{0, 0, 0, 0} : v[w];
             u32x4_t *at = (u32x4_t *)stage + q * NTH + tid;
             if constexpr (ES == 2) {
-                *at = reg[q][0];
+                *at = v[0];
             } else {
                 u32x4_t part[3];
-                split8(reg[q], part);
+                split8_odd(v, part);
 #pragma unroll
                 for (int p = 0; p < 3; ++p)
                     at[p * (ROWS * BK / 8)] = part[p];
@@ -457,8 +448,9 @@ __global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 
     using namespace gemm;
     constexpr int NW = WM * WN, NTH = 64 * NW, RM = BM / WM, RN = BN / WN, FM = RM / 32, FN = RN / 32;
     static_assert(BK % 32 == 0, "two sets of fragments take turns");
+    static_assert(DMA || NSTAGE <= 2, "one or two register sets");
     static_assert(FM >= 1 && FN >= 1 && (!GATED || (FN % 2 == 0 && !BT)), "wave tile");
-    constexpr int NS = DMA ? NSTAGE : 2;
+    constexpr int NS = DMA ? NSTAGE : 2, SETS = DMA ? 1 : NSTAGE;
     constexpr int ES = sizeof(typename E::raw), NP = ES == 4 ? 3 : 1;      // planes of parts
     constexpr int PA = BM * BK * 2, PB = BN * BK * 2, SA = PA * NP, SB = PB * NP;  // bytes per plane and stage
     constexpr int PITCH = (FN >= 2 ? 64 : 32) + 4;  // fp32 per row of the output staging
@@ -472,12 +464,12 @@ __global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 
     const int m0 = mt * BM, n0 = nt * (GATED ? BN / 2 : BN);
     const int mrows = min(BM, g.M - m0);
 
-    Tile<AT, DMA, BM, NTH, BK, ES> ta;
-    Tile<BT, DMA, BN, NTH, BK, ES> tb;
+    Tile<AT, DMA, BM, NTH, BK, ES, SETS> ta;
+    Tile<BT, DMA, BN, NTH, BK, ES, SETS> tb;
     const int nrows = GATED ? 0 : g.N - n0, nlast = g.N - 1 - n0;
-    ta.init(tid, g.M - m0, AT ? g.M : g.K, g.lda, [&](int r) { return (int64_t)min(r, mrows - 1); });
+    ta.init(tid, g.M - m0, g.a[0], g.lda, [&](int r) { return (int64_t)min(r, mrows - 1); });
     // gated: 64 tile rows are 32 of the gate projection, then the same 32 of the up projection
-    tb.init(tid, nrows, BT ? g.N : g.K, g.ldb,
+    tb.init(tid, nrows, g.b[0], g.ldb,
             [&](int r) { return (int64_t)min(GATED ? (r >> 6) * 32 + (r & 31) : r, nlast); });
     Frag<AT, BM, FM, BK> fa;
     Frag<BT, BN, FN, BK> fb;
@@ -527,16 +519,30 @@ __global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 
         else
             tb.template issue<GATED>(rsrc_of(s.b), rsrc_of(GATED ? s.b2 : s.b), q - NLA, s.kleft, to + SA, wave);
     };
-    auto load_reg = [&](int kt) __attribute__((always_inline)) {
+    // register path: k-tile kt into set S, and piece q of set S to `stage`
+    auto load_reg = [&](int kt, auto set) __attribute__((always_inline)) {
+        constexpr int S = decltype(set)::value;
         const Src s = source(kt);
-        ta.template load<false>(s.a, s.a, s.kleft, wave);
-        tb.template load<GATED>(s.b, s.b2, s.kleft, wave);
+        ta.template load<false, S>(s.a, s.a, s.kleft, wave);
+        tb.template load<GATED, S>(s.b, s.b2, s.kleft, wave);
         // issue the loads here, ahead of the MFMAs they travel under
         asm volatile("" ::: "memory");
     };
-    auto put = [&](int stage) __attribute__((always_inline)) {
-        ta.store(lds + stage * (SA + SB), tid);
-        tb.store(lds + stage * (SA + SB) + SA, tid);
+    float odd = 0.f;
+    auto put = [&](int q, int stage, auto set) __attribute__((always_inline)) {
+        constexpr int S = decltype(set)::value;
+        if (q < NLA)
+            ta.template store<S>(q, lds + stage * (SA + SB), tid, odd);
+        else
+            tb.template store<S>(q - NLA, lds + stage * (SA + SB) + SA, tid, odd);
+    };
+    auto put_again = [&](int stage, auto set) __attribute__((always_inline)) {
+        constexpr int S = decltype(set)::value;
+        if (ta.template edge<S>() || tb.template edge<S>() || (NP == 3 && odd != odd)) {
+            ta.template store_again<S>(lds + stage * (SA + SB), tid);
+            tb.template store_again<S>(lds + stage * (SA + SB) + SA, tid);
+            odd = 0.f;
+        }
     };
     // Two sets of fragments: step ks + 1 (or the next k-tile's step 0) is read under
     // the MFMAs of step ks.
@@ -558,21 +564,16 @@ __global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 
     };
     // The MFMAs of the fragments in `set`.  Before MFMA i: fragments of step ks of
     // `stage` into the other set, spread over the MFMAs so that they have the rest of
-    // the step to arrive, and (LOADS) global loads.  The scheduling barriers keep
+    // the step to arrive, and extra(i) (global loads, or LDS stores).  The scheduling barriers keep
     // this order: left alone, the compiler moves the reads behind the last MFMAs.
     constexpr int MF = FM * FN;
-    auto step = [&](int set, int stage, int ks, auto loads, const Src &s, int into) __attribute__((always_inline)) {
-        constexpr bool LOADS = decltype(loads)::value;
+    auto step = [&](int set, int stage, int ks, auto extra) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < MF; ++i) {
 #pragma unroll
             for (int f = i * (FM + FN) / MF; f < (i + 1) * (FM + FN) / MF; ++f)
                 fetch(stage, ks, set ^ 1, f);
-            if constexpr (LOADS) {
-#pragma unroll
-                for (int q = i * NLD / MF; q < (i + 1) * NLD / MF; ++q)
-                    issue(s, into, q);
-            }
+            extra(i);
             const u32x4_t *a = av[set][i / FN], *b = bv[set][i % FN];
             f32x16_t &c = acc[i / FN][i % FN];
             if constexpr (NP == 3) {  // the small products first
@@ -605,30 +606,53 @@ __global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 
                 const Src s = source(kt + NS);
 #pragma unroll
                 for (int ks = 0; ks < NK - 1; ++ks)
-                    step(ks & 1, stage, ks + 1, std::false_type{}, s, 0);
+                    step(ks & 1, stage, ks + 1, [](int) {});
                 const int next = stage + 1 == NS ? 0 : stage + 1;
                 stage_ready<(NS - 2) * NLD>();
-                step((NK - 1) & 1, next, 0, std::true_type{}, s, stage);
+                step((NK - 1) & 1, next, 0, [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int q = i * NLD / MF; q < (i + 1) * NLD / MF; ++q)
+                        issue(s, stage, q);
+                });
                 stage = next;
             }
             stage_ready<0>();
         } else {
-            load_reg(kb);
-            put(0);
-            load_reg(kb + 1);
+            // k-tile kb + i goes through register set i % SETS into stage i % 2: loaded
+            // while k-tile i - 1 - SETS is multiplied, stored while i - 1 is
+            load_reg(kb, std::integral_constant<int, 0>{});
+#pragma unroll
+            for (int q = 0; q < NLD; ++q)
+                put(q, 0, std::integral_constant<int, 0>{});
+            put_again(0, std::integral_constant<int, 0>{});
+            load_reg(kb + 1, std::integral_constant<int, 1 % SETS>{});
+            if constexpr (SETS == 2)
+                load_reg(kb + 2, std::integral_constant<int, 0>{});
             stage_ready<63>();
             fetch_all(0);
             int stage = 0;
-            const Src s{};
-            for (int kt = kb; kt < ke; ++kt) {
-                put(stage ^ 1);
-                load_reg(kt + 2);
+            // k-tile kt; the next one waits in register set S
+            auto tile = [&](int kt, auto set) __attribute__((always_inline)) {
+                constexpr int PIECES = MF * (NK - 1);
 #pragma unroll
                 for (int ks = 0; ks < NK - 1; ++ks)
-                    step(ks & 1, stage, ks + 1, std::false_type{}, s, 0);
+                    step(ks & 1, stage, ks + 1, [&](int i) __attribute__((always_inline)) {
+                        const int at = ks * MF + i;
+#pragma unroll
+                        for (int q = at * NLD / PIECES; q < (at + 1) * NLD / PIECES; ++q)
+                            put(q, stage ^ 1, set);
+                    });
+                put_again(stage ^ 1, set);
+                load_reg(kt + 1 + SETS, set);
                 stage_ready<63>();
                 stage ^= 1;
-                step((NK - 1) & 1, stage, 0, std::false_type{}, s, 0);
+                step((NK - 1) & 1, stage, 0, [](int) {});
+            };
+            for (int kt = kb; kt < ke; kt += SETS) {
+                tile(kt, std::integral_constant<int, 1 % SETS>{});
+                if constexpr (SETS == 2)
+                    if (kt + 1 < ke)
+                        tile(kt + 1, std::integral_constant<int, 0>{});
             }
             stage_ready<63>();
         }

@@ -16,15 +16,15 @@ template <class E, bool AT, bool BT, bool GATED, bool DMA>
 int pick_gemm(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st)
 {
     if constexpr (std::is_same<E, F32>::value) {
-        if (p.tile == 0)  // the order of kTiles32
-            launch_gemm<E, AT, BT, GATED, false, 128, 128, 4, 2, 32, 2>(g, gr, st);
+        if (p.tile == 0)  // the order of the launcher's tables
+            launch_gemm<E, AT, BT, GATED, false, 128, 128, 4, 2, 32, 1>(g, gr, st);
         else
-            launch_gemm<E, AT, BT, GATED, false, 64, 64, 2, 1, 32, 2>(g, gr, st);
-    } else switch (p.tile) {  // the order of kTiles16
-    case 0: launch_gemm<E, AT, BT, GATED, DMA, 256, 256, 2, 4, 64, 2>(g, gr, st); break;
-    case 1: launch_gemm<E, AT, BT, GATED, DMA, 128, 256, 2, 4, 64, 3>(g, gr, st); break;
-    case 2: launch_gemm<E, AT, BT, GATED, DMA, 128, 128, 2, 2, 64, 2>(g, gr, st); break;
-    default: launch_gemm<E, AT, BT, GATED, DMA, 64, 128, 2, 2, 64, 3>(g, gr, st); break;
+            launch_gemm<E, AT, BT, GATED, false, 64, 128, 2, 2, 32, 2>(g, gr, st);
+    } else switch (p.tile) {  // the order of the launcher's tables
+    case 0: launch_gemm<E, AT, BT, GATED, DMA, 256, 256, 2, 4, 64, DMA ? 2 : 1>(g, gr, st); break;
+    case 1: launch_gemm<E, AT, BT, GATED, DMA, 128, 256, 2, 4, 64, DMA ? 3 : 2>(g, gr, st); break;
+    case 2: launch_gemm<E, AT, BT, GATED, DMA, 128, 128, 2, 2, 64, DMA ? 2 : 1>(g, gr, st); break;
+    default: launch_gemm<E, AT, BT, GATED, DMA, 64, 128, 2, 2, 64, DMA ? 3 : 2>(g, gr, st); break;
     }
     if (gr.splits > 1) {
         const int64_t n = gr.np / 8 * g.M * g.mhalves;

@@ -1,5 +1,5 @@
-// Dense feed-forward operators: the choice of a product's kernel, the products of
-// fp32 operands with a short reduction, and the elementwise half of the backward passes.
+// Dense feed-forward operators: the choice of a product's kernel, the products with
+// short rows, and the elementwise half of the backward passes.
 #include <algorithm>
 #include <atomic>
 
@@ -16,14 +16,16 @@ __device__ __forceinline__ void store_el(void *p, int64_t i, float v, int dtype)
         ((uint16_t *)p)[i] = dtype == ECF_BF16 ? BF16::from_f(v) : F16::from_f(v);
 }
 
-// fp32 products over few k (under kShortK) with fp32 FMAs: a block owns a 64 x 64
-// tile of the output, stages 16 k of both operands in LDS and each of its 256
-// threads sums a 4 x 4 patch (two, gated).  grid: x over N, y over M of both halves.
+// Products whose operands have rows of under 8 elements, which the MFMA tiles'
+// 16-byte chunks do not take, and fp32 products over under kShortK k, with fp32
+// FMAs: a block owns a 64 x 64 tile of the output, stages 16 k of both operands in
+// LDS as fp32 and each of its 256 threads sums a 4 x 4 patch (two, gated).
 constexpr int TM = 64, TN = 64, TK = 16;
 
-template <bool GATED>
+template <class E, bool GATED>
 __global__ __launch_bounds__(256) void k_dense_short(DenseGemm g, int tiles_n)
 {
+    typedef typename E::raw R;
     __shared__ float As[TK][TM + 1], Bs[GATED ? 2 : 1][TK][TN + 1];
     const int mt = (g.M + TM - 1) / TM, ty0 = (int)blockIdx.x / tiles_n;
     const int half = ty0 / mt;
@@ -31,21 +33,21 @@ __global__ __launch_bounds__(256) void k_dense_short(DenseGemm g, int tiles_n)
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     float acc[GATED ? 2 : 1][4][4] = {};
     for (int s = 0; s < g.ksegs; ++s) {
-        const float *pa = (const float *)g.a[g.mhalves == 2 ? half : s];
+        const R *pa = (const R *)g.a[g.mhalves == 2 ? half : s];
         for (int k0 = 0; k0 < g.K; k0 += TK) {
             for (int i = tid; i < TM * TK; i += 256) {
                 const int m = g.a_t ? i % TM : i / TK, k = g.a_t ? i / TM : i % TK;
                 const int64_t gm = m0 + m, gk = k0 + k;
-                As[k][m] = gm < g.M && gk < g.K ? pa[g.a_t ? gk * g.lda + gm : gm * g.lda + gk] : 0.f;
+                As[k][m] = gm < g.M && gk < g.K ? E::to_f(pa[g.a_t ? gk * g.lda + gm : gm * g.lda + gk]) : 0.f;
             }
             for (int i = tid; i < TN * TK; i += 256) {
                 const int n = g.b_t ? i % TN : i / TK, k = g.b_t ? i / TN : i % TK;
                 const int64_t gn = n0 + n, gk = k0 + k;
                 const bool in = gn < g.N && gk < g.K;
                 const int64_t at = g.b_t ? gk * g.ldb + gn : gn * g.ldb + gk;
-                Bs[0][k][n] = in ? ((const float *)g.b[GATED ? 0 : s])[at] : 0.f;
+                Bs[0][k][n] = in ? E::to_f(((const R *)g.b[GATED ? 0 : s])[at]) : 0.f;
                 if (GATED)
-                    Bs[GATED][k][n] = in ? ((const float *)g.b[1])[at] : 0.f;
+                    Bs[GATED][k][n] = in ? E::to_f(((const R *)g.b[1])[at]) : 0.f;
             }
             __syncthreads();
 #pragma unroll
@@ -68,19 +70,20 @@ __global__ __launch_bounds__(256) void k_dense_short(DenseGemm g, int tiles_n)
                 continue;
             float z[2];
             for (int q = 0; q < (GATED ? 2 : 1); ++q) {
-                z[q] = acc[q][i][j] + (g.bias[q] ? ((const float *)g.bias[q])[n] : 0.f);
+                z[q] = acc[q][i][j] + (g.bias[q] ? E::to_f(((const R *)g.bias[q])[n]) : 0.f);
                 if (g.save[q])
-                    ((float *)g.save[q])[m * g.ldsave + n] = z[q];
+                    ((R *)g.save[q])[m * g.ldsave + n] = E::from_f(z[q]);
             }
-            float *out = (float *)g.out[half];
+            void *out = g.out[half];
             if (!out)
                 continue;
             float y = act_value(z[0], g.act);
             if (GATED)
                 y *= z[1];
             else if (g.res)
-                y += ((const float *)g.res)[m * g.ldres + n];
-            out[m * g.ldout + n] = y;
+                y += g.out_dtype == ECF_F32 ? ((const float *)g.res)[m * g.ldres + n]
+                                            : E::to_f(((const R *)g.res)[m * g.ldres + n]);
+            store_el(out, m * g.ldout + n, y, g.out_dtype);
         }
 }
 
@@ -193,9 +196,14 @@ struct TileCost {
     int bm, bn, per_cu;
     double us, us1, fixed;
 };
-const TileCost kTiles16[] = {{256, 256, 1, 1.6, 1.6, 8.0}, {128, 256, 1, 0.92, 0.92, 6.0}, {128, 128, 2, 0.98, 0.6, 5.0}, {64, 128, 2, 0.7, 0.45, 4.0}};
-const TileCost kTiles32[] = {{128, 128, 1, 1.6, 1.6, 5.0}, {64, 64, 3, 1.5, 0.8, 4.0}};
+const TileCost kTilesDma[] = {{256, 256, 1, 1.78, 1.78, 8.0}, {128, 256, 1, 0.98, 0.98, 6.0},
+                              {128, 128, 2, 1.05, 0.68, 5.0}, {64, 128, 2, 0.64, 0.40, 4.0}};
+const TileCost kTilesReg[] = {{256, 256, 1, 1.92, 1.92, 8.0}, {128, 256, 1, 1.14, 1.14, 6.0},
+                              {128, 128, 2, 1.24, 0.85, 5.0}, {64, 128, 2, 0.83, 0.70, 4.0}};
+const TileCost kTilesF32[] = {{128, 128, 1, 2.85, 2.85, 5.0}, {64, 128, 2, 3.30, 1.95, 4.0}};
 constexpr int kShortK = 32;
+
+const TileCost *tiles_of(int dtype, bool dma) { return dtype == ECF_F32 ? kTilesF32 : dma ? kTilesDma : kTilesReg; }
 
 bool aligned16(const void *p, int64_t ld, int dtype)
 {
@@ -229,8 +237,8 @@ DensePlan plan_gemm(const DenseGemm &g, int cus, bool may_split)
     for (int s = 0; s < (g.gated || g.ksegs == 2 ? 2 : 1); ++s)
         best.dma = best.dma && aligned16(g.b[s], g.ldb, g.dtype);
     best.dma = best.dma && (g.a_t ? g.M : g.K) % 8 == 0 && (g.b_t ? g.N : g.K) % 8 == 0;
-    const TileCost *tiles = g.dtype == ECF_F32 ? kTiles32 : kTiles16;
     const int n_tiles = g.dtype == ECF_F32 ? 2 : 4;
+    const TileCost *tiles = tiles_of(g.dtype, best.dma);
     const int kt = (g.K + 63) / 64 * g.ksegs;
     const int64_t np = (g.N + 7) / 8 * 8, planes = g.gated ? 2 : g.mhalves;
     double least = 1e300;
@@ -274,18 +282,27 @@ int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st)
         return rc;
     if (!g.a_t && !g.b_t && g.M <= kFewTokens)
         return launch_dense_few(g, cus, st);
-    if (g.dtype == ECF_F32 && g.K < kShortK) {
+    if ((g.a_t ? g.M : g.K) < 8 || (g.b_t ? g.N : g.K) < 8 || (g.dtype == ECF_F32 && g.K < kShortK)) {
         const int tiles_n = (g.N + TN - 1) / TN;
         const dim3 grid((unsigned)tiles_n * ((g.M + TM - 1) / TM) * g.mhalves);
-        if (g.gated)
-            hipLaunchKernelGGL(k_dense_short<true>, grid, dim3(256), 0, st, g, tiles_n);
+        auto go = [&](auto e) {
+            using E = decltype(e);
+            if (g.gated)
+                hipLaunchKernelGGL((k_dense_short<E, true>), grid, dim3(256), 0, st, g, tiles_n);
+            else
+                hipLaunchKernelGGL((k_dense_short<E, false>), grid, dim3(256), 0, st, g, tiles_n);
+        };
+        if (g.dtype == ECF_F32)
+            go(F32{});
+        else if (g.dtype == ECF_BF16)
+            go(BF16{});
         else
-            hipLaunchKernelGGL(k_dense_short<false>, grid, dim3(256), 0, st, g, tiles_n);
+            go(F16{});
         ECF_HIP_CHECK(hipGetLastError());
         return ECF_OK;
     }
     const DensePlan plan = plan_gemm(g, cus, ws != nullptr);
-    const TileCost &t = (g.dtype == ECF_F32 ? kTiles32 : kTiles16)[plan.tile];
+    const TileCost &t = tiles_of(g.dtype, plan.dma)[plan.tile];
     const int bn = g.gated ? t.bn / 2 : t.bn;
     DenseGrid gr{};
     gr.half_tiles = (g.M + t.bm - 1) / t.bm;
