@@ -107,7 +107,7 @@ BackWs back_ws(int64_t in, int64_t cols, int halves, int dtype, int32_t T)
     BackWs w;
     w.pitch = halves * ((cols + 7) / 8 * 8);
     w.colsum = al256((size_t)T * w.pitch * dense_esize(dtype));
-    w.split = w.colsum + al256((size_t)dense_grad_row_blocks(T) * halves * cols * 4);
+    w.split = w.colsum + al256((size_t)dense_grad_max_row_blocks(T) * halves * cols * 4);
     w.total = w.split + std::max(dense_gemm_ws(T, in, 1), dense_gemm_ws(cols, in, halves));
     return w;
 }

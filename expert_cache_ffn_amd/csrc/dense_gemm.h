@@ -264,10 +264,12 @@ struct Tile {
     int valid;         // T: elements of the chunk that exist (up to 8, none if <= 0)
     // register path: the chunks of SETS k-tiles and the k each had left.  No load sits
     // behind a branch (at the branch's end the compiler would wait for it): a lane
-    // with nothing to load reads `safe`, the operand's first 8 elements, and store()
-    // puts zeros.  A chunk that the operand's edge cuts is loaded as the 8 elements
-    // that end at the edge, and store() moves them down; the launcher sends operands
-    // with rows of under 8 elements elsewhere.
+    // with nothing to load reads `safe`, the operand's first 8 elements.  What lies
+    // past the last m is of no account (no output that is stored sees it), what lies
+    // past the last k has to be zero.  So a chunk cut by the last m reads on into the
+    // next row; in the operand's last row it is the 8 elements that end at the edge,
+    // which store_again() moves down, as for a chunk cut by the last k.  The launcher
+    // sends operands with rows of under 8 elements elsewhere.
     const char *safe;
     bool inside;  // T: every row of the tile exists
     int kl[SETS];
@@ -315,7 +317,7 @@ struct Tile {
     __device__ __forceinline__ void load(const void *base, const void *base2, int kleft, int wave)
     {
         const int n = T ? valid : kleft - chunk * 8;
-        const uint32_t back = n < 8 ? (uint32_t)(8 - n) * ES : 0u;
+        const uint32_t back = n < 8 && (!T || kleft <= BK) ? (uint32_t)(8 - n) * ES : 0u;
         kl[S] = kleft;
 #pragma unroll
         for (int q = 0; q < NL; ++q) {
@@ -331,11 +333,11 @@ struct Tile {
         }
     }
 
-    // does the k-tile in set S reach over the operand's edge?
+    // does the k-tile in set S reach over the last k, or hold cut chunks of the last row?
     template <int S>
     __device__ __forceinline__ bool edge() const
     {
-        return kl[S] < BK || (T && !inside);
+        return kl[S] < BK || (T && !inside && kl[S] == BK);
     }
 
     // register path: chunk q of set S to its stage, as if nothing were cut or odd (see split8)
@@ -366,7 +368,9 @@ struct Tile {
 #pragma unroll
             for (int w = 0; w < W; ++w)
                 v[w] = reg[S][q][w];
-            const int n = T ? (row + STEP * q < kl[S] ? valid : 0) : kl[S] - chunk * 8, s = min(8, max(0, 8 - n));
+            // as load() took it: only in the last row's k-tile are chunks cut by the last m moved
+            const int n = !T ? kl[S] - chunk * 8 : row + STEP * q >= kl[S] ? 0 : kl[S] <= BK ? valid : 8;
+            const int s = min(8, max(0, 8 - n));
             if (s & 7) {
                 if constexpr (ES == 2) {
                     v[0] = shift_down16(v[0], s & 7);

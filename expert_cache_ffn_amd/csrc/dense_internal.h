@@ -60,7 +60,8 @@ struct DenseGrad {
     int sums_dtype;
     float *partial;
 };
-int dense_grad_row_blocks(int T);
+// the most row blocks of any call with up to T tokens
+int64_t dense_grad_max_row_blocks(int64_t T);
 int launch_dense_grad(const DenseGrad &g, hipStream_t st);
 
 }  // namespace ecf

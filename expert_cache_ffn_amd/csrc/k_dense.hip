@@ -26,7 +26,7 @@ template <class E, bool GATED>
 __global__ __launch_bounds__(256) void k_dense_short(DenseGemm g, int tiles_n)
 {
     typedef typename E::raw R;
-    __shared__ float As[TK][TM + 1], Bs[GATED ? 2 : 1][TK][TN + 1];
+    __shared__ __attribute__((aligned(16))) float As[TK][TM + 4], Bs[GATED ? 2 : 1][TK][TN + 4];
     const int mt = (g.M + TM - 1) / TM, ty0 = (int)blockIdx.x / tiles_n;
     const int half = ty0 / mt;
     const int m0 = (ty0 % mt) * TM, n0 = ((int)blockIdx.x % tiles_n) * TN;
@@ -56,48 +56,61 @@ __global__ __launch_bounds__(256) void k_dense_short(DenseGemm g, int tiles_n)
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        acc[0][i][j] += As[k][ty * 4 + i] * Bs[0][k][tx + 16 * j];
+                        acc[0][i][j] += As[k][ty * 4 + i] * Bs[0][k][tx * 4 + j];
                         if (GATED)
-                            acc[GATED][i][j] += As[k][ty * 4 + i] * Bs[GATED][k][tx + 16 * j];
+                            acc[GATED][i][j] += As[k][ty * 4 + i] * Bs[GATED][k][tx * 4 + j];
                     }
             __syncthreads();
         }
     }
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+        const int64_t m = m0 + ty * 4 + i, n1 = n0 + tx * 4;
+        void *out = g.out[half];
+        if (m >= g.M || n1 >= g.N)
+            continue;
+        f32x4_t y4;
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty * 4 + i, n = n0 + tx + 16 * j;
-            if (m >= g.M || n >= g.N)
-                continue;
+            const int64_t n = min(n1 + j, (int64_t)g.N - 1);
             float z[2];
             for (int q = 0; q < (GATED ? 2 : 1); ++q) {
                 z[q] = acc[q][i][j] + (g.bias[q] ? E::to_f(((const R *)g.bias[q])[n]) : 0.f);
-                if (g.save[q])
+                if (g.save[q] && n1 + j < g.N)
                     ((R *)g.save[q])[m * g.ldsave + n] = E::from_f(z[q]);
             }
-            void *out = g.out[half];
-            if (!out)
-                continue;
             float y = act_value(z[0], g.act);
             if (GATED)
                 y *= z[1];
             else if (g.res)
                 y += g.out_dtype == ECF_F32 ? ((const float *)g.res)[m * g.ldres + n]
                                             : E::to_f(((const R *)g.res)[m * g.ldres + n]);
-            store_el(out, m * g.ldout + n, y, g.out_dtype);
+            y4[j] = y;
         }
+        if (!out)
+            continue;
+        if (g.out_dtype == ECF_F32 && n1 + 4 <= g.N) {
+            ((any128x4 *)((float *)out + m * g.ldout + n1))->v = y4;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n1 + j < g.N)
+                    store_el(out, m * g.ldout + n1 + j, y4[j], g.out_dtype);
+        }
+    }
 }
 
 // dz = dout * act'(a) (linear) or da = dout * b * act'(a), db = dout * act(a)
 // (gated), rounded once to the operands' type: they are operands of the two
 // matrix products that follow, which the matrix cores take in that type.
 // Bound by memory: reads dout, a and b, writes da and db.  A thread owns 8
-// columns (16-byte accesses) of every 8th of the block's 64 rows; the block's
-// column sums (of the unrounded values) are joined over its 8 row lanes in LDS,
-// always in the same order.
-constexpr int kGradRows = 64, kGradCols = 256;
+// columns (16-byte accesses) of every 8th of the block's rows; the block's column
+// sums (of the unrounded values) are joined over its 8 row lanes in LDS, always in
+// the same order.  64 rows per block, fewer where that leaves CUs without two
+// blocks (777 x 1999 gated fp16: 20 us with 64).
+constexpr int kGradRows = 64, kGradCols = 256, kGradBlocks = 512;
 
 template <class E, class ED, bool GATED>
-__global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks)
+__global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks, int rows)
 {
     constexpr int H = GATED ? 2 : 1;
     __shared__ float red[8][H][kGradCols + 4];
@@ -105,11 +118,11 @@ __global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks)
     const int cg = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int c = cb * kGradCols + cg * 8, n = g.I - c;
     const int64_t half = g.pitch / H;
-    const int t1 = min(g.T, (rb + 1) * kGradRows);
+    const int t1 = min(g.T, (rb + 1) * rows);
     float sum[H][8] = {};
     if (n > 0) {
 #pragma unroll 2
-        for (int64_t t = rb * kGradRows + rl; t < t1; t += 8) {
+        for (int64_t t = (int64_t)rb * rows + rl; t < t1; t += 8) {
             float d[8], a[8], b[8], out[H][8];
             load8<ED>(row_at<ED>(g.dout, t * g.lddout), c, n, d);
             if (g.a)
@@ -174,6 +187,7 @@ __global__ __launch_bounds__(256) void k_dense_colsum(const float *partial, int 
     const int64_t c = (int64_t)blockIdx.x * 64 + lane, cols = (int64_t)n * I;
     float s = 0.f;
     if (c < cols)
+#pragma unroll 8
         for (int64_t r = w; r < row_blocks; r += 4)
             s += partial[r * cols + c];
     red[w][lane] = s;
@@ -317,21 +331,28 @@ int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st)
                    : launch_gemm_nt(g, plan, gr, st);
 }
 
-int dense_grad_row_blocks(int T) { return (T + kGradRows - 1) / kGradRows; }
+int64_t dense_grad_max_row_blocks(int64_t T)
+{
+    return std::min<int64_t>((T + 7) / 8, std::max<int64_t>((T + kGradRows - 1) / kGradRows, 2 * kGradBlocks));
+}
 
 int launch_dense_grad(const DenseGrad &g, hipStream_t st)
 {
-    const int rows = dense_grad_row_blocks(g.T);
+    const int64_t cols = (g.I + kGradCols - 1) / kGradCols;
+    int per = kGradRows;  // rows per block
+    while (per > 8 && ((int64_t)g.T + per - 1) / per * cols < kGradBlocks)
+        per /= 2;
+    const int rows = (g.T + per - 1) / per;
     if (rows > 0) {
         ProfScope p("dense_grad", st);
-        const dim3 grid((unsigned)((g.I + kGradCols - 1) / kGradCols) * rows), block(256);
+        const dim3 grid((unsigned)(cols * rows)), block(256);
         auto go = [&](auto e, auto ed) {
             using E = decltype(e);
             using ED = decltype(ed);
             if (g.gated)
-                hipLaunchKernelGGL((k_dense_grad<E, ED, true>), grid, block, 0, st, g, rows);
+                hipLaunchKernelGGL((k_dense_grad<E, ED, true>), grid, block, 0, st, g, rows, per);
             else
-                hipLaunchKernelGGL((k_dense_grad<E, ED, false>), grid, block, 0, st, g, rows);
+                hipLaunchKernelGGL((k_dense_grad<E, ED, false>), grid, block, 0, st, g, rows, per);
         };
         if (g.dtype == ECF_F32)
             go(F32{}, F32{});

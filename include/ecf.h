@@ -351,11 +351,11 @@ int ecf_bandwidth_profile(const ecf_shape *shape, int32_t n_blobs, const void *c
  * gaps); rows may start at any address that is a multiple of the element size, and
  * sizes may be any number from 1 to 2^22 (n_tokens also 0: nothing is written by a
  * forward call, weight and bias gradients are zeros).  256 rows of any operand must
- * span less than 2 GiB (ECF_EUNSUPPORTED otherwise).  Nothing between the end of a row
- * and the next row's start is read or written.  Products are summed in fp32, biases,
- * activations and residuals are applied to the fp32 sums, and each output is rounded
- * once; the backward passes also round da, db and dz once to `dtype`, the type that
- * the two products behind them multiply.  Results do not depend on what runs beside a
+ * span less than 2 GiB (ECF_EUNSUPPORTED otherwise).  What lies between the end of a
+ * row and the next row's start changes no result and is not written.  Products are
+ * summed in fp32, biases, activations and residuals are applied to the fp32 sums,
+ * and each output is rounded once; the backward passes also round da, db and dz
+ * once to `dtype`, the type that the two products behind them multiply.  Results do not depend on what runs beside a
  * call, and the same call gives the same bits.  An infinite or NaN element makes
  * outputs infinite or NaN only in rows (columns) that it is part of.
  *
