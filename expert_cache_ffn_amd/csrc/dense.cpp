@@ -97,18 +97,18 @@ size_t forward_ws(int64_t T, int64_t out, int planes)
 
 // Backward workspace: dz rows in `dtype` (gated: da and db halves of one row,
 // each half's rows at 16-byte boundaries), the column sums of each row block in
-// fp32, and the partial sums of whichever product runs.
+// fp32, and the products' partial sums.
 struct BackWs {
     int64_t pitch;
     size_t colsum, split, total;
 };
-BackWs back_ws(int64_t in, int64_t cols, int halves, int dtype, int32_t T)
+BackWs back_ws(int64_t cols, int halves, int dtype, int32_t T)
 {
     BackWs w;
     w.pitch = halves * ((cols + 7) / 8 * 8);
     w.colsum = al256((size_t)T * w.pitch * dense_esize(dtype));
     w.split = w.colsum + al256((size_t)dense_grad_max_row_blocks(T) * halves * cols * 4);
-    w.total = w.split + std::max(dense_gemm_ws(T, in, 1), dense_gemm_ws(cols, in, halves));
+    w.total = w.split + kDensePartialBytes;
     return w;
 }
 
@@ -123,7 +123,7 @@ size_t ecf_gated_workspace_bytes(int32_t hidden, int32_t inter, int32_t dtype, i
 {
     if (check_common("ecf_gated_workspace_bytes", hidden, inter, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
-    return backward ? back_ws(hidden, inter, 2, dtype, n_tokens).total : forward_ws(n_tokens, inter, 2);
+    return backward ? back_ws(inter, 2, dtype, n_tokens).total : forward_ws(n_tokens, inter, 2);
 }
 
 int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
@@ -202,7 +202,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         }
         DENSE_TRY(check_vector(me, "d_db_gate", a->d_db_gate, a->wgrad_dtype));
         DENSE_TRY(check_vector(me, "d_db_up", a->d_db_up, a->wgrad_dtype));
-        const BackWs w = back_ws(d, I, 2, a->dtype, T);
+        const BackWs w = back_ws(I, 2, a->dtype, T);
         DENSE_TRY(check_pitch(me, w.pitch, a->dtype));
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
         hipStream_t st = (hipStream_t)a->stream;
@@ -224,34 +224,25 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
             DENSE_TRY(launch_dense_grad(q, st));
         }
         const char *dz2 = dz + (size_t)(w.pitch / 2) * dense_esize(a->dtype);
-        if (want_dx) {
-            DenseGemm g{};
-            g.dtype = g.out_dtype = a->dtype;
-            g.b_t = true;
-            g.ksegs = 2, g.mhalves = 1;
-            g.a[0] = dz, g.a[1] = dz2;
-            g.b[0] = a->d_w_gate, g.b[1] = a->d_w_up;
-            g.lda = w.pitch, g.ldb = ldw;
-            g.M = T, g.N = a->hidden, g.K = a->inter;
-            g.out[0] = a->d_dx;
-            g.ldout = lddx;
-            DENSE_TRY(launch_dense_gemm(g, (char *)a->d_ws + w.split, st));
-        }
-        if (want_dw) {
-            DenseGemm g{};
-            g.dtype = a->dtype;
-            g.out_dtype = a->wgrad_dtype;
-            g.a_t = g.b_t = true;
-            g.ksegs = 1, g.mhalves = 2;
-            g.a[0] = dz, g.a[1] = dz2;
-            g.b[0] = a->d_x;
-            g.lda = w.pitch, g.ldb = ldx;
-            g.M = a->inter, g.N = a->hidden, g.K = T;
-            g.out[0] = a->d_dw_gate, g.out[1] = a->d_dw_up;
-            g.ldout = lddw;
-            DENSE_TRY(launch_dense_gemm(g, (char *)a->d_ws + w.split, st));
-        }
-        return ECF_OK;
+        DenseGemm gx{}, gw{};
+        gx.dtype = gx.out_dtype = gw.dtype = a->dtype;
+        gx.b_t = gw.a_t = gw.b_t = true;
+        gx.ksegs = gw.mhalves = 2;
+        gx.mhalves = gw.ksegs = 1;
+        gx.a[0] = gw.a[0] = dz, gx.a[1] = gw.a[1] = dz2;
+        gx.lda = gw.lda = w.pitch;
+        gx.b[0] = a->d_w_gate, gx.b[1] = a->d_w_up;
+        gx.ldb = ldw;
+        gx.M = T, gx.N = a->hidden, gx.K = a->inter;
+        gx.out[0] = a->d_dx;
+        gx.ldout = lddx;
+        gw.out_dtype = a->wgrad_dtype;
+        gw.b[0] = a->d_x;
+        gw.ldb = ldx;
+        gw.M = a->inter, gw.N = a->hidden, gw.K = T;
+        gw.out[0] = a->d_dw_gate, gw.out[1] = a->d_dw_up;
+        gw.ldout = lddw;
+        return launch_dense_backward(want_dx ? &gx : nullptr, want_dw ? &gw : nullptr, (char *)a->d_ws + w.split, st);
     });
 }
 
@@ -260,7 +251,7 @@ size_t ecf_linear_workspace_bytes(int32_t in_features, int32_t out_features, int
 {
     if (check_common("ecf_linear_workspace_bytes", in_features, out_features, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
-    return backward ? back_ws(in_features, out_features, 1, dtype, n_tokens).total
+    return backward ? back_ws(out_features, 1, dtype, n_tokens).total
                     : forward_ws(n_tokens, out_features, 1);
 }
 
@@ -332,7 +323,7 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         if (a->d_dw)
             DENSE_TRY(check_matrix(me, "d_dw", a->d_dw, lddw, K, a->wgrad_dtype));
         DENSE_TRY(check_vector(me, "d_dbias", a->d_dbias, a->wgrad_dtype));
-        const BackWs w = back_ws(K, N, 1, a->dtype, T);
+        const BackWs w = back_ws(N, 1, a->dtype, T);
         DENSE_TRY(check_pitch(me, w.pitch, a->dtype));
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
         hipStream_t st = (hipStream_t)a->stream;
@@ -357,32 +348,24 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         }
         const void *dz = direct ? a->d_dout : a->d_ws;
         const int64_t lddz = direct ? lddy : w.pitch;
-        DenseGemm g{};
-        g.dtype = a->dtype;
-        g.ksegs = g.mhalves = 1;
-        g.a[0] = dz;
-        g.lda = lddz;
-        g.b_t = true;
-        if (want_dx) {
-            g.out_dtype = a->dtype;
-            g.b[0] = a->d_w;
-            g.ldb = ldw;
-            g.M = T, g.N = a->in_features, g.K = a->out_features;
-            g.out[0] = a->d_dx;
-            g.ldout = lddx;
-            DENSE_TRY(launch_dense_gemm(g, (char *)a->d_ws + w.split, st));
-        }
-        if (a->d_dw) {
-            g.out_dtype = a->wgrad_dtype;
-            g.a_t = true;
-            g.b[0] = a->d_x;
-            g.ldb = ldx;
-            g.M = a->out_features, g.N = a->in_features, g.K = T;
-            g.out[0] = a->d_dw;
-            g.ldout = lddw;
-            DENSE_TRY(launch_dense_gemm(g, (char *)a->d_ws + w.split, st));
-        }
-        return ECF_OK;
+        DenseGemm gx{}, gw{};
+        gx.dtype = gx.out_dtype = gw.dtype = a->dtype;
+        gx.b_t = gw.a_t = gw.b_t = true;
+        gx.ksegs = gx.mhalves = gw.ksegs = gw.mhalves = 1;
+        gx.a[0] = gw.a[0] = dz;
+        gx.lda = gw.lda = lddz;
+        gx.b[0] = a->d_w;
+        gx.ldb = ldw;
+        gx.M = T, gx.N = a->in_features, gx.K = a->out_features;
+        gx.out[0] = a->d_dx;
+        gx.ldout = lddx;
+        gw.out_dtype = a->wgrad_dtype;
+        gw.b[0] = a->d_x;
+        gw.ldb = ldx;
+        gw.M = a->out_features, gw.N = a->in_features, gw.K = T;
+        gw.out[0] = a->d_dw;
+        gw.ldout = lddw;
+        return launch_dense_backward(want_dx ? &gx : nullptr, a->d_dw ? &gw : nullptr, (char *)a->d_ws + w.split, st);
     });
 }
 

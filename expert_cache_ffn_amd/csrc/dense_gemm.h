@@ -444,10 +444,18 @@ struct Frag {
 
 }  // namespace gemm
 
-// grid: 1-D, one block per (split, output tile); see DenseGrid.
+// LDS of a block: the stages, which the output staging takes over at the end.
+template <class E, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE>
+constexpr int gemm_lds_bytes()
+{
+    constexpr int in = (DMA ? NSTAGE : 2) * (BM + BN) * BK * 2 * (sizeof(typename E::raw) == 4 ? 3 : 1);
+    constexpr int out = WM * WN * 32 * ((BN / WN >= 64 ? 64 : 32) + 4) * 4;
+    return in > out ? in : out;
+}
+
+// Block `block` of a product: one (split, output tile), see DenseGrid.
 template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE>
-__global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 2) void k_gemm(DenseGemm g,
-                                                                                                   DenseGrid gr)
+__device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &gr, int block, char *lds)
 {
     using namespace gemm;
     constexpr int NW = WM * WN, NTH = 64 * NW, RM = BM / WM, RN = BN / WN, FM = RM / 32, FN = RN / 32;
@@ -458,11 +466,9 @@ __global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 
     constexpr int ES = sizeof(typename E::raw), NP = ES == 4 ? 3 : 1;      // planes of parts
     constexpr int PA = BM * BK * 2, PB = BN * BK * 2, SA = PA * NP, SB = PB * NP;  // bytes per plane and stage
     constexpr int PITCH = (FN >= 2 ? 64 : 32) + 4;  // fp32 per row of the output staging
-    constexpr int OUT = NW * 32 * PITCH * 4, IN = NS * (SA + SB);
-    __shared__ __attribute__((aligned(16))) char lds[OUT > IN ? OUT : IN];
 
     int split, half, mt, nt;
-    gr.locate(blockIdx.x, split, half, mt, nt);
+    gr.locate(block, split, half, mt, nt);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int m0 = mt * BM, n0 = nt * (GATED ? BN / 2 : BN);
@@ -713,6 +719,31 @@ __global__ __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 
             }
         }
     }
+}
+
+// Waves per SIMD asked of the register allocator: two, but one where a wave's own
+// tile of sums takes more than half the registers.
+#define ECF_GEMM_BOUNDS __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 2)
+
+template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE>
+__global__ ECF_GEMM_BOUNDS void k_gemm(DenseGemm g, DenseGrid gr)
+{
+    __shared__ __attribute__((aligned(16))) char lds[gemm_lds_bytes<E, DMA, BM, BN, WM, WN, BK, NSTAGE>()];
+    gemm_block<E, AT, BT, GATED, DMA, BM, BN, WM, WN, BK, NSTAGE>(g, gr, (int)blockIdx.x, lds);
+}
+
+// The two products of a backward pass, dz W and dz^T x, in one launch: each alone
+// often leaves CUs idle, and neither needs the other.  The blocks of the longer
+// reduction come first.
+template <class E, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE>
+__global__ ECF_GEMM_BOUNDS void k_gemm_pair(DenseGemm gx, DenseGrid grx, DenseGemm gw, DenseGrid grw, int x_first)
+{
+    __shared__ __attribute__((aligned(16))) char lds[gemm_lds_bytes<E, DMA, BM, BN, WM, WN, BK, NSTAGE>()];
+    const int nx = grx.blocks(), nw = grw.blocks(), b = (int)blockIdx.x;
+    if (x_first ? b < nx : b >= nw)
+        gemm_block<E, false, true, false, DMA, BM, BN, WM, WN, BK, NSTAGE>(gx, grx, x_first ? b : b - nw, lds);
+    else
+        gemm_block<E, true, true, false, DMA, BM, BN, WM, WN, BK, NSTAGE>(gw, grw, x_first ? b - nx : b, lds);
 }
 
 // Joins the splits of a product, in order, and applies its epilogue: one thread

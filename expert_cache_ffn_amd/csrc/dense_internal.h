@@ -35,6 +35,9 @@ struct DenseGemm {
 };
 // ws: room for dense_gemm_ws bytes (may be null where that is 0)
 int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st);
+// The products of a backward pass, dx (n-contiguous B) and dW (m- and n-contiguous;
+// either may be null), in one launch or two.  ws: kDensePartialBytes.
+int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, void *ws, hipStream_t st);
 // Forward products of at most kFewTokens rows (k_dense_few.hip) need no workspace.
 constexpr int kFewTokens = 16;
 int launch_dense_few(const DenseGemm &g, int cus, hipStream_t st);

@@ -12,24 +12,63 @@ void launch_gemm(const DenseGemm &g, const DenseGrid &gr, hipStream_t st)
                        g, gr);
 }
 
+template <class E, bool GATED>
+void launch_join(const DenseGemm &g, const DenseGrid &gr, hipStream_t st)
+{
+    const int64_t n = gr.np / 8 * g.M * g.mhalves;
+    hipLaunchKernelGGL((k_dense_join<E, GATED>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, g, gr);
+}
+
 template <class E, bool AT, bool BT, bool GATED, bool DMA>
 int pick_gemm(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st)
 {
+    // the order of the launcher's tables
     if constexpr (std::is_same<E, F32>::value) {
-        if (p.tile == 0)  // the order of the launcher's tables
+        if (p.tile == 0)
             launch_gemm<E, AT, BT, GATED, false, 128, 128, 4, 2, 32, 1>(g, gr, st);
         else
             launch_gemm<E, AT, BT, GATED, false, 64, 128, 2, 2, 32, 2>(g, gr, st);
-    } else switch (p.tile) {  // the order of the launcher's tables
-    case 0: launch_gemm<E, AT, BT, GATED, DMA, 256, 256, 2, 4, 64, DMA ? 2 : 1>(g, gr, st); break;
-    case 1: launch_gemm<E, AT, BT, GATED, DMA, 128, 256, 2, 4, 64, DMA ? 3 : 2>(g, gr, st); break;
-    case 2: launch_gemm<E, AT, BT, GATED, DMA, 128, 128, 2, 2, 64, DMA ? 2 : 1>(g, gr, st); break;
-    default: launch_gemm<E, AT, BT, GATED, DMA, 64, 128, 2, 2, 64, DMA ? 3 : 2>(g, gr, st); break;
+    } else {
+        switch (p.tile) {
+        case 0: launch_gemm<E, AT, BT, GATED, DMA, 256, 256, 2, 4, 64, DMA ? 2 : 1>(g, gr, st); break;
+        case 1: launch_gemm<E, AT, BT, GATED, DMA, 128, 256, 2, 4, 64, DMA ? 3 : 2>(g, gr, st); break;
+        case 2: launch_gemm<E, AT, BT, GATED, DMA, 128, 128, 2, 2, 64, DMA ? 2 : 1>(g, gr, st); break;
+        default: launch_gemm<E, AT, BT, GATED, DMA, 64, 128, 2, 2, 64, DMA ? 3 : 2>(g, gr, st); break;
+        }
     }
-    if (gr.splits > 1) {
-        const int64_t n = gr.np / 8 * g.M * g.mhalves;
-        hipLaunchKernelGGL((k_dense_join<E, GATED>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, g, gr);
+    if (gr.splits > 1)
+        launch_join<E, GATED>(g, gr, st);
+    ECF_HIP_CHECK(hipGetLastError());
+    return ECF_OK;
+}
+
+template <class E, bool DMA, int BM, int BN, int WM, int WN, int BK, int NS>
+void launch_pair(const DenseGemm &gx, const DenseGrid &grx, const DenseGemm &gw, const DenseGrid &grw, hipStream_t st)
+{
+    const int x_first = (int64_t)gx.K * gx.ksegs / grx.splits >= gw.K / grw.splits;
+    hipLaunchKernelGGL((k_gemm_pair<E, DMA, BM, BN, WM, WN, BK, NS>), dim3(grx.blocks() + grw.blocks()),
+                       dim3(64 * WM * WN), 0, st, gx, grx, gw, grw, x_first);
+}
+
+template <class E, bool DMA>
+int pick_pair(const DenseGemm &gx, const DenseGrid &grx, const DenseGemm &gw, const DenseGrid &grw, const DensePlan &p,
+              hipStream_t st)
+{
+    if constexpr (std::is_same<E, F32>::value) {
+        if (p.tile == 0)
+            launch_pair<E, false, 128, 128, 4, 2, 32, 1>(gx, grx, gw, grw, st);
+        else
+            launch_pair<E, false, 64, 128, 2, 2, 32, 2>(gx, grx, gw, grw, st);
+    } else {
+        if (p.tile == 2)
+            launch_pair<E, DMA, 128, 128, 2, 2, 64, DMA ? 2 : 1>(gx, grx, gw, grw, st);
+        else
+            launch_pair<E, DMA, 64, 128, 2, 2, 64, DMA ? 3 : 2>(gx, grx, gw, grw, st);
     }
+    if (grx.splits > 1)
+        launch_join<E, false>(gx, grx, st);
+    if (grw.splits > 1)
+        launch_join<E, false>(gw, grw, st);
     ECF_HIP_CHECK(hipGetLastError());
     return ECF_OK;
 }
@@ -50,5 +89,8 @@ int launch_gemm_gated(const DenseGemm &g, const DensePlan &p, const DenseGrid &g
 int launch_gemm_nt(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st);
 int launch_gemm_nn(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st);
 int launch_gemm_tn(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st);
+
+int launch_gemm_pair(const DenseGemm &gx, const DenseGrid &grx, const DenseGemm &gw, const DenseGrid &grw,
+                     const DensePlan &p, hipStream_t st);
 
 }  // namespace ecf

@@ -240,43 +240,116 @@ int cu_count(int *out)
 }
 
 constexpr int kMaxSplits = 16;
+constexpr double kLaunchUs = 3.0;  // one launch more, host and device
+
+// Rows at 16-byte boundaries and whole 16-byte chunks: operands can go straight to LDS.
+bool dma_ok(const DenseGemm &g)
+{
+    if (g.dtype == ECF_F32)
+        return false;
+    for (int s = 0; s < g.ksegs || s < g.mhalves; ++s)
+        if (!aligned16(g.a[s], g.lda, g.dtype))
+            return false;
+    for (int s = 0; s < (g.gated || g.ksegs == 2 ? 2 : 1); ++s)
+        if (!aligned16(g.b[s], g.ldb, g.dtype))
+            return false;
+    return (g.a_t ? g.M : g.K) % 8 == 0 && (g.b_t ? g.N : g.K) % 8 == 0;
+}
+
+// Rows too short for the MFMA tiles' chunks, or (fp32) a reduction too short to be worth them.
+bool short_rows(const DenseGemm &g)
+{
+    return (g.a_t ? g.M : g.K) < 8 || (g.b_t ? g.N : g.K) < 8 || (g.dtype == ECF_F32 && g.K < kShortK);
+}
+
+int ktiles(const DenseGemm &g) { return (g.K + 63) / 64 * g.ksegs; }
+int64_t out_tiles(const DenseGemm &g, const TileCost &c)
+{
+    const int bn = c.bn / (g.gated ? 2 : 1);
+    return (int64_t)((g.M + c.bm - 1) / c.bm) * g.mhalves * ((g.N + bn - 1) / bn);
+}
+// Bytes of the partial sums, and the join's time for them.
+double partial_bytes(const DenseGemm &g, int splits)
+{
+    return (double)splits * (g.gated ? 2 : g.mhalves) * g.M * ((g.N + 7) / 8 * 8) * 4;
+}
+double join_us(const DenseGemm &g, int splits) { return splits > 1 ? 4.0 + partial_bytes(g, splits) * 2 / 4e6 : 0.0; }
+bool may_split(const DenseGemm &g, int splits, size_t room)
+{
+    return splits == 1 || (ktiles(g) / splits >= 2 && partial_bytes(g, splits) <= (double)room);
+}
 
 // The tile and the splits of K with the least estimated time: rounds of blocks
 // over the CUs times the k-tiles each walks, plus the join of the splits.
-DensePlan plan_gemm(const DenseGemm &g, int cus, bool may_split)
+DensePlan plan_gemm(const DenseGemm &g, int cus, size_t room, double *us_out)
 {
-    DensePlan best{0, 1, g.dtype != ECF_F32};
-    for (int s = 0; s < g.ksegs || s < g.mhalves; ++s)
-        best.dma = best.dma && aligned16(g.a[s], g.lda, g.dtype);
-    for (int s = 0; s < (g.gated || g.ksegs == 2 ? 2 : 1); ++s)
-        best.dma = best.dma && aligned16(g.b[s], g.ldb, g.dtype);
-    best.dma = best.dma && (g.a_t ? g.M : g.K) % 8 == 0 && (g.b_t ? g.N : g.K) % 8 == 0;
-    const int n_tiles = g.dtype == ECF_F32 ? 2 : 4;
+    DensePlan best{0, 1, dma_ok(g)};
+    const int n_tiles = g.dtype == ECF_F32 ? 2 : 4, kt = ktiles(g);
     const TileCost *tiles = tiles_of(g.dtype, best.dma);
-    const int kt = (g.K + 63) / 64 * g.ksegs;
-    const int64_t np = (g.N + 7) / 8 * 8, planes = g.gated ? 2 : g.mhalves;
-    double least = 1e300;
+    *us_out = 1e300;
     for (int t = 0; t < n_tiles; ++t) {
         const TileCost &c = tiles[t];
-        const int bn = c.bn / (g.gated ? 2 : 1);
-        const int64_t tiles_out = (int64_t)((g.M + c.bm - 1) / c.bm) * g.mhalves * ((g.N + bn - 1) / bn);
-        for (int s = 1; s <= kMaxSplits; s *= 2) {
-            const double part = (double)s * planes * g.M * np * 4;
-            if (s > 1 && (!may_split || kt / s < 2 || part > (double)kDensePartialBytes))
-                break;
+        for (int s = 1; s <= kMaxSplits && may_split(g, s, room); s *= 2) {
             // full rounds of per_cu blocks on every CU, then what is left
-            const int64_t blocks = tiles_out * s, round = (int64_t)cus * c.per_cu, rest = blocks % round;
+            const int64_t blocks = out_tiles(g, c) * s, round = (int64_t)cus * c.per_cu, rest = blocks % round;
             const double tail = rest == 0 ? 0.0 : rest <= cus ? c.us1 : c.us;
             const double walk = (double)((kt + s - 1) / s) * ((blocks / round) * c.us + tail);
-            const double us = walk + (double)((blocks + round - 1) / round) * c.fixed + (s > 1 ? 3.0 + part * 2 / 4e6 : 0.0);
-            if (us < least) {
-                least = us;
+            const double us = walk + (double)((blocks + round - 1) / round) * c.fixed + join_us(g, s);
+            if (us < *us_out) {
+                *us_out = us;
                 best.tile = t;
                 best.splits = s;
             }
         }
     }
     return best;
+}
+
+// The same for two products in one launch: the work of all blocks over all CUs,
+// but no less than the longest block's.
+struct PairPlan {
+    DensePlan x;
+    int splits_w;
+};
+PairPlan plan_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t room, double *us_out)
+{
+    PairPlan best{{0, 1, dma_ok(gx) && dma_ok(gw)}, 1};
+    const bool f32 = gx.dtype == ECF_F32;
+    const TileCost *tiles = tiles_of(gx.dtype, best.x.dma);
+    *us_out = 1e300;
+    for (int t = f32 ? 0 : 2; t < (f32 ? 2 : 4); ++t) {
+        const TileCost &c = tiles[t];
+        const int64_t slots = (int64_t)cus * c.per_cu;
+        for (int sx = 1; sx <= kMaxSplits && may_split(gx, sx, room); sx *= 2)
+            for (int sw = 1; sw <= kMaxSplits && may_split(gw, sw, room); sw *= 2) {
+                const int64_t bx = out_tiles(gx, c) * sx, bw = out_tiles(gw, c) * sw;
+                const double kx = (ktiles(gx) + sx - 1) / sx, kw = (ktiles(gw) + sw - 1) / sw;
+                const double full = ((double)bx * kx + (double)bw * kw) * c.us / slots;
+                const double longest = std::max(kx, kw) * (bx + bw <= cus ? c.us1 : c.us);
+                const double us = std::max(full, longest) + (double)((bx + bw + slots - 1) / slots) * c.fixed +
+                                  join_us(gx, sx) + join_us(gw, sw);
+                if (us < *us_out) {
+                    *us_out = us;
+                    best.x.tile = t;
+                    best.x.splits = sx;
+                    best.splits_w = sw;
+                }
+            }
+    }
+    return best;
+}
+
+DenseGrid grid_of(const DenseGemm &g, const TileCost &t, int splits, void *ws)
+{
+    const int bn = g.gated ? t.bn / 2 : t.bn;
+    DenseGrid gr{};
+    gr.half_tiles = (g.M + t.bm - 1) / t.bm;
+    gr.tiles_m = gr.half_tiles * g.mhalves;
+    gr.tiles_n = (g.N + bn - 1) / bn;
+    gr.splits = splits;
+    gr.partial = (float *)ws;
+    gr.np = (g.N + 7) / 8 * 8;
+    return gr;
 }
 
 }  // namespace
@@ -296,7 +369,7 @@ int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st)
         return rc;
     if (!g.a_t && !g.b_t && g.M <= kFewTokens)
         return launch_dense_few(g, cus, st);
-    if ((g.a_t ? g.M : g.K) < 8 || (g.b_t ? g.N : g.K) < 8 || (g.dtype == ECF_F32 && g.K < kShortK)) {
+    if (short_rows(g)) {
         const int tiles_n = (g.N + TN - 1) / TN;
         const dim3 grid((unsigned)tiles_n * ((g.M + TM - 1) / TM) * g.mhalves);
         auto go = [&](auto e) {
@@ -315,20 +388,40 @@ int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st)
         ECF_HIP_CHECK(hipGetLastError());
         return ECF_OK;
     }
-    const DensePlan plan = plan_gemm(g, cus, ws != nullptr);
-    const TileCost &t = tiles_of(g.dtype, plan.dma)[plan.tile];
-    const int bn = g.gated ? t.bn / 2 : t.bn;
-    DenseGrid gr{};
-    gr.half_tiles = (g.M + t.bm - 1) / t.bm;
-    gr.tiles_m = gr.half_tiles * g.mhalves;
-    gr.tiles_n = (g.N + bn - 1) / bn;
-    gr.splits = plan.splits;
-    gr.partial = (float *)ws;
-    gr.np = (g.N + 7) / 8 * 8;
+    double us;
+    const DensePlan plan = plan_gemm(g, cus, ws ? kDensePartialBytes : 0, &us);
+    const DenseGrid gr = grid_of(g, tiles_of(g.dtype, plan.dma)[plan.tile], plan.splits, ws);
     return g.gated ? launch_gemm_gated(g, plan, gr, st)
            : g.a_t ? launch_gemm_tn(g, plan, gr, st)
            : g.b_t ? launch_gemm_nn(g, plan, gr, st)
                    : launch_gemm_nt(g, plan, gr, st);
+}
+
+int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, void *ws, hipStream_t st)
+{
+    if (gx && gw && !short_rows(*gx) && !short_rows(*gw)) {
+        int cus = 0;
+        const int rc = cu_count(&cus);
+        if (rc != ECF_OK)
+            return rc;
+        constexpr size_t half = kDensePartialBytes / 2;
+        double ux, uw, both;
+        plan_gemm(*gx, cus, kDensePartialBytes, &ux);
+        plan_gemm(*gw, cus, kDensePartialBytes, &uw);
+        const PairPlan p = plan_pair(*gx, *gw, cus, half, &both);
+        if (both < ux + uw + kLaunchUs) {
+            ProfScope scope("dense_gemm_pair", st);
+            const TileCost &t = tiles_of(gx->dtype, p.x.dma)[p.x.tile];
+            return launch_gemm_pair(*gx, grid_of(*gx, t, p.x.splits, ws), *gw,
+                                    grid_of(*gw, t, p.splits_w, (char *)ws + half), p.x, st);
+        }
+    }
+    if (gx) {
+        const int rc = launch_dense_gemm(*gx, ws, st);
+        if (rc != ECF_OK)
+            return rc;
+    }
+    return gw ? launch_dense_gemm(*gw, ws, st) : ECF_OK;
 }
 
 int64_t dense_grad_max_row_blocks(int64_t T)
@@ -339,8 +432,8 @@ int64_t dense_grad_max_row_blocks(int64_t T)
 int launch_dense_grad(const DenseGrad &g, hipStream_t st)
 {
     const int64_t cols = (g.I + kGradCols - 1) / kGradCols;
-    int per = kGradRows;  // rows per block
-    while (per > 8 && ((int64_t)g.T + per - 1) / per * cols < kGradBlocks)
+    int per = kGradRows;  // rows per block; one block saves the launch that joins the sums
+    while (per > 8 && !(g.want_sums && g.T <= kGradRows) && ((int64_t)g.T + per - 1) / per * cols < kGradBlocks)
         per /= 2;
     const int rows = (g.T + per - 1) / per;
     if (rows > 0) {

@@ -103,6 +103,7 @@ class Layer:
 # The address of a device's current stream.  torch.cuda.current_stream() builds a
 # Stream object around it, 2.8 us of the 11 a one-token call took on the host.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 _DENSE_DT = {torch.float32: L.ECF_F32, torch.bfloat16: L.ECF_BF16, torch.float16: L.ECF_F16}
 
@@ -115,14 +116,14 @@ def _dense_dt(dtype, what):
 
 def _matrix(name, t, rows, cols, dtype, device):
     """(address, row stride) of a [rows, cols] operand; its rows may lie apart but not overlap."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if not isinstance(t, torch.Tensor) or t.shape != (rows, cols):
         raise ValueError(f"{name} must be a [{rows}, {cols}] tensor, got {tuple(getattr(t, 'shape', ()))}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the weights are on {device}")
     ld, inner = t.stride()
-    if cols > 1 and inner != 1:
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows (strides {t.stride()})")
     if rows <= 1:
         ld = cols  # a single row's stride says nothing
@@ -153,7 +154,7 @@ class _Dense:
             raise ValueError(f"{what} must be a non-empty 2-D tensor on the GPU")
         if act not in L.ACTS:
             raise ValueError(f"act must be one of {sorted(L.ACTS)}, got {act!r}")
-        self.device, self.dtype, self.act = w.device, w.dtype, act
+        self.device, self.dtype, self.act, self._w = w.device, w.dtype, act, w
         self._dt = _dense_dt(w.dtype, what)
         self._ws_of = {}
 
@@ -163,7 +164,7 @@ class _Dense:
         return x.shape[0]
 
     def _run(self, fn, a, T, backward):
-        if torch.cuda.current_device() != self.device.index:
+        if _current_device() != self.device.index:
             with torch.cuda.device(self.device):
                 return self._run(fn, a, T, backward)
         n = self._ws_of.get((T, backward))
@@ -186,7 +187,8 @@ class _Dense:
 
     def _out(self, name, t, rows, cols, dtype):
         if t is None:
-            t = torch.empty((rows, cols), dtype=dtype, device=self.device)
+            t = self._w.new_empty((rows, cols)) if dtype is self.dtype else \
+                torch.empty((rows, cols), dtype=dtype, device=self.device)
             return t, t.data_ptr(), cols
         return (t,) + _matrix(name, t, rows, cols, dtype, self.device)
 
