@@ -231,6 +231,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         gx.mhalves = gw.ksegs = 1;
         gx.a[0] = gw.a[0] = dz, gx.a[1] = gw.a[1] = dz2;
         gx.lda = gw.lda = w.pitch;
+        gx.a_padded = gw.a_padded = true;
         gx.b[0] = a->d_w_gate, gx.b[1] = a->d_w_up;
         gx.ldb = ldw;
         gx.M = T, gx.N = a->hidden, gx.K = a->inter;
@@ -354,6 +355,7 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         gx.ksegs = gx.mhalves = gw.ksegs = gw.mhalves = 1;
         gx.a[0] = gw.a[0] = dz;
         gx.lda = gw.lda = lddz;
+        gx.a_padded = gw.a_padded = !direct;
         gx.b[0] = a->d_w;
         gx.ldb = ldw;
         gx.M = T, gx.N = a->in_features, gx.K = a->out_features;

@@ -19,12 +19,22 @@ struct F32 {
 struct BF16 {
     typedef uint16_t raw;
     static __device__ __forceinline__ float to_f(raw v) { return bf_to_f(v); }
-    static __device__ __forceinline__ raw from_f(float v) { return f_to_bf(v); }
+    // the hardware's conversion (NaN stays NaN), two values per instruction where they are packed
+    static __device__ __forceinline__ raw from_f(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+    static __device__ __forceinline__ uint32_t pack(float a, float b)
+    {
+        const bf16x2_t v = {(__bf16)a, (__bf16)b};
+        return __builtin_bit_cast(uint32_t, v);
+    }
 };
 struct F16 {
     typedef uint16_t raw;
     static __device__ __forceinline__ float to_f(raw v) { return (float)__builtin_bit_cast(_Float16, v); }
     static __device__ __forceinline__ raw from_f(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+    static __device__ __forceinline__ uint32_t pack(float a, float b)
+    {
+        return (uint32_t)from_f(a) | (uint32_t)from_f(b) << 16;
+    }
 };
 
 // v moved down by s 16-bit elements (0..7), zeros from above
@@ -95,7 +105,7 @@ __device__ __forceinline__ void store8(void *row, int64_t col, int n, const floa
             u32x4_t a;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                a[j] = (uint32_t)E::from_f(v[2 * j]) | (uint32_t)E::from_f(v[2 * j + 1]) << 16;
+                a[j] = E::pack(v[2 * j], v[2 * j + 1]);
             ((any128x2 *)q)->v = a;
         }
         return;

@@ -264,25 +264,25 @@ struct Tile {
     int valid;         // T: elements of the chunk that exist (up to 8, none if <= 0)
     // register path: the chunks of SETS k-tiles and the k each had left.  No load sits
     // behind a branch (at the branch's end the compiler would wait for it): a lane
-    // with nothing to load reads `safe`, the operand's first 8 elements.  What lies
+    // with nothing to load reads the tile's first 8 elements.  What lies
     // past the last m is of no account (no output that is stored sees it), what lies
     // past the last k has to be zero.  So a chunk cut by the last m reads on into the
     // next row; in the operand's last row it is the 8 elements that end at the edge,
     // which store_again() moves down, as for a chunk cut by the last k.  The launcher
     // sends operands with rows of under 8 elements elsewhere.
-    const char *safe;
-    bool inside;  // T: every row of the tile exists
+    const char *first;  // the operand's first element, for k-tiles past the end
+    int rows;           // rows from the tile's first on
     int kl[SETS];
     u32x4_t reg[SETS][DMA ? 1 : NL][W];
 
     // `rows` rows from the tile's first on, row stride ld (elements); rowmap turns a
     // tile row into a row relative to the base (clamped to the last one)
     template <class F>
-    __device__ __forceinline__ void init(int tid, int rows, const void *first, int64_t ld, F rowmap)
+    __device__ __forceinline__ void init(int tid, int rows_, const void *first_, int64_t ld, F rowmap)
     {
         row = tid / CPR;
-        safe = (const char *)first;
-        inside = rows >= ROWS;
+        first = (const char *)first_;
+        rows = rows_;
         if constexpr (!T) {
             chunk = (tid % CPR) ^ rswz<BK>(row);
             valid = 8;
@@ -316,14 +316,21 @@ struct Tile {
     template <bool PAIR, int S>
     __device__ __forceinline__ void load(const void *base, const void *base2, int kleft, int wave)
     {
+        // Offsets from 8 elements before the tile, so that none is negative and each
+        // load is a scalar base and one 32-bit register.  back(n): a chunk of n
+        // elements is taken from 8 - n elements further down.
+        auto back = [](int n) { return (uint32_t)min(max(8 - n, 0), 8) * ES; };
+        const bool last = !T || kleft <= BK;  // else cut chunks read on into the next row
         const int n = T ? valid : kleft - chunk * 8;
-        const uint32_t back = n < 8 && (!T || kleft <= BK) ? (uint32_t)(8 - n) * ES : 0u;
+        const uint32_t shift = 8 * ES - (last ? back(n) : 0u);
+        const uint32_t none = kleft <= 0 ? 8u * ES : 8 * ES - (last ? back(T ? rows : kleft) : 0u);
+        const char *b1 = (kleft > 0 ? (const char *)base : first) - 8 * ES;
+        const char *b2 = (kleft > 0 ? (const char *)base2 : first) - 8 * ES;
         kl[S] = kleft;
 #pragma unroll
         for (int q = 0; q < NL; ++q) {
             const bool in = n > 0 && (!T || row + STEP * q < kleft);
-            const char *p = (const char *)(PAIR && second(q, wave) ? base2 : base) + off[q] - back;
-            p = in ? p : safe;
+            const char *p = (PAIR && second(q, wave) ? b2 : b1) + (in ? off[q] + shift : none);
             if constexpr (ES == 2) {
                 reg[S][q][0] = ((const any128x2 *)p)->v;
             } else {
@@ -337,7 +344,7 @@ struct Tile {
     template <int S>
     __device__ __forceinline__ bool edge() const
     {
-        return kl[S] < BK || (T && !inside && kl[S] == BK);
+        return kl[S] < BK || (T && rows < ROWS && kl[S] == BK);
     }
 
     // register path: chunk q of set S to its stage, as if nothing were cut or odd (see split8)
@@ -578,23 +585,32 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
     // this order: left alone, the compiler moves the reads behind the last MFMAs.
     constexpr int MF = FM * FN;
     auto step = [&](int set, int stage, int ks, auto extra) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
+        auto reads = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
             for (int f = i * (FM + FN) / MF; f < (i + 1) * (FM + FN) / MF; ++f)
                 fetch(stage, ks, set ^ 1, f);
             extra(i);
-            const u32x4_t *a = av[set][i / FN], *b = bv[set][i % FN];
-            f32x16_t &c = acc[i / FN][i % FN];
-            if constexpr (NP == 3) {  // the small products first
-                c = mfma16<E>(a[1], b[1], c);
-                c = mfma16<E>(a[0], b[2], c);
-                c = mfma16<E>(a[2], b[0], c);
-                c = mfma16<E>(a[0], b[1], c);
-                c = mfma16<E>(a[1], b[0], c);
+        };
+        if constexpr (NP == 1) {
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                reads(i);
+                acc[i / FN][i % FN] = mfma16<E>(av[set][i / FN][0], bv[set][i % FN][0], acc[i / FN][i % FN]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            c = mfma16<E>(a[0], b[0], c);
-            __builtin_amdgcn_sched_barrier(0);
+        } else {
+            // six products, the small ones first; neighbours write different sums, so
+            // that none waits for the one before it
+            constexpr int PA_[6] = {1, 0, 2, 0, 1, 0}, PB_[6] = {1, 2, 0, 1, 0, 0};
+#pragma unroll
+            for (int x = 0; x < 6 * MF; ++x) {
+                if (x % 6 == 0)
+                    reads(x / 6);
+                const int i = x % MF, p = x / MF;
+                acc[i / FN][i % FN] = mfma16<E>(av[set][i / FN][PA_[p]], bv[set][i % FN][PB_[p]], acc[i / FN][i % FN]);
+                if (x % 6 == 5)
+                    __builtin_amdgcn_sched_barrier(0);
+            }
         }
     };
     if (kb < ke) {

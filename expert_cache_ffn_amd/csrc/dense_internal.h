@@ -20,6 +20,7 @@ struct DenseGemm {
     bool a_t, b_t;
     const void *a[2], *b[2];
     int64_t lda, ldb;
+    bool a_padded;  // rows of A go on with zeros to the next multiple of 8 elements
     int M, N, K;
     int ksegs, mhalves;
     bool gated;

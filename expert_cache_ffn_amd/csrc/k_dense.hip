@@ -102,27 +102,27 @@ __global__ __launch_bounds__(256) void k_dense_short(DenseGemm g, int tiles_n)
 // dz = dout * act'(a) (linear) or da = dout * b * act'(a), db = dout * act(a)
 // (gated), rounded once to the operands' type: they are operands of the two
 // matrix products that follow, which the matrix cores take in that type.
-// Bound by memory: reads dout, a and b, writes da and db.  A thread owns 8
-// columns (16-byte accesses) of every 8th of the block's rows; the block's column
-// sums (of the unrounded values) are joined over its 8 row lanes in LDS, always in
-// the same order.  64 rows per block, fewer where that leaves CUs without two
-// blocks (777 x 1999 gated fp16: 20 us with 64).
-constexpr int kGradRows = 64, kGradCols = 256, kGradBlocks = 512;
+// Bound by memory: reads dout, a and b, writes da and db.  A block owns 64 columns
+// of 64 rows (32 where that leaves CUs without two blocks): a thread takes 8
+// columns (16-byte accesses) of every 32nd row, and the column sums (of the
+// unrounded values) are joined over the 32 row lanes in LDS, always in the same
+// order.  (256 columns and 8 row lanes: 14.6 us for 57 x 6272, a chain of eight rows.)
+constexpr int kGradRows = 64, kGradCols = 64, kGradLanes = 32, kGradBlocks = 512;
 
 template <class E, class ED, bool GATED>
 __global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks, int rows)
 {
     constexpr int H = GATED ? 2 : 1;
-    __shared__ float red[8][H][kGradCols + 4];
+    __shared__ float red[kGradLanes][H][kGradCols + 4];
     const int cb = (int)blockIdx.x / row_blocks, rb = (int)blockIdx.x - cb * row_blocks;
-    const int cg = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int cg = threadIdx.x & 7, rl = threadIdx.x >> 3;
     const int c = cb * kGradCols + cg * 8, n = g.I - c;
     const int64_t half = g.pitch / H;
     const int t1 = min(g.T, (rb + 1) * rows);
     float sum[H][8] = {};
     if (n > 0) {
 #pragma unroll 2
-        for (int64_t t = (int64_t)rb * rows + rl; t < t1; t += 8) {
+        for (int64_t t = (int64_t)rb * rows + rl; t < t1; t += kGradLanes) {
             float d[8], a[8], b[8], out[H][8];
             load8<ED>(row_at<ED>(g.dout, t * g.lddout), c, n, d);
             if (g.a)
@@ -161,15 +161,15 @@ __global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks,
         for (int j = 0; j < 8; ++j)
             red[rl][h][cg * 8 + j] = sum[h][j];
     __syncthreads();
-    const int64_t col = (int64_t)cb * kGradCols + threadIdx.x;
-    if (col >= g.I)
+    if (threadIdx.x >= kGradCols * H)
         return;
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
+    const int h = threadIdx.x / kGradCols, lc = threadIdx.x % kGradCols;
+    const int64_t col = (int64_t)cb * kGradCols + lc;
+    if (col < g.I) {
         float s = 0.f;
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-            s += red[r][h][threadIdx.x];
+        for (int r = 0; r < kGradLanes; ++r)
+            s += red[r][h][lc];
         if (row_blocks > 1)
             g.partial[((int64_t)rb * H + h) * g.I + col] = s;
         else if (g.sums[h])
@@ -253,7 +253,7 @@ bool dma_ok(const DenseGemm &g)
     for (int s = 0; s < (g.gated || g.ksegs == 2 ? 2 : 1); ++s)
         if (!aligned16(g.b[s], g.ldb, g.dtype))
             return false;
-    return (g.a_t ? g.M : g.K) % 8 == 0 && (g.b_t ? g.N : g.K) % 8 == 0;
+    return (g.a_padded || (g.a_t ? g.M : g.K) % 8 == 0) && (g.b_t ? g.N : g.K) % 8 == 0;
 }
 
 // Rows too short for the MFMA tiles' chunks, or (fp32) a reduction too short to be worth them.
@@ -424,17 +424,14 @@ int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, void *ws, hi
     return gw ? launch_dense_gemm(*gw, ws, st) : ECF_OK;
 }
 
-int64_t dense_grad_max_row_blocks(int64_t T)
-{
-    return std::min<int64_t>((T + 7) / 8, std::max<int64_t>((T + kGradRows - 1) / kGradRows, 2 * kGradBlocks));
-}
+int64_t dense_grad_max_row_blocks(int64_t T) { return (T + kGradLanes - 1) / kGradLanes; }
 
 int launch_dense_grad(const DenseGrad &g, hipStream_t st)
 {
     const int64_t cols = (g.I + kGradCols - 1) / kGradCols;
-    int per = kGradRows;  // rows per block; one block saves the launch that joins the sums
-    while (per > 8 && !(g.want_sums && g.T <= kGradRows) && ((int64_t)g.T + per - 1) / per * cols < kGradBlocks)
-        per /= 2;
+    // rows per block; all of a short batch in one block saves the launch that joins the sums
+    const bool few = ((int64_t)g.T + kGradRows - 1) / kGradRows * cols < kGradBlocks;
+    const int per = few && !(g.want_sums && g.T <= kGradRows) ? kGradLanes : kGradRows;
     const int rows = (g.T + per - 1) / per;
     if (rows > 0) {
         ProfScope p("dense_grad", st);
