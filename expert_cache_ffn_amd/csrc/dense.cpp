@@ -90,9 +90,11 @@ int check_grad_dtype(const char *what, int32_t t, int32_t dtype)
             return _rc;                \
     } while (0)
 
-size_t forward_ws(int64_t T, int64_t out, int planes)
+// A few tokens' weights are streamed, without a workspace, unless 16-bit rows of odd
+// length make that the slower way.
+size_t forward_ws(int64_t T, int64_t in, int64_t out, int dtype, int planes)
 {
-    return T <= kFewTokens ? 0 : dense_gemm_ws(T, out, planes);
+    return T <= kAlwaysFew && (dtype == ECF_F32 || in % 2 == 0) ? 0 : dense_gemm_ws(T, out, planes);
 }
 
 // Backward workspace: dz rows in `dtype` (gated: da and db halves of one row,
@@ -123,7 +125,7 @@ size_t ecf_gated_workspace_bytes(int32_t hidden, int32_t inter, int32_t dtype, i
 {
     if (check_common("ecf_gated_workspace_bytes", hidden, inter, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
-    return backward ? back_ws(inter, 2, dtype, n_tokens).total : forward_ws(n_tokens, inter, 2);
+    return backward ? back_ws(inter, 2, dtype, n_tokens).total : forward_ws(n_tokens, hidden, inter, dtype, 2);
 }
 
 int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
@@ -158,7 +160,7 @@ int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
             DENSE_TRY(check_matrix(me, "d_a", a->d_a, g.ldsave, I, a->dtype));
             DENSE_TRY(check_matrix(me, "d_b", a->d_b, g.ldsave, I, a->dtype));
         }
-        const size_t need = forward_ws(T, I, 2);
+        const size_t need = forward_ws(T, d, I, a->dtype, 2);
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, need));
         g.a[0] = a->d_x;
         g.b[0] = a->d_w_gate, g.b[1] = a->d_w_up;
@@ -253,7 +255,7 @@ size_t ecf_linear_workspace_bytes(int32_t in_features, int32_t out_features, int
     if (check_common("ecf_linear_workspace_bytes", in_features, out_features, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
     return backward ? back_ws(out_features, 1, dtype, n_tokens).total
-                    : forward_ws(n_tokens, out_features, 1);
+                    : forward_ws(n_tokens, in_features, out_features, dtype, 1);
 }
 
 int ecf_linear_forward(const ecf_linear_args *a, int32_t T)
@@ -284,7 +286,7 @@ int ecf_linear_forward(const ecf_linear_args *a, int32_t T)
             DENSE_TRY(check_matrix(me, "d_residual", a->d_residual, g.ldres, N, a->out_dtype));
         if (a->d_z)
             DENSE_TRY(check_matrix(me, "d_z", a->d_z, g.ldsave, N, a->dtype));
-        const size_t need = forward_ws(T, N, 1);
+        const size_t need = forward_ws(T, K, N, a->dtype, 1);
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, need));
         g.a[0] = a->d_x, g.b[0] = a->d_w;
         g.bias[0] = a->d_bias;

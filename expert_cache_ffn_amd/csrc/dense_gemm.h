@@ -208,23 +208,23 @@ __device__ __forceinline__ int kswz(int k)
     return ROWS >= 128 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
 }
 
-// 8 fp32 values to three chunks of bf16 parts.  `odd` becomes NaN if one of the
-// values is infinite or NaN; their k-tile is stored again through split8_odd.
+// 8 fp32 values to three chunks of bf16 parts.  `odd` becomes infinite or NaN if one
+// of the values is (or is near 2^90); their k-tile is stored again through split8_odd.
 __device__ __forceinline__ void split8(const u32x4_t v[2], u32x4_t part[3], float &odd)
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const uint32_t u0 = v[j >> 1][2 * (j & 1)], u1 = v[j >> 1][2 * (j & 1) + 1];
         const float x0 = __uint_as_float(u0), x1 = __uint_as_float(u1);
-        odd = __builtin_fmaf(x0, 0.f, odd);
-        odd = __builtin_fmaf(x1, 0.f, odd);
         part[0][j] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);  // the upper halves
         const float r0 = x0 - __uint_as_float(u0 & 0xffff0000u), r1 = x1 - __uint_as_float(u1 & 0xffff0000u);
         const bf16x2_t m = {(__bf16)r0, (__bf16)r1};
         const uint32_t mw = __builtin_bit_cast(uint32_t, m);
         part[1][j] = mw;
         // at most 8 bits are left: their upper half is all of them
-        part[2][j] = __builtin_amdgcn_perm(__float_as_uint(r1 - bf_hi(mw)), __float_as_uint(r0 - bf_lo(mw)), 0x07060302u);
+        const float l0 = r0 - bf_lo(mw), l1 = r1 - bf_hi(mw);
+        part[2][j] = __builtin_amdgcn_perm(__float_as_uint(l1), __float_as_uint(l0), 0x07060302u);
+        odd = __builtin_fmaf(l0, l1, odd);  // what is left of an infinity or NaN is NaN
     }
 }
 
@@ -555,7 +555,7 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
     };
     auto put_again = [&](int stage, auto set) __attribute__((always_inline)) {
         constexpr int S = decltype(set)::value;
-        if (ta.template edge<S>() || tb.template edge<S>() || (NP == 3 && odd != odd)) {
+        if (ta.template edge<S>() || tb.template edge<S>() || (NP == 3 && !(fabsf(odd) < __builtin_huge_valf()))) {
             ta.template store_again<S>(lds + stage * (SA + SB), tid);
             tb.template store_again<S>(lds + stage * (SA + SB) + SA, tid);
             odd = 0.f;

@@ -39,8 +39,11 @@ int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st);
 // The products of a backward pass, dx (n-contiguous B) and dW (m- and n-contiguous;
 // either may be null), in one launch or two.  ws: kDensePartialBytes.
 int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, void *ws, hipStream_t st);
-// Forward products of at most kFewTokens rows (k_dense_few.hip) need no workspace.
-constexpr int kFewTokens = 16;
+// x W^T of at most kFewTokens rows as a stream of the weights (k_dense_few.hip), and
+// the time estimated for it.  It needs no workspace; up to kAlwaysFew rows it is the
+// choice whenever there is none.
+constexpr int kFewTokens = 64, kAlwaysFew = 16;
+double dense_few_us(const DenseGemm &g, int cus);
 int launch_dense_few(const DenseGemm &g, int cus, hipStream_t st);
 // The largest workspace of any product with up to M x N outputs in each plane.
 constexpr size_t kDensePartialBytes = (size_t)32 << 20;  // fp32 sums of split products

@@ -273,7 +273,7 @@ double partial_bytes(const DenseGemm &g, int splits)
 {
     return (double)splits * (g.gated ? 2 : g.mhalves) * g.M * ((g.N + 7) / 8 * 8) * 4;
 }
-double join_us(const DenseGemm &g, int splits) { return splits > 1 ? 4.0 + partial_bytes(g, splits) * 2 / 4e6 : 0.0; }
+double join_us(const DenseGemm &g, int splits) { return splits > 1 ? 2.5 + partial_bytes(g, splits) * 2 / 5e6 : 0.0; }
 bool may_split(const DenseGemm &g, int splits, size_t room)
 {
     return splits == 1 || (ktiles(g) / splits >= 2 && partial_bytes(g, splits) <= (double)room);
@@ -367,9 +367,12 @@ int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st)
     const int rc = cu_count(&cus);
     if (rc != ECF_OK)
         return rc;
-    if (!g.a_t && !g.b_t && g.M <= kFewTokens)
+    const bool few = !g.a_t && !g.b_t && g.M <= kFewTokens;
+    if (few && !ws && g.M <= kAlwaysFew)
         return launch_dense_few(g, cus, st);
     if (short_rows(g)) {
+        if (few)
+            return launch_dense_few(g, cus, st);
         const int tiles_n = (g.N + TN - 1) / TN;
         const dim3 grid((unsigned)tiles_n * ((g.M + TM - 1) / TM) * g.mhalves);
         auto go = [&](auto e) {
@@ -390,6 +393,8 @@ int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st)
     }
     double us;
     const DensePlan plan = plan_gemm(g, cus, ws ? kDensePartialBytes : 0, &us);
+    if (few && dense_few_us(g, cus) <= us)
+        return launch_dense_few(g, cus, st);
     const DenseGrid gr = grid_of(g, tiles_of(g.dtype, plan.dma)[plan.tile], plan.splits, ws);
     return g.gated ? launch_gemm_gated(g, plan, gr, st)
            : g.a_t ? launch_gemm_tn(g, plan, gr, st)

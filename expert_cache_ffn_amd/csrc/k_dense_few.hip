@@ -1,4 +1,4 @@
-// Dense operators for few tokens (at most 16): x W^T, gated or not, as a streaming
+// Dense operators for few tokens (at most 64): x W^T, gated or not, as a streaming
 // read of the weights.  Bound by HBM: every weight byte is read once, straight
 // into MFMA operand registers.
 //
@@ -38,6 +38,15 @@ __device__ __forceinline__ f32x4a mfma_chunk(u32x4_t a, u32x4_t b, f32x4a c)
             c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[j]), __uint_as_float(b[j]), c, 0, 0, 0);
         return c;
     }
+}
+
+template <class E>
+__device__ __forceinline__ u32x4_t load_chunk(const typename E::raw *p)
+{
+    if constexpr (sizeof(typename E::raw) == 2)
+        return ((const any128x2 *)p)->v;
+    else
+        return __builtin_bit_cast(u32x4_t, ((const any128x4 *)p)->v);
 }
 
 // Chunk `ch` (16 bytes) of a row of K elements, zeros past its end.
@@ -108,26 +117,56 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_dense_few(DenseGemm g)
 #pragma unroll
         for (int t = 0; t < TG; ++t)
             acc[h][t] = f32x4a{0.f, 0.f, 0.f, 0.f};
-    for (int s = s0; s < s1; s += U) {
-        u32x4_t wv[U][H], xv[U][TG];
+    // Whole steps: every chunk lies inside its row, so no load sits behind a branch
+    // (at the branch's end the compiler would wait for it).
+    const int whole = min(s1, g.K / (EPC * 4 * P)), at = (place * 4 + kg) * EPC;
+    const typename E::raw *wq[H], *xq[TG];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            // past the wave's last step: past the row's end, zeros
-            const int ch = s + u < s1 ? (s + u) * 4 * P + place * 4 + kg : g.K / EPC + 1;
+    for (int h = 0; h < H; ++h)
+        wq[h] = wp[h] + at;
+#pragma unroll
+    for (int t = 0; t < TG; ++t)
+        xq[t] = xp[t] + at;
+    auto steps_at = [&](int s, auto n) __attribute__((always_inline)) {
+        constexpr int NU = decltype(n)::value;
+        u32x4_t wv[NU][H], xv[NU][TG];
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            const int64_t o = (int64_t)(s + u) * (EPC * 4 * P);
 #pragma unroll
             for (int h = 0; h < H; ++h)
-                wv[u][h] = chunk_of<E>(wp[h], ch, g.K);
+                wv[u][h] = load_chunk<E>(wq[h] + o);
 #pragma unroll
             for (int t = 0; t < TG; ++t)
-                xv[u][t] = chunk_of<E>(xp[t], ch, g.K);
+                xv[u][t] = load_chunk<E>(xq[t] + o);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < NU; ++u)
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
                 for (int t = 0; t < TG; ++t)
                     acc[h][t] = mfma_chunk<E>(wv[u][h], xv[u][t], acc[h][t]);
+    };
+    int s = s0;
+    for (; s + U <= whole; s += U)
+        steps_at(s, std::integral_constant<int, U>{});
+    for (; s < whole; ++s)
+        steps_at(s, std::integral_constant<int, 1>{});
+    if (s < s1) {  // the row's last, partial step
+        const int ch = s * 4 * P + place * 4 + kg;
+        u32x4_t wv[H], xv[TG];
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            wv[h] = chunk_of<E>(wp[h], ch, g.K);
+#pragma unroll
+        for (int t = 0; t < TG; ++t)
+            xv[t] = chunk_of<E>(xp[t], ch, g.K);
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int t = 0; t < TG; ++t)
+                acc[h][t] = mfma_chunk<E>(wv[h], xv[t], acc[h][t]);
     }
     // a lane holds rows 4 kg .. 4 kg + 3 of column r: keep those whose place is the column's
 #pragma unroll
@@ -175,15 +214,35 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_dense_few(DenseGemm g)
     }
 }
 
+// Rows per block (4, 8 or 16; at most four groups of tokens) with the least time, and
+// that time in us.  A CU takes in about 38 KB/us of weights and x together, whatever
+// it is (4096 x 4096 bf16: 8 tokens 9.9 us, 64 tokens 21 us; 1024 x 4096: 4.4 and 7.6),
+// and 16 KB/us where 16-bit rows start at odd elements, whose loads the hardware
+// splits (7353 x 2048 bf16, 8 tokens: 20.8 us).
+int few_rows(const DenseGemm &g, int cus, double *us)
+{
+    const int es = (int)dense_esize(g.dtype), h = g.gated ? 2 : 1;
+    const bool odd = es == 2 && (g.lda % 2 || g.ldb % 2 || ((uintptr_t)g.a[0] | (uintptr_t)g.b[0]) % 4);
+    int best = 16;
+    *us = 1e300;
+    for (int rt = 4; rt <= 16; rt *= 2) {
+        const int64_t blocks = (g.N + rt - 1) / rt, tokens = (g.M + rt - 1) / rt * rt;
+        if (tokens > 4 * rt)
+            continue;
+        const double t = 2.5 + (double)((blocks + cus - 1) / cus) * (rt * h + tokens) * g.K * es / (odd ? 16e3 : 38e3);
+        if (t < *us) {
+            *us = t;
+            best = rt;
+        }
+    }
+    return best;
+}
+
 template <class E, bool GATED>
 void run_few(const DenseGemm &g, int cus, hipStream_t st)
 {
-    // The widest tile that still gives every CU two blocks, for the fewest reads of x;
-    // one block where that spares token groups, each of which costs its MFMAs again
-    // (fp32, 5 tokens, 3312 x 3648 gated: 36 us as two groups of 4)
-    int rt = g.N >= 16 * 2 * cus ? 16 : g.N >= 8 * 2 * cus ? 8 : 4;
-    while (rt < 16 && g.M > rt && g.N >= 2 * rt * cus)
-        rt *= 2;
+    double us;
+    const int rt = few_rows(g, cus, &us);
     const int groups = (g.M + rt - 1) / rt;
     const int epc = 16 / (int)sizeof(typename E::raw);
     const int steps = (g.K + epc * 64 / rt - 1) / (epc * 64 / rt);
@@ -191,12 +250,19 @@ void run_few(const DenseGemm &g, int cus, hipStream_t st)
     const dim3 grid((g.N + rt - 1) / rt), block(64 * waves);
 #define ECF_FEW(R, G) hipLaunchKernelGGL((k_dense_few<E, GATED, R, G>), grid, block, 0, st, g)
     if (rt == 16) {
-        ECF_FEW(16, 1);
+        if (groups == 1)
+            ECF_FEW(16, 1);
+        else if (groups == 2)
+            ECF_FEW(16, 2);
+        else
+            ECF_FEW(16, 4);
     } else if (rt == 8) {
         if (groups == 1)
             ECF_FEW(8, 1);
-        else
+        else if (groups == 2)
             ECF_FEW(8, 2);
+        else
+            ECF_FEW(8, 4);
     } else {
         if (groups == 1)
             ECF_FEW(4, 1);
@@ -209,6 +275,13 @@ void run_few(const DenseGemm &g, int cus, hipStream_t st)
 }
 
 }  // namespace
+
+double dense_few_us(const DenseGemm &g, int cus)
+{
+    double us;
+    few_rows(g, cus, &us);
+    return us;
+}
 
 int launch_dense_few(const DenseGemm &g, int cus, hipStream_t st)
 {
