@@ -456,7 +456,7 @@ template <class E, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE>
 constexpr int gemm_lds_bytes()
 {
     constexpr int in = (DMA ? NSTAGE : 2) * (BM + BN) * BK * 2 * (sizeof(typename E::raw) == 4 ? 3 : 1);
-    constexpr int out = WM * WN * 32 * ((BN / WN >= 64 ? 64 : 32) + 4) * 4;
+    constexpr int out = WM * WN * 32 * (64 + 4) * 4;
     return in > out ? in : out;
 }
 
@@ -468,11 +468,12 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
     constexpr int NW = WM * WN, NTH = 64 * NW, RM = BM / WM, RN = BN / WN, FM = RM / 32, FN = RN / 32;
     static_assert(BK % 32 == 0, "two sets of fragments take turns");
     static_assert(DMA || NSTAGE <= 2, "one or two register sets");
-    static_assert(FM >= 1 && FN >= 1 && (!GATED || (FN % 2 == 0 && !BT)), "wave tile");
+    static_assert(FM >= 1 && (FN == 1 || FN % 2 == 0) && (!GATED || (!BT && WN * FN % 2 == 0)), "wave tile");
     constexpr int NS = DMA ? NSTAGE : 2, SETS = DMA ? 1 : NSTAGE;
     constexpr int ES = sizeof(typename E::raw), NP = ES == 4 ? 3 : 1;      // planes of parts
     constexpr int PA = BM * BK * 2, PB = BN * BK * 2, SA = PA * NP, SB = PB * NP;  // bytes per plane and stage
-    constexpr int PITCH = (FN >= 2 ? 64 : 32) + 4;  // fp32 per row of the output staging
+    constexpr bool MATES = GATED && FN == 1;  // a wave has the gate or the up columns only, its neighbour the others
+    constexpr int PITCH = (FN >= 2 || GATED ? 64 : 32) + 4;  // fp32 per row of the output staging
 
     int split, half, mt, nt;
     gr.locate(block, split, half, mt, nt);
@@ -692,7 +693,10 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
     // unrolled, see the figures at the launcher for the loop).
     constexpr int CB = FN >= 2 ? 2 : 1, GROUPS = FM * (FN / CB);
     constexpr int LPR = (GATED ? 32 : 32 * CB) / 8;  // lanes per output row
-    float *eb = (float *)lds + wave * 32 * PITCH;
+    // (two waves that hold the two projections of the same columns share a buffer,
+    // and take half its rows each)
+    float *eb = (float *)lds + (MATES ? wave / 2 : wave) * 32 * PITCH;
+    const int ecol = MATES ? (wn & 1) * 32 : 0, erow = MATES ? (wn & 1) * 16 : 0;
     const bool partial = gr.splits > 1;
 #pragma unroll 1
     for (int grp = 0; grp < GROUPS; ++grp) {
@@ -704,15 +708,17 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
                 for (int j = 0; j < CB; ++j)
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        eb[((e >> 2) * 8 + (lane >> 5) * 4 + (e & 3)) * PITCH + j * 32 + (lane & 31)] =
+                        eb[((e >> 2) * 8 + (lane >> 5) * 4 + (e & 3)) * PITCH + ecol + j * 32 + (lane & 31)] =
                             acc[i / (FN / CB)][i % (FN / CB) * CB + j][e];
             }
         asm volatile("" ::: "memory");
+        if constexpr (MATES)
+            __syncthreads();
         const int r0 = wm * RM + grp / (FN / CB) * 32;
-        const int c0 = GATED ? (wn * RN + grp % (FN / CB) * 64) / 2 : wn * RN + grp % (FN / CB) * 64;
+        const int c0 = MATES ? wn / 2 * 32 : GATED ? (wn * RN + grp % (FN / CB) * 64) / 2 : wn * RN + grp % (FN / CB) * 64;
 #pragma unroll 1
-        for (int p = 0; p < 32 * LPR / 64; ++p) {
-            const int r = p * (64 / LPR) + lane / LPR, c = (lane % LPR) * 8;
+        for (int p = 0; p < (MATES ? 1 : 32 * LPR / 64); ++p) {
+            const int r = erow + p * (64 / LPR) + lane / LPR, c = (lane % LPR) * 8;
             const int64_t m = m0 + r0 + r;
             const int n = n0 + c0 + c;
             float z[GATED ? 2 : 1][8];
@@ -734,6 +740,8 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
                     store8<F32>(gr.partial, gr.partial_at(g, split, GATED ? q : half, m) + n, 8, z[q]);
             }
         }
+        if constexpr (MATES)
+            __syncthreads();
     }
 }
 

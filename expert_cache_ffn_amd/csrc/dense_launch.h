@@ -24,16 +24,18 @@ int pick_gemm(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipSt
 {
     // the order of the launcher's tables
     if constexpr (std::is_same<E, F32>::value) {
-        if (p.tile == 0)
-            launch_gemm<E, AT, BT, GATED, false, 128, 128, 4, 2, 32, 1>(g, gr, st);
-        else
-            launch_gemm<E, AT, BT, GATED, false, 64, 128, 2, 2, 32, 2>(g, gr, st);
+        switch (p.tile) {
+        case 0: launch_gemm<E, AT, BT, GATED, false, 128, 128, 4, 2, 32, 1>(g, gr, st); break;
+        case 1: launch_gemm<E, AT, BT, GATED, false, 64, 128, 2, 4, 64, 1>(g, gr, st); break;
+        default: launch_gemm<E, AT, BT, GATED, false, 64, 64, 2, 2, 64, 1>(g, gr, st); break;
+        }
     } else {
         switch (p.tile) {
         case 0: launch_gemm<E, AT, BT, GATED, DMA, 256, 256, 2, 4, 64, DMA ? 2 : 1>(g, gr, st); break;
         case 1: launch_gemm<E, AT, BT, GATED, DMA, 128, 256, 2, 4, 64, DMA ? 3 : 2>(g, gr, st); break;
         case 2: launch_gemm<E, AT, BT, GATED, DMA, 128, 128, 2, 2, 64, DMA ? 2 : 1>(g, gr, st); break;
-        default: launch_gemm<E, AT, BT, GATED, DMA, 64, 128, 2, 2, 64, DMA ? 3 : 2>(g, gr, st); break;
+        case 3: launch_gemm<E, AT, BT, GATED, DMA, 64, 128, 2, 2, 64, DMA ? 3 : 2>(g, gr, st); break;
+        default: launch_gemm<E, AT, BT, GATED, DMA, 64, 64, 2, 2, 64, DMA ? 3 : 1>(g, gr, st); break;
         }
     }
     if (gr.splits > 1)
@@ -55,15 +57,17 @@ int pick_pair(const DenseGemm &gx, const DenseGrid &grx, const DenseGemm &gw, co
               hipStream_t st)
 {
     if constexpr (std::is_same<E, F32>::value) {
-        if (p.tile == 0)
-            launch_pair<E, false, 128, 128, 4, 2, 32, 1>(gx, grx, gw, grw, st);
-        else
-            launch_pair<E, false, 64, 128, 2, 2, 32, 2>(gx, grx, gw, grw, st);
+        switch (p.tile) {
+        case 0: launch_pair<E, false, 128, 128, 4, 2, 32, 1>(gx, grx, gw, grw, st); break;
+        case 1: launch_pair<E, false, 64, 128, 2, 4, 64, 1>(gx, grx, gw, grw, st); break;
+        default: launch_pair<E, false, 64, 64, 2, 2, 64, 1>(gx, grx, gw, grw, st); break;
+        }
     } else {
-        if (p.tile == 2)
-            launch_pair<E, DMA, 128, 128, 2, 2, 64, DMA ? 2 : 1>(gx, grx, gw, grw, st);
-        else
-            launch_pair<E, DMA, 64, 128, 2, 2, 64, DMA ? 3 : 2>(gx, grx, gw, grw, st);
+        switch (p.tile) {
+        case 2: launch_pair<E, DMA, 128, 128, 2, 2, 64, DMA ? 2 : 1>(gx, grx, gw, grw, st); break;
+        case 3: launch_pair<E, DMA, 64, 128, 2, 2, 64, DMA ? 3 : 2>(gx, grx, gw, grw, st); break;
+        default: launch_pair<E, DMA, 64, 64, 2, 2, 64, DMA ? 3 : 1>(gx, grx, gw, grw, st); break;
+        }
     }
     if (grx.splits > 1)
         launch_join<E, false>(gx, grx, st);

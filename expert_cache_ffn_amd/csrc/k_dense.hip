@@ -211,10 +211,12 @@ struct TileCost {
     double us, us1, fixed;
 };
 const TileCost kTilesDma[] = {{256, 256, 1, 1.78, 1.78, 8.0}, {128, 256, 1, 0.98, 0.98, 6.0},
-                              {128, 128, 2, 1.05, 0.68, 5.0}, {64, 128, 2, 0.64, 0.40, 4.0}};
+                              {128, 128, 2, 1.05, 0.68, 5.0}, {64, 128, 2, 0.66, 0.41, 4.0},
+                              {64, 64, 2, 0.45, 0.31, 3.5}};
 const TileCost kTilesReg[] = {{256, 256, 1, 1.92, 1.92, 8.0}, {128, 256, 1, 1.14, 1.14, 6.0},
-                              {128, 128, 2, 1.24, 0.85, 5.0}, {64, 128, 2, 0.83, 0.70, 4.0}};
-const TileCost kTilesF32[] = {{128, 128, 1, 2.85, 2.85, 5.0}, {64, 128, 2, 3.30, 1.95, 4.0}};
+                              {128, 128, 2, 1.25, 0.81, 5.0}, {64, 128, 2, 0.88, 0.69, 4.0},
+                              {64, 64, 2, 0.64, 0.57, 3.5}};
+const TileCost kTilesF32[] = {{128, 128, 1, 2.90, 2.90, 5.0}, {64, 128, 1, 1.75, 1.75, 4.0}, {64, 64, 1, 1.22, 1.22, 3.5}};
 constexpr int kShortK = 32;
 
 const TileCost *tiles_of(int dtype, bool dma) { return dtype == ECF_F32 ? kTilesF32 : dma ? kTilesDma : kTilesReg; }
@@ -284,7 +286,7 @@ bool may_split(const DenseGemm &g, int splits, size_t room)
 DensePlan plan_gemm(const DenseGemm &g, int cus, size_t room, double *us_out)
 {
     DensePlan best{0, 1, dma_ok(g)};
-    const int n_tiles = g.dtype == ECF_F32 ? 2 : 4, kt = ktiles(g);
+    const int n_tiles = g.dtype == ECF_F32 ? 3 : 5, kt = ktiles(g);
     const TileCost *tiles = tiles_of(g.dtype, best.dma);
     *us_out = 1e300;
     for (int t = 0; t < n_tiles; ++t) {
@@ -305,8 +307,33 @@ DensePlan plan_gemm(const DenseGemm &g, int cus, size_t room, double *us_out)
     return best;
 }
 
-// The same for two products in one launch: the work of all blocks over all CUs,
-// but no less than the longest block's.
+// When the last of n1 blocks of k1 k-tiles and, behind them, n2 of k2 (k1 >= k2) is
+// done, on `slots` slots that each take the next block when they are free.
+double makespan(int64_t n1, double k1, int64_t n2, double k2, int64_t slots)
+{
+    const int64_t left = n1 % slots;  // slots that start one more long block at t0
+    const double t0 = (double)(n1 / slots) * k1;
+    double t = left ? t0 + k1 : t0;
+    if (n2 == 0)
+        return t;
+    // the others go on with short blocks at t0, those `left` at t0 + k1
+    int64_t early = 0, late = 0;
+    while (early * (slots - left) + late * left < n2) {
+        const double next_early = t0 + (double)(early + 1) * k2, next_late = t0 + k1 + (double)(late + 1) * k2;
+        if (left == 0 || (left < slots && next_early <= next_late)) {
+            ++early;
+            t = std::max(t, next_early);
+        } else {
+            ++late;
+            t = std::max(t, next_late);
+        }
+        if (early + late > 64)  // many rounds: the work over all slots says it well enough
+            return std::max(t, ((double)n1 * k1 + (double)n2 * k2) / (double)slots);
+    }
+    return t;
+}
+
+// The same for two products in one launch.
 struct PairPlan {
     DensePlan x;
     int splits_w;
@@ -317,17 +344,16 @@ PairPlan plan_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t roo
     const bool f32 = gx.dtype == ECF_F32;
     const TileCost *tiles = tiles_of(gx.dtype, best.x.dma);
     *us_out = 1e300;
-    for (int t = f32 ? 0 : 2; t < (f32 ? 2 : 4); ++t) {
+    for (int t = f32 ? 0 : 2; t < (f32 ? 3 : 5); ++t) {
         const TileCost &c = tiles[t];
         const int64_t slots = (int64_t)cus * c.per_cu;
         for (int sx = 1; sx <= kMaxSplits && may_split(gx, sx, room); sx *= 2)
             for (int sw = 1; sw <= kMaxSplits && may_split(gw, sw, room); sw *= 2) {
                 const int64_t bx = out_tiles(gx, c) * sx, bw = out_tiles(gw, c) * sw;
                 const double kx = (ktiles(gx) + sx - 1) / sx, kw = (ktiles(gw) + sw - 1) / sw;
-                const double full = ((double)bx * kx + (double)bw * kw) * c.us / slots;
-                const double longest = std::max(kx, kw) * (bx + bw <= cus ? c.us1 : c.us);
-                const double us = std::max(full, longest) + (double)((bx + bw + slots - 1) / slots) * c.fixed +
-                                  join_us(gx, sx) + join_us(gw, sw);
+                const double walk = kx >= kw ? makespan(bx, kx, bw, kw, slots) : makespan(bw, kw, bx, kx, slots);
+                const double us = walk * (bx + bw <= cus ? c.us1 : c.us) +
+                                  (double)((bx + bw + slots - 1) / slots) * c.fixed + join_us(gx, sx) + join_us(gw, sw);
                 if (us < *us_out) {
                     *us_out = us;
                     best.x.tile = t;
