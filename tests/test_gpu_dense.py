@@ -408,3 +408,105 @@ def test_another_device_is_refused_or_served():
         want = Linear(w).forward(x)
         with torch.cuda.device(1):
             assert torch.equal(Linear(w).forward(x), want)
+
+
+def big(seed, *shape, std=1.0, dtype=torch.float32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+# sizes at which a call takes the larger tiles, splits its reduction, streams the weights or joins its
+# two backward products, with widths on and off the 16-byte chunks and the tiles
+LARGE = [(4096, 1024, 2048), (2048, 4096, 4096), (1500, 2000, 1800), (1501, 1999, 1803), (700, 4096, 1030),
+         (40, 4096, 1024), (64, 512, 768), (24, 1023, 1531), (12, 5001, 640), (9, 2048, 8200), (150, 7000, 260),
+         (5000, 130, 96), (3001, 70, 1210), (18, 8192, 4112), (333, 1200, 5000)]
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,K,N", LARGE)
+def test_larger_linear(T, K, N, dt):
+    say(f"case: larger linear T {T} K {K} N {N} {dt}")
+    dtype = DT[dt]
+    x, w = big(1, T, K, dtype=dtype), big(2, N, K, std=K ** -.5, dtype=dtype)
+    bias, residual = big(4, N, dtype=dtype), big(5, T, N, dtype=dtype)
+    layer = Linear(w, bias, act="silu")
+    ref = R.linear_forward(*d64(x, w, bias), "silu", residual.double(), dtype, dtype)
+    y, z = layer.forward(x, residual=residual, save=True)
+    R.check("z", z, ref["z"])
+    R.check("y", y, ref["y"])
+    assert torch.equal(layer.forward(x, residual=residual), y)
+    del ref
+    dout = big(8, T, N, std=0.1, dtype=dtype)
+    ref = R.linear_backward(*d64(x, w, z, dout), "silu", dtype, dtype, dtype)
+    outs = layer.backward(x, dout, z=z)
+    for name, got in zip(("dx", "dw", "dbias"), outs):
+        R.check(name, got, ref[name])
+    assert all(torch.equal(p, q) for p, q in zip(outs, layer.backward(x, dout, z=z))), "two calls differ"
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,d,I", LARGE)
+def test_larger_gated(T, d, I, dt):
+    say(f"case: larger gated T {T} d {d} I {I} {dt}")
+    dtype = DT[dt]
+    x, wg, wu = big(1, T, d, dtype=dtype), big(2, I, d, std=d ** -.5, dtype=dtype), big(3, I, d, std=d ** -.5, dtype=dtype)
+    bg, bu = big(4, I, dtype=dtype), big(5, I, dtype=dtype)
+    layer = GatedProjection(wg, wu, bg, bu, act="gelu")
+    ref = R.gated_forward(*d64(x, wg, wu, bg, bu), "gelu", dtype)
+    h, a, b = layer.forward(x, save=True)
+    for name, got in (("h", h), ("a", a), ("b", b)):
+        R.check(name, got, ref[name])
+    assert torch.equal(layer.forward(x), h)
+    del ref
+    dh = big(8, T, I, std=0.1, dtype=dtype)
+    ref = R.gated_backward(*d64(x, wg, wu, a, b, dh), "gelu", dtype, dtype)
+    outs = layer.backward(x, a, b, dh)
+    for name, got in zip(("dx", "dw_gate", "dw_up", "db_gate", "db_up"), outs):
+        R.check(name, got, ref[name])
+    assert all(torch.equal(p, q) for p, q in zip(outs, layer.backward(x, a, b, dh))), "two calls differ"
+
+
+@pytest.mark.parametrize("T", [1, 3, 40, 300, 2000])
+def test_fp32_magnitudes(T):
+    """fp32 products over the whole range of exponents: near the largest values,
+    far below bf16's rounding of them, and mixed within one sum."""
+    say(f"case: fp32 magnitudes T {T}")
+    K, N = 200, 150
+    for scale_x, scale_w in ((1e30, 1e-30), (3e37, 1e-3), (1e-25, 1e20), (1e-36, 1.0)):
+        x, w = rand(1, T, K) * scale_x, rand(2, N, K) * scale_w
+        y = Linear(w).forward(x)
+        ref, err = R.product(x.double(), w.double())
+        R.check("y", y, (ref, err + R.half_step(ref, torch.float32) + K * 2.0 ** -134 * float(w.abs().max())))
+    # rows of x of very different sizes stay apart
+    x = rand(1, T, K) * torch.logspace(-30, 30, T, device="cuda")[:, None]
+    w = rand(2, N, K)
+    ref, err = R.product(x.double(), w.double())
+    R.check("y", Linear(w).forward(x), (ref, err + R.half_step(ref, torch.float32)))
+
+
+def test_out_of_place_partial_gradients():
+    """The C entry points compute only what is asked for, and the same bits."""
+    T, d, I = 100, 136, 72
+    dt = torch.bfloat16
+    x, wg, wu = rand(1, T, d, dtype=dt), rand(2, I, d, std=.1, dtype=dt), rand(3, I, d, std=.1, dtype=dt)
+    a, b, dh, bias = rand(6, T, I, dtype=dt), rand(7, T, I, dtype=dt), rand(8, T, I, std=.1, dtype=dt), rand(4, I, dtype=dt)
+    full = GatedProjection(wg, wu, bias, bias).backward(x, a, b, dh)
+    ws = torch.empty(ecf.ecf_gated_workspace_bytes(d, I, ecf.ECF_BF16, T, True), dtype=torch.uint8, device="cuda")
+    for want in (("dx",), ("dw",), ("db_up",), ("dx", "db_gate")):
+        q = ecf.GatedArgs()
+        q.hidden, q.inter, q.dtype, q.wgrad_dtype, q.act = d, I, ecf.ECF_BF16, ecf.ECF_BF16, ecf.ECF_ACT_SILU
+        q.d_x, q.d_w_gate, q.d_w_up, q.d_a, q.d_b, q.d_dh = (t.data_ptr() for t in (x, wg, wu, a, b, dh))
+        q.d_ws, q.ws_bytes = ws.data_ptr(), ws.numel()
+        got = {k: torch.full_like(t, float("nan")) for k, t in zip(("dx", "dw_gate", "dw_up", "db_gate", "db_up"), full)}
+        for k in want:
+            for f in (("dw_gate", "dw_up") if k == "dw" else (k,)):
+                setattr(q, "d_" + f, got[f].data_ptr())
+        ecf.ecf_gated_backward(q, T)
+        torch.cuda.synchronize()
+        for k, t in zip(("dx", "dw_gate", "dw_up", "db_gate", "db_up"), full):
+            asked = k in want or ("dw" in want and k.startswith("dw"))
+            if asked:
+                # another choice of tiles may add in another order: both are within the bound of one rounding
+                R.check(k, got[k], (t.double(), 2 * R.half_step(t.double(), dt) + 1e-4))
+            if not asked:
+                assert got[k].isnan().all(), k
