@@ -230,11 +230,12 @@ class GatedProjection(_Dense):
         self._run(L.ecf_gated_forward, a, T, 0)
         return (h, sa, sb) if save else h
 
-    def backward(self, x, a, b, dh, w_grad_dtype=None, dx=None):
+    def backward(self, x, a, b, dh, w_grad_dtype=None, dx=None, need_dx=True, need_dw=True):
         """(dx, dw_gate, dw_up, db_gate, db_up) for the gradient dh of h, from the x
         of the forward call and the a and b it saved; the last two are None without
-        the biases.  Weight and bias gradients come in w_grad_dtype (the weights'
-        type, or torch.float32)."""
+        the biases, dx without need_dx (the network's first layer), the other four
+        without need_dw (frozen weights).  Weight and bias gradients come in
+        w_grad_dtype (the weights' type, or torch.float32)."""
         T, gd = self._tokens(x), self._wgrad(w_grad_dtype)
         q = L.GatedArgs.from_buffer_copy(self._a)
         q.wgrad_dtype = _DENSE_DT[gd]
@@ -244,16 +245,20 @@ class GatedProjection(_Dense):
         if ld != q.ld_ab:
             raise ValueError(f"a and b must have the same row stride ({q.ld_ab} and {ld})")
         q.d_dh, q.ld_dh = _matrix("dh", dh, T, self.inter, self.dtype, self.device)
-        dx, q.d_dx, q.ld_dx = self._out("dx", dx, T, self.hidden, self.dtype)
-        dwg, q.d_dw_gate, q.ld_dw = self._out("dw_gate", None, self.inter, self.hidden, gd)
-        dwu, q.d_dw_up, _ = self._out("dw_up", None, self.inter, self.hidden, gd)
-        dbg = dbu = None
-        if self.b_gate is not None:
-            dbg = torch.empty(self.inter, dtype=gd, device=self.device)
-            q.d_db_gate = dbg.data_ptr()
-        if self.b_up is not None:
-            dbu = torch.empty(self.inter, dtype=gd, device=self.device)
-            q.d_db_up = dbu.data_ptr()
+        dwg = dwu = dbg = dbu = None
+        if need_dx:
+            dx, q.d_dx, q.ld_dx = self._out("dx", dx, T, self.hidden, self.dtype)
+        elif dx is not None:
+            raise ValueError("dx is given but need_dx is false")
+        if need_dw:
+            dwg, q.d_dw_gate, q.ld_dw = self._out("dw_gate", None, self.inter, self.hidden, gd)
+            dwu, q.d_dw_up, _ = self._out("dw_up", None, self.inter, self.hidden, gd)
+            if self.b_gate is not None:
+                dbg = torch.empty(self.inter, dtype=gd, device=self.device)
+                q.d_db_gate = dbg.data_ptr()
+            if self.b_up is not None:
+                dbu = torch.empty(self.inter, dtype=gd, device=self.device)
+                q.d_db_up = dbu.data_ptr()
         self._run(L.ecf_gated_backward, q, T, 1)
         return dx, dwg, dwu, dbg, dbu
 
@@ -298,10 +303,11 @@ class Linear(_Dense):
         self._run(L.ecf_linear_forward, a, T, 0)
         return (y, z) if save else y
 
-    def backward(self, x, dout, z=None, w_grad_dtype=None, dx=None):
+    def backward(self, x, dout, z=None, w_grad_dtype=None, dx=None, need_dx=True, need_dw=True):
         """(dx, dw, dbias) for the gradient dout of y, from the x of the forward call
-        and, with an activation, the z it saved; dbias is None without a bias.  The
-        residual's gradient is dout itself."""
+        and, with an activation, the z it saved; dbias is None without a bias, dx
+        without need_dx, the other two without need_dw.  The residual's gradient is
+        dout itself."""
         T, gd = self._tokens(x), self._wgrad(w_grad_dtype)
         q = L.LinearArgs.from_buffer_copy(self._a)
         q.wgrad_dtype = _DENSE_DT[gd]
@@ -309,11 +315,15 @@ class Linear(_Dense):
         if self.act != "none":
             q.d_z, q.ld_z = _matrix("z", z, T, self.out_features, self.dtype, self.device)
         q.d_dout, q.ld_dout = _matrix("dout", dout, T, self.out_features, self.out_dtype, self.device)
-        dx, q.d_dx, q.ld_dx = self._out("dx", dx, T, self.in_features, self.dtype)
-        dw, q.d_dw, q.ld_dw = self._out("dw", None, self.out_features, self.in_features, gd)
-        db = None
-        if self.bias is not None:
-            db = torch.empty(self.out_features, dtype=gd, device=self.device)
-            q.d_dbias = db.data_ptr()
+        dw = db = None
+        if need_dx:
+            dx, q.d_dx, q.ld_dx = self._out("dx", dx, T, self.in_features, self.dtype)
+        elif dx is not None:
+            raise ValueError("dx is given but need_dx is false")
+        if need_dw:
+            dw, q.d_dw, q.ld_dw = self._out("dw", None, self.out_features, self.in_features, gd)
+            if self.bias is not None:
+                db = torch.empty(self.out_features, dtype=gd, device=self.device)
+                q.d_dbias = db.data_ptr()
         self._run(L.ecf_linear_backward, q, T, 1)
         return dx, dw, db

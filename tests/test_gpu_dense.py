@@ -510,3 +510,82 @@ def test_out_of_place_partial_gradients():
                 R.check(k, got[k], (t.double(), 2 * R.half_step(t.double(), dt) + 1e-4))
             if not asked:
                 assert got[k].isnan().all(), k
+
+
+# one product at a time, at sizes that between them take every tile on both paths to LDS
+ONE = [(4100, 2050, 4101), (4101, 1025, 4099), (1025, 1030, 2051), (600, 700, 1101), (300, 260, 521), (130, 100, 67),
+       (4096, 4096, 4096), (4096, 1024, 4096), (2048, 2048, 2048), (1024, 1024, 2048), (512, 768, 640), (136, 128, 64)]
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,K,N", ONE)
+def test_one_gradient_at_a_time(T, K, N, dt):
+    say(f"case: one gradient T {T} K {K} N {N} {dt}")
+    dtype = DT[dt]
+    x, w, dout = big(1, T, K, dtype=dtype), big(2, N, K, std=K ** -.5, dtype=dtype), big(8, T, N, std=.1, dtype=dtype)
+    bias = big(3, N, dtype=dtype)
+    layer = Linear(w, bias)
+    ref = R.linear_backward(*d64(x, w), None, dout.double(), "none", dtype, dtype, dtype)
+    dx, dw, db = layer.backward(x, dout, need_dw=False)
+    assert dw is None and db is None
+    R.check("dx", dx, ref["dx"])
+    dx, dw, db = layer.backward(x, dout, need_dx=False)
+    assert dx is None
+    R.check("dw", dw, ref["dw"])
+    R.check("dbias", db, ref["dbias"])
+    R.check("y", layer.forward(x), R.linear_forward(*d64(x, w, bias), "none", None, dtype, dtype)["y"])
+    if N * K * T < 1 << 34:
+        wu = big(4, N, K, std=K ** -.5, dtype=dtype)
+        g = GatedProjection(w, wu)
+        R.check("h", g.forward(x), R.gated_forward(*d64(x, w, wu), None, None, "silu", dtype)["h"])
+        a, b = big(5, T, N, dtype=dtype), big(6, T, N, dtype=dtype)
+        ref = R.gated_backward(*d64(x, w, wu, a, b, dout), "silu", dtype, dtype)
+        R.check("dx", g.backward(x, a, b, dout, need_dw=False)[0], ref["dx"])
+        outs = g.backward(x, a, b, dout, need_dx=False)
+        assert outs[0] is None
+        R.check("dw_gate", outs[1], ref["dw_gate"])
+        R.check("dw_up", outs[2], ref["dw_up"])
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,K,N", [(1, 1024, 4096), (6, 640, 1500), (12, 640, 1500), (14, 333, 2047), (20, 512, 3000), (30, 511, 2301),
+                                   (50, 384, 1000), (64, 200, 300), (7, 2049, 1201), (16, 4096, 96), (3, 16, 5000)])
+def test_few_tokens(T, K, N, dt):
+    """Every shape of the streaming kernel: rows per block, groups of tokens, odd rows."""
+    say(f"case: few tokens T {T} K {K} N {N} {dt}")
+    dtype = DT[dt]
+    x, w, wu = big(1, T, K, dtype=dtype), big(2, N, K, std=K ** -.5, dtype=dtype), big(4, N, K, std=K ** -.5, dtype=dtype)
+    bias, res = big(3, N, dtype=dtype), big(5, T, N)
+    layer = Linear(w, bias, act="gelu_tanh", out_dtype=torch.float32)
+    y, z = layer.forward(x, residual=res, save=True)
+    ref = R.linear_forward(*d64(x, w, bias), "gelu_tanh", res.double(), dtype, torch.float32)
+    R.check("y", y, ref["y"])
+    R.check("z", z, ref["z"])
+    h, a, b = GatedProjection(w, wu, None, bias, act="silu").forward(x, save=True)
+    ref = R.gated_forward(*d64(x, w, wu), None, bias.double(), "silu", dtype)
+    for name, got in (("h", h), ("a", a), ("b", b)):
+        R.check(name, got, ref[name])
+
+
+# M x N outputs over K, such that the estimates choose each tile in turn, with every width a multiple of 8
+# (operands straight to LDS) and odd (through registers)
+TILES = [(5264, 1584, 72), (136, 6416, 4088), (704, 6008, 72), (1296, 1744, 72), (72, 64, 80), (4736, 896, 72), (608, 3328, 72),
+         (160, 5720, 72), (1055, 7703, 71), (3275, 263, 2407), (6957, 519, 75), (3195, 647, 71), (99, 71, 65), (1659, 2703, 67),
+         (1111, 1819, 67), (5705, 171, 71), (6321, 71, 2661)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", TILES)
+def test_every_tile(M, N, K, dt):
+    """One product shape in each place it can have: x W^T, gated, dz W and dz^T x."""
+    say(f"case: tiles M {M} N {N} K {K} {dt}")
+    dtype = DT[dt]
+    a, b, b2 = big(1, M, K, dtype=dtype), big(2, N, K, std=K ** -.5, dtype=dtype), big(3, N, K, std=K ** -.5, dtype=dtype)
+    ref = R.rounded(*R.product(a.double(), b.double()), dtype)
+    R.check("x W^T", Linear(b).forward(a), ref)
+    bt = b.t().contiguous()
+    R.check("dz W", Linear(bt).backward(big(4, M, N, dtype=dtype), a, need_dw=False)[0], ref)
+    at = a.t().contiguous()
+    R.check("dz^T x", Linear(big(5, M, N, dtype=dtype)).backward(bt, at, need_dx=False)[1], ref)
+    R.check("gated", GatedProjection(b, b2, act="none").forward(a),
+            R.gated_forward(*d64(a, b, b2), None, None, "none", dtype)["h"])
