@@ -93,20 +93,32 @@ __device__ __forceinline__ void load8(const void *row, int64_t col, int n, float
         v[j] = j < n ? E::to_f(q[j + s]) : 0.f;
 }
 
+// stream: past the caches (non-temporal), for outputs too large to be found there again
 template <class E>
-__device__ __forceinline__ void store8(void *row, int64_t col, int n, const float v[8])
+__device__ __forceinline__ void store8(void *row, int64_t col, int n, const float v[8], bool stream = false)
 {
+    typedef f32x4_t __attribute__((aligned(4))) f32x4_a4;
+    typedef u32x4_t __attribute__((aligned(2))) u32x4_a2;
     typename E::raw *q = (typename E::raw *)row + col;
     if (n >= 8) {
         if constexpr (sizeof(typename E::raw) == 4) {
-            ((any128x4 *)q)->v = f32x4_t{v[0], v[1], v[2], v[3]};
-            ((any128x4 *)(q + 4))->v = f32x4_t{v[4], v[5], v[6], v[7]};
+            const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+            if (stream) {
+                __builtin_nontemporal_store(a, (f32x4_a4 *)q);
+                __builtin_nontemporal_store(b, (f32x4_a4 *)(q + 4));
+            } else {
+                *(f32x4_a4 *)q = a;
+                *(f32x4_a4 *)(q + 4) = b;
+            }
         } else {
             u32x4_t a;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 a[j] = E::pack(v[2 * j], v[2 * j + 1]);
-            ((any128x2 *)q)->v = a;
+            if (stream)
+                __builtin_nontemporal_store(a, (u32x4_a2 *)q);
+            else
+                *(u32x4_a2 *)q = a;
         }
         return;
     }

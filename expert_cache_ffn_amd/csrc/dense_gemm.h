@@ -98,53 +98,66 @@ struct DenseGrid {
 
 // ---- epilogue on 8 columns of one row -------------------------------------------------
 
-// Bias, saved sums, activation, gated product or residual, and the output of
-// columns n..n+7 of row m; z[q] are the fp32 sums (q = 1: the up projection).
+// Bias of columns n..n+7, of each projection.
 template <class E, bool GATED>
-__device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t m, int n, float z[GATED ? 2 : 1][8])
+__device__ __forceinline__ void load_bias(const DenseGemm &g, int n, float bias[GATED ? 2 : 1][8])
+{
+#pragma unroll
+    for (int q = 0; q < (GATED ? 2 : 1); ++q)
+        if (g.bias[q] && n < g.N)
+            load8<E>(g.bias[q], n, g.N - n, bias[q]);
+}
+
+// Residual of columns n..n+7 of row m.
+template <class E>
+__device__ __forceinline__ void load_res(const DenseGemm &g, int64_t m, int n, float res[8])
+{
+    if (m >= g.M || n >= g.N)
+        return;
+    if (g.out_dtype == ECF_F32)
+        load8<F32>(row_at<F32>(g.res, m * g.ldres), n, g.N - n, res);
+    else
+        load8<E>(row_at<E>(g.res, m * g.ldres), n, g.N - n, res);
+}
+
+// Saved sums, activation ACT, gated product or residual, and the output of columns
+// n..n+7 of row m; z[q] are the fp32 sums (q = 1: the up projection).
+template <class E, bool GATED, int ACT>
+__device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t m, int n, float z[GATED ? 2 : 1][8],
+                                          const float bias[GATED ? 2 : 1][8], const float res[8])
 {
     const int cnt = g.N - n;
-    if (cnt <= 0)
+    if (cnt <= 0 || m >= g.M)
         return;
 #pragma unroll
     for (int q = 0; q < (GATED ? 2 : 1); ++q) {
         if (g.bias[q]) {
-            float bv[8];
-            load8<E>(g.bias[q], n, cnt, bv);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                z[q][j] += bv[j];
+                z[q][j] += bias[q][j];
         }
         if (g.save[q])
-            store8<E>(row_at<E>(g.save[q], m * g.ldsave), n, cnt, z[q]);
+            store8<E>(row_at<E>(g.save[q], m * g.ldsave), n, cnt, z[q], g.stream_out);
     }
     void *out = g.out[half];
     if (!out)
         return;
     float y[8];
-    with_act(g.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = act_value(z[0][j], decltype(act)::value);
-    });
-    if constexpr (GATED) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 8; ++j) {
+        y[j] = act_value(z[0][j], ACT);
+        if constexpr (GATED)
             y[j] *= z[1][j];
-    } else if (g.res) {
-        float r[8];
-        if (g.out_dtype == ECF_F32)
-            load8<F32>(row_at<F32>(g.res, m * g.ldres), n, cnt, r);
-        else
-            load8<E>(row_at<E>(g.res, m * g.ldres), n, cnt, r);
+    }
+    if (!GATED && g.res) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            y[j] += r[j];
+            y[j] += res[j];
     }
     if (g.out_dtype == ECF_F32)
-        store8<F32>(row_at<F32>(out, m * g.ldout), n, cnt, y);
+        store8<F32>(row_at<F32>(out, m * g.ldout), n, cnt, y, g.stream_out);
     else
-        store8<E>(row_at<E>(out, m * g.ldout), n, cnt, y);
+        store8<E>(row_at<E>(out, m * g.ldout), n, cnt, y, g.stream_out);
 }
 
 // ---- operand tiles ----------------------------------------------------------------------
@@ -688,9 +701,9 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
     // Output through LDS: each wave puts 32 rows x (up to) 64 columns of fp32 sums
     // in its own buffer and takes them back by rows.  A wave's LDS accesses
     // complete in order, so only the compiler has to be kept from reordering them.
-    // The loops stay loops, with one copy of the epilogue: unrolled, its code is
-    // fetched from memory by every block (8192 x 16384 outputs of K 128: 350 us
-    // unrolled, see the figures at the launcher for the loop).
+    // The loop over the groups stays a loop: unrolled, the epilogue's code is fetched
+    // from memory by every block (8192 x 16384 bf16 outputs of K 128 took 350 us, as
+    // a loop 133).  Bias and residual of a group are loaded ahead of its LDS round trip.
     constexpr int CB = FN >= 2 ? 2 : 1, GROUPS = FM * (FN / CB);
     constexpr int LPR = (GATED ? 32 : 32 * CB) / 8;  // lanes per output row
     // (two waves that hold the two projections of the same columns share a buffer,
@@ -698,8 +711,21 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
     float *eb = (float *)lds + (MATES ? wave / 2 : wave) * 32 * PITCH;
     const int ecol = MATES ? (wn & 1) * 32 : 0, erow = MATES ? (wn & 1) * 16 : 0;
     const bool partial = gr.splits > 1;
+    constexpr int PASSES = MATES ? 1 : 32 * LPR / 64, Q = GATED ? 2 : 1;
 #pragma unroll 1
     for (int grp = 0; grp < GROUPS; ++grp) {
+        const int r0 = wm * RM + grp / (FN / CB) * 32 + erow + lane / LPR, c = (lane % LPR) * 8;
+        const int c0 = MATES ? wn / 2 * 32 : GATED ? (wn * RN + grp % (FN / CB) * 64) / 2 : wn * RN + grp % (FN / CB) * 64;
+        const int n = n0 + c0 + c;
+        float bias[Q][8], res[GATED ? 1 : PASSES][8];
+        if (!partial) {
+            load_bias<E, GATED>(g, n, bias);
+            if (!GATED && g.res) {
+#pragma unroll
+                for (int p = 0; p < PASSES; ++p)
+                    load_res<E>(g, m0 + r0 + p * (64 / LPR), n, res[GATED ? 0 : p]);
+            }
+        }
         asm volatile("" ::: "memory");
 #pragma unroll
         for (int i = 0; i < GROUPS; ++i)
@@ -714,31 +740,38 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
         asm volatile("" ::: "memory");
         if constexpr (MATES)
             __syncthreads();
-        const int r0 = wm * RM + grp / (FN / CB) * 32;
-        const int c0 = MATES ? wn / 2 * 32 : GATED ? (wn * RN + grp % (FN / CB) * 64) / 2 : wn * RN + grp % (FN / CB) * 64;
-#pragma unroll 1
-        for (int p = 0; p < (MATES ? 1 : 32 * LPR / 64); ++p) {
-            const int r = erow + p * (64 / LPR) + lane / LPR, c = (lane % LPR) * 8;
-            const int64_t m = m0 + r0 + r;
-            const int n = n0 + c0 + c;
-            float z[GATED ? 2 : 1][8];
+        auto take = [&](int p, float z[Q][8]) __attribute__((always_inline)) {
+            const float *at = eb + (erow + p * (64 / LPR) + lane / LPR) * PITCH + c;
 #pragma unroll
-            for (int q = 0; q < (GATED ? 2 : 1); ++q) {
-                const f32x4_t lo = *(const f32x4_t *)(eb + r * PITCH + q * 32 + c);
-                const f32x4_t hi = *(const f32x4_t *)(eb + r * PITCH + q * 32 + c + 4);
+            for (int q = 0; q < Q; ++q) {
+                const f32x4_t lo = *(const f32x4_t *)(at + q * 32), hi = *(const f32x4_t *)(at + q * 32 + 4);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     z[q][e] = lo[e], z[q][4 + e] = hi[e];
             }
-            if (m >= g.M)
-                continue;
-            if (!partial) {
-                epilogue8<E, GATED>(g, half, m, n, z);
-            } else if (n < g.N) {
+        };
+        if (partial) {
 #pragma unroll
-                for (int q = 0; q < (GATED ? 2 : 1); ++q)
-                    store8<F32>(gr.partial, gr.partial_at(g, split, GATED ? q : half, m) + n, 8, z[q]);
+            for (int p = 0; p < PASSES; ++p) {
+                const int64_t m = m0 + r0 + p * (64 / LPR);
+                float z[Q][8];
+                take(p, z);
+                if (m < g.M && n < g.N) {
+#pragma unroll
+                    for (int q = 0; q < Q; ++q)
+                        store8<F32>(gr.partial, gr.partial_at(g, split, GATED ? q : half, m) + n, 8, z[q]);
+                }
             }
+        } else {
+            with_act(g.act, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+                for (int p = 0; p < PASSES; ++p) {
+                    float z[Q][8];
+                    take(p, z);
+                    epilogue8<E, GATED, decltype(act)::value>(g, half, m0 + r0 + p * (64 / LPR), n, z, bias,
+                                                              res[GATED ? 0 : p]);
+                }
+            });
         }
         if constexpr (MATES)
             __syncthreads();
@@ -781,7 +814,10 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseGemm g, DenseGrid gr)
     const int64_t row = i / per;
     const int n = (int)(i - row * per) * 8, half = row >= g.M ? 1 : 0;
     const int64_t m = row - (half ? g.M : 0);
-    float z[GATED ? 2 : 1][8] = {};
+    float z[GATED ? 2 : 1][8] = {}, bias[GATED ? 2 : 1][8], res[8];
+    load_bias<E, GATED>(g, n, bias);
+    if (!GATED && g.res)
+        load_res<E>(g, m, n, res);
 #pragma unroll 4
     for (int s = 0; s < gr.splits; ++s)
 #pragma unroll
@@ -792,7 +828,9 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseGemm g, DenseGrid gr)
             for (int j = 0; j < 8; ++j)
                 z[q][j] += v[j];
         }
-    epilogue8<E, GATED>(g, half, m, n, z);
+    with_act(g.act, [&](auto act) __attribute__((always_inline)) {
+        epilogue8<E, GATED, decltype(act)::value>(g, half, m, n, z, bias, res);
+    });
 }
 
 // How a product is cut: the tile, the splits of K, and whether operands can go

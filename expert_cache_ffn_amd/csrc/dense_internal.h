@@ -33,6 +33,7 @@ struct DenseGemm {
     int64_t ldout;
     void *save[2];
     int64_t ldsave;
+    bool stream_out;  // set by the launcher: the output does not fit the caches
 };
 // ws: room for dense_gemm_ws bytes (may be null where that is 0)
 int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st);

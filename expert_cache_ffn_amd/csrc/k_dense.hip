@@ -242,6 +242,10 @@ int cu_count(int *out)
 }
 
 constexpr int kMaxSplits = 16;
+// Outputs of half the 256 MiB memory-side cache and more are stored past the caches:
+// 8192 x 16384 bf16 of K 4096 907 -> 879 us, 8192 x 2048 (32 MiB) within 1%, and there
+// the next operator finds the output in the cache.
+constexpr int64_t kStreamBytes = (int64_t)128 << 20;
 constexpr double kLaunchUs = 3.0;  // one launch more, host and device
 
 // Rows at 16-byte boundaries and whole 16-byte chunks: operands can go straight to LDS.
@@ -386,8 +390,10 @@ size_t dense_gemm_ws(int64_t M, int64_t N, int planes)
     return std::min(all, kDensePartialBytes);
 }
 
-int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st)
+int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
 {
+    DenseGemm g = gin;
+    g.stream_out = (int64_t)g.M * g.N * (int64_t)dense_esize(g.out_dtype) >= kStreamBytes;
     ProfScope p(g.gated ? "dense_gated" : g.a_t ? "dense_gemm_tn" : g.b_t ? "dense_gemm_nn" : "dense_gemm_nt", st);
     int cus = 0;
     const int rc = cu_count(&cus);
