@@ -121,38 +121,45 @@ __device__ __forceinline__ void load_res(const DenseGemm &g, int64_t m, int n, f
 }
 
 // Saved sums, activation ACT, gated product or residual, and the output of columns
-// n..n+7 of row m; z[q] are the fp32 sums (q = 1: the up projection).
-template <class E, bool GATED, int ACT>
+// n..n+7 of row m; z[q] are the fp32 sums (q = 1: the up projection).  PLAIN: the
+// sums are the output, as in the backward products, whose code stays small for it.
+template <class E, bool GATED, bool PLAIN, int ACT>
 __device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t m, int n, float z[GATED ? 2 : 1][8],
                                           const float bias[GATED ? 2 : 1][8], const float res[8])
 {
     const int cnt = g.N - n;
     if (cnt <= 0 || m >= g.M)
         return;
-#pragma unroll
-    for (int q = 0; q < (GATED ? 2 : 1); ++q) {
-        if (g.bias[q]) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                z[q][j] += bias[q][j];
-        }
-        if (g.save[q])
-            store8<E>(row_at<E>(g.save[q], m * g.ldsave), n, cnt, z[q], g.stream_out);
-    }
     void *out = g.out[half];
-    if (!out)
-        return;
     float y[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        y[j] = act_value(z[0][j], ACT);
-        if constexpr (GATED)
-            y[j] *= z[1][j];
-    }
-    if (!GATED && g.res) {
+    if constexpr (PLAIN) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            y[j] += res[j];
+            y[j] = z[0][j];
+    } else {
+#pragma unroll
+        for (int q = 0; q < (GATED ? 2 : 1); ++q) {
+            if (g.bias[q]) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    z[q][j] += bias[q][j];
+            }
+            if (g.save[q])
+                store8<E>(row_at<E>(g.save[q], m * g.ldsave), n, cnt, z[q], g.stream_out);
+        }
+        if (!out)
+            return;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            y[j] = act_value(z[0][j], ACT);
+            if constexpr (GATED)
+                y[j] *= z[1][j];
+        }
+        if (!GATED && g.res) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                y[j] += res[j];
+        }
     }
     if (g.out_dtype == ECF_F32)
         store8<F32>(row_at<F32>(out, m * g.ldout), n, cnt, y, g.stream_out);
@@ -717,13 +724,14 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
         const int r0 = wm * RM + grp / (FN / CB) * 32 + erow + lane / LPR, c = (lane % LPR) * 8;
         const int c0 = MATES ? wn / 2 * 32 : GATED ? (wn * RN + grp % (FN / CB) * 64) / 2 : wn * RN + grp % (FN / CB) * 64;
         const int n = n0 + c0 + c;
-        float bias[Q][8], res[GATED ? 1 : PASSES][8];
-        if (!partial) {
+        constexpr bool PLAIN = BT;
+        float bias[Q][8], res[GATED || PLAIN ? 1 : PASSES][8];
+        if (!PLAIN && !partial) {
             load_bias<E, GATED>(g, n, bias);
             if (!GATED && g.res) {
 #pragma unroll
                 for (int p = 0; p < PASSES; ++p)
-                    load_res<E>(g, m0 + r0 + p * (64 / LPR), n, res[GATED ? 0 : p]);
+                    load_res<E>(g, m0 + r0 + p * (64 / LPR), n, res[GATED || PLAIN ? 0 : p]);
             }
         }
         asm volatile("" ::: "memory");
@@ -762,14 +770,21 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
                         store8<F32>(gr.partial, gr.partial_at(g, split, GATED ? q : half, m) + n, 8, z[q]);
                 }
             }
+        } else if constexpr (PLAIN) {
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                float z[Q][8];
+                take(p, z);
+                epilogue8<E, GATED, true, ECF_ACT_NONE>(g, half, m0 + r0 + p * (64 / LPR), n, z, bias, res[0]);
+            }
         } else {
             with_act(g.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
                 for (int p = 0; p < PASSES; ++p) {
                     float z[Q][8];
                     take(p, z);
-                    epilogue8<E, GATED, decltype(act)::value>(g, half, m0 + r0 + p * (64 / LPR), n, z, bias,
-                                                              res[GATED ? 0 : p]);
+                    epilogue8<E, GATED, false, decltype(act)::value>(g, half, m0 + r0 + p * (64 / LPR), n, z, bias,
+                                                                     res[GATED || PLAIN ? 0 : p]);
                 }
             });
         }
@@ -829,7 +844,7 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseGemm g, DenseGrid gr)
                 z[q][j] += v[j];
         }
     with_act(g.act, [&](auto act) __attribute__((always_inline)) {
-        epilogue8<E, GATED, decltype(act)::value>(g, half, m, n, z, bias, res);
+        epilogue8<E, GATED, false, decltype(act)::value>(g, half, m, n, z, bias, res);
     });
 }
 
