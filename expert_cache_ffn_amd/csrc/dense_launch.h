@@ -34,8 +34,10 @@ int pick_gemm(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipSt
         case 0: launch_gemm<E, AT, BT, GATED, DMA, 256, 256, 2, 4, 64, DMA ? 2 : 1>(g, gr, st); break;
         case 1: launch_gemm<E, AT, BT, GATED, DMA, 128, 256, 2, 4, 64, DMA ? 3 : 2>(g, gr, st); break;
         case 2: launch_gemm<E, AT, BT, GATED, DMA, 128, 128, 2, 2, 64, DMA ? 2 : 1>(g, gr, st); break;
-        case 3: launch_gemm<E, AT, BT, GATED, DMA, 64, 128, 2, 2, 64, DMA ? 3 : 2>(g, gr, st); break;
-        default: launch_gemm<E, AT, BT, GATED, DMA, 64, 64, 2, 2, 64, DMA ? 3 : 1>(g, gr, st); break;
+        case 3: launch_gemm<E, AT, BT, GATED, DMA, 64, DMA ? 128 : 64, 2, 2, 64, DMA ? 3 : 1>(g, gr, st); break;
+        default:
+            if constexpr (DMA)
+                launch_gemm<E, AT, BT, GATED, true, 64, 64, 2, 2, 64, 3>(g, gr, st);
         }
     }
     if (gr.splits > 1)
@@ -65,8 +67,10 @@ int pick_pair(const DenseGemm &gx, const DenseGrid &grx, const DenseGemm &gw, co
     } else {
         switch (p.tile) {
         case 2: launch_pair<E, DMA, 128, 128, 2, 2, 64, DMA ? 2 : 1>(gx, grx, gw, grw, st); break;
-        case 3: launch_pair<E, DMA, 64, 128, 2, 2, 64, DMA ? 3 : 2>(gx, grx, gw, grw, st); break;
-        default: launch_pair<E, DMA, 64, 64, 2, 2, 64, DMA ? 3 : 1>(gx, grx, gw, grw, st); break;
+        case 3: launch_pair<E, DMA, 64, DMA ? 128 : 64, 2, 2, 64, DMA ? 3 : 1>(gx, grx, gw, grw, st); break;
+        default:
+            if constexpr (DMA)
+                launch_pair<E, true, 64, 64, 2, 2, 64, 3>(gx, grx, gw, grw, st);
         }
     }
     if (grx.splits > 1)

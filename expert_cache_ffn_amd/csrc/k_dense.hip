@@ -204,22 +204,24 @@ __global__ __launch_bounds__(256) void k_dense_colsum(const float *partial, int 
 namespace {
 
 // A tile of the output and what it costs: `us` per k-tile of 64 with per_cu blocks
-// on every CU, `us1` with one (measured, K 4096); `fixed` per block for filling the
-// pipeline and the epilogue.
+// on every CU (measured, K 4096), `us1` with one, `fixed` per block for filling the
+// pipeline and the epilogue.  us1 and fixed are fitted to every tile and split of
+// 6000 products of 1 to 8192 tokens and up to 40 GFLOP: the choice takes 1.7% longer
+// than the best of them on the geometric mean.
 struct TileCost {
     int bm, bn, per_cu;
     double us, us1, fixed;
 };
-const TileCost kTilesDma[] = {{256, 256, 1, 1.78, 1.78, 8.0}, {128, 256, 1, 0.98, 0.98, 6.0},
-                              {128, 128, 2, 1.05, 0.68, 5.0}, {64, 128, 2, 0.66, 0.41, 4.0},
-                              {64, 64, 2, 0.45, 0.31, 3.5}};
-const TileCost kTilesReg[] = {{256, 256, 1, 1.92, 1.92, 8.0}, {128, 256, 1, 1.14, 1.14, 6.0},
-                              {128, 128, 2, 1.25, 0.81, 5.0}, {64, 128, 2, 0.88, 0.69, 4.0},
-                              {64, 64, 2, 0.64, 0.57, 3.5}};
-const TileCost kTilesF32[] = {{128, 128, 1, 2.90, 2.90, 5.0}, {64, 128, 1, 1.75, 1.75, 4.0}, {64, 64, 1, 1.22, 1.22, 3.5}};
+const TileCost kTilesDma[] = {{256, 256, 1, 1.78, 1.78, 10.9}, {128, 256, 1, 0.98, 0.98, 5.7},
+                              {128, 128, 2, 1.05, 0.74, 5.3}, {64, 128, 2, 0.66, 0.34, 5.1},
+                              {64, 64, 2, 0.45, 0.25, 2.5}};
+const TileCost kTilesReg[] = {{256, 256, 1, 1.92, 1.92, 13.6}, {128, 256, 1, 1.14, 1.14, 8.0},
+                              {128, 128, 2, 1.25, 0.83, 7.6}, {64, 64, 2, 0.64, 0.45, 2.8}};
+const TileCost kTilesF32[] = {{128, 128, 1, 2.90, 2.90, 5.3}, {64, 128, 1, 1.75, 1.75, 5.5}, {64, 64, 1, 1.22, 1.22, 5.9}};
 constexpr int kShortK = 32;
 
 const TileCost *tiles_of(int dtype, bool dma) { return dtype == ECF_F32 ? kTilesF32 : dma ? kTilesDma : kTilesReg; }
+int tile_count(int dtype, bool dma) { return dtype == ECF_F32 ? 3 : dma ? 5 : 4; }
 
 bool aligned16(const void *p, int64_t ld, int dtype)
 {
@@ -242,11 +244,12 @@ int cu_count(int *out)
 }
 
 constexpr int kMaxSplits = 16;
+constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, kMaxSplits};
 // Outputs of half the 256 MiB memory-side cache and more are stored past the caches:
 // 8192 x 16384 bf16 of K 4096 907 -> 879 us, 8192 x 2048 (32 MiB) within 1%, and there
 // the next operator finds the output in the cache.
 constexpr int64_t kStreamBytes = (int64_t)128 << 20;
-constexpr double kLaunchUs = 3.0;  // one launch more, host and device
+constexpr double kLaunchUs = 5.0;  // one launch more, host and device
 
 // Rows at 16-byte boundaries and whole 16-byte chunks: operands can go straight to LDS.
 bool dma_ok(const DenseGemm &g)
@@ -279,7 +282,7 @@ double partial_bytes(const DenseGemm &g, int splits)
 {
     return (double)splits * (g.gated ? 2 : g.mhalves) * g.M * ((g.N + 7) / 8 * 8) * 4;
 }
-double join_us(const DenseGemm &g, int splits) { return splits > 1 ? 2.5 + partial_bytes(g, splits) * 2 / 5e6 : 0.0; }
+double join_us(const DenseGemm &g, int splits) { return splits > 1 ? 3.0 + partial_bytes(g, splits) * 2 / 5e6 : 0.0; }
 bool may_split(const DenseGemm &g, int splits, size_t room)
 {
     return splits == 1 || (ktiles(g) / splits >= 2 && partial_bytes(g, splits) <= (double)room);
@@ -290,17 +293,19 @@ bool may_split(const DenseGemm &g, int splits, size_t room)
 DensePlan plan_gemm(const DenseGemm &g, int cus, size_t room, double *us_out)
 {
     DensePlan best{0, 1, dma_ok(g)};
-    const int n_tiles = g.dtype == ECF_F32 ? 3 : 5, kt = ktiles(g);
+    const int n_tiles = tile_count(g.dtype, best.dma), kt = ktiles(g);
     const TileCost *tiles = tiles_of(g.dtype, best.dma);
     *us_out = 1e300;
     for (int t = 0; t < n_tiles; ++t) {
         const TileCost &c = tiles[t];
-        for (int s = 1; s <= kMaxSplits && may_split(g, s, room); s *= 2) {
+        for (const int s : kSplits) {
+            if (!may_split(g, s, room))
+                break;
             // full rounds of per_cu blocks on every CU, then what is left
             const int64_t blocks = out_tiles(g, c) * s, round = (int64_t)cus * c.per_cu, rest = blocks % round;
-            const double tail = rest == 0 ? 0.0 : rest <= cus ? c.us1 : c.us;
-            const double walk = (double)((kt + s - 1) / s) * ((blocks / round) * c.us + tail);
-            const double us = walk + (double)((blocks + round - 1) / round) * c.fixed + join_us(g, s);
+            const double walk = (double)((kt + s - 1) / s);
+            const double tail = rest == 0 ? 0.0 : walk * (rest <= cus ? c.us1 : c.us) + c.fixed;
+            const double us = (double)(blocks / round) * (walk * c.us + c.fixed) + tail + join_us(g, s);
             if (us < *us_out) {
                 *us_out = us;
                 best.tile = t;
@@ -311,8 +316,8 @@ DensePlan plan_gemm(const DenseGemm &g, int cus, size_t room, double *us_out)
     return best;
 }
 
-// When the last of n1 blocks of k1 k-tiles and, behind them, n2 of k2 (k1 >= k2) is
-// done, on `slots` slots that each take the next block when they are free.
+// When the last of n1 blocks that take k1 and, behind them, n2 that take k2 (k1 >= k2)
+// is done, on `slots` slots that each take the next block when they are free.
 double makespan(int64_t n1, double k1, int64_t n2, double k2, int64_t slots)
 {
     const int64_t left = n1 % slots;  // slots that start one more long block at t0
@@ -345,19 +350,26 @@ struct PairPlan {
 PairPlan plan_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t room, double *us_out)
 {
     PairPlan best{{0, 1, dma_ok(gx) && dma_ok(gw)}, 1};
-    const bool f32 = gx.dtype == ECF_F32;
+    const int n_tiles = tile_count(gx.dtype, best.x.dma);
     const TileCost *tiles = tiles_of(gx.dtype, best.x.dma);
     *us_out = 1e300;
-    for (int t = f32 ? 0 : 2; t < (f32 ? 3 : 5); ++t) {
+    for (int t = gx.dtype == ECF_F32 ? 0 : 2; t < n_tiles; ++t) {  // (the large 16-bit tiles: apart)
         const TileCost &c = tiles[t];
         const int64_t slots = (int64_t)cus * c.per_cu;
-        for (int sx = 1; sx <= kMaxSplits && may_split(gx, sx, room); sx *= 2)
-            for (int sw = 1; sw <= kMaxSplits && may_split(gw, sw, room); sw *= 2) {
+        for (const int sx : kSplits) {
+            if (!may_split(gx, sx, room))
+                break;
+            for (const int sw : kSplits) {
+                // (one of the two reductions is long, and splitting the short one too
+                // gains nothing)
+                if ((sx > 2 && sw > 2) || !may_split(gw, sw, room))
+                    break;
                 const int64_t bx = out_tiles(gx, c) * sx, bw = out_tiles(gw, c) * sw;
-                const double kx = (ktiles(gx) + sx - 1) / sx, kw = (ktiles(gw) + sw - 1) / sw;
-                const double walk = kx >= kw ? makespan(bx, kx, bw, kw, slots) : makespan(bw, kw, bx, kx, slots);
-                const double us = walk * (bx + bw <= cus ? c.us1 : c.us) +
-                                  (double)((bx + bw + slots - 1) / slots) * c.fixed + join_us(gx, sx) + join_us(gw, sw);
+                const double us_k = bx + bw <= cus ? c.us1 : c.us;
+                const double tx = (double)((ktiles(gx) + sx - 1) / sx) * us_k + c.fixed;
+                const double tw = (double)((ktiles(gw) + sw - 1) / sw) * us_k + c.fixed;
+                const double us = (tx >= tw ? makespan(bx, tx, bw, tw, slots) : makespan(bw, tw, bx, tx, slots)) +
+                                  join_us(gx, sx) + join_us(gw, sw);
                 if (us < *us_out) {
                     *us_out = us;
                     best.x.tile = t;
@@ -365,6 +377,7 @@ PairPlan plan_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t roo
                     best.splits_w = sw;
                 }
             }
+        }
     }
     return best;
 }

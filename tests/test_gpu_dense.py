@@ -571,7 +571,7 @@ def test_few_tokens(T, K, N, dt):
 # (operands straight to LDS) and odd (through registers)
 TILES = [(5264, 1584, 72), (136, 6416, 4088), (704, 6008, 72), (1296, 1744, 72), (72, 64, 80), (4736, 896, 72), (608, 3328, 72),
          (160, 5720, 72), (1055, 7703, 71), (3275, 263, 2407), (6957, 519, 75), (3195, 647, 71), (99, 71, 65), (1659, 2703, 67),
-         (1111, 1819, 67), (5705, 171, 71), (6321, 71, 2661)]
+         (1111, 1819, 67), (5705, 171, 71), (6321, 71, 2661), (2047, 4093, 515)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
