@@ -209,6 +209,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
         hipStream_t st = (hipStream_t)a->stream;
         char *dz = (char *)a->d_ws;
+        DenseColsum sums{};
         if (want_db || (T > 0 && (want_dw || want_dx))) {
             DenseGrad q{};
             q.dtype = q.dout_dtype = a->dtype;
@@ -223,7 +224,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
             q.sums[0] = a->d_db_gate, q.sums[1] = a->d_db_up;
             q.sums_dtype = a->wgrad_dtype;
             q.partial = (float *)(dz + w.colsum);
-            DENSE_TRY(launch_dense_grad(q, st));
+            DENSE_TRY(launch_dense_grad(q, &sums, st));
         }
         const char *dz2 = dz + (size_t)(w.pitch / 2) * dense_esize(a->dtype);
         DenseGemm gx{}, gw{};
@@ -245,7 +246,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         gw.M = a->inter, gw.N = a->hidden, gw.K = T;
         gw.out[0] = a->d_dw_gate, gw.out[1] = a->d_dw_up;
         gw.ldout = lddw;
-        return launch_dense_backward(want_dx ? &gx : nullptr, want_dw ? &gw : nullptr, (char *)a->d_ws + w.split, st);
+        return launch_dense_backward(want_dx ? &gx : nullptr, want_dw ? &gw : nullptr, sums, (char *)a->d_ws + w.split, st);
     });
 }
 
@@ -333,6 +334,7 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         // without an activation and in the operands' type, dy is dz
         const bool direct = !act && a->out_dtype == a->dtype;
         const bool products = want_dx || (a->d_dw && T > 0);
+        DenseColsum sums{};
         if (a->d_dbias || (T > 0 && products && !direct)) {
             DenseGrad q{};
             q.dtype = a->dtype, q.dout_dtype = a->out_dtype;
@@ -347,7 +349,7 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
             q.sums[0] = a->d_dbias;
             q.sums_dtype = a->wgrad_dtype;
             q.partial = (float *)((char *)a->d_ws + w.colsum);
-            DENSE_TRY(launch_dense_grad(q, st));
+            DENSE_TRY(launch_dense_grad(q, &sums, st));
         }
         const void *dz = direct ? a->d_dout : a->d_ws;
         const int64_t lddz = direct ? lddy : w.pitch;
@@ -369,7 +371,7 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         gw.M = a->out_features, gw.N = a->in_features, gw.K = T;
         gw.out[0] = a->d_dw;
         gw.ldout = lddw;
-        return launch_dense_backward(want_dx ? &gx : nullptr, a->d_dw ? &gw : nullptr, (char *)a->d_ws + w.split, st);
+        return launch_dense_backward(want_dx ? &gx : nullptr, a->d_dw ? &gw : nullptr, sums, (char *)a->d_ws + w.split, st);
     });
 }
 

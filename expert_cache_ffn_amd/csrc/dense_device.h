@@ -238,4 +238,12 @@ __device__ __forceinline__ void *row_at(void *p, int64_t at)
     return (typename E::raw *)p + at;
 }
 
+__device__ __forceinline__ void store_el(void *p, int64_t i, float v, int dtype)
+{
+    if (dtype == ECF_F32)
+        ((float *)p)[i] = v;
+    else
+        ((uint16_t *)p)[i] = dtype == ECF_BF16 ? BF16::from_f(v) : F16::from_f(v);
+}
+
 }  // namespace ecf

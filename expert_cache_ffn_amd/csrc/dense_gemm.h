@@ -804,15 +804,41 @@ __global__ ECF_GEMM_BOUNDS void k_gemm(DenseGemm g, DenseGrid gr)
     gemm_block<E, AT, BT, GATED, DMA, BM, BN, WM, WN, BK, NSTAGE>(g, gr, (int)blockIdx.x, lds);
 }
 
+// Column sums over the row blocks, in order, and zeros where there is no row block
+// at all: block b takes 64 columns, its first four waves a quarter of the row blocks
+// each.  red: 1 KiB of LDS.
+__device__ __forceinline__ void colsum_block(const DenseColsum &s, int b, float *red)
+{
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t c = (int64_t)b * 64 + lane, cols = (int64_t)s.n * s.I;
+    float v = 0.f;
+    if (c < cols && w < 4)
+#pragma unroll 8
+        for (int64_t r = w; r < s.row_blocks; r += 4)
+            v += s.partial[r * cols + c];
+    if (w < 4)
+        red[w * 64 + lane] = v;
+    __syncthreads();
+    if (w || c >= cols)
+        return;
+    void *out = c < s.I ? s.out[0] : s.out[1];
+    if (out)
+        store_el(out, c < s.I ? c : c - s.I, (red[lane] + red[64 + lane]) + (red[128 + lane] + red[192 + lane]),
+                 s.out_dtype);
+}
+
 // The two products of a backward pass, dz W and dz^T x, in one launch: each alone
 // often leaves CUs idle, and neither needs the other.  The blocks of the longer
-// reduction come first.
+// reduction come first, the column sums' last (as a launch of their own: 3.5 us more).
 template <class E, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE>
-__global__ ECF_GEMM_BOUNDS void k_gemm_pair(DenseGemm gx, DenseGrid grx, DenseGemm gw, DenseGrid grw, int x_first)
+__global__ ECF_GEMM_BOUNDS void k_gemm_pair(DenseGemm gx, DenseGrid grx, DenseGemm gw, DenseGrid grw, DenseColsum sums,
+                                              int x_first)
 {
     __shared__ __attribute__((aligned(16))) char lds[gemm_lds_bytes<E, DMA, BM, BN, WM, WN, BK, NSTAGE>()];
     const int nx = grx.blocks(), nw = grw.blocks(), b = (int)blockIdx.x;
-    if (x_first ? b < nx : b >= nw)
+    if (b >= nx + nw)
+        colsum_block(sums, b - nx - nw, (float *)lds);
+    else if (x_first ? b < nx : b >= nw)
         gemm_block<E, false, true, false, DMA, BM, BN, WM, WN, BK, NSTAGE>(gx, grx, x_first ? b : b - nw, lds);
     else
         gemm_block<E, true, true, false, DMA, BM, BN, WM, WN, BK, NSTAGE>(gw, grw, x_first ? b - nx : b, lds);

@@ -37,9 +37,18 @@ struct DenseGemm {
 };
 // ws: room for dense_gemm_ws bytes (may be null where that is 0)
 int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st);
+// Column sums still to be joined over the row blocks of launch_dense_grad: fp32
+// partial [row_blocks][n I], the first I columns into out[0], the others into out[1]
+// (each may be null).  A block takes 64 columns.
+struct DenseColsum {
+    const float *partial;
+    int row_blocks, I, n, out_dtype;
+    void *out[2];
+    int blocks;  // 0: nothing to join
+};
 // The products of a backward pass, dx (n-contiguous B) and dW (m- and n-contiguous;
-// either may be null), in one launch or two.  ws: kDensePartialBytes.
-int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, void *ws, hipStream_t st);
+// either may be null), and the column sums, in one launch or more.  ws: kDensePartialBytes.
+int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseColsum &sums, void *ws, hipStream_t st);
 // x W^T of at most kFewTokens rows as a stream of the weights (k_dense_few.hip), and
 // the time estimated for it.  It needs no workspace; up to kAlwaysFew rows it is the
 // choice whenever there is none.
@@ -54,7 +63,7 @@ size_t dense_gemm_ws(int64_t M, int64_t N, int planes);
 // da = dz[t][i], db = dz[t][pitch / 2 + i] (gated).  Columns from I to the (half)
 // pitch, the next multiple of 8, are zeroed.  With sums, the columns are added up:
 // into `sums` where one row block covers all tokens, else per row block into
-// partial [block][1 or 2][I], which launch_dense_colsum joins.
+// partial [block][1 or 2][I], and `left` says what is still to be joined.
 struct DenseGrad {
     int dtype, dout_dtype, act;
     bool gated;
@@ -70,6 +79,6 @@ struct DenseGrad {
 };
 // the most row blocks of any call with up to T tokens
 int64_t dense_grad_max_row_blocks(int64_t T);
-int launch_dense_grad(const DenseGrad &g, hipStream_t st);
+int launch_dense_grad(const DenseGrad &g, DenseColsum *left, hipStream_t st);
 
 }  // namespace ecf

@@ -47,30 +47,31 @@ int pick_gemm(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipSt
 }
 
 template <class E, bool DMA, int BM, int BN, int WM, int WN, int BK, int NS>
-void launch_pair(const DenseGemm &gx, const DenseGrid &grx, const DenseGemm &gw, const DenseGrid &grw, hipStream_t st)
+void launch_pair(const DenseGemm &gx, const DenseGrid &grx, const DenseGemm &gw, const DenseGrid &grw,
+                 const DenseColsum &sums, hipStream_t st)
 {
     const int x_first = (int64_t)gx.K * gx.ksegs / grx.splits >= gw.K / grw.splits;
-    hipLaunchKernelGGL((k_gemm_pair<E, DMA, BM, BN, WM, WN, BK, NS>), dim3(grx.blocks() + grw.blocks()),
-                       dim3(64 * WM * WN), 0, st, gx, grx, gw, grw, x_first);
+    hipLaunchKernelGGL((k_gemm_pair<E, DMA, BM, BN, WM, WN, BK, NS>), dim3(grx.blocks() + grw.blocks() + sums.blocks),
+                       dim3(64 * WM * WN), 0, st, gx, grx, gw, grw, sums, x_first);
 }
 
 template <class E, bool DMA>
-int pick_pair(const DenseGemm &gx, const DenseGrid &grx, const DenseGemm &gw, const DenseGrid &grw, const DensePlan &p,
-              hipStream_t st)
+int pick_pair(const DenseGemm &gx, const DenseGrid &grx, const DenseGemm &gw, const DenseGrid &grw,
+              const DenseColsum &sums, const DensePlan &p, hipStream_t st)
 {
     if constexpr (std::is_same<E, F32>::value) {
         switch (p.tile) {
-        case 0: launch_pair<E, false, 128, 128, 4, 2, 32, 1>(gx, grx, gw, grw, st); break;
-        case 1: launch_pair<E, false, 64, 128, 2, 4, 64, 1>(gx, grx, gw, grw, st); break;
-        default: launch_pair<E, false, 64, 64, 2, 2, 64, 1>(gx, grx, gw, grw, st); break;
+        case 0: launch_pair<E, false, 128, 128, 4, 2, 32, 1>(gx, grx, gw, grw, sums, st); break;
+        case 1: launch_pair<E, false, 64, 128, 2, 4, 64, 1>(gx, grx, gw, grw, sums, st); break;
+        default: launch_pair<E, false, 64, 64, 2, 2, 64, 1>(gx, grx, gw, grw, sums, st); break;
         }
     } else {
         switch (p.tile) {
-        case 2: launch_pair<E, DMA, 128, 128, 2, 2, 64, DMA ? 2 : 1>(gx, grx, gw, grw, st); break;
-        case 3: launch_pair<E, DMA, 64, DMA ? 128 : 64, 2, 2, 64, DMA ? 3 : 1>(gx, grx, gw, grw, st); break;
+        case 2: launch_pair<E, DMA, 128, 128, 2, 2, 64, DMA ? 2 : 1>(gx, grx, gw, grw, sums, st); break;
+        case 3: launch_pair<E, DMA, 64, DMA ? 128 : 64, 2, 2, 64, DMA ? 3 : 1>(gx, grx, gw, grw, sums, st); break;
         default:
             if constexpr (DMA)
-                launch_pair<E, true, 64, 64, 2, 2, 64, 3>(gx, grx, gw, grw, st);
+                launch_pair<E, true, 64, 64, 2, 2, 64, 3>(gx, grx, gw, grw, sums, st);
         }
     }
     if (grx.splits > 1)
@@ -99,6 +100,6 @@ int launch_gemm_nn(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, 
 int launch_gemm_tn(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipStream_t st);
 
 int launch_gemm_pair(const DenseGemm &gx, const DenseGrid &grx, const DenseGemm &gw, const DenseGrid &grw,
-                     const DensePlan &p, hipStream_t st);
+                     const DenseColsum &sums, const DensePlan &p, hipStream_t st);
 
 }  // namespace ecf

@@ -8,14 +8,6 @@
 namespace ecf {
 namespace {
 
-__device__ __forceinline__ void store_el(void *p, int64_t i, float v, int dtype)
-{
-    if (dtype == ECF_F32)
-        ((float *)p)[i] = v;
-    else
-        ((uint16_t *)p)[i] = dtype == ECF_BF16 ? BF16::from_f(v) : F16::from_f(v);
-}
-
 // Products whose operands have rows of under 8 elements, which the MFMA tiles'
 // 16-byte chunks do not take, and fp32 products over under kShortK k, with fp32
 // FMAs: a block owns a 64 x 64 tile of the output, stages 16 k of both operands in
@@ -177,26 +169,10 @@ __global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks,
     }
 }
 
-// Column sums of the row blocks' sums, and zeros where there is no row at all: a
-// block owns 64 columns, its four waves a quarter of the row blocks each.
-__global__ __launch_bounds__(256) void k_dense_colsum(const float *partial, int row_blocks, int I, int n, int out_dtype,
-                                                      void *out0, void *out1)
+__global__ __launch_bounds__(256) void k_dense_colsum(DenseColsum s)
 {
-    __shared__ float red[4][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane, cols = (int64_t)n * I;
-    float s = 0.f;
-    if (c < cols)
-#pragma unroll 8
-        for (int64_t r = w; r < row_blocks; r += 4)
-            s += partial[r * cols + c];
-    red[w][lane] = s;
-    __syncthreads();
-    if (w || c >= cols)
-        return;
-    void *out = c < I ? out0 : out1;
-    if (out)
-        store_el(out, c < I ? c : c - I, (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]), out_dtype);
+    __shared__ float red[4 * 64];
+    colsum_block(s, (int)blockIdx.x, red);
 }
 
 }  // namespace
@@ -447,7 +423,7 @@ int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
                    : launch_gemm_nt(g, plan, gr, st);
 }
 
-int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, void *ws, hipStream_t st)
+int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseColsum &sums, void *ws, hipStream_t st)
 {
     if (gx && gw && !short_rows(*gx) && !short_rows(*gw)) {
         int cus = 0;
@@ -463,8 +439,13 @@ int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, void *ws, hi
             ProfScope scope("dense_gemm_pair", st);
             const TileCost &t = tiles_of(gx->dtype, p.x.dma)[p.x.tile];
             return launch_gemm_pair(*gx, grid_of(*gx, t, p.x.splits, ws), *gw,
-                                    grid_of(*gw, t, p.splits_w, (char *)ws + half), p.x, st);
+                                    grid_of(*gw, t, p.splits_w, (char *)ws + half), sums, p.x, st);
         }
+    }
+    if (sums.blocks) {
+        ProfScope p("dense_colsum", st);
+        hipLaunchKernelGGL(k_dense_colsum, dim3(sums.blocks), dim3(256), 0, st, sums);
+        ECF_HIP_CHECK(hipGetLastError());
     }
     if (gx) {
         const int rc = launch_dense_gemm(*gx, ws, st);
@@ -476,7 +457,7 @@ int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, void *ws, hi
 
 int64_t dense_grad_max_row_blocks(int64_t T) { return (T + kGradLanes - 1) / kGradLanes; }
 
-int launch_dense_grad(const DenseGrad &g, hipStream_t st)
+int launch_dense_grad(const DenseGrad &g, DenseColsum *left, hipStream_t st)
 {
     const int64_t cols = (g.I + kGradCols - 1) / kGradCols;
     // rows per block; all of a short batch in one block saves the launch that joins the sums
@@ -503,11 +484,9 @@ int launch_dense_grad(const DenseGrad &g, hipStream_t st)
         ECF_HIP_CHECK(hipGetLastError());
     }
     if (g.want_sums && rows != 1) {
-        ProfScope p("dense_colsum", st);
         const int n = g.gated ? 2 : 1;
-        hipLaunchKernelGGL(k_dense_colsum, dim3((unsigned)(((int64_t)n * g.I + 63) / 64)), dim3(256), 0, st, g.partial,
-                           rows, g.I, n, g.sums_dtype, g.sums[0], g.sums[1]);
-        ECF_HIP_CHECK(hipGetLastError());
+        *left = DenseColsum{g.partial, rows, g.I, n, g.sums_dtype, {g.sums[0], g.sums[1]},
+                            (int)(((int64_t)n * g.I + 63) / 64)};
     }
     return ECF_OK;
 }
