@@ -433,20 +433,20 @@ template <bool T, int ROWS, int F, int BK>
 struct Frag {
     static constexpr int NK = BK / 16;
     uint32_t at[T ? F : NK];
-    __device__ __forceinline__ void init(int lane, int r0)
+    __device__ __forceinline__ void init(int lane, int r0, int ks0)  // read()'s step 0 is ks0
     {
         const int g = lane >> 5;
         if constexpr (!T) {
             const int r = r0 + (lane & 31);
 #pragma unroll
             for (int ks = 0; ks < NK; ++ks)
-                at[ks] = r * (BK * 2) + ((NK * g + ks) ^ rswz<BK>(r)) * 16;
+                at[ks] = r * (BK * 2) + ((NK * g + ((ks0 + ks) & (NK - 1))) ^ rswz<BK>(r)) * 16;
         } else {
             const int i = lane & 15, k = BK / 2 * g + (i >> 2);
 #pragma unroll
             for (int f = 0; f < F; ++f) {
                 const int m = r0 + 32 * f + (lane & 16) + (i & 3) * 4;
-                at[f] = k * (ROWS * 2) + (((m >> 3) ^ kswz<ROWS>(k)) * 16) + (m & 4) * 2;
+                at[f] = (k + 8 * ks0) * (ROWS * 2) + (((m >> 3) ^ kswz<ROWS>(k)) * 16) + (m & 4) * 2;
             }
         }
     }
@@ -480,13 +480,18 @@ constexpr int gemm_lds_bytes()
     return in > out ? in : out;
 }
 
-// Block `block` of a product: one (split, output tile), see DenseGrid.
-template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE>
+// Block `block` of a product: one (split, output tile), see DenseGrid.  KW: groups of
+// WM x WN waves that share each k-tile's steps; their sums are joined at the end.  Two
+// groups for the fp32 64 x 64 tile, whose LDS leaves room for one block: with two waves
+// per SIMD one splits operands while the other multiplies (K 4096: 1.22 -> 1.00 us per
+// k-tile of 64).
+template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE, int KW>
 __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &gr, int block, char *lds)
 {
     using namespace gemm;
-    constexpr int NW = WM * WN, NTH = 64 * NW, RM = BM / WM, RN = BN / WN, FM = RM / 32, FN = RN / 32;
-    static_assert(BK % 32 == 0, "two sets of fragments take turns");
+    constexpr int NW = WM * WN, NTH = 64 * NW * KW, RM = BM / WM, RN = BN / WN, FM = RM / 32, FN = RN / 32;
+    static_assert(BK % (32 * KW) == 0, "two sets of fragments take turns");
+    static_assert(KW <= 2 && (KW == 1 || (FM == 1 && FN == 1)), "a group's sums fit the stages' LDS");
     static_assert(DMA || NSTAGE <= 2, "one or two register sets");
     static_assert(FM >= 1 && (FN == 1 || FN % 2 == 0) && (!GATED || (!BT && WN * FN % 2 == 0)), "wave tile");
     constexpr int NS = DMA ? NSTAGE : 2, SETS = DMA ? 1 : NSTAGE;
@@ -498,7 +503,7 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
     int split, half, mt, nt;
     gr.locate(block, split, half, mt, nt);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / WN, wn = wave % WN;
+    const int group = KW > 1 ? wave / NW : 0, gwave = KW > 1 ? wave % NW : wave, wm = gwave / WN, wn = gwave % WN;
     const int m0 = mt * BM, n0 = nt * (GATED ? BN / 2 : BN);
     const int mrows = min(BM, g.M - m0);
 
@@ -511,8 +516,9 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
             [&](int r) { return (int64_t)min(GATED ? (r >> 6) * 32 + (r & 31) : r, nlast); });
     Frag<AT, BM, FM, BK> fa;
     Frag<BT, BN, FN, BK> fb;
-    fa.init(lane, wm * RM);
-    fb.init(lane, wn * RN);
+    constexpr int NK = BK / 16 / KW;  // a group's steps of each k-tile
+    fa.init(lane, wm * RM, group * NK);
+    fb.init(lane, wn * RN, group * NK);
 
     f32x16_t acc[FM][FN];
 #pragma unroll
@@ -584,7 +590,6 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
     };
     // Two sets of fragments: step ks + 1 (or the next k-tile's step 0) is read under
     // the MFMAs of step ks.
-    constexpr int NK = BK / 16;
     u32x4_t av[2][FM][NP], bv[2][FN][NP];
     auto fetch = [&](int stage, int ks, int set, int f) __attribute__((always_inline)) {
         const char *sa = lds + stage * (SA + SB), *sb = sa + SA;
@@ -705,6 +710,23 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
         }
     }
 
+    if constexpr (KW > 1) {
+        // the second group's sums to the first, which stores the output
+        f32x4_t *sums = (f32x4_t *)lds + gwave * 256 + lane;
+        if (group) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sums[64 * e] = f32x4_t{acc[0][0][4 * e], acc[0][0][4 * e + 1], acc[0][0][4 * e + 2], acc[0][0][4 * e + 3]};
+        }
+        __syncthreads();
+        if (!group) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                acc[0][0][e] += sums[64 * (e >> 2)][e & 3];
+        }
+        __syncthreads();
+    }
+
     // Output through LDS: each wave puts 32 rows x (up to) 64 columns of fp32 sums
     // in its own buffer and takes them back by rows.  A wave's LDS accesses
     // complete in order, so only the compiler has to be kept from reordering them.
@@ -715,10 +737,15 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
     constexpr int LPR = (GATED ? 32 : 32 * CB) / 8;  // lanes per output row
     // (two waves that hold the two projections of the same columns share a buffer,
     // and take half its rows each)
-    float *eb = (float *)lds + (MATES ? wave / 2 : wave) * 32 * PITCH;
+    float *eb = (float *)lds + (MATES ? gwave / 2 : gwave) * 32 * PITCH;
     const int ecol = MATES ? (wn & 1) * 32 : 0, erow = MATES ? (wn & 1) * 16 : 0;
     const bool partial = gr.splits > 1;
     constexpr int PASSES = MATES ? 1 : 32 * LPR / 64, Q = GATED ? 2 : 1;
+    if (KW > 1 && group) {
+        for (int i = 0; MATES && i < 2 * GROUPS; ++i)
+            __syncthreads();  // the ones below
+        return;
+    }
 #pragma unroll 1
     for (int grp = 0; grp < GROUPS; ++grp) {
         const int r0 = wm * RM + grp / (FN / CB) * 32 + erow + lane / LPR, c = (lane % LPR) * 8;
@@ -795,13 +822,13 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
 
 // Waves per SIMD asked of the register allocator: two, but one where a wave's own
 // tile of sums takes more than half the registers.
-#define ECF_GEMM_BOUNDS __launch_bounds__(64 * WM * WN, BM / WM * (BN / WN) > 128 * 64 ? 1 : 2)
+#define ECF_GEMM_BOUNDS __launch_bounds__(64 * WM * WN * KW, BM / WM * (BN / WN) > 128 * 64 ? 1 : 2)
 
-template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE>
+template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE, int KW>
 __global__ ECF_GEMM_BOUNDS void k_gemm(DenseGemm g, DenseGrid gr)
 {
     __shared__ __attribute__((aligned(16))) char lds[gemm_lds_bytes<E, DMA, BM, BN, WM, WN, BK, NSTAGE>()];
-    gemm_block<E, AT, BT, GATED, DMA, BM, BN, WM, WN, BK, NSTAGE>(g, gr, (int)blockIdx.x, lds);
+    gemm_block<E, AT, BT, GATED, DMA, BM, BN, WM, WN, BK, NSTAGE, KW>(g, gr, (int)blockIdx.x, lds);
 }
 
 // Column sums over the row blocks, in order, and zeros where there is no row block
@@ -830,7 +857,7 @@ __device__ __forceinline__ void colsum_block(const DenseColsum &s, int b, float 
 // The two products of a backward pass, dz W and dz^T x, in one launch: each alone
 // often leaves CUs idle, and neither needs the other.  The blocks of the longer
 // reduction come first, the column sums' last (as a launch of their own: 3.5 us more).
-template <class E, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE>
+template <class E, bool DMA, int BM, int BN, int WM, int WN, int BK, int NSTAGE, int KW>
 __global__ ECF_GEMM_BOUNDS void k_gemm_pair(DenseGemm gx, DenseGrid grx, DenseGemm gw, DenseGrid grw, DenseColsum sums,
                                               int x_first)
 {
@@ -839,9 +866,9 @@ __global__ ECF_GEMM_BOUNDS void k_gemm_pair(DenseGemm gx, DenseGrid grx, DenseGe
     if (b >= nx + nw)
         colsum_block(sums, b - nx - nw, (float *)lds);
     else if (x_first ? b < nx : b >= nw)
-        gemm_block<E, false, true, false, DMA, BM, BN, WM, WN, BK, NSTAGE>(gx, grx, x_first ? b : b - nw, lds);
+        gemm_block<E, false, true, false, DMA, BM, BN, WM, WN, BK, NSTAGE, KW>(gx, grx, x_first ? b : b - nw, lds);
     else
-        gemm_block<E, true, true, false, DMA, BM, BN, WM, WN, BK, NSTAGE>(gw, grw, x_first ? b - nx : b, lds);
+        gemm_block<E, true, true, false, DMA, BM, BN, WM, WN, BK, NSTAGE, KW>(gw, grw, x_first ? b - nx : b, lds);
 }
 
 // Joins the splits of a product, in order, and applies its epilogue: one thread

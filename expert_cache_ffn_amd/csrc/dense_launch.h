@@ -5,11 +5,11 @@
 
 namespace ecf {
 
-template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN, int BK, int NS>
+template <class E, bool AT, bool BT, bool GATED, bool DMA, int BM, int BN, int WM, int WN, int BK, int NS, int KW = 1>
 void launch_gemm(const DenseGemm &g, const DenseGrid &gr, hipStream_t st)
 {
-    hipLaunchKernelGGL((k_gemm<E, AT, BT, GATED, DMA, BM, BN, WM, WN, BK, NS>), dim3(gr.blocks()), dim3(64 * WM * WN), 0, st,
-                       g, gr);
+    hipLaunchKernelGGL((k_gemm<E, AT, BT, GATED, DMA, BM, BN, WM, WN, BK, NS, KW>), dim3(gr.blocks()),
+                       dim3(64 * WM * WN * KW), 0, st, g, gr);
 }
 
 template <class E, bool GATED>
@@ -27,7 +27,7 @@ int pick_gemm(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipSt
         switch (p.tile) {
         case 0: launch_gemm<E, AT, BT, GATED, false, 128, 128, 4, 2, 32, 1>(g, gr, st); break;
         case 1: launch_gemm<E, AT, BT, GATED, false, 64, 128, 2, 4, 64, 1>(g, gr, st); break;
-        default: launch_gemm<E, AT, BT, GATED, false, 64, 64, 2, 2, 64, 1>(g, gr, st); break;
+        default: launch_gemm<E, AT, BT, GATED, false, 64, 64, 2, 2, 64, 1, 2>(g, gr, st); break;
         }
     } else {
         switch (p.tile) {
@@ -46,13 +46,13 @@ int pick_gemm(const DenseGemm &g, const DensePlan &p, const DenseGrid &gr, hipSt
     return ECF_OK;
 }
 
-template <class E, bool DMA, int BM, int BN, int WM, int WN, int BK, int NS>
+template <class E, bool DMA, int BM, int BN, int WM, int WN, int BK, int NS, int KW = 1>
 void launch_pair(const DenseGemm &gx, const DenseGrid &grx, const DenseGemm &gw, const DenseGrid &grw,
                  const DenseColsum &sums, hipStream_t st)
 {
     const int x_first = (int64_t)gx.K * gx.ksegs / grx.splits >= gw.K / grw.splits;
-    hipLaunchKernelGGL((k_gemm_pair<E, DMA, BM, BN, WM, WN, BK, NS>), dim3(grx.blocks() + grw.blocks() + sums.blocks),
-                       dim3(64 * WM * WN), 0, st, gx, grx, gw, grw, sums, x_first);
+    hipLaunchKernelGGL((k_gemm_pair<E, DMA, BM, BN, WM, WN, BK, NS, KW>), dim3(grx.blocks() + grw.blocks() + sums.blocks),
+                       dim3(64 * WM * WN * KW), 0, st, gx, grx, gw, grw, sums, x_first);
 }
 
 template <class E, bool DMA>
@@ -63,7 +63,7 @@ int pick_pair(const DenseGemm &gx, const DenseGrid &grx, const DenseGemm &gw, co
         switch (p.tile) {
         case 0: launch_pair<E, false, 128, 128, 4, 2, 32, 1>(gx, grx, gw, grw, sums, st); break;
         case 1: launch_pair<E, false, 64, 128, 2, 4, 64, 1>(gx, grx, gw, grw, sums, st); break;
-        default: launch_pair<E, false, 64, 64, 2, 2, 64, 1>(gx, grx, gw, grw, sums, st); break;
+        default: launch_pair<E, false, 64, 64, 2, 2, 64, 1, 2>(gx, grx, gw, grw, sums, st); break;
         }
     } else {
         switch (p.tile) {

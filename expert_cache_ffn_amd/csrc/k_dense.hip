@@ -193,7 +193,7 @@ const TileCost kTilesDma[] = {{256, 256, 1, 1.78, 1.78, 10.9}, {128, 256, 1, 0.9
                               {64, 64, 2, 0.45, 0.25, 2.5}};
 const TileCost kTilesReg[] = {{256, 256, 1, 1.92, 1.92, 13.6}, {128, 256, 1, 1.14, 1.14, 8.0},
                               {128, 128, 2, 1.25, 0.83, 7.6}, {64, 64, 2, 0.64, 0.45, 2.8}};
-const TileCost kTilesF32[] = {{128, 128, 1, 2.90, 2.90, 5.3}, {64, 128, 1, 1.75, 1.75, 5.5}, {64, 64, 1, 1.22, 1.22, 5.9}};
+const TileCost kTilesF32[] = {{128, 128, 1, 2.70, 2.70, 5.9}, {64, 128, 1, 1.75, 1.75, 6.3}, {64, 64, 1, 1.00, 1.00, 5.8}};
 constexpr int kShortK = 32;
 
 const TileCost *tiles_of(int dtype, bool dma) { return dtype == ECF_F32 ? kTilesF32 : dma ? kTilesDma : kTilesReg; }
