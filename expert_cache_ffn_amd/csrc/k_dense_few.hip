@@ -13,6 +13,10 @@
 //
 // The waves of a block share K; their partial sums meet in LDS and are added in a
 // fixed order by one thread per output, which applies the epilogue.
+//
+// 2 x 1024 rows of K 4096, bf16 (16.8 MB): one token 5.0 us, 16 tokens 8.0; 2.5 us of
+// it are launch and first loads, then a CU takes in 38 KB/us (9.7 TB/s of all, the
+// weights lying in the memory-side cache).
 #include "dense_device.h"
 
 namespace ecf {

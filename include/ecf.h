@@ -357,7 +357,8 @@ int ecf_bandwidth_profile(const ecf_shape *shape, int32_t n_blobs, const void *c
  * and each output is rounded once; the backward passes also round da, db and dz
  * once to `dtype`, the type that the two products behind them multiply.  Results do not depend on what runs beside a
  * call, and the same call gives the same bits.  An infinite or NaN element makes
- * outputs infinite or NaN only in rows (columns) that it is part of.
+ * outputs infinite or NaN only in rows (columns) that it is part of (in fp32 an
+ * infinity times an infinity counts as NaN).
  *
  * d_ws needs ecf_*_workspace_bytes bytes at a 256-byte boundary (where that is 0 it may be
  * NULL), holds nothing between calls, and must not be shared by calls that may overlap (two
