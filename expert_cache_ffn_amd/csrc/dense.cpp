@@ -2,6 +2,7 @@
 // workspace, and the matrix products and gradient kernels each call is made of.
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 
 #include "dense_internal.h"
 
@@ -80,6 +81,27 @@ int check_grad_dtype(const char *what, int32_t t, int32_t dtype)
 {
     if (t != dtype && t != ECF_F32)
         return set_error(ECF_EINVAL, "%s: wgrad_dtype must be dtype or ECF_F32 (got %d)", what, t);
+    return ECF_OK;
+}
+
+// An output that starts where another one or an input does: blocks would read what
+// others have written.  (Other overlaps are the caller's to avoid.)
+struct Named {
+    const char *name;
+    const void *p;
+};
+int check_apart(const char *what, std::initializer_list<Named> outs, std::initializer_list<Named> ins)
+{
+    for (const Named *o = outs.begin(); o != outs.end(); ++o) {
+        if (!o->p)
+            continue;
+        for (const Named &i : ins)
+            if (i.p == o->p)
+                return set_error(ECF_EINVAL, "%s: %s and %s are the same memory", what, o->name, i.name);
+        for (const Named *q = outs.begin(); q != o; ++q)
+            if (q->p == o->p)
+                return set_error(ECF_EINVAL, "%s: %s and %s are the same memory", what, o->name, q->name);
+    }
     return ECF_OK;
 }
 
@@ -162,6 +184,9 @@ int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
         }
         const size_t need = forward_ws(T, d, I, a->dtype, 2);
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, need));
+        DENSE_TRY(check_apart(me, {{"d_h", a->d_h}, {"d_a", a->d_a}, {"d_b", a->d_b}, {"d_ws", need ? a->d_ws : nullptr}},
+                              {{"d_x", a->d_x}, {"d_w_gate", a->d_w_gate}, {"d_w_up", a->d_w_up},
+                               {"d_b_gate", a->d_b_gate}, {"d_b_up", a->d_b_up}}));
         g.a[0] = a->d_x;
         g.b[0] = a->d_w_gate, g.b[1] = a->d_w_up;
         g.bias[0] = a->d_b_gate, g.bias[1] = a->d_b_up;
@@ -207,6 +232,10 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         const BackWs w = back_ws(I, 2, a->dtype, T);
         DENSE_TRY(check_pitch(me, w.pitch, a->dtype));
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
+        DENSE_TRY(check_apart(me, {{"d_dx", a->d_dx}, {"d_dw_gate", a->d_dw_gate}, {"d_dw_up", a->d_dw_up},
+                                   {"d_db_gate", a->d_db_gate}, {"d_db_up", a->d_db_up}, {"d_ws", a->d_ws}},
+                              {{"d_x", a->d_x}, {"d_w_gate", a->d_w_gate}, {"d_w_up", a->d_w_up}, {"d_a", a->d_a},
+                               {"d_b", a->d_b}, {"d_dh", a->d_dh}}));
         hipStream_t st = (hipStream_t)a->stream;
         char *dz = (char *)a->d_ws;
         DenseColsum sums{};
@@ -289,6 +318,12 @@ int ecf_linear_forward(const ecf_linear_args *a, int32_t T)
             DENSE_TRY(check_matrix(me, "d_z", a->d_z, g.ldsave, N, a->dtype));
         const size_t need = forward_ws(T, K, N, a->dtype, 1);
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, need));
+        DENSE_TRY(check_apart(me, {{"d_out", a->d_out}, {"d_z", a->d_z}, {"d_ws", need ? a->d_ws : nullptr}},
+                              {{"d_x", a->d_x}, {"d_w", a->d_w}, {"d_bias", a->d_bias}}));
+        DENSE_TRY(check_apart(me, {{"d_z", a->d_z}, {"d_ws", need ? a->d_ws : nullptr}}, {{"d_residual", a->d_residual}}));
+        if (a->d_out == a->d_residual && g.ldout != g.ldres)
+            return set_error(ECF_EINVAL, "%s: d_out is d_residual with another row stride (%lld and %lld)", me,
+                             (long long)g.ldout, (long long)g.ldres);
         g.a[0] = a->d_x, g.b[0] = a->d_w;
         g.bias[0] = a->d_bias;
         g.res = a->d_residual;
@@ -330,6 +365,8 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         const BackWs w = back_ws(N, 1, a->dtype, T);
         DENSE_TRY(check_pitch(me, w.pitch, a->dtype));
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
+        DENSE_TRY(check_apart(me, {{"d_dx", a->d_dx}, {"d_dw", a->d_dw}, {"d_dbias", a->d_dbias}, {"d_ws", a->d_ws}},
+                              {{"d_x", a->d_x}, {"d_w", a->d_w}, {"d_z", a->d_z}, {"d_dout", a->d_dout}}));
         hipStream_t st = (hipStream_t)a->stream;
         // without an activation and in the operands' type, dy is dz
         const bool direct = !act && a->out_dtype == a->dtype;

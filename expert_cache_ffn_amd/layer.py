@@ -142,6 +142,11 @@ def _vector(name, t, n, dtype, device):
     return t.data_ptr()
 
 
+def _kept(*tensors):
+    """The tensors' own views of their memory: it stays theirs if w.data is replaced."""
+    return [None if t is None else t.detach() for t in tensors]
+
+
 class _Dense:
     """What the two operators share: the weights' checks, workspaces and streams.
 
@@ -154,7 +159,7 @@ class _Dense:
             raise ValueError(f"{what} must be a non-empty 2-D tensor on the GPU")
         if act not in L.ACTS:
             raise ValueError(f"act must be one of {sorted(L.ACTS)}, got {act!r}")
-        self.device, self.dtype, self.act, self._w = w.device, w.dtype, act, w
+        self.device, self.dtype, self.act, self._w = w.device, w.dtype, act, w.detach()
         self._dt = _dense_dt(w.dtype, what)
         self._ws_of = {}
 
@@ -198,8 +203,9 @@ class GatedProjection(_Dense):
     feed-forward block (SwiGLU with act "silu"), in one kernel.
 
     w_gate, w_up [inter, hidden] in fp32, bf16 or fp16, with the same row stride;
-    b_gate, b_up [inter] or None.  The object keeps the tensors, so their addresses
-    stay valid; in-place updates of the weights are seen by the next call."""
+    b_gate, b_up [inter] or None.  The object keeps their memory: in-place updates of
+    the weights are seen by the next call, a tensor given other memory (w.data = ...)
+    needs a new object."""
 
     def __init__(self, w_gate, w_up, b_gate=None, b_up=None, act="silu"):
         self._setup(w_gate, act, "w_gate")
@@ -212,7 +218,8 @@ class GatedProjection(_Dense):
             raise ValueError(f"w_gate and w_up must have the same row stride ({a.ld_w} and {ld})")
         a.d_b_gate = _vector("b_gate", b_gate, self.inter, self.dtype, self.device)
         a.d_b_up = _vector("b_up", b_up, self.inter, self.dtype, self.device)
-        self.w_gate, self.w_up, self.b_gate, self.b_up, self._a = w_gate, w_up, b_gate, b_up, a
+        self.w_gate, self.w_up, self.b_gate, self.b_up = _kept(w_gate, w_up, b_gate, b_up)
+        self._a = a
 
     def _ws_bytes(self, T, backward):
         return L.ecf_gated_workspace_bytes(self.hidden, self.inter, self._dt, T, backward)
@@ -267,7 +274,8 @@ class Linear(_Dense):
     """y = act(x W^T + bias) + residual, with bias, activation and residual in the
     product's epilogue.
 
-    w [out_features, in_features] in fp32, bf16 or fp16, bias [out_features] or None.
+    w [out_features, in_features] in fp32, bf16 or fp16, bias [out_features] or None
+    (kept as GatedProjection keeps its weights).
     y, the residual and dy are of out_dtype: the weights' type, or torch.float32 (the
     running sum a moe_layer_forward call takes as its residual)."""
 
@@ -282,7 +290,8 @@ class Linear(_Dense):
         a.out_dtype = _DENSE_DT[self.out_dtype]
         a.d_w, a.ld_w = _matrix("w", w, self.out_features, self.in_features, self.dtype, self.device)
         a.d_bias = _vector("bias", bias, self.out_features, self.dtype, self.device)
-        self.w, self.bias, self._a = w, bias, a
+        self.w, self.bias = _kept(w, bias)
+        self._a = a
 
     def _ws_bytes(self, T, backward):
         return L.ecf_linear_workspace_bytes(self.in_features, self.out_features, self._dt, T, backward)

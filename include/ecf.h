@@ -364,7 +364,8 @@ int ecf_bandwidth_profile(const ecf_shape *shape, int32_t n_blobs, const void *c
  * NULL), holds nothing between calls, and must not be shared by calls that may overlap (two
  * streams, two captured graphs that may run at once).  Calls are asynchronous on
  * `stream`, a stream of the current device, allocate nothing and can be captured.
- * Outputs must not overlap inputs, except that d_out may be d_residual (same stride).
+ * Outputs must not overlap inputs or each other, except that d_out may be d_residual
+ * (same stride); two that start at the same address are refused.
  */
 typedef enum {
     ECF_ACT_NONE = 0,

@@ -135,3 +135,34 @@ def test_python_argument_checks():
     with pytest.raises(ValueError):
         ly._vector("b", torch.zeros(16)[::2], 8, torch.float32, dev)
     assert ctypes.sizeof(ecf.GatedArgs) == 216 and ctypes.sizeof(ecf.LinearArgs) == 200
+
+
+DISTINCT = {f: A + 4096 * i for i, f in enumerate(
+    ("d_x", "d_w", "d_w_gate", "d_w_up", "d_b_gate", "d_b_up", "d_bias", "d_h", "d_a", "d_b", "d_z", "d_dh", "d_dout", "d_out",
+     "d_residual", "d_dx", "d_dw", "d_dw_gate", "d_dw_up", "d_db_gate", "d_db_up", "d_dbias", "d_ws"))}
+
+
+@pytest.mark.parametrize("fn,make,out,others", [
+    (ecf.ecf_gated_forward, gated, "d_h", ("d_x", "d_w_gate", "d_w_up", "d_a", "d_b", "d_b_up")),
+    (ecf.ecf_gated_forward, gated, "d_b", ("d_x", "d_a", "d_h", "d_w_up")),
+    (ecf.ecf_gated_backward, gated, "d_dx", ("d_x", "d_a", "d_b", "d_dh", "d_w_gate", "d_dw_up")),
+    (ecf.ecf_gated_backward, gated, "d_dw_gate", ("d_x", "d_w_gate", "d_dw_up", "d_db_up", "d_ws")),
+    (ecf.ecf_linear_forward, linear, "d_out", ("d_x", "d_w", "d_bias", "d_z")),
+    (ecf.ecf_linear_forward, linear, "d_z", ("d_x", "d_residual")),
+    (ecf.ecf_linear_backward, linear, "d_dx", ("d_x", "d_z", "d_dout", "d_w", "d_dw", "d_dbias")),
+    (ecf.ecf_linear_backward, linear, "d_dw", ("d_w", "d_x", "d_dbias"))])
+def test_outputs_on_other_operands_are_refused(fn, make, out, others):
+    for other in others:
+        args = make(ws_bytes=1 << 30)
+        for f in DISTINCT:
+            if hasattr(args, f):
+                setattr(args, f, DISTINCT[f])
+        setattr(args, out, getattr(args, other))
+        with pytest.raises(ecf.EcfError, match="same memory") as e:
+            fn(args, 4)
+        assert e.value.code == ecf.ECF_EINVAL
+
+
+def test_residual_in_place_needs_its_stride():
+    args = linear(d_x=A, d_w=2 * A, d_out=3 * A, d_residual=3 * A, d_z=0, ld_out=40, ld_residual=48)
+    refused(ecf.ecf_linear_forward, args)

@@ -589,3 +589,17 @@ def test_every_tile(M, N, K, dt):
     R.check("dz^T x", Linear(big(5, M, N, dtype=dtype)).backward(bt, at, need_dx=False)[1], ref)
     R.check("gated", GatedProjection(b, b2, act="none").forward(a),
             R.gated_forward(*d64(a, b, b2), None, None, "none", dtype)["h"])
+
+
+def test_weights_given_other_memory():
+    """w.data = ... leaves the object with the memory it was made on, which nothing else may get."""
+    say("case: replaced weight memory")
+    x, w = big(1, 40, 96), big(2, 64, 96, std=96 ** -.5)
+    ref = R.linear_forward(*d64(x, w), None, "none", None, torch.float32, torch.float32)["y"]
+    p = torch.nn.Parameter(w)
+    layer = Linear(p)
+    del w
+    p.data = torch.zeros(64, 96, device="cuda")
+    junk = [torch.full((64, 96), float("nan"), device="cuda") for _ in range(64)]
+    R.check("y", layer.forward(x), ref)
+    assert len(junk) == 64
