@@ -53,6 +53,7 @@ int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseC
 // the time estimated for it.  It needs no workspace; up to kAlwaysFew rows it is the
 // choice whenever there is none.
 constexpr int kFewTokens = 64, kAlwaysFew = 16;
+constexpr int64_t kAlwaysFewX = 1 << 17;  // elements of x
 double dense_few_us(const DenseGemm &g, int cus);
 int launch_dense_few(const DenseGemm &g, int cus, hipStream_t st);
 // The largest workspace of any product with up to M x N outputs in each plane.

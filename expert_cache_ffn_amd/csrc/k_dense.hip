@@ -471,8 +471,8 @@ int launch_dense_grad(const DenseGrad &g, DenseColsum *left, hipStream_t st)
         auto go = [&](auto e, auto ed) {
             using E = decltype(e);
             using ED = decltype(ed);
-            if (g.gated)
-                hipLaunchKernelGGL((k_dense_grad<E, ED, true>), grid, block, 0, st, g, rows, per);
+            if (g.gated)  // dout is of the operands' type
+                hipLaunchKernelGGL((k_dense_grad<E, E, true>), grid, block, 0, st, g, rows, per);
             else
                 hipLaunchKernelGGL((k_dense_grad<E, ED, false>), grid, block, 0, st, g, rows, per);
         };

@@ -219,10 +219,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_dense_few(DenseGemm g)
 }
 
 // Rows per block (4, 8 or 16; at most four groups of tokens) with the least time, and
-// that time in us.  A CU takes in about 38 KB/us of weights and x together, whatever
+// that time in us.  A CU takes in about 40 KB/us of weights and x together, whatever
 // it is (4096 x 4096 bf16: 8 tokens 9.9 us, 64 tokens 21 us; 1024 x 4096: 4.4 and 7.6),
-// and 16 KB/us where 16-bit rows start at odd elements, whose loads the hardware
-// splits (7353 x 2048 bf16, 8 tokens: 20.8 us).
+// and 17 KB/us where 16-bit rows start at odd elements, whose loads the hardware
+// splits (7353 x 2048 bf16, 8 tokens: 20.8 us).  Fitted against the tiles on 840 calls
+// of up to 64 tokens: the choice between the two costs 1.5% over the better one.
 int few_rows(const DenseGemm &g, int cus, double *us)
 {
     const int es = (int)dense_esize(g.dtype), h = g.gated ? 2 : 1;
@@ -233,7 +234,8 @@ int few_rows(const DenseGemm &g, int cus, double *us)
         const int64_t blocks = (g.N + rt - 1) / rt, tokens = (g.M + rt - 1) / rt * rt;
         if (tokens > 4 * rt)
             continue;
-        const double t = 2.5 + (double)((blocks + cus - 1) / cus) * (rt * h + tokens) * g.K * es / (odd ? 16e3 : 38e3);
+        const double t = (es == 2 ? 4.0 : 2.5) +
+                         (double)((blocks + cus - 1) / cus) * (rt * h + tokens) * g.K * es / (odd ? 17e3 : es == 2 ? 42e3 : 38e3);
         if (t < *us) {
             *us = t;
             best = rt;

@@ -166,3 +166,15 @@ def test_outputs_on_other_operands_are_refused(fn, make, out, others):
 def test_residual_in_place_needs_its_stride():
     args = linear(d_x=A, d_w=2 * A, d_out=3 * A, d_residual=3 * A, d_z=0, ld_out=40, ld_residual=48)
     refused(ecf.ecf_linear_forward, args)
+
+
+def test_few_tokens_need_no_workspace():
+    """Up to 16 tokens and 2^17 elements of x (a captured decode step needs no buffer for it)."""
+    for dt in (ecf.ECF_F32, ecf.ECF_BF16, ecf.ECF_F16):
+        for T, K in ((1, 1), (1, 4096), (16, 4096), (1, 100000)):
+            if K == 1 and dt != ecf.ECF_F32:
+                continue  # 16-bit rows of odd length
+            assert ecf.ecf_gated_workspace_bytes(K, 1024, dt, T) == 0
+            assert ecf.ecf_linear_workspace_bytes(K, 1024, dt, T) == 0
+        assert ecf.ecf_linear_workspace_bytes(8192, 1024, dt, 16) > 0
+        assert ecf.ecf_linear_workspace_bytes(4096, 1024, dt, 17) > 0

@@ -549,7 +549,9 @@ def test_one_gradient_at_a_time(T, K, N, dt):
 
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("T,K,N", [(1, 1024, 4096), (6, 640, 1500), (12, 640, 1500), (14, 333, 2047), (20, 512, 3000), (30, 511, 2301),
-                                   (50, 384, 1000), (64, 200, 300), (7, 2049, 1201), (16, 4096, 96), (3, 16, 5000)])
+                                   (50, 384, 1000), (64, 200, 300), (7, 2049, 1201), (16, 4096, 96), (3, 16, 5000),
+                                   (16, 8200, 130), (9, 16384, 70), (2, 66000, 40), (40, 5, 300),
+                                   (20, 7, 9000), (36, 40, 200000), (24, 40, 200000)])
 def test_few_tokens(T, K, N, dt):
     """Every shape of the streaming kernel: rows per block, groups of tokens, odd rows."""
     say(f"case: few tokens T {T} K {K} N {N} {dt}")
@@ -603,3 +605,23 @@ def test_weights_given_other_memory():
     junk = [torch.full((64, 96), float("nan"), device="cuda") for _ in range(64)]
     R.check("y", layer.forward(x), ref)
     assert len(junk) == 64
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,d,I", [(65, 1, 5), (70, 5, 130), (200, 7, 64), (131, 20, 67), (300, 31, 200)])
+def test_gated_short_rows(T, d, I, dt):
+    """More tokens than are streamed, over rows under 8 elements (fp32: under 32)."""
+    say(f"case: short rows T {T} d {d} I {I} {dt}")
+    dtype = DT[dt]
+    x, wg, wu = big(1, T, d, dtype=dtype), big(2, I, d, dtype=dtype), big(3, I, d, dtype=dtype)
+    bg, bu = big(4, I, dtype=dtype), big(5, I, dtype=dtype)
+    h, a, b = GatedProjection(wg, wu, bg, bu, act="gelu").forward(x, save=True)
+    ref = R.gated_forward(*d64(x, wg, wu, bg, bu), "gelu", dtype)
+    for name, got in (("h", h), ("a", a), ("b", b)):
+        R.check(name, got, ref[name])
+    da, db = big(6, T, I, dtype=dtype), big(7, T, I, dtype=dtype)
+    dh = big(8, T, I, std=.1, dtype=dtype)
+    outs = GatedProjection(wg, wu, bg, bu, act="gelu").backward(x, da, db, dh)
+    ref = R.gated_backward(*d64(x, wg, wu, da, db, dh), "gelu", dtype, dtype)
+    for name, got in zip(("dx", "dw_gate", "dw_up", "db_gate", "db_up"), outs):
+        R.check(name, got, ref[name])
