@@ -625,3 +625,63 @@ def test_gated_short_rows(T, d, I, dt):
     ref = R.gated_backward(*d64(x, wg, wu, da, db, dh), "gelu", dtype, dtype)
     for name, got in zip(("dx", "dw_gate", "dw_up", "db_gate", "db_up"), outs):
         R.check(name, got, ref[name])
+
+
+def wide(seed, rows, cols, dtype, std=1.0):
+    """Rows of normal values, made a part at a time."""
+    t = torch.empty(rows, cols, dtype=dtype, device="cuda")
+    for i, part in enumerate(t.split(8192)):
+        part.copy_(big(seed * 1000 + i, *part.shape, std=std))
+    return t
+
+
+@pytest.mark.parametrize("K,N", [(16, 32768), (17, 32769), (5, 32768)])
+def test_offsets_past_32_bits_in_outputs_and_gradients(K, N):
+    """70000 x 32768 elements pass 2^31: rows at both ends and at the border, for every kind of kernel."""
+    T, dtype = 70000, torch.bfloat16
+    border = (1 << 31) // N
+    rows = torch.tensor([0, 1, border - 1, border, border + 1, border + 2, T - 2, T - 1], device="cuda")
+    cols = torch.tensor([0, 7, 63, 64, N // 2, N - 9, N - 2, N - 1], device="cuda")
+    say(f"case: past 32 bits K {K} N {N}: forward")
+    x, w, bias = big(1, T, K, dtype=dtype), big(2, N, K, std=K ** -.5, dtype=dtype), big(3, N, dtype=dtype)
+    acc = wide(4, T, N, dtype)
+    before = acc[rows].double()
+    layer = Linear(w, bias, act="relu")
+    y, z = layer.forward(x, residual=acc, out=acc, save=True)
+    assert y is acc
+    ref = R.linear_forward(x[rows].double(), *d64(w, bias), "relu", before, dtype, dtype)
+    R.check("y", y[rows], ref["y"])
+    R.check("z", z[rows], ref["z"])
+    say("   backward")
+    dx, dw, db = layer.backward(x, y, z, w_grad_dtype=torch.float32)
+    ref = R.linear_backward(x[rows].double(), w.double(), z[rows].double(), y[rows].double(), "relu", dtype, dtype, torch.float32)
+    R.check("dx", dx[rows], ref["dx"])
+    ref = R.linear_backward(x.double(), w[cols].double(), z[:, cols].double(), y[:, cols].double(), "relu", dtype, dtype,
+                            torch.float32)
+    R.check("dw", dw[cols], ref["dw"])
+    R.check("dbias", db[cols], ref["dbias"])
+    del acc, y, z
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_offsets_past_32_bits_in_weights(T):
+    """Weights of 40000 x 60000 elements: streamed and in tiles, and as an operand of dx."""
+    say(f"case: past 32 bits in weights T {T}")
+    N, K, dtype = 40000, 60000, torch.bfloat16
+    w = wide(5, N, K, dtype, std=K ** -.5)
+    x = big(6, T, K, dtype=dtype)
+    cols = torch.tensor([0, 1, 15, 16, (1 << 31) // K - 1, (1 << 31) // K, (1 << 31) // K + 1, N - 2, N - 1], device="cuda")
+    layer = Linear(w)
+    y = layer.forward(x)
+    R.check("y", y[:, cols], R.linear_forward(x.double(), w[cols].double(), None, "none", None, dtype, dtype)["y"])
+    # rows of dout that touch these weight rows only: dx is a sum of theirs
+    dout = torch.zeros(T, N, dtype=dtype, device="cuda")
+    dout[:, cols] = big(7, T, len(cols), dtype=dtype)
+    dx = layer.backward(x, dout, need_dw=False)[0]
+    ref = R.linear_backward(x.double(), w[cols].double(), None, dout[:, cols].double(), "none", dtype, dtype, dtype)
+    R.check("dx", dx, ref["dx"])
+    dw = layer.backward(x, dout, need_dx=False)[1]
+    R.check("dw", dw[cols], ref["dw"])
+    del w, dw
+    torch.cuda.empty_cache()
