@@ -124,19 +124,27 @@ size_t forward_ws(int64_t T, int64_t in, int64_t out, int dtype, int planes)
 
 // Backward workspace: dz rows in `dtype` (gated: da and db halves of one row,
 // each half's rows at 16-byte boundaries), the column sums of each row block in
-// fp32, and the products' partial sums.
+// fp32, in fp16 what the scale of dz is found from and its inverse, and the products'
+// partial sums.
 struct BackWs {
     int64_t pitch;
-    size_t colsum, split, total;
+    size_t colsum, tops, split, total;
 };
 BackWs back_ws(int64_t cols, int halves, int dtype, int32_t T)
 {
     BackWs w;
     w.pitch = halves * ((cols + 7) / 8 * 8);
     w.colsum = al256((size_t)T * w.pitch * dense_esize(dtype));
-    w.split = w.colsum + al256((size_t)dense_grad_max_row_blocks(T) * halves * cols * 4);
+    w.tops = w.colsum + al256((size_t)dense_grad_max_row_blocks(T) * halves * cols * 4);
+    w.split = w.tops + (dtype == ECF_F16 ? al256((kDenseTops + 1) * 4) : 0);
     w.total = w.split + kDensePartialBytes;
     return w;
+}
+
+void set_scale(DenseGrad &q, void *words)
+{
+    q.tops = (uint32_t *)words;
+    q.unscale = (float *)words + kDenseTops;
 }
 
 }  // namespace
@@ -242,6 +250,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         hipStream_t st = (hipStream_t)a->stream;
         char *dz = (char *)a->d_ws;
         DenseColsum sums{};
+        DenseGemm gx{}, gw{};
         if (want_db || (T > 0 && (want_dw || want_dx))) {
             DenseGrad q{};
             q.dtype = q.dout_dtype = a->dtype;
@@ -256,10 +265,12 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
             q.sums[0] = a->d_db_gate, q.sums[1] = a->d_db_up;
             q.sums_dtype = a->wgrad_dtype;
             q.partial = (float *)(dz + w.colsum);
+            if (q.dz && a->dtype == ECF_F16)
+                set_scale(q, dz + w.tops);
             DENSE_TRY(launch_dense_grad(q, &sums, st));
+            gx.unscale = gw.unscale = q.unscale;
         }
         const char *dz2 = dz + (size_t)(w.pitch / 2) * dense_esize(a->dtype);
-        DenseGemm gx{}, gw{};
         gx.dtype = gx.out_dtype = gw.dtype = a->dtype;
         gx.b_t = gw.a_t = gw.b_t = true;
         gx.ksegs = gw.mhalves = 2;
@@ -375,6 +386,7 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         const bool direct = !act && a->out_dtype == a->dtype;
         const bool products = want_dx || (a->d_dw && T > 0);
         DenseColsum sums{};
+        DenseGemm gx{}, gw{};
         if (a->d_dbias || (T > 0 && products && !direct)) {
             DenseGrad q{};
             q.dtype = a->dtype, q.dout_dtype = a->out_dtype;
@@ -389,11 +401,14 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
             q.sums[0] = a->d_dbias;
             q.sums_dtype = a->wgrad_dtype;
             q.partial = (float *)((char *)a->d_ws + w.colsum);
+            // (relu leaves an fp16 dy what it is, or zero)
+            if (q.dz && a->dtype == ECF_F16 && !(a->act == ECF_ACT_RELU && a->out_dtype == ECF_F16))
+                set_scale(q, (char *)a->d_ws + w.tops);
             DENSE_TRY(launch_dense_grad(q, &sums, st));
+            gx.unscale = gw.unscale = q.unscale;
         }
         const void *dz = direct ? a->d_dout : a->d_ws;
         const int64_t lddz = direct ? lddy : w.pitch;
-        DenseGemm gx{}, gw{};
         gx.dtype = gx.out_dtype = gw.dtype = a->dtype;
         gx.b_t = gw.a_t = gw.b_t = true;
         gx.ksegs = gx.mhalves = gw.ksegs = gw.mhalves = 1;

@@ -128,9 +128,10 @@ __device__ __forceinline__ void load_res(const DenseGemm &g, int64_t m, int n, f
 // Saved sums, activation ACT, gated product or residual, and the output of columns
 // n..n+7 of row m; z[q] are the fp32 sums (q = 1: the up projection).  PLAIN: the
 // sums are the output, as in the backward products, whose code stays small for it.
+// They are multiplied by `mul` first (backward products in fp16).
 template <class E, bool GATED, bool PLAIN, int ACT>
 __device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t m, int n, float z[GATED ? 2 : 1][8],
-                                          const float bias[GATED ? 2 : 1][8], const float res[8])
+                                          const float bias[GATED ? 2 : 1][8], const float res[8], float mul = 1.f)
 {
     const int cnt = g.N - n;
     if (cnt <= 0 || m >= g.M)
@@ -140,7 +141,7 @@ __device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t 
     if constexpr (PLAIN) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            y[j] = z[0][j];
+            y[j] = std::is_same<E, F16>::value ? z[0][j] * mul : z[0][j];
     } else {
 #pragma unroll
         for (int q = 0; q < (GATED ? 2 : 1); ++q) {
@@ -170,6 +171,15 @@ __device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t 
         store8<F32>(row_at<F32>(out, m * g.ldout), n, cnt, y, g.stream_out);
     else
         store8<E>(row_at<E>(out, m * g.ldout), n, cnt, y, g.stream_out);
+}
+
+// What undoes the scale of dz (DenseGemm::unscale), in products that may have one.
+template <class E, bool BT>
+__device__ __forceinline__ float unscale_of(const DenseGemm &g)
+{
+    if constexpr (std::is_same<E, F16>::value && BT)
+        return g.unscale ? *g.unscale : 1.f;
+    return 1.f;
 }
 
 // ---- operand tiles ----------------------------------------------------------------------
@@ -746,6 +756,7 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
     const int ecol = MATES ? (wn & 1) * 32 : 0, erow = MATES ? (wn & 1) * 16 : 0;
     const bool partial = gr.splits > 1;
     constexpr int PASSES = MATES ? 1 : 32 * LPR / 64, Q = GATED ? 2 : 1;
+    const float mul = unscale_of<E, BT>(g);
     if (KW > 1 && group) {
         for (int i = 0; MATES && i < 2 * GROUPS; ++i)
             __syncthreads();  // the ones below
@@ -807,7 +818,7 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
             for (int p = 0; p < PASSES; ++p) {
                 float z[Q][8];
                 take(p, z);
-                epilogue8<E, GATED, true, ECF_ACT_NONE>(g, half, m0 + r0 + p * (64 / LPR), n, z, bias, res[0]);
+                epilogue8<E, GATED, true, ECF_ACT_NONE>(g, half, m0 + r0 + p * (64 / LPR), n, z, bias, res[0], mul);
             }
         } else {
             with_act(g.act, [&](auto act) __attribute__((always_inline)) {
@@ -901,6 +912,12 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseGemm g, DenseGrid gr)
             for (int j = 0; j < 8; ++j)
                 z[q][j] += v[j];
         }
+    if constexpr (std::is_same<E, F16>::value && !GATED) {
+        const float mul = unscale_of<E, true>(g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            z[0][j] *= mul;
+    }
     with_act(g.act, [&](auto act) __attribute__((always_inline)) {
         epilogue8<E, GATED, false, decltype(act)::value>(g, half, m, n, z, bias, res);
     });

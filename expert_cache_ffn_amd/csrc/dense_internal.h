@@ -33,6 +33,9 @@ struct DenseGemm {
     int64_t ldout;
     void *save[2];
     int64_t ldsave;
+    // backward products in fp16: the power of two that undoes the scale of dz (see
+    // DenseGrad), applied to the fp32 sums; null: none
+    const float *unscale;
     bool stream_out;  // set by the launcher: the output does not fit the caches
 };
 // ws: room for dense_gemm_ws bytes (may be null where that is 0)
@@ -77,7 +80,15 @@ struct DenseGrad {
     void *sums[2];  // each may be null
     int sums_dtype;
     float *partial;
+    // fp16: da, db and dz may lie outside the type's range although the products made
+    // of them do not (an fp32 dy of 1e-9 or 1e6; a dh b over 65504).  With `tops`,
+    // kDenseTops words of workspace, they are held times the power of two that puts the
+    // largest finite one at 2^14 to 2^15, and *unscale gets its inverse.  Those within
+    // 2^-28 of the largest keep all their bits; what is below 2^-39 of it is lost.
+    uint32_t *tops;
+    float *unscale;
 };
+constexpr int kDenseTops = 1024;  // most blocks that look for the largest
 // the most row blocks of any call with up to T tokens
 int64_t dense_grad_max_row_blocks(int64_t T);
 int launch_dense_grad(const DenseGrad &g, DenseColsum *left, hipStream_t st);

@@ -55,6 +55,7 @@ __global__ __launch_bounds__(256) void k_dense_short(DenseGemm g, int tiles_n)
             __syncthreads();
         }
     }
+    const float mul = unscale_of<E, true>(g);
     for (int i = 0; i < 4; ++i) {
         const int64_t m = m0 + ty * 4 + i, n1 = n0 + tx * 4;
         void *out = g.out[half];
@@ -66,7 +67,7 @@ __global__ __launch_bounds__(256) void k_dense_short(DenseGemm g, int tiles_n)
             const int64_t n = min(n1 + j, (int64_t)g.N - 1);
             float z[2];
             for (int q = 0; q < (GATED ? 2 : 1); ++q) {
-                z[q] = acc[q][i][j] + (g.bias[q] ? E::to_f(((const R *)g.bias[q])[n]) : 0.f);
+                z[q] = acc[q][i][j] * mul + (g.bias[q] ? E::to_f(((const R *)g.bias[q])[n]) : 0.f);
                 if (g.save[q] && n1 + j < g.N)
                     ((R *)g.save[q])[m * g.ldsave + n] = E::from_f(z[q]);
             }
@@ -102,48 +103,139 @@ __global__ __launch_bounds__(256) void k_dense_short(DenseGemm g, int tiles_n)
 // order.  (256 columns and 8 row lanes: 14.6 us for 57 x 6272, a chain of eight rows.)
 constexpr int kGradRows = 64, kGradCols = 64, kGradLanes = 32, kGradBlocks = 512;
 
+// dz (da and db) of columns c .. c + 7 of row t, zeros where they end (n are left).
 template <class E, class ED, bool GATED>
-__global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks, int rows)
+__device__ __forceinline__ void grad8(const DenseGrad &g, int64_t t, int c, int n, float out[GATED ? 2 : 1][8])
 {
     constexpr int H = GATED ? 2 : 1;
+    float d[8], a[8], b[8];
+    load8<ED>(row_at<ED>(g.dout, t * g.lddout), c, n, d);
+    if (g.a)
+        load8<E>(row_at<E>(g.a, t * g.ldab), c, n, a);
+    if constexpr (GATED)
+        load8<E>(row_at<E>(g.b, t * g.ldab), c, n, b);
+    with_act(g.act, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float v = 0.f, s = 1.f;
+            if constexpr (GATED || decltype(act)::value != ECF_ACT_NONE)
+                act_both(a[j], decltype(act)::value, v, s);
+            out[0][j] = GATED ? d[j] * b[j] * s : d[j] * s;
+            if constexpr (GATED)
+                out[H - 1][j] = d[j] * v;
+        }
+    });
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j >= n)
+                out[h][j] = 0.f;
+}
+
+// The largest of `top` over the block's four waves; red: 4 words.
+__device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t *red)
+{
+#pragma unroll
+    for (int o = 32; o; o >>= 1)
+        top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = top;
+    __syncthreads();
+    return max(max(red[0], red[1]), max(red[2], red[3]));
+}
+
+// The largest finite |dz| that each block meets (as bits, which order as the values
+// do), over the tiles of k_dense_grad.  A pass of its own, because every element's scale
+// needs the largest of all; k_dense_grad then finds its inputs in the cache (777 x 1999,
+// three inputs of odd width: 7.0 us, of which the launch and one load are most; linear
+// 523 x 1411: 4.7).
+template <class E, class ED, bool GATED>
+__global__ __launch_bounds__(256) void k_dense_grad_top(DenseGrad g, int row_blocks, int rows, int tiles)
+{
+    __shared__ uint32_t red[4];
+    const int cg = threadIdx.x & 7, rl = threadIdx.x >> 3;
+    uint32_t top = 0;
+    for (int tile = (int)blockIdx.x; tile < tiles; tile += (int)gridDim.x) {
+        const int cb = tile / row_blocks, rb = tile - cb * row_blocks;
+        const int c = cb * kGradCols + cg * 8, n = g.I - c, t1 = min(g.T, (rb + 1) * rows);
+        if (n > 0)
+            for (int64_t t = (int64_t)rb * rows + rl; t < t1; t += kGradLanes) {
+                float out[GATED ? 2 : 1][8];
+                grad8<E, ED, GATED>(g, t, c, n, out);
+#pragma unroll
+                for (int h = 0; h < (GATED ? 2 : 1); ++h)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t u = __float_as_uint(out[h][j]) & 0x7fffffffu;
+                        top = max(top, u < 0x7f800000u ? u : 0u);
+                    }
+            }
+    }
+    top = block_max(top, red);
+    if (threadIdx.x == 0)
+        g.tops[blockIdx.x] = top;
+}
+
+// The power of two that puts `top` (the bits of a finite value) at 2^14 to 2^15, as far as it and its
+// inverse are normal numbers: 2^-113 to 2^126.
+__device__ __forceinline__ int scale_exponent(uint32_t top)
+{
+    return top ? min(14 + 127 - (int)(top >> 23), 126) : 0;
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+template <class E, class ED, bool GATED>
+__global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks, int rows, int n_tops)
+{
+    constexpr int H = GATED ? 2 : 1;
+    constexpr bool SCALED = std::is_same<E, F16>::value;
     __shared__ float red[kGradLanes][H][kGradCols + 4];
     const int cb = (int)blockIdx.x / row_blocks, rb = (int)blockIdx.x - cb * row_blocks;
     const int cg = threadIdx.x & 7, rl = threadIdx.x >> 3;
     const int c = cb * kGradCols + cg * 8, n = g.I - c;
     const int64_t half = g.pitch / H;
     const int t1 = min(g.T, (rb + 1) * rows);
-    float sum[H][8] = {};
+    float sum[H][8] = {}, scale = 1.f;
+    int64_t t = (int64_t)rb * rows + rl;
+    auto take = [&](float out[H][8]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                sum[h][j] += out[h][j];
+                if (SCALED)
+                    out[h][j] *= scale;
+            }
+            if (g.dz)
+                store8<E>(row_at<E>(g.dz, t * g.pitch + h * half), c, 8, out[h]);
+        }
+        t += kGradLanes;
+    };
+    if (SCALED && n_tops) {
+        // the blocks' largest values travel together with the first row
+        __shared__ uint32_t red4[4];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kDenseTops; i += 256)
+            top = max(top, g.tops[min(i + (int)threadIdx.x, n_tops - 1)]);
+        float out[H][8];
+        const bool in = n > 0 && t < t1;
+        if (in)
+            grad8<E, ED, GATED>(g, t, c, n, out);
+        const int e = scale_exponent(block_max(top, red4));
+        scale = power_of_two(e);
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            *g.unscale = power_of_two(-e);
+        if (in)
+            take(out);
+    }
     if (n > 0) {
 #pragma unroll 2
-        for (int64_t t = (int64_t)rb * rows + rl; t < t1; t += kGradLanes) {
-            float d[8], a[8], b[8], out[H][8];
-            load8<ED>(row_at<ED>(g.dout, t * g.lddout), c, n, d);
-            if (g.a)
-                load8<E>(row_at<E>(g.a, t * g.ldab), c, n, a);
-            if constexpr (GATED)
-                load8<E>(row_at<E>(g.b, t * g.ldab), c, n, b);
-            with_act(g.act, [&](auto act) __attribute__((always_inline)) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float v = 0.f, s = 1.f;
-                    if constexpr (GATED || decltype(act)::value != ECF_ACT_NONE)
-                        act_both(a[j], decltype(act)::value, v, s);
-                    out[0][j] = GATED ? d[j] * b[j] * s : d[j] * s;
-                    if constexpr (GATED)
-                        out[H - 1][j] = d[j] * v;
-                }
-            });
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (j >= n)
-                        out[h][j] = 0.f;
-                    sum[h][j] += out[h][j];
-                }
-                if (g.dz)
-                    store8<E>(row_at<E>(g.dz, t * g.pitch + h * half), c, 8, out[h]);
-            }
+        while (t < t1) {
+            float out[H][8];
+            grad8<E, ED, GATED>(g, t, c, n, out);
+            take(out);
         }
     }
     if (!g.want_sums)
@@ -468,13 +560,20 @@ int launch_dense_grad(const DenseGrad &g, DenseColsum *left, hipStream_t st)
     if (rows > 0) {
         ProfScope p("dense_grad", st);
         const dim3 grid((unsigned)(cols * rows)), block(256);
+        const int tiles = (int)(cols * rows), n_tops = g.tops ? std::min(tiles, kDenseTops) : 0;
         auto go = [&](auto e, auto ed) {
             using E = decltype(e);
             using ED = decltype(ed);
+            if constexpr (std::is_same<E, F16>::value) {
+                if (n_tops && g.gated)
+                    hipLaunchKernelGGL((k_dense_grad_top<E, E, true>), dim3(n_tops), block, 0, st, g, rows, per, tiles);
+                else if (n_tops)
+                    hipLaunchKernelGGL((k_dense_grad_top<E, ED, false>), dim3(n_tops), block, 0, st, g, rows, per, tiles);
+            }
             if (g.gated)  // dout is of the operands' type
-                hipLaunchKernelGGL((k_dense_grad<E, E, true>), grid, block, 0, st, g, rows, per);
+                hipLaunchKernelGGL((k_dense_grad<E, E, true>), grid, block, 0, st, g, rows, per, n_tops);
             else
-                hipLaunchKernelGGL((k_dense_grad<E, ED, false>), grid, block, 0, st, g, rows, per);
+                hipLaunchKernelGGL((k_dense_grad<E, ED, false>), grid, block, 0, st, g, rows, per, n_tops);
         };
         if (g.dtype == ECF_F32)
             go(F32{}, F32{});

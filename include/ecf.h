@@ -355,8 +355,12 @@ int ecf_bandwidth_profile(const ecf_shape *shape, int32_t n_blobs, const void *c
  * row and the next row's start changes no result and is not written.  Products are
  * summed in fp32, biases, activations and residuals are applied to the fp32 sums,
  * and each output is rounded once; the backward passes also round da, db and dz
- * once to `dtype`, the type that the two products behind them multiply.  Results do not depend on what runs beside a
- * call, and the same call gives the same bits.  An infinite or NaN element makes
+ * once to `dtype`, the type that the two products behind them multiply (bias gradients
+ * are sums of the unrounded ones).  In fp16 they are rounded as multiples of a power of
+ * two that the call finds from the largest finite one: none of them overflows, those
+ * within 2^-28 of the largest keep all 11 bits, and those below 2^-39 of it count as
+ * zero.  Results do not depend on what runs beside a call, and the same call gives the
+ * same bits.  An infinite or NaN element makes
  * outputs infinite or NaN only in rows (columns) that it is part of (in fp32 an
  * infinity times an infinity counts as NaN).
  *

@@ -1,0 +1,123 @@
+"""GPU tests of the dense operators' range: gradients whose da, db or dz lie outside
+fp16's range although their products do not, and infinities that meet in fp32."""
+import pytest
+import torch
+
+import dense_ref as R
+from expert_cache_ffn_amd.layer import GatedProjection, Linear
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+F16 = torch.float16
+
+
+def rand(seed, *shape, std=1.0, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g, dtype=torch.float64) * std).to(dtype).cuda()
+
+
+def scaled_half(*ds):
+    """Bounds of the [(value, bound unrounded, ...)] of R.grads once held in fp16 times the power of two that
+    puts the largest of them all at 2^14 to 2^15: half a step of each value, and half a subnormal step
+    (2^-25) on that scale, 2^-39 of the largest."""
+    top = max(float(d[d.isfinite()].abs().max()) for d, _, _ in ds)
+    return [(d, e, e + d.abs() * (2.0 ** -11 * (1 + 1e-3)) + top * 2.0 ** -39) for d, e, _ in ds]
+
+
+# kernels of few and many tokens, aligned and odd widths, rows under 8 elements, split and unsplit products
+SHAPES = [(64, 256, 128), (1, 40, 72), (5, 7, 3), (300, 512, 136), (777, 133, 201), (2049, 264, 513), (40, 4096, 1024),
+          (4100, 64, 1100)]  # (the last: more tiles than blocks that look for the largest)
+
+
+@pytest.mark.parametrize("T,K,N", SHAPES)
+@pytest.mark.parametrize("dy,ws", [(1e-9, 1e3), (3e8, 1e-6), (1e-5, 1.0)])
+@pytest.mark.parametrize("act", ["none", "gelu", "relu"])
+def test_fp16_linear_gradients_from_an_fp32_stream(act, dy, ws, T, K, N):
+    say(f"case: fp16 range, linear {act} dy {dy} w {ws} T {T} K {K} N {N}")
+    x, w = rand(1, T, K, dtype=F16), rand(2, N, K, std=ws, dtype=F16)
+    z, dout = rand(6, T, N, dtype=F16), rand(8, T, N, std=dy)
+    dx, dw, db = Linear(w, rand(4, N, dtype=F16), act=act, out_dtype=torch.float32).backward(
+        x, dout, z=z, w_grad_dtype=torch.float32)
+    (dz, e, r), = scaled_half(*R.grads(dout.double(), z.double(), act, F16))
+    R.check("dx", dx, R.rounded(*R.product(dz, w.double().t().contiguous(), r), F16))
+    R.check("dw", dw, R.rounded(*R.product(dz.t(), x.double().t(), r.t()), torch.float32))
+    R.check("dbias", db, R.colsum(dz, e, torch.float32))
+
+
+@pytest.mark.parametrize("T,d,I", SHAPES)
+@pytest.mark.parametrize("std_h,std_b,std_w", [(30.0, 1e4, 1e-6), (1e-4, 1e-4, 1e3), (0.02, 1.0, 0.05)])
+def test_fp16_gated_gradients_out_of_range(std_h, std_b, std_w, T, d, I):
+    say(f"case: fp16 range, gated dh {std_h} b {std_b} w {std_w} T {T} d {d} I {I}")
+    x, wg, wu = rand(1, T, d, dtype=F16), rand(2, I, d, std=std_w, dtype=F16), rand(3, I, d, std=std_w, dtype=F16)
+    a, b, dh = rand(6, T, I, dtype=F16), rand(7, T, I, std=std_b, dtype=F16), rand(8, T, I, std=std_h, dtype=F16)
+    a, b, dh = a.clamp(-9, 9), b.clamp(-6e4, 6e4), dh.clamp(-200, 200)
+    outs = GatedProjection(wg, wu).backward(x, a, b, dh, w_grad_dtype=torch.float32)
+    (da, _, ra), (db, _, rb) = scaled_half(*R.grads(dh.double(), a.double(), "silu", F16, b.double()))
+    both = torch.cat([wg, wu], 0).double().t().contiguous()
+    R.check("dx", outs[0], R.rounded(*R.product(torch.cat([da, db], 1), both, torch.cat([ra, rb], 1)), F16))
+    R.check("dw_gate", outs[1], R.rounded(*R.product(da.t(), x.double().t(), ra.t()), torch.float32))
+    R.check("dw_up", outs[2], R.rounded(*R.product(db.t(), x.double().t(), rb.t()), torch.float32))
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 125, 1e30, 1.0, 1e-30, 2.0 ** -126, 2.0 ** -140])
+def test_fp16_weight_gradients_over_the_fp32_exponents(scale):
+    """dW in fp32 from an fp32 dy of any size.  (From 2^-112 down the power of two stays at 2^126: half a
+    subnormal step is 2^-151.)"""
+    say(f"case: fp16 range, dy {scale}")
+    T, K, N = 70, 96, 40
+    x, w, dout = rand(1, T, K, dtype=F16), rand(2, N, K, dtype=F16), (rand(8, T, N).clamp(-3.9, 3.9).double() * scale).float()
+    dw = Linear(w, out_dtype=torch.float32).backward(x, dout, w_grad_dtype=torch.float32, need_dx=False)[1]
+    (dz, e, r), = scaled_half(*R.grads(dout.double(), dout.double(), "none", F16))
+    ref, err = R.product(dz.t(), x.double().t(), (r + 2.0 ** -151).t())
+    ref, err = R.rounded(ref, err, torch.float32)
+    # (sums of 70 products of up to 2^127 x 4 pass fp32's largest value: those round to infinity)
+    fits, past = (ref.abs() + err < torch.finfo(torch.float32).max), (ref.abs() - err > torch.finfo(torch.float32).max)
+    R.check("dw", dw[fits], (ref[fits], err[fits]))
+    assert torch.equal(dw[past].double(), torch.sign(ref[past]) * float("inf"))
+
+
+@pytest.mark.parametrize("T", [3, 70, 600])
+def test_fp16_scale_and_special_values(T):
+    """The scale is that of the finite gradients: infinities and NaN change only what they are part of, and
+    no gradient at all is a gradient of zeros."""
+    say(f"case: fp16 range, special values T {T}")
+    K, N = 136, 72
+    x, w, dout = rand(1, T, K, dtype=F16), rand(2, N, K, std=1e3, dtype=F16), rand(8, T, N, std=1e-8)
+    lin = Linear(w, out_dtype=torch.float32)
+    (dz, e, r), = scaled_half(*R.grads(dout.double(), dout.double(), "none", F16))
+    refx = R.rounded(*R.product(dz, w.double().t().contiguous(), r), F16)
+    refw = R.rounded(*R.product(dz.t(), x.double().t(), r.t()), torch.float32)
+    rows, cols = torch.arange(T, device="cuda") != T // 2, torch.arange(N, device="cuda") != 9
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        db = dout.clone()
+        db[T // 2, 9] = bad
+        dx, dw, _ = lin.backward(x, db, w_grad_dtype=torch.float32)
+        R.check("dx", dx[rows], [v[rows] for v in refx])
+        R.check("dw", dw[cols], [v[cols] for v in refw])
+        assert not dx[T // 2].isfinite().any() and not dw[9].isfinite().any()
+    dx, dw, _ = lin.backward(x, torch.zeros_like(dout), w_grad_dtype=torch.float32)
+    assert not dx.any() and not dw.any()
+    dx, dw, _ = lin.backward(x, torch.full_like(dout, float("inf")), w_grad_dtype=torch.float32)
+    assert not dx.isfinite().any() and not dw.isfinite().any()
+
+
+def test_fp16_range_in_a_captured_graph():
+    """Each replay finds the scale of its own gradients."""
+    T, K, N = 200, 136, 264
+    x, w = rand(1, T, K, dtype=F16), rand(2, N, K, dtype=F16)
+    lin = Linear(w, out_dtype=torch.float32)
+    douts = [rand(8 + i, T, N, std=s) for i, s in enumerate((1e-9, 1e7, 1.0, 1e-20))]
+    want = [lin.backward(x, t, w_grad_dtype=torch.float32) for t in douts]
+    torch.cuda.synchronize()
+    cur, side, g = douts[0].clone(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=side):
+        outs = lin.backward(x, cur, w_grad_dtype=torch.float32)
+    for i in (1, 0, 2, 3, 1, 2):
+        cur.copy_(douts[i])
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(p is None or torch.equal(p, q) for p, q in zip(outs, want[i])), f"replay of gradients {i} differs"
+        again = lin.backward(x, douts[(i + 1) % 4], w_grad_dtype=torch.float32)
+        assert all(p is None or torch.equal(p, q) for p, q in zip(again, want[(i + 1) % 4]))
