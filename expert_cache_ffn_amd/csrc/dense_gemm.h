@@ -27,8 +27,10 @@
 // left out, ml' + lm' + ll', is below 2^-22 |x x'| and of either sign, as the
 // rounding of an fp32 sum of a few terms is.  Six bf16 MFMAs of 16 k take 192 cycles
 // of the matrix pipe, the eight fp32 ones they replace 512.  An infinity or NaN goes
-// into l alone, which meets only h' and so gives what it should (but infinity times
-// infinity gives NaN); parts below bf16's subnormals are lost, 2^-134 |x'| per product.
+// into l alone, which meets only h', and so gives what it should; an infinity's h is
+// 2^-100 of its sign, for the other operand's infinity in l' to meet (beside a finite x'
+// it adds 2^-100 x' to an infinity).  Parts below bf16's subnormals are lost, 2^-134 |x'|
+// per product.
 //
 // Output goes out by rows through LDS, 8 columns per lane: bias, activation,
 // residual and the gated product are applied there to the fp32 sums, and loads
@@ -273,7 +275,9 @@ __device__ __forceinline__ void split8_odd(const u32x4_t v[2], u32x4_t part[3])
         if ((u & 0x7f800000u) == 0x7f800000u) {
             const uint32_t keep = j & 1 ? 0x0000ffffu : 0xffff0000u;
             const uint32_t top = (u & 0x7fffffu) ? u | 0x400000u : u;  // a NaN stays one in 16 bits
-            part[0][j >> 1] &= keep;
+            // h of an infinity: +-2^-100 in bf16
+            const uint32_t h = (u & 0x7fffffu) ? 0u : (u >> 16 & 0x8000u) | 0x0d80u;
+            part[0][j >> 1] = (part[0][j >> 1] & keep) | (j & 1 ? h << 16 : h);
             part[1][j >> 1] &= keep;
             part[2][j >> 1] = (part[2][j >> 1] & keep) | (j & 1 ? top & 0xffff0000u : top >> 16);
         }

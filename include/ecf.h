@@ -360,9 +360,9 @@ int ecf_bandwidth_profile(const ecf_shape *shape, int32_t n_blobs, const void *c
  * two that the call finds from the largest finite one: none of them overflows, those
  * within 2^-28 of the largest keep all 11 bits, and those below 2^-39 of it count as
  * zero.  Results do not depend on what runs beside a call, and the same call gives the
- * same bits.  An infinite or NaN element makes
- * outputs infinite or NaN only in rows (columns) that it is part of (in fp32 an
- * infinity times an infinity counts as NaN).
+ * same bits.  An infinite or NaN element makes outputs infinite or NaN only in rows
+ * (columns) that it is part of, as IEEE products and sums do (in fp32 an infinity times
+ * a magnitude below 2^-126 may count as times zero).
  *
  * d_ws needs ecf_*_workspace_bytes bytes at a 256-byte boundary (where that is 0 it may be
  * NULL), holds nothing between calls, and must not be shared by calls that may overlap (two

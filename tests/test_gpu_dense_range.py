@@ -121,3 +121,36 @@ def test_fp16_range_in_a_captured_graph():
         assert all(p is None or torch.equal(p, q) for p, q in zip(outs, want[i])), f"replay of gradients {i} differs"
         again = lin.backward(x, douts[(i + 1) % 4], w_grad_dtype=torch.float32)
         assert all(p is None or torch.equal(p, q) for p, q in zip(again, want[(i + 1) % 4]))
+
+
+def kind(t):
+    """0 finite, 1 NaN, 2 infinity, -2 minus infinity."""
+    t = t.double().cpu()
+    return torch.where(t.isnan(), 1, torch.where(t.isinf(), 2 * torch.sign(t), 0.0))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,K,N", [(5, 40, 24), (64, 200, 150), (65, 200, 150), (300, 137, 131), (1000, 264, 520), (70, 6, 5)])
+def test_infinities_and_nans_that_meet(T, K, N, dt):
+    """Infinities of either sign against infinities, zeros, NaN and finite values at the same k: every kernel
+    gives what IEEE products and sums give, whatever the sizes."""
+    say(f"case: infinities that meet T {T} K {K} N {N} {dt}")
+    dtype = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": F16}[dt]
+    inf, nan = float("inf"), float("nan")
+    x, w = rand(1, T, K, dtype=dtype), rand(2, N, K, dtype=dtype)
+    for i, v in enumerate((inf, -inf, inf, nan, 0.0)):  # rows of x and of w that hold one each, all at k 3
+        x[(7 * i + 1) % T, 3] = v
+        w[(3 * i + 2) % N, 3] = v
+    x[T - 1, K - 1], w[N - 1, K - 1] = -inf, inf
+    x[0, 0] = inf
+    w[0, 0], w[1, 0] = 0.0, -inf
+    ref = kind(x.double().cpu() @ w.double().cpu().t())
+    assert {-2.0, 1.0, 2.0} <= set(ref.unique().tolist())
+    assert torch.equal(kind(Linear(w, out_dtype=torch.float32).forward(x)), ref)
+    _, a, b = GatedProjection(w, w, act="none").forward(x, save=True)
+    assert torch.equal(kind(a), ref) and torch.equal(kind(b), ref)
+    # the same product as dz W and as dz^T x (without an activation dy is dz)
+    wt = w.t().contiguous()
+    assert torch.equal(kind(Linear(wt).backward(rand(3, T, N, dtype=dtype), x, need_dw=False)[0]), ref)
+    dw = Linear(rand(4, T, N, dtype=dtype)).backward(wt, x.t().contiguous(), need_dx=False)[1]
+    assert torch.equal(kind(dw), ref)
