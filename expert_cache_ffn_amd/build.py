@@ -13,7 +13,7 @@ BUILD = os.path.join(os.path.dirname(HERE), "_build")
 
 HIP_SRCS = ["k_route.hip", "k_decode.hip", "k_prefill.hip", "k_util.hip", "noalloc.hip", "k_dense.hip", "k_dense_few.hip",
             "k_dense_gated.hip", "k_dense_nt.hip", "k_dense_nn.hip", "k_dense_tn.hip", "k_dense_pair.hip"]
-CPP_SRCS = ["api.cpp", "cache.cpp", "qstar.cpp", "host_ffn.cpp", "bwprof.cpp", "dense.cpp"]
+CPP_SRCS = ["api.cpp", "cache.cpp", "qstar.cpp", "host_ffn.cpp", "bwprof.cpp", "dense.cpp", "dense_plan.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

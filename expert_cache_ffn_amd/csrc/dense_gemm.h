@@ -927,12 +927,4 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseGemm g, DenseGrid gr)
     });
 }
 
-// How a product is cut: the tile, the splits of K, and whether operands can go
-// straight to LDS.
-struct DensePlan {
-    int tile;  // index into the launcher's tiles
-    int splits;
-    bool dma;
-};
-
 }  // namespace ecf

@@ -52,13 +52,44 @@ struct DenseColsum {
 // The products of a backward pass, dx (n-contiguous B) and dW (m- and n-contiguous;
 // either may be null), and the column sums, in one launch or more.  ws: kDensePartialBytes.
 int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseColsum &sums, void *ws, hipStream_t st);
-// x W^T of at most kFewTokens rows as a stream of the weights (k_dense_few.hip), and
-// the time estimated for it.  It needs no workspace; up to kAlwaysFew rows it is the
-// choice whenever there is none.
+
+// ---- which kernel a product takes (dense_plan.cpp) ----------------------------------
+
+// A product in tiles: the tile, the splits of K, and whether operands can go straight
+// to LDS.
+struct DensePlan {
+    int tile;  // index into the launcher's tiles
+    int splits;
+    bool dma;
+};
+struct DenseTile {
+    int bm, bn;
+};
+DenseTile dense_tile(int dtype, bool dma, int tile);
+// x W^T of at most kFewTokens rows as a stream of the weights (k_dense_few.hip): weight
+// rows per block, groups of as many tokens (1, 2 or 4), waves per block.  It needs no
+// workspace; up to kAlwaysFew rows it is the choice whenever there is none.
+struct DenseFew {
+    int rows, groups, waves;
+};
 constexpr int kFewTokens = 64, kAlwaysFew = 16;
 constexpr int64_t kAlwaysFewX = 1 << 17;  // elements of x
-double dense_few_us(const DenseGemm &g, int cus);
-int launch_dense_few(const DenseGemm &g, int cus, hipStream_t st);
+constexpr int kFewWaves = 8;              // most waves per block
+struct DenseChoice {
+    enum Kind { kFew, kShort, kTiles } kind;
+    DensePlan tiles;
+    DenseFew few;
+};
+// room: bytes of workspace for partial sums
+DenseChoice choose_gemm(const DenseGemm &g, int cus, size_t room);
+// Both products of a backward pass in one launch, where that is the faster way.
+struct DensePair {
+    DensePlan x;
+    int splits_w;
+};
+bool choose_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t room, DensePair *out);
+
+int launch_dense_few(const DenseGemm &g, const DenseFew &f, hipStream_t st);
 // The largest workspace of any product with up to M x N outputs in each plane.
 constexpr size_t kDensePartialBytes = (size_t)32 << 20;  // fp32 sums of split products
 size_t dense_gemm_ws(int64_t M, int64_t N, int planes);

@@ -1,5 +1,5 @@
-// Dense feed-forward operators: the choice of a product's kernel, the products with
-// short rows, and the elementwise half of the backward passes.
+// Dense feed-forward operators: launches of the products by their plan, the products
+// with short rows, and the elementwise half of the backward passes.
 #include <algorithm>
 #include <atomic>
 
@@ -272,31 +272,6 @@ __global__ __launch_bounds__(256) void k_dense_colsum(DenseColsum s)
 
 namespace {
 
-// A tile of the output and what it costs: `us` per k-tile of 64 with per_cu blocks
-// on every CU (measured, K 4096), `us1` with one, `fixed` per block for filling the
-// pipeline and the epilogue.  us1 and fixed are fitted to every tile and split of
-// 6000 products of 1 to 8192 tokens and up to 40 GFLOP: the choice takes 1.7% longer
-// than the best of them on the geometric mean.
-struct TileCost {
-    int bm, bn, per_cu;
-    double us, us1, fixed;
-};
-const TileCost kTilesDma[] = {{256, 256, 1, 1.78, 1.78, 10.9}, {128, 256, 1, 0.98, 0.98, 5.7},
-                              {128, 128, 2, 1.05, 0.74, 5.3}, {64, 128, 2, 0.66, 0.34, 5.1},
-                              {64, 64, 2, 0.45, 0.25, 2.5}};
-const TileCost kTilesReg[] = {{256, 256, 1, 1.92, 1.92, 13.6}, {128, 256, 1, 1.14, 1.14, 8.0},
-                              {128, 128, 2, 1.25, 0.83, 7.6}, {64, 64, 2, 0.64, 0.45, 2.8}};
-const TileCost kTilesF32[] = {{128, 128, 1, 2.70, 2.70, 5.9}, {64, 128, 1, 1.75, 1.75, 6.3}, {64, 64, 1, 1.00, 1.00, 5.8}};
-constexpr int kShortK = 32;
-
-const TileCost *tiles_of(int dtype, bool dma) { return dtype == ECF_F32 ? kTilesF32 : dma ? kTilesDma : kTilesReg; }
-int tile_count(int dtype, bool dma) { return dtype == ECF_F32 ? 3 : dma ? 5 : 4; }
-
-bool aligned16(const void *p, int64_t ld, int dtype)
-{
-    return (uintptr_t)p % 16 == 0 && ld * (int64_t)dense_esize(dtype) % 16 == 0;
-}
-
 // CUs of the current device, asked once per device.
 int cu_count(int *out)
 {
@@ -312,146 +287,12 @@ int cu_count(int *out)
     return ECF_OK;
 }
 
-constexpr int kMaxSplits = 16;
-constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, kMaxSplits};
 // Outputs of half the 256 MiB memory-side cache and more are stored past the caches:
 // 8192 x 16384 bf16 of K 4096 907 -> 879 us, 8192 x 2048 (32 MiB) within 1%, and there
 // the next operator finds the output in the cache.
 constexpr int64_t kStreamBytes = (int64_t)128 << 20;
-constexpr double kLaunchUs = 5.0;  // one launch more, host and device
 
-// Rows at 16-byte boundaries and whole 16-byte chunks: operands can go straight to LDS.
-bool dma_ok(const DenseGemm &g)
-{
-    if (g.dtype == ECF_F32)
-        return false;
-    for (int s = 0; s < g.ksegs || s < g.mhalves; ++s)
-        if (!aligned16(g.a[s], g.lda, g.dtype))
-            return false;
-    for (int s = 0; s < (g.gated || g.ksegs == 2 ? 2 : 1); ++s)
-        if (!aligned16(g.b[s], g.ldb, g.dtype))
-            return false;
-    return (g.a_padded || (g.a_t ? g.M : g.K) % 8 == 0) && (g.b_t ? g.N : g.K) % 8 == 0;
-}
-
-// Rows too short for the MFMA tiles' chunks, or (fp32) a reduction too short to be worth them.
-bool short_rows(const DenseGemm &g)
-{
-    return (g.a_t ? g.M : g.K) < 8 || (g.b_t ? g.N : g.K) < 8 || (g.dtype == ECF_F32 && g.K < kShortK);
-}
-
-int ktiles(const DenseGemm &g) { return (g.K + 63) / 64 * g.ksegs; }
-int64_t out_tiles(const DenseGemm &g, const TileCost &c)
-{
-    const int bn = c.bn / (g.gated ? 2 : 1);
-    return (int64_t)((g.M + c.bm - 1) / c.bm) * g.mhalves * ((g.N + bn - 1) / bn);
-}
-// Bytes of the partial sums, and the join's time for them.
-double partial_bytes(const DenseGemm &g, int splits)
-{
-    return (double)splits * (g.gated ? 2 : g.mhalves) * g.M * ((g.N + 7) / 8 * 8) * 4;
-}
-double join_us(const DenseGemm &g, int splits) { return splits > 1 ? 3.0 + partial_bytes(g, splits) * 2 / 5e6 : 0.0; }
-bool may_split(const DenseGemm &g, int splits, size_t room)
-{
-    return splits == 1 || (ktiles(g) / splits >= 2 && partial_bytes(g, splits) <= (double)room);
-}
-
-// The tile and the splits of K with the least estimated time: rounds of blocks
-// over the CUs times the k-tiles each walks, plus the join of the splits.
-DensePlan plan_gemm(const DenseGemm &g, int cus, size_t room, double *us_out)
-{
-    DensePlan best{0, 1, dma_ok(g)};
-    const int n_tiles = tile_count(g.dtype, best.dma), kt = ktiles(g);
-    const TileCost *tiles = tiles_of(g.dtype, best.dma);
-    *us_out = 1e300;
-    for (int t = 0; t < n_tiles; ++t) {
-        const TileCost &c = tiles[t];
-        for (const int s : kSplits) {
-            if (!may_split(g, s, room))
-                break;
-            // full rounds of per_cu blocks on every CU, then what is left
-            const int64_t blocks = out_tiles(g, c) * s, round = (int64_t)cus * c.per_cu, rest = blocks % round;
-            const double walk = (double)((kt + s - 1) / s);
-            const double tail = rest == 0 ? 0.0 : walk * (rest <= cus ? c.us1 : c.us) + c.fixed;
-            const double us = (double)(blocks / round) * (walk * c.us + c.fixed) + tail + join_us(g, s);
-            if (us < *us_out) {
-                *us_out = us;
-                best.tile = t;
-                best.splits = s;
-            }
-        }
-    }
-    return best;
-}
-
-// When the last of n1 blocks that take k1 and, behind them, n2 that take k2 (k1 >= k2)
-// is done, on `slots` slots that each take the next block when they are free.
-double makespan(int64_t n1, double k1, int64_t n2, double k2, int64_t slots)
-{
-    const int64_t left = n1 % slots;  // slots that start one more long block at t0
-    const double t0 = (double)(n1 / slots) * k1;
-    double t = left ? t0 + k1 : t0;
-    if (n2 == 0)
-        return t;
-    // the others go on with short blocks at t0, those `left` at t0 + k1
-    int64_t early = 0, late = 0;
-    while (early * (slots - left) + late * left < n2) {
-        const double next_early = t0 + (double)(early + 1) * k2, next_late = t0 + k1 + (double)(late + 1) * k2;
-        if (left == 0 || (left < slots && next_early <= next_late)) {
-            ++early;
-            t = std::max(t, next_early);
-        } else {
-            ++late;
-            t = std::max(t, next_late);
-        }
-        if (early + late > 64)  // many rounds: the work over all slots says it well enough
-            return std::max(t, ((double)n1 * k1 + (double)n2 * k2) / (double)slots);
-    }
-    return t;
-}
-
-// The same for two products in one launch.
-struct PairPlan {
-    DensePlan x;
-    int splits_w;
-};
-PairPlan plan_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t room, double *us_out)
-{
-    PairPlan best{{0, 1, dma_ok(gx) && dma_ok(gw)}, 1};
-    const int n_tiles = tile_count(gx.dtype, best.x.dma);
-    const TileCost *tiles = tiles_of(gx.dtype, best.x.dma);
-    *us_out = 1e300;
-    for (int t = gx.dtype == ECF_F32 ? 0 : 2; t < n_tiles; ++t) {  // (the large 16-bit tiles: apart)
-        const TileCost &c = tiles[t];
-        const int64_t slots = (int64_t)cus * c.per_cu;
-        for (const int sx : kSplits) {
-            if (!may_split(gx, sx, room))
-                break;
-            for (const int sw : kSplits) {
-                // (one of the two reductions is long, and splitting the short one too
-                // gains nothing)
-                if ((sx > 2 && sw > 2) || !may_split(gw, sw, room))
-                    break;
-                const int64_t bx = out_tiles(gx, c) * sx, bw = out_tiles(gw, c) * sw;
-                const double us_k = bx + bw <= cus ? c.us1 : c.us;
-                const double tx = (double)((ktiles(gx) + sx - 1) / sx) * us_k + c.fixed;
-                const double tw = (double)((ktiles(gw) + sw - 1) / sw) * us_k + c.fixed;
-                const double us = (tx >= tw ? makespan(bx, tx, bw, tw, slots) : makespan(bw, tw, bx, tx, slots)) +
-                                  join_us(gx, sx) + join_us(gw, sw);
-                if (us < *us_out) {
-                    *us_out = us;
-                    best.x.tile = t;
-                    best.x.splits = sx;
-                    best.splits_w = sw;
-                }
-            }
-        }
-    }
-    return best;
-}
-
-DenseGrid grid_of(const DenseGemm &g, const TileCost &t, int splits, void *ws)
+DenseGrid grid_of(const DenseGemm &g, const DenseTile &t, int splits, void *ws)
 {
     const int bn = g.gated ? t.bn / 2 : t.bn;
     DenseGrid gr{};
@@ -466,12 +307,6 @@ DenseGrid grid_of(const DenseGemm &g, const TileCost &t, int splits, void *ws)
 
 }  // namespace
 
-size_t dense_gemm_ws(int64_t M, int64_t N, int planes)
-{
-    const size_t all = (size_t)kMaxSplits * planes * M * ((N + 7) / 8 * 8) * 4;
-    return std::min(all, kDensePartialBytes);
-}
-
 int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
 {
     DenseGemm g = gin;
@@ -481,12 +316,10 @@ int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
     const int rc = cu_count(&cus);
     if (rc != ECF_OK)
         return rc;
-    const bool few = !g.a_t && !g.b_t && g.M <= kFewTokens;
-    if (few && !ws && g.M <= kAlwaysFew)
-        return launch_dense_few(g, cus, st);
-    if (short_rows(g)) {
-        if (few)
-            return launch_dense_few(g, cus, st);
+    const DenseChoice c = choose_gemm(g, cus, ws ? kDensePartialBytes : 0);
+    if (c.kind == DenseChoice::kFew)
+        return launch_dense_few(g, c.few, st);
+    if (c.kind == DenseChoice::kShort) {
         const int tiles_n = (g.N + TN - 1) / TN;
         const dim3 grid((unsigned)tiles_n * ((g.M + TM - 1) / TM) * g.mhalves);
         auto go = [&](auto e) {
@@ -505,11 +338,8 @@ int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
         ECF_HIP_CHECK(hipGetLastError());
         return ECF_OK;
     }
-    double us;
-    const DensePlan plan = plan_gemm(g, cus, ws ? kDensePartialBytes : 0, &us);
-    if (few && dense_few_us(g, cus) <= us)
-        return launch_dense_few(g, cus, st);
-    const DenseGrid gr = grid_of(g, tiles_of(g.dtype, plan.dma)[plan.tile], plan.splits, ws);
+    const DensePlan &plan = c.tiles;
+    const DenseGrid gr = grid_of(g, dense_tile(g.dtype, plan.dma, plan.tile), plan.splits, ws);
     return g.gated ? launch_gemm_gated(g, plan, gr, st)
            : g.a_t ? launch_gemm_tn(g, plan, gr, st)
            : g.b_t ? launch_gemm_nn(g, plan, gr, st)
@@ -518,19 +348,16 @@ int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
 
 int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseColsum &sums, void *ws, hipStream_t st)
 {
-    if (gx && gw && !short_rows(*gx) && !short_rows(*gw)) {
+    if (gx && gw) {
         int cus = 0;
         const int rc = cu_count(&cus);
         if (rc != ECF_OK)
             return rc;
         constexpr size_t half = kDensePartialBytes / 2;
-        double ux, uw, both;
-        plan_gemm(*gx, cus, kDensePartialBytes, &ux);
-        plan_gemm(*gw, cus, kDensePartialBytes, &uw);
-        const PairPlan p = plan_pair(*gx, *gw, cus, half, &both);
-        if (both < ux + uw + kLaunchUs) {
+        DensePair p;
+        if (choose_pair(*gx, *gw, cus, kDensePartialBytes, &p)) {
             ProfScope scope("dense_gemm_pair", st);
-            const TileCost &t = tiles_of(gx->dtype, p.x.dma)[p.x.tile];
+            const DenseTile t = dense_tile(gx->dtype, p.x.dma, p.x.tile);
             return launch_gemm_pair(*gx, grid_of(*gx, t, p.x.splits, ws), *gw,
                                     grid_of(*gw, t, p.splits_w, (char *)ws + half), sums, p.x, st);
         }

@@ -91,8 +91,6 @@ __device__ __forceinline__ u32x4_t chunk_of(const void *row, int ch, int K)
     return v;
 }
 
-constexpr int kFewWaves = 8;  // most waves per block
-
 // grid: one block per RT weight rows
 template <class E, bool GATED, int RT, int TG>
 __global__ __launch_bounds__(64 * kFewWaves) void k_dense_few(DenseGemm g)
@@ -218,42 +216,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_dense_few(DenseGemm g)
     }
 }
 
-// Rows per block (4, 8 or 16; at most four groups of tokens) with the least time, and
-// that time in us.  A CU takes in about 40 KB/us of weights and x together, whatever
-// it is (4096 x 4096 bf16: 8 tokens 9.9 us, 64 tokens 21 us; 1024 x 4096: 4.4 and 7.6),
-// and 17 KB/us where 16-bit rows start at odd elements, whose loads the hardware
-// splits (7353 x 2048 bf16, 8 tokens: 20.8 us).  Fitted against the tiles on 840 calls
-// of up to 64 tokens: the choice between the two costs 1.5% over the better one.
-int few_rows(const DenseGemm &g, int cus, double *us)
-{
-    const int es = (int)dense_esize(g.dtype), h = g.gated ? 2 : 1;
-    const bool odd = es == 2 && (g.lda % 2 || g.ldb % 2 || ((uintptr_t)g.a[0] | (uintptr_t)g.b[0]) % 4);
-    int best = 16;
-    *us = 1e300;
-    for (int rt = 4; rt <= 16; rt *= 2) {
-        const int64_t blocks = (g.N + rt - 1) / rt, tokens = (g.M + rt - 1) / rt * rt;
-        if (tokens > 4 * rt)
-            continue;
-        const double t = (es == 2 ? 4.0 : 2.5) +
-                         (double)((blocks + cus - 1) / cus) * (rt * h + tokens) * g.K * es / (odd ? 17e3 : es == 2 ? 42e3 : 38e3);
-        if (t < *us) {
-            *us = t;
-            best = rt;
-        }
-    }
-    return best;
-}
-
 template <class E, bool GATED>
-void run_few(const DenseGemm &g, int cus, hipStream_t st)
+void run_few(const DenseGemm &g, const DenseFew &f, hipStream_t st)
 {
-    double us;
-    const int rt = few_rows(g, cus, &us);
-    const int groups = (g.M + rt - 1) / rt;
-    const int epc = 16 / (int)sizeof(typename E::raw);
-    const int steps = (g.K + epc * 64 / rt - 1) / (epc * 64 / rt);
-    const int waves = steps >= 2 * kFewWaves ? kFewWaves : steps >= 4 ? 4 : 1;
-    const dim3 grid((g.N + rt - 1) / rt), block(64 * waves);
+    const int rt = f.rows, groups = f.groups;
+    const dim3 grid((g.N + rt - 1) / rt), block(64 * f.waves);
 #define ECF_FEW(R, G) hipLaunchKernelGGL((k_dense_few<E, GATED, R, G>), grid, block, 0, st, g)
     if (rt == 16) {
         if (groups == 1)
@@ -282,21 +249,14 @@ void run_few(const DenseGemm &g, int cus, hipStream_t st)
 
 }  // namespace
 
-double dense_few_us(const DenseGemm &g, int cus)
-{
-    double us;
-    few_rows(g, cus, &us);
-    return us;
-}
-
-int launch_dense_few(const DenseGemm &g, int cus, hipStream_t st)
+int launch_dense_few(const DenseGemm &g, const DenseFew &f, hipStream_t st)
 {
     auto go = [&](auto e) {
         using E = decltype(e);
         if (g.gated)
-            run_few<E, true>(g, cus, st);
+            run_few<E, true>(g, f, st);
         else
-            run_few<E, false>(g, cus, st);
+            run_few<E, false>(g, f, st);
     };
     if (g.dtype == ECF_F32)
         go(F32{});

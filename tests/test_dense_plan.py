@@ -1,0 +1,87 @@
+"""CPU tests of the dense operators' plan: which kernel each call takes, on 256 CUs.
+The GPU tests pick their sizes so that between them every kernel runs; here the same
+sizes go through the same plan, so that a change of its costs cannot leave a kernel
+untested without a test failing."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+import dense_host
+import expert_cache_ffn_amd as ecf
+import test_gpu_dense as G
+import test_gpu_dense_kernels as GK
+
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    return dense_host.build(tmp_path_factory.mktemp("dense_host"))
+
+
+def parameters(test, names):
+    """The values a GPU test is parametrised with."""
+    return next(m.args[1] for m in test.pytestmark if m.name == "parametrize" and m.args[0] == names)
+
+
+def ok(r):
+    assert r[0] == ecf.ECF_OK
+    return [q for q in r[1] if q["kind"] != "grad"]
+
+
+def layout(q):
+    return "gated" if q["gated"] else "tn" if q["at"] else "nn" if q["bt"] else "nt"
+
+
+def launched(host, dt):
+    """Every product that the GPU tests of tiles, streaming, single gradients, short rows and the SIZES and LARGE
+    lists run in type dt."""
+    seen = []
+    none = ecf.ECF_ACT_NONE
+    if dt != "f32":
+        for M, N, K in G.TILES:
+            seen += ok(host.call("linear_forward", M, K, N, dt, none)) + ok(host.call("gated_forward", M, K, N, dt, none))
+            seen += ok(host.call("linear_backward", M, N, K, dt, none, dw=False))
+            seen += ok(host.call("linear_backward", K, N, M, dt, none, dx=False, db=False))
+    for T, K, N in parameters(G.test_few_tokens, "T,K,N"):
+        seen += ok(host.call("linear_forward", T, K, N, dt, out_dt="f32")) + ok(host.call("gated_forward", T, K, N, dt))
+    for T, K, N in G.ONE:
+        seen += ok(host.call("linear_backward", T, K, N, dt, none, dw=False))
+        seen += ok(host.call("linear_backward", T, K, N, dt, none, dx=False)) + ok(host.call("linear_forward", T, K, N, dt, none))
+        if N * K * T < 1 << 34:
+            seen += ok(host.call("gated_forward", T, K, N, dt)) + ok(host.call("gated_backward", T, K, N, dt, dw=False))
+            seen += ok(host.call("gated_backward", T, K, N, dt, dx=False, db=False))
+    for T, K, N in GK.SPLIT_DW:
+        seen += ok(host.call("linear_backward", T, K, N, dt, dx=False, gd="f32"))
+    for T, d, n in G.SIZES + G.LARGE + parameters(G.test_gated_short_rows, "T,d,I"):
+        for op in ("gated_forward", "gated_backward", "linear_forward", "linear_backward"):
+            seen += ok(host.call(op, T, d, n, dt))
+    return seen
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_the_gpu_tests_run_every_kernel(host, dt):
+    seen = launched(host, dt)
+    tiles = {(layout(q), q["dma"], q["tile"]) for q in seen if q["kind"] == "tiles"}
+    kinds = [(0, 3)] if dt == "f32" else [(0, 4), (1, 5)]
+    assert tiles == {(lay, dma, t) for lay in ("gated", "nt", "nn", "tn") for dma, n in kinds for t in range(n)}
+    # both with and without a join, in every layout
+    assert {(layout(q), q["splits"] > 1) for q in seen if q["kind"] == "tiles"} == {
+        (lay, s) for lay in ("gated", "nt", "nn", "tn") for s in (False, True)}
+    pairs = {(q["dma"], q["tile"]) for q in seen if q["kind"] == "pair"}
+    assert pairs == ({(0, t) for t in range(3)} if dt == "f32" else {(0, 2), (0, 3), (1, 2), (1, 3), (1, 4)})
+    few = {(q["gated"], q["rows"], q["groups"]) for q in seen if q["kind"] == "few"}
+    assert few == {(g, r, t) for g in (0, 1) for r in (4, 8, 16) for t in (1, 2, 4)}
+    assert {q["waves"] for q in seen if q["kind"] == "few"} == {1, 4, 8}
+    assert {layout(q) for q in seen if q["kind"] == "short"} == {"gated", "nt", "nn", "tn"}
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_host_code_under_sanitizers(tmp_path):
+    exe = str(tmp_path / "dense_checks")
+    subprocess.run(["g++", *dense_host.FLAGS, "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined",
+                    *dense_host.SOURCES, os.path.join(dense_host.HERE, "sanitize", "dense_checks.cpp"), "-o", exe], check=True)
+    p = subprocess.run([exe], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True, timeout=600)
+    assert p.returncode == 0 and "dense checks passed" in p.stdout, p.stdout[-4000:]
+    for bad in ("ERROR: AddressSanitizer", "runtime error:"):
+        assert bad not in p.stdout, p.stdout[-4000:]

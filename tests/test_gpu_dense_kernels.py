@@ -1,0 +1,35 @@
+"""GPU tests of dense calls that reach kernels or operands the other files do not."""
+import pytest
+import torch
+
+import dense_ref as R
+from expert_cache_ffn_amd.layer import GatedProjection, Linear
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+# dW alone, over enough tokens to split them
+SPLIT_DW = [(5000, 130, 96), (8001, 71, 65)]
+
+
+def big(seed, *shape, std=1.0, dtype=torch.float32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,K,N", SPLIT_DW)
+def test_split_weight_gradients_alone(T, K, N, dt):
+    say(f"case: split weight gradients T {T} K {K} N {N} {dt}")
+    dtype = DT[dt]
+    x, dout = big(1, T, K, dtype=dtype), big(2, T, N, std=.1, dtype=dtype)
+    w, z = big(3, N, K, dtype=dtype), big(4, T, N, dtype=dtype)
+    ref = R.linear_backward(x.double(), w.double(), z.double(), dout.double(), "silu", dtype, dtype, torch.float32)
+    layer = Linear(w, big(5, N, dtype=dtype), act="silu")
+    dx, dw, db = layer.backward(x, dout, z, w_grad_dtype=torch.float32, need_dx=False)
+    assert dx is None
+    R.check("dw", dw, ref["dw"])
+    R.check("dbias", db, ref["dbias"])
+    assert torch.equal(layer.backward(x, dout, z, w_grad_dtype=torch.float32, need_dx=False)[1], dw)
