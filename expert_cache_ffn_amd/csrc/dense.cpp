@@ -203,7 +203,7 @@ int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
         g.bias[0] = a->d_b_gate, g.bias[1] = a->d_b_up;
         g.out[0] = a->d_h;
         g.save[0] = a->d_a, g.save[1] = a->d_b;
-        return launch_dense_gemm(g, need ? a->d_ws : nullptr, (hipStream_t)a->stream);
+        return launch_dense_gemm(g, need ? a->d_ws : nullptr, need, (hipStream_t)a->stream);
     });
 }
 
@@ -289,7 +289,8 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         gw.M = a->inter, gw.N = a->hidden, gw.K = T;
         gw.out[0] = a->d_dw_gate, gw.out[1] = a->d_dw_up;
         gw.ldout = lddw;
-        return launch_dense_backward(want_dx ? &gx : nullptr, want_dw ? &gw : nullptr, sums, (char *)a->d_ws + w.split, st);
+        return launch_dense_backward(want_dx ? &gx : nullptr, want_dw ? &gw : nullptr, sums, (char *)a->d_ws + w.split,
+                                     w.total - w.split, st);
     });
 }
 
@@ -343,7 +344,7 @@ int ecf_linear_forward(const ecf_linear_args *a, int32_t T)
         g.res = a->d_residual;
         g.out[0] = a->d_out;
         g.save[0] = a->d_z;
-        return launch_dense_gemm(g, need ? a->d_ws : nullptr, (hipStream_t)a->stream);
+        return launch_dense_gemm(g, need ? a->d_ws : nullptr, need, (hipStream_t)a->stream);
     });
 }
 
@@ -426,7 +427,8 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         gw.M = a->out_features, gw.N = a->in_features, gw.K = T;
         gw.out[0] = a->d_dw;
         gw.ldout = lddw;
-        return launch_dense_backward(want_dx ? &gx : nullptr, a->d_dw ? &gw : nullptr, sums, (char *)a->d_ws + w.split, st);
+        return launch_dense_backward(want_dx ? &gx : nullptr, a->d_dw ? &gw : nullptr, sums, (char *)a->d_ws + w.split,
+                                     w.total - w.split, st);
     });
 }
 

@@ -38,8 +38,9 @@ struct DenseGemm {
     const float *unscale;
     bool stream_out;  // set by the launcher: the output does not fit the caches
 };
-// ws: room for dense_gemm_ws bytes (may be null where that is 0)
-int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t st);
+// ws: `room` bytes for the partial sums of a split K (may be null where that is 0); a
+// plan that needs more is not taken
+int launch_dense_gemm(const DenseGemm &g, void *ws, size_t room, hipStream_t st);
 // Column sums still to be joined over the row blocks of launch_dense_grad: fp32
 // partial [row_blocks][n I], the first I columns into out[0], the others into out[1]
 // (each may be null).  A block takes 64 columns.
@@ -50,8 +51,9 @@ struct DenseColsum {
     int blocks;  // 0: nothing to join
 };
 // The products of a backward pass, dx (n-contiguous B) and dW (m- and n-contiguous;
-// either may be null), and the column sums, in one launch or more.  ws: kDensePartialBytes.
-int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseColsum &sums, void *ws, hipStream_t st);
+// either may be null), and the column sums, in one launch or more.
+int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseColsum &sums, void *ws, size_t room,
+                          hipStream_t st);
 
 // ---- which kernel a product takes (dense_plan.cpp) ----------------------------------
 
@@ -80,12 +82,14 @@ struct DenseChoice {
     DensePlan tiles;
     DenseFew few;
 };
-// room: bytes of workspace for partial sums
+// room: bytes of workspace for partial sums, dense_partials of which the choice needs
+size_t dense_partials(const DenseGemm &g, int splits);
 DenseChoice choose_gemm(const DenseGemm &g, int cus, size_t room);
 // Both products of a backward pass in one launch, where that is the faster way.
 struct DensePair {
     DensePlan x;
     int splits_w;
+    size_t at_w;  // dW's partial sums lie this far behind dx's
 };
 bool choose_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t room, DensePair *out);
 

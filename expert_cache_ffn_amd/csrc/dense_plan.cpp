@@ -64,7 +64,7 @@ int64_t out_tiles(const DenseGemm &g, const TileCost &c)
 // Bytes of the partial sums, and the join's time for them.
 double partial_bytes(const DenseGemm &g, int splits)
 {
-    return (double)splits * (g.gated ? 2 : g.mhalves) * g.M * ((g.N + 7) / 8 * 8) * 4;
+    return splits > 1 ? (double)splits * (g.gated ? 2 : g.mhalves) * g.M * ((g.N + 7) / 8 * 8) * 4 : 0.0;
 }
 double join_us(const DenseGemm &g, int splits) { return splits > 1 ? 3.0 + partial_bytes(g, splits) * 2 / 5e6 : 0.0; }
 bool may_split(const DenseGemm &g, int splits, size_t room)
@@ -129,7 +129,8 @@ double makespan(int64_t n1, double k1, int64_t n2, double k2, int64_t slots)
 // The same for two products in one launch.
 DensePair plan_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t room, double *us_out)
 {
-    DensePair best{{0, 1, dma_ok(gx) && dma_ok(gw)}, 1};
+    DensePair best{{0, 1, dma_ok(gx) && dma_ok(gw)}, 1, 0};
+    const size_t each = kDensePartialBytes / 2;  // and both together within the room
     const int n_tiles = tile_count(gx.dtype, best.x.dma);
     const TileCost *tiles = tiles_of(gx.dtype, best.x.dma);
     *us_out = 1e300;
@@ -137,12 +138,13 @@ DensePair plan_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t ro
         const TileCost &c = tiles[t];
         const int64_t slots = (int64_t)cus * c.per_cu;
         for (const int sx : kSplits) {
-            if (!may_split(gx, sx, room))
+            if (!may_split(gx, sx, std::min(each, room)))
                 break;
+            const size_t at_w = (dense_partials(gx, sx) + 255) & ~(size_t)255;
             for (const int sw : kSplits) {
                 // (one of the two reductions is long, and splitting the short one too
                 // gains nothing)
-                if ((sx > 2 && sw > 2) || !may_split(gw, sw, room))
+                if ((sx > 2 && sw > 2) || !may_split(gw, sw, std::min(each, room - std::min(at_w, room))))
                     break;
                 const int64_t bx = out_tiles(gx, c) * sx, bw = out_tiles(gw, c) * sw;
                 const double us_k = bx + bw <= cus ? c.us1 : c.us;
@@ -155,6 +157,7 @@ DensePair plan_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t ro
                     best.x.tile = t;
                     best.x.splits = sx;
                     best.splits_w = sw;
+                    best.at_w = at_w;
                 }
             }
         }
@@ -201,6 +204,8 @@ DenseFew plan_few(const DenseGemm &g, int cus, double *us)
 
 }  // namespace
 
+size_t dense_partials(const DenseGemm &g, int splits) { return (size_t)partial_bytes(g, splits); }
+
 DenseTile dense_tile(int dtype, bool dma, int tile)
 {
     const TileCost &t = tiles_of(dtype, dma)[tile];
@@ -232,7 +237,7 @@ bool choose_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t room,
     double ux, uw, both;
     plan_gemm(gx, cus, room, &ux);
     plan_gemm(gw, cus, room, &uw);
-    *out = plan_pair(gx, gw, cus, room / 2, &both);
+    *out = plan_pair(gx, gw, cus, room, &both);
     return both < ux + uw + kLaunchUs;
 }
 

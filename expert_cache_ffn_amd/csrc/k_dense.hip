@@ -307,7 +307,7 @@ DenseGrid grid_of(const DenseGemm &g, const DenseTile &t, int splits, void *ws)
 
 }  // namespace
 
-int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
+int launch_dense_gemm(const DenseGemm &gin, void *ws, size_t room, hipStream_t st)
 {
     DenseGemm g = gin;
     g.stream_out = (int64_t)g.M * g.N * (int64_t)dense_esize(g.out_dtype) >= kStreamBytes;
@@ -316,7 +316,7 @@ int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
     const int rc = cu_count(&cus);
     if (rc != ECF_OK)
         return rc;
-    const DenseChoice c = choose_gemm(g, cus, ws ? kDensePartialBytes : 0);
+    const DenseChoice c = choose_gemm(g, cus, room);
     if (c.kind == DenseChoice::kFew)
         return launch_dense_few(g, c.few, st);
     if (c.kind == DenseChoice::kShort) {
@@ -346,20 +346,20 @@ int launch_dense_gemm(const DenseGemm &gin, void *ws, hipStream_t st)
                    : launch_gemm_nt(g, plan, gr, st);
 }
 
-int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseColsum &sums, void *ws, hipStream_t st)
+int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseColsum &sums, void *ws, size_t room,
+                          hipStream_t st)
 {
     if (gx && gw) {
         int cus = 0;
         const int rc = cu_count(&cus);
         if (rc != ECF_OK)
             return rc;
-        constexpr size_t half = kDensePartialBytes / 2;
         DensePair p;
-        if (choose_pair(*gx, *gw, cus, kDensePartialBytes, &p)) {
+        if (choose_pair(*gx, *gw, cus, room, &p)) {
             ProfScope scope("dense_gemm_pair", st);
             const DenseTile t = dense_tile(gx->dtype, p.x.dma, p.x.tile);
             return launch_gemm_pair(*gx, grid_of(*gx, t, p.x.splits, ws), *gw,
-                                    grid_of(*gw, t, p.splits_w, (char *)ws + half), sums, p.x, st);
+                                    grid_of(*gw, t, p.splits_w, (char *)ws + p.at_w), sums, p.x, st);
         }
     }
     if (sums.blocks) {
@@ -368,11 +368,11 @@ int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseC
         ECF_HIP_CHECK(hipGetLastError());
     }
     if (gx) {
-        const int rc = launch_dense_gemm(*gx, ws, st);
+        const int rc = launch_dense_gemm(*gx, ws, room, st);
         if (rc != ECF_OK)
             return rc;
     }
-    return gw ? launch_dense_gemm(*gw, ws, st) : ECF_OK;
+    return gw ? launch_dense_gemm(*gw, ws, room, st) : ECF_OK;
 }
 
 int64_t dense_grad_max_row_blocks(int64_t T) { return (T + kGradLanes - 1) / kGradLanes; }

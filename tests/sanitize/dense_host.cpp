@@ -22,7 +22,7 @@ std::string operand(const DenseGemm &g)
            num("unscale", (long long)(uintptr_t)g.unscale);
 }
 
-// bytes of the partial sums that a split product writes
+// bytes of the partial sums that a split product writes: fp32 [split][half or projection][M][N rounded up to 8]
 long long partials(const DenseGemm &g, int splits)
 {
     return splits > 1 ? (long long)splits * (g.gated ? 2 : g.mhalves) * g.M * ((g.N + 7) / 8 * 8) * 4 : 0;
@@ -46,10 +46,10 @@ int set_error(int code, const char *fmt, ...)
     return code;
 }
 
-int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t)
+int launch_dense_gemm(const DenseGemm &g, void *ws, size_t room, hipStream_t)
 {
-    const DenseChoice c = choose_gemm(g, g_cus, ws ? kDensePartialBytes : 0);
-    std::string s = operand(g) + num("ws", (long long)(uintptr_t)ws);
+    const DenseChoice c = choose_gemm(g, g_cus, room);
+    std::string s = operand(g) + num("ws", (long long)(uintptr_t)ws) + num("room", (long long)room);
     if (c.kind == DenseChoice::kFew)
         s += "\"kind\": \"few\", " + num("rows", c.few.rows) + num("groups", c.few.groups) + num("waves", c.few.waves);
     else if (c.kind == DenseChoice::kShort)
@@ -61,18 +61,20 @@ int launch_dense_gemm(const DenseGemm &g, void *ws, hipStream_t)
     return ECF_OK;
 }
 
-int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseColsum &, void *ws, hipStream_t st)
+int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseColsum &, void *ws, size_t room,
+                          hipStream_t st)
 {
     DensePair p;
-    if (gx && gw && choose_pair(*gx, *gw, g_cus, kDensePartialBytes, &p)) {
-        add(operand(*gx) + num("ws", (long long)(uintptr_t)ws) + "\"kind\": \"pair\", " + num("tile", p.x.tile) +
+    if (gx && gw && choose_pair(*gx, *gw, g_cus, room, &p)) {
+        add(operand(*gx) + num("ws", (long long)(uintptr_t)ws) + num("room", (long long)room) + num("at_w", (long long)p.at_w) +
+            "\"kind\": \"pair\", " + num("tile", p.x.tile) +
             num("dma", p.x.dma) + num("splits", p.x.splits) + num("splits_w", p.splits_w) +
             num("partials", partials(*gx, p.x.splits)) + num("partials_w", partials(*gw, p.splits_w)));
         return ECF_OK;
     }
     if (gx)
-        launch_dense_gemm(*gx, ws, st);
-    return gw ? launch_dense_gemm(*gw, ws, st) : ECF_OK;
+        launch_dense_gemm(*gx, ws, room, st);
+    return gw ? launch_dense_gemm(*gw, ws, room, st) : ECF_OK;
 }
 
 int64_t dense_grad_max_row_blocks(int64_t T) { return (T + 31) / 32; }

@@ -2,7 +2,9 @@
 The GPU tests pick their sizes so that between them every kernel runs; here the same
 sizes go through the same plan, so that a change of its costs cannot leave a kernel
 untested without a test failing."""
+import math
 import os
+import random
 import shutil
 import subprocess
 
@@ -74,6 +76,41 @@ def test_the_gpu_tests_run_every_kernel(host, dt):
     assert few == {(g, r, t) for g in (0, 1) for r in (4, 8, 16) for t in (1, 2, 4)}
     assert {q["waves"] for q in seen if q["kind"] == "few"} == {1, 4, 8}
     assert {layout(q) for q in seen if q["kind"] == "short"} == {"gated", "nt", "nn", "tn"}
+
+
+OPS = ("gated_forward", "gated_backward", "linear_forward", "linear_backward")
+
+
+def drawn(n, seed):
+    """Sizes over the whole range, their logarithms spread evenly, a multiple of 64 half of the time."""
+    r = random.Random(seed)
+
+    def size(hi):
+        v = int(round(math.exp(r.uniform(0, math.log(hi)))))
+        return v if r.random() < 0.5 else max(64, v // 64 * 64)
+
+    for _ in range(n):
+        yield r.choice(OPS), size(8192), size(16384), size(16384), r.choice(["f32", "bf16", "f16"])
+
+
+def test_partial_sums_stay_in_their_workspace(host):
+    """What a plan splits fits what the call was given, at the size the query names and not a byte less."""
+    split = 0
+    for op, T, d, n, dt in drawn(4000, 1):
+        code, launches, need = host.call(op, T, d, n, dt)
+        assert code == ecf.ECF_OK
+        base = 62 * dense_host.APART
+        for q in launches:
+            if q["kind"] == "grad" or not q["room"]:
+                assert q["kind"] == "grad" or not q.get("partials")
+                continue
+            assert base <= q["ws"] and q["ws"] + q["room"] <= base + need and q["ws"] % 256 == 0
+            assert q.get("partials", 0) <= q["room"]
+            if q["kind"] == "pair":
+                assert q["at_w"] >= q["partials"] and q["at_w"] % 256 == 0
+                assert not q["partials_w"] or q["at_w"] + q["partials_w"] <= q["room"]
+            split += bool(q.get("partials"))
+    assert split > 300
 
 
 @pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
