@@ -26,6 +26,18 @@ int check_common(const char *what, int32_t in, int32_t out, int32_t dtype, int32
     return ECF_OK;
 }
 
+// 256 rows lie within a 31-bit byte offset.
+int64_t longest_row(int dtype) { return 0x7fffffff / 256 / (int64_t)dense_esize(dtype); }
+
+// What a size query refuses: also widths that no call takes.
+int check_query(const char *what, int32_t in, int32_t out, int32_t dtype, int32_t T)
+{
+    const int rc = check_common(what, in, out, dtype, T);
+    if (rc == ECF_OK && T > 0 && std::max(in, out) > longest_row(dtype))
+        return set_error(ECF_EUNSUPPORTED, "%s: 256 rows of %d elements span 2 GiB or more", what, std::max(in, out));
+    return rc;
+}
+
 // A matrix operand: present, aligned to its element, rows at least as far apart
 // as they are long, and 256 of them within a 31-bit byte offset.
 int check_matrix(const char *what, const char *name, const void *p, int64_t ld, int64_t width, int dtype)
@@ -38,17 +50,9 @@ int check_matrix(const char *what, const char *name, const void *p, int64_t ld, 
     if (ld < width)
         return set_error(ECF_EINVAL, "%s: the row stride of %s (%lld) is below its width %lld", what, name,
                          (long long)ld, (long long)width);
-    if (ld > (int64_t)(0x7fffffff / 256 / e))
+    if (ld > longest_row(dtype))
         return set_error(ECF_EUNSUPPORTED, "%s: 256 rows of %s (stride %lld) span 2 GiB or more", what, name,
                          (long long)ld);
-    return ECF_OK;
-}
-
-// Rows of dz in the workspace obey the same limit.
-int check_pitch(const char *what, int64_t pitch, int dtype)
-{
-    if (pitch > (int64_t)(0x7fffffff / 256 / dense_esize(dtype)))
-        return set_error(ECF_EUNSUPPORTED, "%s: 256 rows of %lld gradients span 2 GiB or more", what, (long long)pitch);
     return ECF_OK;
 }
 
@@ -122,8 +126,9 @@ size_t forward_ws(int64_t T, int64_t in, int64_t out, int dtype, int planes)
     return always ? 0 : dense_gemm_ws(T, out, planes);
 }
 
-// Backward workspace: dz rows in `dtype` (gated: da and db halves of one row,
-// each half's rows at 16-byte boundaries), the column sums of each row block in
+// Backward workspace: dz rows in `dtype` (gated: all of da, then all of db), at 16-byte
+// boundaries (rows of dh or dy rounded up to 8 elements, so the last of 256 starts and
+// ends within a 31-bit byte offset as theirs does), the column sums of each row block in
 // fp32, in fp16 what the scale of dz is found from and its inverse, and the products'
 // partial sums.
 struct BackWs {
@@ -133,8 +138,8 @@ struct BackWs {
 BackWs back_ws(int64_t cols, int halves, int dtype, int32_t T)
 {
     BackWs w;
-    w.pitch = halves * ((cols + 7) / 8 * 8);
-    w.colsum = al256((size_t)T * w.pitch * dense_esize(dtype));
+    w.pitch = (cols + 7) / 8 * 8;
+    w.colsum = al256((size_t)T * w.pitch * halves * dense_esize(dtype));
     w.tops = w.colsum + al256((size_t)dense_grad_max_row_blocks(T) * halves * cols * 4);
     w.split = w.tops + (dtype == ECF_F16 ? al256((kDenseTops + 1) * 4) : 0);
     w.total = w.split + kDensePartialBytes;
@@ -156,7 +161,7 @@ extern "C" {
 
 size_t ecf_gated_workspace_bytes(int32_t hidden, int32_t inter, int32_t dtype, int32_t n_tokens, int32_t backward)
 {
-    if (check_common("ecf_gated_workspace_bytes", hidden, inter, dtype, n_tokens) != ECF_OK)
+    if (check_query("ecf_gated_workspace_bytes", hidden, inter, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
     return backward ? back_ws(inter, 2, dtype, n_tokens).total : forward_ws(n_tokens, hidden, inter, dtype, 2);
 }
@@ -241,7 +246,6 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         DENSE_TRY(check_vector(me, "d_db_gate", a->d_db_gate, a->wgrad_dtype));
         DENSE_TRY(check_vector(me, "d_db_up", a->d_db_up, a->wgrad_dtype));
         const BackWs w = back_ws(I, 2, a->dtype, T);
-        DENSE_TRY(check_pitch(me, w.pitch, a->dtype));
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
         DENSE_TRY(check_apart(me, {{"d_dx", a->d_dx}, {"d_dw_gate", a->d_dw_gate}, {"d_dw_up", a->d_dw_up},
                                    {"d_db_gate", a->d_db_gate}, {"d_db_up", a->d_db_up}, {"d_ws", a->d_ws}},
@@ -270,7 +274,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
             DENSE_TRY(launch_dense_grad(q, &sums, st));
             gx.unscale = gw.unscale = q.unscale;
         }
-        const char *dz2 = dz + (size_t)(w.pitch / 2) * dense_esize(a->dtype);
+        const char *dz2 = dz + (size_t)T * w.pitch * dense_esize(a->dtype);
         gx.dtype = gx.out_dtype = gw.dtype = a->dtype;
         gx.b_t = gw.a_t = gw.b_t = true;
         gx.ksegs = gw.mhalves = 2;
@@ -297,7 +301,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
 size_t ecf_linear_workspace_bytes(int32_t in_features, int32_t out_features, int32_t dtype, int32_t n_tokens,
                                   int32_t backward)
 {
-    if (check_common("ecf_linear_workspace_bytes", in_features, out_features, dtype, n_tokens) != ECF_OK)
+    if (check_query("ecf_linear_workspace_bytes", in_features, out_features, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
     return backward ? back_ws(out_features, 1, dtype, n_tokens).total
                     : forward_ws(n_tokens, in_features, out_features, dtype, 1);
@@ -378,7 +382,6 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
             DENSE_TRY(check_matrix(me, "d_dw", a->d_dw, lddw, K, a->wgrad_dtype));
         DENSE_TRY(check_vector(me, "d_dbias", a->d_dbias, a->wgrad_dtype));
         const BackWs w = back_ws(N, 1, a->dtype, T);
-        DENSE_TRY(check_pitch(me, w.pitch, a->dtype));
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
         DENSE_TRY(check_apart(me, {{"d_dx", a->d_dx}, {"d_dw", a->d_dw}, {"d_dbias", a->d_dbias}, {"d_ws", a->d_ws}},
                               {{"d_x", a->d_x}, {"d_w", a->d_w}, {"d_z", a->d_z}, {"d_dout", a->d_dout}}));

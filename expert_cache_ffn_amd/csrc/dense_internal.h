@@ -98,9 +98,9 @@ int launch_dense_few(const DenseGemm &g, const DenseFew &f, hipStream_t st);
 constexpr size_t kDensePartialBytes = (size_t)32 << 20;  // fp32 sums of split products
 size_t dense_gemm_ws(int64_t M, int64_t N, int planes);
 
-// dz rows of the backward passes, in the operands' type: dz[t][i] (linear) or
-// da = dz[t][i], db = dz[t][pitch / 2 + i] (gated).  Columns from I to the (half)
-// pitch, the next multiple of 8, are zeroed.  With sums, the columns are added up:
+// dz rows of the backward passes, in the operands' type: dz[t][i] (linear), or
+// da = dz[t][i] and db = dz[T + t][i] (gated).  Columns from I to the pitch, the next
+// multiple of 8, are zeroed.  With sums, the columns are added up:
 // into `sums` where one row block covers all tokens, else per row block into
 // partial [block][1 or 2][I], and `left` says what is still to be joined.
 struct DenseGrad {

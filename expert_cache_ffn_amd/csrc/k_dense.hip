@@ -194,7 +194,6 @@ __global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks,
     const int cb = (int)blockIdx.x / row_blocks, rb = (int)blockIdx.x - cb * row_blocks;
     const int cg = threadIdx.x & 7, rl = threadIdx.x >> 3;
     const int c = cb * kGradCols + cg * 8, n = g.I - c;
-    const int64_t half = g.pitch / H;
     const int t1 = min(g.T, (rb + 1) * rows);
     float sum[H][8] = {}, scale = 1.f;
     int64_t t = (int64_t)rb * rows + rl;
@@ -208,7 +207,7 @@ __global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks,
                     out[h][j] *= scale;
             }
             if (g.dz)
-                store8<E>(row_at<E>(g.dz, t * g.pitch + h * half), c, 8, out[h]);
+                store8<E>(row_at<E>(g.dz, ((int64_t)h * g.T + t) * g.pitch), c, 8, out[h]);
         }
         t += kGradLanes;
     };

@@ -408,7 +408,8 @@ typedef struct {
 } ecf_gated_args;
 
 /* Workspace bytes of a call of up to n_tokens tokens (backward 0 or 1); 0 for a valid
- * shape that needs none; SIZE_MAX for an invalid shape (ecf_last_error says why). */
+ * shape that needs none; SIZE_MAX for an invalid shape, also one whose rows are too long
+ * for any call (ecf_last_error says why). */
 size_t ecf_gated_workspace_bytes(int32_t hidden, int32_t inter, int32_t dtype, int32_t n_tokens, int32_t backward);
 int ecf_gated_forward(const ecf_gated_args *args, int32_t n_tokens);
 /* dx = da W_gate + db W_up, dW_gate = da^T x, dW_up = db^T x, db_gate = sum_t da,

@@ -122,3 +122,17 @@ def test_host_code_under_sanitizers(tmp_path):
     assert p.returncode == 0 and "dense checks passed" in p.stdout, p.stdout[-4000:]
     for bad in ("ERROR: AddressSanitizer", "runtime error:"):
         assert bad not in p.stdout, p.stdout[-4000:]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_wide_layers_are_refused_by_the_stated_limit_alone(host, dt):
+    """256 rows of every operand under 2 GiB: what meets that runs, and the size query refuses the widths whose
+    rows alone do not."""
+    limit = ((1 << 31) - 1) // 256 // dense_host.SIZE[dt]  # elements
+    for op in OPS:
+        for d, n in ((8, 1 << 20), (8, limit), (8, limit - 6), (limit, 8), (1 << 20, 1 << 20), (limit, limit)):
+            code, _, need = host.call(op, 5, d, n, dt)
+            assert code == ecf.ECF_OK and need < 1 << 62, (op, d, n, host.error())
+        for d, n in ((8, limit + 1), (limit + 1, 8)):
+            code, _, need = host.call(op, 5, d, n, dt)
+            assert code != ecf.ECF_OK and need == (1 << 64) - 1, (op, d, n)

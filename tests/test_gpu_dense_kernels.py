@@ -33,3 +33,21 @@ def test_split_weight_gradients_alone(T, K, N, dt):
     R.check("dw", dw, ref["dw"])
     R.check("dbias", db, ref["dbias"])
     assert torch.equal(layer.backward(x, dout, z, w_grad_dtype=torch.float32, need_dx=False)[1], dw)
+
+
+@pytest.mark.parametrize("dt", DT)
+def test_gradients_of_the_widest_layers(dt):
+    """inter at the longest rows that are served: da and db lie in rows as long as dh's."""
+    dtype = DT[dt]
+    T, d, I = 5, 8, ((1 << 31) - 1) // 256 // dtype.itemsize
+    say(f"case: widest gated backward T {T} d {d} I {I} {dt}")
+    x, wg, wu = big(1, T, d, dtype=dtype), big(2, I, d, std=.1, dtype=dtype), big(3, I, d, std=.1, dtype=dtype)
+    a, b, dh = big(4, T, I, dtype=dtype), big(5, T, I, dtype=dtype), big(6, T, I, std=.01, dtype=dtype)
+    outs = GatedProjection(wg, wu, wg[:, 0].contiguous(), wu[:, 0].contiguous()).backward(x, a, b, dh)
+    ref = R.gated_backward(*(t.double() for t in (x, wg, wu, a, b, dh)), "silu", dtype, dtype)
+    for name, got in zip(("dx", "dw_gate", "dw_up", "db_gate", "db_up"), outs):
+        R.check(name, got, ref[name])
+    dx, dw, db = Linear(wg, act="gelu").backward(x, dh, a)
+    ref = R.linear_backward(*(t.double() for t in (x, wg, a, dh)), "gelu", dtype, dtype, dtype)
+    R.check("dx", dx, ref["dx"])
+    R.check("dw", dw, ref["dw"])
