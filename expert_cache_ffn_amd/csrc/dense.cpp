@@ -116,14 +116,12 @@ int check_apart(const char *what, std::initializer_list<Named> outs, std::initia
             return _rc;                \
     } while (0)
 
-// A few tokens' weights are streamed, without a workspace, unless 16-bit rows of odd
-// length or a long x, which every block reads, may make that the slower way (16
-// tokens, 2 x 1024 rows in bf16: streamed and in tiles 9.2 and 10.6 us of K 4096, 15.5
-// and 13.1 of K 8192).
+// A few tokens' calls have no workspace: their weights are streamed, or (16-bit rows
+// that start at odd elements) go through tiles that do not split K.  Rows of odd length
+// always start so; there the split tiles may be the fastest.
 size_t forward_ws(int64_t T, int64_t in, int64_t out, int dtype, int planes)
 {
-    const bool always = T <= kAlwaysFew && T * in < kAlwaysFewX && (dtype == ECF_F32 || in % 2 == 0);
-    return always ? 0 : dense_gemm_ws(T, out, planes);
+    return few_needs_no_room(T, in) && (dtype == ECF_F32 || in % 2 == 0) ? 0 : dense_gemm_ws(T, out, planes);
 }
 
 // Backward workspace: dz rows in `dtype` (gated: all of da, then all of db), at 16-byte

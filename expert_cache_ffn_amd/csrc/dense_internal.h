@@ -70,12 +70,16 @@ struct DenseTile {
 DenseTile dense_tile(int dtype, bool dma, int tile);
 // x W^T of at most kFewTokens rows as a stream of the weights (k_dense_few.hip): weight
 // rows per block, groups of as many tokens (1, 2 or 4), waves per block.  It needs no
-// workspace; up to kAlwaysFew rows it is the choice whenever there is none.
+// workspace.  Up to kAlwaysFew rows of kAlwaysFewX elements together it is the faster
+// way, unless 16-bit rows start at odd elements; elsewhere the estimates decide (16
+// tokens, 2 x 1024 rows in bf16: streamed and in tiles 9.2 and 10.6 us of K 4096, 15.5
+// and 13.1 of K 8192, whose x every block reads).
 struct DenseFew {
     int rows, groups, waves;
 };
 constexpr int kFewTokens = 64, kAlwaysFew = 16;
-constexpr int64_t kAlwaysFewX = 1 << 17;  // elements of x
+constexpr int64_t kAlwaysFewX = 1 << 17;
+bool few_needs_no_room(int64_t T, int64_t in);
 constexpr int kFewWaves = 8;              // most waves per block
 struct DenseChoice {
     enum Kind { kFew, kShort, kTiles } kind;

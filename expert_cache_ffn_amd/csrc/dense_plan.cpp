@@ -165,6 +165,13 @@ DensePair plan_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t ro
     return best;
 }
 
+// 16-bit rows that start at odd elements.
+bool odd_rows(const DenseGemm &g)
+{
+    const uintptr_t at = (uintptr_t)g.a[0] | (uintptr_t)g.b[0] | (uintptr_t)(g.gated ? g.b[1] : nullptr);
+    return g.dtype != ECF_F32 && (g.lda % 2 || g.ldb % 2 || at % 4);
+}
+
 // Rows per block (4, 8 or 16; at most four groups of tokens) with the least time, and
 // that time in us.  A CU takes in about 40 KB/us of weights and x together, whatever
 // it is (4096 x 4096 bf16: 8 tokens 9.9 us, 64 tokens 21 us; 1024 x 4096: 4.4 and 7.6),
@@ -174,7 +181,7 @@ DensePair plan_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t ro
 int few_rows(const DenseGemm &g, int cus, double *us)
 {
     const int es = (int)dense_esize(g.dtype), h = g.gated ? 2 : 1;
-    const bool odd = es == 2 && (g.lda % 2 || g.ldb % 2 || ((uintptr_t)g.a[0] | (uintptr_t)g.b[0]) % 4);
+    const bool odd = odd_rows(g);
     int best = 16;
     *us = 1e300;
     for (int rt = 4; rt <= 16; rt *= 2) {
@@ -212,6 +219,8 @@ DenseTile dense_tile(int dtype, bool dma, int tile)
     return DenseTile{t.bm, t.bn};
 }
 
+bool few_needs_no_room(int64_t T, int64_t in) { return T <= kAlwaysFew && T * in < kAlwaysFewX; }
+
 DenseChoice choose_gemm(const DenseGemm &g, int cus, size_t room)
 {
     DenseChoice c{};
@@ -219,13 +228,19 @@ DenseChoice choose_gemm(const DenseGemm &g, int cus, size_t room)
     double few_us = 1e300, us;
     if (few)
         c.few = plan_few(g, cus, &few_us);
-    if ((few && !room && g.M <= kAlwaysFew) || (few && short_rows(g))) {
+    const bool always = few && few_needs_no_room(g.M, g.K);
+    if ((always && !odd_rows(g)) || (few && short_rows(g))) {
         c.kind = DenseChoice::kFew;
     } else if (short_rows(g)) {
         c.kind = DenseChoice::kShort;
     } else {
         c.tiles = plan_gemm(g, cus, room, &us);
-        c.kind = few_us <= us ? DenseChoice::kFew : DenseChoice::kTiles;
+        // Rows at odd elements: 16 x 2048 to 65536 200 us streamed, 76 in tiles; 8 x 8192
+        // to 16384 199 and 105; 2 x 128 to 256 2.5 and 4.2.  (Calls of few tokens have no
+        // room to split K, and their tiles wait for loads that the estimate takes for
+        // hidden: 16 x 4096 to 8192, estimated at 32 us, takes 54, streamed 52.  Over 34
+        // sizes the factor costs at most 1.2 us against streaming.)
+        c.kind = few_us <= us * (always ? 1.5 : 1.0) ? DenseChoice::kFew : DenseChoice::kTiles;
     }
     return c;
 }

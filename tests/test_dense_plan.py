@@ -113,6 +113,26 @@ def test_partial_sums_stay_in_their_workspace(host):
     assert split > 300
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("where", [dict(pad=1), dict(shift=1)])
+def test_few_tokens_of_rows_at_odd_elements(host, where, dt):
+    """16-bit rows that start at odd elements are read at less than half the rate by the streaming kernel: wide
+    layers of up to 16 tokens go through tiles, though they have no workspace to split K in."""
+    def kind(op, *size):
+        launch, = ok(host.call(op, *size, dt, **where))
+        assert launch["room"] == 0 and launch.get("splits", 1) == 1
+        return launch["kind"]
+
+    wide = "few" if dt == "f32" else "tiles"
+    for op, *size in GK.ODD_ROWS:
+        assert kind(op, *size) == wide
+    for T, d, n in ((1, 4096, 1024), (16, 4096, 1024), (2, 128, 256), (16, 256, 64), (9, 640, 1500)):
+        assert kind("linear_forward", T, d, n) == kind("gated_forward", T, d, n) == "few"
+    # whole rows at even elements, whatever the size
+    for op, *size in GK.ODD_ROWS:
+        assert [q["kind"] for q in ok(host.call(op, *size, dt))] == ["few"]
+
+
 @pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
 def test_host_code_under_sanitizers(tmp_path):
     exe = str(tmp_path / "dense_checks")

@@ -51,3 +51,33 @@ def test_gradients_of_the_widest_layers(dt):
     ref = R.linear_backward(*(t.double() for t in (x, wg, a, dh)), "gelu", dtype, dtype, dtype)
     R.check("dx", dx, ref["dx"])
     R.check("dw", dw, ref["dw"])
+
+
+# few tokens of wide layers, whose 16-bit rows at odd elements go through tiles without a workspace
+ODD_ROWS = [("linear_forward", 13, 2046, 34967), ("linear_forward", 1, 4080, 56412), ("linear_forward", 16, 438, 23179),
+            ("gated_forward", 16, 4096, 8192), ("gated_forward", 8, 1392, 24321), ("gated_forward", 13, 2334, 6332)]
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("pad,shift", [(1, 0), (0, 1)])
+@pytest.mark.parametrize("op,T,K,N", ODD_ROWS)
+def test_few_tokens_of_rows_at_odd_elements(op, T, K, N, pad, shift, dt):
+    say(f"case: odd rows {op} T {T} K {K} N {N} pad {pad} shift {shift} {dt}")
+    dtype = DT[dt]
+
+    def rows(seed, r, std):
+        v = big(seed, r * (K + pad) + shift, std=std, dtype=dtype)
+        return v[shift:].view(r, K + pad)[:, :K]
+
+    x, w, bias = rows(1, T, 1.0), rows(2, N, K ** -.5), big(3, N, dtype=dtype)
+    if op == "linear_forward":
+        y, z = Linear(w, bias, act="gelu").forward(x, save=True)
+        ref = R.linear_forward(x.double(), w.double(), bias.double(), "gelu", None, dtype, dtype)
+        R.check("y", y, ref["y"])
+        R.check("z", z, ref["z"])
+        return
+    wu = rows(4, N, K ** -.5)
+    h, a, b = GatedProjection(w, wu, bias).forward(x, save=True)
+    ref = R.gated_forward(x.double(), w.double(), wu.double(), bias.double(), None, "silu", dtype)
+    for name, got in (("h", h), ("a", a), ("b", b)):
+        R.check(name, got, ref[name])
