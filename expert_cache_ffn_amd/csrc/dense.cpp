@@ -121,7 +121,8 @@ int check_apart(const char *what, std::initializer_list<Named> outs, std::initia
 // always start so; there the split tiles may be the fastest.
 size_t forward_ws(int64_t T, int64_t in, int64_t out, int dtype, int planes)
 {
-    return few_needs_no_room(T, in) && (dtype == ECF_F32 || in % 2 == 0) ? 0 : dense_gemm_ws(T, out, planes);
+    return few_needs_no_room(T, in) && (dtype == ECF_F32 || in % 2 == 0) ? 0
+               : dense_gemm_ws(T, out, in, 1, planes);
 }
 
 // Backward workspace: dz rows in `dtype` (gated: all of da, then all of db), at 16-byte
@@ -133,14 +134,15 @@ struct BackWs {
     int64_t pitch;
     size_t colsum, tops, split, total;
 };
-BackWs back_ws(int64_t cols, int halves, int dtype, int32_t T)
+BackWs back_ws(int64_t in, int64_t cols, int halves, int dtype, int32_t T)
 {
     BackWs w;
     w.pitch = (cols + 7) / 8 * 8;
     w.colsum = al256((size_t)T * w.pitch * halves * dense_esize(dtype));
     w.tops = w.colsum + al256((size_t)dense_grad_max_row_blocks(T) * halves * cols * 4);
     w.split = w.tops + (dtype == ECF_F16 ? al256((kDenseTops + 1) * 4) : 0);
-    w.total = w.split + kDensePartialBytes;
+    // both products' in one launch, or either's in turn
+    w.total = w.split + std::min(dense_gemm_ws(T, in, cols, halves, 1) + dense_gemm_ws(cols, in, T, 1, halves), kDensePartialBytes);
     return w;
 }
 
@@ -161,7 +163,7 @@ size_t ecf_gated_workspace_bytes(int32_t hidden, int32_t inter, int32_t dtype, i
 {
     if (check_query("ecf_gated_workspace_bytes", hidden, inter, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
-    return backward ? back_ws(inter, 2, dtype, n_tokens).total : forward_ws(n_tokens, hidden, inter, dtype, 2);
+    return backward ? back_ws(hidden, inter, 2, dtype, n_tokens).total : forward_ws(n_tokens, hidden, inter, dtype, 2);
 }
 
 int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
@@ -243,7 +245,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         }
         DENSE_TRY(check_vector(me, "d_db_gate", a->d_db_gate, a->wgrad_dtype));
         DENSE_TRY(check_vector(me, "d_db_up", a->d_db_up, a->wgrad_dtype));
-        const BackWs w = back_ws(I, 2, a->dtype, T);
+        const BackWs w = back_ws(d, I, 2, a->dtype, T);
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
         DENSE_TRY(check_apart(me, {{"d_dx", a->d_dx}, {"d_dw_gate", a->d_dw_gate}, {"d_dw_up", a->d_dw_up},
                                    {"d_db_gate", a->d_db_gate}, {"d_db_up", a->d_db_up}, {"d_ws", a->d_ws}},
@@ -301,7 +303,7 @@ size_t ecf_linear_workspace_bytes(int32_t in_features, int32_t out_features, int
 {
     if (check_query("ecf_linear_workspace_bytes", in_features, out_features, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
-    return backward ? back_ws(out_features, 1, dtype, n_tokens).total
+    return backward ? back_ws(in_features, out_features, 1, dtype, n_tokens).total
                     : forward_ws(n_tokens, in_features, out_features, dtype, 1);
 }
 
@@ -379,7 +381,7 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         if (a->d_dw)
             DENSE_TRY(check_matrix(me, "d_dw", a->d_dw, lddw, K, a->wgrad_dtype));
         DENSE_TRY(check_vector(me, "d_dbias", a->d_dbias, a->wgrad_dtype));
-        const BackWs w = back_ws(N, 1, a->dtype, T);
+        const BackWs w = back_ws(K, N, 1, a->dtype, T);
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
         DENSE_TRY(check_apart(me, {{"d_dx", a->d_dx}, {"d_dw", a->d_dw}, {"d_dbias", a->d_dbias}, {"d_ws", a->d_ws}},
                               {{"d_x", a->d_x}, {"d_w", a->d_w}, {"d_z", a->d_z}, {"d_dout", a->d_dout}}));

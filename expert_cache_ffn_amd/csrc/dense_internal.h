@@ -98,9 +98,10 @@ struct DensePair {
 bool choose_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t room, DensePair *out);
 
 int launch_dense_few(const DenseGemm &g, const DenseFew &f, hipStream_t st);
-// The largest workspace of any product with up to M x N outputs in each plane.
-constexpr size_t kDensePartialBytes = (size_t)32 << 20;  // fp32 sums of split products
-size_t dense_gemm_ws(int64_t M, int64_t N, int planes);
+// The most workspace that any plan of a product with M x N outputs in each plane over
+// K (ksegs times) asks for: fp32 sums of its splits, 0 where K is too short to split.
+constexpr size_t kDensePartialBytes = (size_t)32 << 20;
+size_t dense_gemm_ws(int64_t M, int64_t N, int64_t K, int ksegs, int planes);
 
 // dz rows of the backward passes, in the operands' type: dz[t][i] (linear), or
 // da = dz[t][i] and db = dz[T + t][i] (gated).  Columns from I to the pitch, the next

@@ -33,6 +33,7 @@ bool aligned16(const void *p, int64_t ld, int dtype)
 
 constexpr int kMaxSplits = 16;
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, kMaxSplits};
+constexpr int kSplitTiles = 2;  // least k-tiles of a split
 constexpr double kLaunchUs = 5.0;  // one launch more, host and device
 
 // Rows at 16-byte boundaries and whole 16-byte chunks: operands can go straight to LDS.
@@ -69,7 +70,7 @@ double partial_bytes(const DenseGemm &g, int splits)
 double join_us(const DenseGemm &g, int splits) { return splits > 1 ? 3.0 + partial_bytes(g, splits) * 2 / 5e6 : 0.0; }
 bool may_split(const DenseGemm &g, int splits, size_t room)
 {
-    return splits == 1 || (ktiles(g) / splits >= 2 && partial_bytes(g, splits) <= (double)room);
+    return splits == 1 || (ktiles(g) / splits >= kSplitTiles && partial_bytes(g, splits) <= (double)room);
 }
 
 // The tile and the splits of K with the least estimated time: rounds of blocks
@@ -256,10 +257,17 @@ bool choose_pair(const DenseGemm &gx, const DenseGemm &gw, int cus, size_t room,
     return both < ux + uw + kLaunchUs;
 }
 
-size_t dense_gemm_ws(int64_t M, int64_t N, int planes)
+size_t dense_gemm_ws(int64_t M, int64_t N, int64_t K, int ksegs, int planes)
 {
-    const size_t all = (size_t)kMaxSplits * planes * M * ((N + 7) / 8 * 8) * 4;
-    return std::min(all, kDensePartialBytes);
+    const int64_t kt = (K + 63) / 64 * ksegs;
+    int most = 1;
+    for (const int s : kSplits)
+        if (kt / s >= kSplitTiles)
+            most = s;
+    if (most == 1)
+        return 0;
+    const size_t all = (size_t)most * planes * M * ((N + 7) / 8 * 8) * 4;
+    return (std::min(all, kDensePartialBytes) + 255) & ~(size_t)255;
 }
 
 }  // namespace ecf

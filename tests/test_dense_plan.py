@@ -144,6 +144,19 @@ def test_host_code_under_sanitizers(tmp_path):
         assert bad not in p.stdout, p.stdout[-4000:]
 
 
+def test_small_layers_ask_for_small_workspaces(host):
+    """No more than dz, the bias sums and what the products of these sizes can split into."""
+    for dt in ("f32", "bf16", "f16"):
+        for op in ("gated_backward", "linear_backward"):
+            assert host.call(op, 64, 256, 128, dt)[2] < 1 << 20
+            assert host.call(op, 8, 64, 64, dt)[2] < 1 << 16
+            # reductions under two k-tiles of 64 are not split
+            assert host.call(op, 100, 4096, 60, dt)[2] < 100 * 64 * 2 * 4 + 4 * 64 * 2 * 4 + 8192 + 2 * 4 * 100 * 4096 * 4
+    assert host.call("linear_forward", 500, 100, 5000, "bf16")[2] == 0
+    big = host.call("linear_backward", 8192, 2048, 4096, "bf16")[2]
+    assert 8192 * 4096 * 2 < big <= 8192 * 4096 * 2 + 256 * 4096 * 4 + (32 << 20) + 4096
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 def test_wide_layers_are_refused_by_the_stated_limit_alone(host, dt):
     """256 rows of every operand under 2 GiB: what meets that runs, and the size query refuses the widths whose
