@@ -132,17 +132,18 @@ size_t forward_ws(int64_t T, int64_t in, int64_t out, int dtype, int planes)
 // partial sums.
 struct BackWs {
     int64_t pitch;
-    size_t colsum, tops, split, total;
+    size_t tops, split, room, dz, total;  // the column sums start it; dz ends it
 };
-BackWs back_ws(int64_t in, int64_t cols, int halves, int dtype, int32_t T)
+BackWs back_ws(int64_t in, int64_t cols, int halves, int dtype, int32_t T, bool dz = true)
 {
     BackWs w;
     w.pitch = (cols + 7) / 8 * 8;
-    w.colsum = al256((size_t)T * w.pitch * halves * dense_esize(dtype));
-    w.tops = w.colsum + al256((size_t)dense_grad_max_row_blocks(T) * halves * cols * 4);
-    w.split = w.tops + (dtype == ECF_F16 ? al256((kDenseTops + 1) * 4) : 0);
+    w.tops = al256((size_t)dense_grad_max_row_blocks(T) * halves * cols * 4);
+    w.split = w.tops + (dtype == ECF_F16 && dz ? al256((kDenseTops + 1) * 4) : 0);
     // both products' in one launch, or either's in turn
-    w.total = w.split + std::min(dense_gemm_ws(T, in, cols, halves, 1) + dense_gemm_ws(cols, in, T, 1, halves), kDensePartialBytes);
+    w.room = std::min(dense_gemm_ws(T, in, cols, halves, 1) + dense_gemm_ws(cols, in, T, 1, halves), kDensePartialBytes);
+    w.dz = w.split + w.room;
+    w.total = w.dz + (dz ? al256((size_t)T * w.pitch * halves * dense_esize(dtype)) : 0);
     return w;
 }
 
@@ -252,7 +253,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
                               {{"d_x", a->d_x}, {"d_w_gate", a->d_w_gate}, {"d_w_up", a->d_w_up}, {"d_a", a->d_a},
                                {"d_b", a->d_b}, {"d_dh", a->d_dh}}));
         hipStream_t st = (hipStream_t)a->stream;
-        char *dz = (char *)a->d_ws;
+        char *ws = (char *)a->d_ws, *dz = ws + w.dz;
         DenseColsum sums{};
         DenseGemm gx{}, gw{};
         if (want_db || (T > 0 && (want_dw || want_dx))) {
@@ -268,9 +269,9 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
             q.want_sums = want_db;
             q.sums[0] = a->d_db_gate, q.sums[1] = a->d_db_up;
             q.sums_dtype = a->wgrad_dtype;
-            q.partial = (float *)(dz + w.colsum);
+            q.partial = (float *)ws;
             if (q.dz && a->dtype == ECF_F16)
-                set_scale(q, dz + w.tops);
+                set_scale(q, ws + w.tops);
             DENSE_TRY(launch_dense_grad(q, &sums, st));
             gx.unscale = gw.unscale = q.unscale;
         }
@@ -293,8 +294,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         gw.M = a->inter, gw.N = a->hidden, gw.K = T;
         gw.out[0] = a->d_dw_gate, gw.out[1] = a->d_dw_up;
         gw.ldout = lddw;
-        return launch_dense_backward(want_dx ? &gx : nullptr, want_dw ? &gw : nullptr, sums, (char *)a->d_ws + w.split,
-                                     w.total - w.split, st);
+        return launch_dense_backward(want_dx ? &gx : nullptr, want_dw ? &gw : nullptr, sums, ws + w.split, w.room, st);
     });
 }
 
@@ -303,7 +303,7 @@ size_t ecf_linear_workspace_bytes(int32_t in_features, int32_t out_features, int
 {
     if (check_query("ecf_linear_workspace_bytes", in_features, out_features, dtype, n_tokens) != ECF_OK)
         return SIZE_MAX;
-    return backward ? back_ws(in_features, out_features, 1, dtype, n_tokens).total
+    return backward ? back_ws(in_features, out_features, 1, dtype, n_tokens, backward != 2).total
                     : forward_ws(n_tokens, in_features, out_features, dtype, 1);
 }
 
@@ -381,13 +381,13 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         if (a->d_dw)
             DENSE_TRY(check_matrix(me, "d_dw", a->d_dw, lddw, K, a->wgrad_dtype));
         DENSE_TRY(check_vector(me, "d_dbias", a->d_dbias, a->wgrad_dtype));
-        const BackWs w = back_ws(K, N, 1, a->dtype, T);
+        // without an activation and in the operands' type, dy is dz
+        const bool direct = !act && a->out_dtype == a->dtype;
+        const BackWs w = back_ws(K, N, 1, a->dtype, T, !direct);
         DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
         DENSE_TRY(check_apart(me, {{"d_dx", a->d_dx}, {"d_dw", a->d_dw}, {"d_dbias", a->d_dbias}, {"d_ws", a->d_ws}},
                               {{"d_x", a->d_x}, {"d_w", a->d_w}, {"d_z", a->d_z}, {"d_dout", a->d_dout}}));
         hipStream_t st = (hipStream_t)a->stream;
-        // without an activation and in the operands' type, dy is dz
-        const bool direct = !act && a->out_dtype == a->dtype;
         const bool products = want_dx || (a->d_dw && T > 0);
         DenseColsum sums{};
         DenseGemm gx{}, gw{};
@@ -399,19 +399,19 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
             q.a = act ? a->d_z : nullptr;
             q.lddout = lddy, q.ldab = ldz;
             q.T = T, q.I = a->out_features;
-            q.dz = products && !direct ? a->d_ws : nullptr;
+            q.dz = products && !direct ? (char *)a->d_ws + w.dz : nullptr;
             q.pitch = w.pitch;
             q.want_sums = a->d_dbias != nullptr;
             q.sums[0] = a->d_dbias;
             q.sums_dtype = a->wgrad_dtype;
-            q.partial = (float *)((char *)a->d_ws + w.colsum);
+            q.partial = (float *)a->d_ws;
             // (relu leaves an fp16 dy what it is, or zero)
             if (q.dz && a->dtype == ECF_F16 && !(a->act == ECF_ACT_RELU && a->out_dtype == ECF_F16))
                 set_scale(q, (char *)a->d_ws + w.tops);
             DENSE_TRY(launch_dense_grad(q, &sums, st));
             gx.unscale = gw.unscale = q.unscale;
         }
-        const void *dz = direct ? a->d_dout : a->d_ws;
+        const void *dz = direct ? a->d_dout : (char *)a->d_ws + w.dz;
         const int64_t lddz = direct ? lddy : w.pitch;
         gx.dtype = gx.out_dtype = gw.dtype = a->dtype;
         gx.b_t = gw.a_t = gw.b_t = true;
@@ -431,7 +431,7 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         gw.out[0] = a->d_dw;
         gw.ldout = lddw;
         return launch_dense_backward(want_dx ? &gx : nullptr, a->d_dw ? &gw : nullptr, sums, (char *)a->d_ws + w.split,
-                                     w.total - w.split, st);
+                                     w.room, st);
     });
 }
 

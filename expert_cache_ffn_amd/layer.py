@@ -292,6 +292,8 @@ class Linear(_Dense):
         a.out_dtype = _DENSE_DT[self.out_dtype]
         a.d_w, a.ld_w = _matrix("w", w, self.out_features, self.in_features, self.dtype, self.device)
         a.d_bias = _vector("bias", bias, self.out_features, self.dtype, self.device)
+        # how the backward pass's workspace is asked for: 2, dy goes into its products as it is
+        self._back = 2 if act == "none" and self.out_dtype is w.dtype else 1
         self.w, self.bias = _kept(w, bias)
         self._a = a
 
@@ -336,5 +338,5 @@ class Linear(_Dense):
             if self.bias is not None:
                 db = self._empty[gd](self.out_features)
                 q.d_dbias = db.data_ptr()
-        self._run(L.ecf_linear_backward, q, T, 1)
+        self._run(L.ecf_linear_backward, q, T, self._back)
         return dx, dw, db

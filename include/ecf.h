@@ -445,6 +445,9 @@ typedef struct {
     void *stream;
 } ecf_linear_args;
 
+/* As ecf_gated_workspace_bytes; backward may also be 2: a backward pass without an
+ * activation and with out_dtype equal to dtype, whose dy goes into the products as it
+ * is. */
 size_t ecf_linear_workspace_bytes(int32_t in_features, int32_t out_features, int32_t dtype, int32_t n_tokens,
                                   int32_t backward);
 int ecf_linear_forward(const ecf_linear_args *args, int32_t n_tokens);

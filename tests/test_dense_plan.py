@@ -158,6 +158,47 @@ def test_small_layers_ask_for_small_workspaces(host):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_no_workspace_for_a_dz_that_is_dy(host, dt):
+    """Without an activation and in the operands' type, nothing is written for dz and nothing asked for it."""
+    none, T, K, N = ecf.ECF_ACT_NONE, 8192, 2048, 4096
+    code, launches, need = host.call("linear_backward", T, K, N, dt, none, want_ws=2)
+    assert code == ecf.ECF_OK and need <= (T // 32) * N * 4 + (32 << 20) + 8192
+    assert all(q["dz"] == 0 if q["kind"] == "grad" else q["a0"] == 4 * dense_host.APART for q in launches)  # dout's place
+    assert host.call("linear_backward", T, K, N, dt, none, want_ws=2, ws=need - 1)[0] == ecf.ECF_ENOSPC
+    # the larger size serves it too, and is what every other call needs
+    full = host.call("linear_backward", T, K, N, dt, none)[2]
+    assert full >= need + T * N * dense_host.SIZE[dt]
+    assert host.call("linear_backward", T, K, N, dt, none)[0] == ecf.ECF_OK
+    assert host.call("linear_backward", T, K, N, dt, ecf.ECF_ACT_RELU, ws=need)[0] == ecf.ECF_ENOSPC
+    if dt != "f32":
+        assert host.call("linear_backward", T, K, N, dt, none, out_dt="f32", ws=need)[0] == ecf.ECF_ENOSPC
+
+
+def test_backward_buffers_lie_apart(host):
+    """Column sums, the words that the scale is found from, partial sums and dz, in the workspace and not on one another."""
+    base = 62 * dense_host.APART
+    for op, T, d, n, dt in drawn(2000, 5):
+        for act in (ecf.ECF_ACT_SILU, ecf.ECF_ACT_NONE):
+            if not op.endswith("backward"):
+                continue
+            code, launches, need = host.call(op, T, d, n, dt, act)
+            assert code == ecf.ECF_OK
+            halves, e, pitch = 1 + (op[0] == "g"), dense_host.SIZE[dt], (n + 7) // 8 * 8
+            spans = []
+            for q in launches:
+                if q["kind"] == "grad":
+                    spans.append((q["partial"], (T + 31) // 32 * halves * n * 4))
+                    spans += [(q["tops"], 1025 * 4)] if q["tops"] else []
+                    spans += [(q["dz"], T * pitch * halves * e)] if q["dz"] else []
+                    assert not q["dz"] or dt != "f16" or q["tops"]
+                elif q.get("partials") or q.get("partials_w"):
+                    spans.append((q["ws"], q["room"]))
+            spans = sorted(set(spans))
+            assert all(at >= base and at % 256 == 0 and at + size <= base + need for at, size in spans)
+            assert all(p[0] + p[1] <= q[0] for p, q in zip(spans, spans[1:]))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 def test_wide_layers_are_refused_by_the_stated_limit_alone(host, dt):
     """256 rows of every operand under 2 GiB: what meets that runs, and the size query refuses the widths whose
     rows alone do not."""
