@@ -3,6 +3,8 @@ structs.  Nothing here computes any part of the layer; every step of the
 forward pass runs in libecf's kernels (or its host expert threads)."""
 from __future__ import annotations
 
+import warnings
+
 import torch
 
 from . import _lib as L
@@ -147,8 +149,21 @@ def _kept(*tensors):
     return [None if t is None else t.detach() for t in tensors]
 
 
+def _warn_untracked(what):
+    """A forward call that something requires gradients of; it gives none where they are on."""
+    if torch.is_grad_enabled():
+        warnings.warn(f"{what}.forward is outside autograd: its output has no gradient function although the weights or "
+                      "an input require gradients.  Run it under torch.no_grad(), and call backward() with the "
+                      "output's gradient", stacklevel=3)
+
+
 class _Dense:
     """What the two operators share: the weights' checks, workspaces and streams.
+
+    They are outside autograd: outputs never carry a gradient function, and a training
+    step calls backward() itself, best under torch.no_grad().  forward() warns where
+    gradients are on, the weights or an input require them and nothing is saved for
+    backward().
 
     A call runs on the current stream of the weights' device and takes its
     workspace from torch's allocator for that stream, so calls on several
@@ -220,6 +235,7 @@ class GatedProjection(_Dense):
             raise ValueError(f"w_gate and w_up must have the same row stride ({a.ld_w} and {ld})")
         a.d_b_gate = _vector("b_gate", b_gate, self.inter, self.dtype, self.device)
         a.d_b_up = _vector("b_up", b_up, self.inter, self.dtype, self.device)
+        self._learns = any(t is not None and t.requires_grad for t in (w_gate, w_up, b_gate, b_up))
         self.w_gate, self.w_up, self.b_gate, self.b_up = _kept(w_gate, w_up, b_gate, b_up)
         self._a = a
 
@@ -232,6 +248,8 @@ class GatedProjection(_Dense):
         T = self._tokens(x)
         a = L.GatedArgs.from_buffer_copy(self._a)
         a.d_x, a.ld_x = _matrix("x", x, T, self.hidden, self.dtype, self.device)
+        if (self._learns or x.requires_grad) and not save:
+            _warn_untracked("GatedProjection")
         h, a.d_h, a.ld_h = self._out("out", out, T, self.inter, self.dtype)
         if save:
             sa, a.d_a, a.ld_ab = self._out("a", None, T, self.inter, self.dtype)
@@ -294,6 +312,7 @@ class Linear(_Dense):
         a.d_bias = _vector("bias", bias, self.out_features, self.dtype, self.device)
         # how the backward pass's workspace is asked for: 2, dy goes into its products as it is
         self._back = 2 if act == "none" and self.out_dtype is w.dtype else 1
+        self._learns = w.requires_grad or (bias is not None and bias.requires_grad)
         self.w, self.bias = _kept(w, bias)
         self._a = a
 
@@ -310,6 +329,8 @@ class Linear(_Dense):
         if residual is not None:
             a.d_residual, a.ld_residual = _matrix("residual", residual, T, self.out_features, self.out_dtype,
                                                   self.device)
+        if (self._learns or x.requires_grad or residual is not None and residual.requires_grad) and not save:
+            _warn_untracked("Linear")
         y, a.d_out, a.ld_out = self._out("out", out, T, self.out_features, self.out_dtype)
         if save:
             z, a.d_z, a.ld_z = self._out("z", None, T, self.out_features, self.dtype)

@@ -178,3 +178,11 @@ def test_few_tokens_need_no_workspace():
             assert ecf.ecf_linear_workspace_bytes(K, 1024, dt, T) == 0
         assert ecf.ecf_linear_workspace_bytes(8192, 1024, dt, 16) > 0
         assert ecf.ecf_linear_workspace_bytes(4096, 1024, dt, 17) > 0
+
+
+def test_lost_gradients_are_said(recwarn):
+    with torch.no_grad():
+        ly._warn_untracked("Linear")
+    assert not recwarn.list
+    with pytest.warns(UserWarning, match="Linear.forward is outside autograd"):
+        ly._warn_untracked("Linear")

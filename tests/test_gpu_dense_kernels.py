@@ -1,4 +1,6 @@
 """GPU tests of dense calls that reach kernels or operands the other files do not."""
+import warnings
+
 import pytest
 import torch
 
@@ -81,3 +83,26 @@ def test_few_tokens_of_rows_at_odd_elements(op, T, K, N, pad, shift, dt):
     ref = R.gated_forward(x.double(), w.double(), wu.double(), bias.double(), None, "silu", dtype)
     for name, got in (("h", h), ("a", a), ("b", b)):
         R.check(name, got, ref[name])
+
+
+def test_a_forward_pass_that_loses_gradients_says_so():
+    """Outputs carry no gradient function; a call whose caller would miss one warns, and gives the same bits."""
+    x, w = big(1, 70, 96), big(2, 64, 96, std=.1)
+    plain = Linear(w).forward(x), GatedProjection(w, w).forward(x)
+    p = torch.nn.Parameter(w)
+    lin, gp = Linear(p), GatedProjection(p, p)
+    for f, want in ((lin.forward, plain[0]), (gp.forward, plain[1])):
+        with pytest.warns(UserWarning, match="outside autograd"):
+            y = f(x)
+        assert torch.equal(y, want) and y.grad_fn is None
+        with pytest.warns(UserWarning, match="outside autograd"):
+            f(x.clone().requires_grad_())
+    with pytest.warns(UserWarning, match="outside autograd"):
+        Linear(w).forward(x, residual=torch.zeros(70, 64, device="cuda", requires_grad=True))
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with torch.no_grad():
+            assert torch.equal(lin.forward(x), plain[0])
+        assert torch.equal(lin.forward(x, save=True)[0], plain[0])  # for backward()
+        assert torch.equal(gp.forward(x, save=True)[0], plain[1])
+        assert torch.equal(Linear(w).forward(x), plain[0])
