@@ -106,3 +106,29 @@ def test_a_forward_pass_that_loses_gradients_says_so():
         assert torch.equal(lin.forward(x, save=True)[0], plain[0])  # for backward()
         assert torch.equal(gp.forward(x, save=True)[0], plain[1])
         assert torch.equal(Linear(w).forward(x), plain[0])
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,K,N", [(8192, 640, 1), (5000, 333, 3), (4099, 72, 7), (6000, 1, 200), (5001, 7, 129), (9000, 5, 6)])
+def test_narrow_layers_over_many_tokens(T, K, N, dt):
+    """Rows of under 8 elements with reductions of thousands: a head of a few outputs, a layer of a few inputs."""
+    say(f"case: narrow T {T} K {K} N {N} {dt}")
+    dtype = DT[dt]
+    x, w, bias = big(1, T, K, dtype=dtype), big(2, N, K, std=K ** -.5, dtype=dtype), big(3, N, dtype=dtype)
+    for act in ("none", "gelu"):
+        layer = Linear(w, bias, act=act)
+        y, z = layer.forward(x, save=True)
+        R.check("y", y, R.linear_forward(x.double(), w.double(), bias.double(), act, None, dtype, dtype)["y"])
+        dout = big(4, T, N, std=.1, dtype=dtype)
+        outs = layer.backward(x, dout, z, w_grad_dtype=torch.float32)
+        ref = R.linear_backward(x.double(), w.double(), z.double(), dout.double(), act, dtype, dtype, torch.float32)
+        for name, got in zip(("dx", "dw", "dbias"), outs):
+            R.check(name, got, ref[name])
+    wu = big(5, N, K, std=K ** -.5, dtype=dtype)
+    gp = GatedProjection(w, wu, bias, bias)
+    h, a, b = gp.forward(x, save=True)
+    R.check("h", h, R.gated_forward(x.double(), w.double(), wu.double(), bias.double(), bias.double(), "silu", dtype)["h"])
+    outs = gp.backward(x, a, b, dout, w_grad_dtype=torch.float32)
+    ref = R.gated_backward(*(t.double() for t in (x, w, wu, a, b, dout)), "silu", dtype, torch.float32)
+    for name, got in zip(("dx", "dw_gate", "dw_up", "db_gate", "db_up"), outs):
+        R.check(name, got, ref[name])
