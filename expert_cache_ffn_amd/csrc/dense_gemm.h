@@ -37,10 +37,11 @@
 // and stores are 16 bytes wide.
 //
 // Bound by the matrix pipe and the loads beside it: 8192 x 16384 of K 4096 in bf16,
-// 910 us (1208 TFLOP/s; with every operand tile in L2 833 us, without any loads 725);
-// gated 4096 x 2 x 1024 of K 4096 62 us (1112 TFLOP/s).  fp32 by splitting the
-// operands, LDS and MFMAs together: 1000 x 1024 of K 2048 38 us (111 TFLOP/s, where
-// fp32 MFMAs reach 152 on large products).
+// 903 to 941 us (1217 to 1168 TFLOP/s; with every operand tile in L2 833 us, without any
+// loads 725); gated 4096 x 2 x 1024 of K 4096 62 to 65 us (1112 to 1062 TFLOP/s).  fp32
+// by splitting the operands, LDS and MFMAs together: 1000 x 1024 of K 2048 38 to 40 us
+// (107 TFLOP/s), 2293 x 2814 of K 3776 forward and backward 159 (the library's fp32
+// products reach 152).
 #pragma once
 
 #include <type_traits>

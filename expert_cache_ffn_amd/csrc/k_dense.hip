@@ -148,8 +148,8 @@ __device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t *red)
 // The largest finite |dz| that each block meets (as bits, which order as the values
 // do), over the tiles of k_dense_grad.  A pass of its own, because every element's scale
 // needs the largest of all; k_dense_grad then finds its inputs in the cache (777 x 1999,
-// three inputs of odd width: 7.0 us, of which the launch and one load are most; linear
-// 523 x 1411: 4.7).
+// three inputs of odd width: 7.1 to 7.4 us, of which the launch and one load are most;
+// linear 523 x 1411: 3.6 to 4.6).
 template <class E, class ED, bool GATED>
 __global__ __launch_bounds__(256) void k_dense_grad_top(DenseGrad g, int row_blocks, int rows, int tiles)
 {

@@ -1,6 +1,6 @@
 // Dense operators for few tokens (at most 64): x W^T, gated or not, as a streaming
-// read of the weights.  Bound by HBM: every weight byte is read once, straight
-// into MFMA operand registers.
+// read of the weights: every weight byte is read once, straight into MFMA operand
+// registers.
 //
 // A 16x16 MFMA takes 16 weight rows and 16 tokens at the same k.  With few rows
 // per block the 16 rows become RT weight rows at P = 16 / RT places of K, and the
@@ -14,9 +14,12 @@
 // The waves of a block share K; their partial sums meet in LDS and are added in a
 // fixed order by one thread per output, which applies the epilogue.
 //
-// 2 x 1024 rows of K 4096, bf16 (16.8 MB): one token 5.0 us, 16 tokens 8.0; 2.5 us of
-// it are launch and first loads, then a CU takes in 38 KB/us (9.7 TB/s of all, the
-// weights lying in the memory-side cache).
+// Bound by what a CU takes in of weights and x together.  2 x 1024 rows of K 4096, bf16
+// (16.8 MB): one token 5.0 to 5.4 us, 16 tokens 8.0 to 9.2; 2.5 us of it are launch and
+// first loads, then a CU takes in 38 KB/us (9.7 TB/s of all, the weights lying in the
+// memory-side cache).  x is read anew for every 16 rows at most, as many bytes as the
+// weights at 9 to 16 tokens, so wide layers stay far from the memory's rate: 16 x 4096 to
+// 16384 in bf16 41 us (134 MB, 3.3 TB/s), 11 x 7469 to 12864 in fp32 165 us (384 MB, 2.3).
 #include "dense_device.h"
 
 namespace ecf {
