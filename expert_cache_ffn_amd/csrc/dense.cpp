@@ -128,29 +128,46 @@ size_t forward_ws(int64_t T, int64_t in, int64_t out, int dtype, int planes)
 // Backward workspace: dz rows in `dtype` (gated: all of da, then all of db), at 16-byte
 // boundaries (rows of dh or dy rounded up to 8 elements, so the last of 256 starts and
 // ends within a 31-bit byte offset as theirs does), the column sums of each row block in
-// fp32, in fp16 what the scale of dz is found from and its inverse, and the products'
-// partial sums.
+// fp32, the products' partial sums, and for a scaled fp16 pass (DenseGrad) a second dz,
+// what the scales are found from and their inverses.
 struct BackWs {
     int64_t pitch;
-    size_t tops, split, room, dz, total;  // the column sums start it; dz ends it
+    size_t split, room, dz, dz_w, row_tops, col_tops, row_inverse, col_inverse, total;  // the column sums start it
 };
 BackWs back_ws(int64_t in, int64_t cols, int halves, int dtype, int32_t T, bool dz = true)
 {
-    BackWs w;
+    BackWs w{};
+    const size_t row_blocks = (size_t)dense_grad_max_row_blocks(T);
     w.pitch = (cols + 7) / 8 * 8;
-    w.tops = al256((size_t)dense_grad_max_row_blocks(T) * halves * cols * 4);
-    w.split = w.tops + (dtype == ECF_F16 && dz ? al256((kDenseTops + 1) * 4) : 0);
+    w.split = al256(row_blocks * halves * cols * 4);
     // both products' in one launch, or either's in turn
     w.room = std::min(dense_gemm_ws(T, in, cols, halves, 1) + dense_gemm_ws(cols, in, T, 1, halves), kDensePartialBytes);
-    w.dz = w.split + w.room;
-    w.total = w.dz + (dz ? al256((size_t)T * w.pitch * halves * dense_esize(dtype)) : 0);
+    w.dz = w.total = w.split + w.room;
+    if (!dz)
+        return w;
+    const size_t plane = al256((size_t)T * w.pitch * halves * dense_esize(dtype));
+    w.dz_w = w.total = w.dz + plane;
+    if (dtype != ECF_F16)
+        return w;
+    w.row_tops = w.dz_w + plane;
+    w.col_tops = w.row_tops + al256((size_t)dense_grad_col_blocks(cols) * T * 4);
+    w.row_inverse = w.col_tops + al256(row_blocks * halves * cols * 4);
+    w.col_inverse = w.row_inverse + al256((size_t)T * 4);
+    w.total = w.col_inverse + al256((size_t)halves * cols * 4);
     return w;
 }
 
-void set_scale(DenseGrad &q, void *words)
+// What of dz a backward pass writes, for the products that are wanted: one for both, or (scaled) one each.
+void set_dz(DenseGrad &q, const BackWs &w, char *ws, bool dx, bool dw, bool scaled)
 {
-    q.tops = (uint32_t *)words;
-    q.unscale = (float *)words + kDenseTops;
+    q.pitch = w.pitch;
+    q.scaled = scaled && (dx || dw);
+    q.dz = dx || (dw && !q.scaled) ? ws + w.dz : nullptr;
+    if (!q.scaled)
+        return;
+    q.dz_w = dw ? ws + w.dz_w : nullptr;
+    q.row_tops = (uint32_t *)(ws + w.row_tops), q.col_tops = (uint32_t *)(ws + w.col_tops);
+    q.row_inverse = (float *)(ws + w.row_inverse), q.col_inverse = (float *)(ws + w.col_inverse);
 }
 
 }  // namespace
@@ -253,7 +270,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
                               {{"d_x", a->d_x}, {"d_w_gate", a->d_w_gate}, {"d_w_up", a->d_w_up}, {"d_a", a->d_a},
                                {"d_b", a->d_b}, {"d_dh", a->d_dh}}));
         hipStream_t st = (hipStream_t)a->stream;
-        char *ws = (char *)a->d_ws, *dz = ws + w.dz;
+        char *ws = (char *)a->d_ws;
         DenseColsum sums{};
         DenseGemm gx{}, gw{};
         if (want_db || (T > 0 && (want_dw || want_dx))) {
@@ -264,23 +281,21 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
             q.dout = a->d_dh, q.a = a->d_a, q.b = a->d_b;
             q.lddout = lddh, q.ldab = ldab;
             q.T = T, q.I = a->inter;
-            q.dz = want_dw || want_dx ? dz : nullptr;
-            q.pitch = w.pitch;
+            set_dz(q, w, ws, want_dx, want_dw, a->dtype == ECF_F16 && T > 0);
             q.want_sums = want_db;
             q.sums[0] = a->d_db_gate, q.sums[1] = a->d_db_up;
             q.sums_dtype = a->wgrad_dtype;
             q.partial = (float *)ws;
-            if (q.dz && a->dtype == ECF_F16)
-                set_scale(q, ws + w.tops);
             DENSE_TRY(launch_dense_grad(q, &sums, st));
-            gx.unscale = gw.unscale = q.unscale;
+            gx.unscale = q.row_inverse, gw.unscale = q.col_inverse;
+            gx.a[0] = q.dz, gw.a[0] = q.scaled ? q.dz_w : q.dz;
         }
-        const char *dz2 = dz + (size_t)T * w.pitch * dense_esize(a->dtype);
+        const size_t half = (size_t)T * w.pitch * dense_esize(a->dtype);
         gx.dtype = gx.out_dtype = gw.dtype = a->dtype;
         gx.b_t = gw.a_t = gw.b_t = true;
         gx.ksegs = gw.mhalves = 2;
         gx.mhalves = gw.ksegs = 1;
-        gx.a[0] = gw.a[0] = dz, gx.a[1] = gw.a[1] = dz2;
+        gx.a[1] = (const char *)gx.a[0] + half, gw.a[1] = (const char *)gw.a[0] + half;
         gx.lda = gw.lda = w.pitch;
         gx.a_padded = gw.a_padded = true;
         gx.b[0] = a->d_w_gate, gx.b[1] = a->d_w_up;
@@ -399,24 +414,24 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
             q.a = act ? a->d_z : nullptr;
             q.lddout = lddy, q.ldab = ldz;
             q.T = T, q.I = a->out_features;
-            q.dz = products && !direct ? (char *)a->d_ws + w.dz : nullptr;
-            q.pitch = w.pitch;
+            // (relu leaves an fp16 dy what it is, or zero)
+            if (products && !direct)
+                set_dz(q, w, (char *)a->d_ws, want_dx, a->d_dw != nullptr,
+                       a->dtype == ECF_F16 && !(a->act == ECF_ACT_RELU && a->out_dtype == ECF_F16));
             q.want_sums = a->d_dbias != nullptr;
             q.sums[0] = a->d_dbias;
             q.sums_dtype = a->wgrad_dtype;
             q.partial = (float *)a->d_ws;
-            // (relu leaves an fp16 dy what it is, or zero)
-            if (q.dz && a->dtype == ECF_F16 && !(a->act == ECF_ACT_RELU && a->out_dtype == ECF_F16))
-                set_scale(q, (char *)a->d_ws + w.tops);
             DENSE_TRY(launch_dense_grad(q, &sums, st));
-            gx.unscale = gw.unscale = q.unscale;
+            gx.unscale = q.row_inverse, gw.unscale = q.col_inverse;
+            gx.a[0] = q.dz, gw.a[0] = q.scaled ? q.dz_w : q.dz;
         }
-        const void *dz = direct ? a->d_dout : (char *)a->d_ws + w.dz;
+        if (direct)
+            gx.a[0] = gw.a[0] = a->d_dout;
         const int64_t lddz = direct ? lddy : w.pitch;
         gx.dtype = gx.out_dtype = gw.dtype = a->dtype;
         gx.b_t = gw.a_t = gw.b_t = true;
         gx.ksegs = gx.mhalves = gw.ksegs = gw.mhalves = 1;
-        gx.a[0] = gw.a[0] = dz;
         gx.lda = gw.lda = lddz;
         gx.a_padded = gw.a_padded = !direct;
         gx.b[0] = a->d_w;

@@ -176,12 +176,12 @@ __device__ __forceinline__ void epilogue8(const DenseGemm &g, int half, int64_t 
         store8<E>(row_at<E>(out, m * g.ldout), n, cnt, y, g.stream_out);
 }
 
-// What undoes the scale of dz (DenseGemm::unscale), in products that may have one.
+// What undoes the scale of row m of A (DenseGemm::unscale), in products that may have one.
 template <class E, bool BT>
-__device__ __forceinline__ float unscale_of(const DenseGemm &g)
+__device__ __forceinline__ float unscale_of(const DenseGemm &g, int half, int64_t m)
 {
     if constexpr (std::is_same<E, F16>::value && BT)
-        return g.unscale ? *g.unscale : 1.f;
+        return g.unscale ? g.unscale[(int64_t)half * g.M + min(m, (int64_t)g.M - 1)] : 1.f;
     return 1.f;
 }
 
@@ -761,7 +761,6 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
     const int ecol = MATES ? (wn & 1) * 32 : 0, erow = MATES ? (wn & 1) * 16 : 0;
     const bool partial = gr.splits > 1;
     constexpr int PASSES = MATES ? 1 : 32 * LPR / 64, Q = GATED ? 2 : 1;
-    const float mul = unscale_of<E, BT>(g);
     if (KW > 1 && group) {
         for (int i = 0; MATES && i < 2 * GROUPS; ++i)
             __syncthreads();  // the ones below
@@ -773,7 +772,12 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
         const int c0 = MATES ? wn / 2 * 32 : GATED ? (wn * RN + grp % (FN / CB) * 64) / 2 : wn * RN + grp % (FN / CB) * 64;
         const int n = n0 + c0 + c;
         constexpr bool PLAIN = BT;
-        float bias[Q][8], res[GATED || PLAIN ? 1 : PASSES][8];
+        float bias[Q][8], res[GATED || PLAIN ? 1 : PASSES][8], mul[PASSES];
+        if (PLAIN && !partial) {
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p)
+                mul[p] = unscale_of<E, PLAIN>(g, half, m0 + r0 + p * (64 / LPR));
+        }
         if (!PLAIN && !partial) {
             load_bias<E, GATED>(g, n, bias);
             if (!GATED && g.res) {
@@ -823,7 +827,7 @@ __device__ __forceinline__ void gemm_block(const DenseGemm &g, const DenseGrid &
             for (int p = 0; p < PASSES; ++p) {
                 float z[Q][8];
                 take(p, z);
-                epilogue8<E, GATED, true, ECF_ACT_NONE>(g, half, m0 + r0 + p * (64 / LPR), n, z, bias, res[0], mul);
+                epilogue8<E, GATED, true, ECF_ACT_NONE>(g, half, m0 + r0 + p * (64 / LPR), n, z, bias, res[0], mul[p]);
             }
         } else {
             with_act(g.act, [&](auto act) __attribute__((always_inline)) {
@@ -918,7 +922,7 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseGemm g, DenseGrid gr)
                 z[q][j] += v[j];
         }
     if constexpr (std::is_same<E, F16>::value && !GATED) {
-        const float mul = unscale_of<E, true>(g);
+        const float mul = unscale_of<E, true>(g, half, m);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             z[0][j] *= mul;

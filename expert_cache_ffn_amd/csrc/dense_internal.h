@@ -33,8 +33,8 @@ struct DenseGemm {
     int64_t ldout;
     void *save[2];
     int64_t ldsave;
-    // backward products in fp16: the power of two that undoes the scale of dz (see
-    // DenseGrad), applied to the fp32 sums; null: none
+    // backward products in fp16: what undoes the scale of A (see DenseGrad), a power of
+    // two per row of the output, [half][M]; null: none
     const float *unscale;
     bool stream_out;  // set by the launcher: the output does not fit the caches
 };
@@ -121,14 +121,21 @@ struct DenseGrad {
     int sums_dtype;
     float *partial;
     // fp16: da, db and dz may lie outside the type's range although the products made
-    // of them do not (an fp32 dy of 1e-9 or 1e6; a dh b over 65504).  With `tops`,
-    // kDenseTops words of workspace, they are held times the power of two that puts the
-    // largest finite one at 2^14 to 2^15, and *unscale gets its inverse.  Those within
-    // 2^-28 of the largest keep all their bits; what is below 2^-39 of it is lost.
-    uint32_t *tops;
-    float *unscale;
+    // of them do not (an fp32 dy of 1e-9 or 1e6; a dh b over 65504).  With `scaled` they
+    // are held twice, times powers of two: `dz`, of which dx is made, row by row (da and
+    // db of a token together), `dz_w`, of which dW is made, column by column (either may
+    // be null: not wanted).  The power puts the largest finite value of the row (column)
+    // at 2^14 to 2^15.  Values within 2^-28 of that one keep all their bits, what is below
+    // 2^-39 of it is lost, and no row of dx or dW hangs on the gradients of another.
+    // (A linear dz of an fp16 dy leaves the range by slopes of up to 1.13 only, but half
+    // of it, which needs no pass, is one bit short in the subnormals.)
+    bool scaled;
+    void *dz_w;
+    uint32_t *row_tops, *col_tops;    // the largest of each tile: [column block][T], [row block][1 or 2][I]
+    float *row_inverse, *col_inverse; // the inverse powers: [T], [1 or 2][I]
 };
-constexpr int kDenseTops = 1024;  // most blocks that look for the largest
+// column blocks of any call
+int64_t dense_grad_col_blocks(int64_t I);
 // the most row blocks of any call with up to T tokens
 int64_t dense_grad_max_row_blocks(int64_t T);
 int launch_dense_grad(const DenseGrad &g, DenseColsum *left, hipStream_t st);

@@ -55,9 +55,9 @@ __global__ __launch_bounds__(256) void k_dense_short(DenseGemm g, int tiles_n)
             __syncthreads();
         }
     }
-    const float mul = unscale_of<E, true>(g);
     for (int i = 0; i < 4; ++i) {
         const int64_t m = m0 + ty * 4 + i, n1 = n0 + tx * 4;
+        const float mul = unscale_of<E, true>(g, half, m);
         void *out = g.out[half];
         if (m >= g.M || n1 >= g.N)
             continue;
@@ -133,51 +133,13 @@ __device__ __forceinline__ void grad8(const DenseGrad &g, int64_t t, int c, int 
                 out[h][j] = 0.f;
 }
 
-// The largest of `top` over the block's four waves; red: 4 words.
-__device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t *red)
+// The bits of |v| where v is finite: they order as the values do.
+__device__ __forceinline__ uint32_t finite_bits(float v)
 {
-#pragma unroll
-    for (int o = 32; o; o >>= 1)
-        top = max(top, (uint32_t)__shfl_xor((int)top, o));
-    if ((threadIdx.x & 63) == 0)
-        red[threadIdx.x >> 6] = top;
-    __syncthreads();
-    return max(max(red[0], red[1]), max(red[2], red[3]));
+    const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
+    return u < 0x7f800000u ? u : 0u;
 }
-
-// The largest finite |dz| that each block meets (as bits, which order as the values
-// do), over the tiles of k_dense_grad.  A pass of its own, because every element's scale
-// needs the largest of all; k_dense_grad then finds its inputs in the cache (777 x 1999,
-// three inputs of odd width: 7.1 to 7.4 us, of which the launch and one load are most;
-// linear 523 x 1411: 3.6 to 4.6).
-template <class E, class ED, bool GATED>
-__global__ __launch_bounds__(256) void k_dense_grad_top(DenseGrad g, int row_blocks, int rows, int tiles)
-{
-    __shared__ uint32_t red[4];
-    const int cg = threadIdx.x & 7, rl = threadIdx.x >> 3;
-    uint32_t top = 0;
-    for (int tile = (int)blockIdx.x; tile < tiles; tile += (int)gridDim.x) {
-        const int cb = tile / row_blocks, rb = tile - cb * row_blocks;
-        const int c = cb * kGradCols + cg * 8, n = g.I - c, t1 = min(g.T, (rb + 1) * rows);
-        if (n > 0)
-            for (int64_t t = (int64_t)rb * rows + rl; t < t1; t += kGradLanes) {
-                float out[GATED ? 2 : 1][8];
-                grad8<E, ED, GATED>(g, t, c, n, out);
-#pragma unroll
-                for (int h = 0; h < (GATED ? 2 : 1); ++h)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t u = __float_as_uint(out[h][j]) & 0x7fffffffu;
-                        top = max(top, u < 0x7f800000u ? u : 0u);
-                    }
-            }
-    }
-    top = block_max(top, red);
-    if (threadIdx.x == 0)
-        g.tops[blockIdx.x] = top;
-}
-
-// The power of two that puts `top` (the bits of a finite value) at 2^14 to 2^15, as far as it and its
+// The power of two that puts `top` (such bits) at 2^14 to 2^15, as far as it and its
 // inverse are normal numbers: 2^-113 to 2^126.
 __device__ __forceinline__ int scale_exponent(uint32_t top)
 {
@@ -185,47 +147,167 @@ __device__ __forceinline__ int scale_exponent(uint32_t top)
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// The largest finite |dz| of each row and column of a tile of k_dense_grad.  A pass of
+// its own, because every element's scales need the largest of its whole row and column;
+// k_dense_grad then finds its inputs in the cache (777 x 1999, three inputs of odd
+// width: 7.4 us, of which the launch and one load are most; linear 523 x 1411: 4.2 to 5.0).
 template <class E, class ED, bool GATED>
-__global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks, int rows, int n_tops)
+__global__ __launch_bounds__(256) void k_dense_grad_top(DenseGrad g, int row_blocks, int rows)
 {
     constexpr int H = GATED ? 2 : 1;
-    constexpr bool SCALED = std::is_same<E, F16>::value;
+    __shared__ uint32_t red[kGradLanes][H][kGradCols + 4];
+    const int cb = (int)blockIdx.x / row_blocks, rb = (int)blockIdx.x - cb * row_blocks;
+    const int cg = threadIdx.x & 7, rl = threadIdx.x >> 3;
+    const int c = cb * kGradCols + cg * 8, n = g.I - c, t1 = min(g.T, (rb + 1) * rows);
+    uint32_t col[H][8] = {};
+    for (int64_t t = (int64_t)rb * rows + rl; t < t1; t += kGradLanes) {
+        uint32_t row = 0;
+        if (n > 0) {
+            float out[H][8];
+            grad8<E, ED, GATED>(g, t, c, n, out);
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t u = finite_bits(out[h][j]);
+                    col[h][j] = max(col[h][j], u);
+                    row = max(row, u);
+                }
+        }
+#pragma unroll
+        for (int o = 4; o; o >>= 1)  // the row's eight lanes
+            row = max(row, (uint32_t)__shfl_xor((int)row, o));
+        if (g.dz && cg == 0)
+            g.row_tops[(int64_t)cb * g.T + t] = row;
+    }
+    if (!g.dz_w)
+        return;
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            red[rl][h][cg * 8 + j] = col[h][j];
+    __syncthreads();
+    const int h = threadIdx.x / kGradCols, lc = threadIdx.x % kGradCols;
+    const int64_t i = (int64_t)cb * kGradCols + lc;
+    if (h >= H || i >= g.I)
+        return;
+    uint32_t top = 0;
+#pragma unroll
+    for (int r = 0; r < kGradLanes; ++r)
+        top = max(top, red[r][h][lc]);
+    g.col_tops[((int64_t)rb * H + h) * g.I + i] = top;
+}
+
+template <class E, class ED, bool GATED>
+__global__ __launch_bounds__(256) void k_dense_grad(DenseGrad g, int row_blocks, int rows, int col_blocks)
+{
+    constexpr int H = GATED ? 2 : 1;
+    constexpr bool F16S = std::is_same<E, F16>::value;  // may be scaled
     __shared__ float red[kGradLanes][H][kGradCols + 4];
+    __shared__ float row_scale[F16S ? kGradRows : 1], col_scale[H][F16S ? kGradCols : 1];
     const int cb = (int)blockIdx.x / row_blocks, rb = (int)blockIdx.x - cb * row_blocks;
     const int cg = threadIdx.x & 7, rl = threadIdx.x >> 3;
     const int c = cb * kGradCols + cg * 8, n = g.I - c;
+    const int64_t t0 = (int64_t)rb * rows;
     const int t1 = min(g.T, (rb + 1) * rows);
-    float sum[H][8] = {}, scale = 1.f;
-    int64_t t = (int64_t)rb * rows + rl;
-    auto take = [&](float out[H][8]) __attribute__((always_inline)) {
+    float sum[H][8] = {};
+    int64_t t = t0 + rl;
+    auto take = [&](const float out[H][8]) __attribute__((always_inline)) {
 #pragma unroll
         for (int h = 0; h < H; ++h) {
+            const int64_t at = ((int64_t)h * g.T + t) * g.pitch;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 8; ++j)
                 sum[h][j] += out[h][j];
-                if (SCALED)
-                    out[h][j] *= scale;
+            if (!F16S || !g.scaled) {
+                if (g.dz)
+                    store8<E>(row_at<E>(g.dz, at), c, 8, out[h]);
+                continue;
             }
-            if (g.dz)
-                store8<E>(row_at<E>(g.dz, ((int64_t)h * g.T + t) * g.pitch), c, 8, out[h]);
+            float q[8];
+            if (g.dz) {
+                const float by = row_scale[F16S ? t - t0 : 0];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    q[j] = out[h][j] * by;
+                store8<E>(row_at<E>(g.dz, at), c, 8, q);
+            }
+            if (g.dz_w) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    q[j] = out[h][j] * col_scale[h][F16S ? cg * 8 + j : 0];
+                store8<E>(row_at<E>(g.dz_w, at), c, 8, q);
+            }
         }
         t += kGradLanes;
     };
-    if (SCALED && n_tops) {
-        // the blocks' largest values travel together with the first row
-        __shared__ uint32_t red4[4];
-        uint32_t top = 0;
+    if (F16S && g.scaled) {
+        // the tiles' largest values, four (or two) lanes per row and column, travel
+        // together with the first row
+        constexpr int CL = kGradCols * H;
+        __shared__ uint32_t tops[2][256];
+        const int tid = threadIdx.x;
+        constexpr int FIRST = 16;  // loads of each kind at once (more are needed beyond 64 blocks)
+        const int64_t i = (int64_t)cb * kGradCols + tid % kGradCols;  // its column, of half tid / 64 % H
+        const int64_t hi = (int64_t)(tid % CL / kGradCols) * g.I + min(i, (int64_t)g.I - 1);
+        const uint32_t *pr = g.row_tops + min(t0 + tid % kGradRows, (int64_t)g.T - 1), *pc = g.col_tops + hi;
+        auto fetch = [&](const uint32_t *p, int64_t ld, int from, int step, int n, uint32_t v[FIRST])
+                         __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < kDenseTops; i += 256)
-            top = max(top, g.tops[min(i + (int)threadIdx.x, n_tops - 1)]);
+            for (int u = 0; u < FIRST; ++u)
+                v[u] = p[min(from + u * step, n - 1) * ld];
+        };
+        auto most = [](uint32_t top, const uint32_t v[FIRST]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int u = 0; u < FIRST; ++u)
+                top = max(top, v[u]);
+            return top;
+        };
+        constexpr int RS = 256 / kGradRows, CS = 256 / CL;
+        uint32_t vr[FIRST] = {}, vc[FIRST] = {}, row = 0, col = 0;
+        if (g.dz)
+            fetch(pr, g.T, tid / kGradRows, RS, col_blocks, vr);
+        if (g.dz_w)
+            fetch(pc, (int64_t)H * g.I, tid / CL, CS, row_blocks, vc);
         float out[H][8];
         const bool in = n > 0 && t < t1;
         if (in)
             grad8<E, ED, GATED>(g, t, c, n, out);
-        const int e = scale_exponent(block_max(top, red4));
-        scale = power_of_two(e);
-        if (blockIdx.x == 0 && threadIdx.x == 0)
-            *g.unscale = power_of_two(-e);
+        row = most(row, vr);
+        col = most(col, vc);
+        if (g.dz)
+            for (int b = tid / kGradRows + FIRST * RS; b < col_blocks; b += FIRST * RS) {
+                fetch(pr, g.T, b, RS, col_blocks, vr);
+                row = most(row, vr);
+            }
+        if (g.dz_w)
+            for (int b = tid / CL + FIRST * CS; b < row_blocks; b += FIRST * CS) {
+                fetch(pc, (int64_t)H * g.I, b, CS, row_blocks, vc);
+                col = most(col, vc);
+            }
+        tops[0][tid] = row;
+        tops[1][tid] = col;
+        __syncthreads();
+        if (tid < kGradRows) {
+#pragma unroll
+            for (int b = kGradRows; b < 256; b += kGradRows)
+                row = max(row, tops[0][tid + b]);
+            const int e = scale_exponent(row);
+            row_scale[tid] = power_of_two(e);
+            if (g.dz && cb == 0 && t0 + tid < t1)
+                g.row_inverse[t0 + tid] = power_of_two(-e);
+        }
+        if (tid < CL) {
+#pragma unroll
+            for (int b = CL; b < 256; b += CL)
+                col = max(col, tops[1][tid + b]);
+            const int e = scale_exponent(col);
+            col_scale[tid / kGradCols][tid % kGradCols] = power_of_two(e);
+            if (g.dz_w && rb == 0 && i < g.I)
+                g.col_inverse[hi] = power_of_two(-e);
+        }
+        __syncthreads();
         if (in)
             take(out);
     }
@@ -374,11 +456,12 @@ int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseC
     return gw ? launch_dense_gemm(*gw, ws, room, st) : ECF_OK;
 }
 
+int64_t dense_grad_col_blocks(int64_t I) { return (I + kGradCols - 1) / kGradCols; }
 int64_t dense_grad_max_row_blocks(int64_t T) { return (T + kGradLanes - 1) / kGradLanes; }
 
 int launch_dense_grad(const DenseGrad &g, DenseColsum *left, hipStream_t st)
 {
-    const int64_t cols = (g.I + kGradCols - 1) / kGradCols;
+    const int64_t cols = dense_grad_col_blocks(g.I);
     // rows per block; all of a short batch in one block saves the launch that joins the sums
     const bool few = ((int64_t)g.T + kGradRows - 1) / kGradRows * cols < kGradBlocks;
     const int per = few && !(g.want_sums && g.T <= kGradRows) ? kGradLanes : kGradRows;
@@ -386,20 +469,19 @@ int launch_dense_grad(const DenseGrad &g, DenseColsum *left, hipStream_t st)
     if (rows > 0) {
         ProfScope p("dense_grad", st);
         const dim3 grid((unsigned)(cols * rows)), block(256);
-        const int tiles = (int)(cols * rows), n_tops = g.tops ? std::min(tiles, kDenseTops) : 0;
         auto go = [&](auto e, auto ed) {
             using E = decltype(e);
             using ED = decltype(ed);
             if constexpr (std::is_same<E, F16>::value) {
-                if (n_tops && g.gated)
-                    hipLaunchKernelGGL((k_dense_grad_top<E, E, true>), dim3(n_tops), block, 0, st, g, rows, per, tiles);
-                else if (n_tops)
-                    hipLaunchKernelGGL((k_dense_grad_top<E, ED, false>), dim3(n_tops), block, 0, st, g, rows, per, tiles);
+                if (g.scaled && g.gated)
+                    hipLaunchKernelGGL((k_dense_grad_top<E, E, true>), grid, block, 0, st, g, rows, per);
+                else if (g.scaled)
+                    hipLaunchKernelGGL((k_dense_grad_top<E, ED, false>), grid, block, 0, st, g, rows, per);
             }
             if (g.gated)  // dout is of the operands' type
-                hipLaunchKernelGGL((k_dense_grad<E, E, true>), grid, block, 0, st, g, rows, per, n_tops);
+                hipLaunchKernelGGL((k_dense_grad<E, E, true>), grid, block, 0, st, g, rows, per, (int)cols);
             else
-                hipLaunchKernelGGL((k_dense_grad<E, ED, false>), grid, block, 0, st, g, rows, per, n_tops);
+                hipLaunchKernelGGL((k_dense_grad<E, ED, false>), grid, block, 0, st, g, rows, per, (int)cols);
         };
         if (g.dtype == ECF_F32)
             go(F32{}, F32{});

@@ -356,11 +356,14 @@ int ecf_bandwidth_profile(const ecf_shape *shape, int32_t n_blobs, const void *c
  * summed in fp32, biases, activations and residuals are applied to the fp32 sums,
  * and each output is rounded once; the backward passes also round da, db and dz
  * once to `dtype`, the type that the two products behind them multiply (bias gradients
- * are sums of the unrounded ones).  In fp16 they are rounded as multiples of a power of
- * two that the call finds from the largest finite one: none of them overflows, those
- * within 2^-28 of the largest keep all 11 bits, and those below 2^-39 of it count as
- * zero.  Results do not depend on what runs beside a call, and the same call gives the
- * same bits.  An infinite or NaN element makes outputs infinite or NaN only in rows
+ * are sums of the unrounded ones).  In fp16 none of them overflows: they are
+ * rounded as multiples of a power of two, found for each row (for dx) and each column
+ * (for dW) from its largest finite value.  Values within 2^-28 of that one keep all 11
+ * bits, those below 2^-39 of it count as zero, and no row of dx or dW hangs on another's
+ * gradients.  (An fp16 dy, as it is or through relu, goes into the products unchanged.)
+ * An fp16 subnormal enters a sum with the absolute precision of 2^-14, the smallest
+ * normal number.  Results do not depend on what runs beside a call, and the same call
+ * gives the same bits.  An infinite or NaN element makes outputs infinite or NaN only in rows
  * (columns) that it is part of, as IEEE products and sums do (in fp32 an infinity times
  * a magnitude below 2^-126 may count as times zero).
  *

@@ -78,11 +78,15 @@ int launch_dense_backward(const DenseGemm *gx, const DenseGemm *gw, const DenseC
 }
 
 int64_t dense_grad_max_row_blocks(int64_t T) { return (T + 31) / 32; }
+int64_t dense_grad_col_blocks(int64_t I) { return (I + 63) / 64; }
 
 int launch_dense_grad(const DenseGrad &g, DenseColsum *, hipStream_t)
 {
     add("\"kind\": \"grad\", " + num("dz", (long long)(uintptr_t)g.dz) + num("pitch", g.pitch) +
-        num("tops", (long long)(uintptr_t)g.tops) + num("sums", g.want_sums) + num("partial", (long long)(uintptr_t)g.partial));
+        num("scaled", g.scaled) + num("dz_w", (long long)(uintptr_t)g.dz_w) +
+        num("row_tops", (long long)(uintptr_t)g.row_tops) + num("col_tops", (long long)(uintptr_t)g.col_tops) +
+        num("row_inverse", (long long)(uintptr_t)g.row_inverse) + num("col_inverse", (long long)(uintptr_t)g.col_inverse) +
+        num("sums", g.want_sums) + num("partial", (long long)(uintptr_t)g.partial));
     return ECF_OK;
 }
 

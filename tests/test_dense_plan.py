@@ -18,6 +18,8 @@ import test_gpu_dense_kernels as GK
 
 @pytest.fixture(scope="module")
 def host(tmp_path_factory):
+    if shutil.which("g++") is None:
+        pytest.skip("needs g++")
     return dense_host.build(tmp_path_factory.mktemp("dense_host"))
 
 
@@ -151,7 +153,7 @@ def test_small_layers_ask_for_small_workspaces(host):
             assert host.call(op, 64, 256, 128, dt)[2] < 1 << 20
             assert host.call(op, 8, 64, 64, dt)[2] < 1 << 16
             # reductions under two k-tiles of 64 are not split
-            assert host.call(op, 100, 4096, 60, dt)[2] < 100 * 64 * 2 * 4 + 4 * 64 * 2 * 4 + 8192 + 2 * 4 * 100 * 4096 * 4
+            assert host.call(op, 100, 4096, 60, dt)[2] < 100 * 64 * 2 * 4 + 8 * 64 * 2 * 4 + 8192 + 2 * 4 * 100 * 4096 * 4
     assert host.call("linear_forward", 500, 100, 5000, "bf16")[2] == 0
     big = host.call("linear_backward", 8192, 2048, 4096, "bf16")[2]
     assert 8192 * 4096 * 2 < big <= 8192 * 4096 * 2 + 256 * 4096 * 4 + (32 << 20) + 4096
@@ -175,12 +177,15 @@ def test_no_workspace_for_a_dz_that_is_dy(host, dt):
 
 
 def test_backward_buffers_lie_apart(host):
-    """Column sums, the words that the scale is found from, partial sums and dz, in the workspace and not on one another."""
+    """Column sums, what the scales are found from and their inverses, partial sums and dz, in the workspace and not
+    on one another."""
     base = 62 * dense_host.APART
     for op, T, d, n, dt in drawn(2000, 5):
-        for act in (ecf.ECF_ACT_SILU, ecf.ECF_ACT_NONE):
-            if not op.endswith("backward"):
-                continue
+        if not op.endswith("backward"):
+            continue
+        # (a linear dz of an fp16 dy is dy, or through relu dy and zeros)
+        scaled = (ecf.ECF_ACT_SILU, ecf.ECF_ACT_NONE, ecf.ECF_ACT_RELU)[: 3 if op[0] == "g" else 1]
+        for act in (ecf.ECF_ACT_SILU, ecf.ECF_ACT_NONE, ecf.ECF_ACT_RELU):
             code, launches, need = host.call(op, T, d, n, dt, act)
             assert code == ecf.ECF_OK
             halves, e, pitch = 1 + (op[0] == "g"), dense_host.SIZE[dt], (n + 7) // 8 * 8
@@ -188,14 +193,28 @@ def test_backward_buffers_lie_apart(host):
             for q in launches:
                 if q["kind"] == "grad":
                     spans.append((q["partial"], (T + 31) // 32 * halves * n * 4))
-                    spans += [(q["tops"], 1025 * 4)] if q["tops"] else []
-                    spans += [(q["dz"], T * pitch * halves * e)] if q["dz"] else []
-                    assert not q["dz"] or dt != "f16" or q["tops"]
-                elif q.get("partials") or q.get("partials_w"):
+                    spans += [(q[z], T * pitch * halves * e) for z in ("dz", "dz_w") if q[z]]
+                    assert q["scaled"] == (dt == "f16" and act in scaled) and bool(q["dz_w"]) == q["scaled"]
+                    if q["scaled"]:
+                        spans += [(q["row_tops"], (n + 63) // 64 * T * 4), (q["col_tops"], (T + 31) // 32 * halves * n * 4),
+                                  (q["row_inverse"], T * 4), (q["col_inverse"], halves * n * 4)]
+                else:
+                    assert bool(q["unscale"]) == (dt == "f16" and act in scaled)
+                if q.get("partials") or q.get("partials_w"):
                     spans.append((q["ws"], q["room"]))
             spans = sorted(set(spans))
             assert all(at >= base and at % 256 == 0 and at + size <= base + need for at, size in spans)
             assert all(p[0] + p[1] <= q[0] for p, q in zip(spans, spans[1:]))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_no_tokens_read_no_scale(host, dt):
+    """Without tokens no scale is written, so none may be read: zeros times what the workspace held are not zeros."""
+    for op in ("gated_backward", "linear_backward"):
+        code, launches, _ = host.call(op, 0, 64, 40, dt, gd="f32")
+        assert code == ecf.ECF_OK
+        products = [q for q in launches if q["kind"] != "grad"]
+        assert products and all(q["unscale"] == 0 for q in products)
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])

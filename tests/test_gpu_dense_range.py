@@ -154,3 +154,104 @@ def test_infinities_and_nans_that_meet(T, K, N, dt):
     assert torch.equal(kind(Linear(wt).backward(rand(3, T, N, dtype=dtype), x, need_dw=False)[0]), ref)
     dw = Linear(rand(4, T, N, dtype=dtype)).backward(wt, x.t().contiguous(), need_dx=False)[1]
     assert torch.equal(kind(dw), ref)
+
+
+@pytest.mark.parametrize("T,d,I", [(6, 40, 72), (70, 256, 128), (333, 133, 201), (700, 512, 1000)])
+@pytest.mark.parametrize("huge", [6e4, 1e3, 0.0])
+def test_fp16_rows_and_columns_keep_apart(huge, T, d, I):
+    """Rows of huge gradients (padding, say) leave the other rows' dx as it is without them, to the bit, and
+    columns of huge gradients the other rows of dW."""
+    say(f"case: fp16 range, huge {huge} rows and columns T {T} d {d} I {I}")
+    x, wg, wu = rand(1, T, d, dtype=F16), rand(2, I, d, std=.05, dtype=F16), rand(3, I, d, std=.05, dtype=F16)
+    a, b, dh = rand(6, T, I, dtype=F16), rand(7, T, I, dtype=F16), rand(8, T, I, std=1e-4, dtype=F16)
+    gp, rows, cols = GatedProjection(wg, wu), torch.arange(T, device="cuda") % 3 != 1, torch.arange(I, device="cuda") % 5 != 2
+    dx, dwg, dwu, *_ = gp.backward(x, a, b, dh, w_grad_dtype=torch.float32)
+    for t in (a, b, dh):
+        t[~rows] = huge
+    assert torch.equal(gp.backward(x, a, b, dh)[0][rows], dx[rows])
+    a, b, dh = rand(6, T, I, dtype=F16), rand(7, T, I, dtype=F16), rand(8, T, I, std=1e-4, dtype=F16)
+    for t in (a, b, dh):
+        t[:, ~cols] = huge
+    outs = gp.backward(x, a, b, dh, w_grad_dtype=torch.float32)
+    assert torch.equal(outs[1][cols], dwg[cols]) and torch.equal(outs[2][cols], dwu[cols])
+    lin = Linear(wg, out_dtype=torch.float32)
+    dy = rand(9, T, I, std=1e-6)
+    dx, dw, _ = lin.backward(x, dy, w_grad_dtype=torch.float32)
+    far = dy.clone()
+    far[~rows] = huge * 1e20
+    assert torch.equal(lin.backward(x, far)[0][rows], dx[rows])
+    far = dy.clone()
+    far[:, ~cols] = huge * 1e20
+    assert torch.equal(lin.backward(x, far, w_grad_dtype=torch.float32)[1][cols], dw[cols])
+
+
+def own_scales(*ds):
+    """As scaled_half, of the scales of rows (for dx) and of columns (for dW): [(value, bound for dx, for dW)]."""
+    fin = [torch.where(d.isfinite(), d.abs(), 0.0) for d, _, _ in ds]
+    row = torch.cat(fin, 1).amax(1, keepdim=True)
+    return [(d, e + d.abs() * (2.0 ** -11 * (1 + 1e-3)) + row * 2.0 ** -39,
+             e + d.abs() * (2.0 ** -11 * (1 + 1e-3)) + f.amax(0, keepdim=True) * 2.0 ** -39) for (d, e, _), f in zip(ds, fin)]
+
+
+@pytest.mark.parametrize("T,d,I", SHAPES)
+def test_fp16_gradients_of_rows_and_columns_of_every_size(T, d, I):
+    """dz from 1e-30 to 1e30 within one call: each row of dx and of dW is as near as if it were alone."""
+    say(f"case: fp16 range, every size T {T} d {d} I {I}")
+    x, w = rand(1, T, d, dtype=F16), rand(2, I, d, dtype=F16)
+    lin = Linear(w, rand(4, I, dtype=F16), act="silu", out_dtype=torch.float32)
+    z = rand(6, T, I, dtype=F16)
+    size_t, size_n = torch.logspace(-30, 4, T, device="cuda")[:, None], torch.logspace(-30, 30, I, device="cuda")[None]
+    dy = rand(8, T, I) * size_t
+    dx = lin.backward(x, dy, z)[0]
+    (dz, r, _), = own_scales(*R.grads(dy.double(), z.double(), "silu", F16))
+    ref, err = R.rounded(*R.product(dz, w.double().t().contiguous(), r), F16)
+    fits = ref.abs() + err < 65504
+    R.check("dx", dx[fits], (ref[fits], err[fits]))
+    dy = rand(8, T, I) * size_n
+    dw = lin.backward(x, dy, z, w_grad_dtype=torch.float32)[1]
+    (dz, _, r), = own_scales(*R.grads(dy.double(), z.double(), "silu", F16))
+    R.check("dw", dw, R.rounded(*R.product(dz.t(), x.double().t(), r.t()), torch.float32))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("T,K,N", SHAPES)
+def test_fp16_slopes_above_one(act, T, K, N):
+    """A linear dz of an fp16 dy near the type's largest value: slopes of up to 1.13 carry it past 65504."""
+    say(f"case: fp16 range, {act} slopes T {T} K {K} N {N}")
+    x, w = rand(1, T, K, dtype=F16), rand(2, N, K, std=1e-3, dtype=F16)
+    z = (rand(6, T, N).double().clamp(-1, 1) * .3 + 1.5).half()
+    dout = (torch.sign(rand(8, T, N)) * (65504 - 2000 * rand(9, T, N).abs())).half()
+    assert float((dout.double() * R.act_both(z.double(), act)[1]).abs().max()) > 65520
+    dx, dw, db = Linear(w, rand(4, N, dtype=F16), act=act).backward(x, dout, z, w_grad_dtype=torch.float32)
+    (dz, e, _), = R.grads(dout.double(), z.double(), act, F16)
+    (_, rx, rw), = own_scales((dz, e, None))
+    ref, err = R.rounded(*R.product(dz, w.double().t().contiguous(), rx), F16)
+    fits = ref.abs() + err < 65504
+    R.check("dx", dx[fits], (ref[fits], err[fits]))
+    R.check("dw", dw, R.rounded(*R.product(dz.t(), x.double().t(), rw.t()), torch.float32))
+    R.check("dbias", db, R.colsum(dz, e, torch.float32))
+
+
+def product_of_subnormals(a, b, da):
+    """R.product where operands are subnormal in fp16.  The matrix instruction aligns its 16 products by the
+    exponents of their operands, in which a subnormal counts as 2^-14, before it adds them in fp32: beside
+    1 * 2^-18, whose exponents say 2^-14, a product of 2^-40 is 2^-26 of that and is lost whole (measured).  So
+    the rounding of an addition, 2^-23 of the sum so far, is one of products whose operands are at least 2^-14."""
+    z, err = R.product(a, b, da)
+    low = 2.0 ** -14
+    return z, err + (a.abs().clamp_min(low) @ b.abs().clamp_min(low).t()) * ((a.shape[1] + 2) * R.EPS23)
+
+
+@pytest.mark.parametrize("T,K,N", SHAPES)
+def test_fp16_linear_gradients_of_small_fp16_dy(T, K, N):
+    """dy of 2^-20 and less, all subnormal: dz keeps its bits."""
+    say(f"case: fp16 range, small fp16 dy T {T} K {K} N {N}")
+    x, w = rand(1, T, K, dtype=F16), rand(2, N, K, std=1e2, dtype=F16)
+    z, dout = rand(6, T, N, dtype=F16), rand(8, T, N, std=1e-6, dtype=F16)
+    for act in ("gelu", "relu"):
+        dx, dw, _ = Linear(w, act=act).backward(x, dout, z, w_grad_dtype=torch.float32)
+        (dz, e, _), = R.grads(dout.double(), z.double(), act, F16)
+        (_, rx, rw), = own_scales((dz, e, None)) if act == "gelu" else [(dz, e, e)]  # (relu's dz is exact)
+        product = R.product if act == "gelu" else product_of_subnormals
+        R.check("dx", dx, R.rounded(*product(dz, w.double().t().contiguous(), rx), F16))
+        R.check("dw", dw, R.rounded(*product(dz.t(), x.double().t(), rw.t()), torch.float32))
