@@ -8,13 +8,13 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, Structure, c_char_p, c_double, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, Structure, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libecf.so")
 
 ECF_OK, ECF_EINVAL, ECF_ENOSPC, ECF_EHIP, ECF_EUNSUPPORTED, ECF_ESTATE = 0, -1, -2, -3, -4, -5
-ECF_F32, ECF_BF16, ECF_MXFP4, ECF_F16 = 0, 1, 2, 3
+ECF_F32, ECF_BF16, ECF_MXFP4, ECF_F16, ECF_MXFP8 = 0, 1, 2, 3, 4
 ECF_Q_AUTO, ECF_Q_ALL_GPU, ECF_Q_ALL_HOST, ECF_Q_FIXED = 0, 1, 2, 3
 ECF_PATH_AUTO, ECF_PATH_DECODE, ECF_PATH_PREFILL = 0, 1, 2
 ECF_ACT_NONE, ECF_ACT_SILU, ECF_ACT_GELU, ECF_ACT_GELU_TANH, ECF_ACT_RELU = 0, 1, 2, 3, 4
@@ -30,7 +30,11 @@ EXPORTS = [
     "prefetch_layer", "moe_layer_forward", "moe_layer_forward_noalloc", "ecf_noalloc_scratch_bytes",
     "ecf_host_experts", "ecf_bandwidth_profile",
     "ecf_gated_workspace_bytes", "ecf_gated_forward", "ecf_gated_backward",
-    "ecf_linear_workspace_bytes", "ecf_linear_forward", "ecf_linear_backward", "ecf_profile_enable",
+    "ecf_linear_workspace_bytes", "ecf_linear_forward", "ecf_linear_backward",
+    "ecf_norm_workspace_bytes", "ecf_norm_forward", "ecf_norm_backward",
+    "ecf_token_sort_workspace_bytes", "ecf_token_sort", "ecf_token_dispatch", "ecf_token_combine",
+    "ecf_token_combine_backward",
+    "ecf_profile_enable",
     "ecf_profile_get", "ecf_profile_reset", "ecf_stream_read", "ecf_mfma_rate",
 ]
 
@@ -107,6 +111,38 @@ class LinearArgs(Structure):
     ]
 
 
+class NormArgs(Structure):
+    _fields_ = [
+        ("hidden", c_int32), ("dtype", c_int32), ("sum_dtype", c_int32), ("weight_dtype", c_int32), ("eps", c_float),
+        ("d_weight", c_void_p), ("d_x", c_void_p), ("d_residual", c_void_p), ("ld_x", c_int64), ("ld_residual", c_int64),
+        ("d_sum", c_void_p), ("ld_sum", c_int64), ("d_y", c_void_p), ("ld_y", c_int64),
+        ("d_q", c_void_p), ("d_q_scale", c_void_p), ("ld_q", c_int64), ("ld_q_scale", c_int64), ("d_rstd", c_void_p),
+        ("d_dy", c_void_p), ("d_dsum", c_void_p), ("ld_dy", c_int64), ("ld_dsum", c_int64),
+        ("d_dx", c_void_p), ("d_ds", c_void_p), ("ld_dx", c_int64), ("ld_ds", c_int64),
+        ("wgrad_dtype", c_int32), ("d_dweight", c_void_p), ("d_ws", c_void_p), ("ws_bytes", c_size_t),
+        ("stream", c_void_p),
+    ]
+
+
+class SortArgs(Structure):
+    _fields_ = [
+        ("n_experts", c_int32), ("top_k", c_int32), ("idx_bytes", c_int32), ("d_idx", c_void_p), ("ld_idx", c_int64),
+        ("d_counts", c_void_p), ("d_offsets", c_void_p), ("d_tiles", c_void_p), ("d_order", c_void_p),
+        ("d_place", c_void_p), ("d_ws", c_void_p), ("ws_bytes", c_size_t), ("stream", c_void_p),
+    ]
+
+
+class TokenArgs(Structure):
+    _fields_ = [
+        ("hidden", c_int32), ("n_experts", c_int32), ("top_k", c_int32), ("dtype", c_int32), ("token_dtype", c_int32),
+        ("d_offsets", c_void_p), ("d_place", c_void_p), ("d_weight", c_void_p), ("d_x", c_void_p), ("d_x_scale", c_void_p),
+        ("ld_x", c_int64), ("ld_x_scale", c_int64), ("d_rows", c_void_p), ("ld_rows", c_int64),
+        ("d_residual", c_void_p), ("ld_residual", c_int64), ("d_out", c_void_p), ("ld_out", c_int64),
+        ("d_dout", c_void_p), ("ld_dout", c_int64), ("d_drows", c_void_p), ("ld_drows", c_int64),
+        ("d_dweight", c_void_p), ("stream", c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -157,6 +193,15 @@ def lib():
             for way in ("forward", "backward"):
                 f = getattr(L, f"ecf_{name}_{way}")
                 f.argtypes, f.restype = [POINTER(args), c_int32], c_int32
+        L.ecf_norm_workspace_bytes.argtypes = [c_int32] * 3
+        L.ecf_token_sort_workspace_bytes.argtypes = [c_int32] * 3
+        for name in ("norm", "token_sort"):
+            getattr(L, f"ecf_{name}_workspace_bytes").restype = c_size_t
+        for name, args in (("norm_forward", NormArgs), ("norm_backward", NormArgs), ("token_sort", SortArgs),
+                           ("token_dispatch", TokenArgs), ("token_combine", TokenArgs),
+                           ("token_combine_backward", TokenArgs)):
+            f = getattr(L, f"ecf_{name}")
+            f.argtypes, f.restype = [POINTER(args), c_int32], c_int32
         L.ecf_profile_enable.argtypes, L.ecf_profile_enable.restype = [c_int32], c_int32
         L.ecf_profile_get.argtypes = [c_int32, POINTER(c_char_p), POINTER(c_int64), POINTER(c_double)]
         L.ecf_profile_get.restype = c_int32
@@ -340,6 +385,38 @@ def ecf_linear_forward(args: LinearArgs, n_tokens):
 
 def ecf_linear_backward(args: LinearArgs, n_tokens):
     _check(lib().ecf_linear_backward(ctypes.byref(args), n_tokens))
+
+
+def ecf_norm_workspace_bytes(hidden, n_tokens, backward=False) -> int:
+    return _dense_ws(lib().ecf_norm_workspace_bytes(int(hidden), int(n_tokens), int(backward)))
+
+
+def ecf_norm_forward(args: NormArgs, n_tokens):
+    _check(lib().ecf_norm_forward(ctypes.byref(args), n_tokens))
+
+
+def ecf_norm_backward(args: NormArgs, n_tokens):
+    _check(lib().ecf_norm_backward(ctypes.byref(args), n_tokens))
+
+
+def ecf_token_sort_workspace_bytes(n_experts, top_k, n_tokens) -> int:
+    return _dense_ws(lib().ecf_token_sort_workspace_bytes(int(n_experts), int(top_k), int(n_tokens)))
+
+
+def ecf_token_sort(args: SortArgs, n_tokens):
+    _check(lib().ecf_token_sort(ctypes.byref(args), n_tokens))
+
+
+def ecf_token_dispatch(args: TokenArgs, n_tokens):
+    _check(lib().ecf_token_dispatch(ctypes.byref(args), n_tokens))
+
+
+def ecf_token_combine(args: TokenArgs, n_tokens):
+    _check(lib().ecf_token_combine(ctypes.byref(args), n_tokens))
+
+
+def ecf_token_combine_backward(args: TokenArgs, n_tokens):
+    _check(lib().ecf_token_combine_backward(ctypes.byref(args), n_tokens))
 
 
 def ecf_profile_enable(on: bool):

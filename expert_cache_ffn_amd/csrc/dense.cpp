@@ -2,19 +2,14 @@
 // workspace, and the matrix products and gradient kernels each call is made of.
 #include <algorithm>
 #include <cstdint>
-#include <initializer_list>
 
+#include "arg_checks.h"
 #include "dense_internal.h"
 
 namespace ecf {
 namespace {
 
 constexpr int32_t kDenseMax = 1 << 22;  // tokens and widths per call
-
-size_t al256(size_t v) { return (v + 255) & ~(size_t)255; }
-int64_t ld_or(int64_t ld, int64_t width) { return ld ? ld : width; }
-
-bool dense_dtype(int32_t t) { return t == ECF_F32 || t == ECF_BF16 || t == ECF_F16; }
 
 int check_common(const char *what, int32_t in, int32_t out, int32_t dtype, int32_t T)
 {
@@ -56,65 +51,12 @@ int check_matrix(const char *what, const char *name, const void *p, int64_t ld, 
     return ECF_OK;
 }
 
-int check_vector(const char *what, const char *name, const void *p, int dtype)
-{
-    if ((uintptr_t)p % dense_esize(dtype))
-        return set_error(ECF_EINVAL, "%s: %s is not aligned to its elements", what, name);
-    return ECF_OK;
-}
-
-int check_ws(const char *what, const void *ws, size_t have, size_t need)
-{
-    if (!need)
-        return ECF_OK;
-    if (!ws || have < need)
-        return set_error(ECF_ENOSPC, "%s: needs %zu bytes of workspace, got %zu", what, need, ws ? have : (size_t)0);
-    if ((uintptr_t)ws % 256)
-        return set_error(ECF_EINVAL, "%s: the workspace is not at a 256-byte boundary", what);
-    return ECF_OK;
-}
-
 int check_act(const char *what, int32_t act)
 {
     if (act < ECF_ACT_NONE || act > ECF_ACT_RELU)
         return set_error(ECF_EINVAL, "%s: unknown activation %d", what, act);
     return ECF_OK;
 }
-
-int check_grad_dtype(const char *what, int32_t t, int32_t dtype)
-{
-    if (t != dtype && t != ECF_F32)
-        return set_error(ECF_EINVAL, "%s: wgrad_dtype must be dtype or ECF_F32 (got %d)", what, t);
-    return ECF_OK;
-}
-
-// An output that starts where another one or an input does: blocks would read what
-// others have written.  (Other overlaps are the caller's to avoid.)
-struct Named {
-    const char *name;
-    const void *p;
-};
-int check_apart(const char *what, std::initializer_list<Named> outs, std::initializer_list<Named> ins)
-{
-    for (const Named *o = outs.begin(); o != outs.end(); ++o) {
-        if (!o->p)
-            continue;
-        for (const Named &i : ins)
-            if (i.p == o->p)
-                return set_error(ECF_EINVAL, "%s: %s and %s are the same memory", what, o->name, i.name);
-        for (const Named *q = outs.begin(); q != o; ++q)
-            if (q->p == o->p)
-                return set_error(ECF_EINVAL, "%s: %s and %s are the same memory", what, o->name, q->name);
-    }
-    return ECF_OK;
-}
-
-#define DENSE_TRY(expr)                \
-    do {                               \
-        const int _rc = (expr);        \
-        if (_rc != ECF_OK)             \
-            return _rc;                \
-    } while (0)
 
 // A few tokens' calls have no workspace: their weights are streamed, or (16-bit rows
 // that start at odd elements) go through tiles that do not split K.  Rows of odd length
@@ -190,8 +132,8 @@ int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
         const char *me = "ecf_gated_forward";
         if (!a)
             return set_error(ECF_EINVAL, "%s: args is NULL", me);
-        DENSE_TRY(check_common(me, a->hidden, a->inter, a->dtype, T));
-        DENSE_TRY(check_act(me, a->act));
+        ECF_TRY(check_common(me, a->hidden, a->inter, a->dtype, T));
+        ECF_TRY(check_act(me, a->act));
         const int64_t d = a->hidden, I = a->inter;
         DenseGemm g{};
         g.dtype = g.out_dtype = a->dtype;
@@ -203,22 +145,22 @@ int ecf_gated_forward(const ecf_gated_args *a, int32_t T)
         g.act = a->act;
         if (T == 0)
             return ECF_OK;
-        DENSE_TRY(check_matrix(me, "d_x", a->d_x, g.lda, d, a->dtype));
-        DENSE_TRY(check_matrix(me, "d_w_gate", a->d_w_gate, g.ldb, d, a->dtype));
-        DENSE_TRY(check_matrix(me, "d_w_up", a->d_w_up, g.ldb, d, a->dtype));
-        DENSE_TRY(check_vector(me, "d_b_gate", a->d_b_gate, a->dtype));
-        DENSE_TRY(check_vector(me, "d_b_up", a->d_b_up, a->dtype));
+        ECF_TRY(check_matrix(me, "d_x", a->d_x, g.lda, d, a->dtype));
+        ECF_TRY(check_matrix(me, "d_w_gate", a->d_w_gate, g.ldb, d, a->dtype));
+        ECF_TRY(check_matrix(me, "d_w_up", a->d_w_up, g.ldb, d, a->dtype));
+        ECF_TRY(check_vector(me, "d_b_gate", a->d_b_gate, a->dtype));
+        ECF_TRY(check_vector(me, "d_b_up", a->d_b_up, a->dtype));
         if (!a->d_a != !a->d_b)
             return set_error(ECF_EINVAL, "%s: d_a and d_b come together", me);
         if (a->d_h || !a->d_a)
-            DENSE_TRY(check_matrix(me, "d_h", a->d_h, g.ldout, I, a->dtype));
+            ECF_TRY(check_matrix(me, "d_h", a->d_h, g.ldout, I, a->dtype));
         if (a->d_a) {
-            DENSE_TRY(check_matrix(me, "d_a", a->d_a, g.ldsave, I, a->dtype));
-            DENSE_TRY(check_matrix(me, "d_b", a->d_b, g.ldsave, I, a->dtype));
+            ECF_TRY(check_matrix(me, "d_a", a->d_a, g.ldsave, I, a->dtype));
+            ECF_TRY(check_matrix(me, "d_b", a->d_b, g.ldsave, I, a->dtype));
         }
         const size_t need = forward_ws(T, d, I, a->dtype, 2);
-        DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, need));
-        DENSE_TRY(check_apart(me, {{"d_h", a->d_h}, {"d_a", a->d_a}, {"d_b", a->d_b}, {"d_ws", need ? a->d_ws : nullptr}},
+        ECF_TRY(check_ws(me, a->d_ws, a->ws_bytes, need));
+        ECF_TRY(check_apart(me, {{"d_h", a->d_h}, {"d_a", a->d_a}, {"d_b", a->d_b}, {"d_ws", need ? a->d_ws : nullptr}},
                               {{"d_x", a->d_x}, {"d_w_gate", a->d_w_gate}, {"d_w_up", a->d_w_up},
                                {"d_b_gate", a->d_b_gate}, {"d_b_up", a->d_b_up}}));
         g.a[0] = a->d_x;
@@ -236,9 +178,9 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
         const char *me = "ecf_gated_backward";
         if (!a)
             return set_error(ECF_EINVAL, "%s: args is NULL", me);
-        DENSE_TRY(check_common(me, a->hidden, a->inter, a->dtype, T));
-        DENSE_TRY(check_act(me, a->act));
-        DENSE_TRY(check_grad_dtype(me, a->wgrad_dtype, a->dtype));
+        ECF_TRY(check_common(me, a->hidden, a->inter, a->dtype, T));
+        ECF_TRY(check_act(me, a->act));
+        ECF_TRY(check_grad_dtype(me, a->wgrad_dtype, a->dtype));
         const int64_t d = a->hidden, I = a->inter;
         const int64_t ldx = ld_or(a->ld_x, d), ldw = ld_or(a->ld_w, d), ldab = ld_or(a->ld_ab, I),
                       lddh = ld_or(a->ld_dh, I), lddx = ld_or(a->ld_dx, d), lddw = ld_or(a->ld_dw, d);
@@ -246,26 +188,26 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
             return set_error(ECF_EINVAL, "%s: d_dw_gate and d_dw_up come together", me);
         const bool want_dw = a->d_dw_gate, want_db = a->d_db_gate || a->d_db_up, want_dx = a->d_dx && T > 0;
         if (T > 0) {
-            DENSE_TRY(check_matrix(me, "d_a", a->d_a, ldab, I, a->dtype));
-            DENSE_TRY(check_matrix(me, "d_b", a->d_b, ldab, I, a->dtype));
-            DENSE_TRY(check_matrix(me, "d_dh", a->d_dh, lddh, I, a->dtype));
+            ECF_TRY(check_matrix(me, "d_a", a->d_a, ldab, I, a->dtype));
+            ECF_TRY(check_matrix(me, "d_b", a->d_b, ldab, I, a->dtype));
+            ECF_TRY(check_matrix(me, "d_dh", a->d_dh, lddh, I, a->dtype));
             if (want_dw)
-                DENSE_TRY(check_matrix(me, "d_x", a->d_x, ldx, d, a->dtype));
+                ECF_TRY(check_matrix(me, "d_x", a->d_x, ldx, d, a->dtype));
         }
         if (want_dx) {
-            DENSE_TRY(check_matrix(me, "d_w_gate", a->d_w_gate, ldw, d, a->dtype));
-            DENSE_TRY(check_matrix(me, "d_w_up", a->d_w_up, ldw, d, a->dtype));
-            DENSE_TRY(check_matrix(me, "d_dx", a->d_dx, lddx, d, a->dtype));
+            ECF_TRY(check_matrix(me, "d_w_gate", a->d_w_gate, ldw, d, a->dtype));
+            ECF_TRY(check_matrix(me, "d_w_up", a->d_w_up, ldw, d, a->dtype));
+            ECF_TRY(check_matrix(me, "d_dx", a->d_dx, lddx, d, a->dtype));
         }
         if (want_dw) {
-            DENSE_TRY(check_matrix(me, "d_dw_gate", a->d_dw_gate, lddw, d, a->wgrad_dtype));
-            DENSE_TRY(check_matrix(me, "d_dw_up", a->d_dw_up, lddw, d, a->wgrad_dtype));
+            ECF_TRY(check_matrix(me, "d_dw_gate", a->d_dw_gate, lddw, d, a->wgrad_dtype));
+            ECF_TRY(check_matrix(me, "d_dw_up", a->d_dw_up, lddw, d, a->wgrad_dtype));
         }
-        DENSE_TRY(check_vector(me, "d_db_gate", a->d_db_gate, a->wgrad_dtype));
-        DENSE_TRY(check_vector(me, "d_db_up", a->d_db_up, a->wgrad_dtype));
+        ECF_TRY(check_vector(me, "d_db_gate", a->d_db_gate, a->wgrad_dtype));
+        ECF_TRY(check_vector(me, "d_db_up", a->d_db_up, a->wgrad_dtype));
         const BackWs w = back_ws(d, I, 2, a->dtype, T);
-        DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
-        DENSE_TRY(check_apart(me, {{"d_dx", a->d_dx}, {"d_dw_gate", a->d_dw_gate}, {"d_dw_up", a->d_dw_up},
+        ECF_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
+        ECF_TRY(check_apart(me, {{"d_dx", a->d_dx}, {"d_dw_gate", a->d_dw_gate}, {"d_dw_up", a->d_dw_up},
                                    {"d_db_gate", a->d_db_gate}, {"d_db_up", a->d_db_up}, {"d_ws", a->d_ws}},
                               {{"d_x", a->d_x}, {"d_w_gate", a->d_w_gate}, {"d_w_up", a->d_w_up}, {"d_a", a->d_a},
                                {"d_b", a->d_b}, {"d_dh", a->d_dh}}));
@@ -286,7 +228,7 @@ int ecf_gated_backward(const ecf_gated_args *a, int32_t T)
             q.sums[0] = a->d_db_gate, q.sums[1] = a->d_db_up;
             q.sums_dtype = a->wgrad_dtype;
             q.partial = (float *)ws;
-            DENSE_TRY(launch_dense_grad(q, &sums, st));
+            ECF_TRY(launch_dense_grad(q, &sums, st));
             gx.unscale = q.row_inverse, gw.unscale = q.col_inverse;
             gx.a[0] = q.dz, gw.a[0] = q.scaled ? q.dz_w : q.dz;
         }
@@ -328,8 +270,8 @@ int ecf_linear_forward(const ecf_linear_args *a, int32_t T)
         const char *me = "ecf_linear_forward";
         if (!a)
             return set_error(ECF_EINVAL, "%s: args is NULL", me);
-        DENSE_TRY(check_common(me, a->in_features, a->out_features, a->dtype, T));
-        DENSE_TRY(check_act(me, a->act));
+        ECF_TRY(check_common(me, a->in_features, a->out_features, a->dtype, T));
+        ECF_TRY(check_act(me, a->act));
         if (a->out_dtype != a->dtype && a->out_dtype != ECF_F32)
             return set_error(ECF_EINVAL, "%s: out_dtype must be dtype or ECF_F32 (got %d)", me, a->out_dtype);
         const int64_t K = a->in_features, N = a->out_features;
@@ -342,19 +284,19 @@ int ecf_linear_forward(const ecf_linear_args *a, int32_t T)
         g.act = a->act;
         if (T == 0)
             return ECF_OK;
-        DENSE_TRY(check_matrix(me, "d_x", a->d_x, g.lda, K, a->dtype));
-        DENSE_TRY(check_matrix(me, "d_w", a->d_w, g.ldb, K, a->dtype));
-        DENSE_TRY(check_matrix(me, "d_out", a->d_out, g.ldout, N, a->out_dtype));
-        DENSE_TRY(check_vector(me, "d_bias", a->d_bias, a->dtype));
+        ECF_TRY(check_matrix(me, "d_x", a->d_x, g.lda, K, a->dtype));
+        ECF_TRY(check_matrix(me, "d_w", a->d_w, g.ldb, K, a->dtype));
+        ECF_TRY(check_matrix(me, "d_out", a->d_out, g.ldout, N, a->out_dtype));
+        ECF_TRY(check_vector(me, "d_bias", a->d_bias, a->dtype));
         if (a->d_residual)
-            DENSE_TRY(check_matrix(me, "d_residual", a->d_residual, g.ldres, N, a->out_dtype));
+            ECF_TRY(check_matrix(me, "d_residual", a->d_residual, g.ldres, N, a->out_dtype));
         if (a->d_z)
-            DENSE_TRY(check_matrix(me, "d_z", a->d_z, g.ldsave, N, a->dtype));
+            ECF_TRY(check_matrix(me, "d_z", a->d_z, g.ldsave, N, a->dtype));
         const size_t need = forward_ws(T, K, N, a->dtype, 1);
-        DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, need));
-        DENSE_TRY(check_apart(me, {{"d_out", a->d_out}, {"d_z", a->d_z}, {"d_ws", need ? a->d_ws : nullptr}},
+        ECF_TRY(check_ws(me, a->d_ws, a->ws_bytes, need));
+        ECF_TRY(check_apart(me, {{"d_out", a->d_out}, {"d_z", a->d_z}, {"d_ws", need ? a->d_ws : nullptr}},
                               {{"d_x", a->d_x}, {"d_w", a->d_w}, {"d_bias", a->d_bias}}));
-        DENSE_TRY(check_apart(me, {{"d_z", a->d_z}, {"d_ws", need ? a->d_ws : nullptr}}, {{"d_residual", a->d_residual}}));
+        ECF_TRY(check_apart(me, {{"d_z", a->d_z}, {"d_ws", need ? a->d_ws : nullptr}}, {{"d_residual", a->d_residual}}));
         if (a->d_out == a->d_residual && g.ldout != g.ldres)
             return set_error(ECF_EINVAL, "%s: d_out is d_residual with another row stride (%lld and %lld)", me,
                              (long long)g.ldout, (long long)g.ldres);
@@ -373,9 +315,9 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
         const char *me = "ecf_linear_backward";
         if (!a)
             return set_error(ECF_EINVAL, "%s: args is NULL", me);
-        DENSE_TRY(check_common(me, a->in_features, a->out_features, a->dtype, T));
-        DENSE_TRY(check_act(me, a->act));
-        DENSE_TRY(check_grad_dtype(me, a->wgrad_dtype, a->dtype));
+        ECF_TRY(check_common(me, a->in_features, a->out_features, a->dtype, T));
+        ECF_TRY(check_act(me, a->act));
+        ECF_TRY(check_grad_dtype(me, a->wgrad_dtype, a->dtype));
         if (a->out_dtype != a->dtype && a->out_dtype != ECF_F32)
             return set_error(ECF_EINVAL, "%s: out_dtype must be dtype or ECF_F32 (got %d)", me, a->out_dtype);
         const int64_t K = a->in_features, N = a->out_features;
@@ -383,24 +325,24 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
                       lddy = ld_or(a->ld_dout, N), lddx = ld_or(a->ld_dx, K), lddw = ld_or(a->ld_dw, K);
         const bool want_dx = a->d_dx && T > 0, act = a->act != ECF_ACT_NONE;
         if (T > 0) {
-            DENSE_TRY(check_matrix(me, "d_dout", a->d_dout, lddy, N, a->out_dtype));
+            ECF_TRY(check_matrix(me, "d_dout", a->d_dout, lddy, N, a->out_dtype));
             if (act)
-                DENSE_TRY(check_matrix(me, "d_z", a->d_z, ldz, N, a->dtype));
+                ECF_TRY(check_matrix(me, "d_z", a->d_z, ldz, N, a->dtype));
             if (a->d_dw)
-                DENSE_TRY(check_matrix(me, "d_x", a->d_x, ldx, K, a->dtype));
+                ECF_TRY(check_matrix(me, "d_x", a->d_x, ldx, K, a->dtype));
         }
         if (want_dx) {
-            DENSE_TRY(check_matrix(me, "d_w", a->d_w, ldw, K, a->dtype));
-            DENSE_TRY(check_matrix(me, "d_dx", a->d_dx, lddx, K, a->dtype));
+            ECF_TRY(check_matrix(me, "d_w", a->d_w, ldw, K, a->dtype));
+            ECF_TRY(check_matrix(me, "d_dx", a->d_dx, lddx, K, a->dtype));
         }
         if (a->d_dw)
-            DENSE_TRY(check_matrix(me, "d_dw", a->d_dw, lddw, K, a->wgrad_dtype));
-        DENSE_TRY(check_vector(me, "d_dbias", a->d_dbias, a->wgrad_dtype));
+            ECF_TRY(check_matrix(me, "d_dw", a->d_dw, lddw, K, a->wgrad_dtype));
+        ECF_TRY(check_vector(me, "d_dbias", a->d_dbias, a->wgrad_dtype));
         // without an activation and in the operands' type, dy is dz
         const bool direct = !act && a->out_dtype == a->dtype;
         const BackWs w = back_ws(K, N, 1, a->dtype, T, !direct);
-        DENSE_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
-        DENSE_TRY(check_apart(me, {{"d_dx", a->d_dx}, {"d_dw", a->d_dw}, {"d_dbias", a->d_dbias}, {"d_ws", a->d_ws}},
+        ECF_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
+        ECF_TRY(check_apart(me, {{"d_dx", a->d_dx}, {"d_dw", a->d_dw}, {"d_dbias", a->d_dbias}, {"d_ws", a->d_ws}},
                               {{"d_x", a->d_x}, {"d_w", a->d_w}, {"d_z", a->d_z}, {"d_dout", a->d_dout}}));
         hipStream_t st = (hipStream_t)a->stream;
         const bool products = want_dx || (a->d_dw && T > 0);
@@ -422,7 +364,7 @@ int ecf_linear_backward(const ecf_linear_args *a, int32_t T)
             q.sums[0] = a->d_dbias;
             q.sums_dtype = a->wgrad_dtype;
             q.partial = (float *)a->d_ws;
-            DENSE_TRY(launch_dense_grad(q, &sums, st));
+            ECF_TRY(launch_dense_grad(q, &sums, st));
             gx.unscale = q.row_inverse, gw.unscale = q.col_inverse;
             gx.a[0] = q.dz, gw.a[0] = q.scaled ? q.dz_w : q.dz;
         }

@@ -2,11 +2,10 @@
 // call and describes its matrix products, the k_dense*.hip launchers run them.
 #pragma once
 
+#include "arg_checks.h"
 #include "ecf_internal.h"
 
 namespace ecf {
-
-inline size_t dense_esize(int dtype) { return dtype == ECF_F32 ? 4 : 2; }
 
 // One matrix product with its epilogue:
 //   acc_g[m][n] = sum_s sum_k A_s(m, k) B(n, k),  s < ksegs, k < K

@@ -56,6 +56,24 @@ __device__ __forceinline__ float wave_sum_f32(float x)
     return (r0 + r1) + (r2 + r3);
 }
 
+__device__ __forceinline__ double wave_sum_f64(double x)
+{
+    const auto step = [](double v, uint64_t o) { return v + __longlong_as_double((long long)o); };
+    x = step(x, dpp64<kDppXor1>((uint64_t)__double_as_longlong(x)));
+    x = step(x, dpp64<kDppXor2>((uint64_t)__double_as_longlong(x)));
+    x = step(x, dpp64<kDppHalfMirror>((uint64_t)__double_as_longlong(x)));
+    x = step(x, dpp64<kDppMirror>((uint64_t)__double_as_longlong(x)));
+    double r[4];
+#pragma unroll
+    for (int row = 0; row < 4; ++row) {
+        const uint64_t b = (uint64_t)__double_as_longlong(x);
+        const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 16 * row);
+        const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 16 * row);
+        r[row] = __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+    }
+    return (r[0] + r[1]) + (r[2] + r[3]);
+}
+
 // Selection key of (logit v, expert e): the fp32 bits mapped to an unsigned
 // order-preserving code (sign folded), then the complement of e, so a larger
 // key is a larger logit, or an equal logit with a lower expert id.  -0 counts as

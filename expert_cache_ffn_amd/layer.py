@@ -4,6 +4,7 @@ forward pass runs in libecf's kernels (or its host expert threads)."""
 from __future__ import annotations
 
 import warnings
+from typing import NamedTuple
 
 import torch
 
@@ -149,11 +150,12 @@ def _kept(*tensors):
     return [None if t is None else t.detach() for t in tensors]
 
 
-def _warn_untracked(what):
+def _warn_untracked(what, call="backward"):
     """A forward call that something requires gradients of; it gives none where they are on."""
     if torch.is_grad_enabled():
-        warnings.warn(f"{what}.forward is outside autograd: its output has no gradient function although the weights or "
-                      "an input require gradients.  Run it under torch.no_grad(), and call backward() with the "
+        name = what if "." in what else f"{what}.forward"
+        warnings.warn(f"{name} is outside autograd: its output has no gradient function although the weights or "
+                      f"an input require gradients.  Run it under torch.no_grad(), and call {call}() with the "
                       "output's gradient", stacklevel=3)
 
 
@@ -361,3 +363,283 @@ class Linear(_Dense):
                 q.d_dbias = db.data_ptr()
         self._run(L.ecf_linear_backward, q, T, self._back)
         return dx, dw, db
+
+
+# ---- token operators ------------------------------------------------------------------
+
+class NormOut(NamedTuple):
+    """What RMSNorm.forward gives; None for what was not asked for."""
+    y: torch.Tensor | None
+    sum: torch.Tensor
+    rstd: torch.Tensor | None
+    q: torch.Tensor | None
+    scale: torch.Tensor | None
+
+
+class _Tokens:
+    """What the token operators share: workspaces and streams.  A call runs on the current
+    stream of the operator's device and takes its workspace and outputs from torch's
+    allocator for that stream, so calls on several streams, and captured graphs, never
+    share one.  As the dense operators they are outside autograd."""
+
+    def _setup(self, device):
+        self.device = device
+        self._empty = {dt: torch.empty(0, dtype=dt, device=device).new_empty
+                       for dt in (torch.float32, torch.bfloat16, torch.float16, torch.int32, torch.uint8)}
+
+    def _run(self, fn, a, T, ws_bytes=0):
+        if _current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self._run(fn, a, T, ws_bytes)
+        if ws_bytes:
+            ws = self._empty[torch.uint8](ws_bytes)
+            a.d_ws, a.ws_bytes = ws.data_ptr(), ws_bytes
+        a.stream = _raw_stream(self.device.index) or None
+        fn(a, T)
+
+    def _out(self, name, t, rows, cols, dtype):
+        if t is None:
+            t = self._empty[dtype]((rows, cols))
+            return t, t.data_ptr(), cols
+        return (t,) + _matrix(name, t, rows, cols, dtype, self.device)
+
+    def _matrix_of(self, name, t, what="tokens"):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError(f"{name} must be a 2-D tensor [{what}, features]")
+        return t.shape[0]
+
+
+def _ws_cached(cache, key, size):
+    n = cache.get(key)
+    if n is None:
+        if len(cache) > 4096:
+            cache.clear()
+        n = cache[key] = size(*key)
+    return n
+
+
+class RMSNorm(_Tokens):
+    """y = sum * rstd * weight with sum = x + residual and rstd = 1 / sqrt(mean(sum^2) + eps).
+
+    weight [hidden] in `dtype` or fp32; dtype (the weight's unless given) is the type of x,
+    y and their gradients, sum_dtype (dtype unless given, or torch.float32) that of the
+    residual, the sum and their gradients: the sum a moe_layer_forward call takes as its
+    residual is fp32.  The object keeps the weight's memory, as GatedProjection does."""
+
+    def __init__(self, weight, eps=1e-6, dtype=None, sum_dtype=None):
+        if not isinstance(weight, torch.Tensor) or weight.dim() != 1 or not weight.is_cuda or 0 in weight.shape:
+            raise ValueError("weight must be a non-empty 1-D tensor on the GPU")
+        self._setup(weight.device)
+        self.hidden, = weight.shape
+        self.dtype = weight.dtype if dtype is None else dtype
+        self.sum_dtype = self.dtype if sum_dtype is None else sum_dtype
+        for name, t in (("weight", weight.dtype), ("sum_dtype", self.sum_dtype)):
+            if t is not self.dtype and t is not torch.float32:
+                raise ValueError(f"{name} must be {self.dtype} or torch.float32, got {t}")
+        a = L.NormArgs()
+        a.hidden, a.eps = self.hidden, float(eps)
+        a.dtype, a.sum_dtype = _dense_dt(self.dtype, "dtype"), _DENSE_DT[self.sum_dtype]
+        a.weight_dtype = a.wgrad_dtype = _DENSE_DT[weight.dtype]
+        a.d_weight = _vector("weight", weight, self.hidden, weight.dtype, self.device)
+        if not 0 <= float(eps) < float("inf"):
+            raise ValueError(f"eps must be finite and not negative, got {eps}")
+        self._learns = weight.requires_grad
+        self.weight, = _kept(weight)
+        self._a = a
+        self._ws_of = {}
+
+    def forward(self, x, residual=None, y=True, mx=False, save=False, out=None, sum_out=None):
+        """NormOut(y, sum, rstd, q, scale): y (into `out` if given); the sum (into sum_out if
+        given, which may be the residual; x itself without a residual); with save, rstd for
+        backward(); with mx, y in 8 bits: q [T, hidden] of torch.float8_e4m3fn and scale
+        [T, ceil(hidden / 32)] of torch.float8_e8m0fnu, y then only with y=True too."""
+        T = self._matrix_of("x", x)
+        a = L.NormArgs.from_buffer_copy(self._a)
+        a.d_x, a.ld_x = _matrix("x", x, T, self.hidden, self.dtype, self.device)
+        if (self._learns or x.requires_grad or residual is not None and residual.requires_grad) and not save:
+            _warn_untracked("RMSNorm")
+        total, o, rstd, q, scale = x, None, None, None, None
+        if residual is not None:
+            a.d_residual, a.ld_residual = _matrix("residual", residual, T, self.hidden, self.sum_dtype, self.device)
+            total, a.d_sum, a.ld_sum = self._out("sum_out", sum_out, T, self.hidden, self.sum_dtype)
+        elif sum_out is not None:
+            raise ValueError("sum_out is given without a residual: the sum is x")
+        if y:
+            o, a.d_y, a.ld_y = self._out("out", out, T, self.hidden, self.dtype)
+        elif out is not None or not mx:
+            raise ValueError("y=False needs mx=True and no out")
+        if mx:
+            q, a.d_q, _ = self._out("q", None, T, self.hidden, torch.uint8)
+            scale, a.d_q_scale, _ = self._out("scale", None, T, (self.hidden + 31) // 32, torch.uint8)
+            q, scale = q.view(torch.float8_e4m3fn), scale.view(torch.float8_e8m0fnu)
+        if save:
+            rstd = self._empty[torch.float32](T)
+            a.d_rstd = rstd.data_ptr()
+        self._run(L.ecf_norm_forward, a, T)
+        return NormOut(o, total, rstd, q, scale)
+
+    def backward(self, total, rstd, dy, dsum=None, w_grad_dtype=None, ds=None, need_dx=True, need_dw=True):
+        """(dx, ds, dweight) for the gradient dy of y and dsum of the sum (what reaches it past
+        the norm, or None), from the sum and rstd of the forward call.  ds (into `ds` if given,
+        which may be dsum) is the gradient of the residual, dx the same values in x's type: one
+        tensor where the types are one.  dx and ds are None without need_dx, dweight
+        without need_dw; it comes in w_grad_dtype (the weight's type, or torch.float32)."""
+        T = self._matrix_of("total", total)
+        a = L.NormArgs.from_buffer_copy(self._a)
+        gd = self.weight.dtype if w_grad_dtype is None else w_grad_dtype
+        if gd is not self.weight.dtype and gd is not torch.float32:
+            raise ValueError(f"w_grad_dtype must be {self.weight.dtype} or torch.float32, got {gd}")
+        a.wgrad_dtype = _DENSE_DT[gd]
+        st = total.dtype  # (a norm without a residual has x for its sum)
+        if st is not self.dtype and st is not self.sum_dtype:
+            raise ValueError(f"total must be {self.sum_dtype} (or {self.dtype}, an x without a residual), got {st}")
+        a.sum_dtype = _DENSE_DT[st]
+        a.d_sum, a.ld_sum = _matrix("total", total, T, self.hidden, st, self.device)
+        a.d_rstd = _vector("rstd", rstd, T, torch.float32, self.device)
+        if a.d_rstd is None and T:
+            raise ValueError("rstd is missing: forward(save=True) gives it")
+        a.d_dy, a.ld_dy = _matrix("dy", dy, T, self.hidden, self.dtype, self.device)
+        if dsum is not None:
+            a.d_dsum, a.ld_dsum = _matrix("dsum", dsum, T, self.hidden, st, self.device)
+        dx = dw = None
+        if need_dx:
+            ds, a.d_ds, a.ld_ds = self._out("ds", ds, T, self.hidden, st)
+            if st is self.dtype:
+                dx = ds
+            else:
+                dx, a.d_dx, a.ld_dx = self._out("dx", None, T, self.hidden, self.dtype)
+        elif ds is not None:
+            raise ValueError("ds is given but need_dx is false")
+        n = 0
+        if need_dw:
+            dw = self._empty[gd](self.hidden)
+            a.d_dweight = dw.data_ptr()
+            n = _ws_cached(self._ws_of, (self.hidden, T, 1), L.ecf_norm_workspace_bytes)
+        self._run(L.ecf_norm_backward, a, T, n)
+        return dx, ds, dw
+
+
+class TokenSort(_Tokens):
+    """The choices of tokens in the order of their experts: ids [T, k] (or [T], k = 1) of
+    torch.int32 or torch.int64, the choice f = t * k + j of token t.  A choice outside
+    [0, n_experts) is of no expert and comes last.
+
+    counts [n_experts], offsets [n_experts + 1] (the rows of expert e are offsets[e] to
+    offsets[e + 1]), order [T * k] (row -> f), place [T, k] (f -> row) and tiles
+    [n_experts + 2] (first tile of 64 rows of each expert) are int32 tensors on the ids'
+    device, made by the constructor's call on the current stream.  The experts between
+    dispatch() and combine() are the caller's: GatedProjection and Linear over the
+    rows of each."""
+
+    def __init__(self, ids, n_experts):
+        if not isinstance(ids, torch.Tensor) or ids.dim() not in (1, 2) or not ids.is_cuda:
+            raise ValueError("ids must be a [tokens, k] or [tokens] tensor on the GPU")
+        if ids.dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
+        self._setup(ids.device)
+        self.tokens, self.top_k = ids.shape if ids.dim() == 2 else (ids.shape[0], 1)
+        self.n_experts = int(n_experts)
+        wide = ids if ids.dim() == 2 else ids.unsqueeze(1)
+        a = L.SortArgs()
+        a.n_experts, a.top_k, a.idx_bytes = self.n_experts, self.top_k, ids.element_size()
+        a.d_idx, a.ld_idx = _matrix("ids", wide, self.tokens, self.top_k, ids.dtype, self.device)
+        n_ws = _ws_cached(_SORT_WS, (self.n_experts, self.top_k, self.tokens), L.ecf_token_sort_workspace_bytes)
+        E, R = self.n_experts, self.tokens * self.top_k
+        # one allocation, its parts at 16-byte boundaries
+        at = [0]
+        for n in (E, E + 1, E + 2, R, R):
+            at.append(at[-1] + (n + 3) // 4 * 4)
+        buf = self._empty[torch.int32](at[-1])
+        self.counts, self.offsets = buf[:E], buf[at[1]:at[1] + E + 1]
+        self.tiles, self.order = buf[at[2]:at[2] + E + 2], buf[at[3]:at[3] + R]
+        self.place = buf[at[4]:at[4] + R].view(self.tokens, self.top_k)
+        p = buf.data_ptr()
+        a.d_counts, a.d_offsets, a.d_tiles, a.d_order, a.d_place = (p + 4 * i for i in at[:5])
+        self._run(L.ecf_token_sort, a, self.tokens, n_ws)
+        t = L.TokenArgs()
+        t.n_experts, t.top_k, t.d_offsets, t.d_place = self.n_experts, self.top_k, a.d_offsets, a.d_place
+        self._a = t
+
+    def _weights(self, w):
+        if not isinstance(w, torch.Tensor) or w.numel() != self.tokens * self.top_k or w.dtype is not torch.float32 \
+                or w.device != self.device or not w.is_contiguous():
+            raise ValueError(f"weights must be a contiguous float32 tensor [{self.tokens}, {self.top_k}] on {self.device}")
+        return w.data_ptr()
+
+    def _args(self, t, rows, name):
+        n = self._matrix_of(name, t)
+        if n != rows:
+            raise ValueError(f"{name} must have {rows} rows, got {n}")
+        a = L.TokenArgs.from_buffer_copy(self._a)
+        a.hidden = t.shape[1]
+        return a, t.shape[1]
+
+    def dispatch(self, x, scale=None, dtype=None, out=None):
+        """rows [T * k, d]: rows[place[t, j]] = x[t], zeros behind the last expert's rows.  With a
+        scale, x is 8-bit (RMSNorm.forward's q and scale) and the rows are of `dtype`."""
+        a, d = self._args(x, self.tokens, "x")
+        if scale is None:
+            if dtype is not None and dtype is not x.dtype:
+                raise ValueError(f"the rows have x's type {x.dtype}, got {dtype}")
+            dtype = x.dtype
+            a.dtype = a.token_dtype = _dense_dt(dtype, "x")
+            a.d_x, a.ld_x = _matrix("x", x, self.tokens, d, dtype, self.device)
+            if x.requires_grad:
+                _warn_untracked("TokenSort.dispatch", call="dispatch_backward")
+        else:
+            a.dtype, a.token_dtype = _dense_dt(dtype, "dtype"), L.ECF_MXFP8
+            a.d_x, a.ld_x = _matrix("x", x, self.tokens, d, torch.float8_e4m3fn, self.device)
+            a.d_x_scale, a.ld_x_scale = _matrix("scale", scale, self.tokens, (d + 31) // 32, torch.float8_e8m0fnu, self.device)
+        rows, a.d_rows, a.ld_rows = self._out("out", out, self.tokens * self.top_k, d, dtype)
+        self._run(L.ecf_token_dispatch, a, self.tokens)
+        return rows
+
+    def combine(self, rows, weights=None, residual=None, out=None, out_dtype=None):
+        """out [T, d] = residual[t] + sum_j weights[t, j] * rows[place[t, j]] over the choices of an
+        expert (into `out` if given, which may be the residual); of the residual's or out_dtype's
+        type, else the rows' (the rows' type or torch.float32)."""
+        a, d = self._args(rows, self.tokens * self.top_k, "rows")
+        a.dtype = _dense_dt(rows.dtype, "rows")
+        a.d_rows, a.ld_rows = _matrix("rows", rows, self.tokens * self.top_k, d, rows.dtype, self.device)
+        od = out_dtype if out_dtype is not None else out.dtype if out is not None \
+            else residual.dtype if residual is not None else rows.dtype
+        if od is not rows.dtype and od is not torch.float32:
+            raise ValueError(f"out_dtype must be {rows.dtype} or torch.float32, got {od}")
+        a.token_dtype = _DENSE_DT[od]
+        if weights is not None:
+            a.d_weight = self._weights(weights)
+        if residual is not None:
+            a.d_residual, a.ld_residual = _matrix("residual", residual, self.tokens, d, od, self.device)
+        if any(t is not None and t.requires_grad for t in (rows, weights, residual)):
+            _warn_untracked("TokenSort.combine", call="combine_backward")
+        out, a.d_out, a.ld_out = self._out("out", out, self.tokens, d, od)
+        self._run(L.ecf_token_combine, a, self.tokens)
+        return out
+
+    def combine_backward(self, rows, weights, dout, need_drows=True, need_dweights=True):
+        """(drows, dweights) for the gradient dout of combine()'s output: drows [T * k, d] in
+        the rows' type, zeros behind the last expert's; dweights [T, k] in fp32, 0 for a choice of
+        no expert, None without need_dweights or weights.  The residual's gradient is dout itself."""
+        a, d = self._args(rows, self.tokens * self.top_k, "rows")
+        a.dtype = _dense_dt(rows.dtype, "rows")
+        a.d_rows, a.ld_rows = _matrix("rows", rows, self.tokens * self.top_k, d, rows.dtype, self.device)
+        if not isinstance(dout, torch.Tensor) or dout.dtype is not rows.dtype and dout.dtype is not torch.float32:
+            raise ValueError(f"dout must be a tensor of {rows.dtype} or torch.float32")
+        a.token_dtype = _DENSE_DT[dout.dtype]
+        a.d_dout, a.ld_dout = _matrix("dout", dout, self.tokens, d, dout.dtype, self.device)
+        drows = dweights = None
+        if weights is not None:
+            a.d_weight = self._weights(weights)
+            if need_dweights:
+                dweights, a.d_dweight, _ = self._out("dweights", None, self.tokens, self.top_k, torch.float32)
+        if need_drows:
+            drows, a.d_drows, a.ld_drows = self._out("drows", None, self.tokens * self.top_k, d, rows.dtype)
+        self._run(L.ecf_token_combine_backward, a, self.tokens)
+        return drows, dweights
+
+    def dispatch_backward(self, drows, residual=None, out=None):
+        """dx [T, d] = residual[t] (a gradient that x has already, or None) + the sum of its rows' gradients."""
+        return self.combine(drows, residual=residual, out=out)
+
+
+_SORT_WS = {}

@@ -62,7 +62,8 @@ typedef enum {
     ECF_F32 = 0,
     ECF_BF16 = 1,
     ECF_MXFP4 = 2,
-    ECF_F16 = 3 /* IEEE half; the dense feed-forward operators only */
+    ECF_F16 = 3,  /* IEEE half; the dense feed-forward and the token operators only */
+    ECF_MXFP8 = 4 /* e4m3 values with E8M0 scales; tokens of ecf_token_dispatch only */
 } ecf_dtype;
 
 typedef struct {
@@ -456,6 +457,137 @@ size_t ecf_linear_workspace_bytes(int32_t in_features, int32_t out_features, int
 int ecf_linear_forward(const ecf_linear_args *args, int32_t n_tokens);
 /* dx = dz W, dW = dz^T x, dbias = sum_t dz, with dz = dy * act'(z). */
 int ecf_linear_backward(const ecf_linear_args *args, int32_t n_tokens);
+
+/* ---- token operators ------------------------------------------------------------------
+ * What surrounds the matrix products of a layer: the norm in front of it, the way of
+ * tokens to experts and back where the experts are the caller's own (dense operators over
+ * slices of the sorted rows, which have gradients), and low-rank adapters beside a
+ * projection.  In fp32, bf16 or fp16 (ECF_F16), forward and backward.
+ *
+ * Matrices are row-major with the given row strides, in elements (0 = rows without gaps);
+ * rows may start at any multiple of the element size.  Sizes: tokens 0 to 2^22, widths 1
+ * to 2^22, strides below 2^31, n_experts and n_adapters 1 to 1024, top_k 1 to 32 with
+ * n_tokens * top_k up to 2^26, rank 1 to 256.  What lies between the end of a row and the
+ * next row's start changes no result and is not written.  Sums are fp32 or wider, each
+ * output is rounded once, nothing uses atomics on floating-point values: the same call
+ * gives the same bits.
+ *
+ * Workspaces, streams and captures as for the dense operators: d_ws needs
+ * ecf_*_workspace_bytes bytes at a 256-byte boundary (may be NULL where that is 0), holds
+ * nothing between calls and is not shared by calls that may overlap; a call is asynchronous
+ * on `stream`, a stream of the current device, allocates nothing and can be captured.  Outputs must not overlap
+ * inputs or each other except where said; two that start at the same address are refused.
+ */
+
+/* The norm: sum = x + residual, rounded to sum_dtype (x itself without a residual), and of
+ * the sum as it is written
+ *   rstd[t] = 1 / sqrt(mean_i sum[t][i]^2 + eps),  y[t][i] = sum[t][i] * rstd[t] * weight[i].
+ * The mean of squares is summed in 64 bits.  y goes to d_y in `dtype`, to d_q and
+ * d_q_scale in 8 bits, or both, each rounded once from fp32.
+ *
+ * 8 bits (ECF_MXFP8): 32 consecutive columns share the E8M0 scale 2^(b - 127), the layout
+ * of the MXFP4 blobs' scales; b is the smallest byte from 0 to 254 with
+ * max |y| <= 448 * 2^(b - 127) over the group's finite values (0 for a group of zeros),
+ * the elements are y / 2^(b - 127) in e4m3 (OCP, round to nearest even).  Infinite and NaN
+ * elements become NaN.  A last group of fewer columns has its own scale. */
+typedef struct {
+    int32_t hidden;
+    int32_t dtype;            /* of x, y and their gradients */
+    int32_t sum_dtype;        /* of the residual, the sum and their gradients: dtype or ECF_F32 */
+    int32_t weight_dtype;     /* of the weight: dtype or ECF_F32 */
+    float eps;                /* >= 0 */
+    const void *d_weight;     /* [d] or NULL: ones */
+    const void *d_x;          /* forward: [T][d] */
+    const void *d_residual;   /* forward: [T][d] or NULL */
+    int64_t ld_x, ld_residual;
+    void *d_sum;              /* [T][d].  Forward: written, may be d_residual (same stride), or NULL; without a
+                                 residual NULL.  Backward: read; without a residual x, with sum_dtype dtype */
+    int64_t ld_sum;
+    void *d_y;                /* forward: [T][d] or NULL */
+    int64_t ld_y;
+    void *d_q;                /* forward: e4m3 [T][d], strides in bytes, or NULL */
+    void *d_q_scale;          /* E8M0 [T][ceil(d / 32)]; with d_q */
+    int64_t ld_q, ld_q_scale;
+    float *d_rstd;            /* [T].  Forward: written, or NULL.  Backward: read */
+    /* backward only */
+    const void *d_dy;         /* [T][d] */
+    const void *d_dsum;       /* [T][d], the gradient that reaches the sum past the norm, or NULL */
+    int64_t ld_dy, ld_dsum;
+    void *d_dx;               /* [T][d] in dtype, or NULL */
+    void *d_ds;               /* [T][d], the same values in sum_dtype, or NULL; may be d_dsum (same stride) */
+    int64_t ld_dx, ld_ds;
+    int32_t wgrad_dtype;      /* of the weight's gradient: weight_dtype or ECF_F32 */
+    void *d_dweight;          /* [d] or NULL */
+    void *d_ws;
+    size_t ws_bytes;
+    void *stream;
+} ecf_norm_args;
+
+/* Workspace bytes of a call of up to n_tokens tokens (forward: 0); SIZE_MAX for an invalid
+ * shape. */
+size_t ecf_norm_workspace_bytes(int32_t hidden, int32_t n_tokens, int32_t backward);
+int ecf_norm_forward(const ecf_norm_args *args, int32_t n_tokens);
+/* ds = dsum + rstd * (g - sum * rstd^2 * mean_i(g * sum)) with g = dy * weight, which is the
+ * gradient of x and of the residual; dweight[i] = sum_t dy[t][i] * sum[t][i] * rstd[t]. */
+int ecf_norm_backward(const ecf_norm_args *args, int32_t n_tokens);
+
+/* Tokens by expert: the n_tokens * top_k choices f = t * top_k + j in the order of their
+ * experts, those of one expert in ascending f.  A choice outside [0, n_experts) (padding,
+ * a token over an expert's capacity) is of no expert and comes after all others. */
+typedef struct {
+    int32_t n_experts, top_k;
+    int32_t idx_bytes;        /* 4 or 8: of an element of d_idx (int32_t or int64_t) */
+    const void *d_idx;        /* [T][k], rows ld_idx elements apart (0: k) */
+    int64_t ld_idx;
+    int32_t *d_counts;        /* [E] choices of each expert */
+    int32_t *d_offsets;       /* [E + 1] the first row of each; [E]: rows of any expert */
+    int32_t *d_tiles;         /* [E + 2] the first of each expert's tiles of 64 rows, then of those of no
+                                 expert, then the number of all */
+    int32_t *d_order;         /* [T * k] row r -> f */
+    int32_t *d_place;         /* [T * k] f -> row r */
+    void *d_ws;
+    size_t ws_bytes;
+    void *stream;
+} ecf_sort_args;
+
+size_t ecf_token_sort_workspace_bytes(int32_t n_experts, int32_t top_k, int32_t n_tokens);
+int ecf_token_sort(const ecf_sort_args *args, int32_t n_tokens);
+
+/* Tokens to rows in the order of their experts, and rows back to tokens:
+ *   dispatch          rows[place[f]] = x[t], zeros for a choice of no expert (so the last
+ *                     T * k - offsets[E] rows are zeros)
+ *   combine           out[t] = residual[t] + sum_j weight[f] * rows[place[f]], j ascending, over
+ *                     the choices of an expert: rows behind those are not read
+ *   combine_backward  drows[place[f]] = weight[f] * dout[t], zeros for a choice of no expert;
+ *                     dweight[f] = sum_i rows[place[f]][i] * dout[t][i], 0 for one
+ * The gradient of dispatch is combine without weights; that of the residual is dout. */
+typedef struct {
+    int32_t hidden, n_experts, top_k;
+    int32_t dtype;            /* of the rows and their gradients */
+    int32_t token_dtype;      /* of x (dispatch: dtype or ECF_MXFP8), of the residual, out and dout (dtype or ECF_F32) */
+    const int32_t *d_offsets, *d_place; /* of ecf_token_sort over the same choices */
+    const float *d_weight;    /* [T][k] without gaps, or NULL: ones (dispatch: not read) */
+    const void *d_x;          /* dispatch: [T][d] */
+    const void *d_x_scale;    /* dispatch of ECF_MXFP8: [T][ceil(d / 32)] */
+    int64_t ld_x, ld_x_scale;
+    void *d_rows;             /* [T * k][d].  dispatch: written.  combine, combine_backward: read (the latter:
+                                 may be NULL without d_dweight) */
+    int64_t ld_rows;
+    const void *d_residual;   /* combine: [T][d] or NULL */
+    int64_t ld_residual;
+    void *d_out;              /* combine: [T][d]; may be d_residual (same stride) */
+    int64_t ld_out;
+    const void *d_dout;       /* combine_backward: [T][d] */
+    int64_t ld_dout;
+    void *d_drows;            /* combine_backward: [T * k][d] or NULL */
+    int64_t ld_drows;
+    float *d_dweight;         /* combine_backward: [T][k] without gaps, or NULL */
+    void *stream;
+} ecf_token_args;
+
+int ecf_token_dispatch(const ecf_token_args *args, int32_t n_tokens);
+int ecf_token_combine(const ecf_token_args *args, int32_t n_tokens);
+int ecf_token_combine_backward(const ecf_token_args *args, int32_t n_tokens);
 
 /* ---- measurement hooks ------------------------------------------------------------- */
 /* When enabled, every kernel launch is bracketed by HIP events on its stream
