@@ -15,7 +15,7 @@ from ._lib import (  # noqa: F401
     ECF_Q_AUTO, ECF_Q_ALL_GPU, ECF_Q_ALL_HOST, ECF_Q_FIXED,
     ECF_PATH_AUTO, ECF_PATH_DECODE, ECF_PATH_PREFILL,
     EcfError, Shape, LayerArgs, StepStats, CacheStats, BwProfile, GatedArgs, LinearArgs, NormArgs, SortArgs,
-    TokenArgs, EXPORTS,
+    TokenArgs, AdapterArgs, EXPORTS,
     lib, make_shape,
     ecf_expert_bytes, ecf_expert_layout, ecf_workspace_bytes, qstar_split,
     ecf_cache_create, ecf_cache_destroy, expert_cache_lookup, expert_cache_evict,
@@ -26,5 +26,6 @@ from ._lib import (  # noqa: F401
     ecf_linear_workspace_bytes, ecf_linear_forward, ecf_linear_backward,
     ecf_norm_workspace_bytes, ecf_norm_forward, ecf_norm_backward,
     ecf_token_sort_workspace_bytes, ecf_token_sort, ecf_token_dispatch, ecf_token_combine, ecf_token_combine_backward,
+    ecf_adapter_workspace_bytes, ecf_adapter_forward, ecf_adapter_backward,
     ecf_profile_enable, ecf_profile_get_all, ecf_profile_reset, ecf_stream_read, ecf_mfma_rate,
 )

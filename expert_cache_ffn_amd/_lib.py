@@ -34,7 +34,7 @@ EXPORTS = [
     "ecf_norm_workspace_bytes", "ecf_norm_forward", "ecf_norm_backward",
     "ecf_token_sort_workspace_bytes", "ecf_token_sort", "ecf_token_dispatch", "ecf_token_combine",
     "ecf_token_combine_backward",
-    "ecf_profile_enable",
+    "ecf_adapter_workspace_bytes", "ecf_adapter_forward", "ecf_adapter_backward", "ecf_profile_enable",
     "ecf_profile_get", "ecf_profile_reset", "ecf_stream_read", "ecf_mfma_rate",
 ]
 
@@ -143,6 +143,18 @@ class TokenArgs(Structure):
     ]
 
 
+class AdapterArgs(Structure):
+    _fields_ = [
+        ("in_features", c_int32), ("out_features", c_int32), ("rank", c_int32), ("n_adapters", c_int32),
+        ("dtype", c_int32), ("out_dtype", c_int32), ("d_a", c_void_p), ("d_b", c_void_p), ("d_scale", c_void_p),
+        ("idx_bytes", c_int32), ("d_idx", c_void_p), ("d_order", c_void_p), ("d_offsets", c_void_p), ("d_tiles", c_void_p),
+        ("d_x", c_void_p), ("ld_x", c_int64), ("d_h", c_void_p), ("d_residual", c_void_p), ("ld_residual", c_int64),
+        ("d_out", c_void_p), ("ld_out", c_int64), ("d_dout", c_void_p), ("ld_dout", c_int64),
+        ("d_dx", c_void_p), ("ld_dx", c_int64), ("wgrad_dtype", c_int32), ("d_da", c_void_p), ("d_db", c_void_p),
+        ("d_ws", c_void_p), ("ws_bytes", c_size_t), ("stream", c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -195,11 +207,13 @@ def lib():
                 f.argtypes, f.restype = [POINTER(args), c_int32], c_int32
         L.ecf_norm_workspace_bytes.argtypes = [c_int32] * 3
         L.ecf_token_sort_workspace_bytes.argtypes = [c_int32] * 3
-        for name in ("norm", "token_sort"):
+        L.ecf_adapter_workspace_bytes.argtypes = [c_int32] * 6
+        for name in ("norm", "token_sort", "adapter"):
             getattr(L, f"ecf_{name}_workspace_bytes").restype = c_size_t
         for name, args in (("norm_forward", NormArgs), ("norm_backward", NormArgs), ("token_sort", SortArgs),
                            ("token_dispatch", TokenArgs), ("token_combine", TokenArgs),
-                           ("token_combine_backward", TokenArgs)):
+                           ("token_combine_backward", TokenArgs), ("adapter_forward", AdapterArgs),
+                           ("adapter_backward", AdapterArgs)):
             f = getattr(L, f"ecf_{name}")
             f.argtypes, f.restype = [POINTER(args), c_int32], c_int32
         L.ecf_profile_enable.argtypes, L.ecf_profile_enable.restype = [c_int32], c_int32
@@ -417,6 +431,19 @@ def ecf_token_combine(args: TokenArgs, n_tokens):
 
 def ecf_token_combine_backward(args: TokenArgs, n_tokens):
     _check(lib().ecf_token_combine_backward(ctypes.byref(args), n_tokens))
+
+
+def ecf_adapter_workspace_bytes(in_features, out_features, rank, n_adapters, n_tokens, backward=False) -> int:
+    return _dense_ws(lib().ecf_adapter_workspace_bytes(int(in_features), int(out_features), int(rank), int(n_adapters),
+                                                       int(n_tokens), int(backward)))
+
+
+def ecf_adapter_forward(args: AdapterArgs, n_tokens):
+    _check(lib().ecf_adapter_forward(ctypes.byref(args), n_tokens))
+
+
+def ecf_adapter_backward(args: AdapterArgs, n_tokens):
+    _check(lib().ecf_adapter_backward(ctypes.byref(args), n_tokens))
 
 
 def ecf_profile_enable(on: bool):

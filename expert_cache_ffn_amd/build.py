@@ -13,8 +13,8 @@ BUILD = os.path.join(os.path.dirname(HERE), "_build")
 
 HIP_SRCS = ["k_route.hip", "k_decode.hip", "k_prefill.hip", "k_util.hip", "noalloc.hip", "k_dense.hip", "k_dense_few.hip",
             "k_dense_gated.hip", "k_dense_nt.hip", "k_dense_nn.hip", "k_dense_tn.hip", "k_dense_pair.hip",
-            "k_norm.hip", "k_tokens.hip"]
-CPP_SRCS = ["api.cpp", "cache.cpp", "qstar.cpp", "host_ffn.cpp", "bwprof.cpp", "dense.cpp", "dense_plan.cpp", "tokens.cpp"]
+            "k_norm.hip", "k_tokens.hip", "k_adapters.hip"]
+CPP_SRCS = ["api.cpp", "cache.cpp", "qstar.cpp", "host_ffn.cpp", "bwprof.cpp", "dense.cpp", "dense_plan.cpp", "tokens.cpp", "adapters.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

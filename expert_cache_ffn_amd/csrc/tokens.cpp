@@ -10,53 +10,12 @@ namespace ecf {
 namespace {
 
 constexpr int32_t kMaxExperts = 1024, kMaxTopK = 32;
-constexpr int64_t kMaxStride = (int64_t)1 << 31;
-
-int check_rows(const char *what, const char *name, const void *p, int64_t ld, int64_t width, size_t esize)
-{
-    if (!p)
-        return set_error(ECF_EINVAL, "%s: %s is NULL", what, name);
-    if ((uintptr_t)p % esize)
-        return set_error(ECF_EINVAL, "%s: %s is not aligned to its %zu-byte elements", what, name, esize);
-    if (ld < width)
-        return set_error(ECF_EINVAL, "%s: the row stride of %s (%lld) is below its width %lld", what, name,
-                         (long long)ld, (long long)width);
-    if (ld >= kMaxStride)
-        return set_error(ECF_EUNSUPPORTED, "%s: the row stride of %s (%lld) is 2^31 or more", what, name, (long long)ld);
-    return ECF_OK;
-}
-int check_rows(const char *what, const char *name, const void *p, int64_t ld, int64_t width, int dtype)
-{
-    return check_rows(what, name, p, ld, width, dense_esize(dtype));
-}
-
-int check_aligned(const char *what, const char *name, const void *p, size_t esize)
-{
-    if ((uintptr_t)p % esize)
-        return set_error(ECF_EINVAL, "%s: %s is not aligned to its %zu-byte elements", what, name, esize);
-    return ECF_OK;
-}
-
-int check_present(const char *what, const char *name, const void *p, size_t esize)
-{
-    if (!p)
-        return set_error(ECF_EINVAL, "%s: %s is NULL", what, name);
-    return check_aligned(what, name, p, esize);
-}
 
 int check_width(const char *what, int32_t d, int32_t T)
 {
     if (d < 1 || d > kTokenMax || T < 0 || T > kTokenMax)
         return set_error(ECF_EINVAL, "%s: the width must be 1..%d and n_tokens 0..%d (d=%d, T=%d)", what, kTokenMax, kTokenMax,
                          d, T);
-    return ECF_OK;
-}
-
-int check_same_stride(const char *what, const char *a, const void *p, int64_t lda, const char *b, const void *q, int64_t ldb)
-{
-    if (p && p == q && lda != ldb)
-        return set_error(ECF_EINVAL, "%s: %s is %s with another row stride (%lld and %lld)", what, a, b, (long long)lda,
-                         (long long)ldb);
     return ECF_OK;
 }
 

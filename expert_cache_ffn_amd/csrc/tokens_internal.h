@@ -75,4 +75,76 @@ int launch_dispatch(const MoveCall &c, hipStream_t st);
 int launch_combine_tokens(const MoveCall &c, hipStream_t st);
 int launch_combine_backward(const MoveCall &c, hipStream_t st);
 
+// ---- low-rank adapters -------------------------------------------------------------------
+// The sorted order of the tokens' adapters.
+struct AdapterOrder {
+    const void *idx;
+    int wide;  // 64-bit ids
+    const int32_t *order, *offsets, *tiles;
+    int T, n;
+};
+// Tokens up to which a forward pass takes them one by one, without an order.
+constexpr int kAdapterFew = 64;
+
+// part[s][t][j] = sum over split s of k of x[t][k] M[a](j, k): A[a] as it lies, [r][K] (of_b
+// false), or B[a]'s transpose (of_b: M[a] lies as [K][r]).
+struct ShrinkCall {
+    AdapterOrder o;
+    int dtype, x_dtype, K, r;
+    bool of_b;
+    const void *m, *x;
+    int64_t ldx;
+    float *part;
+    int splits, split_k;  // split_k: k per split, a multiple of 128
+};
+constexpr int kShrinkBlocks = 512, kShrinkSplits = 8;
+int shrink_splits(int T, int K);
+// Rows of h in all splits of any call of up to T tokens.
+inline int64_t shrink_rows(int64_t T)
+{
+    const int64_t split = kShrinkSplits * T < kShrinkBlocks * kTileRows ? kShrinkSplits * T : kShrinkBlocks * kTileRows;
+    return split > T ? split : T;
+}
+int launch_shrink(const ShrinkCall &c, hipStream_t st);
+
+// h[t][j] = sum of the splits, out[t][i] = residual[t][i] + scale[a] * sum_j h[t][j] M[a](i, j):
+// B[a] as it lies, [N][r], or A[a]'s transpose (of_a: M[a] lies as [r][N]).
+struct ExpandCall {
+    AdapterOrder o;
+    int dtype, out_dtype, N, r;
+    bool of_a;
+    const void *m;
+    const float *scale;  // null: ones
+    const float *part;
+    int splits;
+    float *h;          // [T][r], written; or null
+    bool scaled;       // h is written times the scale
+    const void *residual;
+    int64_t ldres;
+    void *out;  // null: h only
+    int64_t ldout;
+};
+int launch_expand(const ExpandCall &c, hipStream_t st);
+
+// Both for few tokens, in any order; h as above, between the two kernels.
+int launch_few_shrink(const ShrinkCall &c, hipStream_t st);
+int launch_few_expand(const ExpandCall &c, hipStream_t st);
+
+// d[a](j, i) = sum over a's tokens of g[t][j] * gscale[a] * x[t][i], as [r][W] (dA) or [W][r] (dB)
+struct OuterCall {
+    AdapterOrder o;
+    int x_dtype, grad_dtype, W, r;
+    bool of_b;
+    const float *g;
+    const float *gscale;  // null: ones
+    const void *x;
+    int64_t ldx;
+    void *d;
+    float *slots;  // outer_slots bytes
+    int chunks;    // the sorted rows in this many runs, blocks of their own
+};
+int outer_chunks(int T, int W);
+inline size_t outer_slots(int chunks, int W, int r) { return chunks > 1 ? al256((size_t)chunks * 2 * W * r * 4) : 0; }
+int launch_outer(const OuterCall &c, hipStream_t st);
+
 }  // namespace ecf

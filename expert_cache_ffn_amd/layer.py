@@ -519,6 +519,9 @@ class RMSNorm(_Tokens):
         return dx, ds, dw
 
 
+_SORT_WS = {}  # bytes by (experts, k, tokens)
+
+
 class TokenSort(_Tokens):
     """The choices of tokens in the order of their experts: ids [T, k] (or [T], k = 1) of
     torch.int32 or torch.int64, the choice f = t * k + j of token t.  A choice outside
@@ -537,6 +540,7 @@ class TokenSort(_Tokens):
         if ids.dtype not in (torch.int32, torch.int64):
             raise ValueError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
         self._setup(ids.device)
+        self.ids, = _kept(ids)
         self.tokens, self.top_k = ids.shape if ids.dim() == 2 else (ids.shape[0], 1)
         self.n_experts = int(n_experts)
         wide = ids if ids.dim() == 2 else ids.unsqueeze(1)
@@ -642,4 +646,101 @@ class TokenSort(_Tokens):
         return self.combine(drows, residual=residual, out=out)
 
 
-_SORT_WS = {}
+class LowRankAdapters(_Tokens):
+    """out[t] = residual[t] + scale[a] * up[a] (down[a] x[t]), a = ids[t]: low-rank adapters of
+    many requests beside a shared projection, whose output is the residual (or Linear.forward
+    takes this output as its residual).  A token whose id lies outside the stack has none.
+
+    down [n, rank, in_features] and up [n, out_features, rank] in fp32, bf16 or fp16, scale [n]
+    in fp32 or None (ones); the residual, out and dout are of out_dtype: the weights' type, or
+    torch.float32.  ids: [T] of torch.int32 or torch.int64, or a TokenSort over them, which a step
+    makes once for all its layers (the ids then stay as they are).  The object keeps the weights' memory, as Linear does."""
+
+    def __init__(self, down, up, scale=None, out_dtype=None):
+        if not isinstance(down, torch.Tensor) or down.dim() != 3 or not down.is_cuda or 0 in down.shape:
+            raise ValueError("down must be a non-empty tensor [adapters, rank, in_features] on the GPU")
+        self._setup(down.device)
+        self.dtype = down.dtype
+        self.n, self.rank, self.in_features = down.shape
+        if not isinstance(up, torch.Tensor) or up.dim() != 3 or 0 in up.shape or up.shape[0] != self.n or up.shape[2] != self.rank:
+            raise ValueError(f"up must be a non-empty tensor [{self.n}, out_features, {self.rank}]")
+        self.out_features = up.shape[1]
+        for name, t in (("down", down), ("up", up)):
+            if t.dtype is not self.dtype or t.device != self.device or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous tensor of {self.dtype} on {self.device}")
+        self.out_dtype = self.dtype if out_dtype is None else out_dtype
+        if self.out_dtype is not self.dtype and self.out_dtype is not torch.float32:
+            raise ValueError(f"out_dtype must be {self.dtype} or torch.float32, got {out_dtype}")
+        a = L.AdapterArgs()
+        a.in_features, a.out_features, a.rank, a.n_adapters = self.in_features, self.out_features, self.rank, self.n
+        a.dtype, a.out_dtype = _dense_dt(self.dtype, "down"), _DENSE_DT[self.out_dtype]
+        a.d_a, a.d_b = down.data_ptr(), up.data_ptr()
+        a.d_scale = _vector("scale", scale, self.n, torch.float32, self.device)
+        self._learns = down.requires_grad or up.requires_grad
+        self.down, self.up, self.scale = _kept(down, up, scale)
+        self._a = a
+        self._ws_of = {}
+
+    def _ids(self, a, ids, T):
+        if isinstance(ids, TokenSort):
+            if (ids.tokens, ids.top_k, ids.n_experts) != (T, 1, self.n) or ids.device != self.device:
+                raise ValueError(f"the TokenSort must be of {T} tokens, one choice of {self.n} each, on {self.device}")
+            a.d_order, a.d_offsets, a.d_tiles = ids.order.data_ptr(), ids.offsets.data_ptr(), ids.tiles.data_ptr()
+            ids = ids.ids if ids.ids.dim() == 1 else ids.ids[:, 0]
+        wide = isinstance(ids, torch.Tensor) and ids.dtype is torch.int64
+        a.idx_bytes, a.d_idx = 8 if wide else 4, _vector("ids", ids, T, torch.int64 if wide else torch.int32, self.device)
+        if a.d_idx is None and T:
+            raise ValueError("ids is missing")
+
+    def _ws(self, T, backward):
+        return _ws_cached(self._ws_of, (self.in_features, self.out_features, self.rank, self.n, T, backward),
+                          L.ecf_adapter_workspace_bytes)
+
+    def forward(self, x, ids, residual=None, out=None, save=False):
+        """out [T, out_features] (into `out` if given, which may be the residual); with save,
+        (out, h): also h [T, rank] = down[a] x[t] in fp32, for backward()."""
+        T = self._matrix_of("x", x)
+        a = L.AdapterArgs.from_buffer_copy(self._a)
+        a.d_x, a.ld_x = _matrix("x", x, T, self.in_features, self.dtype, self.device)
+        self._ids(a, ids, T)
+        if residual is not None:
+            a.d_residual, a.ld_residual = _matrix("residual", residual, T, self.out_features, self.out_dtype, self.device)
+        if (self._learns or x.requires_grad or residual is not None and residual.requires_grad) and not save:
+            _warn_untracked("LowRankAdapters")
+        y, a.d_out, a.ld_out = self._out("out", out, T, self.out_features, self.out_dtype)
+        if save:
+            h, a.d_h, _ = self._out("h", None, T, self.rank, torch.float32)
+        self._run(L.ecf_adapter_forward, a, T, self._ws(T, 0))
+        return (y, h) if save else y
+
+    def backward(self, x, ids, h, dout, residual=None, w_grad_dtype=None, dx=None, need_dx=True, need_dw=True):
+        """(dx, ddown, dup) for the gradient dout of out, from the x and ids of the forward call
+        and the h it saved.  residual: a gradient that x has already (the projection's), added
+        to dx (which it may be); dx is None without need_dx, ddown and dup without need_dw;
+        they come in w_grad_dtype (the weights' type, or torch.float32), zeros for an
+        adapter of no token.  The forward residual's gradient is dout itself."""
+        T = self._matrix_of("x", x)
+        a = L.AdapterArgs.from_buffer_copy(self._a)
+        gd = self.dtype if w_grad_dtype is None else w_grad_dtype
+        if gd is not self.dtype and gd is not torch.float32:
+            raise ValueError(f"w_grad_dtype must be {self.dtype} or torch.float32, got {gd}")
+        a.wgrad_dtype = _DENSE_DT[gd]
+        a.d_x, a.ld_x = _matrix("x", x, T, self.in_features, self.dtype, self.device)
+        self._ids(a, ids, T)
+        a.d_dout, a.ld_dout = _matrix("dout", dout, T, self.out_features, self.out_dtype, self.device)
+        down = up = None
+        if need_dx:
+            if residual is not None:
+                a.d_residual, a.ld_residual = _matrix("residual", residual, T, self.in_features, self.dtype, self.device)
+            dx, a.d_dx, a.ld_dx = self._out("dx", dx, T, self.in_features, self.dtype)
+        elif dx is not None or residual is not None:
+            raise ValueError("dx or residual is given but need_dx is false")
+        if need_dw:
+            hp, ld = _matrix("h", h, T, self.rank, torch.float32, self.device)
+            if ld != self.rank:
+                raise ValueError(f"h must be contiguous (row stride {ld})")
+            a.d_h = hp
+            down, up = self._empty[gd](self.down.shape), self._empty[gd](self.up.shape)
+            a.d_da, a.d_db = down.data_ptr(), up.data_ptr()
+        self._run(L.ecf_adapter_backward, a, T, self._ws(T, 1))
+        return dx, down, up

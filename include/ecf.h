@@ -589,6 +589,51 @@ int ecf_token_dispatch(const ecf_token_args *args, int32_t n_tokens);
 int ecf_token_combine(const ecf_token_args *args, int32_t n_tokens);
 int ecf_token_combine_backward(const ecf_token_args *args, int32_t n_tokens);
 
+/* Low-rank adapters of many requests beside a shared projection: token t has the adapter
+ * a = idx[t] of a stack, or none (an idx outside [0, n_adapters)):
+ *   h[t] = A[a] x[t],  out[t] = residual[t] + scale[a] * B[a] h[t]
+ * (out[t] = residual[t], h[t] = 0 without an adapter).  The residual is the projection's
+ * output; or the call's output is ecf_linear_forward's residual. */
+typedef struct {
+    int32_t in_features, out_features, rank, n_adapters; /* K, N, r */
+    int32_t dtype;            /* of x, A, B and the gradient of x */
+    int32_t out_dtype;        /* of the residual, out and dout: dtype or ECF_F32 */
+    const void *d_a;          /* [n][r][K] without gaps */
+    const void *d_b;          /* [n][N][r] without gaps */
+    const float *d_scale;     /* [n] or NULL: ones */
+    int32_t idx_bytes;        /* 4 or 8: of an element of d_idx (int32_t or int64_t) */
+    const void *d_idx;        /* [T] */
+    /* of ecf_token_sort over idx with top_k 1; all three or none (then the call sorts where it has to) */
+    const int32_t *d_order, *d_offsets, *d_tiles;
+    const void *d_x;          /* [T][K] */
+    int64_t ld_x;
+    float *d_h;               /* [T][r] without gaps.  Forward: written, or NULL.  Backward: read with d_db */
+    const void *d_residual;   /* forward: [T][N] in out_dtype; backward: [T][K] in dtype, added to dx; or NULL */
+    int64_t ld_residual;
+    void *d_out;              /* forward: [T][N]; may be d_residual (same stride) */
+    int64_t ld_out;
+    /* backward only */
+    const void *d_dout;       /* [T][N] */
+    int64_t ld_dout;
+    void *d_dx;               /* [T][K] or NULL; may be d_residual (same stride) */
+    int64_t ld_dx;
+    int32_t wgrad_dtype;      /* of the two below: dtype or ECF_F32 */
+    void *d_da, *d_db;        /* [n][r][K] and [n][N][r] without gaps, or NULL; zeros for an adapter of no token */
+    void *d_ws;
+    size_t ws_bytes;
+    void *stream;
+} ecf_adapter_args;
+
+/* Workspace bytes of a call of up to n_tokens tokens (backward 0 or 1); SIZE_MAX for an
+ * invalid shape. */
+size_t ecf_adapter_workspace_bytes(int32_t in_features, int32_t out_features, int32_t rank, int32_t n_adapters,
+                                   int32_t n_tokens, int32_t backward);
+int ecf_adapter_forward(const ecf_adapter_args *args, int32_t n_tokens);
+/* g[t] = scale[a] * B[a]^T dout[t], dx[t] = residual[t] + A[a]^T g[t] (residual[t] without an
+ * adapter), dA[a] = sum_t g[t] x[t]^T, dB[a] = scale[a] * sum_t dout[t] h[t]^T over a's tokens.
+ * The gradient of the forward residual is dout. */
+int ecf_adapter_backward(const ecf_adapter_args *args, int32_t n_tokens);
+
 /* ---- measurement hooks ------------------------------------------------------------- */
 /* When enabled, every kernel launch is bracketed by HIP events on its stream
  * and its duration is accumulated per kernel name (adds event overhead). */

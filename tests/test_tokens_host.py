@@ -179,3 +179,67 @@ def test_python_argument_checks():
         with pytest.raises(ValueError):
             make()
     assert (ctypes.sizeof(ecf.NormArgs), ctypes.sizeof(ecf.SortArgs), ctypes.sizeof(ecf.TokenArgs)) == (240, 96, 176)
+
+
+def adapter(**kw):
+    a = ecf.AdapterArgs()
+    a.in_features, a.out_features, a.rank, a.n_adapters, a.idx_bytes = 64, 32, 8, 4, 4
+    a.dtype, a.out_dtype, a.wgrad_dtype, a.ws_bytes = ecf.ECF_BF16, ecf.ECF_F32, ecf.ECF_BF16, 1 << 30
+    return fill(a, ("d_a", "d_b", "d_scale", "d_idx", "d_order", "d_offsets", "d_tiles", "d_x", "d_h", "d_residual", "d_out", "d_dout",
+                    "d_dx", "d_da", "d_db", "d_ws"), **kw)
+
+
+ADAPTER = [dict(in_features=0), dict(out_features=(1 << 22) + 1), dict(rank=0), dict(rank=257), dict(n_adapters=0), dict(n_adapters=1025),
+           dict(dtype=ecf.ECF_MXFP8), dict(out_dtype=ecf.ECF_F16), dict(idx_bytes=2), dict(d_order=0), dict(d_offsets=0), dict(d_tiles=0),
+           dict(d_order=A + 2), dict(d_scale=A + 2), dict(d_h=A + 1), dict(d_idx=0), dict(d_idx=A + 2), dict(d_b=0), dict(d_b=A + 1),
+           dict(d_a=0), dict(d_x=0), dict(ld_x=63)]
+
+
+@pytest.mark.parametrize("bad", ADAPTER + [dict(d_out=0), dict(d_out=A + 2), dict(ld_out=31), dict(d_residual=A + 2), dict(ld_residual=31)])
+def test_adapter_forward_refusals(bad):
+    refused(ecf.ecf_adapter_forward, adapter(**bad))
+
+
+@pytest.mark.parametrize("bad", ADAPTER + [dict(d_dout=0), dict(d_dout=A + 2), dict(ld_dout=31), dict(d_h=0), dict(d_dx=A + 1), dict(ld_dx=63),
+                                           dict(d_residual=A + 1), dict(ld_residual=63), dict(d_da=A + 1), dict(d_db=A + 1),
+                                           dict(wgrad_dtype=ecf.ECF_F16)])
+def test_adapter_backward_refusals(bad):
+    refused(ecf.ecf_adapter_backward, adapter(**bad))
+
+
+@pytest.mark.parametrize("fn,out,others", [
+    (ecf.ecf_adapter_forward, "d_out", ("d_x", "d_a", "d_b", "d_scale", "d_idx", "d_order", "d_offsets", "d_tiles", "d_h", "d_ws")),
+    (ecf.ecf_adapter_forward, "d_h", ("d_x", "d_residual")),
+    (ecf.ecf_adapter_backward, "d_dx", ("d_x", "d_a", "d_dout", "d_h", "d_da", "d_db", "d_ws")),
+    (ecf.ecf_adapter_backward, "d_db", ("d_b", "d_dout", "d_residual", "d_da", "d_order"))])
+def test_adapter_outputs_on_other_operands_are_refused(fn, out, others):
+    for other in others:
+        a = adapter()
+        setattr(a, out, getattr(a, other))
+        refused(fn, a, match="same memory")
+
+
+def test_adapter_counts_strides_and_workspace():
+    for fn in (ecf.ecf_adapter_forward, ecf.ecf_adapter_backward):
+        refused(fn, adapter(), T=-1)
+        refused(fn, adapter(), T=(1 << 22) + 1)
+        refused(fn, adapter(ws_bytes=100), T=100, code=ecf.ECF_ENOSPC)
+        refused(fn, adapter(d_ws=A + 128), T=100)
+        assert getattr(ecf.lib(), fn.__name__)(None, 4) == ecf.ECF_EINVAL
+    refused(ecf.ecf_adapter_forward, adapter(ld_out=1 << 31), code=ecf.ECF_EUNSUPPORTED)
+    refused(ecf.ecf_adapter_forward, adapter(d_out=9 * A, d_residual=9 * A, ld_out=40, ld_residual=48), match="stride")
+    refused(ecf.ecf_adapter_backward, adapter(d_dx=9 * A, d_residual=9 * A, ld_dx=72, ld_residual=80), match="stride")
+    ecf.ecf_adapter_forward(adapter(d_x=0, d_out=0, d_idx=0), 0)
+    for bad in ((0, 32, 8, 4, 10), (64, 32, 300, 4, 10), (64, 32, 8, 4, -1)):
+        with pytest.raises(ecf.EcfError):
+            ecf.ecf_adapter_workspace_bytes(*bad)
+    for back in (False, True):  # what serves so many tokens serves fewer
+        for shape in ((4096, 4096, 16, 64), (64, 100, 3, 1), (300, 8192, 256, 1024)):
+            last = 0
+            for T in sorted({0, 1, 63, 64, 65, 100, 100000, 1 << 20} | {64 * i + d for i in range(1, 600, 7) for d in (-1, 0, 1)}):
+                need = ecf.ecf_adapter_workspace_bytes(*shape, T, back)
+                assert need >= last, (shape, T)
+                last = need
+    assert ctypes.sizeof(ecf.AdapterArgs) == 224
+    with pytest.raises(ValueError):
+        ly.LowRankAdapters(torch.zeros(2, 4, 8), torch.zeros(2, 8, 4))  # not on the GPU

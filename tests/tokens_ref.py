@@ -114,4 +114,60 @@ def combine_backward(rows, place, live, weights, dout, dtype):
     return {"drows": rounded(drows, drows.abs() * E23, dtype), "dweights": (terms.sum(2), terms.abs().sum(2) * 12 * E23 + 1e-37)}
 
 
-__all__ = ["DT", "E23", "half_step", "rand", "strided"]
+
+def _parts(parts):
+    """Relative error of a product with a value held in bf16 parts: 8 bits each, rounded."""
+    return 2.0 ** -(8 * parts + 1)
+
+
+def adapters_forward(q, dtype, out_dtype):
+    """{h, out} with bounds: h a sum of K products in fp32; out the sum of r products of h, held in fp32 or, beside bf16
+    matrices, in two bf16 parts (three for an fp32 output)."""
+    ids = q["ids"].long()
+    n, r, K = q["down"].shape
+    T, N = len(ids), q["up"].shape[1]
+    h = torch.zeros(T, r, dtype=torch.float64, device=ids.device)
+    eh, out, eout = h.clone(), torch.zeros(T, N, dtype=torch.float64, device=ids.device), torch.zeros(T, N, dtype=torch.float64, device=ids.device)
+    split = _parts(3 if out_dtype is torch.float32 else 2) if dtype is torch.bfloat16 else 0
+    for i in range(n):
+        at = (ids == i).nonzero().view(-1)
+        if not len(at):
+            continue
+        x, a, b, s = q["x"][at].double(), q["down"][i].double(), q["up"][i].double(), float(q["scale"][i])
+        h[at] = x @ a.t()
+        eh[at] = (x.abs() @ a.abs().t()) * ((K + 12) * E23)
+        out[at] = s * (h[at] @ b.t())
+        eout[at] = s * ((eh[at] + h[at].abs() * ((r + 8) * E23 + split)) @ b.abs().t())
+    if q["residual"] is not None:
+        out = out + q["residual"].double()
+    return {"h": (h, eh), "out": rounded(out, eout + out.abs() * E23, out_dtype)}
+
+
+def adapters_backward(q, dtype, gd):
+    ids = q["ids"].long()
+    n, r, K = q["down"].shape
+    T, N = len(ids), q["up"].shape[1]
+    dx, edx = torch.zeros(T, K, dtype=torch.float64, device=ids.device), torch.zeros(T, K, dtype=torch.float64, device=ids.device)
+    da, db = torch.zeros(n, r, K, dtype=torch.float64, device=ids.device), torch.zeros(n, N, r, dtype=torch.float64, device=ids.device)
+    eda, edb = torch.zeros_like(da), torch.zeros_like(db)
+    bf = dtype is torch.bfloat16
+    split_x = _parts(2) if bf else 0
+    split_w = _parts(3 if gd is torch.float32 else 2) if bf else 0
+    for i in range(n):
+        at = (ids == i).nonzero().view(-1)
+        if not len(at):
+            continue
+        x, a, b, s = q["x"][at].double(), q["down"][i].double(), q["up"][i].double(), float(q["scale"][i])
+        dy, h = q["dout"][at].double(), q["h"][at].double()
+        g = s * (dy @ b)
+        # (an fp32 dout beside bf16 matrices is held in three parts)
+        eg = s * (dy.abs() @ b.abs()) * ((N + 14) * E23 + (_parts(3) if bf else 0))
+        dx[at] = g @ a
+        edx[at] = (eg + g.abs() * ((r + 8) * E23 + split_x)) @ a.abs()
+        da[i] = g.t() @ x
+        eda[i] = (eg + g.abs() * ((len(at) + 8) * E23 + split_w)).t() @ x.abs()
+        db[i] = s * (dy.t() @ h)
+        edb[i] = s * (dy.abs().t() @ (h.abs() * ((len(at) + 9) * E23 + split_w)))
+    if q["res_x"] is not None:
+        dx = dx + q["res_x"].double()
+    return {"dx": rounded(dx, edx + dx.abs() * E23, dtype), "ddown": rounded(da, eda, gd), "dup": rounded(db, edb, gd)}
