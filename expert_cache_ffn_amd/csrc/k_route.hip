@@ -103,41 +103,6 @@ __global__ __launch_bounds__(256) void k_topk(const float *__restrict__ logits, 
 
 // Exclusive scan of v over the block (blockDim multiple of 64, <= 1024).
 // sh: >= 17 ints of LDS.  *total receives the block sum.
-// Inclusive scan over the wave by DPP: row_shr 1, 2, 4, 8 inside each row of 16
-// lanes, then lane 15 of rows 0 and 2 into rows 1 and 3 (row_bcast:15), then
-// lane 31 into rows 2 and 3 (row_bcast:31).  Lanes a step does not write (no
-// source lane, or a row outside its row mask) take `old` = 0.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t dpp_or0(uint32_t x)
-{
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ uint32_t wave_incl_scan(uint32_t x)
-{
-    x += dpp_or0<0x111, 0xF>(x);
-    x += dpp_or0<0x112, 0xF>(x);
-    x += dpp_or0<0x114, 0xF>(x);
-    x += dpp_or0<0x118, 0xF>(x);
-    x += dpp_or0<0x142, 0xA>(x);
-    x += dpp_or0<0x143, 0xC>(x);
-    return x;
-}
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint64_t dpp_or0_64(uint64_t x)
-{
-    return ((uint64_t)dpp_or0<CTRL, ROWS>((uint32_t)(x >> 32)) << 32) | dpp_or0<CTRL, ROWS>((uint32_t)x);
-}
-__device__ __forceinline__ uint64_t wave_incl_scan64(uint64_t x)
-{
-    x += dpp_or0_64<0x111, 0xF>(x);
-    x += dpp_or0_64<0x112, 0xF>(x);
-    x += dpp_or0_64<0x114, 0xF>(x);
-    x += dpp_or0_64<0x118, 0xF>(x);
-    x += dpp_or0_64<0x142, 0xA>(x);
-    x += dpp_or0_64<0x143, 0xC>(x);
-    return x;
-}
-
 __device__ int block_excl_scan(int v, int *sh, int *total)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, nw = blockDim.x >> 6;

@@ -13,13 +13,17 @@
 namespace ecf {
 namespace {
 
-constexpr int kSortOne = 4096;      // choices up to which one block sorts them all
-constexpr int kSortSegments = 128;  // most segments
-constexpr int kSortRows = 1024;     // choices that a block takes at a time
+constexpr int kSortRows = 1024;          // choices that a block takes at a time
+constexpr int kSortOne = 4 * kSortRows;  // up to which one block sorts them all
+constexpr int kSortSegments = 128;       // most segments
 
-__device__ __forceinline__ int choice(const SortCall &c, int64_t f)
+__device__ __forceinline__ int choice(const SortCall &c, uint32_t f)
 {
-    const int64_t t = f / c.k, at = t * c.ldidx + (f - t * c.k);
+    int64_t at = f;
+    if (c.ldidx != c.k) {
+        const uint32_t t = f / (uint32_t)c.k;
+        at = t * c.ldidx + (f - t * (uint32_t)c.k);
+    }
     const int64_t e = c.wide ? ((const int64_t *)c.idx)[at] : ((const int32_t *)c.idx)[at];
     return e >= 0 && e < c.E ? (int)e : c.E;
 }
@@ -35,40 +39,35 @@ __device__ __forceinline__ uint64_t peers_of(int key, bool valid, int bits)
     return valid ? m : 0ull;
 }
 
-// Exclusive sums over the block's 1024 threads of two counts at once (each below 2^31 in
-// total); sh: 17 values.
+// Exclusive sums over the block's threads (NW waves) of two counts at once, each below 2^31 in
+// total.
+template <int NW>
 __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t *sh, uint64_t *total)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    uint64_t x = v;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint64_t y = __shfl_up(x, o, 64);
-        x += lane >= o ? y : 0;
-    }
+    const uint64_t x = wave_incl_scan64(v);
     if (lane == 63)
         sh[w] = x;
     __syncthreads();
     uint64_t before = 0, all = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < NW; ++i) {
         const uint64_t s = sh[i];
         before += i < w ? s : 0;
         all += s;
     }
-    __syncthreads();
     *total = all;
     return before + x - v;
 }
 
-__global__ __launch_bounds__(1024) void k_token_count(SortCall c, int64_t per)
+__global__ __launch_bounds__(1024) void k_token_count(SortCall c, uint32_t per)
 {
     extern __shared__ int hist[];  // [E + 1]
     for (int e = threadIdx.x; e <= c.E; e += 1024)
         hist[e] = 0;
     __syncthreads();
-    const int64_t rows = (int64_t)c.T * c.k, end = min(rows, ((int64_t)blockIdx.x + 1) * per);
-    for (int64_t f = (int64_t)blockIdx.x * per + threadIdx.x; f < end; f += 1024)
+    const uint32_t rows = (uint32_t)c.T * c.k, beg = blockIdx.x * per, end = min(rows, beg + per);
+    for (uint32_t f = beg + threadIdx.x; f < end; f += 1024)
         atomicAdd(&hist[choice(c, f)], 1);
     __syncthreads();
     for (int e = threadIdx.x; e <= c.E; e += 1024)
@@ -76,36 +75,76 @@ __global__ __launch_bounds__(1024) void k_token_count(SortCall c, int64_t per)
 }
 
 // Each block places its segment; block 0 writes the tables.  segments: the counts of all
-// segments (one segment: counted here).  A wave owns a run of its segment's choices.
-__global__ __launch_bounds__(1024) void k_token_place(SortCall c, int64_t per, int segments, int bits)
+// segments (one segment: counted here).  A wave owns a run of its segment's choices; where that
+// is at most HELD steps of 64, their numbers and ranks stay in registers, otherwise they are
+// counted first and ranked in a second pass.  The block has at least E threads.
+template <int NW, int HELD>
+__global__ __launch_bounds__(64 * NW) void k_token_place(SortCall c, uint32_t per, int segments, int bits)
 {
-    extern __shared__ int base[];  // [16][E + 1]
-    __shared__ uint64_t sh[17];
+    extern __shared__ int base[];  // [NW][E + 1]
+    __shared__ uint64_t sh[NW];
+    constexpr int NT = 64 * NW;
     const int EB = c.E + 1, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const int64_t rows = (int64_t)c.T * c.k, beg = (int64_t)blockIdx.x * per, end = min(rows, beg + per);
-    const int64_t run = ((per + 15) / 16 + 63) / 64 * 64, wb = min(end, beg + w * run), we = min(end, wb + run);
-    for (int i = tid; i < 16 * EB; i += 1024)
-        base[i] = 0;
-    __syncthreads();
-    for (int64_t f = wb + lane; f < we; f += 64)
-        atomicAdd(&base[w * EB + choice(c, f)], 1);
-    __syncthreads();
-    // expert tid's rows, those before this segment, and its first row
-    int all = 0, before = 0;
-    if (tid < c.E) {
-        if (segments == 1)
-            for (int q = 0; q < 16; ++q)
-                all += base[q * EB + tid];
-        else
-#pragma unroll 8
-            for (int s = 0; s < segments; ++s) {
-                const int v = c.segments[(int64_t)s * EB + tid];
-                all += v;
-                before += s < (int)blockIdx.x ? v : 0;
-            }
+    const uint32_t rows = (uint32_t)c.T * c.k, beg = min(rows, blockIdx.x * per), end = min(rows, beg + per);
+    const uint32_t run = ((per + NW - 1) / NW + 63) / 64 * 64, wb = min(end, beg + w * run), we = min(end, wb + run);
+    int key[HELD ? HELD : 1], rank[HELD ? HELD : 1];
+    if constexpr (HELD > 0) {
+#pragma unroll
+        for (int q = 0; q < HELD; ++q) {
+            const uint32_t f = wb + q * 64 + lane;
+            key[q] = f < we ? choice(c, f) : -1;
+        }
     }
+    for (int i = tid; i < NW * EB; i += NT)
+        base[i] = 0;
+    // this expert's rows in all segments and in those before (loads under way over the barrier)
+    int all = 0, before = 0, none_before = 0;
+    if (segments > 1) {
+        const int col = min(tid, c.E);
+#pragma unroll 16
+        for (int s = 0; s < segments; ++s) {
+            const int v = c.segments[(int64_t)s * EB + col];
+            all += v;
+            before += s < (int)blockIdx.x ? v : 0;
+        }
+        // those of no expert, by the last thread, which may have an expert as well
+        if (tid == NT - 1)
+#pragma unroll 16
+            for (int s = 0; s < (int)blockIdx.x; ++s)
+                none_before += c.segments[(int64_t)s * EB + c.E];
+    }
+    __syncthreads();
+    if constexpr (HELD > 0) {
+        // (a wave's own counters: its steps follow each other)
+#pragma unroll
+        for (int q = 0; q < HELD; ++q) {
+            const uint64_t peers = peers_of(key[q], key[q] >= 0, bits);
+            if (key[q] >= 0) {
+                const int n = base[w * EB + key[q]];
+                rank[q] = n + __popcll(peers & lanemask_lt(lane));
+                if (lane == __ffsll((unsigned long long)peers) - 1)
+                    base[w * EB + key[q]] = n + __popcll(peers);
+            }
+        }
+    } else {
+        for (uint32_t f = wb + lane; f < we; f += 64)
+            atomicAdd(&base[w * EB + choice(c, f)], 1);
+    }
+    __syncthreads();
+    // the waves' counts of each expert become what comes before them
+    int mine = 0;
+    if (tid < c.E)
+        for (int q = 0; q < NW; ++q) {
+            const int v = base[q * EB + tid];
+            base[q * EB + tid] = mine;
+            mine += v;
+        }
+    if (segments == 1)
+        all = mine;
+    if (tid >= c.E)
+        all = 0;
     uint64_t total;
-    const uint64_t first = block_scan((uint64_t)all | (uint64_t)((all + kTileRows - 1) / kTileRows) << 32, sh, &total);
+    const uint64_t first = block_scan<NW>((uint64_t)all | (uint64_t)((all + kTileRows - 1) / kTileRows) << 32, sh, &total);
     const int chosen = (int)(uint32_t)total;
     if (blockIdx.x == 0) {
         if (tid < c.E) {
@@ -114,45 +153,49 @@ __global__ __launch_bounds__(1024) void k_token_place(SortCall c, int64_t per, i
             c.tiles[tid] = (int)(first >> 32);
         }
         if (tid == 0) {
-            const int none = (int)(rows - chosen), tiles = (int)(total >> 32);
+            const int none = (int)rows - chosen, tiles = (int)(total >> 32);
             c.offsets[c.E] = chosen;
             c.tiles[c.E] = tiles;
             c.tiles[c.E + 1] = tiles + (none + kTileRows - 1) / kTileRows;
         }
     }
-    // the first row of each wave's choices of each expert
     if (tid < c.E) {
-        int at = (int)(uint32_t)first + before;
-        for (int q = 0; q < 16; ++q) {
-            const int v = base[q * EB + tid];
-            base[q * EB + tid] = at;
-            at += v;
-        }
+        const int at = (int)(uint32_t)first + before;
+#pragma unroll
+        for (int q = 0; q < NW; ++q)
+            base[q * EB + tid] += at;
     }
-    // (those of no expert by the last thread, which may have an expert as well)
-    if (tid == 1023) {
-        int at = chosen;
-        if (segments > 1)
-            for (int s = 0; s < (int)blockIdx.x; ++s)
-                at += c.segments[(int64_t)s * EB + c.E];
-        for (int q = 0; q < 16; ++q) {
+    if (tid == NT - 1) {
+        int at = chosen + none_before;
+        for (int q = 0; q < NW; ++q) {
             const int v = base[q * EB + c.E];
             base[q * EB + c.E] = at;
             at += v;
         }
     }
     __syncthreads();
-    for (int64_t f0 = wb; f0 < we; f0 += 64) {
-        const int64_t f = f0 + lane;
-        const bool valid = f < we;
-        const int key = valid ? choice(c, f) : 0;
-        const uint64_t peers = peers_of(key, valid, bits);
-        if (valid) {
-            const int b = base[w * EB + key], p = b + __popcll(peers & lanemask_lt(lane));
-            c.order[p] = (int)f;
-            c.place[f] = p;
-            if (lane == __ffsll((unsigned long long)peers) - 1)
-                base[w * EB + key] = b + __popcll(peers);
+    if constexpr (HELD > 0) {
+#pragma unroll
+        for (int q = 0; q < HELD; ++q)
+            if (key[q] >= 0) {
+                const uint32_t f = wb + q * 64 + lane;
+                const int p = base[w * EB + key[q]] + rank[q];
+                c.order[p] = (int)f;
+                c.place[f] = p;
+            }
+    } else {
+        for (uint32_t f0 = wb; f0 < we; f0 += 64) {
+            const uint32_t f = f0 + lane;
+            const bool valid = f < we;
+            const int e = valid ? choice(c, f) : 0;
+            const uint64_t peers = peers_of(e, valid, bits);
+            if (valid) {
+                const int b = base[w * EB + e], p = b + __popcll(peers & lanemask_lt(lane));
+                c.order[p] = (int)f;
+                c.place[f] = p;
+                if (lane == __ffsll((unsigned long long)peers) - 1)
+                    base[w * EB + e] = b + __popcll(peers);
+            }
         }
     }
 }
@@ -184,97 +227,103 @@ __device__ __forceinline__ void mx8(const uint8_t *row, const uint8_t *scale, in
     }
 }
 
-// grid: 2^shift threads per token, 256 in a block
-template <class E, bool MX, bool FULL>
-__global__ __launch_bounds__(256) void k_dispatch(MoveCall c, int shift)
+// A block has 256 threads, 2^SHIFT of them per token (8: one token), a thread eight columns;
+// grid: tokens, groups of columns.
+template <int SHIFT>
+__device__ __forceinline__ int64_t token_at()
 {
-    const int64_t t = ((int64_t)blockIdx.x << (8 - shift)) + (threadIdx.x >> shift);
-    if (t >= c.T)
+    return SHIFT == 8 ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x << (8 - SHIFT)) + (threadIdx.x >> SHIFT);
+}
+template <int SHIFT>
+__device__ __forceinline__ int64_t column_at()
+{
+    return (((int64_t)blockIdx.y << SHIFT) + (threadIdx.x & ((1 << SHIFT) - 1))) * 8;
+}
+
+template <class E, bool MX, bool FULL, int SHIFT>
+__global__ __launch_bounds__(256) void k_dispatch(MoveCall c)
+{
+    const int64_t t = token_at<SHIFT>(), col = column_at<SHIFT>();
+    if (t >= c.T || col >= c.d)
         return;
-    const int G = 1 << shift;
     const int n_rows = *c.n_rows;
-    const int64_t all = (int64_t)c.T * c.k;
-    for (int64_t col = (threadIdx.x & (G - 1)) * 8; col < c.d; col += G * 8) {
-        float v[8];
-        if constexpr (MX)
-            mx8<FULL>((const uint8_t *)c.x + t * c.ldx, (const uint8_t *)c.x_scale + t * c.ldxs, col, c.d, v);
-        else
-            widen8<E>(row8<E, FULL>((const typename E::raw *)c.x + t * c.ldx, col, c.d), v);
-        const int n = (int)min((int64_t)8, c.d - col);
-        for (int j0 = 0; j0 < c.k; j0 += 8) {
-            int p[8];
+    const uint32_t all = (uint32_t)c.T * c.k;
+    const int n = (int)min((int64_t)8, c.d - col);
+    float v[8];
+    if constexpr (MX)
+        mx8<FULL>((const uint8_t *)c.x + t * c.ldx, (const uint8_t *)c.x_scale + t * c.ldxs, col, c.d, v);
+    else
+        widen8<E>(row8<E, FULL>((const typename E::raw *)c.x + t * c.ldx, col, c.d), v);
+    for (int j0 = 0; j0 < c.k; j0 += 8) {
+        int p[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                p[u] = c.place[t * c.k + min(j0 + u, c.k - 1)];
+        for (int u = 0; u < 8; ++u)
+            p[u] = c.place[t * c.k + min(j0 + u, c.k - 1)];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (j0 + u < c.k && (uint32_t)p[u] < (uint64_t)all) {
-                    const bool none = p[u] >= n_rows;
-                    float y[8];
+        for (int u = 0; u < 8; ++u)
+            if (j0 + u < c.k && (uint32_t)p[u] < all) {
+                const bool none = p[u] >= n_rows;
+                float y[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        y[i] = none ? 0.f : v[i];
-                    store8<E>((typename E::raw *)c.rows + p[u] * c.ldrows, col, n, y);
-                }
-        }
+                for (int i = 0; i < 8; ++i)
+                    y[i] = none ? 0.f : v[i];
+                store8<E>((typename E::raw *)c.rows + p[u] * c.ldrows, col, n, y);
+            }
     }
 }
 
 // ---- combine ---------------------------------------------------------------------------
 
-template <class E, class O, bool FULL>
-__global__ __launch_bounds__(256) void k_combine_tokens(MoveCall c, int shift)
+// KN: rows whose loads are under way together, k itself up to 8.
+template <class E, class O, bool FULL, int SHIFT, int KN>
+__global__ __launch_bounds__(256) void k_combine_tokens(MoveCall c)
 {
-    const int64_t t = ((int64_t)blockIdx.x << (8 - shift)) + (threadIdx.x >> shift);
-    if (t >= c.T)
+    const int64_t t = token_at<SHIFT>(), col = column_at<SHIFT>();
+    if (t >= c.T || col >= c.d)
         return;
-    const int G = 1 << shift;
     const int n_rows = *c.n_rows;
-    for (int64_t col = (threadIdx.x & (G - 1)) * 8; col < c.d; col += G * 8) {
-        const int n = (int)min((int64_t)8, c.d - col);
-        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (c.residual)
-            widen8<O>(row8<O, FULL>((const typename O::raw *)c.residual + t * c.ldres, col, c.d), r);
-        for (int j0 = 0; j0 < c.k; j0 += 8) {
-            Raw8<E> y[8];
-            bool use[8];
-            float w[8];
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (c.residual)
+        widen8<O>(row8<O, FULL>((const typename O::raw *)c.residual + t * c.ldres, col, c.d), r);
+    for (int j0 = 0; j0 < c.k; j0 += KN) {
+        Raw8<E> y[KN];
+        bool use[KN];
+        float w[KN];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int64_t f = t * c.k + min(j0 + u, c.k - 1);
-                const int p = c.place[f];
-                use[u] = j0 + u < c.k && (uint32_t)p < (uint32_t)n_rows;
-                w[u] = c.weight ? c.weight[f] : 1.f;
-                // a choice of no expert: the first row, left out below (there is one: n_rows may be 0, T k is not)
-                y[u] = row8<E, FULL>((const typename E::raw *)c.rows + (use[u] ? p : 0) * c.ldrows, col, c.d);
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                float v[8];
-                widen8<E>(y[u], v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    s[i] = use[u] ? fmaf(w[u], v[i], s[i]) : s[i];
-            }
+        for (int u = 0; u < KN; ++u) {
+            const int64_t f = t * c.k + min(j0 + u, c.k - 1);
+            const int p = c.place[f];
+            use[u] = j0 + u < c.k && (uint32_t)p < (uint32_t)n_rows;
+            w[u] = c.weight ? c.weight[f] : 1.f;
+            // a choice of no expert: the first row, left out below (there is one: n_rows may be 0, T k is not)
+            y[u] = row8<E, FULL, true>((const typename E::raw *)c.rows + (use[u] ? p : 0) * c.ldrows, col, c.d);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            s[i] = r[i] + s[i];
-        store8<O>((typename O::raw *)c.out + t * c.ldout, col, n, s);
+        for (int u = 0; u < KN; ++u) {
+            float v[8];
+            widen8<E>(y[u], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s[i] = use[u] ? fmaf(w[u], v[i], s[i]) : s[i];
+        }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        s[i] = r[i] + s[i];
+    store8<O>((typename O::raw *)c.out + t * c.ldout, col, (int)min((int64_t)8, c.d - col), s);
 }
 
 // grid: one wave per choice
 template <class E, class O, bool FULL>
 __global__ __launch_bounds__(256) void k_combine_back(MoveCall c)
 {
-    const int64_t f = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), all = (int64_t)c.T * c.k;
+    const uint32_t f = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), all = (uint32_t)c.T * c.k;
     if (f >= all)
         return;
     const int lane = threadIdx.x & 63;
-    const int64_t t = f / c.k;
+    const int64_t t = f / (uint32_t)c.k;
     const int p = c.place[f];
-    const bool none = p >= *c.n_rows, there = (uint32_t)p < (uint64_t)all;
+    const bool none = p >= *c.n_rows, there = (uint32_t)p < all;
     const float w = c.weight ? c.weight[f] : 1.f;
     const typename O::raw *dout = (const typename O::raw *)c.dout + t * c.lddout;
     const typename E::raw *y = (const typename E::raw *)c.rows + (there ? p : 0) * c.ldrows;
@@ -311,19 +360,30 @@ __global__ __launch_bounds__(256) void k_combine_back(MoveCall c)
     }
 }
 
-// Threads per token, as a power of two from 8 to 256: a chunk of eight elements each.
-int token_shift(int d)
+// f(shift) for the threads per token: 8, 32 or 256, enough for a narrow row's chunks of eight.
+template <class F>
+void with_shift(int d, F f)
 {
-    int s = 3;
-    while (s < 8 && (8 << s) < d)
-        ++s;
-    return s;
+    if (d <= 64)
+        f(std::integral_constant<int, 3>{});
+    else if (d <= 512)
+        f(std::integral_constant<int, 5>{});
+    else
+        f(std::integral_constant<int, 8>{});
+}
+template <class F>
+void with_bool(bool b, F f)
+{
+    if (b)
+        f(std::true_type{});
+    else
+        f(std::false_type{});
 }
 
-dim3 token_grid(int T, int shift)
+dim3 token_grid(const MoveCall &c, int shift)
 {
-    const int per = 256 >> shift;
-    return dim3((unsigned)((T + per - 1) / per));
+    const int per = 256 >> shift, cols = 8 << shift;
+    return dim3((unsigned)((c.T + per - 1) / per), (unsigned)((c.d + cols - 1) / cols));
 }
 
 template <class F>
@@ -360,16 +420,26 @@ int sort_segments(int64_t rows)
 int launch_token_sort(const SortCall &c, hipStream_t st)
 {
     ProfScope prof("token_sort", st);
-    const int64_t rows = (int64_t)c.T * c.k;
+    const uint32_t rows = (uint32_t)c.T * c.k;
     const int n = sort_segments(rows);
-    const int64_t per = n == 1 ? (rows < kSortRows ? kSortRows : rows) : ((rows + n - 1) / n + kSortRows - 1) / kSortRows * kSortRows;
+    // one segment or whole steps of a block
+    const uint32_t per = n == 1 ? rows : ((rows + n - 1) / n + kSortRows - 1) / kSortRows * kSortRows;
     const size_t sh = (size_t)(c.E + 1) * 4;
     int bits = 0;
     while ((1 << bits) <= c.E)
         ++bits;
     if (n > 1)
         hipLaunchKernelGGL(k_token_count, dim3(n), dim3(1024), sh, st, c, per);
-    hipLaunchKernelGGL(k_token_place, dim3(n), dim3(1024), 16 * sh, st, c, per, n, bits);
+    if (n > 1 && per > kSortRows)
+        hipLaunchKernelGGL((k_token_place<16, 0>), dim3(n), dim3(1024), 16 * sh, st, c, per, n, bits);
+    else if (n > 1)
+        hipLaunchKernelGGL((k_token_place<16, 1>), dim3(n), dim3(1024), 16 * sh, st, c, per, n, bits);
+    else if (rows <= 256 && c.E <= 256)
+        hipLaunchKernelGGL((k_token_place<4, 1>), dim3(1), dim3(256), 4 * sh, st, c, per, n, bits);
+    else if (rows <= 1024)
+        hipLaunchKernelGGL((k_token_place<16, 1>), dim3(1), dim3(1024), 16 * sh, st, c, per, n, bits);
+    else
+        hipLaunchKernelGGL((k_token_place<16, 4>), dim3(1), dim3(1024), 16 * sh, st, c, per, n, bits);
     ECF_HIP_CHECK(hipGetLastError());
     return ECF_OK;
 }
@@ -377,21 +447,18 @@ int launch_token_sort(const SortCall &c, hipStream_t st)
 int launch_dispatch(const MoveCall &c, hipStream_t st)
 {
     ProfScope prof("token_dispatch", st);
-    const int shift = token_shift(c.d);
-    const bool full = c.d % 8 == 0;
     with_element(c.dtype, [&](auto e) {
-        using E = decltype(e);
-        if (c.token_dtype == ECF_MXFP8) {
-            if (full)
-                hipLaunchKernelGGL((k_dispatch<E, true, true>), token_grid(c.T, shift), dim3(256), 0, st, c, shift);
-            else
-                hipLaunchKernelGGL((k_dispatch<E, true, false>), token_grid(c.T, shift), dim3(256), 0, st, c, shift);
-        } else {
-            if (full)
-                hipLaunchKernelGGL((k_dispatch<E, false, true>), token_grid(c.T, shift), dim3(256), 0, st, c, shift);
-            else
-                hipLaunchKernelGGL((k_dispatch<E, false, false>), token_grid(c.T, shift), dim3(256), 0, st, c, shift);
-        }
+        with_bool(c.d % 8 == 0, [&](auto full) {
+            with_shift(c.d, [&](auto shift) {
+                using E = decltype(e);
+                constexpr bool FULL = decltype(full)::value;
+                constexpr int S = decltype(shift)::value;
+                if (c.token_dtype == ECF_MXFP8)
+                    hipLaunchKernelGGL((k_dispatch<E, true, FULL, S>), token_grid(c, S), dim3(256), 0, st, c);
+                else
+                    hipLaunchKernelGGL((k_dispatch<E, false, FULL, S>), token_grid(c, S), dim3(256), 0, st, c);
+            });
+        });
     });
     ECF_HIP_CHECK(hipGetLastError());
     return ECF_OK;
@@ -400,14 +467,27 @@ int launch_dispatch(const MoveCall &c, hipStream_t st)
 int launch_combine_tokens(const MoveCall &c, hipStream_t st)
 {
     ProfScope prof("token_combine", st);
-    const int shift = token_shift(c.d);
     with_pair(c, [&](auto e, auto o) {
-        using E = decltype(e);
-        using O = decltype(o);
-        if (c.d % 8 == 0)
-            hipLaunchKernelGGL((k_combine_tokens<E, O, true>), token_grid(c.T, shift), dim3(256), 0, st, c, shift);
-        else
-            hipLaunchKernelGGL((k_combine_tokens<E, O, false>), token_grid(c.T, shift), dim3(256), 0, st, c, shift);
+        with_bool(c.d % 8 == 0, [&](auto full) {
+            with_shift(c.d, [&](auto shift) {
+                using E = decltype(e);
+                using O = decltype(o);
+                constexpr bool FULL = decltype(full)::value;
+                constexpr int S = decltype(shift)::value;
+#define ECF_COMBINE(KN) hipLaunchKernelGGL((k_combine_tokens<E, O, FULL, S, KN>), token_grid(c, S), dim3(256), 0, st, c)
+                switch (c.k) {
+                case 1: ECF_COMBINE(1); break;
+                case 2: ECF_COMBINE(2); break;
+                case 3: ECF_COMBINE(3); break;
+                case 4: ECF_COMBINE(4); break;
+                case 5: ECF_COMBINE(5); break;
+                case 6: ECF_COMBINE(6); break;
+                case 7: ECF_COMBINE(7); break;
+                default: ECF_COMBINE(8);
+                }
+#undef ECF_COMBINE
+            });
+        });
     });
     ECF_HIP_CHECK(hipGetLastError());
     return ECF_OK;
@@ -418,12 +498,9 @@ int launch_combine_backward(const MoveCall &c, hipStream_t st)
     ProfScope prof("token_combine_backward", st);
     const dim3 grid((unsigned)(((int64_t)c.T * c.k + 3) / 4));
     with_pair(c, [&](auto e, auto o) {
-        using E = decltype(e);
-        using O = decltype(o);
-        if (c.d % 8 == 0)
-            hipLaunchKernelGGL((k_combine_back<E, O, true>), grid, dim3(256), 0, st, c);
-        else
-            hipLaunchKernelGGL((k_combine_back<E, O, false>), grid, dim3(256), 0, st, c);
+        with_bool(c.d % 8 == 0, [&](auto full) {
+            hipLaunchKernelGGL((k_combine_back<decltype(e), decltype(o), decltype(full)::value>), grid, dim3(256), 0, st, c);
+        });
     });
     ECF_HIP_CHECK(hipGetLastError());
     return ECF_OK;

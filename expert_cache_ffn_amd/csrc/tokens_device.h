@@ -14,11 +14,20 @@ struct Raw8 {
     u32x4_t v[sizeof(typename E::raw) / 2];
 };
 
-template <class E>
+typedef u32x4_t __attribute__((aligned(2))) u32x4_any2;
+typedef u32x4_t __attribute__((aligned(4))) u32x4_any4;
+
+// NT: past the caches, for what is read once
+template <class E, bool NT = false>
 __device__ __forceinline__ Raw8<E> load_raw8(const typename E::raw *p)
 {
+    typedef typename std::conditional<sizeof(typename E::raw) == 2, u32x4_any2, u32x4_any4>::type any_t;
     Raw8<E> r;
-    if constexpr (sizeof(typename E::raw) == 2) {
+    if constexpr (NT) {
+        r.v[0] = __builtin_nontemporal_load((const any_t *)p);
+        if constexpr (sizeof(typename E::raw) == 4)
+            r.v[1] = __builtin_nontemporal_load((const any_t *)(p + 4));
+    } else if constexpr (sizeof(typename E::raw) == 2) {
         r.v[0] = ((const any128x2 *)p)->v;
     } else {
         r.v[0] = __builtin_bit_cast(u32x4_t, ((const any128x4 *)p)->v);
@@ -67,11 +76,11 @@ __device__ __forceinline__ Raw8<E> shift_raw8(Raw8<E> r, int s)
 // alignment of the row.  No lane's load sits behind a branch (d < 8 is the same for all): where the row ends inside
 // or before the eight, its last eight are read and moved down.  FULL: d is a multiple of 8,
 // and nothing has to be moved.
-template <class E, bool FULL>
+template <class E, bool FULL, bool NT = false>
 __device__ __forceinline__ Raw8<E> row8(const typename E::raw *row, int64_t col, int d)
 {
     if constexpr (FULL) {
-        Raw8<E> r = load_raw8<E>(row + min(col, (int64_t)d - 8));
+        Raw8<E> r = load_raw8<E, NT>(row + min(col, (int64_t)d - 8));
         if (col >= d)
 #pragma unroll
             for (unsigned i = 0; i < sizeof(r.v) / sizeof(r.v[0]); ++i)
@@ -80,7 +89,7 @@ __device__ __forceinline__ Raw8<E> row8(const typename E::raw *row, int64_t col,
     } else {
         if (d >= 8) {
             const int64_t at = min(col, (int64_t)d - 8);
-            return shift_raw8<E>(load_raw8<E>(row + at), (int)min(col - at, (int64_t)8));
+            return shift_raw8<E>(load_raw8<E, NT>(row + at), (int)min(col - at, (int64_t)8));
         }
         Raw8<E> r;
 #pragma unroll

@@ -74,6 +74,41 @@ __device__ __forceinline__ double wave_sum_f64(double x)
     return (r[0] + r[1]) + (r[2] + r[3]);
 }
 
+// Inclusive scan over the wave by DPP: row_shr 1, 2, 4, 8 inside each row of 16
+// lanes, then lane 15 of rows 0 and 2 into rows 1 and 3 (row_bcast:15), then
+// lane 31 into rows 2 and 3 (row_bcast:31).  Lanes a step does not write (no
+// source lane, or a row outside its row mask) take `old` = 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_or0(uint32_t x)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_incl_scan(uint32_t x)
+{
+    x += dpp_or0<0x111, 0xF>(x);
+    x += dpp_or0<0x112, 0xF>(x);
+    x += dpp_or0<0x114, 0xF>(x);
+    x += dpp_or0<0x118, 0xF>(x);
+    x += dpp_or0<0x142, 0xA>(x);
+    x += dpp_or0<0x143, 0xC>(x);
+    return x;
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp_or0_64(uint64_t x)
+{
+    return ((uint64_t)dpp_or0<CTRL, ROWS>((uint32_t)(x >> 32)) << 32) | dpp_or0<CTRL, ROWS>((uint32_t)x);
+}
+__device__ __forceinline__ uint64_t wave_incl_scan64(uint64_t x)
+{
+    x += dpp_or0_64<0x111, 0xF>(x);
+    x += dpp_or0_64<0x112, 0xF>(x);
+    x += dpp_or0_64<0x114, 0xF>(x);
+    x += dpp_or0_64<0x118, 0xF>(x);
+    x += dpp_or0_64<0x142, 0xA>(x);
+    x += dpp_or0_64<0x143, 0xC>(x);
+    return x;
+}
+
 // Selection key of (logit v, expert e): the fp32 bits mapped to an unsigned
 // order-preserving code (sign folded), then the complement of e, so a larger
 // key is a larger logit, or an equal logit with a lower expert id.  -0 counts as

@@ -4,6 +4,7 @@ forward pass runs in libecf's kernels (or its host expert threads)."""
 from __future__ import annotations
 
 import warnings
+from functools import cached_property
 from typing import NamedTuple
 
 import torch
@@ -376,6 +377,9 @@ class NormOut(NamedTuple):
     scale: torch.Tensor | None
 
 
+_EMPTY = {}  # torch.empty of each type a call makes, by device
+
+
 class _Tokens:
     """What the token operators share: workspaces and streams.  A call runs on the current
     stream of the operator's device and takes its workspace and outputs from torch's
@@ -384,8 +388,11 @@ class _Tokens:
 
     def _setup(self, device):
         self.device = device
-        self._empty = {dt: torch.empty(0, dtype=dt, device=device).new_empty
-                       for dt in (torch.float32, torch.bfloat16, torch.float16, torch.int32, torch.uint8)}
+        if device not in _EMPTY:
+            _EMPTY[device] = {dt: torch.empty(0, dtype=dt, device=device).new_empty
+                              for dt in (torch.float32, torch.bfloat16, torch.float16, torch.int32, torch.uint8,
+                                         torch.float8_e4m3fn, torch.float8_e8m0fnu)}
+        self._empty = _EMPTY[device]
 
     def _run(self, fn, a, T, ws_bytes=0):
         if _current_device() != self.device.index:
@@ -469,9 +476,8 @@ class RMSNorm(_Tokens):
         elif out is not None or not mx:
             raise ValueError("y=False needs mx=True and no out")
         if mx:
-            q, a.d_q, _ = self._out("q", None, T, self.hidden, torch.uint8)
-            scale, a.d_q_scale, _ = self._out("scale", None, T, (self.hidden + 31) // 32, torch.uint8)
-            q, scale = q.view(torch.float8_e4m3fn), scale.view(torch.float8_e8m0fnu)
+            q, a.d_q, _ = self._out("q", None, T, self.hidden, torch.float8_e4m3fn)
+            scale, a.d_q_scale, _ = self._out("scale", None, T, (self.hidden + 31) // 32, torch.float8_e8m0fnu)
         if save:
             rstd = self._empty[torch.float32](T)
             a.d_rstd = rstd.data_ptr()
@@ -549,20 +555,40 @@ class TokenSort(_Tokens):
         a.d_idx, a.ld_idx = _matrix("ids", wide, self.tokens, self.top_k, ids.dtype, self.device)
         n_ws = _ws_cached(_SORT_WS, (self.n_experts, self.top_k, self.tokens), L.ecf_token_sort_workspace_bytes)
         E, R = self.n_experts, self.tokens * self.top_k
-        # one allocation, its parts at 16-byte boundaries
-        at = [0]
-        for n in (E, E + 1, E + 2, R, R):
-            at.append(at[-1] + (n + 3) // 4 * 4)
-        buf = self._empty[torch.int32](at[-1])
-        self.counts, self.offsets = buf[:E], buf[at[1]:at[1] + E + 1]
-        self.tiles, self.order = buf[at[2]:at[2] + E + 2], buf[at[3]:at[3] + R]
-        self.place = buf[at[4]:at[4] + R].view(self.tokens, self.top_k)
-        p = buf.data_ptr()
-        a.d_counts, a.d_offsets, a.d_tiles, a.d_order, a.d_place = (p + 4 * i for i in at[:5])
+        # one allocation: offsets, counts, tiles, order, place, each at a 16-byte boundary
+        e4, r4 = (E + 5) // 4 * 4, (R + 3) // 4 * 4
+        self._buf = self._empty[torch.int32](3 * e4 + 2 * r4)
+        p = self._buf.data_ptr()
+        a.d_offsets, a.d_counts, a.d_tiles, a.d_order, a.d_place = p, p + 4 * e4, p + 8 * e4, p + 12 * e4, p + 12 * e4 + 4 * r4
         self._run(L.ecf_token_sort, a, self.tokens, n_ws)
-        t = L.TokenArgs()
-        t.n_experts, t.top_k, t.d_offsets, t.d_place = self.n_experts, self.top_k, a.d_offsets, a.d_place
-        self._a = t
+        t = self._a = L.TokenArgs()
+        t.n_experts, t.top_k, t.d_offsets, t.d_place = E, self.top_k, p, a.d_place
+        self._s = a
+
+    def _part(self, address, n):
+        at = (address - self._s.d_offsets) // 4
+        return self._buf[at:at + n]
+
+    # (views of one buffer, made when asked for: each costs the host as much as a launch)
+    @cached_property
+    def counts(self):
+        return self._part(self._s.d_counts, self.n_experts)
+
+    @cached_property
+    def offsets(self):
+        return self._part(self._s.d_offsets, self.n_experts + 1)
+
+    @cached_property
+    def tiles(self):
+        return self._part(self._s.d_tiles, self.n_experts + 2)
+
+    @cached_property
+    def order(self):
+        return self._part(self._s.d_order, self.tokens * self.top_k)
+
+    @cached_property
+    def place(self):
+        return self._part(self._s.d_place, self.tokens * self.top_k).view(self.tokens, self.top_k)
 
     def _weights(self, w):
         if not isinstance(w, torch.Tensor) or w.numel() != self.tokens * self.top_k or w.dtype is not torch.float32 \
@@ -614,7 +640,7 @@ class TokenSort(_Tokens):
             a.d_weight = self._weights(weights)
         if residual is not None:
             a.d_residual, a.ld_residual = _matrix("residual", residual, self.tokens, d, od, self.device)
-        if any(t is not None and t.requires_grad for t in (rows, weights, residual)):
+        if rows.requires_grad or weights is not None and weights.requires_grad or residual is not None and residual.requires_grad:
             _warn_untracked("TokenSort.combine", call="combine_backward")
         out, a.d_out, a.ld_out = self._out("out", out, self.tokens, d, od)
         self._run(L.ecf_token_combine, a, self.tokens)
@@ -685,7 +711,7 @@ class LowRankAdapters(_Tokens):
         if isinstance(ids, TokenSort):
             if (ids.tokens, ids.top_k, ids.n_experts) != (T, 1, self.n) or ids.device != self.device:
                 raise ValueError(f"the TokenSort must be of {T} tokens, one choice of {self.n} each, on {self.device}")
-            a.d_order, a.d_offsets, a.d_tiles = ids.order.data_ptr(), ids.offsets.data_ptr(), ids.tiles.data_ptr()
+            a.d_order, a.d_offsets, a.d_tiles = ids._s.d_order, ids._s.d_offsets, ids._s.d_tiles
             ids = ids.ids if ids.ids.dim() == 1 else ids.ids[:, 0]
         wide = isinstance(ids, torch.Tensor) and ids.dtype is torch.int64
         a.idx_bytes, a.d_idx = 8 if wide else 4, _vector("ids", ids, T, torch.int64 if wide else torch.int32, self.device)
