@@ -25,7 +25,7 @@ int check_shape(const char *what, int32_t K, int32_t N, int32_t r, int32_t n, in
 // g and the outer products' slots.
 struct Workspace {
     size_t counts, offsets, tiles, order, place, sort, sort_bytes, part, g, slots_a, slots_b, total;
-    int splits, chunks_a, chunks_b;
+    int splits;
 };
 Workspace workspace(int32_t K, int32_t N, int32_t r, int32_t n, int32_t T, bool backward)
 {
@@ -50,10 +50,8 @@ Workspace workspace(int32_t K, int32_t N, int32_t r, int32_t n, int32_t T, bool 
     w.part = take((size_t)shrink_rows(T) * r * 4);
     if (backward) {
         w.g = take((size_t)T * r * 4);
-        w.chunks_a = outer_chunks(T, K);
-        w.chunks_b = outer_chunks(T, N);
-        w.slots_a = take(outer_slots(w.chunks_a, K, r));
-        w.slots_b = take(outer_slots(w.chunks_b, N, r));
+        w.slots_a = take(outer_slots(outer_chunks(T, outer_slices(K)), K, r));
+        w.slots_b = take(outer_slots(outer_chunks(T, outer_slices(N)), N, r));
     }
     return w;
 }
@@ -228,27 +226,28 @@ int ecf_adapter_backward(const ecf_adapter_args *a, int32_t T)
             e.out = want_dx ? a->d_dx : nullptr, e.ldout = lddx;
             ECF_TRY(launch_expand(e, st));
         }
-        OuterCall q{};
-        q.o = o;
-        q.grad_dtype = a->wgrad_dtype;
-        q.r = a->rank;
-        if (a->d_da) {
-            q.x_dtype = a->dtype, q.W = a->in_features;
-            q.g = g;
-            q.x = a->d_x, q.ldx = ldx;
-            q.d = a->d_da;
-            q.slots = (float *)(ws + w.slots_a), q.chunks = w.chunks_a;
-            ECF_TRY(launch_outer(q, st));
+        // both in one launch where x and dout are of one type (more slices, so no more runs
+        // than either has room for)
+        OuterCall q[2]{};
+        int n = 0;
+        for (int of_b = 0; of_b < 2; ++of_b) {
+            void *d = of_b ? a->d_db : a->d_da;
+            if (!d)
+                continue;
+            OuterCall &c = q[n++];
+            c.o = o;
+            c.x_dtype = of_b ? a->out_dtype : a->dtype, c.grad_dtype = a->wgrad_dtype;
+            c.W = of_b ? a->out_features : a->in_features, c.r = a->rank;
+            c.of_b = of_b;
+            c.g = of_b ? a->d_h : g, c.gscale = of_b ? a->d_scale : nullptr;
+            c.x = of_b ? a->d_dout : a->d_x, c.ldx = of_b ? lddy : ldx;
+            c.d = d;
+            c.slots = (float *)(ws + (of_b ? w.slots_b : w.slots_a));
         }
-        if (a->d_db) {
-            q.x_dtype = a->out_dtype, q.W = a->out_features;
-            q.of_b = true;
-            q.g = a->d_h, q.gscale = a->d_scale;
-            q.x = a->d_dout, q.ldx = lddy;
-            q.d = a->d_db;
-            q.slots = (float *)(ws + w.slots_b), q.chunks = w.chunks_b;
-            ECF_TRY(launch_outer(q, st));
-        }
+        if (n == 2 && q[0].x_dtype == q[1].x_dtype)
+            return launch_outer(q, 2, outer_chunks(T, outer_slices(q[0].W) + outer_slices(q[1].W)), st);
+        for (int i = 0; i < n; ++i)
+            ECF_TRY(launch_outer(q + i, 1, outer_chunks(T, outer_slices(q[i].W)), st));
         return ECF_OK;
     });
 }

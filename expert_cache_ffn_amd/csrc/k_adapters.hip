@@ -25,25 +25,32 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kKC = 128;   // k per staged chunk of a shrink
 constexpr int kRC = 64;    // most ranks at a time
-constexpr int kCols = 256; // columns per block of an expand
+constexpr int kCols = 512; // columns per block of an expand
 constexpr int kOuterCols = 128;
 
 struct Tile {
     int a, row0, rows;  // adapter (n: none), first row and rows of the order; rows 0: no tile
 };
 
-// The tile's adapter: the last whose first tile is not behind it.
+// The tile's adapter is the last whose first tile is not behind it; what is asked of it is loaded
+// along with the search, for 64 adapters at a time.
 __device__ __forceinline__ Tile tile_of(const AdapterOrder &o, int b)
 {
-    const int lane = threadIdx.x & 63;
-    if (b >= o.tiles[o.n + 1])
-        return {0, 0, 0};
-    int a = -1;
-    for (int e0 = 0; e0 <= o.n; e0 += 64)
-        a += __popcll(__ballot(e0 + lane <= o.n && o.tiles[min(e0 + lane, o.n)] <= b));
-    const int row0 = o.offsets[a] + (b - o.tiles[a]) * kTileRows;
-    const int end = a < o.n ? o.offsets[a + 1] : o.T;
-    return {a, row0, min(kTileRows, end - row0)};
+    const int lane = threadIdx.x & 63, last = o.tiles[o.n + 1];
+    Tile t{-1, 0, 0};
+    for (int e0 = 0; e0 <= o.n; e0 += 64) {
+        const int e = min(e0 + lane, o.n);
+        const int tile = o.tiles[e], from = o.offsets[e], to = o.offsets[min(e + 1, o.n)];
+        const uint64_t before = __ballot(e0 + lane <= o.n && tile <= b);
+        if (before == 0)
+            break;
+        const int i = __popcll(before) - 1;  // (the first tiles never fall)
+        t.a = e0 + i;
+        t.row0 = __builtin_amdgcn_readlane(from, i) + (b - __builtin_amdgcn_readlane(tile, i)) * kTileRows;
+        t.rows = (t.a < o.n ? __builtin_amdgcn_readlane(to, i) : o.T) - t.row0;
+    }
+    t.rows = b < last ? min(kTileRows, t.rows) : 0;
+    return t;
 }
 
 // The adapter of row `row` of the order (one with an adapter): the last that begins at or
@@ -108,13 +115,82 @@ __device__ __forceinline__ f32x4a product32(const Raw8<E> &m, const Raw8<X> &x, 
 
 // ---- shrink ----------------------------------------------------------------------------
 // grid: tiles, splits of K, chunks of 64 ranks.  A wave has 16 tokens, all ranks of the chunk.
-// A chunk of M goes through LDS as [rank][k], zeros past its ends.
-template <class E, class X, bool OF_B, int NJ, bool FULL>
+// A chunk of M goes through LDS as [rank][k], zeros past its ends; the loads of the next one
+// and of its x are under way over the products of this one.
+template <class E, class X, bool OF_B, int NJ, bool FULL, bool RFULL>
+struct Shrink {
+    typedef typename E::raw raw;
+    // per thread: with M as it lies NJ chunks of 8 k of one rank; with its transpose NJ / 2 (1 for 16 ranks, half of
+    // the threads) pairs of 8 ranks at two k
+    static constexpr int RP = NJ * 16, PITCH = kKC + 16 / sizeof(raw), NP = (NJ + 1) / 2;
+    Raw8<X> x[4];
+    Raw8<E> m[OF_B ? 2 * NP : NJ];
+
+    __device__ __forceinline__ void load(const ShrinkCall &c, const raw *mat, const typename X::raw *xrow, int j0, int kc, int kg, bool on)
+    {
+        if (on)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                x[s] = row8<X, FULL>(xrow, kc + s * 32 + kg * 8, c.K);
+        const int tid = threadIdx.x;
+        if constexpr (!OF_B) {
+#pragma unroll
+            for (int q = 0; q < NJ; ++q) {
+                const int i = tid + q * 256, j = i / (kKC / 8), k = i % (kKC / 8) * 8;
+                m[q] = row8<E, FULL>(mat + (int64_t)min(j0 + j, c.r - 1) * c.K, kc + k, c.K);
+                if (j0 + j >= c.r)
+                    m[q] = Raw8<E>{};
+            }
+        } else {
+            const int nj = min(RP, c.r - j0);
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                const int i = tid + q * 256, k = i / (RP / 8) * 2, j = i % (RP / 8) * 8;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    m[2 * q + h] = row8<E, RFULL>(mat + (int64_t)min(kc + k + h, c.K - 1) * c.r + j0, j, nj);
+                    if (kc + k + h >= c.K)
+                        m[2 * q + h] = Raw8<E>{};
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void stage(raw *lds) const
+    {
+        const int tid = threadIdx.x;
+        if constexpr (!OF_B) {
+#pragma unroll
+            for (int q = 0; q < NJ; ++q) {
+                const int i = tid + q * 256;
+                *(Raw8<E> *)(lds + i / (kKC / 8) * PITCH + i % (kKC / 8) * 8) = m[q];
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                const int i = tid + q * 256, k = i / (RP / 8) * 2, j = i % (RP / 8) * 8;
+                if (k < kKC)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        raw *at = lds + (j + e) * PITCH + k;
+                        if constexpr (sizeof(raw) == 2) {
+                            *(uint32_t *)at = __builtin_amdgcn_perm(m[2 * q + 1].v[0][e >> 1], m[2 * q].v[0][e >> 1],
+                                                                    e & 1 ? 0x07060302 : 0x05040100);
+                        } else {
+                            at[0] = __uint_as_float(m[2 * q].v[e >> 2][e & 3]);
+                            at[1] = __uint_as_float(m[2 * q + 1].v[e >> 2][e & 3]);
+                        }
+                    }
+            }
+        }
+    }
+};
+
+template <class E, class X, bool OF_B, int NJ, bool FULL, bool RFULL>
 __global__ __launch_bounds__(256) void k_shrink(ShrinkCall c)
 {
     typedef typename E::raw raw;
-    constexpr int RP = NJ * 16, PITCH = kKC + 16 / sizeof(raw);
-    __shared__ __align__(16) raw lds[RP * PITCH];
+    typedef Shrink<E, X, OF_B, NJ, FULL, RFULL> S;
+    __shared__ __align__(16) raw lds[S::RP * S::PITCH];
     const Tile tl = tile_of(c.o, blockIdx.x);
     if (tl.rows <= 0 || tl.a >= c.o.n)
         return;
@@ -128,50 +204,27 @@ __global__ __launch_bounds__(256) void k_shrink(ShrinkCall c)
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
         acc[j] = f32x4a{0.f, 0.f, 0.f, 0.f};
+    S now, next;
+    if (k0 < k1)
+        now.load(c, m, x, j0, k0, kg, on);
     for (int kc = k0; kc < k1; kc += kKC) {
-        Raw8<X> xr[4];
-        if (on)
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-                xr[s] = row8<X, FULL>(x, kc + s * 32 + kg * 8, c.K);
         __syncthreads();  // the chunk before is read
-        if constexpr (!OF_B) {
-            for (int i = tid; i < RP * (kKC / 8); i += 256) {
-                const int j = i / (kKC / 8), k = i % (kKC / 8) * 8;
-                Raw8<E> v = row8<E, FULL>(m + (int64_t)min(j0 + j, c.r - 1) * c.K, kc + k, c.K);
-                if (j0 + j >= c.r)
-                    v = Raw8<E>{};
-                *(Raw8<E> *)(lds + j * PITCH + k) = v;
-            }
-        } else {
-            // rows of r ranks, one for each k
-            const int nj = min(RP, c.r - j0);
-            for (int i = tid; i < kKC * (RP / 8); i += 256) {
-                const int k = i / (RP / 8), j = i % (RP / 8) * 8;
-                Raw8<E> v{};
-                if (kc + k < c.K && j < nj)
-                    v = row8<E, false>(m + (int64_t)(kc + k) * c.r + j0, j, nj);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if constexpr (sizeof(raw) == 2)
-                        lds[(j + e) * PITCH + k] = (uint16_t)(v.v[0][e >> 1] >> (16 * (e & 1)));
-                    else
-                        lds[(j + e) * PITCH + k] = __uint_as_float(v.v[e >> 2][e & 3]);
-                }
-            }
-        }
+        now.stage(lds);
+        if (kc + kKC < k1)
+            next.load(c, m, x, j0, kc + kKC, kg, on);
         __syncthreads();
         if (on)
 #pragma unroll
             for (int s = 0; s < 4; ++s)
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
-                    const Raw8<E> mr = *(const Raw8<E> *)(lds + (j * 16 + r15) * PITCH + s * 32 + kg * 8);
-                    acc[j] = product32<E, X>(mr, xr[s], acc[j]);
+                    const Raw8<E> mr = *(const Raw8<E> *)(lds + (j * 16 + r15) * S::PITCH + s * 32 + kg * 8);
+                    acc[j] = product32<E, X>(mr, now.x[s], acc[j]);
                 }
+        now = next;
     }
     if (w * 16 + r15 < tl.rows) {
-        float *out = c.part + ((int64_t)blockIdx.y * c.o.T + token) * c.r + j0;
+        float *out = c.part + ((int64_t)blockIdx.y * c.o.T + tl.row0 + w * 16 + r15) * c.r + j0;
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -182,149 +235,216 @@ __global__ __launch_bounds__(256) void k_shrink(ShrinkCall c)
 }
 
 // ---- expand ----------------------------------------------------------------------------
-// grid: tiles, slices of 256 columns.  A wave has 64 columns and the tile's 64 tokens.  Row m of
-// MFMA i is column 16 (m / 4) + 4 i + m % 4, so that a lane's four MFMAs leave it 16 columns
-// in a row of one token.
-template <class E, class O, bool OF_A, bool FULL>
-__global__ __launch_bounds__(256) void k_expand(ExpandCall c)
+// grid: tiles, slices of 512 columns.  h of the tile's 64 tokens lies in LDS; a wave has 128
+// columns: row m of MFMA e is column 32 (m % 4) + 8 (m / 4) + e, so that the eight MFMAs leave
+// a lane four times eight columns in a row, next to those of the lanes of the same token
+// (a lane with 32 in a row stores a quarter of each 64 bytes at a time: 4096 tokens of 4096
+// columns in bf16 30 against 26 us).  M comes straight from memory into operands (the tiles of an
+// adapter share it in the caches) and is held over the tile's tokens up to rank 64.
+// SPREAD, for few tiles: slices of 128 columns, the waves share the tokens, 16 each.
+//
+// A step is 32 places of the reduction.  bf16: the ranks, rounded up to 16 or a multiple of 32
+// (rp), follow each other once for each part of h, M is repeated.  Others: 32 ranks in fp32
+// products, or 16 where there are no more (HALF: a lane has 4 places instead of 8).
+struct ExpandShape {
+    int rp, steps, pitch;  // ranks with padding, steps over them (bf16: over all parts), elements per row of h
+};
+template <bool BF, int PARTS>
+__host__ __device__ __forceinline__ ExpandShape expand_shape(int r)
 {
-    typedef typename E::raw raw;
+    const int rp = r <= 16 ? 16 : (r + 31) / 32 * 32;
+    const int steps = BF ? (PARTS * rp + 31) / 32 : (rp + 31) / 32;
+    return {rp, steps, BF ? steps * 32 + 8 : rp + 4};
+}
+
+// M's operands of one step: of eight MFMAs, 8 places of the reduction each
+template <class E>
+struct Operands {
+    Raw8<E> v[8];
+};
+// Places j .. j + 7 of columns col + e (HALF: j .. j + 3, j a multiple of 4).  OF_A: M lies as [rank][column]; a lane
+// reads eight columns of eight ranks and turns them.
+template <class E, bool OF_A, bool FULL, bool RFULL, bool HALF>
+__device__ __forceinline__ Operands<E> operands(const ExpandCall &c, const typename E::raw *m, int col, int j)
+{
+    Operands<E> o;
+    if constexpr (!OF_A) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            o.v[e] = row8<E, RFULL>(m + (int64_t)min(col + e, c.N - 1) * c.r, HALF ? j & ~7 : j, c.r);
+            if constexpr (HALF)
+                if (j & 4) {
+                    if constexpr (sizeof(typename E::raw) == 2)
+                        o.v[e].v[0] = u32x4_t{o.v[e].v[0][2], o.v[e].v[0][3], 0, 0};
+                    else
+                        o.v[e].v[0] = o.v[e].v[1];
+                }
+        }
+    } else {
+        constexpr int U = HALF ? 4 : 8;
+        Raw8<E> t[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            t[u] = row8<E, FULL>(m + (int64_t)min(j + u, c.r - 1) * c.N, col, c.N);
+            if (j + u >= c.r)
+                t[u] = Raw8<E>{};
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (sizeof(typename E::raw) == 2) {
+#pragma unroll
+                for (int q = 0; q < U / 2; ++q)
+                    o.v[e].v[0][q] = __builtin_amdgcn_perm(t[2 * q + 1].v[0][e >> 1], t[2 * q].v[0][e >> 1],
+                                                           e & 1 ? 0x07060302 : 0x05040100);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    o.v[e].v[u >> 2][u & 3] = t[u].v[e >> 2][e & 3];
+            }
+        }
+    }
+    return o;
+}
+
+template <class E, class O, int SETS>
+constexpr int kExpandWaves = std::is_same<E, BF16>::value && std::is_same<O, BF16>::value && SETS == 1 ? 3 : 1;
+
+// SETS: steps' worth of M held over the tokens (ranks up to 32 or 64), 0: read again for each 16 tokens
+template <class E, class O, bool OF_A, bool FULL, bool RFULL, int SETS, bool HALF, bool SPREAD>
+__global__ __launch_bounds__(256, (kExpandWaves<E, O, SETS>)) void k_expand(ExpandCall c)
+{
     constexpr bool BF = std::is_same<E, BF16>::value;
     constexpr int PARTS = !BF ? 1 : std::is_same<O, F32>::value ? 3 : 2;
-    constexpr int PITCH = kRC + 16 / sizeof(raw);
-    constexpr int HP = BF ? (PARTS * kRC + 31) / 32 * 32 + 8 : kRC + 4;  // of h's rows, in bf16 or fp32
     typedef typename std::conditional<BF, uint16_t, float>::type hraw;
-    __shared__ __align__(16) raw ml[kCols * PITCH];
-    __shared__ __align__(16) hraw hl[kTileRows * HP];
+    extern __shared__ __align__(16) char smem[];
+    hraw *hl = (hraw *)smem;
     const Tile tl = tile_of(c.o, blockIdx.x);
     if (tl.rows <= 0)
         return;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, r15 = lane & 15, kg = lane >> 4;
-    const int n0 = blockIdx.y * kCols;
+    const ExpandShape sh = expand_shape<BF, PARTS>(c.r);
+    const int tid = threadIdx.x, lane = tid & 63, r15 = lane & 15, kg = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool none = tl.a >= c.o.n;  // the tokens without an adapter
     const int a = none ? 0 : tl.a;
     const float scale = none ? 0.f : scale_of(c.scale, a);
-    const raw *m = (const raw *)c.m + (int64_t)a * c.r * c.N;
-    const int col = n0 + w * 64 + kg * 16;
-    int token[4];
+    const typename E::raw *m = (const typename E::raw *)c.m + (int64_t)a * c.r * c.N;
+    const int c0 = SPREAD ? blockIdx.y * 128 : blockIdx.y * kCols + w * 128;
+    const bool on = c.out && c0 < c.N;
+    // the tokens of this wave's 16s, and their residuals, on their way while h is made
+    constexpr int NB = SPREAD ? 1 : 4;
+    const int col = c0 + kg * 8, mcol = c0 + 32 * (r15 & 3) + 8 * (r15 >> 2);
+    int64_t token[NB];
+    Raw8<O> res[NB][4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-        token[b] = c.o.order[tl.row0 + min(b * 16 + r15, tl.rows - 1)];
-    Raw8<O> res[4][2];
-    if (c.residual && c.out)
+    for (int b = 0; b < NB; ++b)
+        token[b] = c.o.order[tl.row0 + min((SPREAD ? w : b) * 16 + r15, tl.rows - 1)];
+    // a step's place of this lane's first rank
+    const auto rank_of = [&](int step) {
+        return HALF ? kg * 4 : BF && sh.rp == 16 ? kg * 8 & 8 : (step * 32) % sh.rp + kg * 8;
+    };
+    Operands<E> held[SETS ? SETS : 1];
+    if (on) {
+        if (c.residual)
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                res[b][q] = row8<O, FULL>((const typename O::raw *)c.residual + token[b] * c.ldres, col + 8 * q, c.N);
-    f32x4a acc[4][4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            acc[b][i] = f32x4a{0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < c.r; j0 += kRC) {
-        const int nj = min(kRC, c.r - j0), rp = (nj + 15) / 16 * 16;
-        __syncthreads();  // the ranks before are read
-        // h of the tile's tokens: the splits' sum, written out once
-        for (int i = tid; i < kTileRows * rp; i += 256) {
-            const int row = i / rp, j = i % rp;
-            float v = 0.f;
-            if (row < tl.rows && j < nj) {
-                const int t = c.o.order[tl.row0 + row];
-                if (!none)
-                    for (int s = 0; s < c.splits; ++s)
-                        v += c.part[((int64_t)s * c.o.T + t) * c.r + j0 + j];
-                if (c.h && blockIdx.y == 0)
-                    c.h[(int64_t)t * c.r + j0 + j] = c.scaled ? v * scale : v;
-                v *= scale;
-            }
-            if constexpr (BF) {
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p)
-                    hl[row * HP + p * rp + j] = bf16_part(v);
-            } else {
-                hl[row * HP + j] = v;
-            }
-        }
-        if (none || !c.out)
-            continue;
-        if constexpr (BF) {  // the parts end in a whole step of 32
-            const int slots = PARTS * rp, more = (32 - slots % 32) % 32;
-            for (int i = tid; i < kTileRows * more; i += 256)
-                hl[i / more * HP + slots + i % more] = 0;
-        }
-        if constexpr (!OF_A) {
-            for (int i = tid; i < kCols * (rp / 8); i += 256) {
-                const int n = i / (rp / 8), j = i % (rp / 8) * 8;
-                Raw8<E> v{};
-                if (n0 + n < c.N && j < nj)
-                    v = row8<E, false>(m + (int64_t)(n0 + n) * c.r + j0, j, nj);
-                *(Raw8<E> *)(ml + n * PITCH + j) = v;
-            }
-        } else {
-            for (int i = tid; i < rp * (kCols / 8); i += 256) {
-                const int j = i / (kCols / 8), n = i % (kCols / 8) * 8;
-                Raw8<E> v{};
-                if (j < nj)
-                    v = row8<E, FULL>(m + (int64_t)(j0 + j) * c.N, n0 + n, c.N);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if constexpr (sizeof(raw) == 2)
-                        ml[(n + e) * PITCH + j] = (uint16_t)(v.v[0][e >> 1] >> (16 * (e & 1)));
-                    else
-                        ml[(n + e) * PITCH + j] = __uint_as_float(v.v[e >> 2][e & 3]);
-                }
-            }
-        }
-        __syncthreads();
-        if constexpr (BF) {
-            const int slots = PARTS * rp;
-            int j = kg * 8;
-            for (int s = 0; s < slots; s += 32, j += 32) {
-                while (j >= rp)
-                    j -= rp;
-                u32x4_t mf[4], hf[4];
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    mf[i] = *(const u32x4_t *)(ml + (w * 64 + 16 * (r15 >> 2) + 4 * i + (r15 & 3)) * PITCH + j);
+                    res[b][i] = row8<O, FULL>((const typename O::raw *)c.residual + token[b] * c.ldres, col + 32 * i, c.N);
+        if (SETS > 0 && !none)
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    hf[b] = *(const u32x4_t *)(hl + (b * 16 + r15) * HP + s + kg * 8);
+            for (int q = 0; q < SETS; ++q)
+                held[q] = operands<E, OF_A, FULL, RFULL, HALF>(c, m, mcol, rank_of(q));
+    }
+    // h of the tile's tokens: the splits' sum, written out once
+    for (int i = tid; i < kTileRows * sh.rp; i += 256) {
+        const int row = i / sh.rp, j = i - row * sh.rp;
+        float v = 0.f;
+        if (row < tl.rows && j < c.r) {
+            if (!none) {
+                float p[kShrinkSplits];
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                for (int s = 0; s < kShrinkSplits; ++s)
+                    p[s] = c.part[(min(s, c.splits - 1) * (int64_t)c.o.T + tl.row0 + row) * c.r + j];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[b][i] = mfma_bf16(mf[i], hf[b], acc[b][i]);
+                for (int s = 0; s < kShrinkSplits; ++s)
+                    v += s < c.splits ? p[s] : 0.f;
             }
+            if (c.h && blockIdx.y == 0)
+                c.h[(int64_t)c.o.order[tl.row0 + row] * c.r + j] = c.scaled ? v * scale : v;
+            v *= scale;
+        }
+        if constexpr (BF) {
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p)
+                hl[row * sh.pitch + p * sh.rp + j] = bf16_part(v);
         } else {
-            for (int s = 0; s < rp; s += 4)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float mv = E::to_f(ml[(w * 64 + 16 * (r15 >> 2) + 4 * i + (r15 & 3)) * PITCH + s + kg]);
-#pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        acc[b][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(mv, hl[(b * 16 + r15) * HP + s + kg], acc[b][i], 0, 0, 0);
-                }
+            hl[row * sh.pitch + j] = v;
         }
     }
-    if (!c.out)
+    if constexpr (BF) {  // the parts end in a whole step
+        const int slots = PARTS * sh.rp, more = sh.steps * 32 - slots;
+        for (int i = tid; i < kTileRows * more; i += 256)
+            hl[i / more * sh.pitch + slots + i % more] = 0;
+    }
+    __syncthreads();
+    if (!on)
         return;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        if (b * 16 + r15 >= tl.rows)
-            continue;
-        typename O::raw *out = (typename O::raw *)c.out + token[b] * c.ldout;
+    for (int b = 0; b < NB; ++b) {
+        const int row = (SPREAD ? w : b) * 16 + r15;
+        if (row - r15 >= tl.rows)
+            break;
+        f32x4a acc[8];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (c.residual)
-                widen8<O>(res[b][q], v);
-            if (!none)
+        for (int e = 0; e < 8; ++e)
+            acc[e] = f32x4a{0.f, 0.f, 0.f, 0.f};
+        const auto step_of = [&](int s, const Operands<E> &o) __attribute__((always_inline)) {
+            if constexpr (BF) {
+                const u32x4_t h = *(const u32x4_t *)(hl + row * sh.pitch + s * 32 + kg * 8);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[e] += acc[b][2 * q + (e >> 2)][e & 3];
-            store8<O>(out, col + 8 * q, max(0, min(8, c.N - col - 8 * q)), v);
+                    acc[e] = mfma_bf16(o.v[e].v[0], h, acc[e]);
+            } else {
+                constexpr int P = HALF ? 4 : 8;
+                float h[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    h[i] = hl[row * sh.pitch + s * 32 + kg * P + i];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float v[8];
+                    widen8<E>(o.v[e], v);
+#pragma unroll
+                    for (int i = 0; i < P; ++i)
+                        acc[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[i], h[i], acc[e], 0, 0, 0);
+                }
+            }
+        };
+        if (!none) {
+            if constexpr (SETS == 0) {
+                for (int s = 0; s < sh.steps; ++s)
+                    step_of(s, operands<E, OF_A, FULL, RFULL, HALF>(c, m, mcol, rank_of(s)));
+            } else {
+                // a part's steps, then the next part's over the same operands
+                for (int s = 0; s < sh.steps; s += SETS)
+#pragma unroll
+                    for (int q = 0; q < SETS; ++q)
+                        step_of(s + q, held[q]);
+            }
+        }
+        if (row < tl.rows) {
+            typename O::raw *out = (typename O::raw *)c.out + token[b] * c.ldout;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (c.residual)
+                    widen8<O>(res[b][i], v);
+                if (!none)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] += acc[e][i];
+                store8<O>(out, col + 32 * i, max(0, min(8, c.N - col - 32 * i)), v);
+            }
         }
     }
 }
@@ -406,22 +526,29 @@ __global__ __launch_bounds__(64) void k_few_expand(ExpandCall c)
 }
 
 // ---- outer -----------------------------------------------------------------------------
-// grid: slices of 128 columns, runs of the sorted rows, chunks of 64 ranks.  In each
-// adapter's part of the run the four waves take 32 tokens in turn and their sums meet in
-// LDS.  An adapter whose tokens all lie in the run is done; the sums of one that goes on in other runs
-// are left in the run's slot 0 (it began in an earlier one) or 1 and added by k_outer_join.
-// A lane has column 8 (lane % 16) + e of the slice in MFMA e and reads 8 columns of 8 tokens.
+// grid: slices of 128 columns (of one call, then of the other's), runs of the sorted rows,
+// chunks of 64 ranks.  In each adapter's part of the run the four waves take 32 tokens in
+// turn and their sums meet in LDS.  An adapter whose tokens all lie in the run is done; the sums of
+// one that goes on in other runs are left in the run's slot 0 (it began in an earlier one)
+// or 1 and added by k_outer_join.  A lane has column 8 (lane % 16) + e of the slice in MFMA e
+// and reads 8 columns of 8 tokens.
+struct OuterPair {
+    OuterCall c[2];
+    int slices;  // of the first
+    int per;     // rows per run, of both
+};
+
 template <class X, int NJ, int PARTS, bool FULL>
-__global__ __launch_bounds__(256) void k_outer(OuterCall c, int per)
+__global__ __launch_bounds__(256) void k_outer(OuterPair two)
 {
     constexpr bool BF = std::is_same<X, BF16>::value;
-    constexpr int RP = NJ * 16, PITCH = kOuterCols + 4;
-    __shared__ float sums[RP * PITCH];
+    constexpr int RP = NJ * 16, PITCH = RP + 4;
+    __shared__ __align__(16) float sums[2][kOuterCols * PITCH];  // [column][rank]
+    const bool second = (int)blockIdx.x >= two.slices;
+    const OuterCall &c = two.c[second];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, r15 = lane & 15, kg = lane >> 4;
-    const int c0 = blockIdx.x * kOuterCols, j0 = blockIdx.z * kRC;
-    const int rows = c.o.offsets[c.o.n], beg = blockIdx.y * per, end = min(rows, beg + per);
-    if (beg >= end)
-        return;
+    const int c0 = (blockIdx.x - (second ? two.slices : 0)) * kOuterCols, j0 = blockIdx.z * kRC;
+    const int rows = c.o.offsets[c.o.n], beg = blockIdx.y * two.per, end = min(rows, beg + two.per);
     for (int s0 = beg, s1; s0 < end; s0 = s1) {
         const int a = adapter_of(c.o, s0), o0 = c.o.offsets[a], o1 = c.o.offsets[a + 1];
         s1 = min(o1, end);
@@ -432,22 +559,43 @@ __global__ __launch_bounds__(256) void k_outer(OuterCall c, int per)
             for (int e = 0; e < 8; ++e)
                 acc[j][e] = f32x4a{0.f, 0.f, 0.f, 0.f};
         const float gs = scale_of(c.gscale, a);
-        for (int t0 = s0 + w * 32; t0 < s1; t0 += 4 * 32) {
+        // (x of the next 32 tokens is under way over the products of these)
+        int t[8];
+        Raw8<X> next[8];
+        const auto tokens = [&](int t0) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                t[u] = c.o.order[min(t0 + 8 * kg + u, s1 - 1)];
+        };
+        const auto read = [&]() {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                next[u] = row8<X, FULL>((const typename X::raw *)c.x + t[u] * c.ldx, c0 + 8 * r15, c.W);
+        };
+        const int first = s0 + w * 32;
+        if (first < s1) {
+            tokens(first);
+            read();
+        }
+        for (int t0 = first; t0 < s1; t0 += 4 * 32) {
             Raw8<X> xr[8];
             float g[NJ][8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const int row = t0 + 8 * kg + u;
-                const int t = c.o.order[min(row, s1 - 1)];
-                xr[u] = row8<X, FULL>((const typename X::raw *)c.x + (int64_t)t * c.ldx, c0 + 8 * r15, c.W);
+                const bool in = t0 + 8 * kg + u < s1;
+                xr[u] = next[u];
+                if (!in)
+                    xr[u] = Raw8<X>{};
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
                     const int at = j0 + j * 16 + r15;
-                    const float v = c.g[(int64_t)t * c.r + min(at, c.r - 1)];
-                    g[j][u] = at < c.r && row < s1 ? v * gs : 0.f;
+                    const float v = c.g[(int64_t)t[u] * c.r + min(at, c.r - 1)];
+                    g[j][u] = at < c.r && in ? v * gs : 0.f;
                 }
-                if (row >= s1)
-                    xr[u] = Raw8<X>{};
+            }
+            if (t0 + 4 * 32 < s1) {
+                tokens(t0 + 4 * 32);
+                read();
             }
             if constexpr (BF) {
                 u32x4_t gp[NJ][PARTS];
@@ -487,17 +635,22 @@ __global__ __launch_bounds__(256) void k_outer(OuterCall c, int per)
                 }
             }
         }
-        for (int q = 0; q < 4; ++q) {
-            if (w == q)
+        // the sums of waves 0 and 1, then those of 2 and 3 onto them
+        for (int q = 0; q < 2; ++q) {
+            if (w >> 1 == q)
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < 8; ++e) {
+                        f32x4a *at = (f32x4a *)(sums[w & 1] + (8 * r15 + e) * PITCH + j * 16 + kg * 4);
+                        if (q) {
+                            const f32x4a v = *at;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float *s = sums + (j * 16 + kg * 4 + i) * PITCH + 8 * r15 + e;
-                            *s = q ? *s + acc[j][e][i] : acc[j][e][i];
+                            for (int i = 0; i < 4; ++i)
+                                acc[j][e][i] += v[i];
                         }
+                        *at = acc[j][e];
+                    }
             __syncthreads();
         }
         const bool whole = o0 >= beg && o1 <= end;
@@ -507,7 +660,7 @@ __global__ __launch_bounds__(256) void k_outer(OuterCall c, int per)
             const int j = c.of_b ? i % RP : i / kOuterCols, x = c.of_b ? i / RP : i % kOuterCols;
             if (j0 + j >= c.r || c0 + x >= c.W)
                 continue;
-            const float v = sums[j * PITCH + x];
+            const float v = sums[0][x * PITCH + j] + sums[1][x * PITCH + j];
             const int64_t at = c.of_b ? (int64_t)(c0 + x) * c.r + j0 + j : (int64_t)(j0 + j) * c.W + c0 + x;
             if (whole)
                 store_el(c.d, (int64_t)a * c.r * c.W + at, v, c.grad_dtype);
@@ -518,22 +671,26 @@ __global__ __launch_bounds__(256) void k_outer(OuterCall c, int per)
     }
 }
 
-// grid: blocks of 1024 elements, adapters
-__global__ __launch_bounds__(256) void k_outer_join(OuterCall c, int per)
+// grid: blocks of 256 elements (of one call, then of the other's), adapters
+__global__ __launch_bounds__(256) void k_outer_join(OuterPair two)
 {
+    const int64_t blocks = ((int64_t)two.c[0].r * two.c[0].W + 255) / 256;
+    const bool second = blockIdx.x >= blocks;
+    const OuterCall &c = two.c[second];
     const int a = blockIdx.y;
     const int o0 = c.o.offsets[a], o1 = c.o.offsets[a + 1];
-    const int first = o0 / per, last = (o1 - 1) / per;
+    const int first = o0 / two.per, last = (o1 - 1) / two.per;
     if (o1 > o0 && first == last)
         return;
-    const int64_t size = (int64_t)c.r * c.W;
-    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < min(size, ((int64_t)blockIdx.x + 1) * 1024); i += 256) {
-        float v = 0.f;
-        if (o1 > o0)
-            for (int q = first; q <= last; ++q)
-                v += c.slots[((int64_t)q * 2 + (q == first)) * size + i];
-        store_el(c.d, (int64_t)a * size + i, v, c.grad_dtype);
-    }
+    const int64_t size = (int64_t)c.r * c.W, i = (blockIdx.x - (second ? blocks : 0)) * 256 + threadIdx.x;
+    if (i >= size)
+        return;
+    float v = 0.f;
+    if (o1 > o0)
+#pragma unroll 16
+        for (int q = first; q <= last; ++q)
+            v += c.slots[((int64_t)q * 2 + (q == first)) * size + i];
+    store_el(c.d, (int64_t)a * size + i, v, c.grad_dtype);
 }
 
 // ---- launches --------------------------------------------------------------------------
@@ -570,25 +727,50 @@ void with_bool(bool b, F f)
 int most_tiles(const AdapterOrder &o) { return o.T / kTileRows + (o.n + 1 < o.T ? o.n + 1 : o.T); }
 int rank_blocks(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 
-template <class E, class X, bool OF_B, bool FULL>
+// (RFULL: whether rows of M of r elements, which only the transpose has, are whole chunks)
+template <class E, class X, bool OF_B, bool FULL, bool RFULL>
 void shrink_of(const ShrinkCall &c, hipStream_t st)
 {
     const dim3 grid(most_tiles(c.o), c.splits, (c.r + kRC - 1) / kRC);
     switch (rank_blocks(c.r)) {
-    case 1: hipLaunchKernelGGL((k_shrink<E, X, OF_B, 1, FULL>), grid, dim3(256), 0, st, c); break;
-    case 2: hipLaunchKernelGGL((k_shrink<E, X, OF_B, 2, FULL>), grid, dim3(256), 0, st, c); break;
-    default: hipLaunchKernelGGL((k_shrink<E, X, OF_B, 4, FULL>), grid, dim3(256), 0, st, c);
+    case 1: hipLaunchKernelGGL((k_shrink<E, X, OF_B, 1, FULL, RFULL>), grid, dim3(256), 0, st, c); break;
+    case 2: hipLaunchKernelGGL((k_shrink<E, X, OF_B, 2, FULL, RFULL>), grid, dim3(256), 0, st, c); break;
+    default: hipLaunchKernelGGL((k_shrink<E, X, OF_B, 4, FULL, RFULL>), grid, dim3(256), 0, st, c);
     }
 }
 
-template <class X, int PARTS, bool FULL>
-void outer_of(const OuterCall &c, int per, hipStream_t st)
+template <class E, class O, bool OF_A, bool FULL, bool RFULL>
+void expand_of(const ExpandCall &c, hipStream_t st)
 {
-    const dim3 grid((c.W + kOuterCols - 1) / kOuterCols, c.chunks, (c.r + kRC - 1) / kRC);
-    switch (rank_blocks(c.r)) {
-    case 1: hipLaunchKernelGGL((k_outer<X, 1, PARTS, FULL>), grid, dim3(256), 0, st, c, per); break;
-    case 2: hipLaunchKernelGGL((k_outer<X, 2, PARTS, FULL>), grid, dim3(256), 0, st, c, per); break;
-    default: hipLaunchKernelGGL((k_outer<X, 4, PARTS, FULL>), grid, dim3(256), 0, st, c, per);
+    constexpr bool BF = std::is_same<E, BF16>::value;
+    constexpr int PARTS = std::is_same<O, F32>::value ? 3 : 2;
+    // fewer than a block a CU: the columns in four times as many slices
+    const int tiles = most_tiles(c.o), slices = (c.N + kCols - 1) / kCols;
+    const bool spread = c.out && c.r <= 64 && (c.o.T / kTileRows + 1) * slices < 256;
+    const dim3 grid(tiles, !c.out ? 1 : spread ? (c.N + 127) / 128 : slices);
+    const size_t lds = (size_t)kTileRows * expand_shape<BF, PARTS>(c.r).pitch * (BF ? 2 : 4);
+    with_bool(spread, [&](auto sp) {
+        constexpr bool SP = decltype(sp)::value;
+        if (c.r <= 16)
+            hipLaunchKernelGGL((k_expand<E, O, OF_A, FULL, RFULL, 1, !BF, SP>), grid, dim3(256), lds, st, c);
+        else if (c.r <= 32)
+            hipLaunchKernelGGL((k_expand<E, O, OF_A, FULL, RFULL, 1, false, SP>), grid, dim3(256), lds, st, c);
+        else if (c.r <= 64)
+            hipLaunchKernelGGL((k_expand<E, O, OF_A, FULL, RFULL, 2, false, SP>), grid, dim3(256), lds, st, c);
+        else if constexpr (!SP)
+            hipLaunchKernelGGL((k_expand<E, O, OF_A, FULL, RFULL, 0, false, false>), grid, dim3(256), lds, st, c);
+    });
+}
+
+template <class X, int PARTS, bool FULL>
+void outer_of(const OuterPair &p, int slices, int chunks, hipStream_t st)
+{
+    const int r = p.c[0].r;
+    const dim3 grid(slices, chunks, (r + kRC - 1) / kRC);
+    switch (rank_blocks(r)) {
+    case 1: hipLaunchKernelGGL((k_outer<X, 1, PARTS, FULL>), grid, dim3(256), 0, st, p); break;
+    case 2: hipLaunchKernelGGL((k_outer<X, 2, PARTS, FULL>), grid, dim3(256), 0, st, p); break;
+    default: hipLaunchKernelGGL((k_outer<X, 4, PARTS, FULL>), grid, dim3(256), 0, st, p);
     }
 }
 
@@ -611,9 +793,12 @@ int launch_shrink(const ShrinkCall &c, hipStream_t st)
     with_bool(c.K % 8 == 0, [&](auto full) {
         constexpr bool FULL = decltype(full)::value;
         if (c.of_b)
-            with_pair(c.dtype, c.x_dtype, [&](auto e, auto x) { shrink_of<decltype(e), decltype(x), true, FULL>(c, st); });
+            with_bool(c.r % 8 == 0, [&](auto rfull) {
+                constexpr bool RFULL = decltype(rfull)::value;
+                with_pair(c.dtype, c.x_dtype, [&](auto e, auto x) { shrink_of<decltype(e), decltype(x), true, FULL, RFULL>(c, st); });
+            });
         else
-            with_element(c.dtype, [&](auto e) { shrink_of<decltype(e), decltype(e), false, FULL>(c, st); });
+            with_element(c.dtype, [&](auto e) { shrink_of<decltype(e), decltype(e), false, FULL, true>(c, st); });
     });
     ECF_HIP_CHECK(hipGetLastError());
     return ECF_OK;
@@ -622,16 +807,14 @@ int launch_shrink(const ShrinkCall &c, hipStream_t st)
 int launch_expand(const ExpandCall &c, hipStream_t st)
 {
     ProfScope prof("adapter_expand", st);
-    const dim3 grid(most_tiles(c.o), c.out ? (c.N + kCols - 1) / kCols : 1);
     with_bool(c.N % 8 == 0, [&](auto full) {
         constexpr bool FULL = decltype(full)::value;
         if (c.of_a)
-            with_element(c.dtype, [&](auto e) {
-                hipLaunchKernelGGL((k_expand<decltype(e), decltype(e), true, FULL>), grid, dim3(256), 0, st, c);
-            });
+            with_element(c.dtype, [&](auto e) { expand_of<decltype(e), decltype(e), true, FULL, true>(c, st); });
         else
-            with_pair(c.dtype, c.out_dtype, [&](auto e, auto o) {
-                hipLaunchKernelGGL((k_expand<decltype(e), decltype(o), false, FULL>), grid, dim3(256), 0, st, c);
+            with_bool(c.r % 8 == 0, [&](auto rfull) {
+                constexpr bool RFULL = decltype(rfull)::value;
+                with_pair(c.dtype, c.out_dtype, [&](auto e, auto o) { expand_of<decltype(e), decltype(o), false, FULL, RFULL>(c, st); });
             });
     });
     ECF_HIP_CHECK(hipGetLastError());
@@ -662,34 +845,46 @@ int launch_few_expand(const ExpandCall &c, hipStream_t st)
     return ECF_OK;
 }
 
+int outer_slices(int W) { return (W + kOuterCols - 1) / kOuterCols; }
+
 // Runs of the sorted rows: two blocks a CU over all slices, 128 rows each at least.
-int outer_chunks(int T, int W)
+int outer_chunks(int T, int slices)
 {
-    const int slices = (W + kOuterCols - 1) / kOuterCols, most = (T + 127) / 128;
-    const int s = 512 / slices;
+    const int most = (T + 127) / 128, s = 512 / slices;
     return s < 1 || most < 1 ? 1 : s < most ? s : most;
 }
 
-int launch_outer(const OuterCall &c, hipStream_t st)
+int launch_outer(const OuterCall *calls, int n, int chunks, hipStream_t st)
 {
     ProfScope prof("adapter_outer", st);
-    const int per = c.o.T > 0 ? ((c.o.T + c.chunks - 1) / c.chunks + 31) / 32 * 32 : 32;
-    with_bool(c.W % 8 == 0, [&](auto full) {
+    OuterPair p{};
+    p.c[0] = calls[0], p.c[1] = calls[n - 1];
+    p.slices = outer_slices(calls[0].W);
+    const int T = calls[0].o.T;
+    p.per = T > 0 ? ((T + chunks - 1) / chunks + 31) / 32 * 32 : 32;
+    int slices = 0;
+    int64_t blocks = 0;
+    bool whole = true;
+    for (int i = 0; i < n; ++i) {
+        slices += outer_slices(calls[i].W);
+        blocks += ((int64_t)calls[i].r * calls[i].W + 255) / 256;
+        whole = whole && calls[i].W % 8 == 0;
+    }
+    with_bool(whole, [&](auto full) {
         constexpr bool FULL = decltype(full)::value;
-        if (c.x_dtype == ECF_BF16) {
-            if (c.grad_dtype == ECF_F32)
-                outer_of<BF16, 3, FULL>(c, per, st);
+        if (calls[0].x_dtype == ECF_BF16) {
+            if (calls[0].grad_dtype == ECF_F32)
+                outer_of<BF16, 3, FULL>(p, slices, chunks, st);
             else
-                outer_of<BF16, 2, FULL>(c, per, st);
-        } else if (c.x_dtype == ECF_F32) {
-            outer_of<F32, 1, FULL>(c, per, st);
+                outer_of<BF16, 2, FULL>(p, slices, chunks, st);
+        } else if (calls[0].x_dtype == ECF_F32) {
+            outer_of<F32, 1, FULL>(p, slices, chunks, st);
         } else {
-            outer_of<F16, 1, FULL>(c, per, st);
+            outer_of<F16, 1, FULL>(p, slices, chunks, st);
         }
     });
     ECF_HIP_CHECK(hipGetLastError());
-    const int64_t size = (int64_t)c.r * c.W;
-    hipLaunchKernelGGL(k_outer_join, dim3((unsigned)((size + 1023) / 1024), c.o.n), dim3(256), 0, st, c, per);
+    hipLaunchKernelGGL(k_outer_join, dim3((unsigned)blocks, calls[0].o.n), dim3(256), 0, st, p);
     ECF_HIP_CHECK(hipGetLastError());
     return ECF_OK;
 }

@@ -13,9 +13,11 @@
 namespace ecf {
 namespace {
 
-constexpr int kSortRows = 1024;          // choices that a block takes at a time
-constexpr int kSortOne = 4 * kSortRows;  // up to which one block sorts them all
-constexpr int kSortSegments = 128;       // most segments
+constexpr int kSortRows = 1024;      // choices that a block takes at a time
+// Segments up to which each block counts the others' choices itself: 5 segments of 60 experts 7.4 us,
+// against 3.1 + 6.3 for a kernel that counts and one that places; 24 of 256 experts 15.3 against 4.9 + 9.1.
+constexpr int kSortSelf = 8;
+constexpr int kSortSegments = 128;   // most segments
 
 __device__ __forceinline__ int choice(const SortCall &c, uint32_t f)
 {
@@ -74,37 +76,34 @@ __global__ __launch_bounds__(1024) void k_token_count(SortCall c, uint32_t per)
         c.segments[(int64_t)blockIdx.x * (c.E + 1) + e] = hist[e];
 }
 
-// Each block places its segment; block 0 writes the tables.  segments: the counts of all
-// segments (one segment: counted here).  A wave owns a run of its segment's choices; where that
-// is at most HELD steps of 64, their numbers and ranks stay in registers, otherwise they are
-// counted first and ranked in a second pass.  The block has at least E threads.
-template <int NW, int HELD>
+// Each block places its segment; block 0 writes the tables.  A wave owns a run of its
+// segment's choices: one step of 64 (HELD), whose numbers and ranks stay in registers, or
+// more, which are counted first and ranked in a second pass.  The block has at least E threads.
+// SELF: the other segments' choices are counted here; otherwise k_token_count has left the
+// counts of each segment.
+template <int NW, bool HELD, bool SELF>
 __global__ __launch_bounds__(64 * NW) void k_token_place(SortCall c, uint32_t per, int segments, int bits)
 {
-    extern __shared__ int base[];  // [NW][E + 1]
+    extern __shared__ int base[];  // [NW][E + 1], SELF: and the counts of the segments after and before this one
     __shared__ uint64_t sh[NW];
     constexpr int NT = 64 * NW;
     const int EB = c.E + 1, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    int *later = base + NW * EB, *earlier = later + EB;
     const uint32_t rows = (uint32_t)c.T * c.k, beg = min(rows, blockIdx.x * per), end = min(rows, beg + per);
     const uint32_t run = ((per + NW - 1) / NW + 63) / 64 * 64, wb = min(end, beg + w * run), we = min(end, wb + run);
-    int key[HELD ? HELD : 1], rank[HELD ? HELD : 1];
-    if constexpr (HELD > 0) {
-#pragma unroll
-        for (int q = 0; q < HELD; ++q) {
-            const uint32_t f = wb + q * 64 + lane;
-            key[q] = f < we ? choice(c, f) : -1;
-        }
-    }
-    for (int i = tid; i < NW * EB; i += NT)
+    int key = -1, rank = 0;
+    if (HELD && wb + lane < we)
+        key = choice(c, wb + lane);
+    for (int i = tid; i < (SELF ? NW + 2 : NW) * EB; i += NT)
         base[i] = 0;
-    // this expert's rows in all segments and in those before (loads under way over the barrier)
+    // this expert's rows in the other segments and in those before (loads under way over the barrier)
     int all = 0, before = 0, none_before = 0;
-    if (segments > 1) {
+    if constexpr (!SELF) {
         const int col = min(tid, c.E);
 #pragma unroll 16
         for (int s = 0; s < segments; ++s) {
             const int v = c.segments[(int64_t)s * EB + col];
-            all += v;
+            all += s == (int)blockIdx.x ? 0 : v;
             before += s < (int)blockIdx.x ? v : 0;
         }
         // those of no expert, by the last thread, which may have an expert as well
@@ -114,17 +113,35 @@ __global__ __launch_bounds__(64 * NW) void k_token_place(SortCall c, uint32_t pe
                 none_before += c.segments[(int64_t)s * EB + c.E];
     }
     __syncthreads();
-    if constexpr (HELD > 0) {
-        // (a wave's own counters: its steps follow each other)
+    if constexpr (SELF) {
+        if (segments > 1) {
+            for (int s0 = 0; s0 < segments; s0 += 8) {
+                int k[8];
 #pragma unroll
-        for (int q = 0; q < HELD; ++q) {
-            const uint64_t peers = peers_of(key[q], key[q] >= 0, bits);
-            if (key[q] >= 0) {
-                const int n = base[w * EB + key[q]];
-                rank[q] = n + __popcll(peers & lanemask_lt(lane));
-                if (lane == __ffsll((unsigned long long)peers) - 1)
-                    base[w * EB + key[q]] = n + __popcll(peers);
+                for (int q = 0; q < 8; ++q) {
+                    const uint32_t f = (s0 + q) * per + tid;
+                    k[q] = s0 + q != (int)blockIdx.x && s0 + q < segments && f < rows ? choice(c, f) : -1;
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (k[q] >= 0)
+                        atomicAdd(s0 + q < (int)blockIdx.x ? &earlier[k[q]] : &later[k[q]], 1);
             }
+            __syncthreads();
+        }
+        if (tid <= c.E) {
+            before = earlier[tid];
+            all = before + later[tid];
+        }
+        if (tid == NT - 1)
+            none_before = earlier[c.E];
+    }
+    if constexpr (HELD) {
+        const uint64_t peers = peers_of(key, key >= 0, bits);
+        if (key >= 0) {
+            rank = __popcll(peers & lanemask_lt(lane));
+            if (rank == 0)
+                base[w * EB + key] = __popcll(peers);
         }
     } else {
         for (uint32_t f = wb + lane; f < we; f += 64)
@@ -139,10 +156,7 @@ __global__ __launch_bounds__(64 * NW) void k_token_place(SortCall c, uint32_t pe
             base[q * EB + tid] = mine;
             mine += v;
         }
-    if (segments == 1)
-        all = mine;
-    if (tid >= c.E)
-        all = 0;
+    all = tid < c.E ? all + mine : 0;
     uint64_t total;
     const uint64_t first = block_scan<NW>((uint64_t)all | (uint64_t)((all + kTileRows - 1) / kTileRows) << 32, sh, &total);
     const int chosen = (int)(uint32_t)total;
@@ -174,15 +188,12 @@ __global__ __launch_bounds__(64 * NW) void k_token_place(SortCall c, uint32_t pe
         }
     }
     __syncthreads();
-    if constexpr (HELD > 0) {
-#pragma unroll
-        for (int q = 0; q < HELD; ++q)
-            if (key[q] >= 0) {
-                const uint32_t f = wb + q * 64 + lane;
-                const int p = base[w * EB + key[q]] + rank[q];
-                c.order[p] = (int)f;
-                c.place[f] = p;
-            }
+    if constexpr (HELD) {
+        if (key >= 0) {
+            const int p = base[w * EB + key] + rank;
+            c.order[p] = (int)(wb + lane);
+            c.place[wb + lane] = p;
+        }
     } else {
         for (uint32_t f0 = wb; f0 < we; f0 += 64) {
             const uint32_t f = f0 + lane;
@@ -411,35 +422,33 @@ void with_pair(const MoveCall &c, F f)
 
 int sort_segments(int64_t rows)
 {
-    if (rows <= kSortOne)
-        return 1;
-    const int64_t n = (rows + kSortRows - 1) / kSortRows;
+    const int64_t n = rows > 0 ? (rows + kSortRows - 1) / kSortRows : 1;
     return (int)(n < kSortSegments ? n : kSortSegments);
 }
+
+bool sort_counts_itself(int segments) { return segments <= kSortSelf; }
 
 int launch_token_sort(const SortCall &c, hipStream_t st)
 {
     ProfScope prof("token_sort", st);
     const uint32_t rows = (uint32_t)c.T * c.k;
     const int n = sort_segments(rows);
-    // one segment or whole steps of a block
-    const uint32_t per = n == 1 ? rows : ((rows + n - 1) / n + kSortRows - 1) / kSortRows * kSortRows;
+    const uint32_t per = ((rows + n - 1) / n + kSortRows - 1) / kSortRows * kSortRows;  // whole steps of a block
     const size_t sh = (size_t)(c.E + 1) * 4;
     int bits = 0;
     while ((1 << bits) <= c.E)
         ++bits;
-    if (n > 1)
+    if (rows <= 256 && c.E <= 256) {
+        hipLaunchKernelGGL((k_token_place<4, true, true>), dim3(1), dim3(256), 6 * sh, st, c, 256, 1, bits);
+    } else if (sort_counts_itself(n)) {
+        hipLaunchKernelGGL((k_token_place<16, true, true>), dim3(n), dim3(1024), 18 * sh, st, c, kSortRows, n, bits);
+    } else {
         hipLaunchKernelGGL(k_token_count, dim3(n), dim3(1024), sh, st, c, per);
-    if (n > 1 && per > kSortRows)
-        hipLaunchKernelGGL((k_token_place<16, 0>), dim3(n), dim3(1024), 16 * sh, st, c, per, n, bits);
-    else if (n > 1)
-        hipLaunchKernelGGL((k_token_place<16, 1>), dim3(n), dim3(1024), 16 * sh, st, c, per, n, bits);
-    else if (rows <= 256 && c.E <= 256)
-        hipLaunchKernelGGL((k_token_place<4, 1>), dim3(1), dim3(256), 4 * sh, st, c, per, n, bits);
-    else if (rows <= 1024)
-        hipLaunchKernelGGL((k_token_place<16, 1>), dim3(1), dim3(1024), 16 * sh, st, c, per, n, bits);
-    else
-        hipLaunchKernelGGL((k_token_place<16, 4>), dim3(1), dim3(1024), 16 * sh, st, c, per, n, bits);
+        if (per == kSortRows)
+            hipLaunchKernelGGL((k_token_place<16, true, false>), dim3(n), dim3(1024), 16 * sh, st, c, per, n, bits);
+        else
+            hipLaunchKernelGGL((k_token_place<16, false, false>), dim3(n), dim3(1024), 16 * sh, st, c, per, n, bits);
+    }
     ECF_HIP_CHECK(hipGetLastError());
     return ECF_OK;
 }

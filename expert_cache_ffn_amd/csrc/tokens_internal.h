@@ -43,12 +43,13 @@ struct SortCall {
     int32_t *counts, *offsets, *tiles, *order, *place;
     int32_t *segments;  // workspace: [sort_segments][E + 1]
 };
-// Segments of the choices that blocks of their own count and place (1: one block does all).
+// Segments of the choices, which blocks of their own place; many have their counts in the workspace.
 int sort_segments(int64_t rows);
+bool sort_counts_itself(int segments);
 inline size_t sort_ws(int64_t rows, int E)
 {
     const int s = sort_segments(rows);
-    return s > 1 ? al256((size_t)s * (E + 1) * 4) : 0;
+    return sort_counts_itself(s) ? 0 : al256((size_t)s * (E + 1) * 4);
 }
 int launch_token_sort(const SortCall &c, hipStream_t st);
 
@@ -87,7 +88,7 @@ struct AdapterOrder {
 constexpr int kAdapterFew = 64;
 
 // part[s][t][j] = sum over split s of k of x[t][k] M[a](j, k): A[a] as it lies, [r][K] (of_b
-// false), or B[a]'s transpose (of_b: M[a] lies as [K][r]).
+// false), or B[a]'s transpose (of_b: M[a] lies as [K][r]); t the row of the order, where there is one.
 struct ShrinkCall {
     AdapterOrder o;
     int dtype, x_dtype, K, r;
@@ -97,7 +98,7 @@ struct ShrinkCall {
     float *part;
     int splits, split_k;  // split_k: k per split, a multiple of 128
 };
-constexpr int kShrinkBlocks = 512, kShrinkSplits = 8;
+constexpr int kShrinkBlocks = 1024, kShrinkSplits = 8;
 int shrink_splits(int T, int K);
 // Rows of h in all splits of any call of up to T tokens.
 inline int64_t shrink_rows(int64_t T)
@@ -141,10 +142,12 @@ struct OuterCall {
     int64_t ldx;
     void *d;
     float *slots;  // outer_slots bytes
-    int chunks;    // the sorted rows in this many runs, blocks of their own
 };
-int outer_chunks(int T, int W);
+int outer_slices(int W);
+// Runs of the sorted rows, blocks of their own, for so many slices of columns.
+int outer_chunks(int T, int slices);
 inline size_t outer_slots(int chunks, int W, int r) { return chunks > 1 ? al256((size_t)chunks * 2 * W * r * 4) : 0; }
-int launch_outer(const OuterCall &c, hipStream_t st);
+// One or two of one rank and x_dtype over the same order.
+int launch_outer(const OuterCall *calls, int n, int chunks, hipStream_t st);
 
 }  // namespace ecf

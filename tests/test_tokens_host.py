@@ -159,9 +159,9 @@ def test_workspace():
     assert need == 100 * 64 * 4 and ecf.ecf_norm_workspace_bytes(64, 100) == 0
     refused(ecf.ecf_norm_backward, norm_bwd(ws_bytes=need - 1), T=100, code=ecf.ECF_ENOSPC)
     refused(ecf.ecf_norm_backward, norm_bwd(d_ws=A + 128), T=100)
-    need = ecf.ecf_token_sort_workspace_bytes(8, 2, 5000)
+    need = ecf.ecf_token_sort_workspace_bytes(8, 2, 50000)
     assert need > 0 and ecf.ecf_token_sort_workspace_bytes(8, 2, 2048) == 0
-    refused(ecf.ecf_token_sort, sort(ws_bytes=need - 1), T=5000, code=ecf.ECF_ENOSPC)
+    refused(ecf.ecf_token_sort, sort(ws_bytes=need - 1), T=50000, code=ecf.ECF_ENOSPC)
     for size, shape in ((ecf.ecf_norm_workspace_bytes, (4096,)), (ecf.ecf_token_sort_workspace_bytes, (256, 6))):
         last = 0
         for T in (0, 1, 16, 500, 700, 5000, 100000, 1 << 22):
