@@ -53,17 +53,6 @@ __device__ __forceinline__ Tile tile_of(const AdapterOrder &o, int b)
     return t;
 }
 
-// The adapter of row `row` of the order (one with an adapter): the last that begins at or
-// before it.
-__device__ __forceinline__ int adapter_of(const AdapterOrder &o, int row)
-{
-    const int lane = threadIdx.x & 63;
-    int a = -1;
-    for (int e0 = 0; e0 < o.n; e0 += 64)
-        a += __popcll(__ballot(e0 + lane < o.n && o.offsets[min(e0 + lane, o.n)] <= row));
-    return a;
-}
-
 __device__ __forceinline__ float scale_of(const float *scale, int a) { return scale ? scale[a] : 1.f; }
 
 // v as a sum of bf16 values, the k-th of them
@@ -526,9 +515,9 @@ __global__ __launch_bounds__(64) void k_few_expand(ExpandCall c)
 }
 
 // ---- outer -----------------------------------------------------------------------------
-// grid: slices of 128 columns (of one call, then of the other's), runs of the sorted rows,
-// chunks of 64 ranks.  In each adapter's part of the run the four waves take 32 tokens in
-// turn and their sums meet in LDS.  An adapter whose tokens all lie in the run is done; the sums of
+// grid: slices of 128 columns (of one call, then of the other's), runs of the sorted rows
+// times `share`, chunks of 64 ranks.  A block takes every share-th adapter of its run; in an
+// adapter's part of the run the four waves take 32 tokens in turn and their sums meet in LDS.  An adapter whose tokens all lie in the run is done; the sums of
 // one that goes on in other runs are left in the run's slot 0 (it began in an earlier one)
 // or 1 and added by k_outer_join.  A lane has column 8 (lane % 16) + e of the slice in MFMA e
 // and reads 8 columns of 8 tokens.
@@ -536,6 +525,7 @@ struct OuterPair {
     OuterCall c[2];
     int slices;  // of the first
     int per;     // rows per run, of both
+    int share;   // blocks that share a run's adapters
 };
 
 template <class X, int NJ, int PARTS, bool FULL>
@@ -548,10 +538,10 @@ __global__ __launch_bounds__(256) void k_outer(OuterPair two)
     const OuterCall &c = two.c[second];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, r15 = lane & 15, kg = lane >> 4;
     const int c0 = (blockIdx.x - (second ? two.slices : 0)) * kOuterCols, j0 = blockIdx.z * kRC;
-    const int rows = c.o.offsets[c.o.n], beg = blockIdx.y * two.per, end = min(rows, beg + two.per);
-    for (int s0 = beg, s1; s0 < end; s0 = s1) {
-        const int a = adapter_of(c.o, s0), o0 = c.o.offsets[a], o1 = c.o.offsets[a + 1];
-        s1 = min(o1, end);
+    const int run = blockIdx.y / two.share, turn = blockIdx.y % two.share;
+    const int beg = run * two.per, stop = beg + two.per;  // (an adapter's rows end by themselves)
+    const auto adapter = [&](int a, int o0, int o1) __attribute__((always_inline)) {
+        const int s0 = max(o0, beg), s1 = min(o1, stop);
         f32x4a acc[NJ][8];
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
@@ -653,8 +643,8 @@ __global__ __launch_bounds__(256) void k_outer(OuterPair two)
                     }
             __syncthreads();
         }
-        const bool whole = o0 >= beg && o1 <= end;
-        float *slot = c.slots + ((int64_t)blockIdx.y * 2 + (o0 >= beg)) * c.r * c.W;
+        const bool whole = o0 >= beg && o1 <= stop;
+        float *slot = c.slots + ((int64_t)run * 2 + (o0 >= beg)) * c.r * c.W;
         for (int i = tid; i < RP * kOuterCols; i += 256) {
             // along the side that is contiguous
             const int j = c.of_b ? i % RP : i / kOuterCols, x = c.of_b ? i / RP : i % kOuterCols;
@@ -668,6 +658,15 @@ __global__ __launch_bounds__(256) void k_outer(OuterPair two)
                 slot[at] = v;
         }
         __syncthreads();
+    };
+    // this block's adapters with rows in the run, found 64 at a time
+    for (int e0 = 0; e0 < c.o.n; e0 += 64) {
+        const int e = e0 + lane, from = c.o.offsets[min(e, c.o.n)], to = c.o.offsets[min(e + 1, c.o.n)];
+        uint64_t mine = __ballot(e < c.o.n && e % two.share == turn && max(from, beg) < min(to, stop));
+        for (; mine; mine &= mine - 1) {
+            const int i = __ffsll((unsigned long long)mine) - 1;
+            adapter(e0 + i, __builtin_amdgcn_readlane(from, i), __builtin_amdgcn_readlane(to, i));
+        }
     }
 }
 
@@ -766,7 +765,7 @@ template <class X, int PARTS, bool FULL>
 void outer_of(const OuterPair &p, int slices, int chunks, hipStream_t st)
 {
     const int r = p.c[0].r;
-    const dim3 grid(slices, chunks, (r + kRC - 1) / kRC);
+    const dim3 grid(slices, chunks * p.share, (r + kRC - 1) / kRC);
     switch (rank_blocks(r)) {
     case 1: hipLaunchKernelGGL((k_outer<X, 1, PARTS, FULL>), grid, dim3(256), 0, st, p); break;
     case 2: hipLaunchKernelGGL((k_outer<X, 2, PARTS, FULL>), grid, dim3(256), 0, st, p); break;
@@ -870,6 +869,13 @@ int launch_outer(const OuterCall *calls, int n, int chunks, hipStream_t st)
         blocks += ((int64_t)calls[i].r * calls[i].W + 255) / 256;
         whole = whole && calls[i].W % 8 == 0;
     }
+    // Many adapters in a run are shared by blocks: by as many as fill the GPU, and so that one has about
+    // four to do (39 tokens of 15 adapters, 219 to 768 in fp16 at rank 64: 285 us by one block a run, 40 so).
+    const int n_adapters = calls[0].o.n, room = 512 / (slices * chunks), each = n_adapters / (4 * chunks);
+    p.share = each > 16 ? 16 : each;
+    p.share = p.share > room ? p.share : room;
+    p.share = p.share < n_adapters ? p.share : n_adapters;
+    p.share = p.share > 1 ? p.share : 1;
     with_bool(whole, [&](auto full) {
         constexpr bool FULL = decltype(full)::value;
         if (calls[0].x_dtype == ECF_BF16) {

@@ -324,14 +324,17 @@ __global__ __launch_bounds__(256) void k_combine_tokens(MoveCall c)
     store8<O>((typename O::raw *)c.out + t * c.ldout, col, (int)min((int64_t)8, c.d - col), s);
 }
 
-// grid: one wave per choice
-template <class E, class O, bool FULL>
+// G lanes per choice, 256 threads in a block.
+template <class E, class O, bool FULL, int G>
 __global__ __launch_bounds__(256) void k_combine_back(MoveCall c)
 {
-    const uint32_t f = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), all = (uint32_t)c.T * c.k;
+    constexpr int PER = 256 / G;
+    // (the same for all of a wave where a choice has one)
+    const uint32_t sub = G == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / G) : threadIdx.x / G;
+    const uint32_t f = blockIdx.x * PER + sub, all = (uint32_t)c.T * c.k;
     if (f >= all)
         return;
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x % G;
     const int64_t t = f / (uint32_t)c.k;
     const int p = c.place[f];
     const bool none = p >= *c.n_rows, there = (uint32_t)p < all;
@@ -341,7 +344,7 @@ __global__ __launch_bounds__(256) void k_combine_back(MoveCall c)
     typename E::raw *dr = (typename E::raw *)c.drows + (there ? p : 0) * c.lddrows;
     const bool dots = c.dweight && !none && there;
     double dot = 0.0;
-    for (int64_t c0 = 0; c0 < c.d; c0 += 64 * 8) {
+    for (int64_t c0 = 0; c0 < c.d; c0 += G * 8) {
         const int64_t col = c0 + lane * 8;
         float g[8], v[8];
         const Raw8<O> gr = row8<O, FULL>(dout, col, c.d);
@@ -365,7 +368,13 @@ __global__ __launch_bounds__(256) void k_combine_back(MoveCall c)
         }
     }
     if (c.dweight) {
-        dot = wave_sum_f64(dot);
+        if constexpr (G == 64) {
+            dot = wave_sum_f64(dot);
+        } else {
+#pragma unroll
+            for (int o = 1; o < G; o <<= 1)
+                dot += __shfl_xor(dot, o, 64);
+        }
         if (lane == 0)
             c.dweight[f] = dots ? (float)dot : 0.f;
     }
@@ -505,10 +514,19 @@ int launch_combine_tokens(const MoveCall &c, hipStream_t st)
 int launch_combine_backward(const MoveCall &c, hipStream_t st)
 {
     ProfScope prof("token_combine_backward", st);
-    const dim3 grid((unsigned)(((int64_t)c.T * c.k + 3) / 4));
+    // a wave per choice, or 8 or 32 lanes where they hold its row
     with_pair(c, [&](auto e, auto o) {
         with_bool(c.d % 8 == 0, [&](auto full) {
-            hipLaunchKernelGGL((k_combine_back<decltype(e), decltype(o), decltype(full)::value>), grid, dim3(256), 0, st, c);
+            using E = decltype(e);
+            using O = decltype(o);
+            constexpr bool FULL = decltype(full)::value;
+            const auto grid = [&](int g) { return dim3((unsigned)(((int64_t)c.T * c.k * g + 255) / 256)); };
+            if (c.d <= 64)
+                hipLaunchKernelGGL((k_combine_back<E, O, FULL, 8>), grid(8), dim3(256), 0, st, c);
+            else if (c.d <= 256)
+                hipLaunchKernelGGL((k_combine_back<E, O, FULL, 32>), grid(32), dim3(256), 0, st, c);
+            else
+                hipLaunchKernelGGL((k_combine_back<E, O, FULL, 64>), grid(64), dim3(256), 0, st, c);
         });
     });
     ECF_HIP_CHECK(hipGetLastError());

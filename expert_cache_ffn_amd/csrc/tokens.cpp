@@ -97,7 +97,7 @@ size_t ecf_norm_workspace_bytes(int32_t hidden, int32_t n_tokens, int32_t backwa
 {
     if (check_width("ecf_norm_workspace_bytes", hidden, n_tokens) != ECF_OK)
         return SIZE_MAX;
-    return backward ? al256((size_t)norm_partial_rows(n_tokens) * hidden * 4) : 0;
+    return backward ? al256((size_t)norm_partial_rows(n_tokens, hidden) * hidden * 4) : 0;
 }
 
 int ecf_norm_forward(const ecf_norm_args *a, int32_t T)

@@ -28,10 +28,10 @@ struct NormCall {
     void *dx, *ds;
     int64_t lddx, ldds;
     void *dweight;
-    float *partial;  // [norm_partial_rows(T)][d]
+    float *partial;  // [norm_partial_rows(T, d)][d]
 };
 // Rows of column sums that the blocks of a backward pass leave behind for the weight's gradient.
-int norm_partial_rows(int T);
+int norm_partial_rows(int T, int d);
 int launch_norm_forward(const NormCall &c, hipStream_t st);
 int launch_norm_backward(const NormCall &c, hipStream_t st);
 

@@ -706,6 +706,7 @@ class LowRankAdapters(_Tokens):
         self.down, self.up, self.scale = _kept(down, up, scale)
         self._a = a
         self._ws_of = {}
+        self._ws(0, 0)  # refuses a shape that no call takes
 
     def _ids(self, a, ids, T):
         if isinstance(ids, TokenSort):
