@@ -9,7 +9,12 @@
 // serves all requests.  Few tokens need no order: each is a block of its own.
 //
 // x, the residual and the output are read and written once, which bounds all of them; the
-// matrices are shared by 64 tokens (by a run of them).
+// matrices are shared by 64 tokens (by a run of them) and come from the caches.  Measured in
+// bf16 (a large copy takes 5.0 TB/s): 4096 tokens, 4096 to 4096, rank 16, 8 adapters: shrink
+// 13.5 us (2.5 TB/s: few chunks a block behind the chain tiles - order - x), expand 22.5 (3.0:
+// all blocks run at once, first all load, then all store); 8192 tokens, 2048 / 4096, rank 32:
+// shrink of dout 20 (3.4), expand to dx 25 (2.7), both outer products 34 (2.9) and 7 for their
+// join; 16 tokens of 16 adapters 3.0 + 3.7 us.
 //
 // What lies between shrink and expand (h, in the backward pass g) stays in fp32.  As an operand
 // of a bf16 product it is split into two bf16 parts (16 bits in all; three parts, so all 24

@@ -3,13 +3,20 @@
 // Forward: s = x + residual (rounded to its type), y = s * rstd * w with
 // rstd = 1 / sqrt(mean s^2 + eps).  A row is read once: its threads hold it in registers
 // over the sum of squares, which is taken in 64 bits (an fp32 square overflows at values of
-// 1.8e19 that bf16 and fp32 hold).
+// 1.8e19 that bf16 and fp32 hold).  8 bits: four lanes have the 32 columns of a scale, so
+// its maximum is two DPP steps.
 //
 // Backward: with h = s rstd and g = dy w, ds = dsum + rstd (g - h mean(g h)), and
-// dw = sum_t dy h.  A block walks over rows, holding its columns' part of dw in
-// registers; the blocks' parts are joined in a fixed order by a second kernel.
+// dw = sum_t dy h.  A group of threads walks over rows, holding its columns' part of dw in
+// registers; the parts are joined in a fixed order by a second kernel.
 //
-// Both are bound by memory.
+// A row has as many threads as hold it in at most four chunks of eight elements each: a
+// wave of its own up to 1024 elements needs no barrier, four waves up to 8192, sixteen up to
+// 16384.  Longer rows are read again from the caches.
+//
+// Bound by memory.  bf16 with an fp32 sum: 8192 x 4096 to 8 bits 70 us (5.3 TB/s, where a large
+// copy takes 5.0), 4096 x 4096 backward 47 us and 5 for the join (5.8 TB/s); one token of
+// 4096 3.1 us, launch and two rounds of loads.
 #include "tokens_device.h"
 
 namespace ecf {

