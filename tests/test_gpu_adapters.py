@@ -29,11 +29,13 @@ SIZES = [(1, 1, 1, 1, 1), (1, 4096, 4096, 16, 64), (3, 7, 5, 3, 2), (16, 1000, 1
          (66, 130, 257, 16, 40), (128, 128, 256, 32, 1), (200, 136, 72, 33, 5), (300, 520, 1030, 64, 4), (257, 1330, 300, 12, 1024),
          (700, 264, 136, 1, 9), (129, 300, 265, 100, 3), (90, 64, 72, 256, 2), (1500, 513, 384, 20, 7), (2100, 1024, 640, 16, 3),
          (5000, 8, 16, 5, 100)]
+# enough tiles and columns for the waves of a block to take columns of their own, forward and backward
+LARGE = [(700, 72, 12100, 12, 3), (700, 12100, 72, 20, 3), (650, 72, 12104, 48, 2), (650, 12104, 72, 64, 2)]
 PAIRS = [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")]
 
 
 @pytest.mark.parametrize("dt,od", PAIRS)
-@pytest.mark.parametrize("T,K,N,r,n", SIZES)
+@pytest.mark.parametrize("T,K,N,r,n", SIZES + LARGE)
 def test_forward(T, K, N, r, n, dt, od):
     say(f"case: adapters forward T {T} K {K} N {N} r {r} n {n} {dt} out {od}")
     q = make(T, K, N, r, n, dt, od)
@@ -52,7 +54,7 @@ def test_forward(T, K, N, r, n, dt, od):
 
 
 @pytest.mark.parametrize("dt,od", PAIRS)
-@pytest.mark.parametrize("T,K,N,r,n", SIZES)
+@pytest.mark.parametrize("T,K,N,r,n", SIZES + LARGE)
 def test_backward(T, K, N, r, n, dt, od):
     say(f"case: adapters backward T {T} K {K} N {N} r {r} n {n} {dt} out {od}")
     q = make(T, K, N, r, n, dt, od, seed=50)
@@ -139,6 +141,23 @@ def test_infinities_stay_in_their_rows(T, dt):
     assert torch.equal(out[keep], clean[keep]) and torch.equal(dx[keep], dx0[keep])
     others = torch.arange(3, device="cuda") != int(q["ids"][7])
     assert torch.equal(dd[others], dd0[others]) and torch.equal(du[others], du0[others])
+
+
+@pytest.mark.parametrize("T", [10, 100])
+def test_fp16_subnormals(T):
+    """Adapters of fp16's smallest numbers, as they are early in training, keep their products."""
+    K, N, r, n = 256, 64, 16, 2
+    q = make(T, K, N, r, n, "f16", "f16", none=0)
+    q["down"], q["up"] = rand(1, n, r, K, std=1e-6).half(), rand(2, n, N, r, std=1e-6).half()
+    q["dout"], q["res_x"] = rand(3, T, N, std=1e-6).half(), None
+    layer = LowRankAdapters(q["down"], q["up"], q["scale"])
+    _, q["h"] = layer.forward(q["x"], q["ids"], save=True)
+    R.check("h", q["h"], TR.adapters_forward(q, torch.float16, torch.float16)["h"])
+    q["h"] = q["h"] * 1e3
+    back = TR.adapters_backward(q, torch.float16, torch.float32)
+    _, dd, du = layer.backward(q["x"], q["ids"], q["h"], q["dout"], w_grad_dtype=torch.float32)
+    R.check("ddown", dd, back["ddown"])
+    R.check("dup", du, back["dup"])
 
 
 def test_gradient_against_differences():

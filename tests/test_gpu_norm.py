@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 # (tokens, d): rows of one element, off the vector width, around each length where another kernel takes over
 SIZES = [(1, 1), (3, 7), (2, 8), (5, 31), (4, 33), (1, 512), (9, 513), (6, 1000), (3, 1024), (5, 1025), (2, 2048), (7, 2731),
          (1, 4096), (33, 4096), (4, 4100), (3, 8192), (2, 8200), (3, 16384), (2, 16385), (1, 16392), (2, 40007), (517, 64),
-         (1100, 129), (2, 16400)]
+         (1100, 129), (2, 16400), (9000, 24)]
 EPS = 1e-6
 
 

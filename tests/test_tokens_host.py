@@ -243,3 +243,11 @@ def test_adapter_counts_strides_and_workspace():
     assert ctypes.sizeof(ecf.AdapterArgs) == 224
     with pytest.raises(ValueError):
         ly.LowRankAdapters(torch.zeros(2, 4, 8), torch.zeros(2, 8, 4))  # not on the GPU
+
+
+def test_8_bits_stay_out_of_the_other_operators():
+    for w, a in ((ecf.ECF_MXFP8, ecf.ECF_BF16), (ecf.ECF_BF16, ecf.ECF_MXFP8), (ecf.ECF_MXFP8, ecf.ECF_MXFP8)):
+        with pytest.raises(ecf.EcfError):
+            ecf.ecf_expert_bytes(ecf.make_shape(256, 64, 4, 2, w, a))
+    with pytest.raises(ecf.EcfError):
+        ecf.ecf_linear_workspace_bytes(64, 32, ecf.ECF_MXFP8, 4)
