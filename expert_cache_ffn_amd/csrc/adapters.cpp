@@ -47,7 +47,9 @@ Workspace workspace(int32_t K, int32_t N, int32_t r, int32_t n, int32_t T, bool 
         w.sort_bytes = sort_ws(T, n);
         w.sort = take(w.sort_bytes);
     }
-    w.part = take((size_t)shrink_rows(T) * r * 4);
+    // (a size query does not know the type: what holds for the widest holds for all)
+    if (!few || !adapter_few_in_one(T, K, N, r, 4))
+        w.part = take((size_t)shrink_rows(T) * r * 4);
     if (backward) {
         w.g = take((size_t)T * r * 4);
         w.slots_a = take(outer_slots(outer_chunks(T, outer_slices(K)), K, r));
@@ -129,10 +131,10 @@ int ecf_adapter_forward(const ecf_adapter_args *a, int32_t T)
             ECF_TRY(check_rows(me, "d_residual", a->d_residual, ldres, N, a->out_dtype));
         const Workspace w = workspace(a->in_features, a->out_features, a->rank, a->n_adapters, T, false);
         ECF_TRY(check_ws(me, a->d_ws, a->ws_bytes, w.total));
-        ECF_TRY(check_apart(me, {{"d_out", a->d_out}, {"d_h", a->d_h}, {"d_ws", a->d_ws}},
+        ECF_TRY(check_apart(me, {{"d_out", a->d_out}, {"d_h", a->d_h}, {"d_ws", w.total ? a->d_ws : nullptr}},
                             {{"d_x", a->d_x}, {"d_a", a->d_a}, {"d_b", a->d_b}, {"d_scale", a->d_scale}, {"d_idx", a->d_idx},
                              {"d_order", a->d_order}, {"d_offsets", a->d_offsets}, {"d_tiles", a->d_tiles}}));
-        ECF_TRY(check_apart(me, {{"d_h", a->d_h}, {"d_ws", a->d_ws}}, {{"d_residual", a->d_residual}}));
+        ECF_TRY(check_apart(me, {{"d_h", a->d_h}, {"d_ws", w.total ? a->d_ws : nullptr}}, {{"d_residual", a->d_residual}}));
         ECF_TRY(check_same_stride(me, "d_out", a->d_out, ldout, "d_residual", a->d_residual, ldres));
         hipStream_t st = (hipStream_t)a->stream;
         const bool few = T <= kAdapterFew;
@@ -155,6 +157,8 @@ int ecf_adapter_forward(const ecf_adapter_args *a, int32_t T)
         e.h = a->d_h;
         e.residual = a->d_residual, e.ldres = ldres;
         e.out = a->d_out, e.ldout = ldout;
+        if (few && adapter_few_in_one(T, K, N, a->rank, 4))
+            return launch_few(s, e, st);
         ECF_TRY(few ? launch_few_shrink(s, st) : launch_shrink(s, st));
         return few ? launch_few_expand(e, st) : launch_expand(e, st);
     });

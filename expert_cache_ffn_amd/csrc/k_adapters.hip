@@ -451,6 +451,75 @@ __device__ __forceinline__ int adapter_at(const AdapterOrder &o, int t)
     return a >= 0 && a < o.n ? (int)a : -1;
 }
 
+// Both products in one launch where a token's A is small: every block of a token makes h
+// itself.  grid: slices of 1024 columns, tokens; sixteen waves share the ranks (fewer ranks: K
+// too), then a thread has a column.  What a column needs of B and the residual is on its way
+// meanwhile.  (16 tokens, 4096 to 4096, rank 16, bf16: a call 7.7 us, 11.1 with two kernels; at rank 64,
+// where a block reads 512 KB of A, 17.8 against 10.9.)
+template <class E, class O, bool FULL, bool RFULL>
+__global__ __launch_bounds__(1024) void k_few(ShrinkCall c, ExpandCall x)
+{
+    __shared__ float sums[256 + 16], h[256 + 8];
+    const int t = blockIdx.y, tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = blockIdx.x * kFewCols + tid, a = adapter_at(c.o, t);
+    const bool none = a < 0, in = n < x.N;
+    const float scale = none ? 0.f : scale_of(x.scale, a);
+    const typename E::raw *up = (const typename E::raw *)x.m + ((int64_t)max(a, 0) * x.N + min(n, x.N - 1)) * c.r;
+    Raw8<E> first[2];
+    float y = 0.f;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        first[q] = row8<E, RFULL>(up, 8 * q, c.r);
+    if (x.residual && in)
+        y = O::to_f(((const typename O::raw *)x.residual)[t * x.ldres + n]);
+    // parts waves a rank
+    const int parts = c.r > 8 ? 1 : c.r > 4 ? 2 : c.r > 2 ? 4 : c.r > 1 ? 8 : 16, ranks = 16 / parts;
+    if (!none)
+        for (int j = w / parts; j < c.r; j += ranks) {
+            const typename E::raw *m = (const typename E::raw *)c.m + ((int64_t)a * c.r + j) * c.K;
+            const typename E::raw *xr = (const typename E::raw *)c.x + (int64_t)t * c.ldx;
+            float s = 0.f;
+#pragma unroll 4
+            for (int k = (w % parts * 64 + lane) * 8; k < c.K; k += parts * 512) {
+                float u[8], v[8];
+                const Raw8<E> mr = row8<E, FULL>(m, k, c.K), xv = row8<E, FULL>(xr, k, c.K);
+                widen8<E>(mr, u);
+                widen8<E>(xv, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    s = fmaf(u[i], v[i], s);
+            }
+            s = wave_sum_f32(s);
+            if (lane == 0)
+                sums[j * parts + w % parts] = s;
+        }
+    __syncthreads();
+    for (int j = tid; j < (c.r + 7) / 8 * 8; j += 1024) {
+        float v = 0.f;
+        if (!none && j < c.r)
+            for (int q = 0; q < parts; ++q)
+                v += sums[j * parts + q];
+        h[j] = v;
+        if (x.h && blockIdx.x == 0 && j < c.r)
+            x.h[(int64_t)t * c.r + j] = v;
+    }
+    __syncthreads();
+    if (!in)
+        return;
+    if (!none) {
+        float s = 0.f;
+        for (int j = 0; j < c.r; j += 8) {
+            float u[8];
+            widen8<E>(j == 0 ? first[0] : j == 8 ? first[1] : row8<E, RFULL>(up, j, c.r), u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s = fmaf(u[i], h[j + i], s);
+        }
+        y += scale * s;
+    }
+    ((typename O::raw *)x.out)[t * x.ldout + n] = O::from_f(y);
+}
+
 // grid: ranks, tokens; the four waves share K
 template <class E, bool FULL>
 __global__ __launch_bounds__(256) void k_few_shrink(ShrinkCall c)
@@ -820,6 +889,22 @@ int launch_expand(const ExpandCall &c, hipStream_t st)
                 constexpr bool RFULL = decltype(rfull)::value;
                 with_pair(c.dtype, c.out_dtype, [&](auto e, auto o) { expand_of<decltype(e), decltype(o), false, FULL, RFULL>(c, st); });
             });
+    });
+    ECF_HIP_CHECK(hipGetLastError());
+    return ECF_OK;
+}
+
+int launch_few(const ShrinkCall &c, const ExpandCall &x, hipStream_t st)
+{
+    ProfScope prof("adapter_few", st);
+    const dim3 grid((x.N + kFewCols - 1) / kFewCols, c.o.T);
+    with_bool(c.K % 8 == 0, [&](auto full) {
+        with_bool(c.r % 8 == 0, [&](auto rfull) {
+            with_pair(x.dtype, x.out_dtype, [&](auto e, auto o) {
+                hipLaunchKernelGGL((k_few<decltype(e), decltype(o), decltype(full)::value, decltype(rfull)::value>), grid, dim3(1024),
+                                   0, st, c, x);
+            });
+        });
     });
     ECF_HIP_CHECK(hipGetLastError());
     return ECF_OK;

@@ -127,7 +127,14 @@ struct ExpandCall {
 };
 int launch_expand(const ExpandCall &c, hipStream_t st);
 
-// Both for few tokens, in any order; h as above, between the two kernels.
+// Few tokens, in any order: both in one launch, without a workspace, or with h between two kernels.
+constexpr int kFewCols = 1024;                // columns per block of the one
+constexpr int64_t kFewBytes = (int64_t)1 << 18;  // of a token's A in fp32, which each of its blocks reads
+inline bool adapter_few_in_one(int64_t T, int64_t K, int64_t N, int64_t r, int esize)
+{
+    return T <= kAdapterFew && T * ((N + kFewCols - 1) / kFewCols) <= 256 && r * K * esize <= kFewBytes;
+}
+int launch_few(const ShrinkCall &c, const ExpandCall &x, hipStream_t st);
 int launch_few_shrink(const ShrinkCall &c, hipStream_t st);
 int launch_few_expand(const ExpandCall &c, hipStream_t st);
 

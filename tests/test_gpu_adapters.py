@@ -23,12 +23,12 @@ def make(T, K, N, r, n, dt, od, seed=0, none=0.15):
                 residual=rand(seed + 5, T, N, dtype=ot), dout=rand(seed + 6, T, N, std=0.1, dtype=ot), res_x=rand(seed + 7, T, K, std=0.1, dtype=dtype))
 
 
-# (tokens, K, N, rank, adapters): single tokens and elements, both sides of the few tokens, ranks off the MFMA's 16 and
+# (tokens, K, N, rank, adapters): single tokens and elements, both sides of the few tokens (in one launch and in two), ranks off the MFMA's 16 and
 # over 64, many adapters of few tokens, one adapter of many, widths around every slice and chunk
 SIZES = [(1, 1, 1, 1, 1), (1, 4096, 4096, 16, 64), (3, 7, 5, 3, 2), (16, 1000, 130, 16, 64), (64, 256, 264, 8, 3), (65, 64, 64, 4, 2),
          (66, 130, 257, 16, 40), (128, 128, 256, 32, 1), (200, 136, 72, 33, 5), (300, 520, 1030, 64, 4), (257, 1330, 300, 12, 1024),
          (700, 264, 136, 1, 9), (129, 300, 265, 100, 3), (90, 64, 72, 256, 2), (1500, 513, 384, 20, 7), (2100, 1024, 640, 16, 3),
-         (5000, 8, 16, 5, 100)]
+         (5000, 8, 16, 5, 100), (40, 8200, 70, 12, 3), (64, 64, 5000, 8, 2), (7, 120, 1100, 2, 4), (9, 2000, 40, 6, 2)]
 # enough tiles and columns for the waves of a block to take columns of their own, forward and backward
 LARGE = [(700, 72, 12100, 12, 3), (700, 12100, 72, 20, 3), (650, 72, 12104, 48, 2), (650, 12104, 72, 64, 2)]
 PAIRS = [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")]

@@ -208,7 +208,7 @@ def test_adapter_backward_refusals(bad):
 
 
 @pytest.mark.parametrize("fn,out,others", [
-    (ecf.ecf_adapter_forward, "d_out", ("d_x", "d_a", "d_b", "d_scale", "d_idx", "d_order", "d_offsets", "d_tiles", "d_h", "d_ws")),
+    (ecf.ecf_adapter_forward, "d_out", ("d_x", "d_a", "d_b", "d_scale", "d_idx", "d_order", "d_offsets", "d_tiles", "d_h")),
     (ecf.ecf_adapter_forward, "d_h", ("d_x", "d_residual")),
     (ecf.ecf_adapter_backward, "d_dx", ("d_x", "d_a", "d_dout", "d_h", "d_da", "d_db", "d_ws")),
     (ecf.ecf_adapter_backward, "d_db", ("d_b", "d_dout", "d_residual", "d_da", "d_order"))])
@@ -224,12 +224,15 @@ def test_adapter_counts_strides_and_workspace():
         refused(fn, adapter(), T=-1)
         refused(fn, adapter(), T=(1 << 22) + 1)
         refused(fn, adapter(ws_bytes=100), T=100, code=ecf.ECF_ENOSPC)
+        refused(fn, adapter(d_ws=adapter().d_x), T=100, match="256-byte|same memory")
         refused(fn, adapter(d_ws=A + 128), T=100)
         assert getattr(ecf.lib(), fn.__name__)(None, 4) == ecf.ECF_EINVAL
     refused(ecf.ecf_adapter_forward, adapter(ld_out=1 << 31), code=ecf.ECF_EUNSUPPORTED)
     refused(ecf.ecf_adapter_forward, adapter(d_out=9 * A, d_residual=9 * A, ld_out=40, ld_residual=48), match="stride")
     refused(ecf.ecf_adapter_backward, adapter(d_dx=9 * A, d_residual=9 * A, ld_dx=72, ld_residual=80), match="stride")
     ecf.ecf_adapter_forward(adapter(d_x=0, d_out=0, d_idx=0), 0)
+    # a decode batch of small adapters needs no buffer
+    assert ecf.ecf_adapter_workspace_bytes(4096, 4096, 16, 64, 16) == 0 < ecf.ecf_adapter_workspace_bytes(4096, 4096, 64, 64, 16)
     for bad in ((0, 32, 8, 4, 10), (64, 32, 300, 4, 10), (64, 32, 8, 4, -1)):
         with pytest.raises(ecf.EcfError):
             ecf.ecf_adapter_workspace_bytes(*bad)
