@@ -229,7 +229,7 @@ __global__ __launch_bounds__(256) void k_shrink(ShrinkCall c)
 }
 
 // ---- expand ----------------------------------------------------------------------------
-// grid: tiles, slices of 512 columns.  h of the tile's 64 tokens lies in LDS; a wave has 128
+// grid: tiles times slices of 512 columns, a tile's next to each other.  h of its 64 tokens lies in LDS; a wave has 128
 // columns: row m of MFMA e is column 32 (m % 4) + 8 (m / 4) + e, so that the eight MFMAs leave
 // a lane four times eight columns in a row, next to those of the lanes of the same token
 // (a lane with 32 in a row stores a quarter of each 64 bytes at a time: 4096 tokens of 4096
@@ -312,7 +312,9 @@ __global__ __launch_bounds__(256, (kExpandWaves<E, O, SETS>)) void k_expand(Expa
     typedef typename std::conditional<BF, uint16_t, float>::type hraw;
     extern __shared__ __align__(16) char smem[];
     hraw *hl = (hraw *)smem;
-    const Tile tl = tile_of(c.o, blockIdx.x);
+    const int slices = !c.out ? 1 : SPREAD ? (c.N + 127) / 128 : (c.N + kCols - 1) / kCols;
+    const int tile = blockIdx.x / slices, slice = blockIdx.x % slices;
+    const Tile tl = tile_of(c.o, tile);
     if (tl.rows <= 0)
         return;
     const ExpandShape sh = expand_shape<BF, PARTS>(c.r);
@@ -322,7 +324,7 @@ __global__ __launch_bounds__(256, (kExpandWaves<E, O, SETS>)) void k_expand(Expa
     const int a = none ? 0 : tl.a;
     const float scale = none ? 0.f : scale_of(c.scale, a);
     const typename E::raw *m = (const typename E::raw *)c.m + (int64_t)a * c.r * c.N;
-    const int c0 = SPREAD ? blockIdx.y * 128 : blockIdx.y * kCols + w * 128;
+    const int c0 = SPREAD ? slice * 128 : slice * kCols + w * 128;
     const bool on = c.out && c0 < c.N;
     // the tokens of this wave's 16s, and their residuals, on their way while h is made
     constexpr int NB = SPREAD ? 1 : 4;
@@ -349,30 +351,55 @@ __global__ __launch_bounds__(256, (kExpandWaves<E, O, SETS>)) void k_expand(Expa
             for (int q = 0; q < SETS; ++q)
                 held[q] = operands<E, OF_A, FULL, RFULL, HALF>(c, m, mcol, rank_of(q));
     }
-    // h of the tile's tokens: the splits' sum, written out once
-    for (int i = tid; i < kTileRows * sh.rp; i += 256) {
-        const int row = i / sh.rp, j = i - row * sh.rp;
-        float v = 0.f;
+    // h of the tile's tokens, four ranks at a time: the splits' sum, written out once
+    const int quads = sh.rp / 4;
+    for (int i = tid; i < kTileRows * quads; i += 256) {
+        const int row = i / quads, j = (i - row * quads) * 4;
+        f32x4a v = {0.f, 0.f, 0.f, 0.f};
         if (row < tl.rows && j < c.r) {
             if (!none) {
-                float p[kShrinkSplits];
+                f32x4a p[kShrinkSplits];
+#pragma unroll
+                for (int s = 0; s < kShrinkSplits; ++s) {
+                    const float *at = c.part + (min(s, c.splits - 1) * (int64_t)c.o.T + tl.row0 + row) * c.r + j;
+                    if (c.r % 4 == 0)
+                        p[s] = *(const f32x4a *)at;
+                    else
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            p[s][q] = at[min(q, c.r - 1 - j)];
+                }
 #pragma unroll
                 for (int s = 0; s < kShrinkSplits; ++s)
-                    p[s] = c.part[(min(s, c.splits - 1) * (int64_t)c.o.T + tl.row0 + row) * c.r + j];
 #pragma unroll
-                for (int s = 0; s < kShrinkSplits; ++s)
-                    v += s < c.splits ? p[s] : 0.f;
+                    for (int q = 0; q < 4; ++q)
+                        v[q] += s < c.splits && j + q < c.r ? p[s][q] : 0.f;
             }
-            if (c.h && blockIdx.y == 0)
-                c.h[(int64_t)c.o.order[tl.row0 + row] * c.r + j] = c.scaled ? v * scale : v;
-            v *= scale;
+            if (c.h && slice == 0) {
+                float *at = c.h + (int64_t)c.o.order[tl.row0 + row] * c.r + j;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (j + q < c.r)
+                        at[q] = c.scaled ? v[q] * scale : v[q];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[q] *= scale;
         }
+        hraw *at = hl + row * sh.pitch + j;
         if constexpr (BF) {
 #pragma unroll
             for (int p = 0; p < PARTS; ++p)
-                hl[row * sh.pitch + p * sh.rp + j] = bf16_part(v);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float left = v[q];
+                    at[p * sh.rp + q] = bf16_part(left);
+                    v[q] = left;
+                }
         } else {
-            hl[row * sh.pitch + j] = v;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                at[q] = v[q];
         }
     }
     if constexpr (BF) {  // the parts end in a whole step
@@ -820,7 +847,7 @@ void expand_of(const ExpandCall &c, hipStream_t st)
     // fewer than a block a CU: the columns in four times as many slices
     const int tiles = most_tiles(c.o), slices = (c.N + kCols - 1) / kCols;
     const bool spread = c.out && c.r <= 64 && (c.o.T / kTileRows + 1) * slices < 256;
-    const dim3 grid(tiles, !c.out ? 1 : spread ? (c.N + 127) / 128 : slices);
+    const dim3 grid(tiles * (!c.out ? 1 : spread ? (c.N + 127) / 128 : slices));
     const size_t lds = (size_t)kTileRows * expand_shape<BF, PARTS>(c.r).pitch * (BF ? 2 : 4);
     with_bool(spread, [&](auto sp) {
         constexpr bool SP = decltype(sp)::value;

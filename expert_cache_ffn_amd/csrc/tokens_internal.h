@@ -98,7 +98,7 @@ struct ShrinkCall {
     float *part;
     int splits, split_k;  // split_k: k per split, a multiple of 128
 };
-constexpr int kShrinkBlocks = 1024, kShrinkSplits = 8;
+constexpr int kShrinkBlocks = 1024, kShrinkSplits = 7;
 int shrink_splits(int T, int K);
 // Rows of h in all splits of any call of up to T tokens.
 inline int64_t shrink_rows(int64_t T)
