@@ -11,10 +11,10 @@
 // x, the residual and the output are read and written once, which bounds all of them; the
 // matrices are shared by 64 tokens (by a run of them) and come from the caches.  Measured in
 // bf16 (a large copy takes 5.0 TB/s): 4096 tokens, 4096 to 4096, rank 16, 8 adapters: shrink
-// 13.5 us (2.5 TB/s: few chunks a block behind the chain tiles - order - x), expand 22.5 (3.0:
+// 12.5 us (2.7 TB/s: few chunks a block behind the chain tiles - order - x), expand 20 (3.3:
 // all blocks run at once, first all load, then all store); 8192 tokens, 2048 / 4096, rank 32:
-// shrink of dout 20 (3.4), expand to dx 25 (2.7), both outer products 34 (2.9) and 7 for their
-// join; 16 tokens of 16 adapters 3.0 + 3.7 us.
+// shrink of dout 20 (3.4), expand to dx 21.5 (3.1), both outer products 34 (2.9) and 7 for their
+// join; 16 tokens of 16 adapters 6.6 us in one kernel.
 //
 // What lies between shrink and expand (h, in the backward pass g) stays in fp32.  As an operand
 // of a bf16 product it is split into two bf16 parts (16 bits in all; three parts, so all 24
@@ -876,8 +876,8 @@ void outer_of(const OuterPair &p, int slices, int chunks, hipStream_t st)
 
 }  // namespace
 
-// Splits of K: two blocks a CU where there are few tiles, 256 of K each at least, at most 8
-// (each adds a part of h that every block of the expand reads).
+// Splits of K: up to four blocks a CU where there are few tiles, 256 of K each at least, at most
+// 7 (each adds a part of h that every block of the expand reads).
 int shrink_splits(int T, int K)
 {
     int s = kShrinkBlocks / (T / kTileRows + 1);

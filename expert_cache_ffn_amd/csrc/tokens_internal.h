@@ -98,7 +98,7 @@ struct ShrinkCall {
     float *part;
     int splits, split_k;  // split_k: k per split, a multiple of 128
 };
-constexpr int kShrinkBlocks = 1024, kShrinkSplits = 7;
+constexpr int kShrinkBlocks = 1024, kShrinkSplits = 7;  // (72 tiles of 64 tokens, K 4096: 12.1 us, 13.5 with 8, 24 with 2)
 int shrink_splits(int T, int K);
 // Rows of h in all splits of any call of up to T tokens.
 inline int64_t shrink_rows(int64_t T)
