@@ -300,6 +300,8 @@ __device__ __forceinline__ Operands<E> operands(const ExpandCall &c, const typen
     return o;
 }
 
+// Three blocks a CU where that costs no spills (146 + 32 registers without, two blocks: 4096 tokens
+// 25.9 against 23.3 us).
 template <class E, class O, int SETS>
 constexpr int kExpandWaves = std::is_same<E, BF16>::value && std::is_same<O, BF16>::value && SETS == 1 ? 3 : 1;
 
@@ -794,35 +796,6 @@ __global__ __launch_bounds__(256) void k_outer_join(OuterPair two)
 }
 
 // ---- launches --------------------------------------------------------------------------
-
-template <class F>
-void with_element(int dtype, F f)
-{
-    if (dtype == ECF_F32)
-        f(F32{});
-    else if (dtype == ECF_BF16)
-        f(BF16{});
-    else
-        f(F16{});
-}
-template <class F>
-void with_pair(int dtype, int other, F f)
-{
-    with_element(dtype, [&](auto e) {
-        if (other == ECF_F32)
-            f(e, F32{});
-        else
-            f(e, e);
-    });
-}
-template <class F>
-void with_bool(bool b, F f)
-{
-    if (b)
-        f(std::true_type{});
-    else
-        f(std::false_type{});
-}
 
 int most_tiles(const AdapterOrder &o) { return o.T / kTileRows + (o.n + 1 < o.T ? o.n + 1 : o.T); }
 int rank_blocks(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }

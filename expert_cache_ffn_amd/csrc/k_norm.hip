@@ -447,18 +447,6 @@ void backward_of(const NormCall &c, const NormPlan &p, int parts, hipStream_t st
 #undef ECF_NORM
 }
 
-template <class F>
-void with_types(const NormCall &c, F f)
-{
-    const bool wide = c.sum_dtype == ECF_F32;
-    if (c.dtype == ECF_F32)
-        f(F32{}, F32{});
-    else if (c.dtype == ECF_BF16)
-        wide ? f(BF16{}, F32{}) : f(BF16{}, BF16{});
-    else
-        wide ? f(F16{}, F32{}) : f(F16{}, F16{});
-}
-
 }  // namespace
 
 // Twice as many for short rows of many tokens, whose groups of threads are small (8192 tokens in bf16: 1024 elements 27.6
@@ -475,7 +463,7 @@ int launch_norm_forward(const NormCall &c, hipStream_t st)
 {
     ProfScope prof("norm", st);
     const NormPlan p = norm_plan(c.d);
-    with_types(c, [&](auto e, auto s) {
+    with_pair(c.dtype, c.sum_dtype, [&](auto e, auto s) {
         using E = decltype(e);
         using S = decltype(s);
         if (c.d % 8 == 0)
@@ -493,7 +481,7 @@ int launch_norm_backward(const NormCall &c, hipStream_t st)
     const int parts = norm_partial_rows(c.T, c.d);
     if (c.T > 0 && (c.dx || c.ds || c.dweight)) {
         const NormPlan p = norm_plan(c.d);
-        with_types(c, [&](auto e, auto s) {
+        with_pair(c.dtype, c.sum_dtype, [&](auto e, auto s) {
             using E = decltype(e);
             using S = decltype(s);
             if (c.d % 8 == 0)

@@ -398,40 +398,11 @@ void with_shift(int d, F f)
     else
         f(std::integral_constant<int, 8>{});
 }
-template <class F>
-void with_bool(bool b, F f)
-{
-    if (b)
-        f(std::true_type{});
-    else
-        f(std::false_type{});
-}
 
 dim3 token_grid(const MoveCall &c, int shift)
 {
     const int per = 256 >> shift, cols = 8 << shift;
     return dim3((unsigned)((c.T + per - 1) / per), (unsigned)((c.d + cols - 1) / cols));
-}
-
-template <class F>
-void with_element(int dtype, F f)
-{
-    if (dtype == ECF_F32)
-        f(F32{});
-    else if (dtype == ECF_BF16)
-        f(BF16{});
-    else
-        f(F16{});
-}
-template <class F>
-void with_pair(const MoveCall &c, F f)
-{
-    with_element(c.dtype, [&](auto e) {
-        if (c.token_dtype == ECF_F32)
-            f(e, F32{});
-        else
-            f(e, e);
-    });
 }
 
 }  // namespace
@@ -492,7 +463,7 @@ int launch_dispatch(const MoveCall &c, hipStream_t st)
 int launch_combine_tokens(const MoveCall &c, hipStream_t st)
 {
     ProfScope prof("token_combine", st);
-    with_pair(c, [&](auto e, auto o) {
+    with_pair(c.dtype, c.token_dtype, [&](auto e, auto o) {
         with_bool(c.d % 8 == 0, [&](auto full) {
             with_shift(c.d, [&](auto shift) {
                 using E = decltype(e);
@@ -522,7 +493,7 @@ int launch_combine_backward(const MoveCall &c, hipStream_t st)
 {
     ProfScope prof("token_combine_backward", st);
     // a wave per choice, or 8 or 32 lanes where they hold its row
-    with_pair(c, [&](auto e, auto o) {
+    with_pair(c.dtype, c.token_dtype, [&](auto e, auto o) {
         with_bool(c.d % 8 == 0, [&](auto full) {
             using E = decltype(e);
             using O = decltype(o);

@@ -158,4 +158,36 @@ __device__ __forceinline__ uint32_t mx_pack4(const float v[4])
     return (uint32_t)r;
 }
 
+// ---- launches: a call of f with types and constants for values -------------------------
+
+template <class F>
+void with_element(int dtype, F f)
+{
+    if (dtype == ECF_F32)
+        f(F32{});
+    else if (dtype == ECF_BF16)
+        f(BF16{});
+    else
+        f(F16{});
+}
+// dtype and another, which is it or ECF_F32
+template <class F>
+void with_pair(int dtype, int other, F f)
+{
+    with_element(dtype, [&](auto e) {
+        if (other == ECF_F32)
+            f(e, F32{});
+        else
+            f(e, e);
+    });
+}
+template <class F>
+void with_bool(bool b, F f)
+{
+    if (b)
+        f(std::true_type{});
+    else
+        f(std::false_type{});
+}
+
 }  // namespace ecf

@@ -538,7 +538,9 @@ class TokenSort(_Tokens):
     [n_experts + 2] (first tile of 64 rows of each expert) are int32 tensors on the ids'
     device, made by the constructor's call on the current stream.  The experts between
     dispatch() and combine() are the caller's: GatedProjection and Linear over the
-    rows of each."""
+    rows of each.  The tables belong to the stream that made them, as any tensor of torch's
+    allocator: where work on another stream reads them, keep the object until it is done.
+    ids are read again by LowRankAdapters: they stay as they are while the object is used."""
 
     def __init__(self, ids, n_experts):
         if not isinstance(ids, torch.Tensor) or ids.dim() not in (1, 2) or not ids.is_cuda:
