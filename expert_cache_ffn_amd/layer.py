@@ -593,7 +593,7 @@ class TokenSort(_Tokens):
         return self._part(self._s.d_place, self.tokens * self.top_k).view(self.tokens, self.top_k)
 
     def _weights(self, w):
-        if not isinstance(w, torch.Tensor) or w.numel() != self.tokens * self.top_k or w.dtype is not torch.float32 \
+        if not isinstance(w, torch.Tensor) or w.shape != (self.tokens, self.top_k) or w.dtype is not torch.float32 \
                 or w.device != self.device or not w.is_contiguous():
             raise ValueError(f"weights must be a contiguous float32 tensor [{self.tokens}, {self.top_k}] on {self.device}")
         return w.data_ptr()

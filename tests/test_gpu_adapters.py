@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import dense_ref as R
+import expert_cache_ffn_amd as ecf
 import tokens_ref as TR
 from expert_cache_ffn_amd.layer import GatedProjection, Linear, LowRankAdapters, RMSNorm, TokenSort
 from gpu_util import say
@@ -223,6 +224,29 @@ def test_long_offsets():
     dx, _, _ = layer.backward(q["x"], q["ids"], h, y, need_dw=False)
     tail |= {"dout": y[-40:], "h": h[-40:], "res_x": None}
     R.check("dx", dx[-40:], TR.adapters_backward(tail, torch.bfloat16, torch.bfloat16)["dx"])
+
+
+def test_refusals():
+    q = make(70, 16, 24, 4, 3, "f32", "f32")
+    layer = LowRankAdapters(q["down"], q["up"], q["scale"])
+    x, ids = q["x"], q["ids"]
+    h = torch.zeros(70, 4, device="cuda")
+    bad = [lambda: LowRankAdapters(q["down"][0], q["up"]), lambda: LowRankAdapters(q["down"], q["up"][:2]),
+           lambda: LowRankAdapters(q["down"], q["up"].bfloat16()), lambda: LowRankAdapters(q["down"][:, :, ::2], q["up"]),
+           lambda: LowRankAdapters(q["down"], q["up"], q["scale"].double()),
+           lambda: LowRankAdapters(q["down"], q["up"], out_dtype=torch.float16), lambda: layer.forward(x, ids[:69]),
+           lambda: layer.forward(x, ids.float()), lambda: layer.forward(x, None), lambda: layer.forward(x, TokenSort(ids, 4)),
+           lambda: layer.forward(x, TokenSort(ids[:69], 3)), lambda: layer.forward(x[:, :8], ids),
+           lambda: layer.forward(x, ids, residual=q["residual"][:, :8]), lambda: layer.backward(x, ids, h[:, :3], q["dout"]),
+           lambda: layer.backward(x, ids, None, q["dout"]), lambda: layer.backward(x, ids, h, q["dout"], need_dx=False, dx=x)]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            raise AssertionError(f"call {i} was not refused")
+    with pytest.raises(ecf.EcfError):
+        LowRankAdapters(torch.zeros(1, 300, 8, device="cuda"), torch.zeros(1, 8, 300, device="cuda"))
+    with pytest.raises(ecf.EcfError):  # dx onto x
+        layer.backward(x, ids, h, q["dout"], dx=x)
 
 
 def test_a_layer_of_all_of_them():

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import dense_ref as R
+import expert_cache_ffn_amd as ecf
 import tokens_ref as TR
 from expert_cache_ffn_amd.layer import RMSNorm, TokenSort
 from gpu_util import say
@@ -218,3 +219,27 @@ def test_graph():
                 assert torch.equal(p, q)
         T = 3000
         ids, x, gates, y = choices(1, T, k, E), rand(1, T, d), rand(2, T, k), rand(3, T * k, d)
+
+
+def test_refusals():
+    """What the Python side turns down before any call."""
+    ids = choices(1, 6, 2, 4)
+    s = TokenSort(ids, 4)
+    x, rows, w = rand(1, 6, 16), rand(2, 12, 16), rand(3, 6, 2)
+    bad = [lambda: TokenSort(ids.float(), 4), lambda: TokenSort(ids[:, :1].expand(6, 2), 4), lambda: TokenSort(ids[None], 4),
+           lambda: s.dispatch(x[:5]), lambda: s.dispatch(x.double()), lambda: s.dispatch(x, dtype=torch.bfloat16),
+           lambda: s.dispatch(x, scale=w), lambda: s.dispatch(x.cpu()), lambda: s.dispatch(x, out=rows[:11]),
+           lambda: s.combine(rows[:11]), lambda: s.combine(rows, w.t().contiguous()), lambda: s.combine(rows, w.bfloat16()),
+           lambda: s.combine(rows, w.view(-1)), lambda: s.combine(rows, torch.cat([w, w], 1)[:, :2]),
+           lambda: s.combine(rows, out_dtype=torch.bfloat16), lambda: s.combine(rows, residual=x[:, :8]),
+           lambda: s.combine_backward(rows, w, x.bfloat16()), lambda: s.combine_backward(rows, w, x[:5]),
+           lambda: RMSNorm(x), lambda: RMSNorm(x[0], eps=-1.0), lambda: RMSNorm(x[0], sum_dtype=torch.bfloat16),
+           lambda: RMSNorm(x[0]).forward(x, y=False), lambda: RMSNorm(x[0]).forward(x, sum_out=x),
+           lambda: RMSNorm(x[0]).backward(x, None, x), lambda: RMSNorm(x[0]).backward(x, x[:, 0].contiguous(), x, ds=x, need_dx=False)]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            raise AssertionError(f"call {i} was not refused")
+    for call in (lambda: TokenSort(ids, 0), lambda: TokenSort(ids, 1025), lambda: s.combine(rows, out=rows[:6])):
+        with pytest.raises(ecf.EcfError):
+            call()
