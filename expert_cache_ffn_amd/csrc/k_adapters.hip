@@ -17,8 +17,9 @@
 // join; 16 tokens of 16 adapters 6.6 us in one kernel.
 //
 // What lies between shrink and expand (h, in the backward pass g) stays in fp32.  As an operand
-// of a bf16 product it is split into two bf16 parts (16 bits in all; three parts, so all 24
-// bits, where the output is fp32); fp16 and fp32 take fp32 products there, whose rate the
+// of a bf16 product it is split into three bf16 parts, all its 24 bits, whatever the output's
+// type: two parts lose what is left where a residual or another token cancels most of the
+// product, and cost about as much.  fp16 and fp32 take fp32 products there, whose rate the
 // memory still hides at ranks up to 32.
 #include "tokens_device.h"
 
@@ -32,6 +33,7 @@ constexpr int kKC = 128;   // k per staged chunk of a shrink
 constexpr int kRC = 64;    // most ranks at a time
 constexpr int kCols = 512; // columns per block of an expand
 constexpr int kOuterCols = 128;
+constexpr int kParts = 3;  // bf16 values that hold an fp32 one
 
 struct Tile {
     int a, row0, rows;  // adapter (n: none), first row and rows of the order; rows 0: no tile
@@ -86,7 +88,7 @@ __device__ __forceinline__ f32x4a product32(const Raw8<E> &m, const Raw8<X> &x, 
         float v[8];
         widen8<X>(x, v);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
+        for (int p = 0; p < kParts; ++p) {
             u32x4_t b;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -243,11 +245,11 @@ __global__ __launch_bounds__(256) void k_shrink(ShrinkCall c)
 struct ExpandShape {
     int rp, steps, pitch;  // ranks with padding, steps over them (bf16: over all parts), elements per row of h
 };
-template <bool BF, int PARTS>
+template <bool BF>
 __host__ __device__ __forceinline__ ExpandShape expand_shape(int r)
 {
     const int rp = r <= 16 ? 16 : (r + 31) / 32 * 32;
-    const int steps = BF ? (PARTS * rp + 31) / 32 : (rp + 31) / 32;
+    const int steps = BF ? (kParts * rp + 31) / 32 : (rp + 31) / 32;
     return {rp, steps, BF ? steps * 32 + 8 : rp + 4};
 }
 
@@ -310,7 +312,6 @@ template <class E, class O, bool OF_A, bool FULL, bool RFULL, int SETS, bool HAL
 __global__ __launch_bounds__(256, (kExpandWaves<E, O, SETS>)) void k_expand(ExpandCall c)
 {
     constexpr bool BF = std::is_same<E, BF16>::value;
-    constexpr int PARTS = !BF ? 1 : std::is_same<O, F32>::value ? 3 : 2;
     typedef typename std::conditional<BF, uint16_t, float>::type hraw;
     extern __shared__ __align__(16) char smem[];
     hraw *hl = (hraw *)smem;
@@ -319,7 +320,7 @@ __global__ __launch_bounds__(256, (kExpandWaves<E, O, SETS>)) void k_expand(Expa
     const Tile tl = tile_of(c.o, tile);
     if (tl.rows <= 0)
         return;
-    const ExpandShape sh = expand_shape<BF, PARTS>(c.r);
+    const ExpandShape sh = expand_shape<BF>(c.r);
     const int tid = threadIdx.x, lane = tid & 63, r15 = lane & 15, kg = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool none = tl.a >= c.o.n;  // the tokens without an adapter
@@ -391,7 +392,7 @@ __global__ __launch_bounds__(256, (kExpandWaves<E, O, SETS>)) void k_expand(Expa
         hraw *at = hl + row * sh.pitch + j;
         if constexpr (BF) {
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p)
+            for (int p = 0; p < kParts; ++p)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     float left = v[q];
@@ -405,7 +406,7 @@ __global__ __launch_bounds__(256, (kExpandWaves<E, O, SETS>)) void k_expand(Expa
         }
     }
     if constexpr (BF) {  // the parts end in a whole step
-        const int slots = PARTS * sh.rp, more = sh.steps * 32 - slots;
+        const int slots = kParts * sh.rp, more = sh.steps * 32 - slots;
         for (int i = tid; i < kTileRows * more; i += 256)
             hl[i / more * sh.pitch + slots + i % more] = 0;
     }
@@ -631,7 +632,7 @@ struct OuterPair {
     int share;   // blocks that share a run's adapters
 };
 
-template <class X, int NJ, int PARTS, bool FULL>
+template <class X, int NJ, bool FULL>
 __global__ __launch_bounds__(256) void k_outer(OuterPair two)
 {
     constexpr bool BF = std::is_same<X, BF16>::value;
@@ -691,11 +692,11 @@ __global__ __launch_bounds__(256) void k_outer(OuterPair two)
                 read();
             }
             if constexpr (BF) {
-                u32x4_t gp[NJ][PARTS];
+                u32x4_t gp[NJ][kParts];
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                    for (int p = 0; p < PARTS; ++p)
+                    for (int p = 0; p < kParts; ++p)
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const uint32_t lo = bf16_part(g[j][2 * q]), hi = bf16_part(g[j][2 * q + 1]);
@@ -712,7 +713,7 @@ __global__ __launch_bounds__(256) void k_outer(OuterPair two)
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                        for (int p = 0; p < PARTS; ++p)
+                        for (int p = 0; p < kParts; ++p)
                             acc[j][e] = mfma_bf16(gp[j][p], b, acc[j][e]);
                 }
             } else {
@@ -816,12 +817,11 @@ template <class E, class O, bool OF_A, bool FULL, bool RFULL>
 void expand_of(const ExpandCall &c, hipStream_t st)
 {
     constexpr bool BF = std::is_same<E, BF16>::value;
-    constexpr int PARTS = std::is_same<O, F32>::value ? 3 : 2;
     // fewer than a block a CU: the columns in four times as many slices
     const int tiles = most_tiles(c.o), slices = (c.N + kCols - 1) / kCols;
     const bool spread = c.out && c.r <= 64 && (c.o.T / kTileRows + 1) * slices < 256;
     const dim3 grid(tiles * (!c.out ? 1 : spread ? (c.N + 127) / 128 : slices));
-    const size_t lds = (size_t)kTileRows * expand_shape<BF, PARTS>(c.r).pitch * (BF ? 2 : 4);
+    const size_t lds = (size_t)kTileRows * expand_shape<BF>(c.r).pitch * (BF ? 2 : 4);
     with_bool(spread, [&](auto sp) {
         constexpr bool SP = decltype(sp)::value;
         if (c.r <= 16)
@@ -835,15 +835,15 @@ void expand_of(const ExpandCall &c, hipStream_t st)
     });
 }
 
-template <class X, int PARTS, bool FULL>
+template <class X, bool FULL>
 void outer_of(const OuterPair &p, int slices, int chunks, hipStream_t st)
 {
     const int r = p.c[0].r;
     const dim3 grid(slices, chunks * p.share, (r + kRC - 1) / kRC);
     switch (rank_blocks(r)) {
-    case 1: hipLaunchKernelGGL((k_outer<X, 1, PARTS, FULL>), grid, dim3(256), 0, st, p); break;
-    case 2: hipLaunchKernelGGL((k_outer<X, 2, PARTS, FULL>), grid, dim3(256), 0, st, p); break;
-    default: hipLaunchKernelGGL((k_outer<X, 4, PARTS, FULL>), grid, dim3(256), 0, st, p);
+    case 1: hipLaunchKernelGGL((k_outer<X, 1, FULL>), grid, dim3(256), 0, st, p); break;
+    case 2: hipLaunchKernelGGL((k_outer<X, 2, FULL>), grid, dim3(256), 0, st, p); break;
+    default: hipLaunchKernelGGL((k_outer<X, 4, FULL>), grid, dim3(256), 0, st, p);
     }
 }
 
@@ -968,16 +968,12 @@ int launch_outer(const OuterCall *calls, int n, int chunks, hipStream_t st)
     p.share = p.share > 1 ? p.share : 1;
     with_bool(whole, [&](auto full) {
         constexpr bool FULL = decltype(full)::value;
-        if (calls[0].x_dtype == ECF_BF16) {
-            if (calls[0].grad_dtype == ECF_F32)
-                outer_of<BF16, 3, FULL>(p, slices, chunks, st);
-            else
-                outer_of<BF16, 2, FULL>(p, slices, chunks, st);
-        } else if (calls[0].x_dtype == ECF_F32) {
-            outer_of<F32, 1, FULL>(p, slices, chunks, st);
-        } else {
-            outer_of<F16, 1, FULL>(p, slices, chunks, st);
-        }
+        if (calls[0].x_dtype == ECF_BF16)
+            outer_of<BF16, FULL>(p, slices, chunks, st);
+        else if (calls[0].x_dtype == ECF_F32)
+            outer_of<F32, FULL>(p, slices, chunks, st);
+        else
+            outer_of<F16, FULL>(p, slices, chunks, st);
     });
     ECF_HIP_CHECK(hipGetLastError());
     hipLaunchKernelGGL(k_outer_join, dim3((unsigned)blocks, calls[0].o.n), dim3(256), 0, st, p);
