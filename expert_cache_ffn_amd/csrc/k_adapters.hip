@@ -62,12 +62,15 @@ __device__ __forceinline__ Tile tile_of(const AdapterOrder &o, int b)
 
 __device__ __forceinline__ float scale_of(const float *scale, int a) { return scale ? scale[a] : 1.f; }
 
-// v as a sum of bf16 values, the k-th of them
+// v as a sum of bf16 values, the next of them: its upper half, so that a finite value near fp32's
+// largest is not rounded to infinity.  Three hold 24 bits; an infinity is the first and zeros, and what
+// is left of a NaN is one, whichever half its bits lie in.
 __device__ __forceinline__ uint16_t bf16_part(float &left)
 {
-    const uint16_t p = BF16::from_f(left);
-    left -= BF16::to_f(p);
-    return p;
+    const uint32_t top = __float_as_uint(left) & 0xffff0000u;
+    const float p = __uint_as_float(top);
+    left = left == p ? 0.f : left - p;
+    return (uint16_t)(top >> 16);
 }
 
 __device__ __forceinline__ f32x4a mfma_bf16(u32x4_t a, u32x4_t b, f32x4a c)

@@ -468,9 +468,10 @@ int ecf_linear_backward(const ecf_linear_args *args, int32_t n_tokens);
  * rows may start at any multiple of the element size.  Sizes: tokens 0 to 2^22, widths 1
  * to 2^22, strides below 2^31, n_experts and n_adapters 1 to 1024, top_k 1 to 32 with
  * n_tokens * top_k up to 2^26, rank 1 to 256.  What lies between the end of a row and the
- * next row's start changes no result and is not written.  Sums are fp32 or wider, each
- * output is rounded once, nothing uses atomics on floating-point values: the same call
- * gives the same bits.
+ * next row's start changes no result and is not written.  Sums, and what lies between the
+ * products of one call, are fp32 or wider, each output is rounded once, nothing uses atomics on
+ * floating-point values: the same call gives the same bits.  An infinite or NaN element makes
+ * outputs that it is part of infinite or NaN, and no others.
  *
  * Workspaces, streams and captures as for the dense operators: d_ws needs
  * ecf_*_workspace_bytes bytes at a 256-byte boundary (may be NULL where that is 0), holds

@@ -130,3 +130,84 @@ def test_weight_gradients_keep_24_bits(T, K, N, r, n, dt, od, gd):
     want = torch.zeros(n, N, r, dtype=torch.float64)
     want[:, :, j] = q["scale"][:, None] * c * p[:, 2:]
     equal("dup", dup.cpu(), want)
+
+
+def same(name, got, want):
+    assert torch.equal(got.double().cpu(), want.to(got.dtype).double()), f"{name}: {got.flatten()[:4]} for {want.flatten()[:4]}"
+
+
+@pytest.mark.parametrize("dt,od", [p for p in PAIRS if p[0] != "f16"])
+@pytest.mark.parametrize("T", [20, 150])
+def test_the_largest_finite_values(T, dt, od):
+    """h, g and dout next to the largest fp32 number, which a bf16 number rounds to infinity, times small ones."""
+    K, N, r, n, small = 64, 72, 8, 2, 2.0 ** -100
+    big = (2 - 2.0 ** -7) * 2.0 ** 127 + 1.5 * 2.0 ** 119  # over the middle between bf16's largest number and 2^128
+    pair = torch.tensor([(2 - 2.0 ** -7) * 2.0 ** 63, 1.5 * 2.0 ** 55], dtype=torch.float64)
+    _, q = case(T, T, K, N, r, n)
+    q["x"][7, :2], q["down"][:, 5, :2], q["up"][:, :, 5] = pair, 2.0 ** 64, small
+    q["scale"].fill_(1)
+    ids, none = q["ids"].int().cuda(), torch.zeros(T, r, device="cuda")
+    out, h = layer_of(q, dt, od).forward(q["x"].to(DT[dt]).cuda(), ids, save=True)
+    want = torch.zeros(T, r, dtype=torch.float64)
+    want[7, 5] = big
+    same("h", h, want)
+    same("out", out, (big * small * (torch.arange(T) == 7))[:, None].expand(T, N).double())
+    # the same through g, from a product or (dout in fp32) from one value
+    _, q = case(T, T, K, N, r, n)
+    q["scale"].fill_(1)
+    a = int(q["ids"][7])
+    douts = [(pair, 2.0 ** 64)] + ([(torch.tensor([big, 0.0]), 1.0)] if od == "f32" else [])
+    for values, up in douts:
+        q["dout"][7, :2], q["up"][:, :2, 5], q["down"][:, 5] = values.double(), up, small
+        q["x"][7] = small
+        dx, ddown, _ = layer_of(q, dt, od).backward(q["x"].to(DT[dt]).cuda(), ids, none, q["dout"].to(DT[od]).cuda())
+        same("dx", dx, (big * small * (torch.arange(T) == 7))[:, None].expand(T, K).double())
+        want = torch.zeros(n, r, K, dtype=torch.float64)
+        want[a, 5] = big * small
+        same("ddown", ddown, want)
+    h = none.clone()
+    h[7, 5] = big
+    q["dout"].zero_()
+    q["dout"][7] = small
+    _, _, dup = layer_of(q, dt, od).backward(q["x"].to(DT[dt]).cuda(), ids, h, q["dout"].to(DT[od]).cuda())
+    want = torch.zeros(n, N, r, dtype=torch.float64)
+    want[a, :, 5] = big * small
+    same("dup", dup, want)
+
+
+@pytest.mark.parametrize("dt,od", PAIRS)
+@pytest.mark.parametrize("T", [20, 150])
+def test_infinities_stay_infinities(T, dt, od):
+    """An infinite h, g or dout times numbers other than zero is one of their signs, as in the formulas; a NaN stays one."""
+    K, N, r, n, inf = 64, 72, 8, 2, float("inf")
+    g, q = case(T, T, K, N, r, n)
+    q["down"], q["up"], q["x"] = powers(g, n, r, K), powers(g, n, N, r), powers(g, T, K)
+    q["up"][:, ::2] *= -1
+    q["down"][:, :, ::2] *= -1
+    q["x"][:, ::2] *= -1
+    q["dout"] = powers(g, T, N)
+    q["dout"][:, ::2] *= -1
+    x, dout, ids = q["x"].clone(), q["dout"].clone(), q["ids"].int().cuda()
+    layer = layer_of(q, dt, od)
+    a = int(q["ids"][7])
+    x[7, 0], x[9, 3] = -inf, float("nan")
+    out, h = layer.forward(x.to(DT[dt]).cuda(), ids, save=True)
+    same("h", h[7], torch.full((r,), inf).double())
+    same("out", out[7], inf * q["up"][a, :, 0])
+    assert torch.isnan(out[9]).all() and torch.isfinite(out[10:]).all()
+    dout[7, 0] = -inf  # g is +inf
+    ones = torch.ones(T, r, device="cuda")
+    dx, ddown, dup = layer.backward(q["x"].to(DT[dt]).cuda(), ids, ones, dout.to(DT[od]).cuda())
+    same("dx", dx[7], inf * q["down"][a, 0])
+    same("ddown", ddown[a], (inf * q["x"][7]).expand(r, K))
+    if od == "bf16":  # an infinite operand meets all parts of h, zeros among them: infinite or NaN
+        assert not torch.isfinite(dup[a, 0]).any()
+    else:
+        same("dup", dup[a, 0], torch.full((r,), -inf).double())
+    assert torch.isfinite(dx[10:]).all() and torch.isfinite(ddown[1 - a]).all() and torch.isfinite(dup[:, 1:]).all()
+    ones[7, 5] = -inf
+    _, _, dup = layer.backward(q["x"].to(DT[dt]).cuda(), ids, ones, q["dout"].to(DT[od]).cuda())
+    same("dup", dup[a, :, 5], -inf * q["dout"][7])
+    dout[7, 0] = float("nan")
+    dx, ddown, _ = layer.backward(q["x"].to(DT[dt]).cuda(), ids, torch.ones(T, r, device="cuda"), dout.to(DT[od]).cuda())
+    assert torch.isnan(dx[7]).all() and torch.isnan(ddown[a]).all() and torch.isfinite(dx[10:]).all()
