@@ -99,6 +99,27 @@ int make_order(const ecf_adapter_args *a, int32_t T, const Workspace &w, Adapter
 int split_k(int32_t K, int splits) { return ((K + splits - 1) / splits + 127) / 128 * 128; }
 
 }  // namespace
+
+// Splits of K: up to four blocks a CU where there are few tiles, 256 of K each at least, at most
+// 7 (each adds a part of h that every block of the expand reads).
+int shrink_splits(int T, int K)
+{
+    int s = kShrinkBlocks / (T / kTileRows + 1);
+    s = s < kShrinkSplits ? s : kShrinkSplits;
+    const int most = (K + 255) / 256;
+    s = s < most ? s : most;
+    return s > 1 ? s : 1;
+}
+
+int outer_slices(int W) { return (W + kOuterCols - 1) / kOuterCols; }
+
+// Runs of the sorted rows: two blocks a CU over all slices, 128 rows each at least.
+int outer_chunks(int T, int slices)
+{
+    const int most = (T + 127) / 128, s = 512 / slices;
+    return s < 1 || most < 1 ? 1 : s < most ? s : most;
+}
+
 }  // namespace ecf
 
 using namespace ecf;

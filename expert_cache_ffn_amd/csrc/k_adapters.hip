@@ -32,7 +32,6 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 constexpr int kKC = 128;   // k per staged chunk of a shrink
 constexpr int kRC = 64;    // most ranks at a time
 constexpr int kCols = 512; // columns per block of an expand
-constexpr int kOuterCols = 128;
 constexpr int kParts = 3;  // bf16 values that hold an fp32 one
 
 struct Tile {
@@ -852,17 +851,6 @@ void outer_of(const OuterPair &p, int slices, int chunks, hipStream_t st)
 
 }  // namespace
 
-// Splits of K: up to four blocks a CU where there are few tiles, 256 of K each at least, at most
-// 7 (each adds a part of h that every block of the expand reads).
-int shrink_splits(int T, int K)
-{
-    int s = kShrinkBlocks / (T / kTileRows + 1);
-    s = s < kShrinkSplits ? s : kShrinkSplits;
-    const int most = (K + 255) / 256;
-    s = s < most ? s : most;
-    return s > 1 ? s : 1;
-}
-
 int launch_shrink(const ShrinkCall &c, hipStream_t st)
 {
     ProfScope prof("adapter_shrink", st);
@@ -935,15 +923,6 @@ int launch_few_expand(const ExpandCall &c, hipStream_t st)
     });
     ECF_HIP_CHECK(hipGetLastError());
     return ECF_OK;
-}
-
-int outer_slices(int W) { return (W + kOuterCols - 1) / kOuterCols; }
-
-// Runs of the sorted rows: two blocks a CU over all slices, 128 rows each at least.
-int outer_chunks(int T, int slices)
-{
-    const int most = (T + 127) / 128, s = 512 / slices;
-    return s < 1 || most < 1 ? 1 : s < most ? s : most;
 }
 
 int launch_outer(const OuterCall *calls, int n, int chunks, hipStream_t st)

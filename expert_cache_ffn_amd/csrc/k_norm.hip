@@ -23,7 +23,6 @@ namespace ecf {
 namespace {
 
 constexpr int kNormWide = 16384;  // longer rows are read again instead of held
-constexpr int kNormParts = 512;   // rows of partial column sums, as far as there are tokens
 
 struct NormPlan {
     int group, chunks;  // threads per row, chunks of 8 elements each holds (0: a loop)
@@ -448,16 +447,6 @@ void backward_of(const NormCall &c, const NormPlan &p, int parts, hipStream_t st
 }
 
 }  // namespace
-
-// Twice as many for short rows of many tokens, whose groups of threads are small (8192 tokens in bf16: 1024 elements 27.6
-// us with 512 parts, 22.4 with 1024, 24.7 with 2048; 4096 elements, 4096 tokens 51.6, 57.7, 62.5).
-int norm_partial_rows(int T, int d)
-{
-    int parts = kNormParts;
-    if (d <= 2048 && T / 8 > parts)
-        parts = T / 8 < 2 * kNormParts ? T / 8 : 2 * kNormParts;
-    return T < parts ? T : parts;
-}
 
 int launch_norm_forward(const NormCall &c, hipStream_t st)
 {

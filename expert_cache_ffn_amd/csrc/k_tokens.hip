@@ -20,11 +20,6 @@
 namespace ecf {
 namespace {
 
-constexpr int kSortRows = 1024;      // choices that a block takes at a time
-// Segments up to which each block counts the others' choices itself: 5 segments of 60 experts 7.4 us,
-// against 3.1 + 6.3 for a kernel that counts and one that places; 24 of 256 experts 15.3 against 4.9 + 9.1.
-constexpr int kSortSelf = 8;
-constexpr int kSortSegments = 128;   // most segments
 
 __device__ __forceinline__ int choice(const SortCall &c, uint32_t f)
 {
@@ -406,14 +401,6 @@ dim3 token_grid(const MoveCall &c, int shift)
 }
 
 }  // namespace
-
-int sort_segments(int64_t rows)
-{
-    const int64_t n = rows > 0 ? (rows + kSortRows - 1) / kSortRows : 1;
-    return (int)(n < kSortSegments ? n : kSortSegments);
-}
-
-bool sort_counts_itself(int segments) { return segments <= kSortSelf; }
 
 int launch_token_sort(const SortCall &c, hipStream_t st)
 {

@@ -43,6 +43,7 @@ struct SortCall {
     int32_t *counts, *offsets, *tiles, *order, *place;
     int32_t *segments;  // workspace: [sort_segments][E + 1]
 };
+constexpr int kSortRows = 1024;  // choices that a block takes at a time
 // Segments of the choices, which blocks of their own place; many have their counts in the workspace.
 int sort_segments(int64_t rows);
 bool sort_counts_itself(int segments);
@@ -150,6 +151,7 @@ struct OuterCall {
     void *d;
     float *slots;  // outer_slots bytes
 };
+constexpr int kOuterCols = 128;  // columns per block
 int outer_slices(int W);
 // Runs of the sorted rows, blocks of their own, for so many slices of columns.
 int outer_chunks(int T, int slices);
