@@ -130,9 +130,9 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void k_norm(NormCall c)
 {
     __shared__ double sh[16];
     constexpr int B = G > 256 ? G : 256;
-    const int64_t t = (int64_t)blockIdx.x * (B / G) + threadIdx.x / G;
+    const int64_t t = block_at() * (B / G) + threadIdx.x / G;
     if (t >= c.T)
-        return;  // (whole waves, and only where a wave has a row of its own)
+        return;  // (whole waves, where a wave has a row of its own, or whole blocks)
     const int i = threadIdx.x % G;
     const typename E::raw *x = (const typename E::raw *)c.x + t * c.ldx;
     const typename S::raw *res = (const typename S::raw *)c.residual + t * c.ldres;
@@ -181,7 +181,9 @@ template <class E, class S>
 __global__ __launch_bounds__(1024) void k_norm_wide(NormCall c)
 {
     __shared__ double sh[16];
-    const int64_t t = blockIdx.x;
+    const int64_t t = block_at();
+    if (t >= c.T)
+        return;
     const typename E::raw *x = (const typename E::raw *)c.x + t * c.ldx;
     const typename S::raw *res = (const typename S::raw *)c.residual + t * c.ldres;
     typename S::raw *sum = (typename S::raw *)c.sum + t * c.ldsum;
@@ -309,12 +311,14 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void k_norm_back(NormCall c, int
         }
 }
 
-// Rows of any length: one block per row (grid-stride), sums of columns by a kernel of their own.
+// Rows of any length: one block per row, sums of columns by a kernel of their own.
 template <class E, class S>
 __global__ __launch_bounds__(1024) void k_norm_back_wide(NormCall c)
 {
     __shared__ double sh[16];
-    const int64_t t = blockIdx.x;
+    const int64_t t = block_at();
+    if (t >= c.T)
+        return;
     const typename S::raw *sum = (const typename S::raw *)c.sum + t * c.ldsum;
     const typename E::raw *dy = (const typename E::raw *)c.dy + t * c.lddy;
     const typename S::raw *past = (const typename S::raw *)c.dsum + t * c.lddsum;
@@ -392,11 +396,12 @@ void forward_of(const NormCall &c, const NormPlan &p, hipStream_t st)
             return;
         }
     } else if (p.chunks == 0) {
-        hipLaunchKernelGGL((k_norm_wide<E, S>), dim3(c.T), dim3(1024), 0, st, c);
+        hipLaunchKernelGGL((k_norm_wide<E, S>), dim_of(block_grid(c.T)), dim3(1024), 0, st, c);
         return;
     }
 #define ECF_NORM(G, NC)                                                                                         \
-    hipLaunchKernelGGL((k_norm<E, S, G, NC, FULL>), dim3((c.T + (G < 256 ? 256 / G : 1) - 1) / (G < 256 ? 256 / G : 1)), \
+    hipLaunchKernelGGL((k_norm<E, S, G, NC, FULL>),                                                             \
+                       dim_of(block_grid((c.T + (G < 256 ? 256 / G : 1) - 1) / (G < 256 ? 256 / G : 1))),       \
                        dim3(G > 256 ? G : 256), 0, st, c)
     if (p.group == 64 && p.chunks == 1)
         ECF_NORM(64, 1);
@@ -423,7 +428,7 @@ void backward_of(const NormCall &c, const NormPlan &p, int parts, hipStream_t st
         }
     } else if (p.chunks == 0) {
         if (c.dx || c.ds)
-            hipLaunchKernelGGL((k_norm_back_wide<E, S>), dim3(c.T), dim3(1024), 0, st, c);
+            hipLaunchKernelGGL((k_norm_back_wide<E, S>), dim_of(block_grid(c.T)), dim3(1024), 0, st, c);
         if (c.dweight)
             hipLaunchKernelGGL((k_norm_cols<E, S>), dim3((c.d + 63) / 64, parts), dim3(64), 0, st, c, parts);
         return;

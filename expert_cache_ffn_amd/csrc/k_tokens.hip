@@ -333,7 +333,7 @@ __global__ __launch_bounds__(256) void k_combine_back(MoveCall c)
     constexpr int PER = 256 / G;
     // (the same for all of a wave where a choice has one)
     const uint32_t sub = G == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / G) : threadIdx.x / G;
-    const uint32_t f = blockIdx.x * PER + sub, all = (uint32_t)c.T * c.k;
+    const uint32_t f = (uint32_t)block_at() * PER + sub, all = (uint32_t)c.T * c.k;
     if (f >= all)
         return;
     const int lane = threadIdx.x % G;
@@ -485,7 +485,7 @@ int launch_combine_backward(const MoveCall &c, hipStream_t st)
             using E = decltype(e);
             using O = decltype(o);
             constexpr bool FULL = decltype(full)::value;
-            const auto grid = [&](int g) { return dim3((unsigned)(((int64_t)c.T * c.k * g + 255) / 256)); };
+            const auto grid = [&](int g) { return dim_of(block_grid(((int64_t)c.T * c.k * g + 255) / 256)); };
             if (c.d <= 64)
                 hipLaunchKernelGGL((k_combine_back<E, O, FULL, 8>), grid(8), dim3(256), 0, st, c);
             else if (c.d <= 256)

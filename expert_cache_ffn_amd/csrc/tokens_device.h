@@ -107,6 +107,9 @@ __device__ __forceinline__ Raw8<E> row8(const typename E::raw *row, int64_t col,
     }
 }
 
+// This block's number in a block_grid
+__device__ __forceinline__ int64_t block_at() { return (int64_t)blockIdx.y * kGridX + blockIdx.x; }
+
 // Sum over the G threads (64, 256 or 1024) that share a row; with G over 64 they are the
 // whole block, `sh` has room for one value a wave, and every thread comes here.
 template <int G>
@@ -158,8 +161,11 @@ __device__ __forceinline__ uint32_t mx_pack4(const float v[4])
     return (uint32_t)r;
 }
 
-// ---- launches: a call of f with types and constants for values -------------------------
+// ---- launches ------------------------------------------------------------------------
 
+inline dim3 dim_of(BlockGrid g) { return dim3(g.x, g.y); }
+
+// A call of f with types and constants for values
 template <class F>
 void with_element(int dtype, F f)
 {

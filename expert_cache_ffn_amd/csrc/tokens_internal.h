@@ -11,6 +11,17 @@ namespace ecf {
 constexpr int32_t kTokenMax = 1 << 22;  // tokens and widths per call
 constexpr int kTileRows = 64;           // rows per tile of the sorted order
 
+// One dimension of a grid takes fewer than 2^32 threads.  Where there may be more, with up to 1024 a block, block b is
+// (b % kGridX, b / kGridX); those behind the last one, which complete the last line, return.
+constexpr int kGridX = 1 << 21;
+struct BlockGrid {
+    unsigned x, y;
+};
+inline BlockGrid block_grid(int64_t blocks)
+{
+    return {(unsigned)(blocks < kGridX ? blocks : kGridX), (unsigned)((blocks + kGridX - 1) / kGridX)};
+}
+
 // ---- norm ---------------------------------------------------------------------------
 struct NormCall {
     int T, d, dtype, sum_dtype, weight_dtype, grad_dtype;

@@ -97,5 +97,10 @@ const char *token_host_launches()
     ecf::t_log.clear();
     return out.c_str();
 }
+void token_host_grid(long long blocks, unsigned *x, unsigned *y)
+{
+    const ecf::BlockGrid g = ecf::block_grid(blocks);
+    *x = g.x, *y = g.y;
+}
 const char *token_host_error() { return ecf::t_error.c_str(); }
 }

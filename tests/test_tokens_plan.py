@@ -59,6 +59,15 @@ def test_sort_and_norm_workspace(host):
             assert q["partial"] == WS and q["parts"] * d * 4 <= ws
 
 
+def test_grids(host):
+    """A block for each row of the most tokens (of 1024 threads) and for every four of the most choices: fewer than 2^32 threads
+    in a dimension, and no more blocks than complete the last line."""
+    for blocks in (1, 2, 1000, (1 << 21) - 1, 1 << 21, (1 << 21) + 1, (1 << 22) - 3, 1 << 22, (1 << 24) - 1, 1 << 24):
+        x, y = host.grid(blocks)
+        assert x * 1024 < 1 << 32 and y < 1 << 16 and x * y >= blocks and x * (y - 1) < blocks
+        assert (y == 1 or x == 1 << 21) and x * y * 4 + blocks < 1 << 32  # (numbers of choices behind the last fit 32 bits)
+
+
 def test_host_code_under_sanitizers(tmp_path):
     if shutil.which("g++") is None:
         pytest.skip("needs g++")

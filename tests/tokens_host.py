@@ -35,6 +35,11 @@ class Host:
         assert code == ecf.ECF_OK, self.lib.token_host_error().decode()
         return json.loads(self.lib.token_host_launches())
 
+    def grid(self, blocks):
+        x, y = ctypes.c_uint32(), ctypes.c_uint32()
+        self.lib.token_host_grid(ctypes.c_int64(blocks), ctypes.byref(x), ctypes.byref(y))
+        return x.value, y.value
+
     def norm_backward(self, T, d, ws=None):
         a = ecf.NormArgs()
         a.hidden = d
