@@ -96,19 +96,25 @@ int make_order(const ecf_adapter_args *a, int32_t T, const Workspace &w, Adapter
     return ECF_OK;
 }
 
-int split_k(int32_t K, int splits) { return ((K + splits - 1) / splits + 127) / 128 * 128; }
-
 }  // namespace
 
-// Splits of K: up to four blocks a CU where there are few tiles, 256 of K each at least, at most
-// 7 (each adds a part of h that every block of the expand reads).
-int shrink_splits(int T, int K)
+// K per split: up to four blocks a CU where there are few tiles, at most 7 splits (each adds a part
+// of h that every block of the expand reads) and one for each 256 of K, in whole chunks.
+int shrink_split_k(int T, int K)
 {
     int s = kShrinkBlocks / (T / kTileRows + 1);
     s = s < kShrinkSplits ? s : kShrinkSplits;
     const int most = (K + 255) / 256;
     s = s < most ? s : most;
-    return s > 1 ? s : 1;
+    s = s > 1 ? s : 1;
+    return ((K + s - 1) / s + kShrinkChunk - 1) / kShrinkChunk * kShrinkChunk;
+}
+
+// Splits that have any of K.
+int shrink_splits(int T, int K)
+{
+    const int k = shrink_split_k(T, K);
+    return (K + k - 1) / k;
 }
 
 int outer_slices(int W) { return (W + kOuterCols - 1) / kOuterCols; }
@@ -170,7 +176,7 @@ int ecf_adapter_forward(const ecf_adapter_args *a, int32_t T)
         s.K = a->in_features, s.r = a->rank;
         s.m = a->d_a, s.x = a->d_x, s.ldx = ldx;
         s.part = (float *)((char *)a->d_ws + w.part);
-        s.splits = w.splits, s.split_k = split_k(s.K, s.splits);
+        s.splits = w.splits, s.split_k = shrink_split_k(T, s.K);
         e.dtype = a->dtype, e.out_dtype = a->out_dtype;
         e.N = a->out_features, e.r = a->rank;
         e.m = a->d_b, e.scale = a->d_scale;
@@ -236,7 +242,7 @@ int ecf_adapter_backward(const ecf_adapter_args *a, int32_t T)
             s.of_b = true;
             s.m = a->d_b, s.x = a->d_dout, s.ldx = lddy;
             s.part = (float *)(ws + w.part);
-            s.splits = w.splits, s.split_k = split_k(s.K, s.splits);
+            s.splits = w.splits, s.split_k = shrink_split_k(T, s.K);
             ECF_TRY(launch_shrink(s, st));
             ExpandCall e{};
             e.o = o;

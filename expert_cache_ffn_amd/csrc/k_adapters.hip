@@ -29,7 +29,7 @@ namespace {
 typedef float f32x4a __attribute__((ext_vector_type(4)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kKC = 128;   // k per staged chunk of a shrink
+constexpr int kKC = kShrinkChunk;
 constexpr int kRC = 64;    // most ranks at a time
 constexpr int kCols = 512; // columns per block of an expand
 constexpr int kParts = 3;  // bf16 values that hold an fp32 one

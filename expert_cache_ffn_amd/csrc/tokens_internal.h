@@ -108,9 +108,11 @@ struct ShrinkCall {
     const void *m, *x;
     int64_t ldx;
     float *part;
-    int splits, split_k;  // split_k: k per split, a multiple of 128
+    int splits, split_k;  // split_k: k per split, a multiple of kShrinkChunk
 };
 constexpr int kShrinkBlocks = 1024, kShrinkSplits = 7;  // (72 tiles of 64 tokens, K 4096: 12.1 us, 13.5 with 8, 24 with 2)
+constexpr int kShrinkChunk = 128;  // k that a block stages at a time
+int shrink_split_k(int T, int K);
 int shrink_splits(int T, int K);
 // Rows of h in all splits of any call of up to T tokens.
 inline int64_t shrink_rows(int64_t T)

@@ -49,6 +49,16 @@ def test_adapters_workspace(host, K, N):
                         assert not overlaps(parts, ws), (T, r, n, back, order)
 
 
+def test_every_split_has_work(host):
+    """The blocks of a split with no k would write zeros, which every block of the expand reads back."""
+    for K in [1, 7, 128, 129, 256, 257, 300, 513, 1000, 1330, 2000, 2048, 2049, 2304, 4096, 8192, 1 << 20] + list(range(64, 5000, 97)):
+        for T in (65, 100, 700, 4096, 8192, 30000, 100000):
+            for back in (False, True):
+                (q,) = [q for q in host.adapters(T, 8 if back else K, K if back else 8, 16, 8, back)[0] if q["kind"] == "shrink"]
+                assert q["k"] == K and q["split_k"] % 128 == 0 and 1 <= q["splits"] <= 7
+                assert (q["splits"] - 1) * q["split_k"] < K <= q["splits"] * q["split_k"], (T, q)
+
+
 def test_sort_and_norm_workspace(host):
     for T in TOKENS:
         for k, E in ((1, 1), (6, 256), (8, 1024), (16, 60)):
