@@ -680,8 +680,8 @@ class LowRankAdapters(_Tokens):
     takes this output as its residual).  A token whose id lies outside the stack has none.
 
     down [n, rank, in_features] and up [n, out_features, rank] in fp32, bf16 or fp16, scale [n]
-    in fp32 or None (ones); the residual, out and dout are of out_dtype: the weights' type, or
-    torch.float32.  ids: [T] of torch.int32 or torch.int64, or a TokenSort over them, which a step
+    in fp32 or None (ones), a constant without a gradient; the residual, out and dout are of out_dtype:
+    the weights' type, or torch.float32.  ids: [T] of torch.int32 or torch.int64, or a TokenSort over them, which a step
     makes once for all its layers (the ids then stay as they are).  The object keeps the weights' memory, as Linear does."""
 
     def __init__(self, down, up, scale=None, out_dtype=None):
@@ -704,6 +704,8 @@ class LowRankAdapters(_Tokens):
         a.dtype, a.out_dtype = _dense_dt(self.dtype, "down"), _DENSE_DT[self.out_dtype]
         a.d_a, a.d_b = down.data_ptr(), up.data_ptr()
         a.d_scale = _vector("scale", scale, self.n, torch.float32, self.device)
+        if scale is not None and scale.requires_grad:
+            raise ValueError("scale is a constant, backward() has no gradient for it: give scale.detach()")
         self._learns = down.requires_grad or up.requires_grad
         self.down, self.up, self.scale = _kept(down, up, scale)
         self._a = a

@@ -601,7 +601,7 @@ typedef struct {
     int32_t out_dtype;        /* of the residual, out and dout: dtype or ECF_F32 */
     const void *d_a;          /* [n][r][K] without gaps */
     const void *d_b;          /* [n][N][r] without gaps */
-    const float *d_scale;     /* [n] or NULL: ones */
+    const float *d_scale;     /* [n], constants (no gradient), or NULL: ones */
     int32_t idx_bytes;        /* 4 or 8: of an element of d_idx (int32_t or int64_t) */
     const void *d_idx;        /* [T] */
     /* of ecf_token_sort over idx with top_k 1; all three or none (then the call sorts where it has to) */
