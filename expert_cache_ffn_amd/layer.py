@@ -713,15 +713,17 @@ class LowRankAdapters(_Tokens):
         self._ws(0, 0)  # refuses a shape that no call takes
 
     def _ids(self, a, ids, T):
+        """The ids as the call reads them, which the caller of this holds over the call."""
         if isinstance(ids, TokenSort):
             if (ids.tokens, ids.top_k, ids.n_experts) != (T, 1, self.n) or ids.device != self.device:
                 raise ValueError(f"the TokenSort must be of {T} tokens, one choice of {self.n} each, on {self.device}")
             a.d_order, a.d_offsets, a.d_tiles = ids._s.d_order, ids._s.d_offsets, ids._s.d_tiles
-            ids = ids.ids if ids.ids.dim() == 1 else ids.ids[:, 0]
+            ids = (ids.ids if ids.ids.dim() == 1 else ids.ids[:, 0]).contiguous()
         wide = isinstance(ids, torch.Tensor) and ids.dtype is torch.int64
         a.idx_bytes, a.d_idx = 8 if wide else 4, _vector("ids", ids, T, torch.int64 if wide else torch.int32, self.device)
         if a.d_idx is None and T:
             raise ValueError("ids is missing")
+        return ids
 
     def _ws(self, T, backward):
         return _ws_cached(self._ws_of, (self.in_features, self.out_features, self.rank, self.n, T, backward),
@@ -733,7 +735,7 @@ class LowRankAdapters(_Tokens):
         T = self._matrix_of("x", x)
         a = L.AdapterArgs.from_buffer_copy(self._a)
         a.d_x, a.ld_x = _matrix("x", x, T, self.in_features, self.dtype, self.device)
-        self._ids(a, ids, T)
+        ids = self._ids(a, ids, T)
         if residual is not None:
             a.d_residual, a.ld_residual = _matrix("residual", residual, T, self.out_features, self.out_dtype, self.device)
         if (self._learns or x.requires_grad or residual is not None and residual.requires_grad) and not save:
@@ -757,7 +759,7 @@ class LowRankAdapters(_Tokens):
             raise ValueError(f"w_grad_dtype must be {self.dtype} or torch.float32, got {gd}")
         a.wgrad_dtype = _DENSE_DT[gd]
         a.d_x, a.ld_x = _matrix("x", x, T, self.in_features, self.dtype, self.device)
-        self._ids(a, ids, T)
+        ids = self._ids(a, ids, T)
         a.d_dout, a.ld_dout = _matrix("dout", dout, T, self.out_features, self.out_dtype, self.device)
         down = up = None
         if need_dx:
