@@ -43,6 +43,14 @@ __device__ __forceinline__ uint64_t peers_of(int key, bool valid, int bits)
     return valid ? m : 0ull;
 }
 
+// What lanes of this wave have written to LDS before is there for all of them after it.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Exclusive sums over the block's threads (NW waves) of two counts at once, each below 2^31 in
 // total.
 template <int NW>
@@ -202,13 +210,15 @@ __global__ __launch_bounds__(64 * NW) void k_token_place(SortCall c, uint32_t pe
             const bool valid = f < we;
             const int e = valid ? choice(c, f) : 0;
             const uint64_t peers = peers_of(e, valid, bits);
+            const int b = base[w * EB + e], p = b + __popcll(peers & lanemask_lt(lane));
             if (valid) {
-                const int b = base[w * EB + e], p = b + __popcll(peers & lanemask_lt(lane));
                 c.order[p] = (int)f;
                 c.place[f] = p;
-                if (lane == __ffsll((unsigned long long)peers) - 1)
-                    base[w * EB + e] = b + __popcll(peers);
             }
+            wave_sync();  // all lanes have read what one of them now moves on for the next 64
+            if (valid && lane == __ffsll((unsigned long long)peers) - 1)
+                base[w * EB + e] = b + __popcll(peers);
+            wave_sync();
         }
     }
 }
