@@ -11,9 +11,9 @@
 // x, the residual and the output are read and written once, which bounds all of them; the
 // matrices are shared by 64 tokens (by a run of them) and come from the caches.  Measured in
 // bf16 (a large copy takes 5.0 TB/s): 4096 tokens, 4096 to 4096, rank 16, 8 adapters: shrink
-// 12.5 us (2.7 TB/s: few chunks a block behind the chain tiles - order - x), expand 20 (3.3:
+// 12.3 us (2.7 TB/s: few chunks a block behind the chain tiles - order - x), expand 20.8 (3.2:
 // all blocks run at once, first all load, then all store); 8192 tokens, 2048 / 4096, rank 32:
-// shrink of dout 20 (3.4), expand to dx 21.5 (3.1), both outer products 34 (2.9) and 7 for their
+// shrink of dout 20 (3.4), expand to dx 21.8 (3.1), both outer products 36.5 (2.8) and 7 for their
 // join; 16 tokens of 16 adapters 6.6 us in one kernel.
 //
 // What lies between shrink and expand (h, in the backward pass g) stays in fp32.  As an operand
@@ -486,8 +486,7 @@ __device__ __forceinline__ int adapter_at(const AdapterOrder &o, int t)
 // Both products in one launch where a token's A is small: every block of a token makes h
 // itself.  grid: slices of 1024 columns, tokens; sixteen waves share the ranks (fewer ranks: K
 // too), then a thread has a column.  What a column needs of B and the residual is on its way
-// meanwhile.  (16 tokens, 4096 to 4096, rank 16, bf16: a call 7.7 us, 11.1 with two kernels; at rank 64,
-// where a block reads 512 KB of A, 17.8 against 10.9.)
+// meanwhile.  Against two kernels see kFewBytes.
 template <class E, class O, bool FULL, bool RFULL>
 __global__ __launch_bounds__(1024) void k_few(ShrinkCall c, ExpandCall x)
 {

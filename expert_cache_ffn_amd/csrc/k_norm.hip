@@ -15,8 +15,11 @@
 // 16384.  Longer rows are read again from the caches.
 //
 // Bound by memory.  bf16 with an fp32 sum: 8192 x 4096 to 8 bits 70 us (5.3 TB/s, where a large
-// copy takes 5.0), 4096 x 4096 backward 47 us and 5 for the join (5.8 TB/s); one token of
-// 4096 3.1 us, launch and two rounds of loads.
+// copy takes 5.0), 4096 x 4096 backward 46 us and 5 for the join (5.8 TB/s); one token of
+// 4096 3.1 us, launch and two rounds of loads.  Backward over rows of 8193 to 16384 the sixteen
+// waves have 128 registers a thread, which 16-bit types spill over (9 or 10 registers with an fp32 sum, 43
+// without): 4096 x 16384 219 us with an fp32 sum (4.9 TB/s), fp32 211 (5.1), bf16 throughout 141
+// (3.8 TB/s, so not at memory's rate).
 #include "tokens_device.h"
 
 namespace ecf {

@@ -11,10 +11,12 @@ namespace {
 
 constexpr int32_t kMaxExperts = 1024, kMaxTopK = 32;
 constexpr int kNormParts = 512;  // rows of partial column sums, as far as there are tokens
-// Segments up to which each block counts the others' choices itself: 5 segments of 60 experts 7.4 us,
-// against 3.1 + 6.3 for a kernel that counts and one that places; 24 of 256 experts 15.3 against 4.9 + 9.1.
+// Segments up to which each block counts the others' choices itself, against a kernel that counts and one that
+// places.  us a call in a graph, of 8 / 60 / 256 / 1024 experts: 5 segments 6.3 / 6.3 / 6.9 / 8.5 against 7.3 / 8.1 /
+// 8.5 / 10.3; 8 segments 7.3 / 6.8 / 7.3 / 9.0 against 7.9 / 9.2 / 9.8 / 11.5; 16 segments 9.3 / 8.7 / 9.3 / 11.0
+// against 8.1 / 8.6 / 9.3 / 11.0; 32 segments 13.7 / 12.7 / 13.2 / 15.1 against 9.9 / 11.0 / 11.4 / 13.4.
 constexpr int kSortSelf = 8;
-constexpr int kSortSegments = 128;   // most segments
+constexpr int kSortSegments = 128;  // most segments
 
 int check_width(const char *what, int32_t d, int32_t T)
 {

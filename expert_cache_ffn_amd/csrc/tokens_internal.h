@@ -110,7 +110,8 @@ struct ShrinkCall {
     float *part;
     int splits, split_k;  // split_k: k per split, a multiple of kShrinkChunk
 };
-constexpr int kShrinkBlocks = 1024, kShrinkSplits = 7;  // (72 tiles of 64 tokens, K 4096: 12.1 us, 13.5 with 8, 24 with 2)
+// Most splits by 72 tiles of 64 tokens, K 4096: 12.1 us, 13.5 with 8, 24 with 2 (fewer tiles were not measured with more).
+constexpr int kShrinkBlocks = 1024, kShrinkSplits = 7;
 constexpr int kShrinkChunk = 128;  // k that a block stages at a time
 int shrink_split_k(int T, int K);
 int shrink_splits(int T, int K);
@@ -143,7 +144,11 @@ int launch_expand(const ExpandCall &c, hipStream_t st);
 
 // Few tokens, in any order: both in one launch, without a workspace, or with h between two kernels.
 constexpr int kFewCols = 1024;                // columns per block of the one
-constexpr int64_t kFewBytes = (int64_t)1 << 18;  // of a token's A in fp32, which each of its blocks reads
+// Of a token's A, which each of its blocks reads, counted in fp32 for all types (the size query does not know it).
+// us a call in a graph, in one launch / in two, 16 tokens, K to K: bf16 rank 16 of 2048 4.4 / 5.5, 32 of 2048 6.2 / 6.3, 16 of
+// 4096 5.4 / 5.9 (64 tokens 8.6 / 7.4), 24 of 4096 6.6 / 6.3, 16 of 8192 10.9 / 6.8; fp32, whose own border is half as
+// far, rank 16 of 2048 5.4 / 5.8, 8 of 4096 5.2 / 5.5, 16 of 4096 7.2 / 6.2, 32 of 2048 9.9 / 6.7.
+constexpr int64_t kFewBytes = (int64_t)1 << 18;
 inline bool adapter_few_in_one(int64_t T, int64_t K, int64_t N, int64_t r, int esize)
 {
     return T <= kAdapterFew && T * ((N + kFewCols - 1) / kFewCols) <= 256 && r * K * esize <= kFewBytes;

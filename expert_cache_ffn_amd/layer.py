@@ -679,10 +679,12 @@ class LowRankAdapters(_Tokens):
     many requests beside a shared projection, whose output is the residual (or Linear.forward
     takes this output as its residual).  A token whose id lies outside the stack has none.
 
-    down [n, rank, in_features] and up [n, out_features, rank] in fp32, bf16 or fp16, scale [n]
-    in fp32 or None (ones), a constant without a gradient; the residual, out and dout are of out_dtype:
-    the weights' type, or torch.float32.  ids: [T] of torch.int32 or torch.int64, or a TokenSort over them, which a step
-    makes once for all its layers (the ids then stay as they are).  The object keeps the weights' memory, as Linear does."""
+    down [n, rank, in_features] and up [n, out_features, rank] in fp32, bf16 or fp16, of one rank
+    (smaller ones are padded with zeros); scale [n] in fp32 or None (ones), a constant without a
+    gradient; the residual, out and dout are of out_dtype: the weights' type, or torch.float32.
+    ids: [T] of torch.int32 or torch.int64, or a TokenSort over them, which a step makes once for
+    all its layers (the ids then stay as they are).  The object keeps the weights' memory, as
+    Linear does."""
 
     def __init__(self, down, up, scale=None, out_dtype=None):
         if not isinstance(down, torch.Tensor) or down.dim() != 3 or not down.is_cuda or 0 in down.shape:
