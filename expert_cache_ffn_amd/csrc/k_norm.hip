@@ -14,7 +14,7 @@
 // wave of its own up to 1024 elements needs no barrier, four waves up to 8192, sixteen up to
 // 16384.  Longer rows are read again from the caches.
 //
-// Bound by memory.  bf16 with an fp32 sum: 8192 x 4096 to 8 bits 70 us (5.3 TB/s, where a large
+// Bound by memory.  bf16 with an fp32 sum: 8192 x 4096 to 8 bits 70 us (5.2 TB/s, where a large
 // copy takes 5.0), 4096 x 4096 backward 46 us and 5 for the join (5.8 TB/s); one token of
 // 4096 3.1 us, launch and two rounds of loads.  Backward over rows of 8193 to 16384 the sixteen
 // waves have 128 registers a thread, which 16-bit types spill over (9 or 10 registers with an fp32 sum, 43
@@ -73,11 +73,17 @@ __device__ __forceinline__ void weight8_of(const NormCall &c, int64_t col, float
         weight8<E>(c, col, w);
 }
 
-// Eight elements of y to their outputs.  Every lane comes here: four share a scale.
+// Eight elements of y, from s, w and v = mean s^2 + eps, to their outputs.  Every lane comes
+// here: four share a scale.
 template <class E>
-__device__ __forceinline__ void put_y(const NormCall &c, int64_t t, int64_t col, const float y[8])
+__device__ __forceinline__ void put_y(const NormCall &c, int64_t t, int64_t col, const float s[8], const float w[8], float rstd,
+                                      double v)
 {
     const int n = (int)max((int64_t)0, min((int64_t)8, c.d - col));
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        y[j] = s[j] * rstd * w[j];
     if (c.y)
         store8<E>((typename E::raw *)c.y + t * c.ldy, col, n, y);
     if (!c.q)
@@ -90,13 +96,29 @@ __device__ __forceinline__ void put_y(const NormCall &c, int64_t t, int64_t col,
     }
     top = max(top, dpp32<kDppXor1>(top));
     top = max(top, dpp32<kDppXor2>(top));
-    const int byte = mx_scale_byte(top);
+    int byte = mx_scale_byte(top);
+    // y has three fp32 roundings, 2.6 steps of its value near a border.  Where they leave open on which side of
+    // 1.75 2^E the largest one lies, (s w)^2 is compared with (1.75 2^E)^2 v in 64 bits (by all four lanes).
+    if ((top & 0x7fffffu) - 0x5ffffcu <= 8u) {
+        const double border = (double)__uint_as_float((top & 0x7f800000u) | 0x600000u), most = border * border * v;
+        uint32_t over = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float sj = s[j];
+            asm volatile("" : "+v"(sj));  // (or s stays in registers in 64 bits from the sum of squares on: 156 registers for four chunks, not 103)
+            const double p = (double)sj * (double)w[j];
+            over |= fabsf(y[j]) < __builtin_inff() && p * p > most;
+        }
+        over |= dpp32<kDppXor1>(over);
+        over |= dpp32<kDppXor2>(over);
+        byte = mx_scale_byte((top & 0x7f800000u) | (0x600000u + over));
+    }
     const float inv = mx_inverse(byte);
-    float v[8];
+    float scaled[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        v[j] = y[j] * inv;
-    uint32_t p[2] = {mx_pack4(v), mx_pack4(v + 4)};
+        scaled[j] = y[j] * inv;
+    uint32_t p[2] = {mx_pack4(scaled), mx_pack4(scaled + 4)};
     uint8_t *q = (uint8_t *)c.q + t * c.ldq + col;
     if (n == 8) {
         struct __attribute__((packed, aligned(1))) any64 {
@@ -161,7 +183,8 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void k_norm(NormCall c)
             q = fma((double)s[k][j], (double)s[k][j], q);
     }
     q = row_sum<G>(q, sh);
-    const float rstd = inverse_root(q / c.d + (double)c.eps);
+    const double v = q / c.d + (double)c.eps;
+    const float rstd = inverse_root(v);
     if (i == 0 && c.rstd)
         c.rstd[t] = rstd;
 #pragma unroll
@@ -169,11 +192,7 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void k_norm(NormCall c)
         const int64_t col = (int64_t)(k * G + i) * 8;
         if (c.sum)
             store8<S>((typename S::raw *)c.sum + t * c.ldsum, col, (int)max((int64_t)0, min((int64_t)8, c.d - col)), s[k]);
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = s[k][j] * rstd * w[k][j];
-        put_y<E>(c, t, col, y);
+        put_y<E>(c, t, col, s[k], w[k], rstd, v);
     }
 }
 
@@ -206,12 +225,13 @@ __global__ __launch_bounds__(1024) void k_norm_wide(NormCall c)
             store8<S>(sum, col, (int)max((int64_t)0, min((int64_t)8, c.d - col)), s);
     }
     q = row_sum<1024>(q, sh);
-    const float rstd = inverse_root(q / c.d + (double)c.eps);
+    const double v = q / c.d + (double)c.eps;
+    const float rstd = inverse_root(v);
     if (threadIdx.x == 0 && c.rstd)
         c.rstd[t] = rstd;
     for (int k = 0; k < rounds; ++k) {
         const int64_t col = ((int64_t)k * 1024 + threadIdx.x) * 8;
-        float s[8], w[8], y[8];
+        float s[8], w[8];
         if (c.sum) {
             widen8<S>(row8<S, false>(sum, col, c.d), s);
         } else {
@@ -221,10 +241,7 @@ __global__ __launch_bounds__(1024) void k_norm_wide(NormCall c)
             sum8<E, S, false>(row8<E, false>(x, col, c.d), r, c.residual, s);
         }
         weight8_of<E>(c, col, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = s[j] * rstd * w[j];
-        put_y<E>(c, t, col, y);
+        put_y<E>(c, t, col, s, w, rstd, v);
     }
 }
 

@@ -148,7 +148,8 @@ __device__ __forceinline__ float mx_scale(uint32_t byte)
 {
     return byte == 255 ? __builtin_nanf("") : __builtin_ldexpf(1.f, (int)byte - 127);
 }
-// Four values within 448 as e4m3, to nearest even; infinite and NaN ones become NaN.
+// Four values as e4m3, to nearest even; finite ones are within 448, or over it by less than its rounding; infinite and
+// NaN ones become NaN.
 __device__ __forceinline__ uint32_t mx_pack4(const float v[4])
 {
     int r = 0;
@@ -156,7 +157,7 @@ __device__ __forceinline__ uint32_t mx_pack4(const float v[4])
     r = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], r, true);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        if (!(fabsf(v[j]) <= 448.f))
+        if (!(fabsf(v[j]) < 449.f))
             r = (r & ~(0xff << (8 * j))) | 0x7f << (8 * j);
     return (uint32_t)r;
 }

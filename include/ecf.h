@@ -488,9 +488,10 @@ int ecf_linear_backward(const ecf_linear_args *args, int32_t n_tokens);
  *
  * 8 bits (ECF_MXFP8): 32 consecutive columns share the E8M0 scale 2^(b - 127), the layout
  * of the MXFP4 blobs' scales; b is the smallest byte from 0 to 254 with
- * max |y| <= 448 * 2^(b - 127) over the group's finite values (0 for a group of zeros),
- * the elements are y / 2^(b - 127) in e4m3 (OCP, round to nearest even).  Infinite and NaN
- * elements become NaN.  A last group of fewer columns has its own scale. */
+ * max |y| <= 448 * 2^(b - 127) over the group's finite values (0 for a group of zeros), by the
+ * formula's y where fp32 leaves open whether it holds; the elements are y / 2^(b - 127) in e4m3
+ * (OCP, round to nearest even).  Infinite and NaN elements become NaN.  A last group of fewer
+ * columns has its own scale. */
 typedef struct {
     int32_t hidden;
     int32_t dtype;            /* of x, y and their gradients */
